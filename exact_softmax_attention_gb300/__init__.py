@@ -31,10 +31,22 @@ ATTN_ERR_SCRATCH_TOO_SMALL = -9
 
 ATTN_FP8_E4M3 = 0
 ATTN_FP8_E5M2 = 1
+ATTN_KV_BF16 = 2
 FP8_FORMATS = {"e4m3": ATTN_FP8_E4M3, "e5m2": ATTN_FP8_E5M2}
+KV_FORMATS = {**FP8_FORMATS, "bf16": ATTN_KV_BF16}
+
+ATTN_TYPE_BF16 = 0
+ATTN_TYPE_F32 = 1
+ELEM_TYPES = {"bf16": ATTN_TYPE_BF16, "f32": ATTN_TYPE_F32}
+ATTN_ROPE_PLAIN = 0
+ATTN_ROPE_LINEAR = 1
+ATTN_ROPE_NTK = 2
+ATTN_ROPE_YARN = 3
+ROPE_SCALINGS = {"plain": ATTN_ROPE_PLAIN, "linear": ATTN_ROPE_LINEAR, "ntk": ATTN_ROPE_NTK, "yarn": ATTN_ROPE_YARN}
 
 #: every symbol the header declares
-EXPORTS = ("attn_fwd", "attn_fwd_hd", "attn_fwd_fp8", "attn_decode_paged", "attn_decode_paged_fp8", "attn_decode_paged_noalloc", "attn_decode_plan",
+EXPORTS = ("attn_fwd", "attn_fwd_hd", "attn_fwd_fp8", "attn_decode_paged", "attn_decode_paged_fp8", "attn_decode_paged_noalloc",
+           "attn_rope", "attn_rope_freqs", "attn_kv_write_paged", "attn_kv_read_paged", "attn_decode_plan",
            "attn_decode_workspace_bytes", "attn_status_string", "attn_get_device_status",
            "attn_set_option", "attn_get_option", "attn_read_counters", "attn_debug_exp2", "attn_debug_watchdog",
            "attn_version")
@@ -52,6 +64,7 @@ if not os.path.exists(LIB_PATH):
 
 lib = ctypes.CDLL(LIB_PATH)
 _vp, _i, _f, _d = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_double
+_ll = ctypes.c_longlong
 lib.attn_fwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _vp]
 lib.attn_fwd.restype = _i
 lib.attn_fwd_hd.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _vp]
@@ -65,6 +78,14 @@ lib.attn_decode_paged_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp
 lib.attn_decode_paged_fp8.restype = _i
 lib.attn_decode_paged_noalloc.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i]
 lib.attn_decode_paged_noalloc.restype = _i
+lib.attn_rope.argtypes = [_vp] * 6 + [_i] * 6 + [_ll] * 4 + [_i] * 3 + [_f, _vp]
+lib.attn_rope.restype = _i
+lib.attn_rope_freqs.argtypes = [ctypes.POINTER(_d), ctypes.POINTER(_d), _i, _d, _i, _d, _d, _d, _d]
+lib.attn_rope_freqs.restype = _i
+lib.attn_kv_write_paged.argtypes = [_vp, _vp, _ll, _ll] + [_vp] * 5 + [_i] * 8 + [_f, _f, _vp, _vp, _i, _i, _i, _f, _vp]
+lib.attn_kv_write_paged.restype = _i
+lib.attn_kv_read_paged.argtypes = [_vp] * 4 + [_ll, _ll] + [_vp] * 3 + [_i] * 8 + [_f, _f, _vp]
+lib.attn_kv_read_paged.restype = _i
 lib.attn_decode_plan.argtypes = [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_i), ctypes.POINTER(_i)]
 lib.attn_decode_plan.restype = _i
 lib.attn_decode_workspace_bytes.argtypes = [_i, _i, _i, _i]
@@ -113,6 +134,10 @@ def _check(code: int, where: str, raise_on_error: bool):
     if raise_on_error and code != ATTN_OK:
         raise AttnError(code, where)
     return code
+
+
+def _code(names, x):
+    return names[x] if isinstance(x, str) else int(x)
 
 
 def status_string(code: int) -> str:
@@ -176,6 +201,53 @@ def attn_decode_paged_noalloc(q, k_cache, v_cache, page_table, seqlens, page_siz
                                        int(page_size), _ptr(o), _ptr(lse), _stream(stream), int(B), int(Hq), int(Hkv),
                                        int(d), int(max_pages_per_seq), int(num_pages), float(scale), int(num_splits))
     return _check(rc, "attn_decode_paged_noalloc", raise_on_error)
+
+
+def attn_rope(q, k, q_out, k_out, positions, inv_freq, T, Hq, Hk, d, rot_begin, rot_dim, q_stride, k_stride, q_out_stride,
+              k_out_stride, elem_type="bf16", interleaved=0, transpose=0, amplitude=1.0, stream=None, raise_on_error=True):
+    """Rotary positions of q and k (``transpose=1``: the gradient); see ``attn_rope`` in include/attn.h.
+    ``elem_type`` is "bf16" or "f32" (or the ATTN_TYPE_* code)."""
+    rc = lib.attn_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(positions), _ptr(inv_freq), int(T), int(Hq), int(Hk),
+                       int(d), int(rot_begin), int(rot_dim), int(q_stride), int(k_stride), int(q_out_stride),
+                       int(k_out_stride), _code(ELEM_TYPES, elem_type), int(interleaved), int(transpose), float(amplitude),
+                       _stream(stream))
+    return _check(rc, "attn_rope", raise_on_error)
+
+
+def attn_rope_freqs(rot_dim, theta=10000.0, scaling="plain", factor=1.0, trained_len=0.0, beta_fast=32.0, beta_slow=1.0):
+    """(frequencies, amplitude) of ``attn_rope``: a list of rot_dim / 2 floats (put it on the device
+    as float64) and the factor that belongs to it; see ``attn_rope_freqs`` in include/attn.h.
+    ``scaling`` is "plain", "linear", "ntk" or "yarn" (or the ATTN_ROPE_* code)."""
+    out, amp = (_d * max(1, int(rot_dim) // 2))(), _d()
+    rc = lib.attn_rope_freqs(out, ctypes.byref(amp), int(rot_dim), float(theta), _code(ROPE_SCALINGS, scaling), float(factor),
+                             float(trained_len), float(beta_fast), float(beta_slow))
+    _check(rc, "attn_rope_freqs", True)
+    return list(out), amp.value
+
+
+def attn_kv_write_paged(k, v, k_stride, v_stride, k_cache, v_cache, page_table, seqlens, cu_seqlens, page_size, T, B, Hkv, d,
+                        max_pages_per_seq, num_pages, kv_format="bf16", k_descale=1.0, v_descale=1.0, positions=None,
+                        inv_freq=None, rot_begin=0, rot_dim=0, interleaved=0, amplitude=1.0, stream=None,
+                        raise_on_error=True):
+    """New keys (optionally rotated) and values into a paged cache; see ``attn_kv_write_paged`` in
+    include/attn.h. ``kv_format`` is "bf16", "e4m3" or "e5m2" (or the code)."""
+    rc = lib.attn_kv_write_paged(_ptr(k), _ptr(v), int(k_stride), int(v_stride), _ptr(k_cache), _ptr(v_cache),
+                                 _ptr(page_table), _ptr(seqlens), _ptr(cu_seqlens), int(page_size), int(T), int(B), int(Hkv),
+                                 int(d), int(max_pages_per_seq), int(num_pages), _code(KV_FORMATS, kv_format),
+                                 float(k_descale), float(v_descale), _ptr(positions), _ptr(inv_freq), int(rot_begin),
+                                 int(rot_dim), int(interleaved), float(amplitude), _stream(stream))
+    return _check(rc, "attn_kv_write_paged", raise_on_error)
+
+
+def attn_kv_read_paged(k_cache, v_cache, k, v, k_stride, v_stride, page_table, seqlens, cu_seqlens, page_size, T, B, Hkv, d,
+                       max_pages_per_seq, num_pages, kv_format="bf16", k_descale=1.0, v_descale=1.0, stream=None,
+                       raise_on_error=True):
+    """Cached tokens back as bf16 rows; see ``attn_kv_read_paged`` in include/attn.h."""
+    rc = lib.attn_kv_read_paged(_ptr(k_cache), _ptr(v_cache), _ptr(k), _ptr(v), int(k_stride), int(v_stride),
+                                _ptr(page_table), _ptr(seqlens), _ptr(cu_seqlens), int(page_size), int(T), int(B), int(Hkv),
+                                int(d), int(max_pages_per_seq), int(num_pages), _code(KV_FORMATS, kv_format),
+                                float(k_descale), float(v_descale), _stream(stream))
+    return _check(rc, "attn_kv_read_paged", raise_on_error)
 
 
 def attn_decode_plan(B, Hq, Hkv, max_pages_per_seq, page_size, num_splits=0, num_sms=0):

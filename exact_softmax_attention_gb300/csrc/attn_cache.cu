@@ -1,0 +1,290 @@
+// Writes into and reads from a paged key/value cache, in bf16 or in 8-bit floating point with one
+// descale per tensor: code = fp8(x / descale), value = descale * fp8(code).
+//
+// A write takes the new rows of each sequence, optionally rotates K by its positions (in fp32, so
+// that a cached key is rounded once), and stores them at the end of the sequence; a read returns
+// the last rows of each sequence as bf16. Both move each element once in and once out and are
+// bounded by memory. What a short call costs is the chain of dependent loads from the packed
+// row to its page (offsets, length, page table); the rows themselves do not depend on it, so each
+// thread loads its first item before the places are known.
+#include "attn.h"
+#include "rows.cuh"
+
+#include <math.h>
+
+namespace attn {
+namespace {
+
+constexpr int kCacheThreads = 256;
+constexpr int kCacheMaxTokens = 8;  // tokens per block, one warp resolves each
+
+struct CacheParams {
+    const __nv_bfloat16* in[2];  // write: k, v
+    __nv_bfloat16* out[2];       // read: k, v
+    long long stride[2];         // elements between rows of k and v
+    uint8_t* cache[2];           // bf16 or 8-bit codes [num_pages * page_size, Hkv, d]
+    float descale[2];
+    PagedRows rows;
+    RopeCols cols;               // rot 0: no rotation
+    const int* positions;
+    const double* inv_freq;
+    float amplitude;
+    int Hkv, tokens, items;      // tokens per block, work items per head
+};
+
+// Two values to a pair of 8-bit codes (low byte first): nearest even, magnitudes above the largest
+// finite one saturate, NaN stays NaN.
+template <int FMT>
+__device__ __forceinline__ uint32_t fp8x2(float lo, float hi) {
+    uint16_t r;
+    if (FMT == ATTN_FP8_E4M3)
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two codes to two floats (exact).
+template <int FMT>
+__device__ __forceinline__ void fp8x2_values(uint32_t two, float& lo, float& hi) {
+    uint32_t h2;
+    const uint16_t v = (uint16_t)two;
+    if (FMT == ATTN_FP8_E4M3)
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(v));
+    else
+        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h2) : "h"(v));
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h2));
+}
+
+// V values into the cache at element offset at.
+template <int FMT, int V>
+__device__ __forceinline__ void store_cache(uint8_t* cache, long long at, const float (&x)[V], float descale) {
+    if constexpr (FMT == ATTN_KV_BF16) {
+        store_row<V>(reinterpret_cast<__nv_bfloat16*>(cache) + at, x);
+    } else if constexpr (V == 8) {
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = fp8x2<FMT>(x[4 * i] / descale, x[4 * i + 1] / descale) |
+                   (fp8x2<FMT>(x[4 * i + 2] / descale, x[4 * i + 3] / descale) << 16);
+        *reinterpret_cast<uint2*>(cache + at) = make_uint2(w[0], w[1]);
+    } else {
+        cache[at] = (uint8_t)fp8x2<FMT>(x[0] / descale, 0.0f);
+    }
+}
+
+template <int FMT, int V>
+__global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheParams p) {
+    extern __shared__ __align__(16) float angles[];
+    __shared__ long long place[kCacheMaxTokens];
+    const int half = p.cols.rot / 2;
+    const int t0 = blockIdx.x * p.tokens;
+    const int tokens = min(p.tokens, p.rows.T - t0);
+    float* cs = angles;
+    float* sn = angles + p.tokens * half;
+    const int per_token = 2 * p.Hkv * p.items;
+    const int n = tokens * per_token;
+    float xa[V], xb[V];
+    int t, kv, head, a, b;
+    bool turned;
+    auto load = [&](int w, int& j) {
+        t = w / per_token;
+        const int r = w - t * per_token;
+        const int h = r / p.items;
+        j = r - h * p.items;
+        kv = h >= p.Hkv;
+        head = kv ? h - p.Hkv : h;
+        if (kv || p.cols.rot == 0) {
+            a = 2 * V * j, b = a + V, turned = false;
+        } else {
+            turned = item_cols<V>(p.cols, j, a, b);
+        }
+        const __nv_bfloat16* src = p.in[kv] + (long long)(t0 + t) * p.stride[kv] + (long long)head * p.cols.d;
+        load_row<V>(src + a, xa);
+        load_row<V>(src + b, xb);
+    };
+    int w = threadIdx.x, j = 0;
+    if (w < n) load(w, j);
+    if (half > 0) block_angles(p.inv_freq, p.positions + t0, tokens, half, p.amplitude, false, cs, sn);
+    const int warp = threadIdx.x >> 5;
+    if (warp < tokens) {
+        const long long r = paged_row(p.rows, t0 + warp);
+        if ((threadIdx.x & 31) == 0) place[warp] = r;
+    }
+    __syncthreads();
+    while (w < n) {
+        if (turned) rotate_item<V>(xa, xb, cs + t * half + V * j, sn + t * half + V * j, p.cols.interleaved != 0);
+        const long long row = place[t];
+        if (row >= 0) {
+            const long long at = (row * p.Hkv + head) * p.cols.d;
+            store_cache<FMT, V>(p.cache[kv], at + a, xa, p.descale[kv]);
+            store_cache<FMT, V>(p.cache[kv], at + b, xb, p.descale[kv]);
+        }
+        w += kCacheThreads;
+        if (w < n) load(w, j);
+    }
+}
+
+// 16 elements per item: one 16-byte load of codes (two of bf16), two 16-byte stores.
+template <int FMT>
+__global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheParams p) {
+    __shared__ long long place[kCacheMaxTokens];
+    const int t0 = blockIdx.x * p.tokens;
+    const int tokens = min(p.tokens, p.rows.T - t0);
+    const int warp = threadIdx.x >> 5;
+    if (warp < tokens) {
+        const long long r = paged_row(p.rows, t0 + warp);
+        if ((threadIdx.x & 31) == 0) place[warp] = r;
+    }
+    __syncthreads();
+    const int per_token = 2 * p.Hkv * p.items;
+    const int n = tokens * per_token;
+    for (int w = threadIdx.x; w < n; w += kCacheThreads) {
+        const int t = w / per_token, r = w - t * per_token;
+        const int kv = r >= per_token / 2;
+        const int c = (kv ? r - per_token / 2 : r) * 16;  // element of the row [Hkv, d]
+        const long long row = place[t];
+        if (row == kRowNone) continue;
+        __nv_bfloat16* dst = p.out[kv] + (long long)(t0 + t) * p.stride[kv] + c;
+        uint4 o0 = make_uint4(0, 0, 0, 0), o1 = o0;  // a bad page reads as zeros
+        if (row >= 0) {
+            const long long at = row * p.Hkv * p.cols.d + c;
+            if constexpr (FMT == ATTN_KV_BF16) {
+                const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.cache[kv]) + at);
+                o0 = src[0], o1 = src[1];
+            } else {
+                const uint4 x = *reinterpret_cast<const uint4*>(p.cache[kv] + at);
+                const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                uint32_t out[8];
+                const float ds = p.descale[kv];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float lo, hi;
+                    fp8x2_values<FMT>(in[i / 2] >> (16 * (i & 1)), lo, hi);
+                    out[i] = pack_bf16x2(lo * ds, hi * ds);
+                }
+                o0 = make_uint4(out[0], out[1], out[2], out[3]);
+                o1 = make_uint4(out[4], out[5], out[6], out[7]);
+            }
+        }
+        reinterpret_cast<uint4*>(dst)[0] = o0;
+        reinterpret_cast<uint4*>(dst)[1] = o1;
+    }
+}
+
+// Tokens per block: one until the blocks fill the GPU several times.
+int cache_tokens(int T, int num_sms) { return T >= 16 * num_sms ? 4 : 1; }
+
+template <int FMT, int V>
+cudaError_t launch_write(CacheParams p, cudaStream_t stream) {
+    p.items = p.cols.d / (2 * V);
+    const int blocks = (p.rows.T + p.tokens - 1) / p.tokens;
+    cache_write_kernel<FMT, V><<<blocks, kCacheThreads, (size_t)p.tokens * p.cols.rot * sizeof(float), stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int FMT>
+cudaError_t launch_read(CacheParams p, cudaStream_t stream) {
+    p.items = p.cols.d / 16;
+    const int blocks = (p.rows.T + p.tokens - 1) / p.tokens;
+    cache_read_kernel<FMT><<<blocks, kCacheThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+bool multiple(const void* p, long long bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// Checks that both directions share; fills what both use.
+attn_status_t check(CacheParams& p, const void* k_cache, const void* v_cache, const void* k, const void* v, long long k_stride,
+                    long long v_stride, bool rows_written, const int* page_table, const int* seqlens, const int* cu_seqlens,
+                    int page_size, int T, int B, int Hkv, int d, int max_pages, int num_pages, int kv_format, float k_descale,
+                    float v_descale) {
+    if (!k_cache || !v_cache || !k || !v || !page_table || !seqlens) return ATTN_ERR_NULL_PTR;
+    if (kv_format != ATTN_FP8_E4M3 && kv_format != ATTN_FP8_E5M2 && kv_format != ATTN_KV_BF16) return ATTN_ERR_BAD_ARG;
+    if (!isfinite(k_descale) || !isfinite(v_descale) || k_descale == 0 || v_descale == 0) return ATTN_ERR_BAD_ARG;
+    if (T < 0 || B < 0 || Hkv <= 0 || Hkv > 65535 || d <= 0 || d % 16 != 0 || d > 256 || page_size <= 0 || max_pages <= 0 ||
+        num_pages <= 0 || (long long)num_pages * page_size > INT32_MAX || (long long)max_pages * page_size > INT32_MAX)
+        return ATTN_ERR_BAD_SHAPE;
+    if (!cu_seqlens && T > 0 && (B == 0 || T % B != 0)) return ATTN_ERR_BAD_SHAPE;
+    const long long row = (long long)Hkv * d;
+    if (k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride < (rows_written ? row : 0) || v_stride < (rows_written ? row : 0))
+        return ATTN_ERR_BAD_SHAPE;
+    if (!multiple(k_cache, 16) || !multiple(v_cache, 16) || !multiple(k, 16) || !multiple(v, 16) || !multiple(page_table, 4) ||
+        !multiple(seqlens, 4) || (cu_seqlens && !multiple(cu_seqlens, 4)))
+        return ATTN_ERR_ALIGN;
+    p.stride[0] = k_stride, p.stride[1] = v_stride;
+    p.cache[0] = static_cast<uint8_t*>(const_cast<void*>(k_cache));
+    p.cache[1] = static_cast<uint8_t*>(const_cast<void*>(v_cache));
+    p.descale[0] = k_descale, p.descale[1] = v_descale;
+    p.rows = PagedRows{page_table, seqlens, cu_seqlens, B, T, max_pages, page_size, num_pages, nullptr};
+    p.cols = RopeCols{d, 0, 0, 0};
+    p.positions = nullptr;
+    p.inv_freq = nullptr;
+    p.amplitude = 1.0f;
+    p.Hkv = Hkv;
+    return ATTN_OK;
+}
+
+}  // namespace
+}  // namespace attn
+
+extern "C" attn_status_t attn_kv_write_paged(const void* k, const void* v, long long k_stride, long long v_stride, void* k_cache,
+                                             void* v_cache, const int* page_table, const int* seqlens, const int* cu_seqlens,
+                                             int page_size, int T, int B, int Hkv, int d, int max_pages_per_seq, int num_pages,
+                                             int kv_format, float k_descale, float v_descale, const int* positions,
+                                             const double* inv_freq, int rot_begin, int rot_dim, int interleaved, float amplitude,
+                                             void* stream) {
+    using namespace attn;
+    CacheParams p;
+    attn_status_t st = check(p, k_cache, v_cache, k, v, k_stride, v_stride, false, page_table, seqlens, cu_seqlens, page_size, T, B,
+                             Hkv, d, max_pages_per_seq, num_pages, kv_format, k_descale, v_descale);
+    if (st != ATTN_OK) return st;
+    if (rot_dim != 0) {
+        if (!positions || !inv_freq) return ATTN_ERR_NULL_PTR;
+        if (rot_dim < 0 || rot_dim % 2 != 0 || rot_begin < 0 || rot_begin > d - rot_dim) return ATTN_ERR_BAD_SHAPE;
+        if ((interleaved != 0 && interleaved != 1) || !isfinite(amplitude)) return ATTN_ERR_BAD_ARG;
+        if (!multiple(positions, 4) || !multiple(inv_freq, 8)) return ATTN_ERR_ALIGN;
+        p.cols = RopeCols{d, rot_begin, rot_dim, interleaved};
+        p.positions = positions;
+        p.inv_freq = inv_freq;
+        p.amplitude = amplitude;
+    }
+    if (T == 0 || B == 0) return ATTN_OK;
+    int num_sms = 0;
+    if ((st = current_device_info(&p.rows.status, &num_sms)) != ATTN_OK) return st;
+    for (int i = 0; i < 2; ++i) p.in[i] = static_cast<const __nv_bfloat16*>(i ? v : k), p.out[i] = nullptr;
+    p.tokens = cache_tokens(T, num_sms);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // whole 16-element items on each side of the rotated columns, else pair by pair
+    const bool wide = p.cols.begin % 16 == 0 && p.cols.rot % 16 == 0;
+    cudaError_t e;
+    if (kv_format == ATTN_FP8_E4M3)
+        e = wide ? launch_write<ATTN_FP8_E4M3, 8>(p, s) : launch_write<ATTN_FP8_E4M3, 1>(p, s);
+    else if (kv_format == ATTN_FP8_E5M2)
+        e = wide ? launch_write<ATTN_FP8_E5M2, 8>(p, s) : launch_write<ATTN_FP8_E5M2, 1>(p, s);
+    else
+        e = wide ? launch_write<ATTN_KV_BF16, 8>(p, s) : launch_write<ATTN_KV_BF16, 1>(p, s);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" attn_status_t attn_kv_read_paged(const void* k_cache, const void* v_cache, void* k, void* v, long long k_stride,
+                                            long long v_stride, const int* page_table, const int* seqlens, const int* cu_seqlens,
+                                            int page_size, int T, int B, int Hkv, int d, int max_pages_per_seq, int num_pages,
+                                            int kv_format, float k_descale, float v_descale, void* stream) {
+    using namespace attn;
+    CacheParams p;
+    attn_status_t st = check(p, k_cache, v_cache, k, v, k_stride, v_stride, true, page_table, seqlens, cu_seqlens, page_size, T, B,
+                             Hkv, d, max_pages_per_seq, num_pages, kv_format, k_descale, v_descale);
+    if (st != ATTN_OK) return st;
+    if (T == 0 || B == 0) return ATTN_OK;
+    int num_sms = 0;
+    if ((st = current_device_info(&p.rows.status, &num_sms)) != ATTN_OK) return st;
+    for (int i = 0; i < 2; ++i) p.in[i] = nullptr, p.out[i] = static_cast<__nv_bfloat16*>(i ? v : k);
+    p.tokens = cache_tokens(T, num_sms);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = kv_format == ATTN_FP8_E4M3   ? launch_read<ATTN_FP8_E4M3>(p, s)
+                          : kv_format == ATTN_FP8_E5M2 ? launch_read<ATTN_FP8_E5M2>(p, s)
+                                                       : launch_read<ATTN_KV_BF16>(p, s);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}

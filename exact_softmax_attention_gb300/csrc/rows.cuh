@@ -1,0 +1,209 @@
+// Helpers of the row-wise operators (rotary positions, paged cache writes and reads): the angle of
+// a position, which columns one work item holds, element packing, and the place of a packed row.
+#pragma once
+
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace attn {
+
+// Rotary part of a head: columns [begin, begin + rot) of d, pairs (i, i + rot / 2), or with
+// interleaved != 0 (2 i, 2 i + 1).
+struct RopeCols {
+    int d, begin, rot, interleaved;
+};
+
+// Work item j of a head (j < d / (2 V)) holds the 2 V columns [a, a + V) and [b, b + V), the rotated
+// ones first: pairs V j .. V j + V - 1 (then true is returned), after them the columns that pass
+// through. V > 1 needs begin and rot to be multiples of 2 V.
+template <int V>
+__device__ __forceinline__ bool item_cols(const RopeCols& c, int j, int& a, int& b) {
+    const int e = 2 * V * j;
+    if (e < c.rot) {
+        a = c.begin + (c.interleaved ? e : V * j);
+        b = c.interleaved ? a + V : a + c.rot / 2;
+        return true;
+    }
+    const int x = e - c.rot, y = x + V;
+    a = x < c.begin ? x : x + c.rot;
+    b = y < c.begin ? y : y + c.rot;
+    return false;
+}
+
+// Rotate the V pairs of an item by the angles whose cosines and sines are c and s.
+template <int V>
+__device__ __forceinline__ void rotate_item(float (&xa)[V], float (&xb)[V], const float* c, const float* s,
+                                            bool interleaved) {
+    if (!interleaved) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float u = xa[e], w = xb[e];
+            xa[e] = u * c[e] - w * s[e];
+            xb[e] = u * s[e] + w * c[e];
+        }
+    } else if constexpr (V == 1) {
+        const float u = xa[0], w = xb[0];
+        xa[0] = u * c[0] - w * s[0];
+        xb[0] = u * s[0] + w * c[0];
+    } else {  // pairs (2 e, 2 e + 1) of the 2 V adjacent columns
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const float u = xa[e], w = xa[e + 1];
+            xa[e] = u * c[e / 2] - w * s[e / 2];
+            xa[e + 1] = u * s[e / 2] + w * c[e / 2];
+        }
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const float u = xb[e], w = xb[e + 1];
+            xb[e] = u * c[(V + e) / 2] - w * s[(V + e) / 2];
+            xb[e + 1] = u * s[(V + e) / 2] + w * c[(V + e) / 2];
+        }
+    }
+}
+
+// A frequency as a 64-bit fraction of a turn per position. The product with an integer position is
+// exact modulo one turn in wrapping 64-bit arithmetic, so far positions lose nothing beyond the
+// rounding of f / (2 pi) to 53 bits (about 3e-7 rad at position 2^31), and 64-bit floating-point
+// work, which is slow on this GPU, is done once per frequency and not once per angle.
+__device__ __forceinline__ unsigned long long turn_fraction(double f) {
+    const double t = f * 0.15915494309189533577;  // 1 / (2 pi)
+    return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);  // (fraction < 1) * 2^64
+}
+
+__device__ __forceinline__ void position_angle(unsigned long long frac, int pos, float& c, float& s) {
+    const long long phase = (long long)(frac * (unsigned long long)(long long)pos);  // turns * 2^64, in [-1/2, 1/2)
+    sincospif(__ll2float_rn(phase) * 1.0842021724855044e-19f, &s, &c);               // * 2^-63: half turns
+}
+
+// cos and sin (times the amplitude) of tokens [0, tokens) of a block into cs[token][rot / 2] and
+// sn[token][rot / 2]. Every thread of the block calls it.
+__device__ __forceinline__ void block_angles(const double* inv_freq, const int* positions, int tokens, int half,
+                                             float amplitude, bool transpose, float* cs, float* sn) {
+    const int nt = blockDim.x, groups = max(1, nt / half);
+    const int first = threadIdx.x % half, grp = threadIdx.x / half;
+    if (grp >= groups) return;
+    for (int i = groups > 1 ? first : (int)threadIdx.x; i < half; i += groups > 1 ? half : nt) {
+        const double f = inv_freq[i];
+        const unsigned long long frac = turn_fraction(f);
+        const float amp = isfinite(f) ? amplitude : __int_as_float(0x7fffffff);  // no angle: NaN
+        for (int t = groups > 1 ? grp : 0; t < tokens; t += groups) {
+            float c, s;
+            position_angle(frac, positions[t], c, s);
+            cs[t * half + i] = c * amp;
+            sn[t * half + i] = (transpose ? -s : s) * amp;
+        }
+    }
+}
+
+// ---- V consecutive elements of a row as floats, by one load or store of 16 bytes (V > 1)
+
+template <int V>
+__device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&x)[V]) {
+    if constexpr (V == 8) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p);
+        const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(r[i] << 16);
+            x[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
+        }
+    } else {
+        static_assert(V == 1, "bf16: 8 or 1");
+        x[0] = __bfloat162float(*p);
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void load_row(const float* p, float (&x)[V]) {
+    if constexpr (V == 4) {
+        const float4 w = *reinterpret_cast<const float4*>(p);
+        x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+    } else {
+        static_assert(V == 1, "fp32: 4 or 1");
+        x[0] = *p;
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&x)[V]) {
+    if constexpr (V == 8)
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    else
+        *p = __float2bfloat16_rn(x[0]);
+}
+
+template <int V>
+__device__ __forceinline__ void store_row(float* p, const float (&x)[V]) {
+    if constexpr (V == 4)
+        *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+        *p = x[0];
+}
+
+// ---- packed rows of a paged cache
+
+// Sequence of packed row t: the number of sequences that end at or before it. A warp probes 32
+// offsets at a time, so 1024 sequences take two rounds of loads. The whole warp calls it.
+__device__ __forceinline__ int warp_find_seq(const int* cu, int B, int t) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = B;  // the answer lies in [lo, hi]
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32;
+        const long long at = (long long)lo + (long long)(lane + 1) * step - 1;
+        const bool before = at < hi && __ldg(cu + at + 1) <= t;
+        const int cnt = __popc(__ballot_sync(0xffffffffu, before));
+        const long long next = (long long)lo + (long long)cnt * step;
+        const long long end = next + step - 1;
+        lo = (int)(next < hi ? next : hi);
+        hi = (int)(end < hi ? end : hi);
+    }
+    return lo;
+}
+
+// Shared by the cache writes and reads: row t of T belongs to sequence b and is its i-th of n
+// rows; it stands for cached token seqlens[b] - n + i.
+struct PagedRows {
+    const int* page_table;  // [B, max_pages]
+    const int* seqlens;     // [B], the n rows included
+    const int* cu_seqlens;  // [B + 1] or nullptr: T / B rows each
+    int B, T, max_pages, page_size, num_pages;
+    int* status;
+};
+
+constexpr long long kRowNone = -1;  // no sequence holds the row: it is left as it is
+constexpr long long kRowBad = -2;   // a length or page out of range (recorded)
+
+// Cache row of packed row t, or kRowNone / kRowBad. The whole warp calls it.
+__device__ __forceinline__ long long paged_row(const PagedRows& p, int t) {
+    int b, i, n;
+    if (p.cu_seqlens) {
+        b = warp_find_seq(p.cu_seqlens, p.B, t);
+        if (b >= p.B) return kRowNone;
+        const long long c0 = __ldg(p.cu_seqlens + b), c1 = __ldg(p.cu_seqlens + b + 1);
+        if (t < c0 || t >= c1 || c0 < 0 || c1 > p.T) {  // offsets that decrease or pass the rows
+            if ((threadIdx.x & 31) == 0) atomicCAS(p.status, 0, kDevBadIndex);
+            return kRowNone;
+        }
+        i = (int)(t - c0);
+        n = (int)(c1 - c0);
+    } else {
+        n = p.T / p.B;
+        b = t / n;
+        i = t - b * n;
+    }
+    const long long len = __ldg(p.seqlens + b);
+    const long long at = len - n + i;
+    int page = -1;
+    if (len >= n && len <= (long long)p.max_pages * p.page_size)
+        page = __ldg(p.page_table + (long long)b * p.max_pages + at / p.page_size);
+    if (page < 0 || page >= p.num_pages) {
+        if ((threadIdx.x & 31) == 0) atomicCAS(p.status, 0, kDevBadIndex);
+        return kRowBad;
+    }
+    return (long long)page * p.page_size + at % p.page_size;
+}
+
+}  // namespace attn

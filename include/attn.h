@@ -51,6 +51,17 @@ typedef int attn_status_t;
 /* 8-bit floating-point formats (OCP FP8) of attn_fwd_fp8 and attn_decode_paged_fp8 */
 #define ATTN_FP8_E4M3 0 /* 4 exponent bits (bias 7), 3 mantissa bits, largest 448, no infinities */
 #define ATTN_FP8_E5M2 1 /* 5 exponent bits (bias 15), 2 mantissa bits, largest 57344 */
+#define ATTN_KV_BF16 2  /* a paged cache in bf16, where a call takes the format of its cache */
+
+/* element types of attn_rope */
+#define ATTN_TYPE_BF16 0
+#define ATTN_TYPE_F32 1
+
+/* frequency tables of attn_rope_freqs */
+#define ATTN_ROPE_PLAIN 0  /* theta^(-2i/rot) */
+#define ATTN_ROPE_LINEAR 1 /* every frequency divided by the factor (position interpolation) */
+#define ATTN_ROPE_NTK 2    /* base theta * factor^(rot / (rot - 2)) */
+#define ATTN_ROPE_YARN 3   /* interpolated by parts, with an amplitude */
 
 /*
  * Forward attention ("FlashAttention: not computing less, moving less", section 01
@@ -217,6 +228,103 @@ attn_status_t attn_decode_paged_noalloc(const void* q, const void* k_cache, cons
                                         const int* seqlens, int page_size, void* o, float* lse, void* stream, int B,
                                         int Hq, int Hkv, int d, int max_pages_per_seq, int num_pages, float scale,
                                         int num_splits);
+
+/*
+ * Rotary positions of the rows of q and k: y = amplitude * R(position) x on the columns
+ * [rot_begin, rot_begin + rot_dim) of every head, the other columns copied. Pair i of a row at
+ * position n turns by the angle n * inv_freq[i]:
+ *   y1 = amplitude (x1 cos - x2 sin),  y2 = amplitude (x1 sin + x2 cos).
+ * With transpose = 1 the angle is negative: the gradient of the output goes in and the gradient
+ * of the input comes out.
+ *
+ * q, q_out   device, [T, Hq, d] in elem_type (ATTN_TYPE_BF16, ATTN_TYPE_F32); row t starts
+ *            q_stride (q_out_stride) elements after row t - 1, the heads of a row are contiguous
+ *            (so q and k may lie in the rows of one fused projection). Strides of inputs >= 0,
+ *            of outputs >= Hq * d. q_out may be q with the same stride (in place); other
+ *            overlaps are not allowed.
+ * k, k_out   the same for [T, Hk, d]; ignored when Hk = 0
+ * positions  device, int32 [T], any value
+ * inv_freq   device, float64 [rot_dim / 2], radians per position (attn_rope_freqs makes it). The
+ *            angle is reduced modulo a turn with 64-bit integers, so far positions keep their
+ *            precision; cos, sin and the products are fp32, rounded once to elem_type.
+ * T          rows (>= 0);  d  even, at most 1024;  rot_dim  even, > 0;  rot_begin >= 0
+ * interleaved  0: pair i is columns (i, i + rot_dim / 2) of the rotated part; 1: (2 i, 2 i + 1)
+ * amplitude  finite (attn_rope_freqs gives the one that belongs to its table)
+ * Alignment: q, k, q_out, k_out to their element; positions 4, inv_freq 8 bytes. Rows that start
+ * on 16-byte boundaries with d, rot_begin and rot_dim multiples of 32 bytes move 16 bytes at a
+ * time; others move element by element.
+ */
+attn_status_t attn_rope(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
+                        const double* inv_freq, int T, int Hq, int Hk, int d, int rot_begin, int rot_dim,
+                        long long q_stride, long long k_stride, long long q_out_stride, long long k_out_stride,
+                        int elem_type, int interleaved, int transpose, float amplitude, void* stream);
+
+/*
+ * Frequencies of attn_rope: host arithmetic in 64 bits, host pointers (copy the table to the
+ * device once). f_i = theta^(-2 i / rot_dim), i < rot_dim / 2, changed by `scaling` for contexts
+ * longer than the trained one by `factor` (>= 1; ignored for ATTN_ROPE_PLAIN):
+ *   ATTN_ROPE_LINEAR  f_i / factor
+ *   ATTN_ROPE_NTK     theta replaced by theta * factor^(rot_dim / (rot_dim - 2)); rot_dim > 2
+ *   ATTN_ROPE_YARN    g_i f_i + (1 - g_i) f_i / factor, with g_i = (r_i - beta_slow) /
+ *                     (beta_fast - beta_slow) clamped to [0, 1] and r_i = trained_len f_i / (2 pi)
+ *                     the turns within the trained length (> 0); *amplitude = 0.1 ln(factor) + 1
+ *                     (Peng et al., "YaRN", 2023, "NTK-by-parts")
+ * *amplitude is 1 otherwise. trained_len, beta_fast, beta_slow are used by ATTN_ROPE_YARN only.
+ */
+attn_status_t attn_rope_freqs(double* inv_freq, double* amplitude, int rot_dim, double theta, int scaling,
+                              double factor, double trained_len, double beta_fast, double beta_slow);
+
+/*
+ * Writes the new keys and values of each sequence into a paged cache, quantised where the cache is
+ * 8-bit: the caches that attn_decode_paged (ATTN_KV_BF16), attn_decode_paged_fp8 and
+ * attn_decode_paged_tree read.
+ *
+ * k, v       device, bf16 [T, Hkv, d], packed by sequence; rows k_stride (v_stride) elements apart
+ *            (>= 0, a multiple of 8), the heads of a row contiguous
+ * k_cache, v_cache  device, [num_pages, page_size, Hkv, d] in kv_format (written)
+ * page_table, page_size, max_pages_per_seq, num_pages  as for attn_decode_paged
+ * seqlens    device, int32 [B], cached tokens of each sequence with the new ones (what the decode
+ *            that follows takes): row i of the n rows of sequence b becomes its cached token
+ *            seqlens[b] - n + i
+ * cu_seqlens device, int32 [B+1], prefix offsets of the sequences' rows in k and v (non-decreasing,
+ *            empty sequences allowed), or NULL: T / B rows each. Rows of k and v behind the last
+ *            sequence are ignored.
+ * T          rows of k and v;  d  a multiple of 16, at most 256
+ * kv_format  ATTN_KV_BF16, ATTN_FP8_E4M3 or ATTN_FP8_E5M2
+ * k_descale, v_descale  finite, not 0; an 8-bit code is fp8(x / descale): nearest, ties to even;
+ *            magnitudes above the largest finite value, infinities among them, saturate; NaN stays
+ *            NaN. Ignored for ATTN_KV_BF16 (pass 1).
+ * positions, inv_freq, rot_begin, rot_dim, interleaved, amplitude  rotation of K on its way as in
+ *            attn_rope, in fp32 before the one rounding to the cache's format; rot_dim = 0: none
+ *            (positions and inv_freq may be NULL)
+ * A sequence whose length is below its rows or above its page table, a page outside
+ * [0, num_pages), and offsets that decrease or pass T are recorded as ATTN_ERR_DEVICE_BAD_INDEX;
+ * their rows are not written. Rows that name the same cache slot (pages shared between sequences)
+ * leave it to one of them, in pieces of 8 elements.
+ * Alignment: k, v, k_cache, v_cache 16 bytes; integers 4; inv_freq 8.
+ */
+attn_status_t attn_kv_write_paged(const void* k, const void* v, long long k_stride, long long v_stride, void* k_cache,
+                                  void* v_cache, const int* page_table, const int* seqlens, const int* cu_seqlens,
+                                  int page_size, int T, int B, int Hkv, int d, int max_pages_per_seq, int num_pages,
+                                  int kv_format, float k_descale, float v_descale, const int* positions,
+                                  const double* inv_freq, int rot_begin, int rot_dim, int interleaved, float amplitude,
+                                  void* stream);
+
+/*
+ * Reads cached tokens back as bf16 rows, for example a cached prefix for attn_fwd. The rows of
+ * sequence b (cu_seqlens, or T / B each) are its last cached tokens below seqlens[b], in order:
+ * the inverse of attn_kv_write_paged without rotation. 8-bit codes become descale * fp8(code),
+ * rounded once to bf16; bf16 caches are copied bit for bit.
+ *
+ * k, v  device, bf16 [T, Hkv, d] (written), strides >= Hkv * d. Rows behind the last sequence are
+ *       left as they were. Rows of a page outside [0, num_pages) or of a sequence whose length is
+ *       out of range are zeros, and ATTN_ERR_DEVICE_BAD_INDEX is recorded.
+ * Everything else is as for attn_kv_write_paged.
+ */
+attn_status_t attn_kv_read_paged(const void* k_cache, const void* v_cache, void* k, void* v, long long k_stride,
+                                 long long v_stride, const int* page_table, const int* seqlens, const int* cu_seqlens,
+                                 int page_size, int T, int B, int Hkv, int d, int max_pages_per_seq, int num_pages,
+                                 int kv_format, float k_descale, float v_descale, void* stream);
 
 /*
  * Host-side split choice of attn_decode_paged (the num_splits = 0 heuristic of "Faster,
