@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libattn_gb300.so")
@@ -46,7 +47,7 @@ ROPE_SCALINGS = {"plain": ATTN_ROPE_PLAIN, "linear": ATTN_ROPE_LINEAR, "ntk": AT
 
 #: every symbol the header declares
 EXPORTS = ("attn_fwd", "attn_fwd_hd", "attn_fwd_fp8", "attn_decode_paged", "attn_decode_paged_fp8", "attn_decode_paged_noalloc",
-           "attn_rope", "attn_rope_freqs", "attn_kv_write_paged", "attn_kv_read_paged", "attn_decode_plan",
+           "attn_rope", "attn_rope_freqs", "attn_kv_write_paged", "attn_kv_read_paged", "attn_decode_paged_tree", "attn_decode_plan",
            "attn_decode_workspace_bytes", "attn_status_string", "attn_get_device_status",
            "attn_set_option", "attn_get_option", "attn_read_counters", "attn_debug_exp2", "attn_debug_watchdog",
            "attn_version")
@@ -86,6 +87,8 @@ lib.attn_kv_write_paged.argtypes = [_vp, _vp, _ll, _ll] + [_vp] * 5 + [_i] * 8 +
 lib.attn_kv_write_paged.restype = _i
 lib.attn_kv_read_paged.argtypes = [_vp] * 4 + [_ll, _ll] + [_vp] * 3 + [_i] * 8 + [_f, _f, _vp]
 lib.attn_kv_read_paged.restype = _i
+lib.attn_decode_paged_tree.argtypes = [_vp] * 7 + [_i, _i] + [_vp] * 3 + [_i] * 8 + [_f, _i, _i, _f, _f]
+lib.attn_decode_paged_tree.restype = _i
 lib.attn_decode_plan.argtypes = [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_i), ctypes.POINTER(_i)]
 lib.attn_decode_plan.restype = _i
 lib.attn_decode_workspace_bytes.argtypes = [_i, _i, _i, _i]
@@ -118,12 +121,9 @@ def _ptr(x):
 
 def _stream(s):
     if s is None:
-        try:
-            import torch
-            if torch.cuda.is_available() and torch.cuda.is_initialized():
-                return torch.cuda.current_stream().cuda_stream
-        except ImportError:
-            pass
+        torch = sys.modules.get("torch")  # not imported: the caller does not use its streams
+        if torch is not None and torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
         return None
     if isinstance(s, int):
         return s
@@ -248,6 +248,19 @@ def attn_kv_read_paged(k_cache, v_cache, k, v, k_stride, v_stride, page_table, s
                                 int(d), int(max_pages_per_seq), int(num_pages), _code(KV_FORMATS, kv_format),
                                 float(k_descale), float(v_descale), _stream(stream))
     return _check(rc, "attn_kv_read_paged", raise_on_error)
+
+
+def attn_decode_paged_tree(q, k_cache, v_cache, page_table, seqlens, cu_seqlens, tree_mask, mask_words, page_size, o, lse,
+                           stream, T, B, max_q, Hq, Hkv, d, max_pages_per_seq, num_pages, scale, num_splits=0,
+                           kv_format="bf16", k_descale=1.0, v_descale=1.0, raise_on_error=True):
+    """Decode of a tree (or, without a mask, a chain) of drafted tokens per sequence; see
+    ``attn_decode_paged_tree`` in include/attn.h."""
+    rc = lib.attn_decode_paged_tree(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seqlens), _ptr(cu_seqlens),
+                                    _ptr(tree_mask), int(mask_words), int(page_size), _ptr(o), _ptr(lse), _stream(stream),
+                                    int(T), int(B), int(max_q), int(Hq), int(Hkv), int(d), int(max_pages_per_seq),
+                                    int(num_pages), float(scale), int(num_splits), _code(KV_FORMATS, kv_format),
+                                    float(k_descale), float(v_descale))
+    return _check(rc, "attn_decode_paged_tree", raise_on_error)
 
 
 def attn_decode_plan(B, Hq, Hkv, max_pages_per_seq, page_size, num_splits=0, num_sms=0):

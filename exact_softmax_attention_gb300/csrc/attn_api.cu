@@ -1,9 +1,10 @@
 // C ABI of the attention library: argument checks, TMA descriptors, launch planning,
 // the device status word and process-wide options. Every compute step runs in the
-// kernels of attn_fwd.cu and attn_decode.cu.
+// kernels of attn_fwd.cu, attn_decode.cu and attn_tree.cu.
 #include "attn.h"
 #include "decode_maps.cuh"
 #include "kernels.cuh"
+#include "tree.cuh"
 
 #include <cudaTypedefs.h>
 
@@ -538,6 +539,83 @@ attn_status_t attn_decode_paged_fp8(const void* q, const void* k_cache, const vo
     if (!(fabs(score_scale_log2) <= (double)FLT_MAX)) return ATTN_ERR_BAD_ARG;  // the kernels use it as a float
     return decode_paged(q, k_cache, v_cache, page_table, seqlens, page_size, o, lse, stream, B, Hq, Hkv, d,
                         max_pages_per_seq, num_pages, scale, num_splits, kv_format, k_descale, v_descale);
+}
+
+attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const void* v_cache, const int* page_table,
+                                     const int* seqlens, const int* cu_seqlens, const unsigned long long* tree_mask,
+                                     int mask_words, int page_size, void* o, float* lse, void* stream, int T, int B,
+                                     int max_q, int Hq, int Hkv, int d, int max_pages_per_seq, int num_pages,
+                                     float scale, int num_splits, int kv_format, float k_descale, float v_descale) {
+    if (!q || !k_cache || !v_cache || !page_table || !seqlens || !o || !lse) return ATTN_ERR_NULL_PTR;
+    if (kv_format != ATTN_FP8_E4M3 && kv_format != ATTN_FP8_E5M2 && kv_format != ATTN_KV_BF16) return ATTN_ERR_BAD_ARG;
+    if (!isfinite(k_descale) || !isfinite(v_descale)) return ATTN_ERR_BAD_ARG;
+    if (T < 0 || B < 0 || B > 65535 || max_q < 1 || max_q > 256 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hkv > 65535 ||
+        (d != 64 && d != 128) || page_size <= 0 || max_pages_per_seq <= 0 || num_pages <= 0 || num_splits < 0)
+        return ATTN_ERR_BAD_SHAPE;
+    const long long rows = (long long)max_q * (Hq / Hkv);  // of one kv head
+    if (rows > 65535) return ATTN_ERR_BAD_SHAPE;
+    if (tree_mask && (mask_words < 1 || mask_words > 4 || max_q > 64 * mask_words)) return ATTN_ERR_BAD_SHAPE;
+    if (!cu_seqlens && T > 0 && (B == 0 || T % B != 0 || T / B > max_q)) return ATTN_ERR_BAD_SHAPE;
+    if ((long long)num_pages * page_size > INT32_MAX) return ATTN_ERR_BAD_SHAPE;  // cache rows are 32-bit indices
+    const long long lmax = (long long)max_pages_per_seq * page_size;
+    if (lmax > INT32_MAX / 2 || (long long)T * Hq > INT32_MAX) return ATTN_ERR_BAD_SHAPE;
+    if (!isfinite(scale)) return ATTN_ERR_BAD_SHAPE;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(lse, 4) ||
+        !aligned(page_table, 4) || !aligned(seqlens, 4) || (cu_seqlens && !aligned(cu_seqlens, 4)) ||
+        (tree_mask && !aligned(tree_mask, 8)))
+        return ATTN_ERR_ALIGN;
+    const bool f8 = kv_format != ATTN_KV_BF16;
+    const double score_scale = (double)scale * (f8 ? (double)k_descale : 1.0);
+    if (!(fabs(score_scale) * 1.4426950408889634 <= (double)FLT_MAX)) return ATTN_ERR_BAD_ARG;  // a float in the kernels
+    if (B == 0 || T == 0) return ATTN_OK;
+    DeviceState* ds = nullptr;
+    attn_status_t st = device_state(&ds);
+    if (st != ATTN_OK) return st;
+    const Options opt = options();
+    attn::TreeParams p;
+    memset(&p, 0, sizeof p);
+    p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.page_table = page_table;
+    p.seqlens = seqlens;
+    p.cu_seqlens = cu_seqlens;
+    p.mask = tree_mask;
+    p.mask_words = tree_mask ? mask_words : 0;
+    p.o = reinterpret_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.B = B;
+    p.T = T;
+    p.max_q = max_q;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.page_size = page_size;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = num_pages;
+    attn::tree_plan(B, Hkv, (int)rows, lmax, num_splits, ds->num_sms, &p.chunk, &p.max_splits);
+    if ((long long)p.max_splits * Hkv * ((rows + 15) / 16) > INT32_MAX) return ATTN_ERR_BAD_SHAPE;  // grid columns
+    // a scale of 0 (or one that rounds to 0) makes every score 0: q times 0, factor 1
+    const double factor = (float)fabs(score_scale) > 0 ? fabs(score_scale) : 0.0;
+    p.q_sign = factor == 0 ? 0.0f : (score_scale < 0 ? -1.0f : 1.0f);
+    p.scale = factor == 0 ? 1.0f : (float)factor;
+    p.scale_log2 = (float)((factor == 0 ? 1.0 : factor) * 1.4426950408889634);
+    p.rescale_thr = (float)opt.rescale_threshold;
+    p.v_descale = f8 ? v_descale : 1.0f;
+    p.status = ds->status;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    void* ws = nullptr;
+    if (p.max_splits > 1) {
+        cudaMemPool_t pool = nullptr;
+        if ((st = device_pool(ds, &pool)) != ATTN_OK) return st;
+        const size_t n = (size_t)T * Hq * p.max_splits;
+        if (cudaMallocFromPoolAsync(&ws, n * ((size_t)d + 1) * sizeof(float), pool, s) != cudaSuccess) return ATTN_ERR_CUDA;
+        p.ws_o = reinterpret_cast<float*>(ws);
+        p.ws_lse = p.ws_o + n * d;
+    }
+    const cudaError_t e = attn::launch_attn_tree(p, d, kv_format, s);
+    if (ws) cudaFreeAsync(ws, s);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 attn_status_t attn_get_device_status(void* stream) {

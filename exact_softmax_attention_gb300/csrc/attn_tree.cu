@@ -1,0 +1,635 @@
+// Attention of the drafted tokens of each sequence over its paged cache (a tree of drafted tokens,
+// or a chain), for sm_103a.
+//
+// Sequence b has len cached tokens, the last n of them the drafted ones. Row (i, h), drafted token i
+// and query head h, sees the first len - n tokens and those drafted tokens j whose bit is set in
+// mask[i] (no mask: j <= i); o = softmax(scale q k^T) v over what it sees, with the online-softmax
+// recurrence. The n G rows of a kv head (G query heads each) are the rows of one product, so one
+// pass over the cache serves all drafted tokens. Several blocks share a long sequence (splits of
+// its keys) and a second kernel joins their partial results by log-sum-exp.
+//
+// Masked keys contribute exactly nothing, whatever their slots hold: scores are replaced by -inf,
+// and in the key tiles where a row may not see every key the non-finite values of V are taken out of
+// the product (0 times NaN would be NaN) and added to the rows that do see them at the end.
+#include "attn.h"
+#include "ptx.cuh"
+#include "tree.cuh"
+
+#include <math.h>
+
+namespace attn {
+namespace {
+
+__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+// Rows and cached tokens of sequence b. False: it has no rows in the output (none given, or offsets
+// out of range, which is recorded). A length out of range counts as 0 and is recorded.
+struct TreeSeq {
+    int q0, n;     // first row of q, rows
+    int len, ctx;  // cached tokens, those before the drafted ones
+};
+__device__ __forceinline__ bool tree_seq(const TreeParams& p, int b, TreeSeq& s) {
+    if (p.cu_seqlens) {
+        const long long c0 = __ldg(p.cu_seqlens + b), c1 = __ldg(p.cu_seqlens + b + 1);
+        if (c0 < 0 || c1 < c0 || c1 > p.T || c1 - c0 > p.max_q) {
+            if (threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadIndex);
+            return false;
+        }
+        s.q0 = (int)c0, s.n = (int)(c1 - c0);
+    } else {
+        s.n = p.T / p.B;
+        s.q0 = b * s.n;
+    }
+    if (s.n == 0) return false;
+    int len = __ldg(p.seqlens + b);
+    if (len != 0 && (len < s.n || len > (long long)p.max_pages * p.page_size)) {
+        if (threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadIndex);
+        len = 0;
+    }
+    s.len = len;
+    s.ctx = len - s.n;
+    return true;
+}
+
+// Bits of the keys kb .. kb + 63 that drafted token i of the sequence sees. row: its mask words, or
+// nullptr for a chain.
+__device__ __forceinline__ unsigned long long tree_window(const unsigned long long* row, int words, int i, int ctx, int len,
+                                                          int kb) {
+    const int rel = kb - ctx;  // drafted index of bit 0
+    unsigned long long w = ~0ull;
+    if (rel > -64) {
+        if (row) {
+            if (rel < 0) {
+                w = (__ldg(row) << -rel) | ((1ull << -rel) - 1);
+            } else {
+                const int x = rel >> 6, sh = rel & 63;
+                w = x < words ? __ldg(row + x) >> sh : 0;
+                if (sh && x + 1 < words) w |= __ldg(row + x + 1) << (64 - sh);
+            }
+        } else {
+            const int cnt = i - rel + 1;
+            w = cnt >= 64 ? ~0ull : (cnt <= 0 ? 0 : (1ull << cnt) - 1);
+        }
+    }
+    const int lim = len - kb;
+    if (lim < 64) w &= lim <= 0 ? 0 : (1ull << lim) - 1;
+    return w;
+}
+
+// Cache row of token tok of a sequence (pt: its row of the page table), or -1 for a page out of range.
+__device__ __forceinline__ int cache_row(const TreeParams& p, const int* pt, int tok) {
+    const int q = p.ps_magic ? (int)(__umulhi((unsigned)tok, p.ps_magic) >> p.ps_shift) : tok;
+    const int pg = __ldg(pt + q);
+    if (pg < 0 || pg >= p.num_pages) {
+        atomicCAS(p.status, 0, kDevBadIndex);
+        return -1;
+    }
+    return pg * p.page_size + (tok - q * p.page_size);  // < num_pages * page_size <= INT32_MAX
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t fp8x2_f16x2(uint32_t two_codes) {
+    const uint16_t v = (uint16_t)two_codes;
+    uint32_t d;
+    if (FMT == ATTN_FP8_E4M3)
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(v));
+    else
+        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(d) : "h"(v));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float half_value(uint16_t h) {
+    float f;
+    asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(h));
+    return f;
+}
+
+// Value e of a V row in the cache as a float (without the descale).
+template <int FMT>
+__device__ __forceinline__ float cached_value(const void* cache, long long e) {
+    if constexpr (FMT == ATTN_KV_BF16)
+        return __bfloat162float(static_cast<const __nv_bfloat16*>(cache)[e]);
+    else
+        return half_value((uint16_t)fp8x2_f16x2<FMT>(static_cast<const uint8_t*>(cache)[e]));
+}
+
+// Sum of the non-finite values in column d of the V rows of tokens [t0, t1) that row i sees: what the
+// products left out of the tiles where they took them for zero.
+template <int FMT>
+__device__ float nonfinite_sum(const TreeParams& p, const int* pt, const unsigned long long* mrow, int i, const TreeSeq& s,
+                               int t0, int t1, int kvh, int D, int d) {
+    float sum = 0.0f;
+    for (int t = t0; t < t1; ++t) {
+        if (!(tree_window(mrow, p.mask_words, i, s.ctx, s.len, t) & 1)) continue;
+        const int row = cache_row(p, pt, t);
+        if (row < 0) continue;
+        const float v = cached_value<FMT>(p.v_cache, ((long long)row * p.Hkv + kvh) * D + d);
+        if (!isfinite(v)) sum += v;
+    }
+    return sum;
+}
+
+// Is either 16-bit half of w non-finite (f16 when half_fmt, else bf16)? Mask with ones in the finite
+// halves.
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w, bool half_fmt) {
+    const uint32_t e = half_fmt ? 0x7C00u : 0x7F80u;
+    return ((w & e) == e ? 0u : 0xFFFFu) | (((w >> 16) & e) == e ? 0u : 0xFFFF0000u);
+}
+
+// ------------------------------------------------------------------------------ few rows
+//
+// One block of four warps per (sequence, split, kv head, group of 16 rows). Each warp streams its own
+// 16-token groups through a private three-stage cp.async ring (any page size: each row's address
+// comes from the page table), and multiplies with mma.sync, whose 16 rows are the group's rows: for
+// up to 16 rows per kv head the kernel is bounded by the cache reads, so a wider product would
+// only add work on padding. 8-bit codes become f16 pairs in registers (exact); the order of d
+// inside both products is permuted so that one 16-byte shared load feeds several products.
+
+constexpr int kWarps = 4;
+constexpr int kGroup = 16;
+constexpr int kStages = 3;
+
+template <int D, int FMT>
+struct SmallLayout {
+    static constexpr int kElem = FMT == ATTN_KV_BF16 ? 2 : 1;
+    static constexpr int kRow = D * kElem;         // bytes of a cached row of one head
+    static constexpr int kTile = kGroup * kRow;    // one K or V stage of a warp
+    static constexpr int kChunks = kRow / 16;
+    static constexpr int kRing = kWarps * kStages * 2 * kTile;
+    static constexpr int kMerge = (kWarps * 16 * D + 2 * kWarps * 16) * 4;
+    static constexpr int kBytes = kRing > kMerge ? kRing : kMerge;
+};
+
+// Byte offset of 16-byte chunk c of row r of a stage tile (rows of kChunks chunks, XOR swizzle).
+template <int kChunks>
+__device__ __forceinline__ uint32_t swz_chunk(int r, int c) {
+    constexpr int m = kChunks < 8 ? kChunks - 1 : 7;
+    return (uint32_t)(r * kChunks * 16 + ((c ^ (r & m)) << 4));
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[4]) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[2]) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+}
+
+// GN: row slots that hold rows (8 or 16).
+template <int D, int GN, int FMT>
+__global__ void __launch_bounds__(kWarps * 32) tree_small_kernel(const TreeParams p) {
+    grid_dependents_launch();
+    using L = SmallLayout<D, FMT>;
+    constexpr bool F8 = FMT != ATTN_KV_BF16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int odd_v;  // a V tile held a non-finite value that was taken out
+    const int HG = p.Hkv * p.groups;
+    const int b = blockIdx.y, split = (int)(blockIdx.x / (unsigned)HG), hg = (int)(blockIdx.x % (unsigned)HG);
+    const int kvh = hg / p.groups, r0 = (hg % p.groups) * 16;
+    TreeSeq s;
+    if (!tree_seq(p, b, s)) return;
+    const int R = min(16, s.n * p.G - r0);  // rows of this group
+    if (R <= 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nsplit = cdiv(s.len, p.chunk);
+    const int t_begin = split * p.chunk;
+    // output row of local row r: (s.q0 + i) * Hq + kvh * G + g with (i, g) = divmod(r0 + r, G)
+    auto out_row = [&](int r) {
+        const int i = (r0 + r) / p.G;
+        return (long long)(s.q0 + i) * p.Hq + kvh * p.G + (r0 + r - i * p.G);
+    };
+    if (s.len == 0) {
+        if (split == 0)
+            for (int x = threadIdx.x; x < R * D; x += blockDim.x) {
+                const long long orow = out_row(x / D);
+                p.o[orow * D + x % D] = __float2bfloat16(0.0f);
+                if (x % D == 0) p.lse[orow] = -INFINITY;
+            }
+        return;
+    }
+    if (t_begin >= s.len) return;
+    const int t_end = min(s.len, t_begin + p.chunk);
+    if (threadIdx.x == 0) odd_v = 0;
+    __syncthreads();
+
+    const int g0 = lane >> 2, qd = lane & 3;
+    const bool v0 = g0 < R, v1 = GN == 16 && g0 + 8 < R;
+    // what the lane's two rows see among the drafted tokens; rows of padding see every key
+    const int i0 = v0 ? (r0 + g0) / p.G : s.n - 1, i1 = v1 ? (r0 + g0 + 8) / p.G : s.n - 1;
+    const unsigned long long* mrow0 = p.mask ? p.mask + (long long)(s.q0 + i0) * p.mask_words : nullptr;
+    const unsigned long long* mrow1 = p.mask ? p.mask + (long long)(s.q0 + i1) * p.mask_words : nullptr;
+
+    // ---- query fragments. 8-bit caches: column 2 qd + e of k-step kk is d = (D/4) qd + 4 kk + e,
+    // column 2 qd + 8 + e is that + 2
+    uint32_t aq[D / 16][4];
+    {
+        const uint32_t* q0p = reinterpret_cast<const uint32_t*>(p.q + (v0 ? out_row(g0) : 0) * D);
+        const uint32_t* q1p = reinterpret_cast<const uint32_t*>(p.q + (v1 ? out_row(g0 + 8) : 0) * D);
+        auto word = [&](const uint32_t* src, bool valid, int c) -> uint32_t {
+            if (!valid) return 0u;
+            const uint32_t w = __ldg(src + c);
+            const float lo = __uint_as_float(w << 16) * p.q_sign, hi = __uint_as_float(w & 0xFFFF0000u) * p.q_sign;
+            return F8 ? pack_half2(lo, hi) : pack_bf16x2(lo, hi);
+        };
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const int c = F8 ? (D / 8) * qd + 2 * kk : kk * 8 + qd, step = F8 ? 1 : 4;
+            aq[kk][0] = word(q0p, v0, c);
+            aq[kk][1] = word(q1p, v1, c);
+            aq[kk][2] = word(q0p, v0, c + step);
+            aq[kk][3] = word(q1p, v1, c + step);
+        }
+    }
+
+    // ---- the warp's ring: token groups t_begin + 16 (warp + 4 i)
+    const uint32_t ring = smem_u32(smem) + warp * kStages * 2 * L::kTile;
+    const int* pt = p.page_table + (long long)b * p.max_pages;
+    const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache);
+    const uint8_t* vc = static_cast<const uint8_t*>(p.v_cache);
+    constexpr int kRowsPerIter = 32 / L::kChunks;
+    const int my_chunk = lane % L::kChunks, my_row = lane / L::kChunks;
+    const long long row_bytes = (long long)p.Hkv * L::kRow;
+    const int col = kvh * L::kRow + my_chunk * 16;
+    const int total = cdiv(t_end - t_begin, kGroup);
+    const int mine = total > warp ? cdiv(total - warp, kWarps) : 0;
+    auto issue = [&](int i) {
+        const int tok = t_begin + kGroup * (warp + kWarps * i) + (lane & 15);
+        const int row = tok < t_end ? cache_row(p, pt, tok) : -1;  // no token or a bad page: zeros
+        const uint32_t kd = ring + (i % kStages) * 2 * L::kTile, vd = kd + L::kTile;
+#pragma unroll
+        for (int it = 0; it < kGroup / kRowsPerIter; ++it) {
+            const int r = it * kRowsPerIter + my_row;
+            const int rr = __shfl_sync(0xffffffffu, row, r);
+            const long long off = rr >= 0 ? rr * row_bytes + col : 0;
+            const uint32_t n = rr >= 0 ? 16u : 0u;
+            cp_async16(kd + swz_chunk<L::kChunks>(r, my_chunk), kc + off, n);
+            cp_async16(vd + swz_chunk<L::kChunks>(r, my_chunk), vc + off, n);
+        }
+    };
+
+    constexpr int NH = GN / 8;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    float oacc[NH][D / 16][4] = {};
+    const float sl2 = p.scale_log2;
+    const int lm_row = (lane & 7) + ((lane >> 4) << 3), lm_par = (lane >> 3) & 1;
+
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i < mine) issue(i);
+        cp_async_commit();
+    }
+    for (int i = 0; i < mine; ++i) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();
+        if (i + kStages - 1 < mine) issue(i + kStages - 1);
+        cp_async_commit();
+        const uint32_t kt = ring + (i % kStages) * 2 * L::kTile, vt = kt + L::kTile;
+        const int g = t_begin + kGroup * (warp + kWarps * i);
+
+        // S = Q K^T: rows of the group x 16 tokens
+        float sc[2][4] = {};
+        if constexpr (F8) {
+            constexpr int W = D / 64;  // 16-byte chunks of K bytes per lane and token
+            uint32_t kw[2][W][4];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int j = 0; j < W; ++j) lds_words(kt + swz_chunk<L::kChunks>(g0 + 8 * nt, W * qd + j), kw[nt][j]);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const uint32_t w = kw[nt][kk >> 2][kk & 3];
+                    mma_f16(sc[nt], aq[kk], fp8x2_f16x2<FMT>(w), fp8x2_f16x2<FMT>(w >> 16));
+                }
+        } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                uint32_t b0, b1, b2, b3;
+                ldmatrix_x4(kt + swz_chunk<L::kChunks>(lm_row, 2 * kk + lm_par), b0, b1, b2, b3);
+                mma_bf16_16816(sc[0], aq[kk], b0, b1);
+                mma_bf16_16816(sc[1], aq[kk], b2, b3);
+            }
+        }
+        if (g + kGroup > s.ctx) {  // drafted tokens, or the end of the sequence
+            const uint32_t w0 = (uint32_t)tree_window(mrow0, p.mask_words, i0, s.ctx, s.len, g);
+            const uint32_t w1 = (uint32_t)tree_window(mrow1, p.mask_words, i1, s.ctx, s.len, g);
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int bit = 2 * qd + 8 * nt + e;
+                    if (!((w0 >> bit) & 1)) sc[nt][e] = -INFINITY;
+                    if (!((w1 >> bit) & 1)) sc[nt][2 + e] = -INFINITY;
+                }
+            // take non-finite values out of V (in place; the rows that see them get them at the end)
+            bool odd = false;
+            for (int c = lane; c < L::kTile / 16; c += 32) {
+                uint32_t w[4];
+                const uint32_t at = vt + 16 * c;
+                lds_words(at, w);
+                bool bad = false;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t keep;
+                    if constexpr (F8) {  // a code is non-finite when its f16 value is
+                        const uint32_t lo = finite_halves(fp8x2_f16x2<FMT>(w[x]), true);
+                        const uint32_t hi = finite_halves(fp8x2_f16x2<FMT>(w[x] >> 16), true);
+                        keep = __byte_perm(lo, hi, 0x6420);
+                    } else {
+                        keep = finite_halves(w[x], false);
+                    }
+                    bad |= keep != 0xFFFFFFFFu;
+                    w[x] &= keep;
+                }
+                if (bad)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                 : "memory");
+                odd |= bad;
+            }
+            if (odd) odd_v = 1;
+            __syncwarp();
+        }
+
+        float mx0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+        float mx1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+        const float mc0 = fmaxf(m0, mx0), mc1 = fmaxf(m1, mx1);
+        const bool need = ((mc0 - m0) * sl2 > p.rescale_thr) || (GN == 16 && (mc1 - m1) * sl2 > p.rescale_thr);
+        if (__any_sync(0xffffffffu, need)) {
+            const float a0 = m0 == -INFINITY ? 0.0f : ex2_mufu((m0 - mc0) * sl2);
+            const float a1 = m1 == -INFINITY ? 0.0f : ex2_mufu((m1 - mc1) * sl2);
+            l0 *= a0, l1 *= a1;
+            m0 = mc0, m1 = mc1;
+            const int src = qd * 8;  // lane of row 2 qd; O^T columns are rows 2 qd, 2 qd + 1 (+ 8)
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh) {
+                const float c0 = __shfl_sync(0xffffffffu, nh ? a1 : a0, src);
+                const float c1 = __shfl_sync(0xffffffffu, nh ? a1 : a0, src + 4);
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt) {
+                    oacc[nh][mt][0] *= c0;
+                    oacc[nh][mt][1] *= c1;
+                    oacc[nh][mt][2] *= c0;
+                    oacc[nh][mt][3] *= c1;
+                }
+            }
+        }
+        const float n0 = m0 == -INFINITY ? 0.0f : -m0 * sl2, n1 = m1 == -INFINITY ? 0.0f : -m1 * sl2;
+        float pr[2][4];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            pr[nt][0] = ex2_mufu(fmaf(sc[nt][0], sl2, n0));
+            pr[nt][1] = ex2_mufu(fmaf(sc[nt][1], sl2, n0));
+            pr[nt][2] = ex2_mufu(fmaf(sc[nt][2], sl2, n1));
+            pr[nt][3] = ex2_mufu(fmaf(sc[nt][3], sl2, n1));
+        }
+        l0 += (pr[0][0] + pr[0][1]) + (pr[1][0] + pr[1][1]);
+        l1 += (pr[0][2] + pr[0][3]) + (pr[1][2] + pr[1][3]);
+        // O^T += V^T P^T; P is rounded to the 16-bit type of the product (bf16, or f16 for 8-bit caches)
+        uint32_t pb[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float lo = pr[x & 1][2 * (x >> 1)], hi = pr[x & 1][2 * (x >> 1) + 1];
+            pb[x] = F8 ? pack_half2(lo, hi) : pack_bf16x2(lo, hi);
+        }
+        if constexpr (F8) {
+            // tokens 2 qd, 2 qd + 1, 2 qd + 8, 2 qd + 9; bytes [(D/8) g0, (D/8) g0 + D/8) of each
+            uint32_t vw[4][D / 32];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int tok = 2 * qd + (t & 1) + 8 * (t >> 1);
+                if constexpr (D == 128)
+                    lds_words(vt + swz_chunk<L::kChunks>(tok, g0), vw[t]);
+                else
+                    lds_words(vt + swz_chunk<L::kChunks>(tok, g0 >> 1) + (g0 & 1) * 8, vw[t]);
+            }
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+                const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;  // bytes 2 j and 2 j + 1 of both tokens
+                const uint32_t lo = __byte_perm(vw[0][mt >> 1], vw[1][mt >> 1], sel);
+                const uint32_t hi = __byte_perm(vw[2][mt >> 1], vw[3][mt >> 1], sel);
+                const uint32_t a[4] = {fp8x2_f16x2<FMT>(lo), fp8x2_f16x2<FMT>(lo >> 16), fp8x2_f16x2<FMT>(hi),
+                                       fp8x2_f16x2<FMT>(hi >> 16)};
+                mma_f16(oacc[0][mt], a, pb[0], pb[1]);
+                if (GN == 16) mma_f16(oacc[NH - 1][mt], a, pb[2], pb[3]);
+            }
+        } else {
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+                uint32_t a[4];
+                ldmatrix_x4_trans(vt + swz_chunk<L::kChunks>(lm_row, 2 * mt + lm_par), a[0], a[1], a[2], a[3]);
+                mma_bf16_16816(oacc[0][mt], a, pb[0], pb[1]);
+                if (GN == 16) mma_bf16_16816(oacc[NH - 1][mt], a, pb[2], pb[3]);
+            }
+        }
+    }
+    cp_async_wait<0>();
+
+    // ---- merge the warps through shared memory: sm_o[warp][row][d], maxima, sums
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    __syncthreads();  // every warp is done with its ring
+    float* sm_o = reinterpret_cast<float*>(smem);
+    float* sm_m = sm_o + kWarps * GN * D;
+    float* sm_l = sm_m + kWarps * GN;
+    if (qd == 0) {
+        sm_m[warp * GN + g0] = m0;
+        sm_l[warp * GN + g0] = l0;
+        if (GN == 16) {
+            sm_m[warp * GN + g0 + 8] = m1;
+            sm_l[warp * GN + g0 + 8] = l1;
+        }
+    }
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+            // rows of O^T: d, in the permuted order of the 8-bit products
+            const int d0 = F8 ? (D / 8) * g0 + 2 * mt : mt * 16 + g0, d1 = F8 ? d0 + 1 : d0 + 8;
+            float* base = sm_o + (warp * GN + nh * 8 + 2 * qd) * D;
+            base[d0] = oacc[nh][mt][0];
+            base[D + d0] = oacc[nh][mt][1];
+            base[d1] = oacc[nh][mt][2];
+            base[D + d1] = oacc[nh][mt][3];
+        }
+    __syncthreads();
+    const bool odd = odd_v != 0;
+    for (int x = threadIdx.x; x < R * D; x += blockDim.x) {
+        const int r = x / D, d = x - r * D;
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w * GN + r]);
+        float ll = 0.0f, acc = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            // a warp without a visible key has m = -inf and only zeros (or NaN, which has to stay)
+            const float mw = sm_m[w * GN + r];
+            const float f = mw == -INFINITY ? 1.0f : ex2_mufu((mw - mm) * sl2);
+            ll += f * sm_l[w * GN + r];
+            acc += f * sm_o[(w * GN + r) * D + d];
+        }
+        if (odd) {
+            const int i = (r0 + r) / p.G;
+            acc += nonfinite_sum<FMT>(p, pt, p.mask ? p.mask + (long long)(s.q0 + i) * p.mask_words : nullptr, i, s,
+                                      max(t_begin, s.ctx / kGroup * kGroup), t_end, kvh, D, d);
+        }
+        const float o = ll == 0.0f ? 0.0f : acc / ll * p.v_descale;
+        const float lse = ll == 0.0f ? -INFINITY : mm * p.scale + logf(ll);
+        const long long orow = out_row(r);
+        if (nsplit == 1) {
+            p.o[orow * D + d] = __float2bfloat16(o);
+            if (d == 0) p.lse[orow] = lse;
+        } else {
+            p.ws_o[(orow * p.max_splits + split) * D + d] = o;
+            if (d == 0) p.ws_lse[orow * p.max_splits + split] = lse;
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------ join of the splits
+//
+// One warp per output row: LSE = log sum_s exp(lse_s), O = sum_s exp(lse_s - LSE) O_s in split order.
+// Launched as a programmatic dependent of the split kernel; rows of one split are already written.
+template <int D>
+__global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    TreeSeq s;
+    const bool rows = tree_seq(p, blockIdx.y, s);
+    const long long r = (long long)blockIdx.x * 4 + warp;
+    grid_dependency_wait();
+    if (!rows || r >= (long long)s.n * p.Hq) return;
+    const int ns = cdiv(s.len, p.chunk);
+    if (ns <= 1) return;
+    const long long row = (long long)s.q0 * p.Hq + r;
+    const float* wl = p.ws_lse + row * p.max_splits;
+    const float* wo = p.ws_o + row * p.max_splits * D;
+    float mx = -INFINITY;
+    for (int i = lane; i < ns; i += 32) mx = fmaxf(mx, wl[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    // a split that the row sees nothing of has -inf and weight 0; a NaN stays
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    float sum = 0.0f;
+    for (int i = lane; i < ns; i += 32) sum += expf(wl[i] - base);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    constexpr int PER = D / 32;
+    float acc[PER] = {};
+    if (sum != 0.0f) {
+        const float lse = base + logf(sum);
+        for (int i = 0; i < ns; ++i) {
+            const float li = wl[i];
+            if (li == -INFINITY) continue;  // its partial output is zeros
+            const float w = expf(li - lse);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] += w * wo[(long long)i * D + lane * PER + e];
+        }
+        if (lane == 0) p.lse[row] = lse;
+    } else if (lane == 0) {
+        p.lse[row] = -INFINITY;
+    }
+    __nv_bfloat16* out = p.o + row * D + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e], acc[e + 1]);
+}
+
+template <int D>
+cudaError_t launch_join(const TreeParams& p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((long long)p.max_q * p.Hq + 3) / 4), (unsigned)p.B);
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D>, p);
+}
+
+template <int D, int GN, int FMT>
+cudaError_t launch_small(TreeParams p, cudaStream_t stream) {
+    constexpr int bytes = SmallLayout<D, FMT>::kBytes;
+    static std::atomic<bool> attr_set[kMaxAttrDevices];
+    cudaError_t e = ensure_smem_attr(tree_small_kernel<D, GN, FMT>, bytes, attr_set);
+    if (e != cudaSuccess) return e;
+    p.groups = (int)(((long long)p.max_q * p.G + 15) / 16);
+    const long long x = (long long)p.max_splits * p.Hkv * p.groups;
+    if (x > INT32_MAX) return cudaErrorInvalidConfiguration;
+    tree_small_kernel<D, GN, FMT><<<dim3((unsigned)x, (unsigned)p.B), kWarps * 32, bytes, stream>>>(p);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && p.max_splits > 1) e = launch_join<D>(p, stream);
+    return e;
+}
+
+template <int D, int FMT>
+cudaError_t launch_rows(const TreeParams& p, cudaStream_t stream) {
+    return (long long)p.max_q * p.G <= 8 ? launch_small<D, 8, FMT>(p, stream) : launch_small<D, 16, FMT>(p, stream);
+}
+
+template <int D>
+cudaError_t launch_fmt(const TreeParams& p, int fmt, cudaStream_t stream) {
+    return fmt == ATTN_FP8_E4M3   ? launch_rows<D, ATTN_FP8_E4M3>(p, stream)
+           : fmt == ATTN_FP8_E5M2 ? launch_rows<D, ATTN_FP8_E5M2>(p, stream)
+                                  : launch_rows<D, ATTN_KV_BF16>(p, stream);
+}
+
+}  // namespace
+
+void tree_plan(int B, int Hkv, int rows, long long lmax, int num_splits, int num_sms, int* chunk, int* max_splits) {
+    long long c;
+    if (num_splits > 0) {
+        c = (lmax + num_splits - 1) / num_splits;
+    } else {
+        const long long groups = (rows + 15) / 16;
+        const long long work = (long long)B * Hkv * groups * ((lmax + 1) / 2);
+        c = (work + 18LL * num_sms - 1) / (18LL * num_sms);
+        if (c < 256) c = 256;
+        if (c < 128LL * (rows < 16 ? rows : 16)) c = 128LL * (rows < 16 ? rows : 16);
+        if (c > 8192) c = 8192;
+    }
+    c = (c + 63) / 64 * 64;
+    const long long whole = (lmax + 63) / 64 * 64;
+    if (c > whole) c = whole;
+    if (c < 64) c = 64;
+    *chunk = (int)c;
+    *max_splits = (int)((lmax + c - 1) / c);
+}
+
+cudaError_t launch_attn_tree(const TreeParams& p_in, int d, int kv_format, cudaStream_t stream) {
+    TreeParams p = p_in;
+    // tok / page_size for tok < 2^31: multiplier ceil(2^(31+k) / page_size), k = ceil(log2 page_size)
+    p.ps_magic = 0;
+    p.ps_shift = 0;
+    if (p.page_size > 1) {
+        int k = 0;
+        while ((1LL << k) < p.page_size) ++k;
+        p.ps_magic = (unsigned)(((1ULL << (31 + k)) + (unsigned long long)p.page_size - 1) / (unsigned long long)p.page_size);
+        p.ps_shift = k - 1;
+    }
+    return d == 128 ? launch_fmt<128>(p, kv_format, stream) : launch_fmt<64>(p, kv_format, stream);
+}
+
+}  // namespace attn

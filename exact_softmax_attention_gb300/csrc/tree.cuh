@@ -1,0 +1,39 @@
+// Interface between attn_api.cu and attn_tree.cu: attention of drafted tokens over a paged cache.
+#pragma once
+
+#include "kernels.cuh"
+
+namespace attn {
+
+struct TreeParams {
+    const __nv_bfloat16* q;  // [T, Hq, d]
+    const void* k_cache;     // [num_pages, page_size, Hkv, d], bf16 or 8-bit codes
+    const void* v_cache;
+    const int* page_table;   // [B, max_pages]
+    const int* seqlens;      // [B], the drafted tokens included
+    const int* cu_seqlens;   // [B + 1] or nullptr: T / B rows each
+    const unsigned long long* mask;  // [T, mask_words] or nullptr: a chain
+    int mask_words;
+    __nv_bfloat16* o;        // [T, Hq, d]
+    float* lse;              // [T, Hq]
+    float* ws_o;             // [T, Hq, max_splits, d] partial outputs
+    float* ws_lse;           // [T, Hq, max_splits]
+    int B, T, max_q, Hq, Hkv, G, page_size, max_pages, num_pages;
+    int chunk, max_splits;   // tokens per split (a multiple of 64), splits of the longest sequence
+    int groups;              // row groups per kv head (rows: drafted token x query head of the kv head)
+    // q is multiplied by q_sign (-1, 0, 1) and the scores by |scale|, so that masking and maxima
+    // work on scores that grow with q.k for every finite scale (scale 0: q_sign 0, factor 1)
+    float q_sign, scale, scale_log2;  // |scale| (key descale included), times log2(e)
+    float v_descale, rescale_thr;
+    unsigned int ps_magic;   // tok / page_size by multiplication, as in DecodeParams
+    int ps_shift;
+    int* status;
+};
+
+// kv_format: ATTN_KV_BF16, ATTN_FP8_E4M3, ATTN_FP8_E5M2; d 64 or 128.
+cudaError_t launch_attn_tree(const TreeParams& p, int d, int kv_format, cudaStream_t stream);
+
+// Tokens per split and splits of the longest sequence (lmax tokens).
+void tree_plan(int B, int Hkv, int rows, long long lmax, int num_splits, int num_sms, int* chunk, int* max_splits);
+
+}  // namespace attn

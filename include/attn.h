@@ -327,6 +327,52 @@ attn_status_t attn_kv_read_paged(const void* k_cache, const void* v_cache, void*
                                  int kv_format, float k_descale, float v_descale, void* stream);
 
 /*
+ * Decode of several new tokens per sequence over a paged cache: a tree of drafted tokens (to be
+ * verified in one step), or a chain of them.
+ *
+ * The last n cached tokens of sequence b are its drafted tokens (written before, for example by
+ * attn_kv_write_paged), in the order of its rows of q. Row i sees every cached token before the
+ * drafted ones and those drafted tokens j whose bit is set in its mask.
+ *
+ * q          device, bf16 [T, Hq, d], packed by sequence
+ * k_cache, v_cache  device, [num_pages, page_size, Hkv, d] in kv_format (ATTN_KV_BF16, or codes in
+ *            ATTN_FP8_E4M3 / ATTN_FP8_E5M2 that stand for descale * fp8(code))
+ * page_table, page_size, max_pages_per_seq, num_pages  as for attn_decode_paged
+ * seqlens    device, int32 [B], cached tokens of each sequence, the drafted ones included. A
+ *            sequence of length 0 gets o = 0, lse = -inf; so does one whose length is below its rows
+ *            or above its page table, which is recorded as ATTN_ERR_DEVICE_BAD_INDEX.
+ * cu_seqlens device, int32 [B+1], prefix offsets of the sequences' rows in q, o and lse
+ *            (non-decreasing, empty sequences allowed), or NULL: T / B rows each. Rows behind the
+ *            last sequence, and of one whose offsets decrease, pass T or hold more than max_q rows
+ *            (recorded), are left as they were.
+ * tree_mask  device, uint64 [T, mask_words] (int64 storage will do): bit j % 64 of word j / 64 of
+ *            row i is set when drafted token i sees drafted token j of its sequence (usually its
+ *            ancestors and itself). Bits at or above n are ignored; a row that sees no token at all
+ *            gets o = 0 and lse = -inf. NULL: token i sees the drafted tokens 0 .. i.
+ * o, lse     device, bf16 [T, Hq, d] and fp32 [T, Hq] as for attn_decode_paged (written)
+ * max_q      largest number of rows of a sequence, 1 .. 256 (at least T / B without cu_seqlens; at
+ *            most 64 * mask_words with a mask); max_q * Hq / Hkv at most 65535
+ * mask_words words per row of tree_mask, 1 .. 4 (ignored without a mask)
+ * Hq, Hkv, d as for attn_decode_paged (d = 64 or 128); scale finite
+ * num_splits 0: choose the number of key splits from the SM count and the sizes; n > 0: at most n
+ * k_descale, v_descale  finite; ignored for ATTN_KV_BF16 (pass 1)
+ * What a masked or unused cache slot holds does not matter, NaN and infinities included. A page
+ * outside [0, num_pages) is not read: its rows count as zeros and ATTN_ERR_DEVICE_BAD_INDEX is
+ * recorded.
+ * Arithmetic: products of 16-bit values on the tensor cores with fp32 accumulation (8-bit codes are
+ * widened exactly to f16 and q is converted to f16, see attn_decode_paged_fp8), fp32 softmax,
+ * probabilities rounded to bf16 (8-bit caches: f16) for the second product.
+ * Workspace, launches and programmatic dependents as for attn_decode_paged: partial outputs of the
+ * splits (T * Hq * splits * (d + 1) floats) from the library's stream-ordered pool on `stream`.
+ * Alignment: q, o, k_cache, v_cache 16 bytes; tree_mask 8; lse, page_table, seqlens, cu_seqlens 4.
+ */
+attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const void* v_cache, const int* page_table,
+                                     const int* seqlens, const int* cu_seqlens, const unsigned long long* tree_mask,
+                                     int mask_words, int page_size, void* o, float* lse, void* stream, int T, int B,
+                                     int max_q, int Hq, int Hkv, int d, int max_pages_per_seq, int num_pages,
+                                     float scale, int num_splits, int kv_format, float k_descale, float v_descale);
+
+/*
  * Host-side split choice of attn_decode_paged (the num_splits = 0 heuristic of "Faster,
  * more flexible FA4 for LLM inference", PR 1940 section; the pages give no formula).
  * Writes the tokens per split (*chunk, a multiple of 64) and the splits the workspace

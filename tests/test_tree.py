@@ -1,0 +1,422 @@
+"""attn_decode_paged_tree: refusals on the CPU; on the GPU every row and head against 64-bit
+arithmetic with a bound that counts the roundings, over formats, head layouts, lengths, page sizes,
+masks that leave rows empty, and slots that hold anything."""
+import math
+
+import numpy as np
+import pytest
+
+from helpers import ensure_built
+
+torch = pytest.importorskip("torch")
+DEV = "cuda:0"
+BIG = {"e4m3": 448.0, "e5m2": 57344.0}
+
+
+@pytest.fixture(scope="module")
+def A():
+    ensure_built()
+    import exact_softmax_attention_gb300 as mod
+    return mod
+
+
+# ------------------------------------------------------------------------------------- CPU
+
+def status(A, **kw):
+    a = dict(q=0x1000, k_cache=0x2000, v_cache=0x3000, page_table=0x4000, seqlens=0x5000, cu_seqlens=None, tree_mask=0x6000,
+             mask_words=1, page_size=16, o=0x7000, lse=0x8000, stream=0, T=0, B=1, max_q=8, Hq=8, Hkv=2, d=128,
+             max_pages_per_seq=4, num_pages=8, scale=0.1, num_splits=0, kv_format="e4m3", k_descale=0.5, v_descale=2.0)
+    a.update(kw)
+    return A.attn_decode_paged_tree(**a, raise_on_error=False)
+
+
+def test_refusals(A):
+    null, shape, align, arg = A.ATTN_ERR_NULL_PTR, A.ATTN_ERR_BAD_SHAPE, A.ATTN_ERR_ALIGN, A.ATTN_ERR_BAD_ARG
+    assert status(A) == A.ATTN_OK and status(A, B=0) == A.ATTN_OK and status(A, tree_mask=None, mask_words=9) == A.ATTN_OK
+    for name in ("q", "k_cache", "v_cache", "page_table", "seqlens", "o", "lse"):
+        assert status(A, **{name: None}) == null
+    for bad in (dict(T=-1), dict(B=-1), dict(B=65536), dict(max_q=0), dict(max_q=257, mask_words=4), dict(max_q=65), dict(mask_words=0),
+                dict(mask_words=5), dict(Hq=0), dict(Hq=9), dict(Hkv=0), dict(d=96), dict(page_size=0), dict(max_pages_per_seq=0),
+                dict(num_pages=0), dict(num_splits=-1), dict(T=9, B=2), dict(T=9, B=1), dict(T=4, B=0),
+                dict(num_pages=1 << 27), dict(max_pages_per_seq=1 << 27), dict(scale=float("nan")),
+                dict(max_q=64, Hq=2048, Hkv=1)):
+        assert status(A, **bad) == shape, bad
+    for bad in (dict(kv_format=3), dict(k_descale=float("nan")), dict(v_descale=float("inf")), dict(scale=1e30, k_descale=1e30)):
+        assert status(A, **bad) == arg, bad
+    for bad in (dict(q=0x1008), dict(o=0x7008), dict(k_cache=0x2001), dict(v_cache=0x3008), dict(lse=0x8002), dict(page_table=0x4001),
+                dict(seqlens=0x5002), dict(cu_seqlens=0x9002), dict(tree_mask=0x6004)):
+        assert status(A, **bad) == align, bad
+
+
+# ------------------------------------------------------------------------------------- GPU
+
+def random_tree(rs, n):
+    """Ancestor bits of a random tree of n nodes, each node's parent one before it (or the context)."""
+    seen = np.zeros((n, n), bool)
+    for i in range(n):
+        p = rs.randint(-1, i) if i else -1
+        if p >= 0:
+            seen[i] = seen[p]
+        seen[i, i] = True
+    return seen
+
+
+class Case:
+    """n[b] drafted of lens[b] cached tokens; tree: "tree", "chain", "any" (random bits, some rows
+    empty), "none" (no drafted token sees any)."""
+
+    def __init__(self, fmt, Hq, Hkv, d, page, n, lens, tree="tree", seed=0, dense=False, qmult=1.0, tail=2):
+        rs = np.random.RandomState(seed)
+        self.fmt, self.Hq, self.Hkv, self.d, self.page, self.n, self.lens, self.dense = fmt, Hq, Hkv, d, page, n, lens, dense
+        self.B, self.T = len(n), sum(n) + (0 if dense else tail)
+        self.max_q = max(1, max(n))
+        pages = [-(-l // page) for l in lens]
+        self.num, self.width = sum(pages) + 2, max(1, max(pages))
+        perm, at = rs.permutation(self.num), 0
+        self.pt = np.full((self.B, self.width), 2**31 - 1, np.int32)  # unused entries are never read
+        for b, c in enumerate(pages):
+            self.pt[b, :c] = perm[at:at + c]
+            at += c
+        shape = (self.num, page, Hkv, d)
+        self.ds = (1.0, 1.0) if fmt == "bf16" else (0.02, 0.03)
+        x = torch.from_numpy(rs.standard_normal((2, *shape)).astype(np.float32))
+        if fmt == "bf16":
+            self.c = [y.bfloat16().to(DEV) for y in x]
+        else:
+            t = torch.float8_e4m3fn if fmt == "e4m3" else torch.float8_e5m2
+            self.c = [(y / s).to(t).view(torch.uint8).to(DEV) for y, s in zip(x, self.ds)]
+        self.q = (torch.from_numpy(rs.standard_normal((self.T, Hq, d))) * qmult).bfloat16().to(DEV)
+        self.cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+        self.seen = [np.tril(np.ones((m, m), bool)) if tree == "chain" else np.zeros((m, m), bool) if tree == "none"
+                     else rs.rand(m, m) < 0.2 if tree == "any" else random_tree(rs, m) for m in n]
+        self.words = -(-self.max_q // 64)
+        bits = np.full((self.T, self.words), 2**64 - 1, np.uint64)  # bits at and above n are ignored
+        for b, m in enumerate(n):
+            for i in range(m):
+                v = (2**(64 * self.words) - 1) >> m << m
+                for j in range(m):
+                    v |= int(self.seen[b][i, j]) << j
+                for w in range(self.words):
+                    bits[self.cu[b] + i, w] = (v >> (64 * w)) & (2**64 - 1)
+        self.mask = None if tree == "chain" else torch.from_numpy(bits.view(np.int64)).to(DEV)
+        self.scale = 1.0 / math.sqrt(d)
+        self.dev = {"pt": torch.from_numpy(self.pt).to(DEV), "lens": torch.tensor(lens, dtype=torch.int32, device=DEV),
+                    "cu": None if dense else torch.from_numpy(self.cu).to(DEV)}
+        self.o = torch.full((self.T, Hq, d), 7.0, dtype=torch.bfloat16, device=DEV)
+        self.lse = torch.full((self.T, Hq), 7.0, dtype=torch.float32, device=DEV)
+
+    def run(self, A, num_splits=0, scale=None, stream=None):
+        d = self.dev
+        A.attn_decode_paged_tree(self.q, self.c[0], self.c[1], d["pt"], d["lens"], d["cu"], self.mask, self.words, self.page, self.o,
+                                 self.lse, stream, self.T, self.B, self.max_q, self.Hq, self.Hkv, self.d, self.width, self.num,
+                                 self.scale if scale is None else scale, num_splits, self.fmt, *self.ds)
+
+    def values(self):
+        out = []
+        for c, s in zip(self.c, self.ds):
+            v = c if self.fmt == "bf16" else c.view(torch.float8_e4m3fn if self.fmt == "e4m3" else torch.float8_e5m2)
+            out.append(v.double().cpu().numpy().reshape(-1, self.Hkv, self.d) * float(np.float32(s)))
+        return out
+
+    def reference(self, scale=None):
+        """(o, lse, bound of o, bound of lse) in 64 bits; rows that see nothing: 0, -inf."""
+        scale = self.scale if scale is None else float(np.float32(scale))
+        K, V = self.values()
+        q = self.q.double().cpu().numpy()
+        o, lse = np.zeros((self.T, self.Hq, self.d)), np.full((self.T, self.Hq), -np.inf)
+        bo, bl = np.zeros_like(o), np.zeros_like(lse)
+        G = self.Hq // self.Hkv
+        for b, (m, l) in enumerate(zip(self.n, self.lens)):
+            at = np.arange(l)
+            rows = self.pt[b, at // self.page].astype(np.int64) * self.page + at % self.page
+            vis = np.ones((m, l), bool)
+            if l:
+                vis[:, l - m:] = self.seen[b]
+            for i in range(m):
+                keys = rows[vis[i]] if l else rows
+                if not len(keys):
+                    continue
+                for h in range(self.Hq):
+                    k, v, x = K[keys, h // G], V[keys, h // G], q[self.cu[b] + i, h]
+                    s = k @ x * scale
+                    z = s.max() + np.log(np.exp(s - s.max()).sum())
+                    w = np.exp(s - z)
+                    o[self.cu[b] + i, h], lse[self.cu[b] + i, h] = w @ v, z
+                    aw = w @ np.abs(v)
+                    # fp32 scores (d products and sums), the exponent's argument and 2^x (2^-21 together
+                    # with |s| 2^-23 for s log2 e), and the sums over the keys
+                    e = (np.abs(k) @ np.abs(x)).max() * abs(scale) * (self.d + 4) * 2.0**-24 + 2.0**-20 + np.abs(s).max() * 2.0**-22 \
+                        + (len(keys) / 16 + 40) * 2.0**-24
+                    p_step = 2.0**-8 if self.fmt == "bf16" else 2.0**-11  # half a step of P, relative
+                    small = 0.0 if self.fmt == "bf16" else len(keys) * 2.0**-25 * np.abs(v).max()  # f16 below its normal range
+                    bo[self.cu[b] + i, h] = aw * (p_step + 2 * e) + small
+                    bl[self.cu[b] + i, h] = e + abs(z) * 2.0**-22
+        bo += 2.0**-8 * (np.abs(o) + bo)  # the rounding of the output
+        return o, lse, bo + 1e-30, bl
+
+    def check(self, scale=None):
+        ro, rl, bo, bl = self.reference(scale)
+        n = sum(self.n)
+        o, lse = self.o.double().cpu().numpy(), self.lse.double().cpu().numpy()
+        assert np.array_equal(np.isneginf(lse[:n]), np.isneginf(rl[:n]))
+        assert np.isfinite(o[:n]).all()
+        do = np.abs(o[:n] - ro[:n]) / bo[:n]
+        assert (do <= 1).all(), f"o: {do.max():.3f} of the bound"
+        f = np.isfinite(rl[:n])
+        dl = np.abs(lse[:n][f] - rl[:n][f]) / bl[:n][f]
+        assert (dl <= 1).all(), f"lse: {dl.max():.3f} of the bound"
+        assert (o[n:] == 7).all() and (lse[n:] == 7).all()  # rows behind the last sequence
+
+
+CASES = {
+    "one_row": ("bf16", 1, 1, 128, 16, [1], [1], "chain"),
+    "gqa4_n4": ("bf16", 8, 2, 128, 16, [4, 4, 4], [4, 300, 1000], "tree"),
+    "d64_p7": ("bf16", 6, 2, 64, 7, [5, 1, 3], [5, 64, 500], "tree"),
+    "n8_g4": ("bf16", 8, 2, 128, 16, [8, 0, 7, 8], [1024, 5, 63, 65], "tree"),
+    "n16_g8": ("bf16", 16, 2, 128, 64, [16, 16], [700, 2000], "tree"),
+    "n33_g4": ("bf16", 4, 1, 128, 16, [33, 20, 1], [33, 800, 129], "tree"),
+    "n64_g4": ("bf16", 8, 2, 128, 16, [64, 63], [64, 900], "any"),
+    "n70_g3": ("bf16", 3, 1, 128, 1, [70, 65, 2], [70, 401, 500], "tree"),
+    "n256_g1": ("bf16", 1, 1, 64, 32, [256, 129], [256, 400], "any"),
+    "n200_chain": ("bf16", 2, 1, 128, 16, [200, 1], [500, 1], "chain"),
+    "none": ("bf16", 4, 2, 128, 16, [5, 20], [5, 100], "none"),
+    "mqa_g40": ("bf16", 40, 1, 64, 16, [3, 2], [300, 2], "tree"),
+    "e4m3_n3": ("e4m3", 8, 2, 128, 16, [3, 3], [600, 3], "tree"),
+    "e4m3_n16": ("e4m3", 8, 2, 128, 16, [16, 16, 9], [16, 1000, 130], "tree"),
+    "e4m3_n48_d64": ("e4m3", 4, 1, 64, 5, [48, 17], [48, 333], "any"),
+    "e5m2_n5_d64": ("e5m2", 12, 3, 64, 7, [5, 1, 4, 0], [900, 1, 4, 9], "chain"),
+    "e5m2_n64": ("e5m2", 8, 1, 128, 16, [64], [700], "tree"),
+    "e4m3_n130": ("e4m3", 2, 2, 128, 1000, [130], [1500], "tree"),
+    "zero_lengths": ("e4m3", 4, 2, 128, 16, [4, 2, 0], [0, 2, 0], "tree"),
+    "zero_lengths_many_rows": ("bf16", 8, 1, 64, 16, [30, 30], [0, 30], "tree"),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", CASES)
+@pytest.mark.parametrize("num_splits", [0, 1, 5])
+def test_parity(A, name, num_splits):
+    c = Case(*CASES[name], seed=len(name))
+    c.run(A, num_splits)
+    assert A.attn_get_device_status() == 0
+    c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [3, 24])
+def test_dense_rows_need_no_offsets(A, fmt, n):
+    c = Case(fmt, 4, 2, 128, 16, [n] * 3, [n, 90, 400], "tree", 5, dense=True)
+    c.run(A)
+    c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 40])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0, 1e-46])
+def test_any_finite_scale(A, n, scale):
+    """Negative and zero scales (a plain product with -inf would be +inf or NaN), and sharp ones."""
+    c = Case("bf16", 4, 2, 64, 16, [n, n], [n + 3, 300], "any", 6)
+    c.run(A, 2, scale)
+    assert A.attn_get_device_status() == 0
+    c.check(scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,n,d", [("bf16", 3, 128), ("e5m2", 3, 64), ("bf16", 37, 64), ("e5m2", 37, 128), ("e4m3", 37, 128)])
+@pytest.mark.parametrize("num_splits", [1, 4])
+def test_masked_slots_hold_anything(A, fmt, n, d, num_splits):
+    """NaN (and infinities) in unused slots of the last page and in drafted tokens nobody sees."""
+    c = Case(fmt, 4, 2, d, 16, [n, n], [n + 61, 300 + n], "tree", 7)
+    dead = n // 2
+    for s in c.seen:
+        s[:, dead] = False
+    m = c.mask.cpu().numpy().view(np.uint64)
+    m &= ~(np.uint64(1) << np.uint64(dead))
+    c.mask = torch.from_numpy(m.view(np.int64)).to(DEV)
+    fills = [float("nan"), float("inf")] if fmt == "bf16" else [0x7F, 0x7C] if fmt == "e5m2" else [0x7F]
+    for cache in c.c:
+        flat = cache.view(-1, c.Hkv, d)
+        for b in range(2):
+            last = c.lens[b] - 1
+            page = int(c.pt[b, last // 16]) * 16
+            flat[page + last % 16 + 1:page + 16] = fills[0]
+            at = c.lens[b] - n + dead
+            flat[int(c.pt[b, at // 16]) * 16 + at % 16] = fills[-1]
+        used = c.pt[c.pt < c.num]
+        for page in set(range(c.num)) - set(used.tolist()):
+            cache[page] = fills[0]
+    c.run(A, num_splits)
+    assert A.attn_get_device_status() == 0
+    keep = c.values
+    c.values = lambda: [np.nan_to_num(x, nan=0.0, posinf=0.0, neginf=0.0) for x in keep()]
+    c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [3, 37])
+@pytest.mark.parametrize("where", ["drafted", "context"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_visible_nonfinite_values_stay(A, n, where, value):
+    """A non-finite V element reaches exactly the rows that see its token, and only its column."""
+    c = Case("bf16", 4, 2, 64, 16, [n], [n + 70], "tree", 8)
+    tok = (69 if where == "context" else 70 + 1)
+    row = int(c.pt[0, tok // 16]) * 16 + tok % 16
+    c.c[1].view(-1, 2, 64)[row, 1, 5] = value
+    c.run(A, 3)
+    o = c.o.double().cpu().numpy()
+    hit = np.zeros((c.T, 4, 64), bool)
+    rows = np.ones(n, bool) if where == "context" else c.seen[0][:, 1]
+    hit[:n][rows, 2:, 5] = True
+    assert np.array_equal(~np.isfinite(o), hit)
+    assert (np.isposinf(o[hit]) if value == float("inf") else np.isnan(o[hit])).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 30])
+def test_nan_query_stays_in_its_rows(A, n):
+    c = Case("bf16", 4, 2, 64, 16, [n, n], [n, 200], "tree", 9)
+    c.q[1, 2] = float("nan")
+    c.run(A, 2)
+    bad = torch.isnan(c.lse)
+    assert bad[1, 2] and bad.sum() == 1
+    assert torch.isnan(c.o[1, 2].float()).all() and torch.isnan(c.o.float()).sum() == 64
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,n", [("bf16", 3), ("e4m3", 3), ("bf16", 20), ("e4m3", 20)])
+def test_bad_lengths_pages_and_offsets(A, fmt, n):
+    bad = A.ATTN_ERR_DEVICE_BAD_INDEX
+
+    def fresh():
+        return Case(fmt, 4, 2, 128, 16, [n, n, n], [n, 100, 400], "tree", 11)
+
+    for b, length in ((0, n - 1), (1, -4), (2, 401 + 16 * 100)):
+        c = fresh()
+        c.dev["lens"][b] = length
+        c.run(A)
+        assert A.attn_get_device_status() == bad
+        c.lens[b] = 0
+        c.check()
+    c = fresh()  # pages out of range count as zero rows
+    c.dev["pt"][2, 3], c.dev["pt"][2, 7] = -1, c.num
+    c.run(A, 2)
+    assert A.attn_get_device_status() == bad
+    ghost = c.num  # two more pages of zeros stand for them
+    c.pt[2, 3] = c.pt[2, 7] = ghost
+    vals = c.values()
+    c.values = lambda: [np.concatenate([x, np.zeros((16, *x.shape[1:]))]) for x in vals]
+    c.check()
+    c = fresh()  # the last sequence passes the rows, or holds more than max_q of them: its rows stay
+    for change in ("rows", "max_q"):
+        c = fresh()
+        if change == "rows":
+            c.dev["cu"][3] = c.T + 1
+        else:
+            c.dev["cu"][3] += 1
+        c.run(A)
+        assert A.attn_get_device_status() == bad
+        c.n = [n, n]
+        c.T, keep = 2 * n, (c.o, c.lse)
+        assert (c.o[2 * n:] == 7).all() and (c.lse[2 * n:] == 7).all()
+        c.lens, c.B = c.lens[:2], 2
+        c.check()
+
+
+@pytest.mark.gpu
+def test_agrees_with_the_one_token_decode(A):
+    """One drafted token that sees itself is the decode of one token."""
+    c = Case("bf16", 16, 4, 128, 16, [1] * 5, [1, 16, 17, 300, 1500], "chain", 12, dense=True)
+    c.run(A)
+    o, lse = torch.empty_like(c.o), torch.empty_like(c.lse)
+    A.attn_decode_paged(c.q, c.c[0], c.c[1], c.dev["pt"], c.dev["lens"], 16, o, lse, None, c.B, 16, 4, 128, c.width, c.num, c.scale)
+    assert (o.float() - c.o.float()).abs().max().item() <= 2e-2
+    assert (lse - c.lse).abs().max().item() <= 2e-3
+
+
+@pytest.mark.gpu
+def test_two_streams_give_the_same_bytes(A):
+    """Calls that overlap on two streams do not share workspace; a repeated call is bit-identical."""
+    a = Case("bf16", 8, 2, 128, 16, [24, 24], [900, 2000], "tree", 13)
+    b = Case("e4m3", 8, 2, 128, 16, [2, 2], [3000, 2000], "tree", 14)
+    want = []
+    for c in (a, b):
+        c.run(A, 6)
+        want.append((c.o.clone(), c.lse.clone()))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s in zip((a, b), streams):
+            c.run(A, 6, stream=s)
+    torch.cuda.synchronize()
+    for c, (o, lse) in zip((a, b), want):
+        assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
+    assert A.attn_get_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [2, 20])
+def test_captured_and_replayed(A, fmt, n):
+    """A graph follows new queries, lengths and masks in the captured buffers."""
+    c = Case(fmt, 8, 2, 128, 16, [n] * 3, [n + 500, n + 40, n + 900], "tree", 15, dense=True)
+    c.run(A)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run(A)
+    c.q.copy_(torch.randn_like(c.q))
+    c.dev["lens"].sub_(7)
+    c.mask.bitwise_or_(1)  # every node sees the first one too
+    c.lens = [x - 7 for x in c.lens]
+    for s in c.seen:
+        s[:, 0] = True
+    c.o.fill_(7)
+    g.replay()
+    torch.cuda.synchronize()
+    assert A.attn_get_device_status() == 0
+    c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "e5m2"])
+@pytest.mark.parametrize("n", [3, 24])
+def test_step_rotate_write_attend_read(A, fmt, n):
+    """A serving step as its calls: q and k rotated at the nodes' depths out of one projection, keys
+    and values written behind the context, the tree attended, the drafted rows read back."""
+    Hq, Hkv, d, page = 8, 2, 128, 16
+    c = Case(fmt, Hq, Hkv, d, page, [n, n - 1], [n + 50, 200 + n], "tree", 16)
+    T, W = c.T, (Hq + 2 * Hkv) * d
+    g = torch.Generator().manual_seed(1)
+    qkv = torch.randn((T, W), generator=g).bfloat16().to(DEV)
+    freqs, amp = A.attn_rope_freqs(d)
+    inv = torch.tensor(freqs, dtype=torch.float64, device=DEV)
+    depth = np.zeros(T, np.int32)
+    for b, m in enumerate(c.n):
+        depth[c.cu[b]:c.cu[b] + m] = c.lens[b] - m + c.seen[b].sum(1) - 1
+    pos = torch.from_numpy(depth).to(DEV)
+    k, v = qkv[:, Hq * d:(Hq + Hkv) * d], qkv[:, (Hq + Hkv) * d:]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        A.attn_rope(qkv, None, c.q, None, pos, inv, T, Hq, 0, d, 0, d, W, 0, Hq * d, 0, amplitude=amp)
+        A.attn_kv_write_paged(k, v, W, W, c.c[0], c.c[1], c.dev["pt"], c.dev["lens"], c.dev["cu"], page, T, c.B, Hkv, d, c.width, c.num,
+                              fmt, *c.ds, positions=pos, inv_freq=inv, rot_dim=d, amplitude=amp)
+        c.run(A)
+        kr, vr = (torch.full((T, Hkv, d), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        A.attn_kv_read_paged(c.c[0], c.c[1], kr, vr, Hkv * d, Hkv * d, c.dev["pt"], c.dev["lens"], c.dev["cu"], page, T, c.B, Hkv, d,
+                             c.width, c.num, fmt, *c.ds)
+    s.synchronize()
+    assert A.attn_get_device_status() == 0
+    c.check()  # on the cache and the queries as the calls left them
+    m = sum(c.n)
+    # the read-back rows are the projection's: one rounding to the cache's format, one to bf16
+    step = {"bf16": 0.0, "e4m3": 2.0**-4, "e5m2": 2.0**-3}[fmt]
+    floor = 0.0 if fmt == "bf16" else c.ds[1] * {"e4m3": 2.0**-10, "e5m2": 2.0**-17}[fmt]
+    x = v[:m].double().reshape(m, Hkv, d)
+    assert ((vr[:m].double() - x).abs() <= x.abs() * (step + 2.0**-8 * (step > 0)) * 1.01 + floor).all()
+    assert (vr[m:] == 7).all() and (kr[m:] == 7).all()
+    # rotation keeps each pair's length: keys too, up to the roundings of both members
+    z = k[:m].double().reshape(m, Hkv, d)
+    before = (z[..., :64] ** 2 + z[..., 64:] ** 2).sqrt()
+    after = (kr[:m, :, :64].double() ** 2 + kr[:m, :, 64:].double() ** 2).sqrt()
+    assert ((after - before).abs() <= before * (step + 2.0**-7) * 1.5 + 2 * floor).all()
