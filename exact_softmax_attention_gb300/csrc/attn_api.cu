@@ -121,6 +121,21 @@ attn_status_t make_cache_map(CUtensorMap* m, const void* base, long long rows, i
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+// 2-D map over a paged cache viewed as [rows, row_elems] for gather copies of four rows: box one row of
+// 128 bytes with the 128-byte swizzle, or of d = 64 8-bit codes without one.
+attn_status_t make_gather_map(CUtensorMap* m, const void* base, long long rows, long long row_elems, int d, int elem) {
+    cuuint64_t dims[2] = {(cuuint64_t)row_elems, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)row_elems * elem};
+    const int box_bytes = d * elem < 128 ? d * elem : 128;
+    cuuint32_t box[2] = {(cuuint32_t)(box_bytes / elem), 1};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = g_encode(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 Options options() {
@@ -603,6 +618,16 @@ attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const v
     p.rescale_thr = (float)opt.rescale_threshold;
     p.v_descale = f8 ? v_descale : 1.0f;
     p.status = ds->status;
+    p.watchdog_ns = (unsigned long long)(opt.watchdog_ms * 1e6);
+    attn::TreeTmaps tm;
+    memset(&tm, 0, sizeof tm);
+    if (attn::tree_takes_tiles(rows)) {
+        const long long cache_rows = (long long)num_pages * page_size;
+        if ((st = encode_fn()) != ATTN_OK ||
+            (st = make_gather_map(&tm.k, k_cache, cache_rows, (long long)Hkv * d, d, f8 ? 1 : 2)) != ATTN_OK ||
+            (st = make_gather_map(&tm.v, v_cache, cache_rows, (long long)Hkv * d, d, f8 ? 1 : 2)) != ATTN_OK)
+            return st;
+    }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     void* ws = nullptr;
     if (p.max_splits > 1) {
@@ -613,7 +638,7 @@ attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const v
         p.ws_o = reinterpret_cast<float*>(ws);
         p.ws_lse = p.ws_o + n * d;
     }
-    const cudaError_t e = attn::launch_attn_tree(p, d, kv_format, s);
+    const cudaError_t e = attn::launch_attn_tree(p, tm, d, kv_format, s);
     if (ws) cudaFreeAsync(ws, s);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

@@ -1,0 +1,546 @@
+// Attention of drafted tokens over a paged cache for more than 16 rows (drafted tokens x query heads)
+// per kv head: 128-row tiles on the tcgen05 tensor cores.
+//
+// A block takes one (sequence, split of the keys, kv head, 128-row tile) and walks the split's keys in
+// tiles of 64. Per tile S = Q K^T (M 128, N 64) and O += P V (M 128, N d), accumulators in tensor
+// memory, P as the 16-bit A operand from tensor memory over S. Two blocks share an SM (96 KB of
+// shared memory and 256 tensor-memory columns each), so that one block's start, softmax latency and
+// end are covered by the other's loads. Roles of the eight warps:
+//   warp 0      loads: gather copies of four cache rows each through a tensor map of the cache viewed
+//               as [rows, Hkv d]; the row indices come from the page table, so any page size takes
+//               the same path, and rows past the end or of a bad page lie outside the map and arrive
+//               as zeros
+//   warp 1      issues the products and owns the tensor memory
+//   warps 2, 3  16-bit caches: pass the V tiles on, taking non-finite values out of those a row may
+//               not see in full. 8-bit caches: widen K and V tiles to f16 (exact) in shared memory
+//   warps 4-7   softmax, one row per thread: maximum, conditional rescale of O (only when a maximum
+//               grows by more than the threshold), exponentials, P; at the end O / l and the LSE
+// A 64-key tile of bf16 K and V is 32 KB, 1390 clocks of an SM's share of the memory bandwidth
+// (6.8 TB/s over 152 SMs at 1.9 GHz), against about 640 clocks of products: with up to 128 rows the
+// kernel should be bounded by the cache reads.
+#include "tree_device.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kTileRows = 128;  // rows per block
+constexpr int kTileKeys = 64;
+constexpr int kTileThreads = 256;
+
+template <int D, int FMT>
+struct TileLayout {
+    static constexpr bool kF8 = FMT != ATTN_KV_BF16;
+    static constexpr int kQBytes = kTileRows * D * 2;
+    static constexpr int kChunkQ = kTileRows * 128;  // one [128 rows x 128 bytes] chunk of Q
+    static constexpr int kTile16 = kTileKeys * D * 2;  // a 16-bit K or V tile the products read
+    static constexpr int kChunk16 = kTileKeys * 128;
+    static constexpr int kLoad = kF8 ? kTileKeys * D : kTile16;  // a K or V tile as loaded
+    static constexpr int kStages = D == 128 ? 2 : 4;  // loaded K/V tile pairs in flight
+    static constexpr int kQOff = 0;
+    static constexpr int kRingOff = kQBytes;  // stage s: K tile, V tile
+    static constexpr int kWideOff = kRingOff + kStages * 2 * kLoad;  // 8-bit caches: the f16 K and V tile
+    static constexpr int kBarOff = kWideOff + (kF8 ? 2 * kTile16 : 0);
+    // barriers
+    static constexpr int bQ = 0, bO = 1, bS = 2, bP = 4, bWK = 6, bWV = 7, bWKFree = 8, bWVFree = 9, bDrain = 10, bLast = 11;
+    static constexpr int bK = 12, bV = bK + kStages, bKFree = bV + kStages, bVFree = bKFree + kStages;
+    static constexpr int bClean = bVFree + kStages;
+    static constexpr int kBars = bClean + kStages;
+    static constexpr int kMiscOff = kBarOff + kBars * 8;  // tensor-memory base, abort flag, odd-value flag
+    static constexpr int kBytes = kMiscOff + 16;
+    // at least 80 KB, so that no more than two blocks (256 tensor-memory columns each) share an SM
+    static constexpr int kAlloc = kBytes + 1024 > 81920 ? kBytes + 1024 : 81920;
+    static_assert(kAlloc <= 115712, "two blocks per SM");
+};
+
+constexpr uint32_t kColS = 0, kColO = 128, kCols = 256;  // S buffers at 0 and 64
+
+__device__ __forceinline__ void fence_smem_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Rows r[0..3] (columns c .. c + box) of a 2-D map into shared memory, completing on an mbarrier.
+__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c, const int (&r)[4]) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
+        "%6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+        : "memory");
+}
+
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit));
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t at, uint32_t (&w)[4]) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+}
+
+// Widen the 64-row tile of 8-bit codes at src into f16 at dst (chunks of [64 rows x 128 bytes],
+// 128-byte swizzle); thread t of 64. clean: take non-finite values out, return whether there were any.
+template <int D, int FMT>
+__device__ __forceinline__ bool widen_tile(uint32_t src, uint32_t dst, int t, bool clean) {
+    constexpr int U = D / 16;  // 16-byte units of codes per row
+    bool odd = false;
+#pragma unroll 4
+    for (int x = t; x < kTileKeys * U; x += 64) {
+        const int r = x / U, u = x % U;
+        uint32_t w[4], h[8];
+        // 128-byte rows arrive in the 128-byte swizzle, 64-byte rows plain
+        lds128(src + r * D + ((D == 128 ? u ^ (r & 7) : u) << 4), w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = fp8x2_f16x2<FMT>(w[i / 2] >> (16 * (i & 1)));
+        if (clean) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t keep = finite_halves(h[i], true);
+                odd |= keep != 0xFFFFFFFFu;
+                h[i] &= keep;
+            }
+        }
+        // the two f16 units of this one; every other group of four lanes starts with the second, so
+        // that the eight lanes of a row write different banks
+        const uint32_t row = dst + (u >> 2) * (kTileKeys * 128) + r * 128;
+        const uint32_t a0 = row + (((2 * (u & 3)) ^ (r & 7)) << 4), a1 = row + (((2 * (u & 3) + 1) ^ (r & 7)) << 4);
+        if (u & 4) {
+            sts128(a1, h[4], h[5], h[6], h[7]);
+            sts128(a0, h[0], h[1], h[2], h[3]);
+        } else {
+            sts128(a0, h[0], h[1], h[2], h[3]);
+            sts128(a1, h[4], h[5], h[6], h[7]);
+        }
+    }
+    return odd;
+}
+
+// Instruction descriptor of kind::f16 with fp32 accumulation: A and B both f16 or both bf16.
+__host__ __device__ constexpr uint32_t idesc16(bool f16, uint32_t M, uint32_t N, uint32_t b_mn_major) {
+    return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn_major << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kTileThreads, 2)
+    tree_tile_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
+    grid_dependents_launch();
+    using L = TileLayout<D, FMT>;
+    constexpr bool F8 = L::kF8;
+    constexpr int NS = L::kStages;
+    const int HG = p.Hkv * p.groups;
+    const int b = blockIdx.y, split = (int)(blockIdx.x / (unsigned)HG), hg = (int)(blockIdx.x % (unsigned)HG);
+    const int kvh = hg / p.groups, r0 = (hg % p.groups) * kTileRows;
+    TreeSeq s;
+    if (!tree_seq(p, b, s)) return;
+    const int R = min(kTileRows, s.n * p.G - r0);  // rows of this tile
+    if (R <= 0) return;
+    const int nsplit = cdiv(s.len, p.chunk);
+    const int t_begin = split * p.chunk;
+    auto out_row = [&](int r) {
+        const int i = (r0 + r) / p.G;
+        return (long long)(s.q0 + i) * p.Hq + kvh * p.G + (r0 + r - i * p.G);
+    };
+    if (s.len == 0) {
+        if (split == 0)
+            for (int x = threadIdx.x; x < R * D; x += blockDim.x) {
+                const long long orow = out_row(x / D);
+                p.o[orow * D + x % D] = __float2bfloat16(0.0f);
+                if (x % D == 0) p.lse[orow] = -INFINITY;
+            }
+        return;
+    }
+    if (t_begin >= s.len) return;
+    const int t_end = min(s.len, t_begin + p.chunk);
+    const int tiles = cdiv(t_end - t_begin, kTileKeys);
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+    volatile int* odd_v = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 8);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t wd = p.watchdog_ns;
+    const int* pt = p.page_table + (long long)b * p.max_pages;
+    if (threadIdx.x == 0) {
+        mbar_init(&bars[L::bQ], 4);
+        mbar_init(&bars[L::bO], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[L::bS + i], 1);
+            mbar_init(&bars[L::bP + i], 4);
+        }
+        mbar_init(&bars[L::bWK], 2);
+        mbar_init(&bars[L::bWV], 2);
+        mbar_init(&bars[L::bWKFree], 1);
+        mbar_init(&bars[L::bWVFree], 1);
+        mbar_init(&bars[L::bDrain], 1);
+        mbar_init(&bars[L::bLast], 1);
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&bars[L::bK + i], 1);
+            mbar_init(&bars[L::bV + i], 1);
+            mbar_init(&bars[L::bKFree + i], F8 ? 2 : 1);  // 8-bit: the two widening warps; else the products
+            mbar_init(&bars[L::bVFree + i], F8 ? 2 : 1);
+            mbar_init(&bars[L::bClean + i], 2);
+        }
+        *abort_flag = 0;
+        *odd_v = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t ring = smem_u32(smem + L::kRingOff);
+    // tiles from this one on hold drafted tokens or the end of the sequence
+    const int first_mixed = s.ctx <= t_begin ? 0 : (s.ctx - t_begin) / kTileKeys;
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- loads
+        const int none = p.num_pages * p.page_size;  // the first row past the cache: zeros
+        const int quad = lane & 15, half = lane >> 4;  // four rows; 64-column half (128-column rows)
+        constexpr bool kHalves = !F8 && D == 128;
+        auto rows_of = [&](int i, int (&r)[4]) {
+            const int tok = t_begin + i * kTileKeys + 4 * quad;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = tok + e < t_end ? cache_row(p, pt, tok + e) : none;
+                r[e] = row < 0 ? none : row;
+            }
+        };
+        const int col = kvh * D + (kHalves ? half * 64 : 0);
+        const bool active = kHalves || half == 0;
+        const uint32_t dst = (kHalves ? half * L::kChunk16 : 0) + quad * 4 * (F8 ? D : 128);
+        int r[4];
+        rows_of(0, r);
+        bool ok = true;
+        int issued_k = 0, issued_v = 0;
+        for (int i = 0; i < tiles; ++i) {
+            const int st = i % NS;
+            const uint32_t par = (uint32_t)((i / NS) & 1) ^ 1u;
+            const uint32_t base = ring + st * 2 * L::kLoad + dst;
+            if (!(ok = wait_all(&bars[L::bKFree + st], par, abort_flag, wd))) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bars[L::bK + st], L::kLoad);
+            __syncwarp();
+            if (active) gather4(base, &tmK, &bars[L::bK + st], col, r);
+            issued_k = i + 1;
+            if (!(ok = wait_all(&bars[L::bVFree + st], par, abort_flag, wd))) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bars[L::bV + st], L::kLoad);
+            __syncwarp();
+            if (active) gather4(base + L::kLoad, &tmV, &bars[L::bV + st], col, r);
+            issued_v = i + 1;
+            if (i + 1 < tiles) rows_of(i + 1, r);
+        }
+        if (!ok) {
+            // let the copies in flight land before the block can end
+            int dummy = 0;
+            for (int i = issued_k > NS ? issued_k - NS : 0; i < issued_k; ++i)
+                mbar_wait(&bars[L::bK + i % NS], (uint32_t)((i / NS) & 1), &dummy, 20000000ull);
+            for (int i = issued_v > NS ? issued_v - NS : 0; i < issued_v; ++i)
+                mbar_wait(&bars[L::bV + i % NS], (uint32_t)((i / NS) & 1), &dummy, 20000000ull);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- products
+        // Order: S(0), then S(i), PV(i - 1) for every i, then the last PV. S(i) goes to the buffer of
+        // P(i - 2), which PV(i - 2), issued before it, has read.
+        const uint32_t leader = lane == 0;
+        constexpr uint32_t idS = idesc16(F8, kTileRows, kTileKeys, 0), idO = idesc16(F8, kTileRows, D, 1);
+        const uint64_t dq = smem_desc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
+        const uint32_t k_base = F8 ? smem_u32(smem + L::kWideOff) : ring;
+        const uint32_t v_base = k_base + L::kTile16;
+        const uint64_t dk = smem_desc_sw128(k_base, 16, 1024);
+        const uint64_t dv = smem_desc_sw128(v_base, L::kChunk16, 1024);
+        bool ok = wait_all(&bars[L::bQ], 0, abort_flag, wd);
+        bool any = false;
+        auto pv = [&](int j) -> bool {
+            const int st = j % NS, sb = j & 1;
+            if (!F8 && !wait_all(&bars[L::bV + st], (uint32_t)((j / NS) & 1), abort_flag, wd)) return false;
+            if (!wait_all(F8 ? &bars[L::bWV] : &bars[L::bClean + st], F8 ? (uint32_t)(j & 1) : (uint32_t)((j / NS) & 1), abort_flag, wd))
+                return false;
+            if (!wait_all(&bars[L::bP + sb], (uint32_t)((j >> 1) & 1), abort_flag, wd)) return false;
+            tc_fence_after();
+            const uint64_t vd = dv + (uint64_t)(F8 ? 0 : (st * 2 * L::kLoad) >> 4);
+#pragma unroll
+            for (int k = 0; k < kTileKeys / 16; ++k)
+                tc_mma_ts_by(leader, tmem + kColO, tmem + kColS + 64 * sb + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idO,
+                             j > 0 || k > 0 ? 1u : 0u);
+            __syncwarp();
+            tc_commit_by(leader, j == tiles - 1 ? &bars[L::bLast] : &bars[L::bO]);
+            tc_commit_by(leader, F8 ? &bars[L::bWVFree] : &bars[L::bVFree + st]);
+            return true;
+        };
+        for (int i = 0; i < tiles && ok; ++i) {
+            const int st = i % NS;
+            if (!(ok = wait_all(F8 ? &bars[L::bWK] : &bars[L::bK + st], F8 ? (uint32_t)(i & 1) : (uint32_t)((i / NS) & 1), abort_flag,
+                                wd)))
+                break;
+            tc_fence_after();
+            any = true;
+            const uint64_t kd = dk + (uint64_t)(F8 ? 0 : (st * 2 * L::kLoad) >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                tc_mma_ss_by(leader, tmem + kColS + 64 * (i & 1), dq + (uint64_t)(((k >> 2) * L::kChunkQ + (k & 3) * 32) >> 4),
+                             kd + (uint64_t)(((k >> 2) * L::kChunk16 + (k & 3) * 32) >> 4), idS, k > 0 ? 1u : 0u);
+            __syncwarp();
+            tc_commit_by(leader, &bars[L::bS + (i & 1)]);
+            tc_commit_by(leader, F8 ? &bars[L::bWKFree] : &bars[L::bKFree + st]);
+            if (i > 0) ok = pv(i - 1);
+        }
+        if (ok) ok = pv(tiles - 1);
+        if (any) {
+            // every product has completed before the tensor memory is released
+            tc_commit_by(leader, &bars[L::bDrain]);
+            int dummy = 0;
+            if (leader) mbar_wait(&bars[L::bDrain], 0, &dummy, 50000000ull);
+            __syncwarp();
+        }
+    } else if (warp < 4) {
+        // ---------------------------------------------------------------- V tiles (8-bit: K too)
+        const int t = threadIdx.x - 64;
+        bool ok = true;
+        for (int i = 0; i < tiles && ok; ++i) {
+            const int st = i % NS;
+            const uint32_t par = (uint32_t)((i / NS) & 1);
+            const bool mixed = i >= first_mixed;
+            const uint32_t kt = ring + st * 2 * L::kLoad, vt = kt + L::kLoad;
+            if constexpr (F8) {
+                const uint32_t wide = smem_u32(smem + L::kWideOff);
+                if (!(ok = wait_all(&bars[L::bK + st], par, abort_flag, wd))) break;
+                if (!(ok = wait_all(&bars[L::bWKFree], (uint32_t)(i & 1) ^ 1u, abort_flag, wd))) break;
+                widen_tile<D, FMT>(kt, wide, t, false);
+                fence_smem_to_async();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars[L::bWK]);
+                    mbar_arrive(&bars[L::bKFree + st]);
+                }
+                if (!(ok = wait_all(&bars[L::bV + st], par, abort_flag, wd))) break;
+                if (!(ok = wait_all(&bars[L::bWVFree], (uint32_t)(i & 1) ^ 1u, abort_flag, wd))) break;
+                if (mixed) {
+                    if (widen_tile<D, FMT>(vt, wide + L::kTile16, t, true)) *odd_v = 1;
+                } else {
+                    widen_tile<D, FMT>(vt, wide + L::kTile16, t, false);
+                }
+                fence_smem_to_async();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars[L::bWV]);
+                    mbar_arrive(&bars[L::bVFree + st]);
+                }
+            } else {
+                if (!(ok = wait_all(&bars[L::bV + st], par, abort_flag, wd))) break;
+                if (mixed) {
+                    bool odd = false;
+                    for (int x = t; x < L::kTile16 / 16; x += 64) {
+                        uint32_t w[4];
+                        lds128(vt + 16 * x, w);
+                        bool bad = false;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t keep = finite_halves(w[e], false);
+                            bad |= keep != 0xFFFFFFFFu;
+                            w[e] &= keep;
+                        }
+                        if (bad) sts128(vt + 16 * x, w[0], w[1], w[2], w[3]);
+                        odd |= bad;
+                    }
+                    if (odd) *odd_v = 1;
+                    fence_smem_to_async();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[L::bClean + st]);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax and output
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;
+        const bool valid = row < R;
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tO = tmem + lane_off + kColO;
+        const long long orow = valid ? out_row(row) : 0;
+        const int node = valid ? (r0 + row) / p.G : s.n - 1;  // rows of padding see what the last node sees
+        const unsigned long long* mrow = p.mask ? p.mask + (long long)(s.q0 + node) * p.mask_words : nullptr;
+        {
+            // this thread's row of Q into the K-major 128-byte swizzle
+            const uint32_t q = smem_u32(smem + L::kQOff) + row * 128;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                uint32_t w[4] = {0, 0, 0, 0};
+                if (valid) {
+                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.q + orow * D) + c);
+                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float lo = __uint_as_float(in[e] << 16) * p.q_sign;
+                        const float hi = __uint_as_float(in[e] & 0xFFFF0000u) * p.q_sign;
+                        w[e] = F8 ? pack_half2(lo, hi) : pack_bf16x2(lo, hi);
+                    }
+                }
+                sts128(q + (c >> 3) * L::kChunkQ + (((c & 7) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+            }
+            fence_smem_to_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[L::bQ]);
+        }
+        const float sl2 = p.scale_log2;
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int i = 0; i < tiles; ++i) {
+            const int sb = i & 1;
+            const uint32_t tS = tmem + lane_off + kColS + 64 * sb;
+            if (!(ok = wait_all(&bars[L::bS + sb], (uint32_t)((i >> 1) & 1), abort_flag, wd))) break;
+            tc_fence_after();
+            uint32_t rr[2][32];
+            tmem_ld32(tS, rr[0]);
+            tmem_ld32(tS + 32, rr[1]);
+            tc_wait_ld();
+            reg_fence(rr[0]);
+            reg_fence(rr[1]);
+            float sv[kTileKeys];
+#pragma unroll
+            for (int c = 0; c < kTileKeys; ++c) sv[c] = __uint_as_float(rr[c >> 5][c & 31]);
+            if (i >= first_mixed) {
+                const unsigned long long w = tree_window(mrow, p.mask_words, node, s.ctx, s.len, t_begin + i * kTileKeys);
+                const uint32_t w0 = (uint32_t)w, w1 = (uint32_t)(w >> 32);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    if (!((w0 >> c) & 1)) sv[c] = -INFINITY;
+                    if (!((w1 >> c) & 1)) sv[32 + c] = -INFINITY;
+                }
+            }
+            float mx[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx[e] = fmaxf(sv[e], sv[e + 8]);
+#pragma unroll
+            for (int c = 16; c < kTileKeys; c += 16)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mx[e] = max3f(mx[e], sv[c + e], sv[c + 8 + e]);
+            const float mt = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+            const float mc = fmaxf(m, mt);
+            if (__any_sync(0xffffffffu, (mc - m) * sl2 > p.rescale_thr)) {  // NaN (both -inf) is false
+                const float alpha = m == -INFINITY ? 0.0f : ex2_mufu((m - mc) * sl2);
+                if (i > 0) {
+                    // O += P(i - 1) V is complete before O is rescaled (S(i) was issued before it)
+                    if (!(ok = wait_all(&bars[L::bO], (uint32_t)(i - 1) & 1u, abort_flag, wd))) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + c, o);
+                        tc_wait_ld();
+                        reg_fence(o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st16(tO + c, o);
+                    }
+                }
+                l *= alpha;
+                m = mc;
+            }
+            const float neg = m == -INFINITY ? 0.0f : -m * sl2;
+            float sum[4] = {0, 0, 0, 0};
+            uint32_t pk[kTileKeys / 2];
+#pragma unroll
+            for (int c = 0; c < kTileKeys; c += 2) {
+                float x0, x1;
+                ffma2(x0, x1, sv[c], sv[c + 1], sl2, sl2, neg, neg);
+                const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
+                const int a = ((c >> 1) & 1) * 2;
+                fadd2(sum[a], sum[a + 1], sum[a], sum[a + 1], p0, p1);
+                pk[c >> 1] = F8 ? pack_half2(p0, p1) : pack_bf16x2(p0, p1);
+            }
+            tmem_st32(tS, pk);
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[L::bP + sb]);
+        }
+        // the last product has a barrier of its own: bO may be one phase ahead by now or not
+        if (ok) ok = wait_all(&bars[L::bLast], 0, abort_flag, wd);
+        if (ok) {
+            tc_fence_after();
+            const bool odd = *odd_v != 0;
+            const float inv = l == 0.0f ? 0.0f : p.v_descale / l;
+            const bool empty = l == 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tO + c, o);
+                tc_wait_ld();
+                reg_fence(o);
+                float v[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]);
+                if (odd && valid) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        v[e] += nonfinite_sum<FMT>(p, pt, mrow, node, s, max(t_begin, s.ctx / kTileKeys * kTileKeys), t_end, kvh, D, c + e);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = empty ? 0.0f : v[e] * inv;
+                if (valid && nsplit == 1) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D + c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        dst[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                                            pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+                } else if (valid) {
+                    float4* dst = reinterpret_cast<float4*>(p.ws_o + (orow * p.max_splits + split) * D + c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                }
+                __syncwarp();
+            }
+            if (valid) {
+                const float lse = empty ? -INFINITY : m * p.scale + logf(l);
+                if (nsplit == 1)
+                    p.lse[orow] = lse;
+                else
+                    p.ws_lse[orow * p.max_splits + split] = lse;
+            }
+        }
+    }
+
+    // -------------------------------------------------------------------- end
+    __syncwarp();
+    tc_fence_before();
+    named_bar_sync(1, kTileThreads);
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, kCols);
+    if (threadIdx.x == 0 && *abort_flag) atomicCAS(p.status, 0, kDevTimeout);
+}
+
+template <int D, int FMT>
+cudaError_t launch_tiles(TreeParams p, const TreeTmaps& tm, cudaStream_t stream) {
+    constexpr int bytes = TileLayout<D, FMT>::kAlloc;
+    static std::atomic<bool> attr_set[kMaxAttrDevices];
+    cudaError_t e = ensure_smem_attr(tree_tile_kernel<D, FMT>, bytes, attr_set);
+    if (e != cudaSuccess) return e;
+    p.groups = (int)(((long long)p.max_q * p.G + kTileRows - 1) / kTileRows);
+    const long long x = (long long)p.max_splits * p.Hkv * p.groups;
+    if (x > INT32_MAX) return cudaErrorInvalidConfiguration;
+    tree_tile_kernel<D, FMT><<<dim3((unsigned)x, (unsigned)p.B), kTileThreads, bytes, stream>>>(p, tm.k, tm.v);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_fmt(const TreeParams& p, const TreeTmaps& tm, int fmt, cudaStream_t stream) {
+    return fmt == ATTN_FP8_E4M3   ? launch_tiles<D, ATTN_FP8_E4M3>(p, tm, stream)
+           : fmt == ATTN_FP8_E5M2 ? launch_tiles<D, ATTN_FP8_E5M2>(p, tm, stream)
+                                  : launch_tiles<D, ATTN_KV_BF16>(p, tm, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_tiles(const TreeParams& p, const TreeTmaps& tm, int d, int kv_format, cudaStream_t stream) {
+    return d == 128 ? launch_fmt<128>(p, tm, kv_format, stream) : launch_fmt<64>(p, tm, kv_format, stream);
+}
+
+}  // namespace attn

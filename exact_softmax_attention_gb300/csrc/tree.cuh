@@ -28,10 +28,23 @@ struct TreeParams {
     unsigned int ps_magic;   // tok / page_size by multiplication, as in DecodeParams
     int ps_shift;
     int* status;
+    unsigned long long watchdog_ns;
 };
 
+// 2-D maps over the caches viewed as [num_pages * page_size, Hkv * d], box one row of 128 bytes (64
+// for 8-bit d = 64), for gather copies of four rows.
+struct TreeTmaps {
+    CUtensorMap k, v;
+};
+
+// Rows per kv head from which the 128-row tiles take over from the 16-row products.
+constexpr int kTreeTileRows = 17;
+
 // kv_format: ATTN_KV_BF16, ATTN_FP8_E4M3, ATTN_FP8_E5M2; d 64 or 128.
-cudaError_t launch_attn_tree(const TreeParams& p, int d, int kv_format, cudaStream_t stream);
+// tm: the maps when tree_takes_tiles(rows of a kv head), else unused.
+cudaError_t launch_attn_tree(const TreeParams& p, const TreeTmaps& tm, int d, int kv_format, cudaStream_t stream);
+cudaError_t launch_tree_tiles(const TreeParams& p, const TreeTmaps& tm, int d, int kv_format, cudaStream_t stream);
+inline bool tree_takes_tiles(long long rows) { return rows >= kTreeTileRows; }
 
 // Tokens per split and splits of the longest sequence (lmax tokens).
 void tree_plan(int B, int Hkv, int rows, long long lmax, int num_splits, int num_sms, int* chunk, int* max_splits);
