@@ -121,13 +121,14 @@ attn_status_t make_cache_map(CUtensorMap* m, const void* base, long long rows, i
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// 2-D map over a paged cache viewed as [rows, row_elems] for gather copies of four rows: box one row of
-// 128 bytes with the 128-byte swizzle, or of d = 64 8-bit codes without one.
-attn_status_t make_gather_map(CUtensorMap* m, const void* base, long long rows, long long row_elems, int d, int elem) {
+// 2-D map over a paged cache viewed as [rows, row_elems]: boxes of box_rows rows (1: for gather copies of
+// four rows), 128 bytes wide with the 128-byte swizzle, or d = 64 8-bit codes without one.
+attn_status_t make_tree_map(CUtensorMap* m, const void* base, long long rows, long long row_elems, int d, int elem,
+                            int box_rows) {
     cuuint64_t dims[2] = {(cuuint64_t)row_elems, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)row_elems * elem};
     const int box_bytes = d * elem < 128 ? d * elem : 128;
-    cuuint32_t box[2] = {(cuuint32_t)(box_bytes / elem), 1};
+    cuuint32_t box[2] = {(cuuint32_t)(box_bytes / elem), (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = g_encode(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
                           const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -623,9 +624,10 @@ attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const v
     memset(&tm, 0, sizeof tm);
     if (attn::tree_takes_tiles(rows)) {
         const long long cache_rows = (long long)num_pages * page_size;
+        p.box_rows = page_size % 64 == 0 ? 64 : (page_size % 16 == 0 ? 16 : 1);
         if ((st = encode_fn()) != ATTN_OK ||
-            (st = make_gather_map(&tm.k, k_cache, cache_rows, (long long)Hkv * d, d, f8 ? 1 : 2)) != ATTN_OK ||
-            (st = make_gather_map(&tm.v, v_cache, cache_rows, (long long)Hkv * d, d, f8 ? 1 : 2)) != ATTN_OK)
+            (st = make_tree_map(&tm.k, k_cache, cache_rows, (long long)Hkv * d, d, f8 ? 1 : 2, p.box_rows)) != ATTN_OK ||
+            (st = make_tree_map(&tm.v, v_cache, cache_rows, (long long)Hkv * d, d, f8 ? 1 : 2, p.box_rows)) != ATTN_OK)
             return st;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -5,16 +5,19 @@
 // tiles of 64. Per tile S = Q K^T (M 128, N 64) and O += P V (M 128, N d), accumulators in tensor
 // memory, P as the 16-bit A operand from tensor memory over S. Two blocks share an SM (96 KB of
 // shared memory and 256 tensor-memory columns each), so that one block's start, softmax latency and
-// end are covered by the other's loads. Roles of the eight warps:
-//   warp 0      loads: gather copies of four cache rows each through a tensor map of the cache viewed
-//               as [rows, Hkv d]; the row indices come from the page table, so any page size takes
-//               the same path, and rows past the end or of a bad page lie outside the map and arrive
-//               as zeros
+// end are covered by the other's loads. Roles of the warps:
+//   warps 0, 2  loads of K and of V, through tensor maps of the caches viewed as [rows, Hkv d]: boxes of
+//               64 or 16 rows where the page size is a multiple of that, else gather copies of four
+//               rows whose indices come from the page table. Rows past the end or of a bad page lie
+//               outside the map and arrive as zeros. (A copy instruction costs its warp about 66
+//               clocks: 64 gathers of a 32 KB tile took one warp 4600 clocks.)
 //   warp 1      issues the products and owns the tensor memory
-//   warps 2, 3  16-bit caches: pass the V tiles on, taking non-finite values out of those a row may
-//               not see in full. 8-bit caches: widen K and V tiles to f16 (exact) in shared memory
+//   warp 3      16-bit caches: passes the V tiles on, taking non-finite values out of those that a row
+//               may not see in full
 //   warps 4-7   softmax, one row per thread: maximum, conditional rescale of O (only when a maximum
 //               grows by more than the threshold), exponentials, P; at the end O / l and the LSE
+//   warps 8-11  8-bit caches only: two warps each widen the K and the V tiles to f16 (exact) in shared
+//               memory, V as warp 3 does
 // A 64-key tile of bf16 K and V is 32 KB, 1390 clocks of an SM's share of the memory bandwidth
 // (6.8 TB/s over 152 SMs at 1.9 GHz), against about 640 clocks of products: with up to 128 rows the
 // kernel should be bounded by the cache reads.
@@ -25,11 +28,11 @@ namespace {
 
 constexpr int kTileRows = 128;  // rows per block
 constexpr int kTileKeys = 64;
-constexpr int kTileThreads = 256;
 
 template <int D, int FMT>
 struct TileLayout {
     static constexpr bool kF8 = FMT != ATTN_KV_BF16;
+    static constexpr int kThreads = kF8 ? 384 : 256;
     static constexpr int kQBytes = kTileRows * D * 2;
     static constexpr int kChunkQ = kTileRows * 128;  // one [128 rows x 128 bytes] chunk of Q
     static constexpr int kTile16 = kTileKeys * D * 2;  // a 16-bit K or V tile the products read
@@ -65,6 +68,14 @@ __device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, ui
         : "memory");
 }
 
+// A box of rows (columns c .. c + box) from row r on.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c, int r) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(r)
+        : "memory");
+}
+
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit));
 }
@@ -81,33 +92,39 @@ __device__ __forceinline__ void lds128(uint32_t at, uint32_t (&w)[4]) {
 template <int D, int FMT>
 __device__ __forceinline__ bool widen_tile(uint32_t src, uint32_t dst, int t, bool clean) {
     constexpr int U = D / 16;  // 16-byte units of codes per row
+    constexpr int kBatch = 4;  // units loaded before the first is converted and stored
     bool odd = false;
-#pragma unroll 4
-    for (int x = t; x < kTileKeys * U; x += 64) {
-        const int r = x / U, u = x % U;
-        uint32_t w[4], h[8];
-        // 128-byte rows arrive in the 128-byte swizzle, 64-byte rows plain
-        lds128(src + r * D + ((D == 128 ? u ^ (r & 7) : u) << 4), w);
+#pragma unroll 1
+    for (int x0 = t; x0 < kTileKeys * U; x0 += 64 * kBatch) {
+        uint32_t w[kBatch][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = fp8x2_f16x2<FMT>(w[i / 2] >> (16 * (i & 1)));
-        if (clean) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t keep = finite_halves(h[i], true);
-                odd |= keep != 0xFFFFFFFFu;
-                h[i] &= keep;
-            }
+        for (int n = 0; n < kBatch; ++n) {
+            const int r = (x0 + 64 * n) / U, u = (x0 + 64 * n) % U;
+            // 128-byte rows arrive in the 128-byte swizzle, 64-byte rows plain
+            lds128(src + r * D + ((D == 128 ? u ^ (r & 7) : u) << 4), w[n]);
         }
-        // the two f16 units of this one; every other group of four lanes starts with the second, so
-        // that the eight lanes of a row write different banks
-        const uint32_t row = dst + (u >> 2) * (kTileKeys * 128) + r * 128;
-        const uint32_t a0 = row + (((2 * (u & 3)) ^ (r & 7)) << 4), a1 = row + (((2 * (u & 3) + 1) ^ (r & 7)) << 4);
-        if (u & 4) {
-            sts128(a1, h[4], h[5], h[6], h[7]);
-            sts128(a0, h[0], h[1], h[2], h[3]);
-        } else {
-            sts128(a0, h[0], h[1], h[2], h[3]);
-            sts128(a1, h[4], h[5], h[6], h[7]);
+#pragma unroll
+        for (int n = 0; n < kBatch; ++n) {
+            const int r = (x0 + 64 * n) / U, u = (x0 + 64 * n) % U;
+            uint32_t h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = fp8x2_f16x2<FMT>(w[n][i / 2] >> (16 * (i & 1)));
+            if (clean) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t keep = finite_halves(h[i], true);
+                    odd |= keep != 0xFFFFFFFFu;
+                    h[i] &= keep;
+                }
+            }
+            // the two f16 units of this one; lanes with u >= 4 start with the second, so that the
+            // eight lanes of a row write different banks
+            const bool second = (u & 4) != 0;
+            const uint32_t row = dst + (u >> 2) * (kTileKeys * 128) + r * 128;
+            const uint32_t a0 = row + (((2 * (u & 3) + second) ^ (r & 7)) << 4);
+            const uint32_t a1 = row + (((2 * (u & 3) + !second) ^ (r & 7)) << 4);
+            sts128(a0, second ? h[4] : h[0], second ? h[5] : h[1], second ? h[6] : h[2], second ? h[7] : h[3]);
+            sts128(a1, second ? h[0] : h[4], second ? h[1] : h[5], second ? h[2] : h[6], second ? h[3] : h[7]);
         }
     }
     return odd;
@@ -119,7 +136,7 @@ __host__ __device__ constexpr uint32_t idesc16(bool f16, uint32_t M, uint32_t N,
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kTileThreads, 2)
+__global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     tree_tile_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
     grid_dependents_launch();
     using L = TileLayout<D, FMT>;
@@ -178,7 +195,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
             mbar_init(&bars[L::bV + i], 1);
             mbar_init(&bars[L::bKFree + i], F8 ? 2 : 1);  // 8-bit: the two widening warps; else the products
             mbar_init(&bars[L::bVFree + i], F8 ? 2 : 1);
-            mbar_init(&bars[L::bClean + i], 2);
+            mbar_init(&bars[L::bClean + i], 1);
         }
         *abort_flag = 0;
         *odd_v = 0;
@@ -200,49 +217,54 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     // tiles from this one on hold drafted tokens or the end of the sequence
     const int first_mixed = s.ctx <= t_begin ? 0 : (s.ctx - t_begin) / kTileKeys;
 
-    if (warp == 0) {
-        // ---------------------------------------------------------------- loads
+    if (warp == 0 || warp == 2) {
+        // ---------------------------------------------------------------- loads of K (warp 0), V (warp 2)
+        const bool v = warp == 2;
+        const CUtensorMap* map = v ? &tmV : &tmK;
+        uint64_t* full = &bars[v ? L::bV : L::bK];
+        uint64_t* free = &bars[v ? L::bVFree : L::bKFree];
         const int none = p.num_pages * p.page_size;  // the first row past the cache: zeros
-        const int quad = lane & 15, half = lane >> 4;  // four rows; 64-column half (128-column rows)
-        constexpr bool kHalves = !F8 && D == 128;
+        // lane: its rows of the tile (four of them, or a box) and, for rows of two 128-byte chunks, which
+        constexpr int kParts = !F8 && D == 128 ? 2 : 1;
+        const int step = p.box_rows > 1 ? p.box_rows : 4;
+        const int per_part = kTileKeys / step;
+        const bool active = lane < kParts * per_part;
+        const int part = lane / per_part, first = (lane - part * per_part) * step;
+        const int col = kvh * D + part * 64;
+        const uint32_t dst = ring + (v ? L::kLoad : 0) + part * L::kChunk16 + first * (F8 ? D : 128);
         auto rows_of = [&](int i, int (&r)[4]) {
-            const int tok = t_begin + i * kTileKeys + 4 * quad;
+            const int tok = t_begin + i * kTileKeys + first;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int row = tok + e < t_end ? cache_row(p, pt, tok + e) : none;
+                if (e > 0 && p.box_rows > 1) break;  // a box lies in one page
+                const int row = active && tok + e < t_end ? cache_row(p, pt, tok + e) : none;
                 r[e] = row < 0 ? none : row;
             }
         };
-        const int col = kvh * D + (kHalves ? half * 64 : 0);
-        const bool active = kHalves || half == 0;
-        const uint32_t dst = (kHalves ? half * L::kChunk16 : 0) + quad * 4 * (F8 ? D : 128);
-        int r[4];
+        int r[4] = {0, 0, 0, 0};
         rows_of(0, r);
         bool ok = true;
-        int issued_k = 0, issued_v = 0;
+        int issued = 0;
         for (int i = 0; i < tiles; ++i) {
             const int st = i % NS;
-            const uint32_t par = (uint32_t)((i / NS) & 1) ^ 1u;
-            const uint32_t base = ring + st * 2 * L::kLoad + dst;
-            if (!(ok = wait_all(&bars[L::bKFree + st], par, abort_flag, wd))) break;
-            if (lane == 0) mbar_arrive_expect_tx(&bars[L::bK + st], L::kLoad);
+            if (!(ok = wait_all(&free[st], (uint32_t)((i / NS) & 1) ^ 1u, abort_flag, wd))) break;
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], L::kLoad);
             __syncwarp();
-            if (active) gather4(base, &tmK, &bars[L::bK + st], col, r);
-            issued_k = i + 1;
-            if (!(ok = wait_all(&bars[L::bVFree + st], par, abort_flag, wd))) break;
-            if (lane == 0) mbar_arrive_expect_tx(&bars[L::bV + st], L::kLoad);
+            if (active) {
+                if (p.box_rows > 1)
+                    copy_box(dst + st * 2 * L::kLoad, map, &full[st], col, r[0]);
+                else
+                    gather4(dst + st * 2 * L::kLoad, map, &full[st], col, r);
+            }
             __syncwarp();
-            if (active) gather4(base + L::kLoad, &tmV, &bars[L::bV + st], col, r);
-            issued_v = i + 1;
+            issued = i + 1;
             if (i + 1 < tiles) rows_of(i + 1, r);
         }
         if (!ok) {
             // let the copies in flight land before the block can end
             int dummy = 0;
-            for (int i = issued_k > NS ? issued_k - NS : 0; i < issued_k; ++i)
-                mbar_wait(&bars[L::bK + i % NS], (uint32_t)((i / NS) & 1), &dummy, 20000000ull);
-            for (int i = issued_v > NS ? issued_v - NS : 0; i < issued_v; ++i)
-                mbar_wait(&bars[L::bV + i % NS], (uint32_t)((i / NS) & 1), &dummy, 20000000ull);
+            for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
+                mbar_wait(&full[i % NS], (uint32_t)((i / NS) & 1), &dummy, 20000000ull);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- products
@@ -299,44 +321,17 @@ __global__ void __launch_bounds__(kTileThreads, 2)
             if (leader) mbar_wait(&bars[L::bDrain], 0, &dummy, 50000000ull);
             __syncwarp();
         }
-    } else if (warp < 4) {
-        // ---------------------------------------------------------------- V tiles (8-bit: K too)
-        const int t = threadIdx.x - 64;
-        bool ok = true;
-        for (int i = 0; i < tiles && ok; ++i) {
-            const int st = i % NS;
-            const uint32_t par = (uint32_t)((i / NS) & 1);
-            const bool mixed = i >= first_mixed;
-            const uint32_t kt = ring + st * 2 * L::kLoad, vt = kt + L::kLoad;
-            if constexpr (F8) {
-                const uint32_t wide = smem_u32(smem + L::kWideOff);
-                if (!(ok = wait_all(&bars[L::bK + st], par, abort_flag, wd))) break;
-                if (!(ok = wait_all(&bars[L::bWKFree], (uint32_t)(i & 1) ^ 1u, abort_flag, wd))) break;
-                widen_tile<D, FMT>(kt, wide, t, false);
-                fence_smem_to_async();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bars[L::bWK]);
-                    mbar_arrive(&bars[L::bKFree + st]);
-                }
-                if (!(ok = wait_all(&bars[L::bV + st], par, abort_flag, wd))) break;
-                if (!(ok = wait_all(&bars[L::bWVFree], (uint32_t)(i & 1) ^ 1u, abort_flag, wd))) break;
-                if (mixed) {
-                    if (widen_tile<D, FMT>(vt, wide + L::kTile16, t, true)) *odd_v = 1;
-                } else {
-                    widen_tile<D, FMT>(vt, wide + L::kTile16, t, false);
-                }
-                fence_smem_to_async();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bars[L::bWV]);
-                    mbar_arrive(&bars[L::bVFree + st]);
-                }
-            } else {
-                if (!(ok = wait_all(&bars[L::bV + st], par, abort_flag, wd))) break;
-                if (mixed) {
+    } else if (warp == 3) {
+        // ---------------------------------------------------------------- 16-bit V tiles
+        if constexpr (!F8) {
+            for (int i = 0; i < tiles; ++i) {
+                const int st = i % NS;
+                if (!wait_all(&bars[L::bV + st], (uint32_t)((i / NS) & 1), abort_flag, wd)) break;
+                if (i >= first_mixed) {
+                    const uint32_t vt = ring + st * 2 * L::kLoad + L::kLoad;
                     bool odd = false;
-                    for (int x = t; x < L::kTile16 / 16; x += 64) {
+#pragma unroll 4
+                    for (int x = lane; x < L::kTile16 / 16; x += 32) {
                         uint32_t w[4];
                         lds128(vt + 16 * x, w);
                         bool bad = false;
@@ -354,6 +349,33 @@ __global__ void __launch_bounds__(kTileThreads, 2)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[L::bClean + st]);
+            }
+        }
+    } else if (warp >= 8) {
+        // ---------------------------------------------------------------- 8-bit tiles to f16
+        if constexpr (F8) {
+            const bool v = warp >= 10;
+            const int t = threadIdx.x & 63;
+            const uint32_t wide = smem_u32(smem + L::kWideOff) + (v ? L::kTile16 : 0);
+            uint64_t* full = &bars[v ? L::bV : L::bK];
+            uint64_t* free = &bars[v ? L::bVFree : L::bKFree];
+            uint64_t* wide_free = &bars[v ? L::bWVFree : L::bWKFree];
+            for (int i = 0; i < tiles; ++i) {
+                const int st = i % NS;
+                if (!wait_all(&full[st], (uint32_t)((i / NS) & 1), abort_flag, wd)) break;
+                if (!wait_all(wide_free, (uint32_t)(i & 1) ^ 1u, abort_flag, wd)) break;
+                const uint32_t src = ring + st * 2 * L::kLoad + (v ? L::kLoad : 0);
+                if (v && i >= first_mixed) {
+                    if (widen_tile<D, FMT>(src, wide, t, true)) *odd_v = 1;
+                } else {
+                    widen_tile<D, FMT>(src, wide, t, false);
+                }
+                fence_smem_to_async();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars[v ? L::bWV : L::bWK]);
+                    mbar_arrive(&free[st]);
+                }
             }
         }
     } else {
@@ -396,33 +418,38 @@ __global__ void __launch_bounds__(kTileThreads, 2)
             const uint32_t tS = tmem + lane_off + kColS + 64 * sb;
             if (!(ok = wait_all(&bars[L::bS + sb], (uint32_t)((i >> 1) & 1), abort_flag, wd))) break;
             tc_fence_after();
-            uint32_t rr[2][32];
-            tmem_ld32(tS, rr[0]);
-            tmem_ld32(tS + 32, rr[1]);
-            tc_wait_ld();
-            reg_fence(rr[0]);
-            reg_fence(rr[1]);
-            float sv[kTileKeys];
-#pragma unroll
-            for (int c = 0; c < kTileKeys; ++c) sv[c] = __uint_as_float(rr[c >> 5][c & 31]);
+            // The row's 64 scores pass through 32 registers, the first half twice: maximum of keys
+            // 0-31, maximum and exponentials of 32-63, exponentials of 0-31.
+            uint32_t w0 = ~0u, w1 = ~0u;
             if (i >= first_mixed) {
                 const unsigned long long w = tree_window(mrow, p.mask_words, node, s.ctx, s.len, t_begin + i * kTileKeys);
-                const uint32_t w0 = (uint32_t)w, w1 = (uint32_t)(w >> 32);
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    if (!((w0 >> c) & 1)) sv[c] = -INFINITY;
-                    if (!((w1 >> c) & 1)) sv[32 + c] = -INFINITY;
-                }
+                w0 = (uint32_t)w, w1 = (uint32_t)(w >> 32);
             }
-            float mx[8];
+            uint32_t x[32];
+            auto load_scores = [&](int c0, uint32_t seen) {
+                tmem_ld32(tS + c0, x);
+                tc_wait_ld();
+                reg_fence(x);
+                if (i >= first_mixed) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) mx[e] = fmaxf(sv[e], sv[e + 8]);
+                    for (int c = 0; c < 32; ++c)
+                        if (!((seen >> c) & 1)) x[c] = 0xFF800000u;  // -inf
+                }
+            };
+            auto top_score = [&]() {
+                float mx[4];
 #pragma unroll
-            for (int c = 16; c < kTileKeys; c += 16)
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 4]));
 #pragma unroll
-                for (int e = 0; e < 8; ++e) mx[e] = max3f(mx[e], sv[c + e], sv[c + 8 + e]);
-            const float mt = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-            const float mc = fmaxf(m, mt);
+                for (int c = 8; c < 32; c += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[e] = max3f(mx[e], __uint_as_float(x[c + e]), __uint_as_float(x[c + 4 + e]));
+                return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            };
+            load_scores(0, w0);
+            float mc = fmaxf(m, top_score());
+            load_scores(32, w1);
+            mc = fmaxf(mc, top_score());
             if (__any_sync(0xffffffffu, (mc - m) * sl2 > p.rescale_thr)) {  // NaN (both -inf) is false
                 const float alpha = m == -INFINITY ? 0.0f : ex2_mufu((m - mc) * sl2);
                 if (i > 0) {
@@ -445,17 +472,23 @@ __global__ void __launch_bounds__(kTileThreads, 2)
             }
             const float neg = m == -INFINITY ? 0.0f : -m * sl2;
             float sum[4] = {0, 0, 0, 0};
-            uint32_t pk[kTileKeys / 2];
+            uint32_t pk[16];
+            auto exponentials = [&]() {
 #pragma unroll
-            for (int c = 0; c < kTileKeys; c += 2) {
-                float x0, x1;
-                ffma2(x0, x1, sv[c], sv[c + 1], sl2, sl2, neg, neg);
-                const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
-                const int a = ((c >> 1) & 1) * 2;
-                fadd2(sum[a], sum[a + 1], sum[a], sum[a + 1], p0, p1);
-                pk[c >> 1] = F8 ? pack_half2(p0, p1) : pack_bf16x2(p0, p1);
-            }
-            tmem_st32(tS, pk);
+                for (int c = 0; c < 32; c += 2) {
+                    float x0, x1;
+                    ffma2(x0, x1, __uint_as_float(x[c]), __uint_as_float(x[c + 1]), sl2, sl2, neg, neg);
+                    const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
+                    const int a = ((c >> 1) & 1) * 2;
+                    fadd2(sum[a], sum[a + 1], sum[a], sum[a + 1], p0, p1);
+                    pk[c >> 1] = F8 ? pack_half2(p0, p1) : pack_bf16x2(p0, p1);
+                }
+            };
+            exponentials();
+            load_scores(0, w0);  // before P of keys 32-63 goes over them
+            tmem_st16(tS + 16, pk);
+            exponentials();
+            tmem_st16(tS, pk);
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tc_wait_st();
             tc_fence_before();
@@ -466,7 +499,6 @@ __global__ void __launch_bounds__(kTileThreads, 2)
         if (ok) ok = wait_all(&bars[L::bLast], 0, abort_flag, wd);
         if (ok) {
             tc_fence_after();
-            const bool odd = *odd_v != 0;
             const float inv = l == 0.0f ? 0.0f : p.v_descale / l;
             const bool empty = l == 0.0f;
 #pragma unroll 1
@@ -478,11 +510,6 @@ __global__ void __launch_bounds__(kTileThreads, 2)
                 float v[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]);
-                if (odd && valid) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        v[e] += nonfinite_sum<FMT>(p, pt, mrow, node, s, max(t_begin, s.ctx / kTileKeys * kTileKeys), t_end, kvh, D, c + e);
-                }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = empty ? 0.0f : v[e] * inv;
                 if (valid && nsplit == 1) {
@@ -498,6 +525,18 @@ __global__ void __launch_bounds__(kTileThreads, 2)
                 }
                 __syncwarp();
             }
+            if (*odd_v && valid && !empty) {
+                // what was taken out of V replaces the outputs that it reaches (finite + inf = inf)
+#pragma unroll 1
+                for (int c = 0; c < D; ++c) {
+                    const float x = nonfinite_sum<FMT>(p, pt, mrow, node, s, max(t_begin, s.ctx / kTileKeys * kTileKeys), t_end, kvh, D, c);
+                    if (x == 0.0f) continue;
+                    if (nsplit == 1)
+                        p.o[orow * D + c] = __float2bfloat16(x * inv);
+                    else
+                        p.ws_o[(orow * p.max_splits + split) * D + c] = x * inv;
+                }
+            }
             if (valid) {
                 const float lse = empty ? -INFINITY : m * p.scale + logf(l);
                 if (nsplit == 1)
@@ -511,7 +550,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     // -------------------------------------------------------------------- end
     __syncwarp();
     tc_fence_before();
-    named_bar_sync(1, kTileThreads);
+    named_bar_sync(1, L::kThreads);
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, kCols);
     if (threadIdx.x == 0 && *abort_flag) atomicCAS(p.status, 0, kDevTimeout);
@@ -526,7 +565,7 @@ cudaError_t launch_tiles(TreeParams p, const TreeTmaps& tm, cudaStream_t stream)
     p.groups = (int)(((long long)p.max_q * p.G + kTileRows - 1) / kTileRows);
     const long long x = (long long)p.max_splits * p.Hkv * p.groups;
     if (x > INT32_MAX) return cudaErrorInvalidConfiguration;
-    tree_tile_kernel<D, FMT><<<dim3((unsigned)x, (unsigned)p.B), kTileThreads, bytes, stream>>>(p, tm.k, tm.v);
+    tree_tile_kernel<D, FMT><<<dim3((unsigned)x, (unsigned)p.B), TileLayout<D, FMT>::kThreads, bytes, stream>>>(p, tm.k, tm.v);
     return cudaGetLastError();
 }
 

@@ -27,12 +27,13 @@ struct TreeParams {
     float v_descale, rescale_thr;
     unsigned int ps_magic;   // tok / page_size by multiplication, as in DecodeParams
     int ps_shift;
+    int box_rows;            // rows of a box of the maps (64 or 16, dividing the page size), 1: gather copies
     int* status;
     unsigned long long watchdog_ns;
 };
 
-// 2-D maps over the caches viewed as [num_pages * page_size, Hkv * d], box one row of 128 bytes (64
-// for 8-bit d = 64), for gather copies of four rows.
+// 2-D maps over the caches viewed as [num_pages * page_size, Hkv * d], box box_rows rows of 128 bytes
+// (64 for 8-bit d = 64); with one row, for gather copies of four rows.
 struct TreeTmaps {
     CUtensorMap k, v;
 };

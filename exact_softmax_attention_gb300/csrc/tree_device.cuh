@@ -113,7 +113,7 @@ __device__ __forceinline__ float cached_value(const void* cache, long long e) {
 // Sum of the non-finite values in column d of the V rows of tokens [t0, t1) that row i sees: what the
 // products left out of the tiles where they took them for zero.
 template <int FMT>
-__device__ __noinline__ float nonfinite_sum(const TreeParams& p, const int* pt, const unsigned long long* mrow, int i, const TreeSeq& s,
+__device__ __forceinline__ float nonfinite_sum(const TreeParams& p, const int* pt, const unsigned long long* mrow, int i, const TreeSeq& s,
                                int t0, int t1, int kvh, int D, int d) {
     float sum = 0.0f;
     for (int t = t0; t < t1; ++t) {
