@@ -474,12 +474,18 @@ void tree_plan(int B, int Hkv, int rows, long long lmax, int num_splits, int num
     long long c;
     if (num_splits > 0) {
         c = (lmax + num_splits - 1) / num_splits;
+    } else if (tree_takes_tiles(rows)) {
+        // One item per resident block (two per SM) when the sequences are few, so that one wave covers
+        // them; at most 8192 tokens per item, so that sequences of different lengths balance.
+        const long long pairs = (long long)B * Hkv * ((rows + 127) / 128);
+        const long long splits = 2LL * num_sms / pairs;
+        c = splits > 1 ? (lmax + splits - 1) / splits : lmax;
+        if (c < 128) c = 128;
+        if (c > 8192) c = 8192;
     } else {
-        const bool tiles = tree_takes_tiles(rows);
-        const long long groups = tiles ? (rows + 127) / 128 : 1;
-        const long long work = (long long)B * Hkv * groups * ((lmax + 1) / 2);
-        const long long items = (tiles ? 8LL : 18LL) * num_sms, least = tiles ? 256 : 128LL * (rows > 2 ? rows : 2);
-        c = (work + items - 1) / items;
+        const long long work = (long long)B * Hkv * ((lmax + 1) / 2);
+        const long long least = 128LL * (rows > 2 ? rows : 2);
+        c = (work + 18LL * num_sms - 1) / (18LL * num_sms);
         if (c < least) c = least;
         if (c > 8192) c = 8192;
     }

@@ -41,17 +41,18 @@ struct TileLayout {
     static constexpr int kStages = D == 128 ? 2 : 4;  // loaded K/V tile pairs in flight
     static constexpr int kQOff = 0;
     static constexpr int kRingOff = kQBytes;  // stage s: K tile, V tile
-    static constexpr int kWideOff = kRingOff + kStages * 2 * kLoad;  // 8-bit caches: the f16 K and V tile
-    static constexpr int kBarOff = kWideOff + (kF8 ? 2 * kTile16 : 0);
+    static constexpr int kWideOff = kRingOff + kStages * 2 * kLoad;  // 8-bit caches: f16 tiles, K twice and V
+    static constexpr int kBarOff = kWideOff + (kF8 ? 3 * kTile16 : 0);
     // barriers
-    static constexpr int bQ = 0, bO = 1, bS = 2, bP = 4, bWK = 6, bWV = 7, bWKFree = 8, bWVFree = 9, bDrain = 10, bLast = 11;
-    static constexpr int bK = 12, bV = bK + kStages, bKFree = bV + kStages, bVFree = bKFree + kStages;
+    static constexpr int bQ = 0, bO = 1, bS = 2, bP = 4, bWK = 6, bWKFree = 8, bWV = 10, bWVFree = 11, bDrain = 12, bLast = 13;
+    static constexpr int bK = 14, bV = bK + kStages, bKFree = bV + kStages, bVFree = bKFree + kStages;
     static constexpr int bClean = bVFree + kStages;
     static constexpr int kBars = bClean + kStages;
     static constexpr int kMiscOff = kBarOff + kBars * 8;  // tensor-memory base, abort flag, odd-value flag
     static constexpr int kBytes = kMiscOff + 16;
-    // at least 80 KB, so that no more than two blocks (256 tensor-memory columns each) share an SM
-    static constexpr int kAlloc = kBytes + 1024 > 81920 ? kBytes + 1024 : 81920;
+    // at least 80 KB, so that no more than two blocks (256 tensor-memory columns each) share an SM; the
+    // dynamic shared memory has to start on a 1024-byte boundary (checked)
+    static constexpr int kAlloc = kBytes > 81920 ? kBytes : 81920;
     static_assert(kAlloc <= 115712, "two blocks per SM");
 };
 
@@ -87,29 +88,44 @@ __device__ __forceinline__ void lds128(uint32_t at, uint32_t (&w)[4]) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
 }
 
+// Two 8-bit codes in the low (or high) half of w as an f16 pair; e5m2 is the upper byte of an f16.
+template <int FMT, int HI>
+__device__ __forceinline__ uint32_t widen_pair(uint32_t w) {
+    if constexpr (FMT == ATTN_FP8_E5M2)
+        return __byte_perm(w, 0, HI ? 0x3424 : 0x1404);
+    else
+        return fp8x2_f16x2<FMT>(HI ? w >> 16 : w);
+}
+
 // Widen the 64-row tile of 8-bit codes at src into f16 at dst (chunks of [64 rows x 128 bytes],
-// 128-byte swizzle); thread t of 64. clean: take non-finite values out, return whether there were any.
-template <int D, int FMT>
-__device__ __forceinline__ bool widen_tile(uint32_t src, uint32_t dst, int t, bool clean) {
-    constexpr int U = D / 16;  // 16-byte units of codes per row
-    constexpr int kBatch = 4;  // units loaded before the first is converted and stored
+// 128-byte swizzle); thread t of 64. kClean: take non-finite values out, return whether there were any.
+// Eight neighbouring threads take four 16-byte units each of a row pair (at d = 128 the lower units of
+// one row and the upper ones of the other), so that neither the loads nor the stores conflict.
+template <int D, int FMT, bool kClean>
+__device__ __forceinline__ bool widen_tile(uint32_t src, uint32_t dst, int t) {
+    constexpr int kSteps = D == 128 ? 2 : 1;  // units per thread and row pair
+    const int odd_row = (t >> 2) & 1, row = 2 * (t >> 3) + odd_row, low = t & 3;
+    const uint32_t sw = (uint32_t)(row & 7);  // rows advance by 16: the same swizzle
     bool odd = false;
-#pragma unroll 1
-    for (int x0 = t; x0 < kTileKeys * U; x0 += 64 * kBatch) {
-        uint32_t w[kBatch][4];
 #pragma unroll
-        for (int n = 0; n < kBatch; ++n) {
-            const int r = (x0 + 64 * n) / U, u = (x0 + 64 * n) % U;
-            // 128-byte rows arrive in the 128-byte swizzle, 64-byte rows plain
-            lds128(src + r * D + ((D == 128 ? u ^ (r & 7) : u) << 4), w[n]);
-        }
+    for (int half = 0; half < kSteps; ++half) {
+        const int u = D == 128 ? low + 4 * (odd_row ^ half) : low;
+        // 128-byte rows arrive in the 128-byte swizzle, 64-byte rows plain
+        const uint32_t from = src + row * D + ((D == 128 ? u ^ sw : (uint32_t)u) << 4);
+        const uint32_t to = dst + (u >> 2) * (kTileKeys * 128) + row * 128;
+        const uint32_t to0 = to + (((2 * (u & 3)) ^ sw) << 4), to1 = to + (((2 * (u & 3) + 1) ^ sw) << 4);
+        uint32_t w[4][4];  // rows row, row + 16, ...: loaded before the first is stored
 #pragma unroll
-        for (int n = 0; n < kBatch; ++n) {
-            const int r = (x0 + 64 * n) / U, u = (x0 + 64 * n) % U;
+        for (int n = 0; n < 4; ++n) lds128(from + n * 16 * D, w[n]);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
             uint32_t h[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = fp8x2_f16x2<FMT>(w[n][i / 2] >> (16 * (i & 1)));
-            if (clean) {
+            for (int i = 0; i < 4; ++i) {
+                h[2 * i] = widen_pair<FMT, 0>(w[n][i]);
+                h[2 * i + 1] = widen_pair<FMT, 1>(w[n][i]);
+            }
+            if (kClean) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint32_t keep = finite_halves(h[i], true);
@@ -117,14 +133,8 @@ __device__ __forceinline__ bool widen_tile(uint32_t src, uint32_t dst, int t, bo
                     h[i] &= keep;
                 }
             }
-            // the two f16 units of this one; lanes with u >= 4 start with the second, so that the
-            // eight lanes of a row write different banks
-            const bool second = (u & 4) != 0;
-            const uint32_t row = dst + (u >> 2) * (kTileKeys * 128) + r * 128;
-            const uint32_t a0 = row + (((2 * (u & 3) + second) ^ (r & 7)) << 4);
-            const uint32_t a1 = row + (((2 * (u & 3) + !second) ^ (r & 7)) << 4);
-            sts128(a0, second ? h[4] : h[0], second ? h[5] : h[1], second ? h[6] : h[2], second ? h[7] : h[3]);
-            sts128(a1, second ? h[0] : h[4], second ? h[1] : h[5], second ? h[2] : h[6], second ? h[3] : h[7]);
+            sts128(to0 + n * 16 * 128, h[0], h[1], h[2], h[3]);
+            sts128(to1 + n * 16 * 128, h[4], h[5], h[6], h[7]);
         }
     }
     return odd;
@@ -168,8 +178,11 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     const int t_end = min(s.len, t_begin + p.chunk);
     const int tiles = cdiv(t_end - t_begin, kTileKeys);
 
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {  // the swizzles count from such boundaries
+        if (threadIdx.x == 0) atomicCAS(p.status, 0, kDevTimeout);
+        return;
+    }
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
@@ -177,16 +190,19 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t wd = p.watchdog_ns;
     const int* pt = p.page_table + (long long)b * p.max_pages;
+    // Warps with rows. The rows of padding hold whatever they find in shared and tensor memory: every
+    // row of the products depends on its own row of Q and P alone.
+    const int row_warps = cdiv(R, 32);
     if (threadIdx.x == 0) {
-        mbar_init(&bars[L::bQ], 4);
+        mbar_init(&bars[L::bQ], row_warps);
         mbar_init(&bars[L::bO], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars[L::bS + i], 1);
-            mbar_init(&bars[L::bP + i], 4);
+            mbar_init(&bars[L::bP + i], row_warps);
+            mbar_init(&bars[L::bWK + i], 2);
+            mbar_init(&bars[L::bWKFree + i], 1);
         }
-        mbar_init(&bars[L::bWK], 2);
         mbar_init(&bars[L::bWV], 2);
-        mbar_init(&bars[L::bWKFree], 1);
         mbar_init(&bars[L::bWVFree], 1);
         mbar_init(&bars[L::bDrain], 1);
         mbar_init(&bars[L::bLast], 1);
@@ -232,21 +248,34 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
         const int part = lane / per_part, first = (lane - part * per_part) * step;
         const int col = kvh * D + part * 64;
         const uint32_t dst = ring + (v ? L::kLoad : 0) + part * L::kChunk16 + first * (F8 ? D : 128);
-        auto rows_of = [&](int i, int (&r)[4]) {
+        // The pages of the next tile are looked up before the copies of this one are issued, all loads
+        // before the first is used. n: rows (gather) or boxes of this lane with a token.
+        const int width = p.box_rows > 1 ? 1 : 4;
+        int page[4], slot[4], n = 0;
+        auto look_up = [&](int i) {
             const int tok = t_begin + i * kTileKeys + first;
+            n = active ? min(width, max(0, t_end - tok)) : 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (e > 0 && p.box_rows > 1) break;  // a box lies in one page
-                const int row = active && tok + e < t_end ? cache_row(p, pt, tok + e) : none;
-                r[e] = row < 0 ? none : row;
-            }
+            for (int e = 0; e < 4; ++e)
+                if (e < n) page[e] = __ldg(pt + page_of(p, tok + e, slot[e]));
         };
-        int r[4] = {0, 0, 0, 0};
-        rows_of(0, r);
+        look_up(0);
         bool ok = true;
         int issued = 0;
         for (int i = 0; i < tiles; ++i) {
             const int st = i % NS;
+            int r[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                r[e] = none;
+                if (e < n) {
+                    if (page[e] >= 0 && page[e] < p.num_pages)
+                        r[e] = page[e] * p.page_size + slot[e];  // < num_pages * page_size <= INT32_MAX
+                    else
+                        atomicCAS(p.status, 0, kDevBadIndex);
+                }
+            }
+            if (i + 1 < tiles) look_up(i + 1);
             if (!(ok = wait_all(&free[st], (uint32_t)((i / NS) & 1) ^ 1u, abort_flag, wd))) break;
             if (lane == 0) mbar_arrive_expect_tx(&full[st], L::kLoad);
             __syncwarp();
@@ -258,7 +287,6 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
             }
             __syncwarp();
             issued = i + 1;
-            if (i + 1 < tiles) rows_of(i + 1, r);
         }
         if (!ok) {
             // let the copies in flight land before the block can end
@@ -274,7 +302,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
         constexpr uint32_t idS = idesc16(F8, kTileRows, kTileKeys, 0), idO = idesc16(F8, kTileRows, D, 1);
         const uint64_t dq = smem_desc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
         const uint32_t k_base = F8 ? smem_u32(smem + L::kWideOff) : ring;
-        const uint32_t v_base = k_base + L::kTile16;
+        const uint32_t v_base = k_base + (F8 ? 2 : 1) * L::kTile16;
         const uint64_t dk = smem_desc_sw128(k_base, 16, 1024);
         const uint64_t dv = smem_desc_sw128(v_base, L::kChunk16, 1024);
         bool ok = wait_all(&bars[L::bQ], 0, abort_flag, wd);
@@ -298,19 +326,19 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
         };
         for (int i = 0; i < tiles && ok; ++i) {
             const int st = i % NS;
-            if (!(ok = wait_all(F8 ? &bars[L::bWK] : &bars[L::bK + st], F8 ? (uint32_t)(i & 1) : (uint32_t)((i / NS) & 1), abort_flag,
-                                wd)))
+            if (!(ok = wait_all(F8 ? &bars[L::bWK + (i & 1)] : &bars[L::bK + st],
+                                F8 ? (uint32_t)((i >> 1) & 1) : (uint32_t)((i / NS) & 1), abort_flag, wd)))
                 break;
             tc_fence_after();
             any = true;
-            const uint64_t kd = dk + (uint64_t)(F8 ? 0 : (st * 2 * L::kLoad) >> 4);
+            const uint64_t kd = dk + (uint64_t)((F8 ? (i & 1) * L::kTile16 : st * 2 * L::kLoad) >> 4);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
                 tc_mma_ss_by(leader, tmem + kColS + 64 * (i & 1), dq + (uint64_t)(((k >> 2) * L::kChunkQ + (k & 3) * 32) >> 4),
                              kd + (uint64_t)(((k >> 2) * L::kChunk16 + (k & 3) * 32) >> 4), idS, k > 0 ? 1u : 0u);
             __syncwarp();
             tc_commit_by(leader, &bars[L::bS + (i & 1)]);
-            tc_commit_by(leader, F8 ? &bars[L::bWKFree] : &bars[L::bKFree + st]);
+            tc_commit_by(leader, F8 ? &bars[L::bWKFree + (i & 1)] : &bars[L::bKFree + st]);
             if (i > 0) ok = pv(i - 1);
         }
         if (ok) ok = pv(tiles - 1);
@@ -356,29 +384,28 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
         if constexpr (F8) {
             const bool v = warp >= 10;
             const int t = threadIdx.x & 63;
-            const uint32_t wide = smem_u32(smem + L::kWideOff) + (v ? L::kTile16 : 0);
+            const uint32_t wide = smem_u32(smem + L::kWideOff) + (v ? 2 * L::kTile16 : 0);
             uint64_t* full = &bars[v ? L::bV : L::bK];
             uint64_t* free = &bars[v ? L::bVFree : L::bKFree];
-            uint64_t* wide_free = &bars[v ? L::bWVFree : L::bWKFree];
             for (int i = 0; i < tiles; ++i) {
-                const int st = i % NS;
+                const int st = i % NS, wb = v ? 0 : i & 1;  // two f16 K tiles, one V tile
                 if (!wait_all(&full[st], (uint32_t)((i / NS) & 1), abort_flag, wd)) break;
-                if (!wait_all(wide_free, (uint32_t)(i & 1) ^ 1u, abort_flag, wd)) break;
-                const uint32_t src = ring + st * 2 * L::kLoad + (v ? L::kLoad : 0);
+                if (!wait_all(&bars[v ? L::bWVFree : L::bWKFree + wb], (uint32_t)((v ? i : i >> 1) & 1) ^ 1u, abort_flag, wd)) break;
+                const uint32_t src = ring + st * 2 * L::kLoad + (v ? L::kLoad : 0), dst = wide + wb * L::kTile16;
                 if (v && i >= first_mixed) {
-                    if (widen_tile<D, FMT>(src, wide, t, true)) *odd_v = 1;
+                    if (widen_tile<D, FMT, true>(src, dst, t)) *odd_v = 1;
                 } else {
-                    widen_tile<D, FMT>(src, wide, t, false);
+                    widen_tile<D, FMT, false>(src, dst, t);
                 }
                 fence_smem_to_async();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&bars[v ? L::bWV : L::bWK]);
+                    mbar_arrive(&bars[v ? L::bWV : L::bWK + wb]);
                     mbar_arrive(&free[st]);
                 }
             }
         }
-    } else {
+    } else if (warp - 4 < row_warps) {
         // ---------------------------------------------------------------- softmax and output
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;

@@ -67,15 +67,22 @@ __device__ __forceinline__ unsigned long long tree_window(const unsigned long lo
     return w;
 }
 
+// Page-table index and slot of token tok (0 <= tok < 2^31).
+__device__ __forceinline__ int page_of(const TreeParams& p, int tok, int& slot) {
+    const int q = p.ps_magic ? (int)(__umulhi((unsigned)tok, p.ps_magic) >> p.ps_shift) : tok;
+    slot = tok - q * p.page_size;
+    return q;
+}
+
 // Cache row of token tok of a sequence (pt: its row of the page table), or -1 for a page out of range.
 __device__ __forceinline__ int cache_row(const TreeParams& p, const int* pt, int tok) {
-    const int q = p.ps_magic ? (int)(__umulhi((unsigned)tok, p.ps_magic) >> p.ps_shift) : tok;
-    const int pg = __ldg(pt + q);
+    int slot;
+    const int pg = __ldg(pt + page_of(p, tok, slot));
     if (pg < 0 || pg >= p.num_pages) {
         atomicCAS(p.status, 0, kDevBadIndex);
         return -1;
     }
-    return pg * p.page_size + (tok - q * p.page_size);  // < num_pages * page_size <= INT32_MAX
+    return pg * p.page_size + slot;  // < num_pages * page_size <= INT32_MAX
 }
 
 template <int FMT>
