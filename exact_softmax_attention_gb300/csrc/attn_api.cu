@@ -122,7 +122,7 @@ attn_status_t make_cache_map(CUtensorMap* m, const void* base, long long rows, i
 }
 
 // 2-D map over a paged cache viewed as [rows, row_elems]: boxes of box_rows rows (1: for gather copies of
-// four rows), 128 bytes wide with the 128-byte swizzle, or d = 64 8-bit codes without one.
+// four rows), 128 bytes wide with the 128-byte swizzle, or d = 64 8-bit codes with the 64-byte one.
 attn_status_t make_tree_map(CUtensorMap* m, const void* base, long long rows, long long row_elems, int d, int elem,
                             int box_rows) {
     cuuint64_t dims[2] = {(cuuint64_t)row_elems, (cuuint64_t)rows};
@@ -132,7 +132,7 @@ attn_status_t make_tree_map(CUtensorMap* m, const void* base, long long rows, lo
     cuuint32_t estr[2] = {1, 1};
     CUresult r = g_encode(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
                           const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                          box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }

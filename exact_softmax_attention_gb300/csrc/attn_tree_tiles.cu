@@ -32,19 +32,19 @@ constexpr int kTileKeys = 64;
 template <int D, int FMT>
 struct TileLayout {
     static constexpr bool kF8 = FMT != ATTN_KV_BF16;
-    static constexpr int kThreads = kF8 ? 384 : 256;
-    static constexpr int kQBytes = kTileRows * D * 2;
-    static constexpr int kChunkQ = kTileRows * 128;  // one [128 rows x 128 bytes] chunk of Q
-    static constexpr int kTile16 = kTileKeys * D * 2;  // a 16-bit K or V tile the products read
-    static constexpr int kChunk16 = kTileKeys * 128;
+    static constexpr int kThreads = kF8 ? 384 : 288;
+    static constexpr int kQBytes = kTileRows * D * 2;  // 16-bit Q, or its two 8-bit parts
+    static constexpr int kChunkQ = kTileRows * 128;    // one [128 rows x 128 bytes] chunk of 16-bit Q
+    static constexpr int kTile16 = kTileKeys * D * 2;  // a 16-bit K or V tile
+    static constexpr int kChunk16 = kTileKeys * 128;   // one [64 keys x 128 bytes] chunk of it
     static constexpr int kLoad = kF8 ? kTileKeys * D : kTile16;  // a K or V tile as loaded
-    static constexpr int kStages = D == 128 ? 2 : 4;  // loaded K/V tile pairs in flight
+    static constexpr int kStages = D == 128 ? (kF8 ? 3 : 2) : (kF8 ? 6 : 4);  // loaded K/V tile pairs in flight
     static constexpr int kQOff = 0;
     static constexpr int kRingOff = kQBytes;  // stage s: K tile, V tile
-    static constexpr int kWideOff = kRingOff + kStages * 2 * kLoad;  // 8-bit caches: f16 tiles, K twice and V
-    static constexpr int kBarOff = kWideOff + (kF8 ? 3 * kTile16 : 0);
-    // barriers
-    static constexpr int bQ = 0, bO = 1, bS = 2, bP = 4, bWK = 6, bWKFree = 8, bWV = 10, bWVFree = 11, bDrain = 12, bLast = 13;
+    static constexpr int kWideOff = kRingOff + kStages * 2 * kLoad;  // 8-bit caches: two f16 V tiles
+    static constexpr int kBarOff = kWideOff + (kF8 ? 2 * kTile16 : 0);
+    // barriers; pairs are [tile parity]
+    static constexpr int bQ = 0, bS = 1, bP = 3, bPFree = 5, bWV = 7, bWVFree = 9, bDrain = 11, bLast = 13;
     static constexpr int bK = 14, bV = bK + kStages, bKFree = bV + kStages, bVFree = bKFree + kStages;
     static constexpr int bClean = bVFree + kStages;
     static constexpr int kBars = bClean + kStages;
@@ -77,6 +77,21 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// D (+)= A B of 8-bit operands in shared memory.
+__device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// K-major shared-memory descriptor of rows of 64 bytes with the 64-byte swizzle (eight rows are 512 bytes).
+__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(512 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)4 << 61;
+}
+
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit));
 }
@@ -98,51 +113,64 @@ __device__ __forceinline__ uint32_t widen_pair(uint32_t w) {
 }
 
 // Widen the 64-row tile of 8-bit codes at src into f16 at dst (chunks of [64 rows x 128 bytes],
-// 128-byte swizzle); thread t of 64. kClean: take non-finite values out, return whether there were any.
+// 128-byte swizzle); thread t of 128. kClean: take non-finite values out, return whether there were any.
 // Eight neighbouring threads take four 16-byte units each of a row pair (at d = 128 the lower units of
 // one row and the upper ones of the other), so that neither the loads nor the stores conflict.
 template <int D, int FMT, bool kClean>
 __device__ __forceinline__ bool widen_tile(uint32_t src, uint32_t dst, int t) {
-    constexpr int kSteps = D == 128 ? 2 : 1;  // units per thread and row pair
+    constexpr int kHalves = D == 128 ? 2 : 1;  // units per thread and row pair
+    constexpr int kPasses = 2;                 // row pairs t / 8 and t / 8 + 16
     const int odd_row = (t >> 2) & 1, row = 2 * (t >> 3) + odd_row, low = t & 3;
-    const uint32_t sw = (uint32_t)(row & 7);  // rows advance by 16: the same swizzle
+    const uint32_t sw = (uint32_t)(row & 7);  // rows advance by 32: the same swizzle
+    uint32_t w[kHalves * kPasses][4];  // all loaded before the first is stored
+#pragma unroll
+    for (int x = 0; x < kHalves * kPasses; ++x) {
+        const int u = D == 128 ? low + 4 * (odd_row ^ (x & 1)) : low;
+        const int n = D == 128 ? x >> 1 : x;
+        // 128-byte rows arrive in the 128-byte swizzle, 64-byte rows in the 64-byte one
+        lds128(src + (row + 32 * n) * D + ((D == 128 ? u ^ sw : u ^ ((sw >> 1) & 3)) << 4), w[x]);
+    }
     bool odd = false;
 #pragma unroll
-    for (int half = 0; half < kSteps; ++half) {
-        const int u = D == 128 ? low + 4 * (odd_row ^ half) : low;
-        // 128-byte rows arrive in the 128-byte swizzle, 64-byte rows plain
-        const uint32_t from = src + row * D + ((D == 128 ? u ^ sw : (uint32_t)u) << 4);
-        const uint32_t to = dst + (u >> 2) * (kTileKeys * 128) + row * 128;
-        const uint32_t to0 = to + (((2 * (u & 3)) ^ sw) << 4), to1 = to + (((2 * (u & 3) + 1) ^ sw) << 4);
-        uint32_t w[4][4];  // rows row, row + 16, ...: loaded before the first is stored
+    for (int x = 0; x < kHalves * kPasses; ++x) {
+        const int u = D == 128 ? low + 4 * (odd_row ^ (x & 1)) : low;
+        const int n = D == 128 ? x >> 1 : x;
+        uint32_t h[8];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) lds128(from + n * 16 * D, w[n]);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            uint32_t h[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                h[2 * i] = widen_pair<FMT, 0>(w[n][i]);
-                h[2 * i + 1] = widen_pair<FMT, 1>(w[n][i]);
-            }
-            if (kClean) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t keep = finite_halves(h[i], true);
-                    odd |= keep != 0xFFFFFFFFu;
-                    h[i] &= keep;
-                }
-            }
-            sts128(to0 + n * 16 * 128, h[0], h[1], h[2], h[3]);
-            sts128(to1 + n * 16 * 128, h[4], h[5], h[6], h[7]);
+        for (int i = 0; i < 4; ++i) {
+            h[2 * i] = widen_pair<FMT, 0>(w[x][i]);
+            h[2 * i + 1] = widen_pair<FMT, 1>(w[x][i]);
         }
+        if (kClean) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t keep = finite_halves(h[i], true);
+                odd |= keep != 0xFFFFFFFFu;
+                h[i] &= keep;
+            }
+        }
+        const uint32_t to = dst + (u >> 2) * (kTileKeys * 128) + (row + 32 * n) * 128;
+        sts128(to + (((2 * (u & 3)) ^ sw) << 4), h[0], h[1], h[2], h[3]);
+        sts128(to + (((2 * (u & 3) + 1) ^ sw) << 4), h[4], h[5], h[6], h[7]);
     }
     return odd;
 }
 
-// Instruction descriptor of kind::f16 with fp32 accumulation: A and B both f16 or both bf16.
+// Four values to four e4m3 codes (they are in range and finite).
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | (uint32_t)hi << 16;
+}
+
+// Instruction descriptors with fp32 accumulation: 16-bit operands (both f16 or both bf16), and 8-bit
+// ones (A e4m3, B e4m3 or e5m2).
 __host__ __device__ constexpr uint32_t idesc16(bool f16, uint32_t M, uint32_t N, uint32_t b_mn_major) {
     return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn_major << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t idesc8(uint32_t b_format, uint32_t M, uint32_t N) {
+    return (1u << 4) | (b_format << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
 template <int D, int FMT>
@@ -195,22 +223,20 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     const int row_warps = cdiv(R, 32);
     if (threadIdx.x == 0) {
         mbar_init(&bars[L::bQ], row_warps);
-        mbar_init(&bars[L::bO], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars[L::bS + i], 1);
             mbar_init(&bars[L::bP + i], row_warps);
-            mbar_init(&bars[L::bWK + i], 2);
-            mbar_init(&bars[L::bWKFree + i], 1);
+            mbar_init(&bars[L::bPFree + i], 1);
+            mbar_init(&bars[L::bWV + i], 4);
+            mbar_init(&bars[L::bWVFree + i], 1);
+            mbar_init(&bars[L::bDrain + i], 1);
         }
-        mbar_init(&bars[L::bWV], 2);
-        mbar_init(&bars[L::bWVFree], 1);
-        mbar_init(&bars[L::bDrain], 1);
         mbar_init(&bars[L::bLast], 1);
         for (int i = 0; i < NS; ++i) {
             mbar_init(&bars[L::bK + i], 1);
             mbar_init(&bars[L::bV + i], 1);
-            mbar_init(&bars[L::bKFree + i], F8 ? 2 : 1);  // 8-bit: the two widening warps; else the products
-            mbar_init(&bars[L::bVFree + i], F8 ? 2 : 1);
+            mbar_init(&bars[L::bKFree + i], 1);
+            mbar_init(&bars[L::bVFree + i], F8 ? 4 : 1);  // 8-bit: the widening warps; else the products
             mbar_init(&bars[L::bClean + i], 1);
         }
         *abort_flag = 0;
@@ -295,49 +321,42 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                 mbar_wait(&full[i % NS], (uint32_t)((i / NS) & 1), &dummy, 20000000ull);
         }
     } else if (warp == 1) {
-        // ---------------------------------------------------------------- products
-        // Order: S(0), then S(i), PV(i - 1) for every i, then the last PV. S(i) goes to the buffer of
-        // P(i - 2), which PV(i - 2), issued before it, has read.
-        // One thread issues in a branch of its own: a product costs it 34 to 64 clocks (what it takes to
-        // execute), against 70 clocks when the whole warp issues it under a predicate.
-        constexpr uint32_t idS = idesc16(F8, kTileRows, kTileKeys, 0), idO = idesc16(F8, kTileRows, D, 1);
-        const uint64_t dq = smem_desc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
-        const uint32_t k_base = F8 ? smem_u32(smem + L::kWideOff) : ring;
-        const uint32_t v_base = k_base + (F8 ? 2 : 1) * L::kTile16;
-        const uint64_t dk = smem_desc_sw128(k_base, 16, 1024);
-        const uint64_t dv = smem_desc_sw128(v_base, L::kChunk16, 1024);
+        // ---------------------------------------------------------------- S = Q K^T
+        // S(i) goes to buffer i & 1, over P(i - 2), once the product with that is complete.
+        constexpr uint32_t idS = F8 ? idesc8(FMT == ATTN_FP8_E5M2 ? 1 : 0, kTileRows, kTileKeys) : idesc16(false, kTileRows, kTileKeys, 0);
+        const uint32_t q_base = smem_u32(smem + L::kQOff);
+        const uint64_t dq = F8 && D == 64 ? smem_desc_sw64(q_base) : smem_desc_sw128(q_base, 16, 1024);
+        const uint64_t dk = F8 && D == 64 ? smem_desc_sw64(ring) : smem_desc_sw128(ring, 16, 1024);
         if (lane == 0) {
-            auto wait = [&](int bar, int phase) { return mbar_wait(&bars[bar], (uint32_t)phase & 1u, abort_flag, wd); };
-            auto pv = [&](int j) -> bool {
-                const int st = j % NS, sb = j & 1;
-                if (!wait(L::bP + sb, j >> 1)) return false;
-                if (F8 ? !wait(L::bWV, j) : !wait(L::bV + st, j / NS) || !wait(L::bClean + st, j / NS)) return false;
-                tc_fence_after();
-                const uint64_t vd = dv + (uint64_t)(F8 ? 0 : (st * 2 * L::kLoad) >> 4);
+            auto wait = [&](int bar, uint32_t parity) { return mbar_wait(&bars[bar], parity, abort_flag, wd); };
+            bool any = false;
+            int st = 0;
+            uint32_t par = 0;
+            if (wait(L::bQ, 0)) {
+                for (int i = 0; i < tiles; ++i) {
+                    const int sb = i & 1;
+                    if (!wait(L::bPFree + sb, ((uint32_t)(i >> 1) & 1u) ^ 1u) || !wait(L::bK + st, par)) break;
+                    tc_fence_after();
+                    any = true;
+                    const uint64_t kd = dk + (uint64_t)((st * 2 * L::kLoad) >> 4);
+                    if constexpr (F8) {
 #pragma unroll
-                for (int k = 0; k < kTileKeys / 16; ++k)
-                    tc_mma_ts(tmem + kColO, tmem + kColS + 64 * sb + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idO,
-                              j > 0 || k > 0 ? 1u : 0u);
-                tc_commit(j == tiles - 1 ? &bars[L::bLast] : &bars[L::bO]);
-                tc_commit(F8 ? &bars[L::bWVFree] : &bars[L::bVFree + st]);
-                return true;
-            };
-            bool ok = wait(L::bQ, 0), any = false;
-            for (int i = 0; i < tiles && ok; ++i) {
-                const int st = i % NS;
-                if (!(ok = F8 ? wait(L::bWK + (i & 1), i >> 1) : wait(L::bK + st, i / NS))) break;
-                tc_fence_after();
-                any = true;
-                const uint64_t kd = dk + (uint64_t)((F8 ? (i & 1) * L::kTile16 : st * 2 * L::kLoad) >> 4);
+                        for (int x = 0; x < 2 * (D / 32); ++x) {  // both parts of Q
+                            const int part = x / (D / 32), k = x % (D / 32);
+                            mma8_ss(tmem + kColS + 64 * sb, dq + (uint64_t)((part * kTileRows * D + k * 32) >> 4), kd + (uint64_t)((k * 32) >> 4),
+                                    idS, x > 0);
+                        }
+                    } else {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    tc_mma_ss(tmem + kColS + 64 * (i & 1), dq + (uint64_t)(((k >> 2) * L::kChunkQ + (k & 3) * 32) >> 4),
-                              kd + (uint64_t)(((k >> 2) * L::kChunk16 + (k & 3) * 32) >> 4), idS, k > 0 ? 1u : 0u);
-                tc_commit(&bars[L::bS + (i & 1)]);
-                tc_commit(F8 ? &bars[L::bWKFree + (i & 1)] : &bars[L::bKFree + st]);
-                if (i > 0) ok = pv(i - 1);
+                        for (int k = 0; k < D / 16; ++k)
+                            tc_mma_ss(tmem + kColS + 64 * sb, dq + (uint64_t)(((k >> 2) * L::kChunkQ + (k & 3) * 32) >> 4),
+                                      kd + (uint64_t)(((k >> 2) * L::kChunk16 + (k & 3) * 32) >> 4), idS, k > 0);
+                    }
+                    tc_commit(&bars[L::bS + sb]);
+                    tc_commit(&bars[L::bKFree + st]);
+                    if (++st == NS) st = 0, par ^= 1u;
+                }
             }
-            if (ok) pv(tiles - 1);
             if (any) {
                 // every product has completed before the tensor memory is released
                 tc_commit(&bars[L::bDrain]);
@@ -347,6 +366,38 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
         }
         __syncwarp();
     } else if (warp == 3) {
+        // ---------------------------------------------------------------- O += P V
+        constexpr uint32_t idO = idesc16(F8, kTileRows, D, 1);
+        const uint64_t dv = smem_desc_sw128(F8 ? smem_u32(smem + L::kWideOff) : ring + L::kLoad, L::kChunk16, 1024);
+        if (lane == 0) {
+            auto wait = [&](int bar, uint32_t parity) { return mbar_wait(&bars[bar], parity, abort_flag, wd); };
+            bool any = false;
+            int st = 0;
+            uint32_t par = 0;
+            for (int i = 0; i < tiles; ++i) {
+                const int sb = i & 1;
+                const uint32_t half = (uint32_t)(i >> 1) & 1u;
+                if (F8 ? !wait(L::bWV + sb, half) : !wait(L::bV + st, par) || !wait(L::bClean + st, par)) break;
+                if (!wait(L::bP + sb, half)) break;
+                tc_fence_after();
+                any = true;
+                const uint64_t vd = dv + (uint64_t)((F8 ? sb * L::kTile16 : st * 2 * L::kLoad) >> 4);
+#pragma unroll
+                for (int k = 0; k < kTileKeys / 16; ++k)
+                    tc_mma_ts(tmem + kColO, tmem + kColS + 64 * sb + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idO, i > 0 || k > 0);
+                tc_commit(&bars[L::bPFree + sb]);
+                tc_commit(F8 ? &bars[L::bWVFree + sb] : &bars[L::bVFree + st]);
+                if (i == tiles - 1) tc_commit(&bars[L::bLast]);
+                if (++st == NS) st = 0, par ^= 1u;
+            }
+            if (any) {
+                tc_commit(&bars[L::bDrain + 1]);
+                int dummy = 0;
+                mbar_wait(&bars[L::bDrain + 1], 0, &dummy, 50000000ull);
+            }
+        }
+        __syncwarp();
+    } else if (!F8 && warp == 8) {
         // ---------------------------------------------------------------- 16-bit V tiles
         if constexpr (!F8) {
             for (int i = 0; i < tiles; ++i) {
@@ -370,6 +421,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                         odd |= bad;
                     }
                     if (odd) *odd_v = 1;
+                    __threadfence_block();
                     fence_smem_to_async();
                 }
                 __syncwarp();
@@ -377,28 +429,26 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
             }
         }
     } else if (warp >= 8) {
-        // ---------------------------------------------------------------- 8-bit tiles to f16
+        // ---------------------------------------------------------------- 8-bit V tiles to f16
         if constexpr (F8) {
-            const bool v = warp >= 10;
-            const int t = threadIdx.x & 63;
-            const uint32_t wide = smem_u32(smem + L::kWideOff) + (v ? 2 * L::kTile16 : 0);
-            uint64_t* full = &bars[v ? L::bV : L::bK];
-            uint64_t* free = &bars[v ? L::bVFree : L::bKFree];
+            const int t = threadIdx.x & 127;
+            const uint32_t wide = smem_u32(smem + L::kWideOff);
             for (int i = 0; i < tiles; ++i) {
-                const int st = i % NS, wb = v ? 0 : i & 1;  // two f16 K tiles, one V tile
-                if (!wait_all(&full[st], (uint32_t)((i / NS) & 1), abort_flag, wd)) break;
-                if (!wait_all(&bars[v ? L::bWVFree : L::bWKFree + wb], (uint32_t)((v ? i : i >> 1) & 1) ^ 1u, abort_flag, wd)) break;
-                const uint32_t src = ring + st * 2 * L::kLoad + (v ? L::kLoad : 0), dst = wide + wb * L::kTile16;
-                if (v && i >= first_mixed) {
+                const int st = i % NS, wb = i & 1;
+                if (!wait_all(&bars[L::bV + st], (uint32_t)((i / NS) & 1), abort_flag, wd)) break;
+                if (!wait_all(&bars[L::bWVFree + wb], (uint32_t)((i >> 1) & 1) ^ 1u, abort_flag, wd)) break;
+                const uint32_t src = ring + st * 2 * L::kLoad + L::kLoad, dst = wide + wb * L::kTile16;
+                if (i >= first_mixed) {
                     if (widen_tile<D, FMT, true>(src, dst, t)) *odd_v = 1;
+                    __threadfence_block();
                 } else {
                     widen_tile<D, FMT, false>(src, dst, t);
                 }
                 fence_smem_to_async();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&bars[v ? L::bWV : L::bWK + wb]);
-                    mbar_arrive(&free[st]);
+                    mbar_arrive(&bars[L::bWV + wb]);
+                    mbar_arrive(&bars[L::bVFree + st]);
                 }
             }
         }
@@ -412,29 +462,75 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
         const long long orow = valid ? out_row(row) : 0;
         const int node = valid ? (r0 + row) / p.G : s.n - 1;  // rows of padding see what the last node sees
         const unsigned long long* mrow = p.mask ? p.mask + (long long)(s.q0 + node) * p.mask_words : nullptr;
+        float row_scale = 1.0f;  // 8-bit caches: what the row's Q was divided by
         {
-            // this thread's row of Q into the K-major 128-byte swizzle
-            const uint32_t q = smem_u32(smem + L::kQOff) + row * 128;
+            // this thread's row of Q into shared memory, K-major with the swizzle of its row length
+            const uint32_t q = smem_u32(smem + L::kQOff);
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * D);
+            auto load = [&](int c, float (&f)[8]) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (valid) x = __ldg(src + c);
+                const uint32_t in[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                uint32_t w[4] = {0, 0, 0, 0};
-                if (valid) {
-                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.q + orow * D) + c);
-                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                for (int e = 0; e < 4; ++e) {
+                    f[2 * e] = __uint_as_float(in[e] << 16) * p.q_sign;
+                    f[2 * e + 1] = __uint_as_float(in[e] & 0xFFFF0000u) * p.q_sign;
+                }
+            };
+            if constexpr (!F8) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float lo = __uint_as_float(in[e] << 16) * p.q_sign;
-                        const float hi = __uint_as_float(in[e] & 0xFFFF0000u) * p.q_sign;
-                        w[e] = F8 ? pack_half2(lo, hi) : pack_bf16x2(lo, hi);
+                for (int c = 0; c < D / 8; ++c) {
+                    float f[8];
+                    load(c, f);
+                    sts128(q + (c >> 3) * L::kChunkQ + row * 128 + (((c & 7) ^ (row & 7)) << 4), pack_bf16x2(f[0], f[1]),
+                           pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+                }
+            } else {
+                // 2^up brings the largest magnitude of the row into [128, 256); a row with a non-finite
+                // element becomes NaN
+                float top = 0.0f;
+                bool finite = true;
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    float f[8];
+                    load(c, f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        finite = finite && isfinite(f[e]);
+                        top = fmaxf(top, fabsf(f[e]));
                     }
                 }
-                sts128(q + (c >> 3) * L::kChunkQ + (((c & 7) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+                const int up = finite && top > 0.0f ? min(120, 7 - ilogbf(top)) : 0;
+                const float mul = finite ? exp2f((float)up) : __int_as_float(0x7fffffff);
+                row_scale = exp2f((float)-up);
+#pragma unroll 2
+                for (int u = 0; u < D / 16; ++u) {  // 16 codes of each part
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float f[8];
+                        load(2 * u + c, f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] *= mul;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t w = e4m3x4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                            hi[2 * c + e] = w;
+                            const uint32_t a = fp8x2_f16x2<ATTN_FP8_E4M3>(w), b = fp8x2_f16x2<ATTN_FP8_E4M3>(w >> 16);
+                            lo[2 * c + e] = e4m3x4(f[4 * e] - half_value((uint16_t)a), f[4 * e + 1] - half_value((uint16_t)(a >> 16)),
+                                                   f[4 * e + 2] - half_value((uint16_t)b), f[4 * e + 3] - half_value((uint16_t)(b >> 16)));
+                        }
+                    }
+                    const uint32_t at = q + row * D + ((D == 128 ? u ^ (row & 7) : u ^ ((row >> 1) & 3)) << 4);
+                    sts128(at, hi[0], hi[1], hi[2], hi[3]);
+                    sts128(at + kTileRows * D, lo[0], lo[1], lo[2], lo[3]);
+                }
             }
             fence_smem_to_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[L::bQ]);
         }
-        const float sl2 = p.scale_log2;
+        const float scale = F8 ? p.scale * row_scale : p.scale, sl2 = F8 ? p.scale_log2 * row_scale : p.scale_log2;
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int i = 0; i < tiles; ++i) {
@@ -478,7 +574,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                 const float alpha = m == -INFINITY ? 0.0f : ex2_mufu((m - mc) * sl2);
                 if (i > 0) {
                     // O += P(i - 1) V is complete before O is rescaled (S(i) was issued before it)
-                    if (!(ok = wait_all(&bars[L::bO], (uint32_t)(i - 1) & 1u, abort_flag, wd))) break;
+                    if (!(ok = wait_all(&bars[L::bPFree + (sb ^ 1)], (uint32_t)((i - 1) >> 1) & 1u, abort_flag, wd))) break;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
@@ -519,7 +615,6 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[L::bP + sb]);
         }
-        // the last product has a barrier of its own: bO may be one phase ahead by now or not
         if (ok) ok = wait_all(&bars[L::bLast], 0, abort_flag, wd);
         if (ok) {
             tc_fence_after();
@@ -562,7 +657,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                 }
             }
             if (valid) {
-                const float lse = empty ? -INFINITY : m * p.scale + logf(l);
+                const float lse = empty ? -INFINITY : m * scale + logf(l);
                 if (nsplit == 1)
                     p.lse[orow] = lse;
                 else
