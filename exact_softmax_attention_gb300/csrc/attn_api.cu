@@ -121,8 +121,8 @@ attn_status_t make_cache_map(CUtensorMap* m, const void* base, long long rows, i
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// 2-D map over a paged cache viewed as [rows, row_elems]: boxes of box_rows rows (1: for gather copies of
-// four rows), 128 bytes wide with the 128-byte swizzle, or d = 64 8-bit codes with the 64-byte one.
+// 2-D map over a paged cache viewed as [rows, row_elems]: boxes of box_rows rows, 128 bytes wide with the
+// 128-byte swizzle, or d = 64 8-bit codes with the 64-byte one.
 attn_status_t make_tree_map(CUtensorMap* m, const void* base, long long rows, long long row_elems, int d, int elem,
                             int box_rows) {
     cuuint64_t dims[2] = {(cuuint64_t)row_elems, (cuuint64_t)rows};
@@ -625,9 +625,10 @@ attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const v
     if (attn::tree_takes_tiles(rows)) {
         const long long cache_rows = (long long)num_pages * page_size;
         p.box_rows = page_size % 64 == 0 ? 64 : (page_size % 16 == 0 ? 16 : 1);
-        if ((st = encode_fn()) != ATTN_OK ||
-            (st = make_tree_map(&tm.k, k_cache, cache_rows, (long long)Hkv * d, d, f8 ? 1 : 2, p.box_rows)) != ATTN_OK ||
-            (st = make_tree_map(&tm.v, v_cache, cache_rows, (long long)Hkv * d, d, f8 ? 1 : 2, p.box_rows)) != ATTN_OK)
+        if (p.box_rows > 1 &&
+            ((st = encode_fn()) != ATTN_OK ||
+             (st = make_tree_map(&tm.k, k_cache, cache_rows, (long long)Hkv * d, d, f8 ? 1 : 2, p.box_rows)) != ATTN_OK ||
+             (st = make_tree_map(&tm.v, v_cache, cache_rows, (long long)Hkv * d, d, f8 ? 1 : 2, p.box_rows)) != ATTN_OK))
             return st;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

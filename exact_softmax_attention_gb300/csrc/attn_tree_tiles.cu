@@ -6,11 +6,11 @@
 // memory, P as the 16-bit A operand from tensor memory over S. Two blocks share an SM (96 KB of
 // shared memory and 256 tensor-memory columns each), so that one block's start, softmax latency and
 // end are covered by the other's loads. Roles of the warps:
-//   warps 0, 2  loads of K and of V, through tensor maps of the caches viewed as [rows, Hkv d]: boxes of
-//               64 or 16 rows where the page size is a multiple of that, else gather copies of four
-//               rows whose indices come from the page table. Rows past the end or of a bad page lie
-//               outside the map and arrive as zeros. (A copy instruction costs its warp about 66
-//               clocks: 64 gathers of a 32 KB tile took one warp 4600 clocks.)
+//   warps 0, 2  loads of K and of V: boxes of 64 or 16 rows through tensor maps of the caches viewed as
+//               [rows, Hkv d] where the page size is a multiple of that (rows past the end or of a bad
+//               page lie outside the map and arrive as zeros), else 16-byte copies of rows that the
+//               page table gives. (A tensor copy costs its warp about 66 clocks, so gather copies of
+//               four rows, 64 for a 32 KB tile, took 4600.)
 //   warp 1      issues the products and owns the tensor memory
 //   warp 3      16-bit caches: passes the V tiles on, taking non-finite values out of those that a row
 //               may not see in full
@@ -59,15 +59,6 @@ struct TileLayout {
 constexpr uint32_t kColS = 0, kColO = 128, kCols = 256;  // S buffers at 0 and 64
 
 __device__ __forceinline__ void fence_smem_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// Rows r[0..3] (columns c .. c + box) of a 2-D map into shared memory, completing on an mbarrier.
-__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c, const int (&r)[4]) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
-        "%6, %7}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-        : "memory");
-}
 
 // A box of rows (columns c .. c + box) from row r on.
 __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c, int r) {
@@ -262,63 +253,108 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     if (warp == 0 || warp == 2) {
         // ---------------------------------------------------------------- loads of K (warp 0), V (warp 2)
         const bool v = warp == 2;
-        const CUtensorMap* map = v ? &tmV : &tmK;
         uint64_t* full = &bars[v ? L::bV : L::bK];
         uint64_t* free = &bars[v ? L::bVFree : L::bKFree];
-        const int none = p.num_pages * p.page_size;  // the first row past the cache: zeros
-        // lane: its rows of the tile (four of them, or a box) and, for rows of two 128-byte chunks, which
-        constexpr int kParts = !F8 && D == 128 ? 2 : 1;
-        const int step = p.box_rows > 1 ? p.box_rows : 4;
-        const int per_part = kTileKeys / step;
-        const bool active = lane < kParts * per_part;
-        const int part = lane / per_part, first = (lane - part * per_part) * step;
-        const int col = kvh * D + part * 64;
-        const uint32_t dst = ring + (v ? L::kLoad : 0) + part * L::kChunk16 + first * (F8 ? D : 128);
-        // The pages of the next tile are looked up before the copies of this one are issued, all loads
-        // before the first is used. n: rows (gather) or boxes of this lane with a token.
-        const int width = p.box_rows > 1 ? 1 : 4;
-        int page[4], slot[4], n = 0;
-        auto look_up = [&](int i) {
-            const int tok = t_begin + i * kTileKeys + first;
-            n = active ? min(width, max(0, t_end - tok)) : 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < n) page[e] = __ldg(pt + page_of(p, tok + e, slot[e]));
-        };
-        look_up(0);
+        const uint32_t tile = ring + (v ? L::kLoad : 0);
         bool ok = true;
-        int issued = 0;
-        for (int i = 0; i < tiles; ++i) {
-            const int st = i % NS;
-            int r[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                r[e] = none;
-                if (e < n) {
-                    if (page[e] >= 0 && page[e] < p.num_pages)
-                        r[e] = page[e] * p.page_size + slot[e];  // < num_pages * page_size <= INT32_MAX
+        if (p.box_rows > 1) {
+            // boxes: lane -> 16 or 64 rows of one page, and which 128-byte chunk of them
+            const CUtensorMap* map = v ? &tmV : &tmK;
+            constexpr int kParts = !F8 && D == 128 ? 2 : 1;
+            const int per_part = kTileKeys / p.box_rows;
+            const bool active = lane < kParts * per_part;
+            const int part = lane / per_part, first = (lane - part * per_part) * p.box_rows;
+            const int col = kvh * D + part * 64;
+            const uint32_t dst = tile + part * L::kChunk16 + first * (F8 ? D : 128);
+            const int none = p.num_pages * p.page_size;  // the first row past the cache: zeros
+            // the page of the next tile's box is looked up before the copies of this one are issued
+            int page = 0, slot = 0;
+            bool some = false;
+            auto look_up = [&](int i) {
+                const int tok = t_begin + i * kTileKeys + first;
+                some = active && tok < t_end;
+                if (some) page = __ldg(pt + page_of(p, tok, slot));
+            };
+            look_up(0);
+            int issued = 0;
+            for (int i = 0; i < tiles; ++i) {
+                const int st = i % NS;
+                int row = none;
+                if (some) {
+                    if (page >= 0 && page < p.num_pages)
+                        row = page * p.page_size + slot;  // < num_pages * page_size <= INT32_MAX
                     else
                         atomicCAS(p.status, 0, kDevBadIndex);
                 }
+                if (i + 1 < tiles) look_up(i + 1);
+                if (!(ok = wait_all(&free[st], (uint32_t)((i / NS) & 1) ^ 1u, abort_flag, wd))) break;
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], L::kLoad);
+                __syncwarp();
+                if (active) copy_box(dst + st * 2 * L::kLoad, map, &full[st], col, row);
+                __syncwarp();
+                issued = i + 1;
             }
-            if (i + 1 < tiles) look_up(i + 1);
-            if (!(ok = wait_all(&free[st], (uint32_t)((i / NS) & 1) ^ 1u, abort_flag, wd))) break;
-            if (lane == 0) mbar_arrive_expect_tx(&full[st], L::kLoad);
-            __syncwarp();
-            if (active) {
-                if (p.box_rows > 1)
-                    copy_box(dst + st * 2 * L::kLoad, map, &full[st], col, r[0]);
-                else
-                    gather4(dst + st * 2 * L::kLoad, map, &full[st], col, r);
+            if (!ok) {
+                // let the copies in flight land before the block can end
+                int dummy = 0;
+                for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
+                    mbar_wait(&full[i % NS], (uint32_t)((i / NS) & 1), &dummy, 20000000ull);
             }
-            __syncwarp();
-            issued = i + 1;
-        }
-        if (!ok) {
-            // let the copies in flight land before the block can end
-            int dummy = 0;
-            for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
-                mbar_wait(&full[i % NS], (uint32_t)((i / NS) & 1), &dummy, 20000000ull);
+        } else {
+            // other page sizes: each lane finds the cache rows of tokens lane and lane + 32, and copies 16-byte
+            // pieces of all rows; a tile is handed over once the copies of the next one are on their way
+            constexpr int kRowBytes = F8 ? D : 2 * D, kPieces = kRowBytes / 16, kRows = 32 / kPieces;
+            const uint8_t* cache = static_cast<const uint8_t*>(v ? p.v_cache : p.k_cache);
+            const int piece = lane % kPieces, sub = lane / kPieces;
+            const long long row_bytes = (long long)p.Hkv * kRowBytes;
+            const int col = kvh * kRowBytes + piece * 16;
+            int page[2], slot[2], n = 0;
+            auto look_up = [&](int i) {
+                const int tok = t_begin + i * kTileKeys + lane;
+                n = tok >= t_end ? 0 : (tok + 32 >= t_end ? 1 : 2);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (e < n) page[e] = __ldg(pt + page_of(p, tok + 32 * e, slot[e]));
+            };
+            auto hand_over = [&](int i) {
+                fence_smem_to_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[i % NS]);
+            };
+            look_up(0);
+            for (int i = 0; i < tiles; ++i) {
+                const int st = i % NS;
+                int row[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    row[e] = -1;  // no token, or a bad page: zeros
+                    if (e < n) {
+                        if (page[e] >= 0 && page[e] < p.num_pages)
+                            row[e] = page[e] * p.page_size + slot[e];
+                        else
+                            atomicCAS(p.status, 0, kDevBadIndex);
+                    }
+                }
+                if (i + 1 < tiles) look_up(i + 1);
+                if (!(ok = wait_all(&free[st], (uint32_t)((i / NS) & 1) ^ 1u, abort_flag, wd))) break;
+#pragma unroll
+                for (int it = 0; it < kTileKeys / kRows; ++it) {
+                    const int r = it * kRows + sub;
+                    const int rr = __shfl_sync(0xffffffffu, row[it * kRows / 32], r & 31);
+                    const uint32_t at = tile + st * 2 * L::kLoad +
+                                        (kPieces == 16  ? (piece >> 3) * L::kChunk16 + r * 128 + (((piece & 7) ^ (r & 7)) << 4)
+                                         : kPieces == 8 ? r * 128 + ((piece ^ (r & 7)) << 4)
+                                                        : r * 64 + ((piece ^ ((r >> 1) & 3)) << 4));
+                    cp_async16(at, cache + (rr >= 0 ? rr * row_bytes + col : 0), rr >= 0 ? 16u : 0u);
+                }
+                cp_async_commit();
+                if (i > 0) {
+                    cp_async_wait<1>();
+                    hand_over(i - 1);
+                }
+            }
+            cp_async_wait<0>();
+            if (ok) hand_over(tiles - 1);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- S = Q K^T

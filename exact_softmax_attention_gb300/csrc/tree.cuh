@@ -27,13 +27,13 @@ struct TreeParams {
     float v_descale, rescale_thr;
     unsigned int ps_magic;   // tok / page_size by multiplication, as in DecodeParams
     int ps_shift;
-    int box_rows;            // rows of a box of the maps (64 or 16, dividing the page size), 1: gather copies
+    int box_rows;            // rows of a box of the maps (64 or 16, dividing the page size), 1: no maps
     int* status;
     unsigned long long watchdog_ns;
 };
 
 // 2-D maps over the caches viewed as [num_pages * page_size, Hkv * d], box box_rows rows of 128 bytes
-// (64 for 8-bit d = 64); with one row, for gather copies of four rows.
+// (64 for 8-bit d = 64).
 struct TreeTmaps {
     CUtensorMap k, v;
 };
@@ -42,7 +42,7 @@ struct TreeTmaps {
 constexpr int kTreeTileRows = 17;
 
 // kv_format: ATTN_KV_BF16, ATTN_FP8_E4M3, ATTN_FP8_E5M2; d 64 or 128.
-// tm: the maps when tree_takes_tiles(rows of a kv head), else unused.
+// tm: the maps when tree_takes_tiles(rows of a kv head) and box_rows > 1, else unused.
 cudaError_t launch_attn_tree(const TreeParams& p, const TreeTmaps& tm, int d, int kv_format, cudaStream_t stream);
 cudaError_t launch_tree_tiles(const TreeParams& p, const TreeTmaps& tm, int d, int kv_format, cudaStream_t stream);
 inline bool tree_takes_tiles(long long rows) { return rows >= kTreeTileRows; }
