@@ -475,18 +475,36 @@ void tree_plan(int B, int Hkv, int rows, long long lmax, int num_splits, int num
     if (num_splits > 0) {
         c = (lmax + num_splits - 1) / num_splits;
     } else if (tree_takes_tiles(rows)) {
-        // One item per resident block (two per SM) when the sequences are few, so that one wave covers
-        // them; at most 8192 tokens per item, so that sequences of different lengths balance.
-        const long long pairs = (long long)B * Hkv * ((rows + 127) / 128);
-        const long long splits = 2LL * num_sms / pairs;
-        c = splits > 1 ? (lmax + splits - 1) / splits : lmax;
+        // Blocks of 128 rows, two per SM. Fewer (sequence, kv head, row tile) groups than SMs: as many splits
+        // as fit at once (a few blocks more would cost a second wave), at least four of 1024 tokens or more,
+        // which balance sequences of different lengths. Else none but for the cap of 8192 tokens, because the
+        // partial results of 128 rows cost as much traffic as 130 cached tokens of one head and the join is a
+        // second launch. Measured, 8 drafted tokens x 4 query heads, bf16, splits -> us: 32 sequences of 4096
+        // (256 groups) 1: 88, 2: 98, 4: 109; 64 of U[1K, 32K] (512 groups) 2: 692, 4: 667, 8: 680; 4 of 32768
+        // (32 groups) 8: 96, 9: 97, 10: 125; 8 of U[128, 8192] (64 groups) 2: 56, 4: 42, 6: 37, 8: 39; one of
+        // 32768 (8 groups) 8: 55, 16: 39, 38: 42, 64: 54; 48 chains of U[1, 8000], e5m2, 3 kv heads (144
+        // groups) 2: 55, 4: 45, 8: 49.
+        const long long groups = (long long)B * Hkv * ((rows + 127) / 128);
+        long long splits = 1;
+        if (groups < num_sms) {
+            const long long balance = lmax / 1024 < 4 ? lmax / 1024 : 4;
+            splits = 2LL * num_sms / groups;
+            if (splits < balance) splits = balance;
+        }
+        c = (lmax + splits - 1) / splits;
         if (c < 128) c = 128;
         if (c > 8192) c = 8192;
     } else {
-        const long long work = (long long)B * Hkv * ((lmax + 1) / 2);
-        const long long least = 128LL * (rows > 2 ? rows : 2);
-        c = (work + 18LL * num_sms - 1) / (18LL * num_sms);
-        if (c < least) c = least;
+        // Blocks of 16 rows, up to four per SM. Many tokens: about 12 items per SM, assuming half-full page
+        // tables; fewer: two items per SM, up to 2048 tokens each. Measured, 4 drafted tokens x 4 query heads,
+        // bf16, splits -> us: 64 sequences of U[1K, 32K] 8: 657, 11: 671, 16: 695; 8 of U[128, 8192] 2: 63,
+        // 4: 44, 8: 43, 16: 51; one of 32768 8: 62, 16: 42, 32: 43, 64: 60; one of 1024 1: 23, 2: 18, 8: 15.
+        const long long tokens = (long long)B * Hkv * lmax;
+        c = (tokens + 4LL * num_sms - 1) / (4LL * num_sms) * 2;  // two items per SM
+        if (c > 2048) c = 2048;
+        const long long many = (tokens / 2 + 12LL * num_sms - 1) / (12LL * num_sms);
+        if (c < many) c = many;
+        if (c < 128) c = 128;
         if (c > 8192) c = 8192;
     }
     c = (c + 63) / 64 * 64;
