@@ -20,9 +20,9 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxDim = 1024;
 
 struct RopeParams {
-    const void* in[2];   // q, k
-    void* out[2];
-    long long in_stride[2], out_stride[2];  // elements between rows
+    const void *q, *k;
+    void *q_out, *k_out;
+    long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements between rows
     const int* positions;
     const double* inv_freq;
     RopeCols cols;
@@ -37,27 +37,40 @@ template <typename E, int V>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
     extern __shared__ __align__(16) float angles[];
     const int half = p.cols.rot / 2;
-    const int t0 = blockIdx.x * p.tokens;
-    const int tokens = min(p.tokens, p.T - t0);
+    const long long t0 = (long long)blockIdx.x * p.tokens;
+    const int tokens = (int)min((long long)p.tokens, p.T - t0);
     float* cs = angles;
     float* sn = angles + p.tokens * half;
+    // An item is loaded while the one before is rotated and stored; the first before the angles are
+    // computed, which it does not need.
+    typedef typename RawOf<E, V>::type Raw;
+    ItemWalk at(p.H, p.items);
+    Raw ra, rb;
+    auto load = [&]() {
+        const bool k = at.h >= p.Hq;
+        const E* src = static_cast<const E*>(k ? p.k : p.q) + (t0 + at.t) * (k ? p.k_stride : p.q_stride) +
+                       (long long)(k ? at.h - p.Hq : at.h) * p.cols.d;
+        int a, b;
+        item_cols<V>(p.cols, at.j, a, b);
+        ra = load_raw<E, V>(src + a);
+        rb = load_raw<E, V>(src + b);
+    };
+    if (at.t < tokens) load();
     block_angles(p.inv_freq, p.positions + t0, tokens, half, p.amplitude, p.transpose != 0, cs, sn);
     __syncthreads();
-    const int per_token = p.H * p.items;
-    const int n = tokens * per_token;
-    for (int w = threadIdx.x; w < n; w += kRopeThreads) {
-        const int t = w / per_token, r = w - t * per_token;
-        const int h = r / p.items, j = r - h * p.items;
-        const int kv = h >= p.Hq;
-        const int head = kv ? h - p.Hq : h;
-        const E* src = static_cast<const E*>(p.in[kv]) + (long long)(t0 + t) * p.in_stride[kv] + (long long)head * p.cols.d;
-        E* dst = static_cast<E*>(p.out[kv]) + (long long)(t0 + t) * p.out_stride[kv] + (long long)head * p.cols.d;
-        int a, b;
-        const bool turned = item_cols<V>(p.cols, j, a, b);
+    while (at.t < tokens) {
+        const int t = at.t, j = at.j;
+        const bool k = at.h >= p.Hq;
+        E* dst = static_cast<E*>(k ? p.k_out : p.q_out) + (t0 + t) * (k ? p.k_out_stride : p.q_out_stride) +
+                 (long long)(k ? at.h - p.Hq : at.h) * p.cols.d;
         float xa[V], xb[V];
-        load_row<V>(src + a, xa);
-        load_row<V>(src + b, xb);
-        if (turned) rotate_item<V>(xa, xb, cs + t * half + V * j, sn + t * half + V * j, p.cols.interleaved != 0);
+        unpack<E, V>(ra, xa);
+        unpack<E, V>(rb, xb);
+        at.next();
+        if (at.t < tokens) load();
+        int a, b;
+        if (item_cols<V>(p.cols, j, a, b))
+            rotate_item<V>(xa, xb, p.cols, j, cs + t * half, sn + t * half);
         store_row<V>(dst + a, xa);
         store_row<V>(dst + b, xb);
     }
@@ -65,10 +78,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
 
 template <typename E, int V>
 cudaError_t launch_rope(RopeParams p, bool in_place, int num_sms, cudaStream_t stream) {
-    // One token per block until the blocks fill the GPU several times, then more, so that the
-    // angles of a block keep all its threads busy.
-    p.tokens = p.T >= 16 * num_sms ? 4 : 1;
     p.items = (in_place ? p.cols.rot : p.cols.d) / (2 * V);
+    // (the angles of a block's tokens take at most 32 KB)
+    p.tokens = block_tokens(p.T, (long long)p.H * p.items, kRopeThreads, 8192 / p.cols.rot, num_sms);
     const int blocks = (p.T + p.tokens - 1) / p.tokens;
     const size_t smem = (size_t)p.tokens * p.cols.rot * sizeof(float);
     rope_kernel<E, V><<<blocks, kRopeThreads, smem, stream>>>(p);
@@ -106,10 +118,10 @@ extern "C" attn_status_t attn_rope(const void* q, const void* k, void* q_out, vo
     const attn_status_t st = current_device_info(&status, &num_sms);
     if (st != ATTN_OK) return st;
     RopeParams p;
-    p.in[0] = q, p.in[1] = k;
-    p.out[0] = q_out, p.out[1] = k_out;
-    p.in_stride[0] = q_stride, p.in_stride[1] = k_stride;
-    p.out_stride[0] = q_out_stride, p.out_stride[1] = k_out_stride;
+    p.q = q, p.k = k;
+    p.q_out = q_out, p.k_out = k_out;
+    p.q_stride = q_stride, p.k_stride = k_stride;
+    p.q_out_stride = q_out_stride, p.k_out_stride = k_out_stride;
     p.positions = positions;
     p.inv_freq = inv_freq;
     p.cols = RopeCols{d, rot_begin, rot_dim, interleaved};

@@ -16,50 +16,50 @@ struct RopeCols {
     int d, begin, rot, interleaved;
 };
 
-// Work item j of a head (j < d / (2 V)) holds the 2 V columns [a, a + V) and [b, b + V), the rotated
-// ones first: pairs V j .. V j + V - 1 (then true is returned), after them the columns that pass
-// through. V > 1 needs begin and rot to be multiples of 2 V.
+// Work item j of a head (j < d / (2 V)) holds the 2 V columns [a, a + V) and [b, b + V): first the rotated
+// ones (then true is returned), a in the lower and b in the upper half of the rotated part, then in the
+// same way those that pass through, so that neighbouring items are neighbours in memory. (Single
+// interleaved pairs, V = 1, are columns 2 j and 2 j + 1.) V > 1 needs begin and rot to be multiples of 2 V.
 template <int V>
 __device__ __forceinline__ bool item_cols(const RopeCols& c, int j, int& a, int& b) {
-    const int e = 2 * V * j;
-    if (e < c.rot) {
-        a = c.begin + (c.interleaved ? e : V * j);
-        b = c.interleaved ? a + V : a + c.rot / 2;
+    const int x = V * j, turned = c.rot / 2;
+    if (x < turned) {
+        a = c.begin + (V == 1 && c.interleaved ? 2 * j : x);
+        b = a + (V == 1 && c.interleaved ? 1 : turned);
         return true;
     }
-    const int x = e - c.rot, y = x + V;
-    a = x < c.begin ? x : x + c.rot;
-    b = y < c.begin ? y : y + c.rot;
+    a = x - turned;
+    b = a + (c.d - c.rot) / 2;
+    if (a >= c.begin) a += c.rot;
+    if (b >= c.begin) b += c.rot;
     return false;
 }
 
-// Rotate the V pairs of an item by the angles whose cosines and sines are c and s.
+// Rotate the pairs of item j; cs and sn: cosines and sines of the token, one per pair.
 template <int V>
-__device__ __forceinline__ void rotate_item(float (&xa)[V], float (&xb)[V], const float* c, const float* s,
-                                            bool interleaved) {
-    if (!interleaved) {
+__device__ __forceinline__ void rotate_item(float (&xa)[V], float (&xb)[V], const RopeCols& cols, int j, const float* cs,
+                                            const float* sn) {
+    if (V == 1 || !cols.interleaved) {
+        const float *c = cs + V * j, *s = sn + V * j;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const float u = xa[e], w = xb[e];
             xa[e] = u * c[e] - w * s[e];
             xb[e] = u * s[e] + w * c[e];
         }
-    } else if constexpr (V == 1) {
-        const float u = xa[0], w = xb[0];
-        xa[0] = u * c[0] - w * s[0];
-        xb[0] = u * s[0] + w * c[0];
-    } else {  // pairs (2 e, 2 e + 1) of the 2 V adjacent columns
+    } else {  // pairs of adjacent columns: V / 2 in each part
+        const int first = V / 2 * j, second = first + cols.rot / 4;
 #pragma unroll
-        for (int e = 0; e < V; e += 2) {
-            const float u = xa[e], w = xa[e + 1];
-            xa[e] = u * c[e / 2] - w * s[e / 2];
-            xa[e + 1] = u * s[e / 2] + w * c[e / 2];
+        for (int e = 0; e + 1 < V; e += 2) {
+            const float u = xa[e], w = xa[e + 1], c = cs[first + e / 2], s = sn[first + e / 2];
+            xa[e] = u * c - w * s;
+            xa[e + 1] = u * s + w * c;
         }
 #pragma unroll
-        for (int e = 0; e < V; e += 2) {
-            const float u = xb[e], w = xb[e + 1];
-            xb[e] = u * c[(V + e) / 2] - w * s[(V + e) / 2];
-            xb[e + 1] = u * s[(V + e) / 2] + w * c[(V + e) / 2];
+        for (int e = 0; e + 1 < V; e += 2) {
+            const float u = xb[e], w = xb[e + 1], c = cs[second + e / 2], s = sn[second + e / 2];
+            xb[e] = u * c - w * s;
+            xb[e + 1] = u * s + w * c;
         }
     }
 }
@@ -98,32 +98,36 @@ __device__ __forceinline__ void block_angles(const double* inv_freq, const int* 
     }
 }
 
-// ---- V consecutive elements of a row as floats, by one load or store of 16 bytes (V > 1)
+// ---- V consecutive elements of a row: as loaded (16 bytes at once when V > 1), and as floats
 
-template <int V>
-__device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&x)[V]) {
+template <typename E, int V>
+struct RawOf {
+    static_assert(V * sizeof(E) == 16, "16 bytes");
+    typedef uint4 type;
+};
+template <typename E>
+struct RawOf<E, 1> {
+    typedef E type;
+};
+
+template <typename E, int V>
+__device__ __forceinline__ typename RawOf<E, V>::type load_raw(const E* p) {
+    return *reinterpret_cast<const typename RawOf<E, V>::type*>(p);
+}
+
+template <typename E, int V>
+__device__ __forceinline__ void unpack(const typename RawOf<E, V>::type& w, float (&x)[V]) {
     if constexpr (V == 8) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p);
         const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             x[2 * i] = __uint_as_float(r[i] << 16);
             x[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
         }
+    } else if constexpr (V == 4) {
+        x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
     } else {
-        static_assert(V == 1, "bf16: 8 or 1");
-        x[0] = __bfloat162float(*p);
-    }
-}
-
-template <int V>
-__device__ __forceinline__ void load_row(const float* p, float (&x)[V]) {
-    if constexpr (V == 4) {
-        const float4 w = *reinterpret_cast<const float4*>(p);
-        x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
-    } else {
-        static_assert(V == 1, "fp32: 4 or 1");
-        x[0] = *p;
+        x[0] = (float)w;
     }
 }
 
@@ -141,6 +145,42 @@ __device__ __forceinline__ void store_row(float* p, const float (&x)[V]) {
         *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
     else
         *p = x[0];
+}
+
+// ---- the items of a block of tokens, this thread's ones blockDim apart
+//
+// Item (t, h, j): token t of the block, head h of `heads`, item j of `items` per head, in that order. The
+// three indices advance without divisions.
+struct ItemWalk {
+    int t, h, j, dt, dh, dj, heads, items;
+    __device__ __forceinline__ ItemWalk(int heads_, int items_) : heads(heads_), items(items_) {
+        const int n = blockDim.x;
+        j = threadIdx.x % items;
+        h = threadIdx.x / items;
+        t = h / heads;
+        h -= t * heads;
+        dj = n % items;
+        dh = n / items;
+        dt = dh / heads;
+        dh -= dt * heads;
+    }
+    __device__ __forceinline__ void next() {
+        j += dj;
+        h += dh;
+        t += dt;
+        if (j >= items) j -= items, ++h;
+        if (h >= heads) h -= heads, ++t;
+    }
+};
+
+// Tokens per block, at most `most`: enough for eight items per thread, as long as every SM still gets
+// eight blocks.
+inline int block_tokens(int T, long long items_per_token, int threads, int most, int num_sms) {
+    long long n = (8LL * threads + items_per_token - 1) / items_per_token;
+    const long long spread = T / (8LL * num_sms);
+    if (n > spread) n = spread;
+    if (n > most) n = most;
+    return n < 1 ? 1 : (int)n;
 }
 
 // ---- packed rows of a paged cache
