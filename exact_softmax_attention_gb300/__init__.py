@@ -123,7 +123,8 @@ def _stream(s):
     if s is None:
         torch = sys.modules.get("torch")  # not imported: the caller does not use its streams
         if torch is not None and torch.cuda.is_initialized():
-            return torch.cuda.current_stream().cuda_stream
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without making a Stream object
+            return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
         return None
     if isinstance(s, int):
         return s

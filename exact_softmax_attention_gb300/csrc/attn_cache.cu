@@ -15,7 +15,7 @@
 namespace attn {
 namespace {
 
-constexpr int kCacheThreads = 256;
+constexpr int kCacheThreads = 512;  // at most
 constexpr int kCacheMaxTokens = 32;  // tokens per block
 
 struct CacheParams {
@@ -23,14 +23,23 @@ struct CacheParams {
     __nv_bfloat16* out[2];       // read: k, v
     long long stride[2];         // elements between rows of k and v
     uint8_t* cache[2];           // bf16 or 8-bit codes [num_pages * page_size, Hkv, d]
-    float descale[2], inv[2];    // inv: 1 / descale, or 0 where quotient() has to divide
+    float descale[2], inv[2];    // inv: 1 / descale, or 0 where divide() has to divide
     PagedRows rows;
     RopeCols cols;               // rot 0: no rotation
     const int* positions;
     const double* inv_freq;
     float amplitude;
-    int Hkv, tokens, items;      // tokens per block, work items per head
+    RowShare share;
+    int Hkv, items;              // work items per head
 };
+
+// Cache rows of tokens [t0, t0 + tokens), a warp for each in turn. Every thread of the block calls it.
+__device__ __forceinline__ void find_places(const PagedRows& rows, int t0, int tokens, long long* place) {
+    for (int t = threadIdx.x >> 5; t < tokens; t += blockDim.x >> 5) {
+        const long long r = paged_row(rows, t0 + t);
+        if ((threadIdx.x & 31) == 0) place[t] = r;
+    }
+}
 
 // Two values to a pair of 8-bit codes (low byte first): nearest even, magnitudes above the largest
 // finite one saturate, NaN stays NaN.
@@ -58,33 +67,38 @@ __device__ __forceinline__ void fp8x2_values(uint32_t two, float& lo, float& hi)
         : "r"(h2));
 }
 
-// x / d rounded to fp32, with inv the rounded 1 / d: the product with inv, corrected by the exact remainder
-// (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990). Far
-// beyond the 8-bit range, where the remainder may overflow or x is not finite, the product will do: it
-// saturates, or is NaN. The conversions of a write are bounded by such arithmetic: with a division per
-// element the write took 1.4 times as long.
-__device__ __forceinline__ float quotient(float x, float d, float inv) {
-    if (inv == 0.0f) return x / d;
-    const float q = x * inv;
-    const float c = fmaf(fmaf(-q, d, x), inv, q);
-    // 0 < |q| < 1e6 by the bits of |q| (the correction would lose the sign of a zero)
-    return (__float_as_uint(q) & 0x7FFFFFFFu) - 1u < 0x497423FFu ? c : q;
+// x[e] / d rounded to fp32, with inv the rounded 1 / d: the product with inv, corrected by the exact
+// remainder (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990); far beyond the 8-bit range, where the remainder may overflow or x is not finite, the product alone
+// saturates or is NaN. inv = 0 asks for the division. The write is bounded by instruction issue: with a
+// division per element it took 1.4 times as long.
+template <int V>
+__device__ __forceinline__ void divide(float (&x)[V], float d, float inv) {
+    if (inv != 0.0f) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float q = x[e] * inv;
+            const float c = fmaf(-fmaf(q, d, -x[e]), inv, q);  // (in this order -0 stays -0)
+            x[e] = fabsf(q) < 1e6f ? c : q;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[e] /= d;
+    }
 }
 
 // V values into the cache at element offset at.
 template <int FMT, int V>
-__device__ __forceinline__ void store_cache(uint8_t* cache, long long at, const float (&x)[V], float descale, float inv) {
+__device__ __forceinline__ void store_cache(uint8_t* cache, long long at, float (&x)[V], float descale, float inv) {
     if constexpr (FMT == ATTN_KV_BF16) {
         store_row<V>(reinterpret_cast<__nv_bfloat16*>(cache) + at, x);
-    } else if constexpr (V == 8) {
-        uint32_t w[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            w[i] = fp8x2<FMT>(quotient(x[4 * i], descale, inv), quotient(x[4 * i + 1], descale, inv)) |
-                   (fp8x2<FMT>(quotient(x[4 * i + 2], descale, inv), quotient(x[4 * i + 3], descale, inv)) << 16);
-        *reinterpret_cast<uint2*>(cache + at) = make_uint2(w[0], w[1]);
     } else {
-        cache[at] = (uint8_t)fp8x2<FMT>(quotient(x[0], descale, inv), 0.0f);
+        divide<V>(x, descale, inv);
+        if constexpr (V == 8)
+            *reinterpret_cast<uint2*>(cache + at) = make_uint2(fp8x2<FMT>(x[0], x[1]) | (fp8x2<FMT>(x[2], x[3]) << 16),
+                                                               fp8x2<FMT>(x[4], x[5]) | (fp8x2<FMT>(x[6], x[7]) << 16));
+        else
+            cache[at] = (uint8_t)fp8x2<FMT>(x[0], 0.0f);
     }
 }
 
@@ -92,71 +106,77 @@ template <int FMT, int V>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheParams p) {
     extern __shared__ __align__(16) float angles[];
     __shared__ long long place[kCacheMaxTokens];
-    const int half = p.cols.rot / 2;
-    const long long t0 = (long long)blockIdx.x * p.tokens;
-    const int tokens = (int)min((long long)p.tokens, p.rows.T - t0);
-    float* cs = angles;
-    float* sn = angles + p.tokens * half;
-    // Items: heads of K, then of V. One is loaded while the one before is converted and stored.
     typedef typename RawOf<__nv_bfloat16, V>::type Raw;
-    ItemWalk at(2 * p.Hkv, p.items);
-    Raw ra, rb;
-    auto cols = [&](bool v, int j, int& a, int& b) -> bool {
-        if (!v) return item_cols<V>(p.cols, j, a, b);
-        a = V * j, b = a + p.cols.d / 2;
-        return false;
-    };
-    auto load = [&]() {
-        const bool v = at.h >= p.Hkv;
-        const __nv_bfloat16* src = (v ? p.in[1] : p.in[0]) + (t0 + at.t) * (v ? p.stride[1] : p.stride[0]) +
-                                   (long long)(v ? at.h - p.Hkv : at.h) * p.cols.d;
-        int a, b;
-        cols(v, at.j, a, b);
-        ra = load_raw<__nv_bfloat16, V>(src + a);
-        rb = load_raw<__nv_bfloat16, V>(src + b);
-    };
-    if (at.t < tokens) load();
-    if (half > 0) block_angles(p.inv_freq, p.positions + t0, tokens, half, p.amplitude, false, cs, sn);
-    for (int t = threadIdx.x >> 5; t < tokens; t += kCacheThreads / 32) {
-        const long long r = paged_row(p.rows, (int)t0 + t);
-        if ((threadIdx.x & 31) == 0) place[t] = r;
-    }
-    __syncthreads();
-    while (at.t < tokens) {
-        const int t = at.t, j = at.j, h = at.h;
-        float xa[V], xb[V];
-        unpack<__nv_bfloat16, V>(ra, xa);
-        unpack<__nv_bfloat16, V>(rb, xb);
-        at.next();
-        if (at.t < tokens) load();
+    const int half = p.cols.rot / 2;
+    const long long t0 = (long long)blockIdx.x * p.share.tokens;
+    const int tokens = (int)min((long long)p.share.tokens, p.rows.T - t0);
+    float* cs = angles;
+    float* sn = angles + p.share.tokens * half;
+    const int groups = blockDim.x / p.share.width, group = threadIdx.x / p.share.width;
+    const int pairs = 2 * p.Hkv * p.items;  // heads of K, then of V
+    int pair = threadIdx.x - group * p.share.width;
+    bool first = true;
+    do {  // (threads without a pair only take part in the angles and places)
+        const bool mine = group < groups && pair < pairs;
+        const int h = mine ? pair / p.items : 0, j = mine ? pair - h * p.items : 0;
         const bool v = h >= p.Hkv;
-        int a, b;
-        if (cols(v, j, a, b)) rotate_item<V>(xa, xb, p.cols, j, cs + t * half, sn + t * half);
-        const long long row = place[t];
-        if (row >= 0) {
-            uint8_t* cache = v ? p.cache[1] : p.cache[0];
-            const float descale = v ? p.descale[1] : p.descale[0], inv = v ? p.inv[1] : p.inv[0];
-            const long long to = (row * p.Hkv + (v ? h - p.Hkv : h)) * p.cols.d;
+        const int head = v ? h - p.Hkv : h;
+        const long long stride = v ? p.stride[1] : p.stride[0];
+        uint8_t* cache = v ? p.cache[1] : p.cache[0];
+        const float descale = v ? p.descale[1] : p.descale[0], inv = v ? p.inv[1] : p.inv[0];
+        int a = V * j, b = a + p.cols.d / 2;
+        const bool turned = !v && item_cols<V>(p.cols, j, a, b);
+        const __nv_bfloat16* src = (v ? p.in[1] : p.in[0]) + (t0 + group) * stride + (long long)head * p.cols.d;
+        // an item is loaded while the one before is converted and stored, the first while the places of the
+        // tokens are looked up
+        Raw ra, rb;
+        const int last = mine ? tokens : 0;
+        if (group < last) {
+            ra = load_raw<__nv_bfloat16, V>(src + a);
+            rb = load_raw<__nv_bfloat16, V>(src + b);
+        }
+        if (first) {
+            if (half > 0) block_angles(p.inv_freq, p.positions + t0, tokens, half, p.amplitude, false, cs, sn);
+            find_places(p.rows, (int)t0, tokens, place);
+            __syncthreads();
+            first = false;
+        }
+        for (int t = group; t < last; t += groups) {
+            float xa[V], xb[V];
+            unpack<__nv_bfloat16, V>(ra, xa);
+            unpack<__nv_bfloat16, V>(rb, xb);
+            src += groups * stride;
+            if (t + groups < last) {
+                ra = load_raw<__nv_bfloat16, V>(src + a);
+                rb = load_raw<__nv_bfloat16, V>(src + b);
+            }
+            if (turned) rotate_item<V>(xa, xb, p.cols, j, cs + t * half, sn + t * half);
+            const long long row = place[t];
+            if (row < 0) continue;
+            const long long to = (row * p.Hkv + head) * p.cols.d;
             store_cache<FMT, V>(cache, to + a, xa, descale, inv);
             store_cache<FMT, V>(cache, to + b, xb, descale, inv);
         }
-    }
+        pair += p.share.width;
+    } while (pair < pairs);
 }
 
 // 16 elements per item: one 16-byte load of codes (two of bf16), two 16-byte stores.
 template <int FMT>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheParams p) {
     __shared__ long long place[kCacheMaxTokens];
-    const long long t0 = (long long)blockIdx.x * p.tokens;
-    const int tokens = (int)min((long long)p.tokens, p.rows.T - t0);
-    for (int t = threadIdx.x >> 5; t < tokens; t += kCacheThreads / 32) {
-        const long long r = paged_row(p.rows, (int)t0 + t);
-        if ((threadIdx.x & 31) == 0) place[t] = r;
-    }
+    const long long t0 = (long long)blockIdx.x * p.share.tokens;
+    const int tokens = (int)min((long long)p.share.tokens, p.rows.T - t0);
+    find_places(p.rows, (int)t0, tokens, place);
     __syncthreads();
+    const int groups = blockDim.x / p.share.width, group = threadIdx.x / p.share.width;
+    const int pairs = 2 * p.Hkv * p.items;
+    if (group >= groups) return;
+    for (int pair = threadIdx.x - group * p.share.width; pair < pairs; pair += p.share.width)
 #pragma unroll 2
-    for (ItemWalk at(2, p.Hkv * p.items); at.t < tokens; at.next()) {
-        const int t = at.t, kv = at.h, c = at.j * 16;  // element of the row [Hkv, d]
+    for (int t = group; t < tokens; t += groups) {
+        const bool kv = pair >= pairs / 2;
+        const int c = (kv ? pair - pairs / 2 : pair) * 16;  // element of the row [Hkv, d]
         const long long row = place[t];
         if (row == kRowNone) continue;
         __nv_bfloat16* dst = (kv ? p.out[1] : p.out[0]) + (t0 + t) * (kv ? p.stride[1] : p.stride[0]) + c;
@@ -190,18 +210,19 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CachePa
 template <int FMT, int V>
 cudaError_t launch_write(CacheParams p, int num_sms, cudaStream_t stream) {
     p.items = p.cols.d / (2 * V);
-    p.tokens = block_tokens(p.rows.T, 2LL * p.Hkv * p.items, kCacheThreads, kCacheMaxTokens, num_sms);
-    const int blocks = (p.rows.T + p.tokens - 1) / p.tokens;
-    cache_write_kernel<FMT, V><<<blocks, kCacheThreads, (size_t)p.tokens * p.cols.rot * sizeof(float), stream>>>(p);
+    p.share = share_rows(p.rows.T, 2 * p.Hkv * p.items, kCacheMaxTokens, num_sms);
+    const long long blocks = ((long long)p.rows.T + p.share.tokens - 1) / p.share.tokens;
+    const size_t smem = (size_t)p.share.tokens * p.cols.rot * sizeof(float);
+    cache_write_kernel<FMT, V><<<(unsigned)blocks, p.share.threads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <int FMT>
 cudaError_t launch_read(CacheParams p, int num_sms, cudaStream_t stream) {
     p.items = p.cols.d / 16;
-    p.tokens = block_tokens(p.rows.T, 2LL * p.Hkv * p.items, kCacheThreads, kCacheMaxTokens, num_sms);
-    const int blocks = (p.rows.T + p.tokens - 1) / p.tokens;
-    cache_read_kernel<FMT><<<blocks, kCacheThreads, 0, stream>>>(p);
+    p.share = share_rows(p.rows.T, 2 * p.Hkv * p.items, kCacheMaxTokens, num_sms);
+    const long long blocks = ((long long)p.rows.T + p.share.tokens - 1) / p.share.tokens;
+    cache_read_kernel<FMT><<<(unsigned)blocks, p.share.threads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

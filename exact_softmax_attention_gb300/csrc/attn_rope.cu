@@ -33,6 +33,40 @@ struct RopeParams {
     int transpose;
 };
 
+// The items of a block of tokens, this thread's ones blockDim apart. Item (t, h, j): token t of the
+// block, head h of `heads`, item j of `items` per head, in that order; the indices advance without divisions.
+struct ItemWalk {
+    int t, h, j, dt, dh, dj, heads, items;
+    __device__ __forceinline__ ItemWalk(int heads_, int items_) : heads(heads_), items(items_) {
+        const int n = blockDim.x;
+        j = threadIdx.x % items;
+        h = threadIdx.x / items;
+        t = h / heads;
+        h -= t * heads;
+        dj = n % items;
+        dh = n / items;
+        dt = dh / heads;
+        dh -= dt * heads;
+    }
+    __device__ __forceinline__ void next() {
+        j += dj;
+        h += dh;
+        t += dt;
+        if (j >= items) j -= items, ++h;
+        if (h >= heads) h -= heads, ++t;
+    }
+};
+
+// Tokens per block, at most `most`: enough for eight items per thread, as long as every SM still gets
+// two blocks.
+int block_tokens(int T, long long items_per_token, int threads, int most, int num_sms) {
+    long long n = (8LL * threads + items_per_token - 1) / items_per_token;
+    const long long spread = T / (2LL * num_sms);
+    if (n > spread) n = spread;
+    if (n > most) n = most;
+    return n < 1 ? 1 : (int)n;
+}
+
 template <typename E, int V>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
     extern __shared__ __align__(16) float angles[];

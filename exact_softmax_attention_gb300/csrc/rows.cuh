@@ -73,9 +73,17 @@ __device__ __forceinline__ unsigned long long turn_fraction(double f) {
     return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);  // (fraction < 1) * 2^64
 }
 
+// The quarter turn nearest to the angle is split off in integers too, so that what is rounded to fp32 is at
+// most an eighth of a turn: the angle is off by 2^-25 of that, 2e-8 rad.
 __device__ __forceinline__ void position_angle(unsigned long long frac, int pos, float& c, float& s) {
-    const long long phase = (long long)(frac * (unsigned long long)(long long)pos);  // turns * 2^64, in [-1/2, 1/2)
-    sincospif(__ll2float_rn(phase) * 1.0842021724855044e-19f, &s, &c);               // * 2^-63: half turns
+    const unsigned long long phase = frac * (unsigned long long)(long long)pos;  // turns * 2^64
+    const unsigned quarter = (unsigned)((phase + (1ull << 61)) >> 62);
+    const long long rest = (long long)(phase - ((unsigned long long)quarter << 62));  // [-2^61, 2^61)
+    float c0, s0;
+    sincospif(__ll2float_rn(rest) * 1.0842021724855044e-19f, &s0, &c0);  // * 2^-63: half turns
+    const float u = quarter & 1 ? -s0 : c0, w = quarter & 1 ? c0 : s0;   // one quarter turn further
+    c = quarter & 2 ? -u : u;
+    s = quarter & 2 ? -w : w;
 }
 
 // cos and sin (times the amplitude) of tokens [0, tokens) of a block into cs[token][rot / 2] and
@@ -147,40 +155,29 @@ __device__ __forceinline__ void store_row(float* p, const float (&x)[V]) {
         *p = x[0];
 }
 
-// ---- the items of a block of tokens, this thread's ones blockDim apart
+// ---- how the threads of a block share the items of its tokens
 //
-// Item (t, h, j): token t of the block, head h of `heads`, item j of `items` per head, in that order. The
-// three indices advance without divisions.
-struct ItemWalk {
-    int t, h, j, dt, dh, dj, heads, items;
-    __device__ __forceinline__ ItemWalk(int heads_, int items_) : heads(heads_), items(items_) {
-        const int n = blockDim.x;
-        j = threadIdx.x % items;
-        h = threadIdx.x / items;
-        t = h / heads;
-        h -= t * heads;
-        dj = n % items;
-        dh = n / items;
-        dt = dh / heads;
-        dh -= dt * heads;
-    }
-    __device__ __forceinline__ void next() {
-        j += dj;
-        h += dh;
-        t += dt;
-        if (j >= items) j -= items, ++h;
-        if (h >= heads) h -= heads, ++t;
-    }
+// A token has `pairs` = heads * items per head (head, item) pairs. `width` threads take one pair each (in
+// turns, when there are more pairs) and keep it over all tokens of the block, so that heads, columns and
+// angles are worked out once; blockDim / width groups of threads take the tokens in turn.
+struct RowShare {
+    int width, threads;  // threads per token, threads of the block
+    int tokens;          // tokens per block
 };
 
-// Tokens per block, at most `most`: enough for eight items per thread, as long as every SM still gets
-// eight blocks.
-inline int block_tokens(int T, long long items_per_token, int threads, int most, int num_sms) {
-    long long n = (8LL * threads + items_per_token - 1) / items_per_token;
-    const long long spread = T / (8LL * num_sms);
+// Eight items per thread, and no more than `most` tokens, as long as every SM still gets two blocks.
+inline RowShare share_rows(int T, int pairs, int most, int num_sms) {
+    RowShare s;
+    const int turns = (pairs + 511) / 512;
+    s.width = (pairs + turns - 1) / turns;
+    const int groups = s.width >= 256 ? 1 : 256 / s.width;
+    s.threads = (s.width * groups + 31) / 32 * 32;
+    long long n = (8LL * groups + turns - 1) / turns;
+    const long long spread = T / (2LL * num_sms);
     if (n > spread) n = spread;
     if (n > most) n = most;
-    return n < 1 ? 1 : (int)n;
+    s.tokens = n < 1 ? 1 : (int)n;
+    return s;
 }
 
 // ---- packed rows of a paged cache
