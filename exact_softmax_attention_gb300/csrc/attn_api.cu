@@ -616,7 +616,8 @@ attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const v
     p.q_sign = factor == 0 ? 0.0f : (score_scale < 0 ? -1.0f : 1.0f);
     p.scale = factor == 0 ? 1.0f : (float)factor;
     p.scale_log2 = (float)((factor == 0 ? 1.0 : factor) * 1.4426950408889634);
-    p.rescale_thr = (float)opt.rescale_threshold;
+    // (P of 8-bit caches is f16: up to 2^threshold has to stay in its range)
+    p.rescale_thr = (float)(f8 && opt.rescale_threshold > 15 ? 15.0 : opt.rescale_threshold);
     p.v_descale = f8 ? v_descale : 1.0f;
     p.status = ds->status;
     p.watchdog_ns = (unsigned long long)(opt.watchdog_ms * 1e6);
@@ -637,7 +638,10 @@ attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const v
         cudaMemPool_t pool = nullptr;
         if ((st = device_pool(ds, &pool)) != ATTN_OK) return st;
         const size_t n = (size_t)T * Hq * p.max_splits;
-        if (cudaMallocFromPoolAsync(&ws, n * ((size_t)d + 1) * sizeof(float), pool, s) != cudaSuccess) return ATTN_ERR_CUDA;
+        if (cudaMallocFromPoolAsync(&ws, n * ((size_t)d + 1) * sizeof(float), pool, s) != cudaSuccess) {
+            cudaGetLastError();  // (out of memory is no error of the next call)
+            return ATTN_ERR_CUDA;
+        }
         p.ws_o = reinterpret_cast<float*>(ws);
         p.ws_lse = p.ws_o + n * d;
     }

@@ -8,6 +8,7 @@
 // row to its page (offsets, length, page table); the rows themselves do not depend on it, so each
 // thread loads its first item before the places are known.
 #include "attn.h"
+#include "launch.cuh"
 #include "rows.cuh"
 
 #include <math.h>
@@ -213,8 +214,7 @@ cudaError_t launch_write(CacheParams p, int num_sms, cudaStream_t stream) {
     p.share = share_rows(p.rows.T, 2 * p.Hkv * p.items, kCacheMaxTokens, num_sms);
     const long long blocks = ((long long)p.rows.T + p.share.tokens - 1) / p.share.tokens;
     const size_t smem = (size_t)p.share.tokens * p.cols.rot * sizeof(float);
-    cache_write_kernel<FMT, V><<<(unsigned)blocks, p.share.threads, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(cache_write_kernel<FMT, V>, dim3((unsigned)blocks), p.share.threads, smem, stream, false, p);
 }
 
 template <int FMT>
@@ -222,8 +222,7 @@ cudaError_t launch_read(CacheParams p, int num_sms, cudaStream_t stream) {
     p.items = p.cols.d / 16;
     p.share = share_rows(p.rows.T, 2 * p.Hkv * p.items, kCacheMaxTokens, num_sms);
     const long long blocks = ((long long)p.rows.T + p.share.tokens - 1) / p.share.tokens;
-    cache_read_kernel<FMT><<<(unsigned)blocks, p.share.threads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(cache_read_kernel<FMT>, dim3((unsigned)blocks), p.share.threads, 0, stream, false, p);
 }
 
 bool multiple(const void* p, long long bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }

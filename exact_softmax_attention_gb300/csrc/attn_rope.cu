@@ -9,6 +9,7 @@
 // One block takes a few tokens, computes their cosines and sines once into shared memory (shared by
 // all heads), and streams the heads through 16-byte loads and stores.
 #include "attn.h"
+#include "launch.cuh"
 #include "rows.cuh"
 
 #include <math.h>
@@ -115,10 +116,9 @@ cudaError_t launch_rope(RopeParams p, bool in_place, int num_sms, cudaStream_t s
     p.items = (in_place ? p.cols.rot : p.cols.d) / (2 * V);
     // (the angles of a block's tokens take at most 32 KB)
     p.tokens = block_tokens(p.T, (long long)p.H * p.items, kRopeThreads, 8192 / p.cols.rot, num_sms);
-    const int blocks = (p.T + p.tokens - 1) / p.tokens;
+    const long long blocks = ((long long)p.T + p.tokens - 1) / p.tokens;
     const size_t smem = (size_t)p.tokens * p.cols.rot * sizeof(float);
-    rope_kernel<E, V><<<blocks, kRopeThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(rope_kernel<E, V>, dim3((unsigned)blocks), kRopeThreads, smem, stream, false, p);
 }
 
 bool multiple(const void* p, long long bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }

@@ -11,6 +11,7 @@
 // Masked keys contribute exactly nothing, whatever their slots hold: scores are replaced by -inf,
 // and in the key tiles where a row may not see every key the non-finite values of V are taken out of
 // the product (0 times NaN would be NaN) and added to the rows that do see them at the end.
+#include "launch.cuh"
 #include "tree_device.cuh"
 
 namespace attn {
@@ -431,16 +432,8 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p) {
 
 template <int D>
 cudaError_t launch_join(const TreeParams& p, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((long long)p.max_q * p.Hq + 3) / 4), (unsigned)p.B);
-    cfg.blockDim = dim3(128);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D>, p);
+    const dim3 grid((unsigned)(((long long)p.max_q * p.Hq + 3) / 4), (unsigned)p.B);
+    return launch_kernel(tree_combine_kernel<D>, grid, 128, 0, stream, true, p);
 }
 
 template <int D, int GN, int FMT>
@@ -452,8 +445,7 @@ cudaError_t launch_small(TreeParams p, cudaStream_t stream) {
     p.groups = (int)(((long long)p.max_q * p.G + 15) / 16);
     const long long x = (long long)p.max_splits * p.Hkv * p.groups;
     if (x > INT32_MAX) return cudaErrorInvalidConfiguration;
-    tree_small_kernel<D, GN, FMT><<<dim3((unsigned)x, (unsigned)p.B), kWarps * 32, bytes, stream>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(tree_small_kernel<D, GN, FMT>, dim3((unsigned)x, (unsigned)p.B), kWarps * 32, bytes, stream, false, p);
 }
 
 template <int D, int FMT>

@@ -3,24 +3,46 @@
 //
 // A block takes one (sequence, split of the keys, kv head, 128-row tile) and walks the split's keys in
 // tiles of 64. Per tile S = Q K^T (M 128, N 64) and O += P V (M 128, N d), accumulators in tensor
-// memory, P as the 16-bit A operand from tensor memory over S. Two blocks share an SM (96 KB of
-// shared memory and 256 tensor-memory columns each), so that one block's start, softmax latency and
-// end are covered by the other's loads. Roles of the warps:
-//   warps 0, 2  loads of K and of V: boxes of 64 or 16 rows through tensor maps of the caches viewed as
-//               [rows, Hkv d] where the page size is a multiple of that (rows past the end or of a bad
-//               page lie outside the map and arrive as zeros), else 16-byte copies of rows that the
-//               page table gives. (A tensor copy costs its warp about 66 clocks, so gather copies of
-//               four rows, 64 for a 32 KB tile, took 4600.)
-//   warp 1      issues the products and owns the tensor memory
-//   warp 3      16-bit caches: passes the V tiles on, taking non-finite values out of those that a row
-//               may not see in full
-//   warps 4-7   softmax, one row per thread: maximum, conditional rescale of O (only when a maximum
-//               grows by more than the threshold), exponentials, P; at the end O / l and the LSE
-//   warps 8-11  8-bit caches only: two warps each widen the K and the V tiles to f16 (exact) in shared
-//               memory, V as warp 3 does
-// A 64-key tile of bf16 K and V is 32 KB, 1390 clocks of an SM's share of the memory bandwidth
-// (6.8 TB/s over 152 SMs at 1.9 GHz), against about 640 clocks of products: with up to 128 rows the
-// kernel should be bounded by the cache reads.
+// memory, P as the 16-bit A operand from tensor memory over S; two S buffers, so that the products of a
+// tile run during the softmax of the one before. Two blocks share an SM (up to 113 KB of shared memory
+// and 256 tensor-memory columns each), so that one block's start, latencies and end are covered by the
+// other.
+//
+// 8-bit caches: K is multiplied as it is (kind::f8f6f4). Q is split into two e4m3 parts after scaling
+// each row by a power of two: eight significant bits of bf16 are four and four, so the two parts hold q
+// exactly unless an element is more than 2^9 below the row's largest (then it is off by at most 2^-17 of
+// that). V is widened to f16 (exact), because P needs more than an 8-bit format: its small values, summed
+// over a long context, are not small.
+//
+// Roles of the warps:
+//   warps 0, 2   loads of K and of V: boxes of 64 or 16 rows through tensor maps of the caches viewed as
+//                [rows, Hkv d] where the page size is a multiple of that (rows past the end or of a bad
+//                page lie outside the map and arrive as zeros), else 16-byte copies of rows that the
+//                page table gives. (A tensor copy costs its warp about 66 clocks, so gather copies of
+//                four rows, 64 for a 32 KB tile, took 4600.)
+//   warps 1, 3   one thread each issues S and P V. (Issued by a whole warp under a predicate, a product
+//                costs 70 clocks instead of the 34 to 64 that it takes to execute; and the waits and commits
+//                of S and P V in one thread made about 2000 clocks a tile.)
+//   warps 4-7    softmax, one row per thread: maximum, conditional rescale of O (only when a maximum
+//                grows by more than the threshold), exponentials, P; at the end O / l and the LSE. Warps
+//                whose 32 rows are all padding do nothing
+//   warp 8       16-bit caches: passes the V tiles on, taking non-finite values out of those that a row
+//                may not see in full
+//   warps 8-11   8-bit caches: widen the V tiles, taking out non-finite values in the same way
+//
+// What bounds it. 64 keys of bf16 K and V of a head are 32 KB; the products take 640 clocks of the SM
+// (S 8 x 48, bound by the 6 KB of shared memory that each reads, P V 4 x 64). With up to 128 rows the bf16
+// form is bounded by the memory: 16 drafted tokens x 4 query heads over 64 sequences of U[1K, 32K] tokens
+// take 682 us, 6350 GB/s, 0.94 of the measured copy rate (page size 64: 658 us; sequences of equal
+// length: 6980 GB/s). 8-bit caches have half the bytes for the same products: 512 us, 4250 GB/s (0.63),
+// bounded by the tensor pipe and the chain S -> softmax -> P V of two buffers. More than 128 rows: every
+// further tile reads the cache again through the L2 (64 drafted tokens: 1060 us, 1045 TFLOP/s, 0.54 of
+// the measured bf16 rate).
+// Tried and slower, same case, bf16 / 8-bit (first kernel of this form 698 / 584): Q in tensor memory with
+// one S buffer 713 / 753, or with S in steps of 32 keys 813 / 844 (a product takes 32 clocks at least); one
+// S buffer with two separate P 685 / 531; one block of 512 threads per SM with two streams of even and
+// odd tiles 696 / 721.
+#include "launch.cuh"
 #include "tree_device.cuh"
 
 namespace attn {
@@ -720,8 +742,8 @@ cudaError_t launch_tiles(TreeParams p, const TreeTmaps& tm, cudaStream_t stream)
     p.groups = (int)(((long long)p.max_q * p.G + kTileRows - 1) / kTileRows);
     const long long x = (long long)p.max_splits * p.Hkv * p.groups;
     if (x > INT32_MAX) return cudaErrorInvalidConfiguration;
-    tree_tile_kernel<D, FMT><<<dim3((unsigned)x, (unsigned)p.B), TileLayout<D, FMT>::kThreads, bytes, stream>>>(p, tm.k, tm.v);
-    return cudaGetLastError();
+    return launch_kernel(tree_tile_kernel<D, FMT>, dim3((unsigned)x, (unsigned)p.B), TileLayout<D, FMT>::kThreads, bytes, stream,
+                         false, p, tm.k, tm.v);
 }
 
 template <int D>

@@ -220,6 +220,7 @@ __device__ __forceinline__ long long paged_row(const PagedRows& p, int t) {
         b = warp_find_seq(p.cu_seqlens, p.B, t);
         if (b >= p.B) return kRowNone;
         const long long c0 = __ldg(p.cu_seqlens + b), c1 = __ldg(p.cu_seqlens + b + 1);
+        if (b == 0 && t < c0) return kRowNone;  // rows before the first sequence
         if (t < c0 || t >= c1 || c0 < 0 || c1 > p.T) {  // offsets that decrease or pass the rows
             if ((threadIdx.x & 31) == 0) atomicCAS(p.status, 0, kDevBadIndex);
             return kRowNone;

@@ -287,8 +287,8 @@ attn_status_t attn_rope_freqs(double* inv_freq, double* amplitude, int rot_dim, 
  *            that follows takes): row i of the n rows of sequence b becomes its cached token
  *            seqlens[b] - n + i
  * cu_seqlens device, int32 [B+1], prefix offsets of the sequences' rows in k and v (non-decreasing,
- *            empty sequences allowed), or NULL: T / B rows each. Rows of k and v behind the last
- *            sequence are ignored.
+ *            empty sequences allowed), or NULL: T / B rows each. Rows of k and v before the first
+ *            and behind the last sequence are ignored.
  * T          rows of k and v;  d  a multiple of 16, at most 256
  * kv_format  ATTN_KV_BF16, ATTN_FP8_E4M3 or ATTN_FP8_E5M2
  * k_descale, v_descale  finite, not 0; an 8-bit code is fp8(x / descale): nearest, ties to even;
@@ -316,8 +316,8 @@ attn_status_t attn_kv_write_paged(const void* k, const void* v, long long k_stri
  * the inverse of attn_kv_write_paged without rotation. 8-bit codes become descale * fp8(code),
  * rounded once to bf16; bf16 caches are copied bit for bit.
  *
- * k, v  device, bf16 [T, Hkv, d] (written), strides >= Hkv * d. Rows behind the last sequence are
- *       left as they were. Rows of a page outside [0, num_pages) or of a sequence whose length is
+ * k, v  device, bf16 [T, Hkv, d] (written), strides >= Hkv * d. Rows before the first and behind the
+ *       last sequence are left as they were. Rows of a page outside [0, num_pages) or of a sequence whose length is
  *       out of range are zeros, and ATTN_ERR_DEVICE_BAD_INDEX is recorded.
  * Everything else is as for attn_kv_write_paged.
  */
@@ -351,7 +351,7 @@ attn_status_t attn_kv_read_paged(const void* k_cache, const void* v_cache, void*
  *            gets o = 0 and lse = -inf. NULL: token i sees the drafted tokens 0 .. i.
  * o, lse     device, bf16 [T, Hq, d] and fp32 [T, Hq] as for attn_decode_paged (written)
  * max_q      largest number of rows of a sequence, 1 .. 256 (at least T / B without cu_seqlens; at
- *            most 64 * mask_words with a mask); max_q * Hq / Hkv at most 65535
+ *            most 64 * mask_words with a mask); max_q * Hq / Hkv at most 65535, T * Hq below 2^31
  * mask_words words per row of tree_mask, 1 .. 4 (ignored without a mask)
  * Hq, Hkv, d as for attn_decode_paged (d = 64 or 128); scale finite
  * num_splits 0: choose the number of key splits from the SM count and the sizes; n > 0: at most n
@@ -359,9 +359,12 @@ attn_status_t attn_kv_read_paged(const void* k_cache, const void* v_cache, void*
  * What a masked or unused cache slot holds does not matter, NaN and infinities included. A page
  * outside [0, num_pages) is not read: its rows count as zeros and ATTN_ERR_DEVICE_BAD_INDEX is
  * recorded.
- * Arithmetic: products of 16-bit values on the tensor cores with fp32 accumulation (8-bit codes are
- * widened exactly to f16 and q is converted to f16, see attn_decode_paged_fp8), fp32 softmax,
- * probabilities rounded to bf16 (8-bit caches: f16) for the second product.
+ * Arithmetic: products on the tensor cores with fp32 accumulation, fp32 softmax, probabilities
+ * rounded to bf16 (8-bit caches: f16) for the second product. bf16 caches: bf16 products. 8-bit
+ * caches, up to 16 rows (max_q * Hq / Hkv): codes widened exactly to f16, q converted to f16 (see
+ * attn_decode_paged_fp8). More rows: keys multiplied as they are by q split into two e4m3 parts (after
+ * scaling each row by a power of two), exact for elements down to 2^-9 of the row's largest and
+ * within 2^-17 of that for smaller ones; values widened exactly to f16.
  * Workspace, launches and programmatic dependents as for attn_decode_paged: partial outputs of the
  * splits (T * Hq * splits * (d + 1) floats) from the library's stream-ordered pool on `stream`.
  * Alignment: q, o, k_cache, v_cache 16 bytes; tree_mask 8; lse, page_table, seqlens, cu_seqlens 4.

@@ -240,6 +240,37 @@ def test_bad_lengths_pages_and_offsets(A):
 
 
 @pytest.mark.gpu
+def test_rows_before_the_first_sequence(A):
+    """Offsets are absolute rows: a call on the later sequences ignores the rows before them."""
+    c = Cache("e5m2", 2, 64, 4, [3, 2, 4], [9, 2, 30], seed=6)
+    before = c.kc.clone()
+    args = (c.ptd[1:], c.lend[1:], c.cu[1:], 4, c.T, 2, 2, 64, c.width, c.num, "e5m2", c.kds, c.vds)
+    A.attn_kv_write_paged(c.k, c.v, c.x.stride(0), c.x.stride(0), c.kc, c.vc, *args)
+    k = torch.full((c.T, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    v = k.clone()
+    A.attn_kv_read_paged(c.kc, c.vc, k, v, 128, 128, *args)
+    assert A.attn_get_device_status() == 0
+    touched = np.flatnonzero((c.kc != before).view(c.num * 4, -1).any(1).cpu().numpy())
+    assert set(touched) <= set(c.rows()[3:])
+    assert (k[:3] == 7).all() and (k[9:] == 7).all() and (k[3:9] != 7).any(1).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("descale", [1e-38, 2.0**-126, 1e38, -0.02, 3e-39])
+def test_extreme_descales(A, descale):
+    """The quotient holds where a reciprocal would leave the range of fp32, and for negative factors."""
+    c = Cache("e4m3", 1, 64, 4, [4], [4], seed=7, dense=True)
+    ds = float(np.float32(descale))
+    c.x.copy_((torch.randn(c.x.shape, dtype=torch.float64) * 50 * abs(ds)).bfloat16())
+    c.kds = c.vds = descale
+    c.write(A)
+    ref = c.k.double().cpu().numpy().reshape(4, 1, 64) / ds
+    got = c.values(c.kc)[c.rows()]
+    ref = np.clip(ref, -448, 448)
+    assert (np.abs(got - ref) <= half_step(np.abs(ref) * (1 + 2.0**-23), "e4m3") + 2.0**-23 * np.abs(ref)).all()
+
+
+@pytest.mark.gpu
 def test_write_on_a_side_stream_in_a_graph(A):
     """Captured and replayed: the replay follows new rows and new lengths."""
     c = Cache("e4m3", 4, 128, 16, [1] * 6, [5, 17, 1, 16, 33, 40], seed=9, dense=True)

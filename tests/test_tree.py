@@ -147,6 +147,8 @@ class Case:
                     # with |s| 2^-23 for s log2 e), and the sums over the keys
                     e = (np.abs(k) @ np.abs(x)).max() * abs(scale) * (self.d + 4) * 2.0**-24 + 2.0**-20 + np.abs(s).max() * 2.0**-22 \
                         + (len(keys) / 16 + 40) * 2.0**-24
+                    if self.fmt != "bf16":  # q as two e4m3 parts: elements off by at most 2^-17 of the row's largest
+                        e += np.abs(x).max() * 2.0**-17 * np.abs(k).sum(1).max() * abs(scale)
                     p_step = 2.0**-8 if self.fmt == "bf16" else 2.0**-11  # half a step of P, relative
                     small = 0.0 if self.fmt == "bf16" else len(keys) * 2.0**-25 * np.abs(v).max()  # f16 below its normal range
                     bo[self.cu[b] + i, h] = aw * (p_step + 2 * e) + small
@@ -270,6 +272,93 @@ def test_visible_nonfinite_values_stay(A, n, where, value):
     hit[:n][rows, 2:, 5] = True
     assert np.array_equal(~np.isfinite(o), hit)
     assert (np.isposinf(o[hit]) if value == float("inf") else np.isnan(o[hit])).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,n", [("e4m3", 3), ("e4m3", 30), ("e5m2", 30), ("bf16", 30)])
+def test_queries_of_any_range(A, fmt, n):
+    """Rows of q scaled from 2^-100 to 2^12, with elements spread over 2^20 within a row, zero rows, and scores
+    that a small scale brings back into range."""
+    c = Case(fmt, 4, 2, 128, 16, [n, n], [n, 250], "tree", 21)
+    rs = np.random.RandomState(3)
+    spread = torch.from_numpy(2.0 ** rs.randint(-20, 1, c.q.shape)).to(DEV)
+    c.q.copy_((c.q.double() * spread).bfloat16())
+    c.q[0] *= 2.0**-100 if fmt == "bf16" or n > 16 else 2.0**-10  # up to 16 rows q passes through f16
+    c.q[1] *= 2.0**12
+    c.q[2, 1] = 0
+    c.run(A, 2, 2.0**-12)
+    assert A.attn_get_device_status() == 0
+    c.check(2.0**-12)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [2, 30])
+@pytest.mark.parametrize("threshold", [0.0, 60.0])
+def test_any_rescale_threshold(A, fmt, n, threshold):
+    """Rescaling on every rise of the maximum, and (nearly) never: both are exact."""
+    c = Case(fmt, 4, 2, 128, 16, [n], [600], "tree", 22, qmult=3.0)
+    A.attn_set_option("rescale_threshold", threshold)
+    try:
+        c.run(A, 2)
+    finally:
+        A.attn_set_option("rescale_threshold", 8.0)
+    assert A.attn_get_device_status() == 0
+    c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,n,page", [("bf16", 2, 16), ("bf16", 20, 16), ("bf16", 20, 7), ("e4m3", 3, 16), ("e4m3", 20, 16)])
+def test_cache_offsets_beyond_32_bits(A, fmt, n, page):
+    """Rows written, read back and attended more than 2^32 bytes (and elements) into the caches."""
+    Hkv, d = 8, 128
+    c = Case(fmt, 8, Hkv, d, page, [n, n], [n, 120], "tree", 23)
+    rows = (1 << 32) // (Hkv * d) + 40 * page
+    c.num = rows // page
+    t = torch.bfloat16 if fmt == "bf16" else torch.uint8
+    small = c.c
+    big = [torch.empty((c.num, page, Hkv, d), dtype=t, device=DEV) for _ in range(2)]
+    moved = c.pt < 1 << 20
+    shift = c.num - small[0].shape[0]  # the case's pages move to the end of the large caches
+    for b, s in zip(big, small):
+        b[shift:] = s
+    c.pt = np.where(moved, c.pt + shift, c.pt).astype(np.int32)
+    c.dev["pt"] = torch.from_numpy(c.pt).to(DEV)
+    c.c = big
+    vals = c.values
+    x = torch.randn((c.T, 2 * Hkv * d), device=DEV, dtype=torch.bfloat16)
+    k, v = x[:, :Hkv * d], x[:, Hkv * d:]
+    A.attn_kv_write_paged(k, v, x.stride(0), x.stride(0), *c.c, c.dev["pt"], c.dev["lens"], c.dev["cu"], page, c.T, c.B, Hkv, d, c.width,
+                          c.num, fmt, *c.ds)
+    c.run(A, 2)
+    back = torch.zeros((2, c.T, Hkv * d), device=DEV, dtype=torch.bfloat16)
+    A.attn_kv_read_paged(*c.c, back[0], back[1], Hkv * d, Hkv * d, c.dev["pt"], c.dev["lens"], c.dev["cu"], page, c.T, c.B, Hkv, d,
+                         c.width, c.num, fmt, *c.ds)
+    assert A.attn_get_device_status() == 0
+    m = sum(c.n)
+    step = {"bf16": 0.0, "e4m3": 2.0**-4 + 2.0**-8}[fmt]
+    assert ((back[1][:m].double() - v[:m].double()).abs() <= v[:m].double().abs() * step * 1.01 + 1e-3 * (step > 0)).all()
+    c.c = [b[shift:].clone() for b in big]  # what the reference reads
+    c.pt = np.where(moved, c.pt - shift, c.pt).astype(np.int32)
+    del big, vals
+    c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 20])
+def test_a_slice_of_the_offsets(A, n):
+    """Offsets are absolute rows: a call on the later sequences leaves the rows before them alone."""
+    c = Case("bf16", 4, 2, 64, 16, [n, n, n], [40, 300, n], "tree", 24)
+    c.run(A)
+    want = c.o.clone(), c.lse.clone()
+    c.o.fill_(7)
+    c.lse.fill_(7)
+    d = c.dev
+    A.attn_decode_paged_tree(c.q, *c.c, d["pt"][1:], d["lens"][1:], d["cu"][1:], c.mask, c.words, 16, c.o, c.lse, None, c.T, 2, c.max_q, 4,
+                             2, 64, c.width, c.num, c.scale)
+    assert A.attn_get_device_status() == 0
+    assert (c.o[:n] == 7).all() and (c.lse[:n] == 7).all()
+    assert torch.equal(c.o[n:], torch.cat((want[0][n:3 * n], c.o[3 * n:]))) and (c.o[3 * n:] == 7).all()
 
 
 @pytest.mark.gpu
