@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(kWarps * 32) tree_small_kernel(const TreeParam
     constexpr bool F8 = FMT != ATTN_KV_BF16;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int odd_v;  // a V tile held a non-finite value that was taken out
-    const int HG = p.Hkv * p.groups;
-    const int b = blockIdx.y, split = (int)(blockIdx.x / (unsigned)HG), hg = (int)(blockIdx.x % (unsigned)HG);
+    int b, split, hg;
+    if (!tree_item(p, reinterpret_cast<int*>(smem), b, split, hg)) return;
     const int kvh = hg / p.groups, r0 = (hg % p.groups) * 16;
     TreeSeq s;
     if (!tree_seq(p, b, s)) return;
@@ -83,6 +83,10 @@ __global__ void __launch_bounds__(kWarps * 32) tree_small_kernel(const TreeParam
     if (R <= 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nsplit = cdiv(s.len, p.chunk);
+    if (split < 0)
+        split = nsplit > 0 ? nsplit - 1 : 0;
+    else if (p.full_rows >= 0 && split >= nsplit - 1)
+        return;  // the last split has its own block
     const int t_begin = split * p.chunk;
     // output row of local row r: (s.q0 + i) * Hq + kvh * G + g with (i, g) = divmod(r0 + r, G)
     auto out_row = [&](int r) {
@@ -443,9 +447,8 @@ cudaError_t launch_small(TreeParams p, cudaStream_t stream) {
     cudaError_t e = ensure_smem_attr(tree_small_kernel<D, GN, FMT>, bytes, attr_set);
     if (e != cudaSuccess) return e;
     p.groups = (int)(((long long)p.max_q * p.G + 15) / 16);
-    const long long x = (long long)p.max_splits * p.Hkv * p.groups;
-    if (x > INT32_MAX) return cudaErrorInvalidConfiguration;
-    return launch_kernel(tree_small_kernel<D, GN, FMT>, dim3((unsigned)x, (unsigned)p.B), kWarps * 32, bytes, stream, false, p);
+    const dim3 grid = tree_grid(p);
+    return launch_kernel(tree_small_kernel<D, GN, FMT>, grid, kWarps * 32, bytes, stream, false, p);
 }
 
 template <int D, int FMT>
@@ -467,37 +470,41 @@ void tree_plan(int B, int Hkv, int rows, long long lmax, int num_splits, int num
     if (num_splits > 0) {
         c = (lmax + num_splits - 1) / num_splits;
     } else if (tree_takes_tiles(rows)) {
-        // Blocks of 128 rows, two per SM. Fewer (sequence, kv head, row tile) groups than SMs: as many splits
-        // as fit at once (a few blocks more would cost a second wave), at least four of 1024 tokens or more,
-        // which balance sequences of different lengths. Else none but for the cap of 8192 tokens, because the
-        // partial results of 128 rows cost as much traffic as 130 cached tokens of one head and the join is a
-        // second launch. Measured, 8 drafted tokens x 4 query heads, bf16, splits -> us: 32 sequences of 4096
-        // (256 groups) 1: 88, 2: 98, 4: 109; 64 of U[1K, 32K] (512 groups) 2: 692, 4: 667, 8: 680; 4 of 32768
-        // (32 groups) 8: 96, 9: 97, 10: 125; 8 of U[128, 8192] (64 groups) 2: 56, 4: 42, 6: 37, 8: 39; one of
-        // 32768 (8 groups) 8: 55, 16: 39, 38: 42, 64: 54; 48 chains of U[1, 8000], e5m2, 3 kv heads (144
-        // groups) 2: 55, 4: 45, 8: 49.
+        // Blocks of 128 rows, two per SM. With fewer (sequence, kv head, row tile) groups than SMs: as many
+        // splits as fit at once (a few blocks more would cost a second wave), at least four of 1024 tokens
+        // or more, which balance sequences of different lengths. With enough groups for two blocks per SM:
+        // none, because the partial results of 128 rows cost as much traffic as 130 cached tokens of one
+        // head and the join is a second launch; the longest sequences start first. In between, a cap of 8192
+        // tokens. Measured, 8 or 16 drafted tokens x 4 query heads, splits -> us (bf16 unless noted): 64
+        // sequences of U[1K, 32K] (512 groups) 1: 631, 2: 643, 4: 639, 8: 671, e4m3 1: 434, 2: 470, 4: 483;
+        // 32 of 4096 (256 groups) 1: 88, 2: 98, 4: 109; 4 of 32768 (32 groups) 8: 96, 9: 97, 10: 125; 8 of
+        // U[128, 8192] (64 groups) 2: 57, 4: 41, 6: 37, 8: 38; one of 32768 (8 groups) 8: 55, 16: 39, 38: 42,
+        // 64: 54; 48 chains of U[1, 8000], e5m2, 3 kv heads (144 groups) 2: 50, 4: 39, 6: 48.
         const long long groups = (long long)B * Hkv * ((rows + 127) / 128);
-        long long splits = 1;
+        long long splits = 1, most = 65536;
         if (groups < num_sms) {
             const long long balance = lmax / 1024 < 4 ? lmax / 1024 : 4;
             splits = 2LL * num_sms / groups;
             if (splits < balance) splits = balance;
         }
+        if (groups < 2LL * num_sms) most = 8192;
         c = (lmax + splits - 1) / splits;
         if (c < 128) c = 128;
-        if (c > 8192) c = 8192;
+        if (c > most) c = most;
     } else {
-        // Blocks of 16 rows, up to four per SM. Many tokens: about 12 items per SM, assuming half-full page
+        // Blocks of 16 rows, up to four per SM. Many tokens: about 6 items per SM, assuming half-full page
         // tables; fewer: two items per SM, up to 2048 tokens each. Measured, 4 drafted tokens x 4 query heads,
-        // bf16, splits -> us: 64 sequences of U[1K, 32K] 8: 657, 11: 671, 16: 695; 8 of U[128, 8192] 2: 63,
-        // 4: 44, 8: 43, 16: 51; one of 32768 8: 62, 16: 42, 32: 43, 64: 60; one of 1024 1: 23, 2: 18, 8: 15.
+        // bf16 / e4m3, splits -> us: 64 sequences of U[1K, 32K] 2: 619 / 367, 4: 623 / 383, 8: 652 / 394,
+        // 16: 694 / 454 (one token each 2: 609 / 342, 4: 598 / 349, 8: 608 / 346); 8 of U[128, 8192] 4: 44 / 42,
+        // 8: 40 / 37, 16: 51 / 43; one of 32768 8: 62 / 59, 16: 42 / 39, 32: 43 / 37, 64: 60 / 42; one of 1024
+        // 1: 23, 2: 18, 8: 15.
         const long long tokens = (long long)B * Hkv * lmax;
         c = (tokens + 4LL * num_sms - 1) / (4LL * num_sms) * 2;  // two items per SM
         if (c > 2048) c = 2048;
-        const long long many = (tokens / 2 + 12LL * num_sms - 1) / (12LL * num_sms);
+        const long long many = (tokens / 2 + 6LL * num_sms - 1) / (6LL * num_sms);
         if (c < many) c = many;
         if (c < 128) c = 128;
-        if (c > 8192) c = 8192;
+        if (c > 16384) c = 16384;
     }
     c = (c + 63) / 64 * 64;
     const long long whole = (lmax + 63) / 64 * 64;

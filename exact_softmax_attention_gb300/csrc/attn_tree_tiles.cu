@@ -193,14 +193,19 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     using L = TileLayout<D, FMT>;
     constexpr bool F8 = L::kF8;
     constexpr int NS = L::kStages;
-    const int HG = p.Hkv * p.groups;
-    const int b = blockIdx.y, split = (int)(blockIdx.x / (unsigned)HG), hg = (int)(blockIdx.x % (unsigned)HG);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    int b, split, hg;
+    if (!tree_item(p, reinterpret_cast<int*>(smem), b, split, hg)) return;
     const int kvh = hg / p.groups, r0 = (hg % p.groups) * kTileRows;
     TreeSeq s;
     if (!tree_seq(p, b, s)) return;
     const int R = min(kTileRows, s.n * p.G - r0);  // rows of this tile
     if (R <= 0) return;
     const int nsplit = cdiv(s.len, p.chunk);
+    if (split < 0)
+        split = nsplit > 0 ? nsplit - 1 : 0;
+    else if (p.full_rows >= 0 && split >= nsplit - 1)
+        return;  // the last split has its own block
     const int t_begin = split * p.chunk;
     auto out_row = [&](int r) {
         const int i = (r0 + r) / p.G;
@@ -219,7 +224,6 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     const int t_end = min(s.len, t_begin + p.chunk);
     const int tiles = cdiv(t_end - t_begin, kTileKeys);
 
-    extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {  // the swizzles count from such boundaries
         if (threadIdx.x == 0) atomicCAS(p.status, 0, kDevTimeout);
         return;
@@ -740,10 +744,8 @@ cudaError_t launch_tiles(TreeParams p, const TreeTmaps& tm, cudaStream_t stream)
     cudaError_t e = ensure_smem_attr(tree_tile_kernel<D, FMT>, bytes, attr_set);
     if (e != cudaSuccess) return e;
     p.groups = (int)(((long long)p.max_q * p.G + kTileRows - 1) / kTileRows);
-    const long long x = (long long)p.max_splits * p.Hkv * p.groups;
-    if (x > INT32_MAX) return cudaErrorInvalidConfiguration;
-    return launch_kernel(tree_tile_kernel<D, FMT>, dim3((unsigned)x, (unsigned)p.B), TileLayout<D, FMT>::kThreads, bytes, stream,
-                         false, p, tm.k, tm.v);
+    const dim3 grid = tree_grid(p);
+    return launch_kernel(tree_tile_kernel<D, FMT>, grid, TileLayout<D, FMT>::kThreads, bytes, stream, false, p, tm.k, tm.v);
 }
 
 template <int D>

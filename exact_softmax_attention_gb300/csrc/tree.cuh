@@ -21,6 +21,10 @@ struct TreeParams {
     int B, T, max_q, Hq, Hkv, G, page_size, max_pages, num_pages;
     int chunk, max_splits;   // tokens per split (a multiple of 64), splits of the longest sequence
     int groups;              // row groups per kv head (rows: drafted token x query head of the kv head)
+    // Work order (tree_grid): grid rows y < full_rows list the splits of sequence y before its last one, the
+    // rows after them the last split of every sequence, in decreasing length when ranked. full_rows < 0:
+    // row y holds all splits of sequence y.
+    int full_rows, ranked;
     // q is multiplied by q_sign (-1, 0, 1) and the scores by |scale|, so that masking and maxima
     // work on scores that grow with q.k for every finite scale (scale 0: q_sign 0, factor 1)
     float q_sign, scale, scale_log2;  // |scale| (key descale included), times log2(e)
@@ -46,6 +50,22 @@ constexpr int kTreeTileRows = 17;
 cudaError_t launch_attn_tree(const TreeParams& p, const TreeTmaps& tm, int d, int kv_format, cudaStream_t stream);
 cudaError_t launch_tree_tiles(const TreeParams& p, const TreeTmaps& tm, int d, int kv_format, cudaStream_t stream);
 inline bool tree_takes_tiles(long long rows) { return rows >= kTreeTileRows; }
+
+// Grid of a split kernel; sets the work order. The last splits are shorter in general: started after all
+// others, the longest first, they fill the SMs that the last full-length ones leave idle.
+inline dim3 tree_grid(TreeParams& p) {
+    const long long HG = (long long)p.Hkv * p.groups;
+    const long long X = (p.max_splits > 1 ? p.max_splits - 1 : 1) * HG;
+    const long long full = p.max_splits > 1 ? p.B : 0, part = ((long long)p.B * HG + X - 1) / X;
+    if (full + part <= 65535) {
+        p.full_rows = (int)full;
+        p.ranked = p.B <= 256;  // (each block of that part ranks the lengths)
+        return dim3((unsigned)X, (unsigned)(full + part));
+    }
+    p.full_rows = -1;
+    p.ranked = 0;
+    return dim3((unsigned)(p.max_splits * HG), (unsigned)p.B);
+}
 
 // Tokens per split and splits of the longest sequence (lmax tokens).
 void tree_plan(int B, int Hkv, int rows, long long lmax, int num_splits, int num_sms, int* chunk, int* max_splits);

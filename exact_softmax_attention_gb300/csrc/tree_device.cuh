@@ -42,6 +42,44 @@ __device__ __forceinline__ bool tree_seq(const TreeParams& p, int b, TreeSeq& s)
     return true;
 }
 
+// Work item of a block: sequence, split (-1: the sequence's last one) and head group (kv head * groups +
+// row group). False (for the whole block) when it has none. scratch: 2 B + 1 ints of shared memory when
+// ranked; every thread calls it.
+__device__ __forceinline__ bool tree_item(const TreeParams& p, int* scratch, int& b, int& split, int& hg) {
+    const int HG = p.Hkv * p.groups;
+    if (p.full_rows < 0 || (int)blockIdx.y < p.full_rows) {
+        b = blockIdx.y;
+        split = (int)(blockIdx.x / (unsigned)HG);
+        hg = (int)(blockIdx.x % (unsigned)HG);
+        return true;
+    }
+    const long long j = (long long)(blockIdx.y - p.full_rows) * gridDim.x + blockIdx.x;
+    if (j >= (long long)p.B * HG) return false;
+    hg = (int)(j % HG);
+    b = (int)(j / HG);
+    split = -1;
+    if (p.ranked) {
+        // the sequence whose last split has rank b in decreasing length (ties: the lower one first)
+        const int max_len = p.max_pages * p.page_size;
+        int* found = scratch + p.B;
+        for (int t = threadIdx.x; t < p.B; t += blockDim.x) {
+            const int len = min(max(__ldg(p.seqlens + t), 0), max_len), ns = cdiv(len, p.chunk);
+            scratch[t] = len - (ns > 0 ? ns - 1 : 0) * p.chunk;
+        }
+        __syncthreads();
+        for (int t = threadIdx.x; t < p.B; t += blockDim.x) {
+            const int mine = scratch[t];
+            int rank = 0;
+            for (int u = 0; u < p.B; ++u) rank += scratch[u] > mine || (scratch[u] == mine && u < t);
+            if (rank == b) *found = t;
+        }
+        __syncthreads();
+        b = *found;
+        __syncthreads();  // the scratch has other uses
+    }
+    return true;
+}
+
 // Bits of the keys kb .. kb + 63 that drafted token i of the sequence sees. row: its mask words, or
 // nullptr for a chain.
 __device__ __forceinline__ unsigned long long tree_window(const unsigned long long* row, int words, int i, int ctx, int len,
