@@ -7,6 +7,11 @@
 // bounded by memory. What a short call costs is the chain of dependent loads from the packed
 // row to its page (offsets, length, page table); the rows themselves do not depend on it, so each
 // thread loads its first item before the places are known.
+//
+// Measured: 264 K tokens (8 heads of 128) from e4m3 to bf16 rows in 248 us, 0.97 of the measured copy
+// rate; 131072 tokens to a bf16 cache 170 us (0.93), to e4m3 149 us (0.80), with rotation 175 us (0.68): the
+// 8-bit writes are bounded by instruction issue (about ten instructions per element for the rotation, the
+// quotient and the conversion); 64 tokens 4.1 us.
 #include "attn.h"
 #include "launch.cuh"
 #include "rows.cuh"

@@ -7,7 +7,11 @@
 // (transpose). The operator moves each element once in and once out and computes three
 // multiply-adds per pair: it is bounded by memory, and the angles must not cost more than that.
 // One block takes a few tokens, computes their cosines and sines once into shared memory (shared by
-// all heads), and streams the heads through 16-byte loads and stores.
+// all heads), and streams the heads through 16-byte loads and stores, the next item's loads ahead of
+// this one's stores. Measured: 18432 rows of 40 bf16 heads of 128 in 61.8 us, 6110 GB/s, 0.90 of the
+// measured copy rate (65536 rows 0.99); 8192 rows of 32 fp32 heads, 64 of 192 columns rotated, 0.94;
+// 64 rows 3.6 us. (Threads that keep their head and columns over the tokens, as in the cache writes,
+// need more registers and gave 65 and 74 us for the first two.)
 #include "attn.h"
 #include "launch.cuh"
 #include "rows.cuh"

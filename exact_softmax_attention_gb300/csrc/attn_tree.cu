@@ -25,6 +25,9 @@ namespace {
 // up to 16 rows per kv head the kernel is bounded by the cache reads, so a wider product would
 // only add work on padding. 8-bit codes become f16 pairs in registers (exact); the order of d
 // inside both products is permuted so that one 16-byte shared load feeds several products.
+// Measured, 64 sequences of U[1K, 32K] tokens, 4 query heads on each of 8 kv heads: one token each 604 us
+// (7140 GB/s, 1.05 of the measured copy rate, which also writes), four 629 us; e4m3 342 us (6300 GB/s) and
+// 370 us, where the conversions and the shared loads of the products take over.
 
 constexpr int kWarps = 4;
 constexpr int kGroup = 16;

@@ -33,15 +33,14 @@
 // What bounds it. 64 keys of bf16 K and V of a head are 32 KB; the products take 640 clocks of the SM
 // (S 8 x 48, bound by the 6 KB of shared memory that each reads, P V 4 x 64). With up to 128 rows the bf16
 // form is bounded by the memory: 16 drafted tokens x 4 query heads over 64 sequences of U[1K, 32K] tokens
-// take 682 us, 6350 GB/s, 0.94 of the measured copy rate (page size 64: 658 us; sequences of equal
-// length: 6980 GB/s). 8-bit caches have half the bytes for the same products: 512 us, 4250 GB/s (0.63),
-// bounded by the tensor pipe and the chain S -> softmax -> P V of two buffers. More than 128 rows: every
-// further tile reads the cache again through the L2 (64 drafted tokens: 1060 us, 1045 TFLOP/s, 0.54 of
-// the measured bf16 rate).
-// Tried and slower, same case, bf16 / 8-bit (first kernel of this form 698 / 584): Q in tensor memory with
-// one S buffer 713 / 753, or with S in steps of 32 keys 813 / 844 (a product takes 32 clocks at least); one
-// S buffer with two separate P 685 / 531; one block of 512 threads per SM with two streams of even and
-// odd tiles 696 / 721.
+// take 640 us, 6770 GB/s, 1.00 of the measured copy rate (8 tokens with page size 64: 618 us; page size 1:
+// 770 us). 8-bit caches have half the bytes for the same products: 439 us, 4950 GB/s (0.73), bounded by the
+// tensor pipe, the shared memory and the chain S -> softmax -> P V of two buffers. More than 128 rows:
+// every further tile reads the cache again through the L2 (64 drafted tokens: 918 us, 0.71 of the floor).
+// Tried and slower (same case, bf16 / 8-bit, before the work order; this form then took 698 / 584, with S and
+// P V in a thread each and raw K 685 / 511): Q in tensor memory with one S buffer 713 / 753, or with S in
+// steps of 32 keys 813 / 844 (a product takes 32 clocks at least); one S buffer with two separate P
+// 685 / 531; one block of 512 threads per SM with two streams of even and odd tiles 696 / 721.
 #include "launch.cuh"
 #include "tree_device.cuh"
 
