@@ -613,6 +613,7 @@ attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const v
     if ((long long)p.max_splits * Hkv * ((rows + 15) / 16) > INT32_MAX) return ATTN_ERR_BAD_SHAPE;  // grid columns
     // a scale of 0 (or one that rounds to 0) makes every score 0: q times 0, factor 1
     const double factor = (float)fabs(score_scale) > 0 ? fabs(score_scale) : 0.0;
+    p.num_sms = ds->num_sms;
     p.q_sign = factor == 0 ? 0.0f : (score_scale < 0 ? -1.0f : 1.0f);
     p.scale = factor == 0 ? 1.0f : (float)factor;
     p.scale_log2 = (float)((factor == 0 ? 1.0 : factor) * 1.4426950408889634);

@@ -24,7 +24,7 @@ struct TreeParams {
     // Work order (tree_grid): grid rows y < full_rows list the splits of sequence y before its last one, the
     // rows after them the last split of every sequence, in decreasing length when ranked. full_rows < 0:
     // row y holds all splits of sequence y.
-    int full_rows, ranked;
+    int full_rows, ranked, num_sms;
     // q is multiplied by q_sign (-1, 0, 1) and the scores by |scale|, so that masking and maxima
     // work on scores that grow with q.k for every finite scale (scale 0: q_sign 0, factor 1)
     float q_sign, scale, scale_log2;  // |scale| (key descale included), times log2(e)
@@ -59,7 +59,9 @@ inline dim3 tree_grid(TreeParams& p) {
     const long long full = p.max_splits > 1 ? p.B : 0, part = ((long long)p.B * HG + X - 1) / X;
     if (full + part <= 65535) {
         p.full_rows = (int)full;
-        p.ranked = p.B <= 256;  // (each block of that part ranks the lengths)
+        // Each block of that part ranks the lengths, which costs it about a microsecond: not when all
+        // blocks start at once anyway.
+        p.ranked = p.B <= 256 && p.B > 1 && X * (full + part) > 2LL * p.num_sms;
         return dim3((unsigned)X, (unsigned)(full + part));
     }
     p.full_rows = -1;

@@ -292,6 +292,17 @@ def test_queries_of_any_range(A, fmt, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt,n", [("e4m3", 30), ("bf16", 30), ("bf16", 3)])
+def test_vanishing_queries_and_scales(A, fmt, n):
+    """Scores far below the range of fp32: a plain mean over what each row sees."""
+    c = Case(fmt, 4, 2, 64, 16, [n], [n + 70], "any", 25)
+    c.q.mul_(2.0**-115)
+    c.run(A, 2, 2.0**-60)
+    assert A.attn_get_device_status() == 0
+    c.check(2.0**-60)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("n", [2, 30])
 @pytest.mark.parametrize("threshold", [0.0, 60.0])
