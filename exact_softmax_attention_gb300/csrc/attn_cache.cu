@@ -9,9 +9,9 @@
 // thread loads its first item before the places are known.
 //
 // Measured: 264 K tokens (8 heads of 128) from e4m3 to bf16 rows in 248 us, 0.97 of the measured copy
-// rate; 131072 tokens to a bf16 cache 170 us (0.93), to e4m3 149 us (0.80), with rotation 175 us (0.68): the
+// rate; 131072 tokens to a bf16 cache 169 us (0.93), to e4m3 143 us (0.83), with rotation 163 us (0.73): the
 // 8-bit writes are bounded by instruction issue (about ten instructions per element for the rotation, the
-// quotient and the conversion); 64 tokens 4.1 us.
+// quotient and the conversion); 64 tokens 4.2 us.
 #include "attn.h"
 #include "launch.cuh"
 #include "rows.cuh"
@@ -75,18 +75,20 @@ __device__ __forceinline__ void fp8x2_values(uint32_t two, float& lo, float& hi)
 
 // x[e] / d rounded to fp32, with inv the rounded 1 / d: the product with inv, corrected by the exact
 // remainder (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor",
-// 1990); far beyond the 8-bit range, where the remainder may overflow or x is not finite, the product alone
-// saturates or is NaN. inv = 0 asks for the division. The write is bounded by instruction issue: with a
-// division per element it took 1.4 times as long.
+// 1990). Far beyond the 8-bit range, where the remainder may overflow or x is not finite, and where inv = 0
+// asks for it, by division. The write is bounded by instruction issue: with a division per element it took
+// 1.4 times as long.
 template <int V>
 __device__ __forceinline__ void divide(float (&x)[V], float d, float inv) {
-    if (inv != 0.0f) {
+    float q[V], top = 0.0f;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float q = x[e] * inv;
-            const float c = fmaf(-fmaf(q, d, -x[e]), inv, q);  // (in this order -0 stays -0)
-            x[e] = fabsf(q) < 1e6f ? c : q;
-        }
+    for (int e = 0; e < V; ++e) {
+        q[e] = x[e] * inv;
+        top = fmaxf(top, fabsf(q[e]));
+    }
+    if (inv != 0.0f && top < 1e6f) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[e] = fmaf(-fmaf(q[e], d, -x[e]), inv, q[e]);  // (in this order -0 stays -0)
     } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) x[e] /= d;

@@ -35,32 +35,52 @@ __device__ __forceinline__ bool item_cols(const RopeCols& c, int j, int& a, int&
     return false;
 }
 
+// N neighbouring cosines or sines by loads as wide as they allow (aligned to min(16, 4 N) bytes).
+template <int N>
+__device__ __forceinline__ void load_angles(const float* p, float (&x)[N]) {
+    if constexpr (N >= 4) {
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(p + e);
+            x[e] = w.x, x[e + 1] = w.y, x[e + 2] = w.z, x[e + 3] = w.w;
+        }
+    } else if constexpr (N == 2) {
+        const float2 w = *reinterpret_cast<const float2*>(p);
+        x[0] = w.x, x[1] = w.y;
+    } else {
+        x[0] = *p;
+    }
+}
+
 // Rotate the pairs of item j; cs and sn: cosines and sines of the token, one per pair.
 template <int V>
 __device__ __forceinline__ void rotate_item(float (&xa)[V], float (&xb)[V], const RopeCols& cols, int j, const float* cs,
                                             const float* sn) {
     if (V == 1 || !cols.interleaved) {
-        const float *c = cs + V * j, *s = sn + V * j;
+        float c[V], s[V];
+        load_angles<V>(cs + V * j, c);
+        load_angles<V>(sn + V * j, s);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const float u = xa[e], w = xb[e];
             xa[e] = u * c[e] - w * s[e];
             xb[e] = u * s[e] + w * c[e];
         }
-    } else {  // pairs of adjacent columns: V / 2 in each part
+    } else if constexpr (V > 1) {  // pairs of adjacent columns: V / 2 in each part
         const int first = V / 2 * j, second = first + cols.rot / 4;
+        auto turn = [&](float(&x)[V], int at) {
+            float c[V / 2], s[V / 2];
+            load_angles<V / 2>(cs + at, c);
+            load_angles<V / 2>(sn + at, s);
 #pragma unroll
-        for (int e = 0; e + 1 < V; e += 2) {
-            const float u = xa[e], w = xa[e + 1], c = cs[first + e / 2], s = sn[first + e / 2];
-            xa[e] = u * c - w * s;
-            xa[e + 1] = u * s + w * c;
-        }
-#pragma unroll
-        for (int e = 0; e + 1 < V; e += 2) {
-            const float u = xb[e], w = xb[e + 1], c = cs[second + e / 2], s = sn[second + e / 2];
-            xb[e] = u * c - w * s;
-            xb[e + 1] = u * s + w * c;
-        }
+            for (int e = 0; e < V / 2; ++e) {
+                const float u = x[2 * e], w = x[2 * e + 1];
+                x[2 * e] = u * c[e] - w * s[e];
+                x[2 * e + 1] = u * s[e] + w * c[e];
+            }
+        };
+        turn(xa, first);
+        turn(xb, second);
     }
 }
 
