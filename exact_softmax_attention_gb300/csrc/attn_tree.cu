@@ -40,7 +40,8 @@ struct SmallLayout {
     static constexpr int kTile = kGroup * kRow;    // one K or V stage of a warp
     static constexpr int kChunks = kRow / 16;
     static constexpr int kRing = kWarps * kStages * 2 * kTile;
-    static constexpr int kMerge = (kWarps * 16 * D + 2 * kWarps * 16) * 4;
+    static constexpr int kRowO = D + 4;            // floats of a merged row: eight rows' columns in different banks
+    static constexpr int kMerge = (kWarps * 16 * kRowO + 2 * kWarps * 16) * 4;
     static constexpr int kBytes = kRing > kMerge ? kRing : kMerge;
 };
 
@@ -117,6 +118,44 @@ __global__ void __launch_bounds__(kWarps * 32) tree_small_kernel(const TreeParam
     const unsigned long long* mrow0 = p.mask ? p.mask + (long long)(s.q0 + i0) * p.mask_words : nullptr;
     const unsigned long long* mrow1 = p.mask ? p.mask + (long long)(s.q0 + i1) * p.mask_words : nullptr;
 
+    // ---- the warp's ring: token groups t_begin + 16 (warp + 4 i)
+    const uint32_t ring = smem_u32(smem) + warp * kStages * 2 * L::kTile;
+    const int* pt = p.page_table + (long long)b * p.max_pages;
+    const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache);
+    const uint8_t* vc = static_cast<const uint8_t*>(p.v_cache);
+    constexpr int kRowsPerIter = 32 / L::kChunks;
+    const int my_chunk = lane % L::kChunks, my_row = lane / L::kChunks;
+    const long long row_bytes = (long long)p.Hkv * L::kRow;
+    const int col = kvh * L::kRow + my_chunk * 16;
+    const int total = cdiv(t_end - t_begin, kGroup);
+    const int mine = total > warp ? cdiv(total - warp, kWarps) : 0;
+    auto row_of = [&](int i) {  // cache row of the lane's token of group i; no token or a bad page: zeros
+        const int tok = t_begin + kGroup * (warp + kWarps * i) + (lane & 15);
+        return i < mine && tok < t_end ? cache_row(p, pt, tok) : -1;
+    };
+    auto issue = [&](int i, int row) {
+        const uint32_t kd = ring + (i % kStages) * 2 * L::kTile, vd = kd + L::kTile;
+#pragma unroll
+        for (int it = 0; it < kGroup / kRowsPerIter; ++it) {
+            const int r = it * kRowsPerIter + my_row;
+            const int rr = __shfl_sync(0xffffffffu, row, r);
+            const long long off = rr >= 0 ? rr * row_bytes + col : 0;
+            const uint32_t n = rr >= 0 ? 16u : 0u;
+            cp_async16(kd + swz_chunk<L::kChunks>(r, my_chunk), kc + off, n);
+            cp_async16(vd + swz_chunk<L::kChunks>(r, my_chunk), vc + off, n);
+        }
+    };
+    // (the page table is read a group ahead, so that a copy does not wait for it)
+    int rows_at[kStages];
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) rows_at[i] = row_of(i);
+    int next_row = rows_at[kStages - 1];
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i < mine) issue(i, rows_at[i]);
+        cp_async_commit();
+    }
+
     // ---- query fragments. 8-bit caches: column 2 qd + e of k-step kk is d = (D/4) qd + 4 kk + e,
     // column 2 qd + 8 + e is that + 2
     uint32_t aq[D / 16][4];
@@ -139,47 +178,19 @@ __global__ void __launch_bounds__(kWarps * 32) tree_small_kernel(const TreeParam
         }
     }
 
-    // ---- the warp's ring: token groups t_begin + 16 (warp + 4 i)
-    const uint32_t ring = smem_u32(smem) + warp * kStages * 2 * L::kTile;
-    const int* pt = p.page_table + (long long)b * p.max_pages;
-    const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache);
-    const uint8_t* vc = static_cast<const uint8_t*>(p.v_cache);
-    constexpr int kRowsPerIter = 32 / L::kChunks;
-    const int my_chunk = lane % L::kChunks, my_row = lane / L::kChunks;
-    const long long row_bytes = (long long)p.Hkv * L::kRow;
-    const int col = kvh * L::kRow + my_chunk * 16;
-    const int total = cdiv(t_end - t_begin, kGroup);
-    const int mine = total > warp ? cdiv(total - warp, kWarps) : 0;
-    auto issue = [&](int i) {
-        const int tok = t_begin + kGroup * (warp + kWarps * i) + (lane & 15);
-        const int row = tok < t_end ? cache_row(p, pt, tok) : -1;  // no token or a bad page: zeros
-        const uint32_t kd = ring + (i % kStages) * 2 * L::kTile, vd = kd + L::kTile;
-#pragma unroll
-        for (int it = 0; it < kGroup / kRowsPerIter; ++it) {
-            const int r = it * kRowsPerIter + my_row;
-            const int rr = __shfl_sync(0xffffffffu, row, r);
-            const long long off = rr >= 0 ? rr * row_bytes + col : 0;
-            const uint32_t n = rr >= 0 ? 16u : 0u;
-            cp_async16(kd + swz_chunk<L::kChunks>(r, my_chunk), kc + off, n);
-            cp_async16(vd + swz_chunk<L::kChunks>(r, my_chunk), vc + off, n);
-        }
-    };
-
     constexpr int NH = GN / 8;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
     float oacc[NH][D / 16][4] = {};
     const float sl2 = p.scale_log2;
     const int lm_row = (lane & 7) + ((lane >> 4) << 3), lm_par = (lane >> 3) & 1;
 
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-        if (i < mine) issue(i);
-        cp_async_commit();
-    }
     for (int i = 0; i < mine; ++i) {
         cp_async_wait<kStages - 2>();
         __syncwarp();
-        if (i + kStages - 1 < mine) issue(i + kStages - 1);
+        if (i + kStages - 1 < mine) {
+            issue(i + kStages - 1, next_row);
+            next_row = row_of(i + kStages);
+        }
         cp_async_commit();
         const uint32_t kt = ring + (i % kStages) * 2 * L::kTile, vt = kt + L::kTile;
         const int g = t_begin + kGroup * (warp + kWarps * i);
@@ -334,7 +345,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_small_kernel(const TreeParam
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
     __syncthreads();  // every warp is done with its ring
     float* sm_o = reinterpret_cast<float*>(smem);
-    float* sm_m = sm_o + kWarps * GN * D;
+    float* sm_m = sm_o + kWarps * GN * L::kRowO;
     float* sm_l = sm_m + kWarps * GN;
     if (qd == 0) {
         sm_m[warp * GN + g0] = m0;
@@ -350,42 +361,50 @@ __global__ void __launch_bounds__(kWarps * 32) tree_small_kernel(const TreeParam
         for (int mt = 0; mt < D / 16; ++mt) {
             // rows of O^T: d, in the permuted order of the 8-bit products
             const int d0 = F8 ? (D / 8) * g0 + 2 * mt : mt * 16 + g0, d1 = F8 ? d0 + 1 : d0 + 8;
-            float* base = sm_o + (warp * GN + nh * 8 + 2 * qd) * D;
+            float* base = sm_o + (warp * GN + nh * 8 + 2 * qd) * L::kRowO;
             base[d0] = oacc[nh][mt][0];
-            base[D + d0] = oacc[nh][mt][1];
+            base[L::kRowO + d0] = oacc[nh][mt][1];
             base[d1] = oacc[nh][mt][2];
-            base[D + d1] = oacc[nh][mt][3];
+            base[L::kRowO + d1] = oacc[nh][mt][3];
         }
     __syncthreads();
     const bool odd = odd_v != 0;
-    for (int x = threadIdx.x; x < R * D; x += blockDim.x) {
-        const int r = x / D, d = x - r * D;
+    // four neighbouring elements per thread, so that the rows of a block take few rounds of latency
+    constexpr int kPerRow = D / 4, kAtOnce = kWarps * 32 / kPerRow;
+    const int d0 = threadIdx.x % kPerRow * 4;
+#pragma unroll
+    for (int k = 0; k < GN / kAtOnce; ++k) {
+        const int r = k * kAtOnce + threadIdx.x / kPerRow;
+        if (r >= R) break;
         float mm = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w * GN + r]);
-        float ll = 0.0f, acc = 0.0f;
+        float ll = 0.0f, acc[4] = {};
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             // a warp without a visible key has m = -inf and only zeros (or NaN, which has to stay)
             const float mw = sm_m[w * GN + r];
             const float f = mw == -INFINITY ? 1.0f : ex2_mufu((mw - mm) * sl2);
             ll += f * sm_l[w * GN + r];
-            acc += f * sm_o[(w * GN + r) * D + d];
+            const float4 o = *reinterpret_cast<const float4*>(sm_o + (w * GN + r) * L::kRowO + d0);
+            acc[0] += f * o.x, acc[1] += f * o.y, acc[2] += f * o.z, acc[3] += f * o.w;
         }
         if (odd) {
             const int i = (r0 + r) / p.G;
-            acc += nonfinite_sum<FMT>(p, pt, p.mask ? p.mask + (long long)(s.q0 + i) * p.mask_words : nullptr, i, s,
-                                      max(t_begin, s.ctx / kGroup * kGroup), t_end, kvh, D, d);
+            for (int e = 0; e < 4; ++e)
+                acc[e] += nonfinite_sum<FMT>(p, pt, p.mask ? p.mask + (long long)(s.q0 + i) * p.mask_words : nullptr, i, s,
+                                             max(t_begin, s.ctx / kGroup * kGroup), t_end, kvh, D, d0 + e);
         }
-        const float o = ll == 0.0f ? 0.0f : acc / ll * p.v_descale;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = ll == 0.0f ? 0.0f : acc[e] / ll * p.v_descale;
         const float lse = ll == 0.0f ? -INFINITY : mm * p.scale + logf(ll);
         const long long orow = out_row(r);
         if (nsplit == 1) {
-            p.o[orow * D + d] = __float2bfloat16(o);
-            if (d == 0) p.lse[orow] = lse;
+            *reinterpret_cast<uint2*>(p.o + orow * D + d0) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+            if (d0 == 0) p.lse[orow] = lse;
         } else {
-            p.ws_o[(orow * p.max_splits + split) * D + d] = o;
-            if (d == 0) p.ws_lse[orow * p.max_splits + split] = lse;
+            *reinterpret_cast<float4*>(p.ws_o + (orow * p.max_splits + split) * D + d0) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (d0 == 0) p.ws_lse[orow * p.max_splits + split] = lse;
         }
     }
 }
@@ -405,28 +424,40 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p) {
     const int ns = cdiv(s.len, p.chunk);
     if (ns <= 1) return;
     const long long row = (long long)s.q0 * p.Hq + r;
+    constexpr int PER = D / 32;
     const float* wl = p.ws_lse + row * p.max_splits;
-    const float* wo = p.ws_o + row * p.max_splits * D;
-    float mx = -INFINITY;
-    for (int i = lane; i < ns; i += 32) mx = fmaxf(mx, wl[i]);
+    const float* wo = p.ws_o + row * p.max_splits * D + lane * PER;
+    const float first = lane < ns ? wl[lane] : -INFINITY;  // of the first 32 splits, mostly all there are
+    float mx = first;
+    for (int i = lane + 32; i < ns; i += 32) mx = fmaxf(mx, wl[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    // a split that the row sees nothing of has -inf and weight 0; a NaN stays
+    // a split that the row sees nothing of has -inf, zeros as its output and weight 0; a NaN stays
     const float base = mx == -INFINITY ? 0.0f : mx;
-    float sum = 0.0f;
-    for (int i = lane; i < ns; i += 32) sum += expf(wl[i] - base);
+    float sum = expf(first - base);
+    for (int i = lane + 32; i < ns; i += 32) sum += expf(wl[i] - base);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    constexpr int PER = D / 32;
     float acc[PER] = {};
     if (sum != 0.0f) {
         const float lse = base + logf(sum);
-        for (int i = 0; i < ns; ++i) {
-            const float li = wl[i];
-            if (li == -INFINITY) continue;  // its partial output is zeros
-            const float w = expf(li - lse);
+        for (int at = 0; at < ns; at += 32) {
+            const float weight = at + lane < ns ? expf((at == 0 ? first : wl[at + lane]) - lse) : 0.0f;
+            const int n = min(32, ns - at);
+            constexpr int kAhead = 4;  // loads in flight
+            for (int i = 0; i < n; i += kAhead) {
+                float v[kAhead][PER];
 #pragma unroll
-            for (int e = 0; e < PER; ++e) acc[e] += w * wo[(long long)i * D + lane * PER + e];
+                for (int x = 0; x < kAhead; ++x)
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) v[x][e] = i + x < n ? wo[(long long)(at + i + x) * D + e] : 0.0f;
+#pragma unroll
+                for (int x = 0; x < kAhead; ++x) {
+                    const float w = __shfl_sync(0xffffffffu, weight, i + x);
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) acc[e] += w * v[x][e];
+                }
+            }
         }
         if (lane == 0) p.lse[row] = lse;
     } else if (lane == 0) {
