@@ -609,11 +609,11 @@ attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const v
     p.page_size = page_size;
     p.max_pages = max_pages_per_seq;
     p.num_pages = num_pages;
-    attn::tree_plan(B, Hkv, (int)rows, lmax, num_splits, ds->num_sms, &p.chunk, &p.max_splits);
+    p.num_sms = ds->num_sms;
+    attn::tree_plan(p, d, f8, num_splits);
     if ((long long)p.max_splits * Hkv * ((rows + 15) / 16) > INT32_MAX) return ATTN_ERR_BAD_SHAPE;  // grid columns
     // a scale of 0 (or one that rounds to 0) makes every score 0: q times 0, factor 1
     const double factor = (float)fabs(score_scale) > 0 ? fabs(score_scale) : 0.0;
-    p.num_sms = ds->num_sms;
     p.q_sign = factor == 0 ? 0.0f : (score_scale < 0 ? -1.0f : 1.0f);
     p.scale = factor == 0 ? 1.0f : (float)factor;
     p.scale_log2 = (float)((factor == 0 ? 1.0 : factor) * 1.4426950408889634);
@@ -639,12 +639,13 @@ attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const v
         cudaMemPool_t pool = nullptr;
         if ((st = device_pool(ds, &pool)) != ATTN_OK) return st;
         const size_t n = (size_t)T * Hq * p.max_splits;
-        if (cudaMallocFromPoolAsync(&ws, n * ((size_t)d + 1) * sizeof(float), pool, s) != cudaSuccess) {
+        if (cudaMallocFromPoolAsync(&ws, (n * ((size_t)d + 1) + 1) * sizeof(float), pool, s) != cudaSuccess) {
             cudaGetLastError();  // (out of memory is no error of the next call)
             return ATTN_ERR_CUDA;
         }
         p.ws_o = reinterpret_cast<float*>(ws);
         p.ws_lse = p.ws_o + n * d;
+        p.ws_chunk = reinterpret_cast<int*>(p.ws_lse + n);
     }
     const cudaError_t e = attn::launch_attn_tree(p, tm, d, kv_format, s);
     if (ws) cudaFreeAsync(ws, s);

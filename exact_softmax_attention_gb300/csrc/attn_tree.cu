@@ -14,6 +14,8 @@
 #include "launch.cuh"
 #include "tree_device.cuh"
 
+#include <type_traits>
+
 namespace attn {
 namespace {
 
@@ -25,9 +27,11 @@ namespace {
 // up to 16 rows per kv head the kernel is bounded by the cache reads, so a wider product would
 // only add work on padding. 8-bit codes become f16 pairs in registers (exact); the order of d
 // inside both products is permuted so that one 16-byte shared load feeds several products.
-// Measured, 64 sequences of U[1K, 32K] tokens, 4 query heads on each of 8 kv heads: one token each 604 us
-// (7140 GB/s, 1.05 of the measured copy rate, which also writes), four 629 us; e4m3 342 us (6300 GB/s) and
-// 370 us, where the conversions and the shared loads of the products take over.
+// Measured, 64 sequences of U[1K, 32K] tokens, 4 query heads on each of 8 kv heads: one token each 597 us
+// (7220 GB/s, 1.06 of the measured copy rate, which also writes), four 608 us; e4m3 329 us (6550 GB/s) and
+// 353 us, where the conversions and the shared loads of the products take over. One sequence of 1000 tokens:
+// one token 7.4 us, four 10.3 us (before the page table was read a group ahead of the copies, and the merge and
+// the join had their loads side by side: 11.0 and 16.1).
 
 constexpr int kWarps = 4;
 constexpr int kGroup = 16;
@@ -72,26 +76,26 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[2]) {
 
 // GN: row slots that hold rows (8 or 16).
 template <int D, int GN, int FMT>
-__global__ void __launch_bounds__(kWarps * 32) tree_small_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, tree_small_blocks(D, FMT != ATTN_KV_BF16)) tree_small_kernel(const TreeParams p) {
     grid_dependents_launch();
     using L = SmallLayout<D, FMT>;
     constexpr bool F8 = FMT != ATTN_KV_BF16;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int odd_v;  // a V tile held a non-finite value that was taken out
-    int b, split, hg;
-    if (!tree_item(p, reinterpret_cast<int*>(smem), b, split, hg)) return;
+    int chunk, b, split, hg;
+    if (!tree_item(p, reinterpret_cast<int*>(smem), chunk, b, split, hg)) return;
     const int kvh = hg / p.groups, r0 = (hg % p.groups) * 16;
     TreeSeq s;
     if (!tree_seq(p, b, s)) return;
     const int R = min(16, s.n * p.G - r0);  // rows of this group
     if (R <= 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nsplit = cdiv(s.len, p.chunk);
+    const int nsplit = cdiv(s.len, chunk);
     if (split < 0)
         split = nsplit > 0 ? nsplit - 1 : 0;
     else if (p.full_rows >= 0 && split >= nsplit - 1)
         return;  // the last split has its own block
-    const int t_begin = split * p.chunk;
+    const int t_begin = split * chunk;
     // output row of local row r: (s.q0 + i) * Hq + kvh * G + g with (i, g) = divmod(r0 + r, G)
     auto out_row = [&](int r) {
         const int i = (r0 + r) / p.G;
@@ -107,7 +111,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_small_kernel(const TreeParam
         return;
     }
     if (t_begin >= s.len) return;
-    const int t_end = min(s.len, t_begin + p.chunk);
+    const int t_end = min(s.len, t_begin + chunk);
     if (threadIdx.x == 0) odd_v = 0;
     __syncthreads();
 
@@ -421,42 +425,45 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p) {
     const long long r = (long long)blockIdx.x * 4 + warp;
     grid_dependency_wait();
     if (!rows || r >= (long long)s.n * p.Hq) return;
-    const int ns = cdiv(s.len, p.chunk);
+    const int ns = cdiv(s.len, p.slots > 0 ? *p.ws_chunk : p.chunk);
     if (ns <= 1) return;
     const long long row = (long long)s.q0 * p.Hq + r;
     constexpr int PER = D / 32;
     const float* wl = p.ws_lse + row * p.max_splits;
     const float* wo = p.ws_o + row * p.max_splits * D + lane * PER;
-    const float first = lane < ns ? wl[lane] : -INFINITY;  // of the first 32 splits, mostly all there are
-    float mx = first;
-    for (int i = lane + 32; i < ns; i += 32) mx = fmaxf(mx, wl[i]);
+    typedef typename std::conditional<D == 128, float4, float2>::type Vec;
+    constexpr int kAhead = 8;  // loads in flight; the first ones do not wait for the weights
+    Vec v[kAhead];
+    auto load = [&](int i) {
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) v[x] = i + x < ns ? *reinterpret_cast<const Vec*>(wo + (long long)(i + x) * D) : Vec{};
+    };
+    load(0);
+    // of the first 64 splits, mostly all there are
+    const float l0 = lane < ns ? wl[lane] : -INFINITY, l1 = lane + 32 < ns ? wl[lane + 32] : -INFINITY;
+    float mx = fmaxf(l0, l1);
+    for (int i = lane + 64; i < ns; i += 32) mx = fmaxf(mx, wl[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     // a split that the row sees nothing of has -inf, zeros as its output and weight 0; a NaN stays
     const float base = mx == -INFINITY ? 0.0f : mx;
-    float sum = expf(first - base);
-    for (int i = lane + 32; i < ns; i += 32) sum += expf(wl[i] - base);
+    float sum = expf(l0 - base) + expf(l1 - base);
+    for (int i = lane + 64; i < ns; i += 32) sum += expf(wl[i] - base);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     float acc[PER] = {};
     if (sum != 0.0f) {
         const float lse = base + logf(sum);
-        for (int at = 0; at < ns; at += 32) {
-            const float weight = at + lane < ns ? expf((at == 0 ? first : wl[at + lane]) - lse) : 0.0f;
-            const int n = min(32, ns - at);
-            constexpr int kAhead = 4;  // loads in flight
-            for (int i = 0; i < n; i += kAhead) {
-                float v[kAhead][PER];
+        float weight = 0.0f;
+        for (int i = 0; i < ns; i += kAhead) {
+            if (i > 0) load(i);
+            if (i % 32 == 0) weight = expf((i == 0 ? l0 : i == 32 ? l1 : i + lane < ns ? wl[i + lane] : -INFINITY) - lse);
 #pragma unroll
-                for (int x = 0; x < kAhead; ++x)
+            for (int x = 0; x < kAhead; ++x) {
+                const float w = __shfl_sync(0xffffffffu, weight, (i + x) & 31);
+                const float* vx = reinterpret_cast<const float*>(&v[x]);
 #pragma unroll
-                    for (int e = 0; e < PER; ++e) v[x][e] = i + x < n ? wo[(long long)(at + i + x) * D + e] : 0.0f;
-#pragma unroll
-                for (int x = 0; x < kAhead; ++x) {
-                    const float w = __shfl_sync(0xffffffffu, weight, i + x);
-#pragma unroll
-                    for (int e = 0; e < PER; ++e) acc[e] += w * v[x][e];
-                }
+                for (int e = 0; e < PER; ++e) acc[e] += w * vx[e];
             }
         }
         if (lane == 0) p.lse[row] = lse;
@@ -499,22 +506,32 @@ cudaError_t launch_fmt(const TreeParams& p, int fmt, cudaStream_t stream) {
 
 }  // namespace
 
-void tree_plan(int B, int Hkv, int rows, long long lmax, int num_splits, int num_sms, int* chunk, int* max_splits) {
+void tree_plan(TreeParams& p, int d, bool f8, int num_splits) {
+    const int B = p.B, Hkv = p.Hkv, rows = p.max_q * p.G, num_sms = p.num_sms;
+    const long long lmax = (long long)p.max_pages * p.page_size;
+    const bool tiles = tree_takes_tiles(rows);
+    const long long groups = (long long)B * Hkv * (tiles ? (rows + 127) / 128 : (rows + 15) / 16);
+    const long long slots = (long long)num_sms * (tiles ? kTreeTileBlocks : tree_small_blocks(d, f8));
     long long c;
-    if (num_splits > 0) {
+    p.slots = 0;
+    if (num_splits == 0 && groups <= slots && B <= kTreeFitSeqs) {
+        // Fewer (sequence, kv head, row group) groups than blocks that fit at once: the blocks choose by the
+        // lengths (tree_fit), as long as the table's capacity leaves anything to choose. The workspace is for
+        // sequences that fill an eighth of it.
+        c = (lmax * groups + 8 * slots - 1) / (8 * slots);
+        if (c < 128) c = 128;
+        if ((lmax + c - 1) / c * groups > slots) p.slots = (int)slots;
+    } else if (num_splits > 0) {
         c = (lmax + num_splits - 1) / num_splits;
-    } else if (tree_takes_tiles(rows)) {
+    } else if (tiles) {
         // Blocks of 128 rows, two per SM. With fewer (sequence, kv head, row tile) groups than SMs: as many
-        // splits as fit at once (a few blocks more would cost a second wave), at least four of 1024 tokens
-        // or more, which balance sequences of different lengths. With enough groups for two blocks per SM:
-        // none, because the partial results of 128 rows cost as much traffic as 130 cached tokens of one
-        // head and the join is a second launch; the longest sequences start first. In between, a cap of 8192
-        // tokens. Measured, 8 or 16 drafted tokens x 4 query heads, splits -> us (bf16 unless noted): 64
-        // sequences of U[1K, 32K] (512 groups) 1: 631, 2: 643, 4: 639, 8: 671, e4m3 1: 434, 2: 470, 4: 483;
-        // 32 of 4096 (256 groups) 1: 88, 2: 98, 4: 109; 4 of 32768 (32 groups) 8: 96, 9: 97, 10: 125; 8 of
-        // U[128, 8192] (64 groups) 2: 57, 4: 41, 6: 37, 8: 38; one of 32768 (8 groups) 8: 55, 16: 39, 38: 42,
-        // 64: 54; 48 chains of U[1, 8000], e5m2, 3 kv heads (144 groups) 2: 50, 4: 39, 6: 48.
-        const long long groups = (long long)B * Hkv * ((rows + 127) / 128);
+        // splits as fit at once, at least four of 1024 tokens or more, which balance sequences of different
+        // lengths. With enough groups for two blocks per SM: none, because the partial results of 128 rows cost
+        // as much traffic as 130 cached tokens of one head and the join is a second launch; the longest
+        // sequences start first. In between, a cap of 8192 tokens. Measured, splits -> us: 64 sequences of
+        // U[1K, 32K], 16 drafted tokens x 4 query heads x 8 kv heads (512 groups), bf16 1: 633, 2: 650, 4: 644,
+        // 8: 668, e4m3 1: 433, 2: 459, 4: 486; 100 of U[100, 4000], 8 drafted tokens x 4 query heads (100
+        // groups), bf16 1: 48, 2: 38, 4: 29, 8: 35.
         long long splits = 1, most = 65536;
         if (groups < num_sms) {
             const long long balance = lmax / 1024 < 4 ? lmax / 1024 : 4;
@@ -526,12 +543,12 @@ void tree_plan(int B, int Hkv, int rows, long long lmax, int num_splits, int num
         if (c < 128) c = 128;
         if (c > most) c = most;
     } else {
-        // Blocks of 16 rows, up to four per SM. Many tokens: about 6 items per SM, assuming half-full page
-        // tables; fewer: two items per SM, up to 2048 tokens each. Measured, 4 drafted tokens x 4 query heads,
-        // bf16 / e4m3, splits -> us: 64 sequences of U[1K, 32K] 2: 619 / 367, 4: 623 / 383, 8: 652 / 394,
-        // 16: 694 / 454 (one token each 2: 609 / 342, 4: 598 / 349, 8: 608 / 346); 8 of U[128, 8192] 4: 44 / 42,
-        // 8: 40 / 37, 16: 51 / 43; one of 32768 8: 62 / 59, 16: 42 / 39, 32: 43 / 37, 64: 60 / 42; one of 1024
-        // 1: 23, 2: 18, 8: 15.
+        // Blocks of 16 rows, two to four per SM. Many tokens: about 6 items per SM, assuming half-full page
+        // tables; fewer: two items per SM, up to 2048 tokens each. Measured, bf16 / e4m3, splits -> us: 64
+        // sequences of U[1K, 32K], 4 drafted tokens x 4 query heads x 8 kv heads 2: 624 / 363, 4: 613 / 372,
+        // 8: 628 / 372, 16: 655 / 407 (one token each 2: 611 / 345, 4: 601 / 348, 8: 604 / 340); 100 of
+        // U[100, 4000], 2 drafted tokens x 4 query heads 1: 49 / 44, 2: 33 / 31, 4: 23 / 23, 8: 27 / 20,
+        // 16: 32 / 25.
         const long long tokens = (long long)B * Hkv * lmax;
         c = (tokens + 4LL * num_sms - 1) / (4LL * num_sms) * 2;  // two items per SM
         if (c > 2048) c = 2048;
@@ -544,8 +561,9 @@ void tree_plan(int B, int Hkv, int rows, long long lmax, int num_splits, int num
     const long long whole = (lmax + 63) / 64 * 64;
     if (c > whole) c = whole;
     if (c < 64) c = 64;
-    *chunk = (int)c;
-    *max_splits = (int)((lmax + c - 1) / c);
+    p.chunk = (int)c;
+    p.max_splits = (int)((lmax + c - 1) / c);
+    if (p.max_splits == 1) p.slots = 0;
 }
 
 cudaError_t launch_attn_tree(const TreeParams& p_in, const TreeTmaps& tm, int d, int kv_format, cudaStream_t stream) {

@@ -69,7 +69,7 @@ struct TileLayout {
     static constexpr int bK = 14, bV = bK + kStages, bKFree = bV + kStages, bVFree = bKFree + kStages;
     static constexpr int bClean = bVFree + kStages;
     static constexpr int kBars = bClean + kStages;
-    static constexpr int kMiscOff = kBarOff + kBars * 8;  // tensor-memory base, abort flag, odd-value flag
+    static constexpr int kMiscOff = kBarOff + kBars * 8;  // tensor-memory base, abort flag, odd-value flag, split
     static constexpr int kBytes = kMiscOff + 16;
     // at least 80 KB, so that no more than two blocks (256 tensor-memory columns each) share an SM; the
     // dynamic shared memory has to start on a 1024-byte boundary (checked)
@@ -193,19 +193,19 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     constexpr bool F8 = L::kF8;
     constexpr int NS = L::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
-    int b, split, hg;
-    if (!tree_item(p, reinterpret_cast<int*>(smem), b, split, hg)) return;
+    int chunk, b, split, hg;
+    if (!tree_item(p, reinterpret_cast<int*>(smem), chunk, b, split, hg)) return;
     const int kvh = hg / p.groups, r0 = (hg % p.groups) * kTileRows;
     TreeSeq s;
     if (!tree_seq(p, b, s)) return;
     const int R = min(kTileRows, s.n * p.G - r0);  // rows of this tile
     if (R <= 0) return;
-    const int nsplit = cdiv(s.len, p.chunk);
+    const int nsplit = cdiv(s.len, chunk);
     if (split < 0)
         split = nsplit > 0 ? nsplit - 1 : 0;
     else if (p.full_rows >= 0 && split >= nsplit - 1)
         return;  // the last split has its own block
-    const int t_begin = split * p.chunk;
+    const int t_begin = split * chunk;
     auto out_row = [&](int r) {
         const int i = (r0 + r) / p.G;
         return (long long)(s.q0 + i) * p.Hq + kvh * p.G + (r0 + r - i * p.G);
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
         return;
     }
     if (t_begin >= s.len) return;
-    const int t_end = min(s.len, t_begin + p.chunk);
+    const int t_end = min(s.len, t_begin + chunk);
     const int tiles = cdiv(t_end - t_begin, kTileKeys);
 
     if (smem_u32(smem) & 1023u) {  // the swizzles count from such boundaries
@@ -231,6 +231,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
     volatile int* odd_v = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 8);
+    volatile int* part_slot = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 12);  // (keeps it out of the registers)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t wd = p.watchdog_ns;
     const int* pt = p.page_table + (long long)b * p.max_pages;
@@ -257,6 +258,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
         }
         *abort_flag = 0;
         *odd_v = 0;
+        *part_slot = nsplit == 1 ? -1 : split;
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
@@ -682,6 +684,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
             tc_fence_after();
             const float inv = l == 0.0f ? 0.0f : p.v_descale / l;
             const bool empty = l == 0.0f;
+            const int part = *part_slot;  // split, -1: the only one
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -693,14 +696,14 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                 for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = empty ? 0.0f : v[e] * inv;
-                if (valid && nsplit == 1) {
+                if (valid && part < 0) {
                     uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D + c);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         dst[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
                                             pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
                 } else if (valid) {
-                    float4* dst = reinterpret_cast<float4*>(p.ws_o + (orow * p.max_splits + split) * D + c);
+                    float4* dst = reinterpret_cast<float4*>(p.ws_o + (orow * p.max_splits + part) * D + c);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                 }
@@ -712,18 +715,18 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                 for (int c = 0; c < D; ++c) {
                     const float x = nonfinite_sum<FMT>(p, pt, mrow, node, s, max(t_begin, s.ctx / kTileKeys * kTileKeys), t_end, kvh, D, c);
                     if (x == 0.0f) continue;
-                    if (nsplit == 1)
+                    if (part < 0)
                         p.o[orow * D + c] = __float2bfloat16(x * inv);
                     else
-                        p.ws_o[(orow * p.max_splits + split) * D + c] = x * inv;
+                        p.ws_o[(orow * p.max_splits + part) * D + c] = x * inv;
                 }
             }
             if (valid) {
                 const float lse = empty ? -INFINITY : m * scale + logf(l);
-                if (nsplit == 1)
+                if (part < 0)
                     p.lse[orow] = lse;
                 else
-                    p.ws_lse[orow * p.max_splits + split] = lse;
+                    p.ws_lse[orow * p.max_splits + part] = lse;
             }
         }
     }

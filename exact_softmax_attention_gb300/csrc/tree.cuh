@@ -18,12 +18,14 @@ struct TreeParams {
     float* lse;              // [T, Hq]
     float* ws_o;             // [T, Hq, max_splits, d] partial outputs
     float* ws_lse;           // [T, Hq, max_splits]
+    int* ws_chunk;           // tokens per split in use, when slots > 0
     int B, T, max_q, Hq, Hkv, G, page_size, max_pages, num_pages;
     int chunk, max_splits;   // tokens per split (a multiple of 64), splits of the longest sequence
+    int slots;               // > 0: chunk is the least one; the blocks choose it by the lengths, for so many at once
     int groups;              // row groups per kv head (rows: drafted token x query head of the kv head)
     // Work order (tree_grid): grid rows y < full_rows list the splits of sequence y before its last one, the
     // rows after them the last split of every sequence, in decreasing length when ranked. full_rows < 0:
-    // row y holds all splits of sequence y.
+    // row y holds all splits of sequence y. slots > 0: one row, see tree_fit.
     int full_rows, ranked, num_sms;
     // q is multiplied by q_sign (-1, 0, 1) and the scores by |scale|, so that masking and maxima
     // work on scores that grow with q.k for every finite scale (scale 0: q_sign 0, factor 1)
@@ -55,6 +57,11 @@ inline bool tree_takes_tiles(long long rows) { return rows >= kTreeTileRows; }
 // others, the longest first, they fill the SMs that the last full-length ones leave idle.
 inline dim3 tree_grid(TreeParams& p) {
     const long long HG = (long long)p.Hkv * p.groups;
+    if (p.slots > 0) {  // (blocks without work cost a microsecond or two each, so there are few more than fit at once)
+        p.full_rows = 0;
+        p.ranked = 0;
+        return dim3((unsigned)(p.slots + p.slots / 2));
+    }
     const long long X = (p.max_splits > 1 ? p.max_splits - 1 : 1) * HG;
     const long long full = p.max_splits > 1 ? p.B : 0, part = ((long long)p.B * HG + X - 1) / X;
     if (full + part <= 65535) {
@@ -69,7 +76,14 @@ inline dim3 tree_grid(TreeParams& p) {
     return dim3((unsigned)(p.max_splits * HG), (unsigned)p.B);
 }
 
-// Tokens per split and splits of the longest sequence (lmax tokens).
-void tree_plan(int B, int Hkv, int rows, long long lmax, int num_splits, int num_sms, int* chunk, int* max_splits);
+// Sequences up to which the blocks choose the split size by the lengths (two per lane of a warp).
+constexpr int kTreeFitSeqs = 64;
+
+// Blocks of the split kernels that share an SM.
+constexpr int tree_small_blocks(int d, bool f8) { return d == 64 ? 4 : (f8 ? 3 : 2); }
+constexpr int kTreeTileBlocks = 2;
+
+// Sets chunk, max_splits and slots of p (B, Hkv, G, max_q, max_pages, page_size and num_sms given).
+void tree_plan(TreeParams& p, int d, bool f8, int num_splits);
 
 }  // namespace attn

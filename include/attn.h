@@ -354,7 +354,8 @@ attn_status_t attn_kv_read_paged(const void* k_cache, const void* v_cache, void*
  *            most 64 * mask_words with a mask); max_q * Hq / Hkv at most 65535, T * Hq below 2^31
  * mask_words words per row of tree_mask, 1 .. 4 (ignored without a mask)
  * Hq, Hkv, d as for attn_decode_paged (d = 64 or 128); scale finite
- * num_splits 0: choose the number of key splits from the SM count and the sizes; n > 0: at most n
+ * num_splits 0: choose the number of key splits from the SM count, the sizes and the lengths (in a captured
+ *            graph those of the replay); n > 0: at most n
  * k_descale, v_descale  finite; ignored for ATTN_KV_BF16 (pass 1)
  * What a masked or unused cache slot holds does not matter, NaN and infinities included. A page
  * outside [0, num_pages) is not read: its rows count as zeros and ATTN_ERR_DEVICE_BAD_INDEX is

@@ -454,6 +454,61 @@ def test_two_streams_give_the_same_bytes(A):
     assert A.attn_get_device_status() == 0
 
 
+BATCHES = {  # cached tokens of each sequence, and how many times wider than needed the page table is
+    "equal": ([512] * 20, 1),
+    "ragged": ([(i * 97) % 500 + 20 for i in range(18)] + [0, 22], 1),
+    "one_long": ([20 + i % 3 for i in range(15)] + [6000], 1),
+    "wide_table": ([64 * (i + 1) for i in range(10)], 12),
+    "many": ([20 + (i * 37) % 300 for i in range(63)], 3),
+    "all_empty": ([0] * 20, 30),
+}
+
+
+def widened(c, times):
+    pt = np.full((c.B, c.width * times), 2**31 - 1, np.int32)
+    pt[:, :c.width] = c.pt
+    c.pt, c.width = pt, c.width * times
+    c.dev["pt"] = torch.from_numpy(pt).to(DEV)
+    return c
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,n,d", [("bf16", 2, 128), ("e4m3", 2, 64), ("bf16", 20, 64), ("e4m3", 20, 128)])
+@pytest.mark.parametrize("batch", BATCHES)
+def test_splits_chosen_by_the_lengths(A, fmt, n, d, batch):
+    """Batches of fewer groups than the GPU holds blocks: the split size follows the lengths."""
+    lens, times = BATCHES[batch]
+    Hkv = 2 if batch == "many" else 8
+    c = widened(Case(fmt, Hkv, Hkv, d, 16, [n] * len(lens), lens, "tree", 21), times)
+    c.run(A)
+    o, lse = c.o.clone(), c.lse.clone()
+    c.run(A)
+    assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
+    assert A.attn_get_device_status() == 0
+    c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,n", [("bf16", 2), ("e4m3", 20)])
+def test_replay_with_other_lengths(A, fmt, n):
+    """The split size of a graph's call follows the lengths of each replay, a bad one among them."""
+    full = [800, 300] * 8
+    c = widened(Case(fmt, 8, 8, 64, 16, [n] * 16, full, "chain", 22, dense=True), 5)
+    c.run(A)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run(A)
+    for lens in ([n] * 16, [800] + [n + 1] * 15, full, [n + 250] * 16):
+        c.lens = lens
+        c.dev["lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        c.dev["lens"][3] = 10**9 if lens is full else lens[3]
+        g.replay()
+        bad = A.attn_get_device_status()
+        assert bad == (A.ATTN_ERR_DEVICE_BAD_INDEX if lens is full else 0)
+        c.lens = [0 if lens is full and b == 3 else x for b, x in enumerate(lens)]
+        c.check()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("n", [2, 20])
