@@ -8,8 +8,8 @@
 // row to its page (offsets, length, page table); the rows themselves do not depend on it, so each
 // thread loads its first item before the places are known.
 //
-// Measured: 264 K tokens (8 heads of 128) from e4m3 to bf16 rows in 248 us, 0.97 of the measured copy
-// rate; 131072 tokens to a bf16 cache 169 us (0.93), to e4m3 143 us (0.83), with rotation 163 us (0.73): the
+// Measured: 264 K tokens (8 heads of 128) from e4m3 to bf16 rows in 247 us, 0.97 of the measured copy
+// rate; 131072 tokens to a bf16 cache 170 us (0.93), to e4m3 142 us (0.84), with rotation 160 us (0.74): the
 // 8-bit writes are bounded by instruction issue (about ten instructions per element for the rotation, the
 // quotient and the conversion); 64 tokens 4.2 us.
 #include "attn.h"
@@ -23,6 +23,10 @@ namespace {
 
 constexpr int kCacheThreads = 512;  // at most
 constexpr int kCacheMaxTokens = 32;  // tokens per block
+// Threads that an SM holds (64 and 32 registers each), and items per thread, at most. Measured, us: 14155 tokens to
+// e4m3 with rotation, items 8: 23.1, 12: 22.0, 16: 22.0 (885 blocks, whole waves or not, 24.3); 131072 tokens 8: 163,
+// 12: 160; to bf16 8: 169, 12: 170. 14155 tokens read from e4m3 4: 17.7, 8: 20.5; 131072 from bf16 4: 160, 8: 163.
+constexpr int kWriteThreads = 1024, kReadThreads = 2048, kWriteItems = 12, kReadItems = 4;
 
 struct CacheParams {
     const __nv_bfloat16* in[2];  // write: k, v
@@ -218,7 +222,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CachePa
 template <int FMT, int V>
 cudaError_t launch_write(CacheParams p, int num_sms, cudaStream_t stream) {
     p.items = p.cols.d / (2 * V);
-    p.share = share_rows(p.rows.T, 2 * p.Hkv * p.items, kCacheMaxTokens, num_sms);
+    p.share = share_rows(p.rows.T, 2 * p.Hkv * p.items, kWriteItems, kCacheMaxTokens, kWriteThreads, num_sms);
     const long long blocks = ((long long)p.rows.T + p.share.tokens - 1) / p.share.tokens;
     const size_t smem = (size_t)p.share.tokens * p.cols.rot * sizeof(float);
     return launch_kernel(cache_write_kernel<FMT, V>, dim3((unsigned)blocks), p.share.threads, smem, stream, false, p);
@@ -227,7 +231,7 @@ cudaError_t launch_write(CacheParams p, int num_sms, cudaStream_t stream) {
 template <int FMT>
 cudaError_t launch_read(CacheParams p, int num_sms, cudaStream_t stream) {
     p.items = p.cols.d / 16;
-    p.share = share_rows(p.rows.T, 2 * p.Hkv * p.items, kCacheMaxTokens, num_sms);
+    p.share = share_rows(p.rows.T, 2 * p.Hkv * p.items, kReadItems, kCacheMaxTokens, kReadThreads, num_sms);
     const long long blocks = ((long long)p.rows.T + p.share.tokens - 1) / p.share.tokens;
     return launch_kernel(cache_read_kernel<FMT>, dim3((unsigned)blocks), p.share.threads, 0, stream, false, p);
 }

@@ -8,8 +8,8 @@
 // multiply-adds per pair: it is bounded by memory, and the angles must not cost more than that.
 // One block takes a few tokens, computes their cosines and sines once into shared memory (shared by
 // all heads), and streams the heads through 16-byte loads and stores, the next item's loads ahead of
-// this one's stores. Measured: 18432 rows of 40 bf16 heads of 128 in 61.8 us, 6110 GB/s, 0.90 of the
-// measured copy rate (65536 rows 0.99); 8192 rows of 32 fp32 heads, 64 of 192 columns rotated, 0.94;
+// this one's stores. Measured: 18432 rows of 40 bf16 heads of 128 in 59.5 us, 6340 GB/s, 0.93 of the
+// measured copy rate (65536 rows 1.00); 8192 rows of 32 fp32 heads, 64 of 192 columns rotated, 0.95;
 // 64 rows 3.6 us. (Threads that keep their head and columns over the tokens, as in the cache writes,
 // need more registers and gave 65 and 74 us for the first two.)
 #include "attn.h"
@@ -22,6 +22,10 @@ namespace attn {
 namespace {
 
 constexpr int kRopeThreads = 256;
+// Blocks that an SM holds (48 registers per thread), and items per thread, at most. Measured, us, whole waves of 5
+// blocks and items 2: 63.8, 3: 60.2, 4: 59.5, of 6 blocks and items 8: 61.2, 16: 63.7 (18432 rows of 40 bf16 heads of
+// 128); of 5 blocks and items 2: 61.0, 4: 62.2, of 6 blocks and items 8: 63.1 (8192 rows of 32 fp32 heads).
+constexpr int kRopeBlocks = 5, kRopeItems = 4;
 constexpr int kRopeMaxDim = 1024;
 
 struct RopeParams {
@@ -61,16 +65,6 @@ struct ItemWalk {
         if (h >= heads) h -= heads, ++t;
     }
 };
-
-// Tokens per block, at most `most`: enough for eight items per thread, as long as every SM still gets
-// two blocks.
-int block_tokens(int T, long long items_per_token, int threads, int most, int num_sms) {
-    long long n = (8LL * threads + items_per_token - 1) / items_per_token;
-    const long long spread = T / (2LL * num_sms);
-    if (n > spread) n = spread;
-    if (n > most) n = most;
-    return n < 1 ? 1 : (int)n;
-}
 
 template <typename E, int V>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
@@ -118,8 +112,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
 template <typename E, int V>
 cudaError_t launch_rope(RopeParams p, bool in_place, int num_sms, cudaStream_t stream) {
     p.items = (in_place ? p.cols.rot : p.cols.d) / (2 * V);
-    // (the angles of a block's tokens take at most 32 KB)
-    p.tokens = block_tokens(p.T, (long long)p.H * p.items, kRopeThreads, 8192 / p.cols.rot, num_sms);
+    const int each = p.H * p.items, most = 8192 / p.cols.rot;  // (the angles of a block's tokens: 32 KB at most)
+    const int n = (kRopeItems * kRopeThreads + each - 1) / each;
+    p.tokens = whole_waves(p.T, n < most ? n : most, (long long)num_sms * kRopeBlocks);
     const long long blocks = ((long long)p.T + p.tokens - 1) / p.tokens;
     const size_t smem = (size_t)p.tokens * p.cols.rot * sizeof(float);
     return launch_kernel(rope_kernel<E, V>, dim3((unsigned)blocks), kRopeThreads, smem, stream, false, p);

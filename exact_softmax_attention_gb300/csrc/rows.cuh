@@ -198,18 +198,24 @@ struct RowShare {
     int tokens;          // tokens per block
 };
 
-// Eight items per thread, and no more than `most` tokens, as long as every SM still gets two blocks.
-inline RowShare share_rows(int T, int pairs, int most, int num_sms) {
+// Tokens per block: `most`, fewer where that fills whole waves of `slots` blocks, since a last wave of few blocks
+// costs as much as a full one.
+inline int whole_waves(int T, long long most, long long slots) {
+    if (most < 1) most = 1;
+    const long long waves = (T + slots * most - 1) / (slots * most);
+    return (int)((T + slots * waves - 1) / (slots * waves));
+}
+
+// Tokens for `items` items per thread, `most` at most; `resident` threads fit on an SM.
+inline RowShare share_rows(int T, int pairs, int items, int most, int resident, int num_sms) {
     RowShare s;
     const int turns = (pairs + 511) / 512;
     s.width = (pairs + turns - 1) / turns;
     const int groups = s.width >= 256 ? 1 : 256 / s.width;
     s.threads = (s.width * groups + 31) / 32 * 32;
-    long long n = (8LL * groups + turns - 1) / turns;
-    const long long spread = T / (2LL * num_sms);
-    if (n > spread) n = spread;
+    long long n = ((long long)items * groups + turns - 1) / turns;
     if (n > most) n = most;
-    s.tokens = n < 1 ? 1 : (int)n;
+    s.tokens = whole_waves(T, n, (long long)num_sms * (resident / s.threads));
     return s;
 }
 
