@@ -635,7 +635,7 @@ attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const v
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     void* ws = nullptr;
-    if (p.max_splits > 1) {
+    if (p.max_splits > 1 && p.cluster == 0) {
         cudaMemPool_t pool = nullptr;
         if ((st = device_pool(ds, &pool)) != ATTN_OK) return st;
         const size_t n = (size_t)T * Hq * p.max_splits;

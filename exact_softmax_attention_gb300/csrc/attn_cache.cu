@@ -225,7 +225,7 @@ cudaError_t launch_write(CacheParams p, int num_sms, cudaStream_t stream) {
     p.share = share_rows(p.rows.T, 2 * p.Hkv * p.items, kWriteItems, kCacheMaxTokens, kWriteThreads, num_sms);
     const long long blocks = ((long long)p.rows.T + p.share.tokens - 1) / p.share.tokens;
     const size_t smem = (size_t)p.share.tokens * p.cols.rot * sizeof(float);
-    return launch_kernel(cache_write_kernel<FMT, V>, dim3((unsigned)blocks), p.share.threads, smem, stream, false, p);
+    return launch_kernel(cache_write_kernel<FMT, V>, dim3((unsigned)blocks), p.share.threads, smem, stream, {}, p);
 }
 
 template <int FMT>
@@ -233,7 +233,7 @@ cudaError_t launch_read(CacheParams p, int num_sms, cudaStream_t stream) {
     p.items = p.cols.d / 16;
     p.share = share_rows(p.rows.T, 2 * p.Hkv * p.items, kReadItems, kCacheMaxTokens, kReadThreads, num_sms);
     const long long blocks = ((long long)p.rows.T + p.share.tokens - 1) / p.share.tokens;
-    return launch_kernel(cache_read_kernel<FMT>, dim3((unsigned)blocks), p.share.threads, 0, stream, false, p);
+    return launch_kernel(cache_read_kernel<FMT>, dim3((unsigned)blocks), p.share.threads, 0, stream, {}, p);
 }
 
 bool multiple(const void* p, long long bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }

@@ -117,7 +117,7 @@ cudaError_t launch_rope(RopeParams p, bool in_place, int num_sms, cudaStream_t s
     p.tokens = whole_waves(p.T, n < most ? n : most, (long long)num_sms * kRopeBlocks);
     const long long blocks = ((long long)p.T + p.tokens - 1) / p.tokens;
     const size_t smem = (size_t)p.tokens * p.cols.rot * sizeof(float);
-    return launch_kernel(rope_kernel<E, V>, dim3((unsigned)blocks), kRopeThreads, smem, stream, false, p);
+    return launch_kernel(rope_kernel<E, V>, dim3((unsigned)blocks), kRopeThreads, smem, stream, {}, p);
 }
 
 bool multiple(const void* p, long long bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }

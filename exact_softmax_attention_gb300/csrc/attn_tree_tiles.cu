@@ -71,6 +71,9 @@ struct TileLayout {
     static constexpr int kBars = bClean + kStages;
     static constexpr int kMiscOff = kBarOff + kBars * 8;  // tensor-memory base, abort flag, odd-value flag, split
     static constexpr int kBytes = kMiscOff + 16;
+    // the block's result for the cluster's join, over the tiles when they are done with: [row][kPartRow], LSE
+    static constexpr int kPartRow = D + 4, kPartLse = kTileRows * kPartRow * 4;
+    static_assert(kPartLse + kTileRows * 4 <= kBarOff, "room for the block's result");
     // at least 80 KB, so that no more than two blocks (256 tensor-memory columns each) share an SM; the
     // dynamic shared memory has to start on a 1024-byte boundary (checked)
     static constexpr int kAlloc = kBytes > 81920 ? kBytes : 81920;
@@ -185,7 +188,7 @@ __host__ __device__ constexpr uint32_t idesc8(uint32_t b_format, uint32_t M, uin
     return (1u << 4) | (b_format << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool kCluster>
 __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     tree_tile_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
     grid_dependents_launch();
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     constexpr int NS = L::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     int chunk, b, split, hg;
-    if (!tree_item(p, reinterpret_cast<int*>(smem), chunk, b, split, hg)) return;
+    if (!tree_item<kCluster>(p, reinterpret_cast<int*>(smem), chunk, b, split, hg)) return;
     const int kvh = hg / p.groups, r0 = (hg % p.groups) * kTileRows;
     TreeSeq s;
     if (!tree_seq(p, b, s)) return;
@@ -219,7 +222,14 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
             }
         return;
     }
-    if (t_begin >= s.len) return;
+    float* part_o = reinterpret_cast<float*>(smem);
+    float* part_lse = reinterpret_cast<float*>(smem + L::kPartLse);
+    const long long out_first = (long long)s.q0 * p.Hq + kvh * p.G;
+    const bool joins = kCluster && nsplit > 1;  // the same in all blocks of a cluster
+    if (t_begin >= s.len) {
+        if (joins) cluster_join<D, L::kPartRow>(part_o, part_lse, p.o, p.lse, out_first, r0, R, p.G, p.Hq, p.cluster, nsplit);
+        return;
+    }
     const int t_end = min(s.len, t_begin + chunk);
     const int tiles = cdiv(t_end - t_begin, kTileKeys);
 
@@ -258,7 +268,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
         }
         *abort_flag = 0;
         *odd_v = 0;
-        *part_slot = nsplit == 1 ? -1 : split;
+        *part_slot = nsplit == 1 ? -1 : joins ? -2 : split;
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
@@ -684,7 +694,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
             tc_fence_after();
             const float inv = l == 0.0f ? 0.0f : p.v_descale / l;
             const bool empty = l == 0.0f;
-            const int part = *part_slot;  // split, -1: the only one
+            const int part = *part_slot;  // split, -1: the only one, -2: for the cluster's join
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -696,14 +706,14 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                 for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = empty ? 0.0f : v[e] * inv;
-                if (valid && part < 0) {
+                if (valid && part == -1) {
                     uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D + c);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         dst[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
                                             pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
                 } else if (valid) {
-                    float4* dst = reinterpret_cast<float4*>(p.ws_o + (orow * p.max_splits + part) * D + c);
+                    float4* dst = reinterpret_cast<float4*>((kCluster ? part_o + row * L::kPartRow : p.ws_o + (orow * p.max_splits + part) * D) + c);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                 }
@@ -715,16 +725,20 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                 for (int c = 0; c < D; ++c) {
                     const float x = nonfinite_sum<FMT>(p, pt, mrow, node, s, max(t_begin, s.ctx / kTileKeys * kTileKeys), t_end, kvh, D, c);
                     if (x == 0.0f) continue;
-                    if (part < 0)
+                    if (part == -1)
                         p.o[orow * D + c] = __float2bfloat16(x * inv);
+                    else if (kCluster)
+                        part_o[row * L::kPartRow + c] = x * inv;
                     else
                         p.ws_o[(orow * p.max_splits + part) * D + c] = x * inv;
                 }
             }
             if (valid) {
                 const float lse = empty ? -INFINITY : m * scale + logf(l);
-                if (part < 0)
+                if (part == -1)
                     p.lse[orow] = lse;
+                else if (kCluster)
+                    part_lse[row] = lse;
                 else
                     p.ws_lse[orow * p.max_splits + part] = lse;
             }
@@ -738,30 +752,33 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, kCols);
     if (threadIdx.x == 0 && *abort_flag) atomicCAS(p.status, 0, kDevTimeout);
+    if (kCluster && *part_slot == -2) cluster_join<D, L::kPartRow>(part_o, part_lse, p.o, p.lse, out_first, r0, R, p.G, p.Hq, p.cluster, nsplit);
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool kCluster>
 cudaError_t launch_tiles(TreeParams p, const TreeTmaps& tm, cudaStream_t stream) {
     constexpr int bytes = TileLayout<D, FMT>::kAlloc;
     static std::atomic<bool> attr_set[kMaxAttrDevices];
-    cudaError_t e = ensure_smem_attr(tree_tile_kernel<D, FMT>, bytes, attr_set);
+    cudaError_t e = ensure_smem_attr(tree_tile_kernel<D, FMT, kCluster>, bytes, attr_set);
     if (e != cudaSuccess) return e;
     p.groups = (int)(((long long)p.max_q * p.G + kTileRows - 1) / kTileRows);
     const dim3 grid = tree_grid(p);
-    return launch_kernel(tree_tile_kernel<D, FMT>, grid, TileLayout<D, FMT>::kThreads, bytes, stream, false, p, tm.k, tm.v);
+    return launch_kernel(tree_tile_kernel<D, FMT, kCluster>, grid, TileLayout<D, FMT>::kThreads, bytes, stream, {false, p.cluster}, p, tm.k, tm.v);
 }
 
-template <int D>
+template <int D, bool kCluster>
 cudaError_t launch_fmt(const TreeParams& p, const TreeTmaps& tm, int fmt, cudaStream_t stream) {
-    return fmt == ATTN_FP8_E4M3   ? launch_tiles<D, ATTN_FP8_E4M3>(p, tm, stream)
-           : fmt == ATTN_FP8_E5M2 ? launch_tiles<D, ATTN_FP8_E5M2>(p, tm, stream)
-                                  : launch_tiles<D, ATTN_KV_BF16>(p, tm, stream);
+    return fmt == ATTN_FP8_E4M3   ? launch_tiles<D, ATTN_FP8_E4M3, kCluster>(p, tm, stream)
+           : fmt == ATTN_FP8_E5M2 ? launch_tiles<D, ATTN_FP8_E5M2, kCluster>(p, tm, stream)
+                                  : launch_tiles<D, ATTN_KV_BF16, kCluster>(p, tm, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_tiles(const TreeParams& p, const TreeTmaps& tm, int d, int kv_format, cudaStream_t stream) {
-    return d == 128 ? launch_fmt<128>(p, tm, kv_format, stream) : launch_fmt<64>(p, tm, kv_format, stream);
+    if (p.cluster > 0)
+        return d == 128 ? launch_fmt<128, true>(p, tm, kv_format, stream) : launch_fmt<64, true>(p, tm, kv_format, stream);
+    return d == 128 ? launch_fmt<128, false>(p, tm, kv_format, stream) : launch_fmt<64, false>(p, tm, kv_format, stream);
 }
 
 }  // namespace attn

@@ -22,6 +22,7 @@ struct TreeParams {
     int B, T, max_q, Hq, Hkv, G, page_size, max_pages, num_pages;
     int chunk, max_splits;   // tokens per split (a multiple of 64), splits of the longest sequence
     int slots;               // > 0: chunk is the least one; the blocks choose it by the lengths, for so many at once
+    int cluster;             // > 0: max_splits blocks of a cluster hold the splits of one group and join them themselves
     int groups;              // row groups per kv head (rows: drafted token x query head of the kv head)
     // Work order (tree_grid): grid rows y < full_rows list the splits of sequence y before its last one, the
     // rows after them the last split of every sequence, in decreasing length when ranked. full_rows < 0:
@@ -57,6 +58,11 @@ inline bool tree_takes_tiles(long long rows) { return rows >= kTreeTileRows; }
 // others, the longest first, they fill the SMs that the last full-length ones leave idle.
 inline dim3 tree_grid(TreeParams& p) {
     const long long HG = (long long)p.Hkv * p.groups;
+    if (p.cluster > 0) {
+        p.full_rows = -1;
+        p.ranked = 0;
+        return dim3((unsigned)(p.max_splits * HG), (unsigned)p.B);
+    }
     if (p.slots > 0) {  // (blocks without work cost a microsecond or two each, so there are few more than fit at once)
         p.full_rows = 0;
         p.ranked = 0;
@@ -83,7 +89,10 @@ constexpr int kTreeFitSeqs = 64;
 constexpr int tree_small_blocks(int d, bool f8) { return d == 64 ? 4 : (f8 ? 3 : 2); }
 constexpr int kTreeTileBlocks = 2;
 
-// Sets chunk, max_splits and slots of p (B, Hkv, G, max_q, max_pages, page_size and num_sms given).
+// Largest cluster that every GPU of this kind can place.
+constexpr int kTreeCluster = 8;
+
+// Sets chunk, max_splits, slots and cluster of p (B, Hkv, G, max_q, max_pages, page_size and num_sms given).
 void tree_plan(TreeParams& p, int d, bool f8, int num_splits);
 
 }  // namespace attn

@@ -8,6 +8,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 namespace attn {
 namespace {
 
@@ -150,8 +152,16 @@ __device__ __noinline__ void tree_fit(const int* seqlens, int* chunk_out, int B,
 // Work item of a block: tokens per split, sequence, split (-1: the sequence's last one) and head group (kv
 // head * groups + row group). False (for the whole block) when it has none. scratch: 4 or, when ranked, B + 1
 // ints of shared memory; every thread calls it.
+template <bool kCluster>
 __device__ __forceinline__ bool tree_item(const TreeParams& p, int* scratch, int& chunk, int& b, int& split, int& hg) {
     const int HG = p.Hkv * p.groups;
+    if constexpr (kCluster) {
+        chunk = p.chunk;
+        b = blockIdx.y;
+        split = (int)(blockIdx.x % (unsigned)p.cluster);
+        hg = (int)(blockIdx.x / (unsigned)p.cluster);
+        return true;
+    }
     if (p.slots > 0) {
         if (threadIdx.x < 32)
             tree_fit(p.seqlens, p.ws_chunk, p.B, p.max_pages * p.page_size, HG, p.slots, p.chunk >> 6, blockIdx.x,
@@ -193,6 +203,85 @@ __device__ __forceinline__ bool tree_item(const TreeParams& p, int* scratch, int
         __syncthreads();  // the scratch has other uses
     }
     return true;
+}
+
+// Join of a row's splits by a warp: LSE = log sum_s exp(lse_s), O = sum_s exp(lse_s - LSE) O_s in split order.
+// lse_of(i), row_of(i): LSE and D outputs (this lane's ones first) of split i.
+template <int D, typename Lse, typename Row>
+__device__ __forceinline__ void join_row(int ns, Lse lse_of, Row row_of, __nv_bfloat16* o, float* lse_out) {
+    constexpr int PER = D / 32;
+    const int lane = threadIdx.x & 31;
+    typedef typename std::conditional<D == 128, float4, float2>::type Vec;
+    constexpr int kAhead = 8;  // loads in flight; the first ones do not wait for the weights
+    Vec v[kAhead];
+    auto load = [&](int i) {
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) v[x] = i + x < ns ? *reinterpret_cast<const Vec*>(row_of(i + x) + lane * PER) : Vec{};
+    };
+    load(0);
+    // of the first 64 splits, mostly all there are
+    const float l0 = lane < ns ? lse_of(lane) : -INFINITY, l1 = lane + 32 < ns ? lse_of(lane + 32) : -INFINITY;
+    float mx = fmaxf(l0, l1);
+    for (int i = lane + 64; i < ns; i += 32) mx = fmaxf(mx, lse_of(i));
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+    // a split that the row sees nothing of has -inf, zeros as its output and weight 0; a NaN stays
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    float sum = expf(l0 - base) + expf(l1 - base);
+    for (int i = lane + 64; i < ns; i += 32) sum += expf(lse_of(i) - base);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    float acc[PER] = {}, lse = -INFINITY;
+    if (sum != 0.0f) {
+        lse = base + logf(sum);
+        float weight = 0.0f;
+        for (int i = 0; i < ns; i += kAhead) {
+            if (i > 0) load(i);
+            if (i % 32 == 0) weight = expf((i == 0 ? l0 : i == 32 ? l1 : i + lane < ns ? lse_of(i + lane) : -INFINITY) - lse);
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+                const float w = __shfl_sync(0xffffffffu, weight, (i + x) & 31);
+                const float* vx = reinterpret_cast<const float*>(&v[x]);
+#pragma unroll
+                for (int e = 0; e < PER; ++e) acc[e] += w * vx[e];
+            }
+        }
+    }
+    if (lane == 0) *lse_out = lse;
+#pragma unroll
+    for (int e = 0; e < PER; e += 2) *reinterpret_cast<uint32_t*>(o + lane * PER + e) = pack_bf16x2(acc[e], acc[e + 1]);
+}
+
+// ---- blocks of a cluster
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The same place of the shared memory of another block.
+__device__ __forceinline__ const float* of_block(const float* p, int rank) {
+    const float* r;
+    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
+    return r;
+}
+
+// Join of the ns splits of R rows by the blocks of a cluster, split i in block i: outputs o_part (rows kStride
+// apart) and lse_part of each in its shared memory. Row r of the group is o row first + (r0 + r) / G Hq +
+// (r0 + r) % G. Every thread of all blocks calls it. (Not inlined: the kernels' own code stays as short.)
+template <int D, int kStride>
+__device__ __noinline__ void cluster_join(const float* o_part, const float* lse_part, __nv_bfloat16* o, float* lse, long long first, int r0,
+                                          int R, int G, int Hq, int cluster, int ns) {
+    __syncwarp();
+    cluster_sync();
+    const int rank = (int)(blockIdx.x % (unsigned)cluster), warps = blockDim.x >> 5;
+    for (int r = rank + cluster * (int)(threadIdx.x >> 5); r < R; r += cluster * warps) {
+        const int i = (r0 + r) / G;
+        const long long row = first + (long long)i * Hq + (r0 + r - i * G);
+        join_row<D>(
+            ns, [&](int x) { return *of_block(lse_part + r, x); }, [&](int x) { return of_block(o_part + r * kStride, x); }, o + row * D,
+            lse + row);
+    }
+    cluster_sync();  // a block stays until the others have read its part
 }
 
 // Bits of the keys kb .. kb + 63 that drafted token i of the sequence sees. row: its mask words, or

@@ -366,8 +366,10 @@ attn_status_t attn_kv_read_paged(const void* k_cache, const void* v_cache, void*
  * attn_decode_paged_fp8). More rows: keys multiplied as they are by q split into two e4m3 parts (after
  * scaling each row by a power of two), exact for elements down to 2^-9 of the row's largest and
  * within 2^-17 of that for smaller ones; values widened exactly to f16.
- * Workspace, launches and programmatic dependents as for attn_decode_paged: partial outputs of the
- * splits (T * Hq * splits * (d + 1) floats) from the library's stream-ordered pool on `stream`.
+ * Up to eight splits per sequence, when all blocks fit on the GPU at once: one launch (the splits of a group are a
+ * thread-block cluster, which joins them) and no workspace. Else workspace, launches and programmatic dependents as
+ * for attn_decode_paged: partial outputs of the splits (T * Hq * splits * (d + 1) + 1 floats) from the library's
+ * stream-ordered pool on `stream`.
  * Alignment: q, o, k_cache, v_cache 16 bytes; tree_mask 8; lse, page_table, seqlens, cu_seqlens 4.
  */
 attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const void* v_cache, const int* page_table,

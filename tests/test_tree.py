@@ -454,6 +454,52 @@ def test_two_streams_give_the_same_bytes(A):
     assert A.attn_get_device_status() == 0
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,n,d,page", [("bf16", 4, 128, 16), ("e5m2", 2, 64, 7), ("e4m3", 3, 128, 16), ("bf16", 20, 128, 16),
+                                          ("bf16", 33, 64, 5), ("e4m3", 20, 128, 16), ("e5m2", 40, 64, 64)])
+@pytest.mark.parametrize("num_splits", [2, 8, 9, 40])
+def test_splits_joined_in_a_cluster_or_by_a_second_kernel(A, fmt, n, d, page, num_splits):
+    """Up to eight splits that all fit at once are joined by their blocks; sequences of fewer splits, of one, of no
+    tokens and of no rows among them, and a non-finite value that every row of a sequence sees."""
+    c = Case(fmt, 4, 2, d, page, [n, n, 0, 1, n], [2600, n + 70, 0, 1, n + 700], "tree", 23)
+    c.run(A, num_splits)
+    o, lse = c.o.clone(), c.lse.clone()
+    c.run(A, num_splits)
+    assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
+    assert A.attn_get_device_status() == 0
+    c.check()
+    tok = 1300
+    row = int(c.pt[0, tok // page]) * page + tok % page
+    c.c[1].view(-1, 2, d)[row, 1, 5] = float("nan") if fmt == "bf16" else 0x7F
+    c.run(A, num_splits)
+    nan = torch.isnan(c.o)
+    want = torch.zeros_like(nan)
+    want[:n, 2:, 5] = True
+    assert torch.equal(nan, want)
+    assert torch.equal(c.o[~nan], o[~nan]) and torch.equal(c.lse, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("num_splits", [8, 20])
+def test_streams_at_once_with_few_and_many_splits(A, num_splits):
+    cases = [Case("bf16", 8, 2, 128, 16, [24, 24], [900, 2000], "tree", 13), Case("e4m3", 8, 2, 128, 16, [2, 2], [3000, 2000], "tree", 14),
+             Case("e5m2", 8, 8, 64, 16, [24], [2500], "chain", 15)]
+    want = []
+    for c in cases:
+        c.run(A, num_splits)
+        want.append((c.o.clone(), c.lse.clone()))
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s in zip(cases, streams):
+            c.run(A, num_splits, stream=s)
+    torch.cuda.synchronize()
+    for c, (o, lse) in zip(cases, want):
+        assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
+        c.check()
+    assert A.attn_get_device_status() == 0
+
+
 BATCHES = {  # cached tokens of each sequence, and how many times wider than needed the page table is
     "equal": ([512] * 20, 1),
     "ragged": ([(i * 97) % 500 + 20 for i in range(18)] + [0, 22], 1),
