@@ -23,7 +23,7 @@ namespace {
 // ------------------------------------------------------------------------------ few rows
 //
 // One block of four warps per (sequence, split, kv head, group of 16 rows). Each warp streams its own
-// 16-token groups through a private three-stage cp.async ring (any page size: each row's address
+// 16-token groups through a private cp.async ring of two to four groups (any page size: each row's address
 // comes from the page table), and multiplies with mma.sync, whose 16 rows are the group's rows: for
 // up to 16 rows per kv head the kernel is bounded by the cache reads, so a wider product would
 // only add work on padding. 8-bit codes become f16 pairs in registers (exact); the order of d
@@ -36,11 +36,14 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kGroup = 16;
-constexpr int kStages = 3;
 
-template <int D, int FMT>
+template <int D, int GN, int FMT>
 struct SmallLayout {
     static constexpr int kElem = FMT == ATTN_KV_BF16 ? 2 : 1;
+    // Token groups in flight per warp. With 128 bf16 elements two, so that three blocks share an SM (three groups and
+    // two blocks: 64 sequences of U[100, 1000], 4 drafted tokens 36.7 us, not 33.5; of U[1K, 32K] 0.2% faster); with
+    // 8-bit codes four (three: 1% slower over long contexts).
+    static constexpr int kStages = D == 64 ? 3 : FMT == ATTN_KV_BF16 ? 2 : 4;
     static constexpr int kRow = D * kElem;         // bytes of a cached row of one head
     static constexpr int kTile = kGroup * kRow;    // one K or V stage of a warp
     static constexpr int kChunks = kRow / 16;
@@ -78,10 +81,11 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[2]) {
 
 // GN: row slots that hold rows (8 or 16). kCluster: the splits of a group are the blocks of a cluster.
 template <int D, int GN, int FMT, bool kCluster>
-__global__ void __launch_bounds__(kWarps * 32, tree_small_blocks(D, FMT != ATTN_KV_BF16)) tree_small_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, tree_small_blocks(D, FMT != ATTN_KV_BF16, GN)) tree_small_kernel(const TreeParams p) {
     grid_dependents_launch();
-    using L = SmallLayout<D, FMT>;
+    using L = SmallLayout<D, GN, FMT>;
     constexpr bool F8 = FMT != ATTN_KV_BF16;
+    constexpr int kStages = L::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int odd_v;  // a V tile held a non-finite value that was taken out
     int chunk, b, split, hg;
@@ -454,7 +458,7 @@ cudaError_t launch_join(const TreeParams& p, cudaStream_t stream) {
 
 template <int D, int GN, int FMT, bool kCluster>
 cudaError_t launch_small(TreeParams p, cudaStream_t stream) {
-    constexpr int bytes = SmallLayout<D, FMT>::kBytes;
+    constexpr int bytes = SmallLayout<D, GN, FMT>::kBytes;
     static std::atomic<bool> attr_set[kMaxAttrDevices];
     cudaError_t e = ensure_smem_attr(tree_small_kernel<D, GN, FMT, kCluster>, bytes, attr_set);
     if (e != cudaSuccess) return e;
@@ -484,7 +488,7 @@ void tree_plan(TreeParams& p, int d, bool f8, int num_splits) {
     const long long lmax = (long long)p.max_pages * p.page_size;
     const bool tiles = tree_takes_tiles(rows);
     const long long groups = (long long)B * Hkv * (tiles ? (rows + 127) / 128 : (rows + 15) / 16);
-    const long long slots = (long long)num_sms * (tiles ? kTreeTileBlocks : tree_small_blocks(d, f8));
+    const long long slots = (long long)num_sms * (tiles ? kTreeTileBlocks : tree_small_blocks(d, f8, rows));
     long long c;
     p.slots = 0;
     if (num_splits == 0 && groups <= slots && B <= kTreeFitSeqs) {

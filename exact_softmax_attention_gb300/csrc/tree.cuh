@@ -85,8 +85,9 @@ inline dim3 tree_grid(TreeParams& p) {
 // Sequences up to which the blocks choose the split size by the lengths (two per lane of a warp).
 constexpr int kTreeFitSeqs = 64;
 
-// Blocks of the split kernels that share an SM.
-constexpr int tree_small_blocks(int d, bool f8) { return d == 64 ? 4 : (f8 ? 3 : 2); }
+// Blocks of the split kernels that share an SM. (64 8-bit codes, up to 8 rows, five, not four: 64 sequences of U[100, 1000]
+// 17.0 us, not 20.1, of U[1K, 32K] 197, not 206; with up to 16 rows the registers do not suffice: 242, not 218.)
+constexpr int tree_small_blocks(int d, bool f8, int rows) { return d == 128 ? 3 : f8 && rows <= 8 ? 5 : 4; }
 constexpr int kTreeTileBlocks = 2;
 
 // Largest cluster that every GPU of this kind can place.
