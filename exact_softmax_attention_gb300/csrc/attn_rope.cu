@@ -139,7 +139,7 @@ extern "C" attn_status_t attn_rope(const void* q, const void* k, void* q_out, vo
         return ATTN_ERR_BAD_SHAPE;
     const long long wq = (long long)Hq * d, wk = (long long)Hk * d;
     // rows of an output may not overlap; those of an input may (stride 0 repeats one row)
-    if (q_stride < 0 || k_stride < 0 || q_out_stride < wq || (Hk > 0 && k_out_stride < wk)) return ATTN_ERR_BAD_SHAPE;
+    if (q_stride < 0 || (Hk > 0 && k_stride < 0) || q_out_stride < wq || (Hk > 0 && k_out_stride < wk)) return ATTN_ERR_BAD_SHAPE;
     const int size = elem_type == ATTN_TYPE_BF16 ? 2 : 4;
     if (!multiple(q, size) || !multiple(q_out, size) || !multiple(positions, 4) || !multiple(inv_freq, 8) ||
         (Hk > 0 && (!multiple(k, size) || !multiple(k_out, size))))

@@ -40,7 +40,9 @@
 // Tried and slower (same case, bf16 / 8-bit, before the work order; this form then took 698 / 584, with S and
 // P V in a thread each and raw K 685 / 511): Q in tensor memory with one S buffer 713 / 753, or with S in
 // steps of 32 keys 813 / 844 (a product takes 32 clocks at least); one S buffer with two separate P
-// 685 / 531; one block of 512 threads per SM with two streams of even and odd tiles 696 / 721.
+// 685 / 531; one block of 512 threads per SM with two streams of even and odd tiles 696 / 721. In the present form
+// (640 / 440): up to 64 rows copied over the idle softmax warps, each copy with a part of the keys (all of V has to be
+// finite then) 1130 / 427; S as a product of M = 64 for them 643 / 450.
 #include "launch.cuh"
 #include "tree_device.cuh"
 

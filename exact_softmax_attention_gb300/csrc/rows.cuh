@@ -106,14 +106,21 @@ __device__ __forceinline__ unsigned long long turn_fraction(double f) {
     return f < 0 ? 0 - turns : turns;
 }
 
-// The quarter turn nearest to the angle is split off in integers too, so that what is rounded to fp32 is at
-// most an eighth of a turn: the angle is off by 2^-25 of that, 2e-8 rad.
+// The quarter turn nearest to the angle is split off in integers too; the rest, at most an eighth of a turn, is
+// rounded to fp32, and what that leaves out is added as a rotation by that small angle. So the cosine and sine are
+// off by little more than those of sincospif.
 __device__ __forceinline__ void position_angle(unsigned long long frac, int pos, float& c, float& s) {
     const unsigned long long phase = frac * (unsigned long long)(long long)pos;  // turns * 2^64
     const unsigned quarter = (unsigned)((phase + (1ull << 61)) >> 62);
     const long long rest = (long long)(phase - ((unsigned long long)quarter << 62));  // [-2^61, 2^61)
+    const int top = (int)(rest >> 30);  // 2^-33 half turns, [-2^31, 2^31)
+    const float hi = (float)top;
+    const float lo = (float)(top - (int)hi) + (float)((int)rest & 0x3FFFFFFF) * 0x1p-30f;
     float c0, s0;
-    sincospif(__ll2float_rn(rest) * 1.0842021724855044e-19f, &s0, &c0);  // * 2^-63: half turns
+    sincospif(hi * 0x1p-33f, &s0, &c0);
+    const float d = lo * 3.657295198e-10f, sx = s0;  // radians: pi * 2^-33
+    s0 = fmaf(d, c0, s0);
+    c0 = fmaf(-d, sx, c0);
     const float u = quarter & 1 ? -s0 : c0, w = quarter & 1 ? c0 : s0;   // one quarter turn further
     c = quarter & 2 ? -u : u;
     s = quarter & 2 ? -w : w;

@@ -154,6 +154,38 @@ def test_rope_parity(A, T, Hq, Hk, d, begin, rot, inter, et, transpose):
 
 
 @pytest.mark.gpu
+def test_rope_angles_of_any_frequency(A):
+    """cos and sin of position * frequency against exact integers: frequencies above and below one turn, negative,
+    tiny and zero, positions over the whole range; non-finite frequencies give NaN in their columns only."""
+    from fractions import Fraction
+    two_pi = 2 * Fraction(31415926535897932384626433832795028841971693993751058209749445923, 10**64)
+    freqs = [1.0, 0.5, 2.0**-9, 2.0**-9 - 2.0**-62, 2.0**-10, 3e-5, 1e-12, 1e-18, 1e-300, 5e-324, 0.0, -0.37, 6.283185307179586, 3.0, 1000.123,
+             2.0**20 + 0.25, 2.0**60, float("inf"), float("-inf"), float("nan")]
+    pos = [0, 1, -1, 7, 4095, 131071, 2**24 + 1, 10**9 + 7, 2**31 - 1, -(2**31)]
+    n, T = len(freqs), len(pos)
+    x = torch.cat([torch.ones(T, n), torch.zeros(T, n)], 1).to(DEV)
+    y = torch.empty_like(x)
+    A.attn_rope(x, None, y, None, torch.tensor(pos, dtype=torch.int32, device=DEV), torch.tensor(freqs, dtype=torch.float64, device=DEV), T, 1, 0,
+                2 * n, 0, 2 * n, 2 * n, 0, 2 * n, 0, "f32")
+    y = y.double().cpu().numpy()
+    for i, f in enumerate(freqs):
+        for t, m in enumerate(pos):
+            c, s = y[t, i], y[t, n + i]
+            if not math.isfinite(f):
+                assert math.isnan(c) and math.isnan(s)
+                continue
+            # sincospif within 1.5 ulp, the added rotation and the products rounded once each: 4 * 2^-24; the fraction
+            # of a turn is cut to 2^-64 and 1 / (2 pi) rounded to 67 bits: (1 + f / 8) 2^-64 turns per position
+            tol = 2.0**-22 + 2 * math.pi * abs(m) * (1 + abs(f) / 8) * 2.0**-64
+            if tol > 1:
+                assert abs(c) <= 1.001 and abs(s) <= 1.001
+                continue
+            turns = Fraction(f) * m / two_pi
+            angle = float((turns - round(turns)) * two_pi)
+            assert abs(c - math.cos(angle)) <= tol and abs(s - math.sin(angle)) <= tol, (f, m)
+
+
+@pytest.mark.gpu
 def test_rope_in_place_and_gradient(A):
     """In place gives the same bytes; transpose undoes the rotation and is its gradient by differences."""
     T, H, d, rot = 40, 3, 96, 64
