@@ -624,7 +624,7 @@ attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const v
     p.watchdog_ns = (unsigned long long)(opt.watchdog_ms * 1e6);
     attn::TreeTmaps tm;
     memset(&tm, 0, sizeof tm);
-    if (attn::tree_takes_tiles(rows)) {
+    if (p.tiles) {
         const long long cache_rows = (long long)num_pages * page_size;
         p.box_rows = page_size % 64 == 0 ? 64 : (page_size % 16 == 0 ? 16 : 1);
         if (p.box_rows > 1 &&

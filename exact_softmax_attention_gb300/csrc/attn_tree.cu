@@ -25,8 +25,8 @@ namespace {
 // One block of four warps per (sequence, split, kv head, group of 16 rows). Each warp streams its own
 // 16-token groups through a private cp.async ring of two to four groups (any page size: each row's address
 // comes from the page table), and multiplies with mma.sync, whose 16 rows are the group's rows: for
-// up to 16 rows per kv head the kernel is bounded by the cache reads, so a wider product would
-// only add work on padding. 8-bit codes become f16 pairs in registers (exact); the order of d
+// up to 16 rows per kv head the kernel is bounded by the cache reads, so a wider product would only add work on
+// padding (two groups only where tree_takes_tiles says so). 8-bit codes become f16 pairs in registers (exact); the order of d
 // inside both products is permuted so that one 16-byte shared load feeds several products.
 // Measured, 64 sequences of U[1K, 32K] tokens, 4 query heads on each of 8 kv heads: one token each 597 us
 // (7220 GB/s, 1.06 of the measured copy rate, which also writes), four 608 us; e4m3 329 us (6550 GB/s) and
@@ -486,7 +486,8 @@ cudaError_t launch_fmt(const TreeParams& p, int fmt, cudaStream_t stream) {
 void tree_plan(TreeParams& p, int d, bool f8, int num_splits) {
     const int B = p.B, Hkv = p.Hkv, rows = p.max_q * p.G, num_sms = p.num_sms;
     const long long lmax = (long long)p.max_pages * p.page_size;
-    const bool tiles = tree_takes_tiles(rows);
+    const bool tiles = tree_takes_tiles(rows, d, f8, (long long)B * Hkv * lmax, num_sms);
+    p.tiles = tiles;
     const long long groups = (long long)B * Hkv * (tiles ? (rows + 127) / 128 : (rows + 15) / 16);
     const long long slots = (long long)num_sms * (tiles ? kTreeTileBlocks : tree_small_blocks(d, f8, rows));
     long long c;
@@ -556,7 +557,7 @@ cudaError_t launch_attn_tree(const TreeParams& p_in, const TreeTmaps& tm, int d,
         p.ps_shift = k - 1;
     }
     cudaError_t e;
-    if (tree_takes_tiles((long long)p.max_q * p.G))
+    if (p.tiles)
         e = launch_tree_tiles(p, tm, d, kv_format, stream);
     else
         e = d == 128 ? launch_fmt<128>(p, kv_format, stream) : launch_fmt<64>(p, kv_format, stream);

@@ -1,5 +1,5 @@
 // Attention of drafted tokens over a paged cache for more than 16 rows (drafted tokens x query heads)
-// per kv head: 128-row tiles on the tcgen05 tensor cores.
+// per kv head, in short calls with d = 64 more than 32: 128-row tiles on the tcgen05 tensor cores.
 //
 // A block takes one (sequence, split of the keys, kv head, 128-row tile) and walks the split's keys in
 // tiles of 64. Per tile S = Q K^T (M 128, N 64) and O += P V (M 128, N d), accumulators in tensor

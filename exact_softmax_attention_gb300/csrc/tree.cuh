@@ -22,6 +22,7 @@ struct TreeParams {
     int B, T, max_q, Hq, Hkv, G, page_size, max_pages, num_pages;
     int chunk, max_splits;   // tokens per split (a multiple of 64), splits of the longest sequence
     int slots;               // > 0: chunk is the least one; the blocks choose it by the lengths, for so many at once
+    int tiles;               // 128-row tiles, not 16-row products
     int cluster;             // > 0: max_splits blocks of a cluster hold the splits of one group and join them themselves
     int groups;              // row groups per kv head (rows: drafted token x query head of the kv head)
     // Work order (tree_grid): grid rows y < full_rows list the splits of sequence y before its last one, the
@@ -45,14 +46,21 @@ struct TreeTmaps {
     CUtensorMap k, v;
 };
 
-// Rows per kv head from which the 128-row tiles take over from the 16-row products.
-constexpr int kTreeTileRows = 17;
-
 // kv_format: ATTN_KV_BF16, ATTN_FP8_E4M3, ATTN_FP8_E5M2; d 64 or 128.
-// tm: the maps when tree_takes_tiles(rows of a kv head) and box_rows > 1, else unused.
+// tm: the maps when p.tiles and box_rows > 1, else unused.
 cudaError_t launch_attn_tree(const TreeParams& p, const TreeTmaps& tm, int d, int kv_format, cudaStream_t stream);
 cudaError_t launch_tree_tiles(const TreeParams& p, const TreeTmaps& tm, int d, int kv_format, cudaStream_t stream);
-inline bool tree_takes_tiles(long long rows) { return rows >= kTreeTileRows; }
+
+// 128-row tiles, or 16-row products? The latter up to 16 rows per kv head, where the cache is read once either way.
+// Up to 32 rows they read it twice (once through the L2), but start sooner and need no padding: with d = 64 and
+// little work (tokens: of all sequences and kv heads, by the capacity of the page table) they are faster. Measured,
+// 24 rows, 16-row products / tiles, us: 8-bit codes 48 sequences of up to 8000 tokens x 3 kv heads (7600 tokens
+// per SM) 34 / 39 to 41 / 42, 16 of 4096 x 8 (3400) 36.5 / 34.5, 64 of up to 1000 x 8 (3400) 26 / 28, 64 of up to
+// 8000 x 8 114 / 87; bf16 64 of up to 1000 x 3 (1300) 17 / 19, 16 of 4096 x 8 38.6 / 34.4. With d = 128: 8-bit codes 64 of
+// up to 1000 x 8 46 / 34, bf16 48 / 40.
+inline bool tree_takes_tiles(long long rows, int d, bool f8, long long tokens, int num_sms) {
+    return rows > 16 && (d != 64 || rows > 32 || tokens > (f8 ? 8192LL : 2048LL) * num_sms);
+}
 
 // Grid of a split kernel; sets the work order. The last splits are shorter in general: started after all
 // others, the longest first, they fill the SMs that the last full-length ones leave idle.
@@ -93,7 +101,7 @@ constexpr int kTreeTileBlocks = 2;
 // Largest cluster that every GPU of this kind can place.
 constexpr int kTreeCluster = 8;
 
-// Sets chunk, max_splits, slots and cluster of p (B, Hkv, G, max_q, max_pages, page_size and num_sms given).
+// Sets tiles, chunk, max_splits, slots and cluster of p (B, Hkv, G, max_q, max_pages, page_size and num_sms given).
 void tree_plan(TreeParams& p, int d, bool f8, int num_splits);
 
 }  // namespace attn

@@ -535,6 +535,39 @@ def test_splits_chosen_by_the_lengths(A, fmt, n, d, batch):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt,n,d", [("bf16", 20, 128), ("bf16", 40, 64), ("e5m2", 40, 64)])
+@pytest.mark.parametrize("batch", ["ragged", "one_long", "wide_table"])
+def test_tiles_split_by_the_lengths(A, fmt, n, d, batch):
+    lens, times = BATCHES[batch]
+    lens = [x and max(x, n) for x in lens]
+    c = widened(Case(fmt, 8, 8, d, 16, [n] * len(lens), lens, "tree", 24), times)
+    c.run(A)
+    assert A.attn_get_device_status() == 0
+    c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "e5m2"])
+@pytest.mark.parametrize("n,page,num_splits", [(5, 16, 0), (8, 7, 1), (7, 1, 3), (6, 64, 12), (8, 16, 8)])
+def test_two_row_groups_of_narrow_heads(A, fmt, n, page, num_splits):
+    """17 to 32 rows of 64 elements: ragged row counts whose second group is partly or wholly empty, rows that see
+    nothing, a masked NaN."""
+    c = Case(fmt, 8, 2, 64, page, [n, 1, n - 1, 0, n], [n + 900, 1, n + 60, 5, n], "any", 26)
+    tok = c.lens[0] - n  # the first drafted token, which no row is to see
+    c.seen[0][:, 0] = False
+    m = c.mask.cpu().numpy().view(np.uint64)
+    m[:n] &= ~np.uint64(1)
+    c.mask = torch.from_numpy(m.view(np.int64)).to(DEV)
+    for cache in c.c:
+        cache.view(-1, 2, 64)[int(c.pt[0, tok // page]) * page + tok % page] = float("nan") if fmt == "bf16" else 0x7F
+    c.run(A, num_splits)
+    assert A.attn_get_device_status() == 0
+    keep = c.values
+    c.values = lambda: [np.nan_to_num(x, nan=0.0) for x in keep()]
+    c.check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt,n", [("bf16", 2), ("e4m3", 20)])
 def test_replay_with_other_lengths(A, fmt, n):
     """The split size of a graph's call follows the lengths of each replay, a bad one among them."""
