@@ -293,3 +293,33 @@ def test_write_on_a_side_stream_in_a_graph(A):
     again = c.kc.clone()
     c.write(A, **kw)
     assert torch.equal(again, c.kc) and A.attn_get_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "e5m2"])
+def test_cache_offsets_beyond_32_bits(A, fmt):
+    """Rows on the last pages of a cache of more than 2^31 elements, out of rows further apart than that."""
+    Hkv, d, page, B, n = 8, 128, 16, 3, 5
+    num = 2**31 // (page * Hkv * d) + 9
+    t = torch.bfloat16 if fmt == "bf16" else torch.uint8
+    kc, vc = (torch.empty((num, page, Hkv, d), dtype=t, device=DEV) for _ in range(2))
+    pt = torch.tensor([[num - 1, 0], [num - 2, num - 5], [1, num - 3]], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([9, 20, 32], dtype=torch.int32, device=DEV)
+    stride = 2**28 + 8
+    x = torch.empty(B * n * stride, dtype=torch.bfloat16, device=DEV)
+    k = x.as_strided((B * n, Hkv * d), (stride, 1))
+    k.copy_(torch.randn(B * n, Hkv * d))
+    v = torch.randn(B * n, Hkv * d, device=DEV).bfloat16()
+    A.attn_kv_write_paged(k, v, stride, Hkv * d, kc, vc, pt, lens, None, page, B * n, B, Hkv, d, 2, num, fmt, 0.5, 0.25)
+    at = [(int(pt[b, i // page]), i % page) for b in range(B) for i in range(int(lens[b]) - n, int(lens[b]))]
+    for cache, y, ds in ((kc, k, 0.5), (vc, v, 0.25)):
+        got = torch.stack([cache[p, o] for p, o in at]).view(B * n, -1)
+        want = y if fmt == "bf16" else (y.float() / ds).to(torch.float8_e5m2).view(torch.uint8)
+        assert torch.equal(got, want)
+    k2, v2 = torch.empty_like(v), torch.empty_like(v)
+    k.zero_()
+    A.attn_kv_read_paged(kc, vc, k, v2, stride, Hkv * d, pt, lens, None, page, B * n, B, Hkv, d, 2, num, fmt, 0.5, 0.25)
+    A.attn_kv_read_paged(kc, vc, k2, v2, Hkv * d, Hkv * d, pt, lens, None, page, B * n, B, Hkv, d, 2, num, fmt, 0.5, 0.25)
+    assert torch.equal(k, k2) and A.attn_get_device_status() == 0
+    want = v if fmt == "bf16" else ((v.float() / 0.25).to(torch.float8_e5m2).float() * 0.25).bfloat16()
+    assert torch.equal(v2, want)

@@ -226,3 +226,21 @@ def test_rope_stream_and_repeated_rows(A):
     s.synchronize()
     A.attn_rope(x.expand(T, -1).contiguous(), None, z, None, pos, inv, T, H, 0, d, 0, d, H * d, 0, H * d, 0)
     assert torch.equal(y, z) and torch.equal(y[:1], x)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("et", ["bf16", "f32"])
+def test_rope_offsets_beyond_32_bits(A, et):
+    """Rows further apart than 2^31 elements in all, in and out."""
+    T, H, d, stride = 17, 2, 64, 2**27 + 8
+    t = torch.bfloat16 if et == "bf16" else torch.float32
+    x = torch.empty(T * stride, dtype=t, device=DEV).as_strided((T, H * d), (stride, 1))
+    y = torch.empty(T * stride, dtype=t, device=DEV).as_strided((T, H * d), (stride, 1))
+    q = torch.randn(T, H * d, device=DEV).to(t)
+    x.copy_(q)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV) * 1000
+    inv = torch.tensor(A.attn_rope_freqs(d)[0], dtype=torch.float64, device=DEV)
+    near = torch.empty_like(q)
+    A.attn_rope(q, None, near, None, pos, inv, T, H, 0, d, 0, d, H * d, 0, H * d, 0, et)
+    A.attn_rope(x, None, y, None, pos, inv, T, H, 0, d, 0, d, stride, 0, stride, 0, et)
+    assert torch.equal(y, near)

@@ -568,6 +568,21 @@ def test_two_row_groups_of_narrow_heads(A, fmt, n, page, num_splits):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt,B,n,Hkv,d", [("bf16", 70, 2, 2, 128), ("e4m3", 300, 1, 2, 64), ("bf16", 70, 18, 1, 128), ("e5m2", 45, 18, 8, 128),
+                                           ("bf16", 100, 1, 8, 128)])
+@pytest.mark.parametrize("num_splits", [0, 3])
+def test_more_groups_than_blocks_at_once(A, fmt, B, n, Hkv, d, num_splits):
+    """Many sequences: last splits after all others, longest first (up to 256 sequences)."""
+    rs = np.random.RandomState(27)
+    lens = [int(x) for x in rs.randint(n, 400, B)]
+    lens[3], lens[B - 1] = 0, 900
+    c = Case(fmt, Hkv, Hkv, d, 16, [n] * B, lens, "tree", 28)
+    c.run(A, num_splits)
+    assert A.attn_get_device_status() == 0
+    c.check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt,n", [("bf16", 2), ("e4m3", 20)])
 def test_replay_with_other_lengths(A, fmt, n):
     """The split size of a graph's call follows the lengths of each replay, a bad one among them."""
