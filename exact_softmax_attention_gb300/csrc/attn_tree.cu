@@ -490,15 +490,14 @@ void tree_plan(TreeParams& p, int d, bool f8, int num_splits) {
     p.tiles = tiles;
     const long long groups = (long long)B * Hkv * (tiles ? (rows + 127) / 128 : (rows + 15) / 16);
     const long long slots = (long long)num_sms * (tiles ? kTreeTileBlocks : tree_small_blocks(d, f8, rows));
+    const bool fit = num_splits == 0 && groups <= slots && B <= kTreeFitSeqs;
     long long c;
-    p.slots = 0;
-    if (num_splits == 0 && groups <= slots && B <= kTreeFitSeqs) {
+    if (fit) {
         // Fewer (sequence, kv head, row group) groups than blocks that fit at once: the blocks choose by the
         // lengths (tree_fit), as long as the table's capacity leaves anything to choose. The workspace is for
         // sequences that fill an eighth of it.
         c = (lmax * groups + 8 * slots - 1) / (8 * slots);
         if (c < 128) c = 128;
-        if ((lmax + c - 1) / c * groups > slots) p.slots = (int)slots;
     } else if (num_splits > 0) {
         c = (lmax + num_splits - 1) / num_splits;
     } else if (tiles) {
@@ -541,8 +540,9 @@ void tree_plan(TreeParams& p, int d, bool f8, int num_splits) {
     if (c < 64) c = 64;
     p.chunk = (int)c;
     p.max_splits = (int)((lmax + c - 1) / c);
-    if (p.max_splits == 1) p.slots = 0;
-    p.cluster = p.max_splits > 1 && p.max_splits <= kTreeCluster && groups * p.max_splits <= slots ? p.max_splits : 0;
+    const bool at_once = groups * p.max_splits <= slots;
+    p.slots = fit && !at_once ? (int)slots : 0;
+    p.cluster = p.max_splits > 1 && p.max_splits <= kTreeCluster && at_once ? p.max_splits : 0;
 }
 
 cudaError_t launch_attn_tree(const TreeParams& p_in, const TreeTmaps& tm, int d, int kv_format, cudaStream_t stream) {
