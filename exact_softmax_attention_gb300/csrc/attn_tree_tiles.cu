@@ -722,17 +722,18 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                 __syncwarp();
             }
             if (*odd_v && valid && !empty) {
-                // what was taken out of V replaces the outputs that it reaches (finite + inf = inf)
+                // what was taken out of V, added to what the products gave (finite + inf = inf; a value of a tile that
+                // the row sees in full may be infinite as well: inf - inf = NaN)
 #pragma unroll 1
                 for (int c = 0; c < D; ++c) {
                     const float x = nonfinite_sum<FMT>(p, pt, mrow, node, s, max(t_begin, s.ctx / kTileKeys * kTileKeys), t_end, kvh, D, c);
                     if (x == 0.0f) continue;
-                    if (part == -1)
-                        p.o[orow * D + c] = __float2bfloat16(x * inv);
-                    else if (kCluster)
-                        part_o[row * L::kPartRow + c] = x * inv;
-                    else
-                        p.ws_o[(orow * p.max_splits + part) * D + c] = x * inv;
+                    if (part == -1) {
+                        __nv_bfloat16* to = p.o + orow * D + c;
+                        *to = __float2bfloat16(__bfloat162float(*to) + x * inv);
+                    } else {
+                        (kCluster ? part_o + row * L::kPartRow : p.ws_o + (orow * p.max_splits + part) * D)[c] += x * inv;
+                    }
                 }
             }
             if (valid) {

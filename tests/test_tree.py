@@ -275,6 +275,26 @@ def test_visible_nonfinite_values_stay(A, n, where, value):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt,n", [("bf16", 3), ("e5m2", 3), ("bf16", 37), ("e5m2", 37)])
+@pytest.mark.parametrize("num_splits", [1, 2, 8, 20])
+def test_infinities_of_both_signs(A, fmt, n, num_splits):
+    """-inf in a context token of a tile that every row sees in full, +inf in a drafted one (in the same split or
+    another): inf - inf is NaN in the rows that see both, -inf in the others."""
+    c = Case(fmt, 4, 2, 64, 16, [n], [n + 700], "tree", 8)
+    for tok, value, code in ((600, -math.inf, 0xFC), (700 + 1, math.inf, 0x7C)):
+        row = int(c.pt[0, tok // 16]) * 16 + tok % 16
+        c.c[1].view(-1, 2, 64)[row, 1, 5] = value if fmt == "bf16" else code
+    c.run(A, num_splits)
+    assert A.attn_get_device_status() == 0
+    o = c.o[:n].float().cpu().numpy()
+    both = c.seen[0][:, 1]
+    assert both.any() and not both.all()
+    assert np.isnan(o[both, 2:, 5]).all() and np.isneginf(o[~both, 2:, 5]).all()
+    o[:, 2:, 5] = 0
+    assert np.isfinite(o).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt,n", [("e4m3", 3), ("e4m3", 30), ("e5m2", 30), ("bf16", 30)])
 def test_queries_of_any_range(A, fmt, n):
     """Rows of q scaled from 2^-100 to 2^12, with elements spread over 2^20 within a row, zero rows, and scores
