@@ -130,11 +130,12 @@ __device__ __forceinline__ uint32_t widen_pair(uint32_t w) {
 }
 
 // Widen the 64-row tile of 8-bit codes at src into f16 at dst (chunks of [64 rows x 128 bytes],
-// 128-byte swizzle); thread t of 128. kClean: take non-finite values out, return whether there were any.
+// 128-byte swizzle); thread t of 128. kClean: take non-finite values out, return whether there were any in the
+// first `held` rows.
 // Eight neighbouring threads take four 16-byte units each of a row pair (at d = 128 the lower units of
 // one row and the upper ones of the other), so that neither the loads nor the stores conflict.
 template <int D, int FMT, bool kClean>
-__device__ __forceinline__ bool widen_tile(uint32_t src, uint32_t dst, int t) {
+__device__ __forceinline__ bool widen_tile(uint32_t src, uint32_t dst, int t, int held) {
     constexpr int kHalves = D == 128 ? 2 : 1;  // units per thread and row pair
     constexpr int kPasses = 2;                 // row pairs t / 8 and t / 8 + 16
     const int odd_row = (t >> 2) & 1, row = 2 * (t >> 3) + odd_row, low = t & 3;
@@ -162,7 +163,7 @@ __device__ __forceinline__ bool widen_tile(uint32_t src, uint32_t dst, int t) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t keep = finite_halves(h[i], true);
-                odd |= keep != 0xFFFFFFFFu;
+                odd |= keep != 0xFFFFFFFFu && row + 32 * n < held;
                 h[i] &= keep;
             }
         }
@@ -479,6 +480,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                 const int st = i % NS;
                 if (!wait_all(&bars[L::bV + st], (uint32_t)((i / NS) & 1), abort_flag, wd)) break;
                 if (i >= first_mixed) {
+                    const int held = t_end - t_begin - i * kTileKeys;  // the boxes also bring rows behind the last token
                     const uint32_t vt = ring + st * 2 * L::kLoad + L::kLoad;
                     bool odd = false;
 #pragma unroll 4
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                             w[e] &= keep;
                         }
                         if (bad) sts128(vt + 16 * x, w[0], w[1], w[2], w[3]);
-                        odd |= bad;
+                        odd |= bad && ((x >> 3) & (kTileKeys - 1)) < held;
                     }
                     if (odd) *odd_v = 1;
                     __threadfence_block();
@@ -514,10 +516,10 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                 if (!wait_all(&bars[L::bWVFree + wb], (uint32_t)((i >> 1) & 1) ^ 1u, abort_flag, wd)) break;
                 const uint32_t src = ring + st * 2 * L::kLoad + L::kLoad, dst = wide + wb * L::kTile16;
                 if (i >= first_mixed) {
-                    if (widen_tile<D, FMT, true>(src, dst, t)) *odd_v = 1;
+                    if (widen_tile<D, FMT, true>(src, dst, t, t_end - t_begin - i * kTileKeys)) *odd_v = 1;
                     __threadfence_block();
                 } else {
-                    widen_tile<D, FMT, false>(src, dst, t);
+                    widen_tile<D, FMT, false>(src, dst, t, kTileKeys);
                 }
                 fence_smem_to_async();
                 __syncwarp();

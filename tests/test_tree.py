@@ -274,6 +274,37 @@ def test_visible_nonfinite_values_stay(A, n, where, value):
     assert (np.isposinf(o[hit]) if value == float("inf") else np.isnan(o[hit])).all()
 
 
+def shortest(f, calls=10, rounds=6):
+    """Least time of a call among others, in us."""
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    best = math.inf
+    for _ in range(rounds):
+        ev[0].record()
+        for _ in range(calls):
+            f()
+        ev[1].record()
+        ev[1].synchronize()
+        best = min(best, ev[0].elapsed_time(ev[1]) * 1e3 / calls)
+    return best
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,n,d,page", [("bf16", 16, 128, 16), ("e4m3", 16, 128, 64), ("e5m2", 40, 64, 64), ("bf16", 4, 128, 64)])
+def test_unused_slots_cost_nothing(A, fmt, n, d, page):
+    """NaN behind the last token of every sequence: the work is the same as over zeros there, and so is the time (half as
+    much again and 5 us are for the clock; a search for rows that see them took a millisecond or more)."""
+    times = []
+    for fill in (0, float("nan") if fmt == "bf16" else 0x7F):
+        c = Case(fmt, 8, 2, d, page, [n] * 4, [n + 900 + 3 * i for i in range(4)], "tree", 7)
+        for cache in c.c:
+            for b, l in enumerate(c.lens):
+                at = int(c.pt[b, (l - 1) // page]) * page
+                cache.view(-1, 2, d)[at + (l - 1) % page + 1:at + page] = fill
+        times.append(shortest(lambda: c.run(A)))
+        c.check()
+    assert times[1] <= 1.5 * times[0] + 5, times
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt,n", [("bf16", 3), ("e5m2", 3), ("bf16", 37), ("e5m2", 37)])
 @pytest.mark.parametrize("num_splits", [1, 2, 8, 20])
