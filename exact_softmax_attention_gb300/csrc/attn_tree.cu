@@ -81,7 +81,7 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[2]) {
 
 // GN: row slots that hold rows (8 or 16). kCluster: the splits of a group are the blocks of a cluster.
 template <int D, int GN, int FMT, bool kCluster>
-__global__ void __launch_bounds__(kWarps * 32, tree_small_blocks(D, FMT != ATTN_KV_BF16, GN)) tree_small_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, tree_small_blocks(D, FMT != ATTN_KV_BF16, GN)) tree_small_kernel(const __grid_constant__ TreeParams p) {
     grid_dependents_launch();
     using L = SmallLayout<D, GN, FMT>;
     constexpr bool F8 = FMT != ATTN_KV_BF16;
@@ -385,7 +385,6 @@ __global__ void __launch_bounds__(kWarps * 32, tree_small_blocks(D, FMT != ATTN_
             base[L::kRowO + d1] = oacc[nh][mt][3];
         }
     __syncthreads();
-    const bool odd = odd_v != 0;
     // four neighbouring elements per thread, so that the rows of a block take few rounds of latency
     constexpr int kPerRow = D / 4, kAtOnce = kWarps * 32 / kPerRow;
     const int d0 = threadIdx.x % kPerRow * 4;
@@ -406,12 +405,6 @@ __global__ void __launch_bounds__(kWarps * 32, tree_small_blocks(D, FMT != ATTN_
             const float4 o = *reinterpret_cast<const float4*>(sm_o + (w * GN + r) * L::kRowO + d0);
             acc[0] += f * o.x, acc[1] += f * o.y, acc[2] += f * o.z, acc[3] += f * o.w;
         }
-        if (odd) {
-            const int i = (r0 + r) / p.G;
-            for (int e = 0; e < 4; ++e)
-                acc[e] += nonfinite_sum<FMT>(p, pt, p.mask ? p.mask + (long long)(s.q0 + i) * p.mask_words : nullptr, i, s,
-                                             max(t_begin, s.ctx / kGroup * kGroup), t_end, kvh, D, d0 + e);
-        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[e] = ll == 0.0f ? 0.0f : acc[e] / ll * p.v_descale;
         const float lse = ll == 0.0f ? -INFINITY : mm * p.scale + logf(ll);
@@ -426,6 +419,11 @@ __global__ void __launch_bounds__(kWarps * 32, tree_small_blocks(D, FMT != ATTN_
             *reinterpret_cast<float4*>(p.ws_o + (orow * p.max_splits + split) * D + d0) = make_float4(acc[0], acc[1], acc[2], acc[3]);
             if (d0 == 0) p.ws_lse[orow * p.max_splits + split] = lse;
         }
+    }
+    if (odd_v) {  // (written before the barriers above; the same for the whole block)
+        __syncthreads();
+        for (int t = max(t_begin, s.ctx / kGroup * kGroup); t < t_end; t += 64)
+            add_nonfinite<D, FMT>(p, b, kvh, r0, warp, kWarps, R, t, t_end, nsplit == 1 ? -1 : joins ? -2 : split, part_o, D);
     }
     if (joins) cluster_join<D, D>(part_o, part_lse, p.o, p.lse, out_first, r0, R, p.G, p.Hq, p.cluster, nsplit);
 }

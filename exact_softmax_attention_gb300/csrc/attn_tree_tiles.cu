@@ -71,8 +71,9 @@ struct TileLayout {
     static constexpr int bK = 14, bV = bK + kStages, bKFree = bV + kStages, bVFree = bKFree + kStages;
     static constexpr int bClean = bVFree + kStages;
     static constexpr int kBars = bClean + kStages;
-    static constexpr int kMiscOff = kBarOff + kBars * 8;  // tensor-memory base, abort flag, odd-value flag, split
-    static constexpr int kBytes = kMiscOff + 16;
+    // tensor-memory base, abort flag, tiles with odd values, split; sequence, head group, tokens from, to
+    static constexpr int kMiscOff = kBarOff + kBars * 8;
+    static constexpr int kBytes = kMiscOff + 32;
     // the block's result for the cluster's join, over the tiles when they are done with: [row][kPartRow], LSE
     static constexpr int kPartRow = D + 4, kPartLse = kTileRows * kPartRow * 4;
     static_assert(kPartLse + kTileRows * 4 <= kBarOff, "room for the block's result");
@@ -174,6 +175,30 @@ __device__ __forceinline__ bool widen_tile(uint32_t src, uint32_t dst, int t, in
     return odd;
 }
 
+// The same with cleaning, for the few tiles that need it (out of line, to leave the loop's registers as they are).
+template <int D, int FMT>
+__device__ __noinline__ bool widen_clean(uint32_t src, uint32_t dst, int t, int held) {
+    return widen_tile<D, FMT, true>(src, dst, t, held);
+}
+
+// Tiles from this one on (six at most) hold drafted tokens or the end of the sequence.
+__device__ __forceinline__ int first_mixed_tile(int ctx, int t_begin) { return ctx <= t_begin ? 0 : (ctx - t_begin) / kTileKeys; }
+
+// What was taken out of V, tile by tile, to the outputs of a softmax warp. item: the block's sequence, head group and
+// tokens (from shared memory, so that nothing of this rare path stays in the kernel's registers); odd: bit i for
+// mixed tile i; split and part as for add_nonfinite.
+template <int D, int FMT>
+__device__ __noinline__ void add_odd_values(const TreeParams& p, const int* item, int odd, int split, float* part) {
+    const int b = item[0], kvh = item[1] / p.groups, r0 = item[1] % p.groups * kTileRows, first = (threadIdx.x >> 5 & 3) * 32;
+    TreeSeq s;
+    if (!tree_seq(p, b, s)) return;
+    const int rows = min(min(kTileRows, s.n * p.G - r0), first + 32), tile = first_mixed_tile(s.ctx, item[2]);
+    if (first >= rows) return;
+    for (; odd; odd &= odd - 1)
+        add_nonfinite<D, FMT>(p, b, kvh, r0, first, 1, rows, item[2] + (tile + __ffs(odd) - 1) * kTileKeys, item[3], split, part,
+                              TileLayout<D, FMT>::kPartRow);
+}
+
 // Four values to four e4m3 codes (they are in range and finite).
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     uint16_t lo, hi;
@@ -193,7 +218,7 @@ __host__ __device__ constexpr uint32_t idesc8(uint32_t b_format, uint32_t M, uin
 
 template <int D, int FMT, bool kCluster>
 __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
-    tree_tile_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
+    tree_tile_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
     grid_dependents_launch();
     using L = TileLayout<D, FMT>;
     constexpr bool F8 = L::kF8;
@@ -243,8 +268,9 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
-    volatile int* odd_v = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 8);
+    int* odd_v = reinterpret_cast<int*>(smem + L::kMiscOff + 8);
     volatile int* part_slot = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 12);  // (keeps it out of the registers)
+    int* item = reinterpret_cast<int*>(smem + L::kMiscOff + 16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t wd = p.watchdog_ns;
     const int* pt = p.page_table + (long long)b * p.max_pages;
@@ -271,6 +297,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
         }
         *abort_flag = 0;
         *odd_v = 0;
+        item[0] = b, item[1] = hg, item[2] = t_begin, item[3] = t_end;
         *part_slot = nsplit == 1 ? -1 : joins ? -2 : split;
         fence_mbar_init();
     }
@@ -287,8 +314,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t ring = smem_u32(smem + L::kRingOff);
-    // tiles from this one on hold drafted tokens or the end of the sequence
-    const int first_mixed = s.ctx <= t_begin ? 0 : (s.ctx - t_begin) / kTileKeys;
+    const int first_mixed = first_mixed_tile(s.ctx, t_begin);
 
     if (warp == 0 || warp == 2) {
         // ---------------------------------------------------------------- loads of K (warp 0), V (warp 2)
@@ -497,7 +523,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                         if (bad) sts128(vt + 16 * x, w[0], w[1], w[2], w[3]);
                         odd |= bad && ((x >> 3) & (kTileKeys - 1)) < held;
                     }
-                    if (odd) *odd_v = 1;
+                    if (odd) atomicOr(odd_v, 1 << (i - first_mixed));
                     __threadfence_block();
                     fence_smem_to_async();
                 }
@@ -510,13 +536,14 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
         if constexpr (F8) {
             const int t = threadIdx.x & 127;
             const uint32_t wide = smem_u32(smem + L::kWideOff);
-            for (int i = 0; i < tiles; ++i) {
+            // (two loops and the cleaning out of line: as branches of one loop 431 us became 485, 64 x U[1K, 32K], 16 drafted)
+            auto step = [&](int i, auto clean) {
                 const int st = i % NS, wb = i & 1;
-                if (!wait_all(&bars[L::bV + st], (uint32_t)((i / NS) & 1), abort_flag, wd)) break;
-                if (!wait_all(&bars[L::bWVFree + wb], (uint32_t)((i >> 1) & 1) ^ 1u, abort_flag, wd)) break;
+                if (!wait_all(&bars[L::bV + st], (uint32_t)((i / NS) & 1), abort_flag, wd)) return false;
+                if (!wait_all(&bars[L::bWVFree + wb], (uint32_t)((i >> 1) & 1) ^ 1u, abort_flag, wd)) return false;
                 const uint32_t src = ring + st * 2 * L::kLoad + L::kLoad, dst = wide + wb * L::kTile16;
-                if (i >= first_mixed) {
-                    if (widen_tile<D, FMT, true>(src, dst, t, t_end - t_begin - i * kTileKeys)) *odd_v = 1;
+                if constexpr (decltype(clean)::value) {
+                    if (widen_clean<D, FMT>(src, dst, t, t_end - t_begin - i * kTileKeys)) atomicOr(odd_v, 1 << (i - first_mixed));
                     __threadfence_block();
                 } else {
                     widen_tile<D, FMT, false>(src, dst, t, kTileKeys);
@@ -527,7 +554,12 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                     mbar_arrive(&bars[L::bWV + wb]);
                     mbar_arrive(&bars[L::bVFree + st]);
                 }
-            }
+                return true;
+            };
+            int i = 0;
+            bool go = true;
+            for (; go && i < min(first_mixed, tiles); ++i) go = step(i, std::false_type{});
+            for (; go && i < tiles; ++i) go = step(i, std::true_type{});
         }
     } else if (warp - 4 < row_warps) {
         // ---------------------------------------------------------------- softmax and output
@@ -723,21 +755,6 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                 }
                 __syncwarp();
             }
-            if (*odd_v && valid && !empty) {
-                // what was taken out of V, added to what the products gave (finite + inf = inf; a value of a tile that
-                // the row sees in full may be infinite as well: inf - inf = NaN)
-#pragma unroll 1
-                for (int c = 0; c < D; ++c) {
-                    const float x = nonfinite_sum<FMT>(p, pt, mrow, node, s, max(t_begin, s.ctx / kTileKeys * kTileKeys), t_end, kvh, D, c);
-                    if (x == 0.0f) continue;
-                    if (part == -1) {
-                        __nv_bfloat16* to = p.o + orow * D + c;
-                        *to = __float2bfloat16(__bfloat162float(*to) + x * inv);
-                    } else {
-                        (kCluster ? part_o + row * L::kPartRow : p.ws_o + (orow * p.max_splits + part) * D)[c] += x * inv;
-                    }
-                }
-            }
             if (valid) {
                 const float lse = empty ? -INFINITY : m * scale + logf(l);
                 if (part == -1)
@@ -757,6 +774,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, kCols);
     if (threadIdx.x == 0 && *abort_flag) atomicCAS(p.status, 0, kDevTimeout);
+    if (warp >= 4 && warp < 8 && *odd_v) add_odd_values<D, FMT>(p, item, *odd_v, *part_slot, part_o);
     if (kCluster && *part_slot == -2) cluster_join<D, L::kPartRow>(part_o, part_lse, p.o, p.lse, out_first, r0, R, p.G, p.Hq, p.cluster, nsplit);
 }
 

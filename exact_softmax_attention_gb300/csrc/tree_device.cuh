@@ -359,20 +359,62 @@ __device__ __forceinline__ float cached_value(const void* cache, long long e) {
         return half_value((uint16_t)fp8x2_f16x2<FMT>(static_cast<const uint8_t*>(cache)[e]));
 }
 
-// Sum of the non-finite values in column d of the V rows of tokens [t0, t1) that row i sees: what the
-// products left out of the tiles where they took them for zero.
-template <int FMT>
-__device__ __forceinline__ float nonfinite_sum(const TreeParams& p, const int* pt, const unsigned long long* mrow, int i, const TreeSeq& s,
-                               int t0, int t1, int kvh, int D, int d) {
-    float sum = 0.0f;
-    for (int t = t0; t < t1; ++t) {
-        if (!(tree_window(mrow, p.mask_words, i, s.ctx, s.len, t) & 1)) continue;
-        const int row = cache_row(p, pt, t);
-        if (row < 0) continue;
-        const float v = cached_value<FMT>(p.v_cache, ((long long)row * p.Hkv + kvh) * D + d);
-        if (!isfinite(v)) sum += v;
+// Adds to the outputs of a warp's rows (first, first + step, ... < rows of the group that starts at row r0; 32 at
+// most) the non-finite values of V of the tokens [t0, t0 + 64) below t_end that each sees: what the products
+// left out of the tiles where they took them for zero. Every lane owns D / 32 columns and keeps for each which
+// tokens hold infinities and NaN, so the values are read once for all rows. split >= 0: the outputs are those
+// of that split in the workspace; -1: the call's; -2: rows part_stride apart from `part` on. (A rare path, out
+// of line: the kernels' registers stay as they are.)
+template <int D, int FMT>
+__device__ __noinline__ void add_nonfinite(const TreeParams& p, int b, int kvh, int r0, int first, int step, int rows, int t0, int t_end,
+                                           int split, float* part, int part_stride) {
+    constexpr int PER = D / 32;
+    const int lane = threadIdx.x & 31;
+    TreeSeq s;
+    if (!tree_seq(p, b, s)) return;
+    const int* pt = p.page_table + (long long)b * p.max_pages;
+    unsigned long long seen = 0;  // by row first + lane step
+    if (first + lane * step < rows) {
+        const int i = (r0 + first + lane * step) / p.G;
+        seen = tree_window(p.mask ? p.mask + (long long)(s.q0 + i) * p.mask_words : nullptr, p.mask_words, i, s.ctx, s.len, t0);
+        if (t_end - t0 < 64) seen &= (1ull << (t_end - t0)) - 1;
     }
-    return sum;
+    int row[2];  // of tokens lane and lane + 32
+#pragma unroll
+    for (int e = 0; e < 2; ++e) row[e] = t0 + lane + 32 * e < t_end ? cache_row(p, pt, t0 + lane + 32 * e) : -1;
+    unsigned long long pos[PER] = {}, neg[PER] = {}, nan[PER] = {};
+#pragma unroll 8
+    for (int t = 0; t < 64; ++t) {
+        const int r = __shfl_sync(0xffffffffu, t < 32 ? row[0] : row[1], t & 31);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const float v = r >= 0 ? cached_value<FMT>(p.v_cache, ((long long)r * p.Hkv + kvh) * D + lane * PER + e) : 0.0f;
+            if (!isfinite(v)) (isnan(v) ? nan : v > 0 ? pos : neg)[e] |= 1ull << t;
+        }
+    }
+    for (int k = 0; first + k * step < rows; ++k) {
+        const unsigned long long w = __shfl_sync(0xffffffffu, seen, k);
+        const int r = first + k * step, i = (r0 + r) / p.G;
+        const long long orow = (long long)(s.q0 + i) * p.Hq + kvh * p.G + (r0 + r - i * p.G);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            float x = 0.0f;
+            if (w & pos[e]) x += INFINITY;
+            if (w & neg[e]) x -= INFINITY;
+            if (w & nan[e]) x = __int_as_float(0x7fffffff);
+            if (x == 0.0f) continue;
+            x *= p.v_descale;  // (its sign; the weight of a seen token is above 0)
+            const int c = lane * PER + e;
+            if (split == -1) {
+                __nv_bfloat16* to = p.o + orow * D + c;
+                *to = __float2bfloat16(__bfloat162float(*to) + x);
+            } else if (split == -2) {
+                part[r * part_stride + c] += x;
+            } else {
+                p.ws_o[(orow * p.max_splits + split) * D + c] += x;
+            }
+        }
+    }
 }
 
 // Is either 16-bit half of w non-finite (f16 when half_fmt, else bf16)? Mask with ones in the finite

@@ -306,6 +306,30 @@ def test_unused_slots_cost_nothing(A, fmt, n, d, page):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt,n,d,page", [("bf16", 16, 128, 16), ("e4m3", 64, 128, 64), ("e5m2", 200, 64, 64), ("bf16", 256, 64, 7),
+                                          ("bf16", 4, 128, 64), ("e4m3", 8, 64, 7)])
+@pytest.mark.parametrize("where", ["a masked token", "every drafted token"])
+def test_time_of_nonfinite_drafted_values(A, fmt, n, d, page, where):
+    """Non-finite values of drafted tokens, that no row sees or that most do: at most one pass over the 64-token tiles
+    that hold drafted tokens, read once per warp of rows. 64 rows of V in loads eight at a time (2 us each with the look-ups), and,
+    where they are seen, 32 rows of outputs read and written at 1 us: 50 us a tile at most. (Row by row, column by column
+    and token by token it took milliseconds.)"""
+    times = []
+    for fill in (0, float("nan") if fmt == "bf16" else 0x7F):
+        c = Case(fmt, 8, 2, d, page, [n] * 4, [n + 900 + 3 * i for i in range(4)], "tree", 7)
+        for b, l in enumerate(c.lens):
+            for t in [l - n // 2] if where == "a masked token" else range(l - n, l):
+                c.c[1].view(-1, 2, d)[int(c.pt[b, t // page]) * page + t % page] = fill
+        if where == "a masked token":
+            m = c.mask.cpu().numpy().view(np.uint64)
+            m[:, (n - n // 2) // 64] &= ~(np.uint64(1) << np.uint64((n - n // 2) % 64))
+            c.mask = torch.from_numpy(m.view(np.int64)).to(DEV)
+        times.append(shortest(lambda: c.run(A), 3))
+    tiles = 1 if where == "a masked token" else (n + 63) // 64 + 1
+    assert times[1] <= 1.5 * times[0] + 50 * tiles, times
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt,n", [("bf16", 3), ("e5m2", 3), ("bf16", 37), ("e5m2", 37)])
 @pytest.mark.parametrize("num_splits", [1, 2, 8, 20])
 def test_infinities_of_both_signs(A, fmt, n, num_splits):
