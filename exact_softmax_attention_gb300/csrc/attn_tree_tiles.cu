@@ -301,7 +301,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
         *part_slot = nsplit == 1 ? -1 : joins ? -2 : split;
         fence_mbar_init();
     }
-    if (warp == 0 && lane == 0) {
+    if (p.box_rows > 1 && warp == 0 && lane == 0) {  // (else there are no maps)
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }

@@ -622,6 +622,19 @@ def test_tiles_split_by_the_lengths(A, fmt, n, d, batch):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt,n,d,page", [("bf16", 20, 128, 7), ("bf16", 40, 64, 1), ("e4m3", 20, 128, 24), ("e5m2", 40, 64, 13)])
+@pytest.mark.parametrize("batch", ["ragged", "one_long", "wide_table"])
+def test_tiles_of_odd_pages_split_by_the_lengths(A, fmt, n, d, page, batch):
+    """Page sizes that no box divides (rows are copied one by one, and there are no tensor maps)."""
+    lens, times = BATCHES[batch]
+    lens = [x and max(x, n) for x in lens]
+    c = widened(Case(fmt, 8, 8, d, page, [n] * len(lens), lens, "tree", 25), times)
+    c.run(A)
+    assert A.attn_get_device_status() == 0
+    c.check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3", "e5m2"])
 @pytest.mark.parametrize("n,page,num_splits", [(5, 16, 0), (8, 7, 1), (7, 1, 3), (6, 64, 12), (8, 16, 8)])
 def test_two_row_groups_of_narrow_heads(A, fmt, n, page, num_splits):
