@@ -17,6 +17,8 @@
 #include "launch.cuh"
 #include "tree_device.cuh"
 
+#include <float.h>
+
 namespace attn {
 namespace {
 
@@ -174,31 +176,52 @@ __global__ void __launch_bounds__(kWarps * 32, tree_small_blocks(D, FMT != ATTN_
     }
 
     // ---- query fragments. 8-bit caches: column 2 qd + e of k-step kk is d = (D/4) qd + 4 kk + e,
-    // column 2 qd + 8 + e is that + 2
+    // column 2 qd + 8 + e is that + 2; and f16, after scaling each row by a power of two that brings its largest
+    // magnitude into [2^14, 2^15): exact for elements down to 2^-31 of that, within 2^-39 of it for smaller ones. The
+    // power goes back into the row's factor of the scores (exactly), so nothing else notices it.
     uint32_t aq[D / 16][4];
+    float s0 = p.scale_log2, s1 = p.scale_log2;  // scores of the lane's two rows to exponents of two
     {
         const uint32_t* q0p = reinterpret_cast<const uint32_t*>(p.q + (v0 ? out_row(g0) : 0) * D);
         const uint32_t* q1p = reinterpret_cast<const uint32_t*>(p.q + (v1 ? out_row(g0 + 8) : 0) * D);
-        auto word = [&](const uint32_t* src, bool valid, int c) -> uint32_t {
-            if (!valid) return 0u;
-            const uint32_t w = __ldg(src + c);
-            const float lo = __uint_as_float(w << 16) * p.q_sign, hi = __uint_as_float(w & 0xFFFF0000u) * p.q_sign;
-            return F8 ? pack_half2(lo, hi) : pack_bf16x2(lo, hi);
-        };
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             const int c = F8 ? (D / 8) * qd + 2 * kk : kk * 8 + qd, step = F8 ? 1 : 4;
-            aq[kk][0] = word(q0p, v0, c);
-            aq[kk][1] = word(q1p, v1, c);
-            aq[kk][2] = word(q0p, v0, c + step);
-            aq[kk][3] = word(q1p, v1, c + step);
+            aq[kk][0] = v0 ? __ldg(q0p + c) : 0u;
+            aq[kk][1] = v1 ? __ldg(q1p + c) : 0u;
+            aq[kk][2] = v0 ? __ldg(q0p + c + step) : 0u;
+            aq[kk][3] = v1 ? __ldg(q1p + c + step) : 0u;
         }
+        float mul[2] = {p.q_sign, p.q_sign};
+        if constexpr (F8) {
+#pragma unroll
+            for (int x = 0; x < GN / 8; ++x) {
+                uint32_t top = 0;  // the row's largest magnitude, as bf16
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int e = x; e < 4; e += 2) top = max(top, max(aq[kk][e] & 0x7FFFu, (aq[kk][e] >> 16) & 0x7FFFu));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int up = top == 0 || top >= 0x7F80u ? 0 : min(120, 141 - (int)(top >> 7));
+                mul[x] *= __int_as_float((127 + up) << 23);
+                // (a factor that rounds to 0, or to infinity, would turn scores of -inf, or 0, into NaN)
+                (x ? s1 : s0) = fminf(fmaxf(p.scale_log2 * __int_as_float((127 - up) << 23), 0x1p-126f), FLT_MAX);
+            }
+        }
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t w = aq[kk][e];
+                const float lo = __uint_as_float(w << 16) * mul[e & 1], hi = __uint_as_float(w & 0xFFFF0000u) * mul[e & 1];
+                aq[kk][e] = F8 ? pack_half2(lo, hi) : pack_bf16x2(lo, hi);
+            }
     }
 
     constexpr int NH = GN / 8;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
     float oacc[NH][D / 16][4] = {};
-    const float sl2 = p.scale_log2;
     const int lm_row = (lane & 7) + ((lane >> 4) << 3), lm_par = (lane >> 3) & 1;
 
     for (int i = 0; i < mine; ++i) {
@@ -284,10 +307,10 @@ __global__ void __launch_bounds__(kWarps * 32, tree_small_blocks(D, FMT != ATTN_
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
         const float mc0 = fmaxf(m0, mx0), mc1 = fmaxf(m1, mx1);
-        const bool need = ((mc0 - m0) * sl2 > p.rescale_thr) || (GN == 16 && (mc1 - m1) * sl2 > p.rescale_thr);
+        const bool need = ((mc0 - m0) * s0 > p.rescale_thr) || (GN == 16 && (mc1 - m1) * s1 > p.rescale_thr);
         if (__any_sync(0xffffffffu, need)) {
-            const float a0 = m0 == -INFINITY ? 0.0f : ex2_mufu((m0 - mc0) * sl2);
-            const float a1 = m1 == -INFINITY ? 0.0f : ex2_mufu((m1 - mc1) * sl2);
+            const float a0 = m0 == -INFINITY ? 0.0f : ex2_mufu((m0 - mc0) * s0);
+            const float a1 = m1 == -INFINITY ? 0.0f : ex2_mufu((m1 - mc1) * s1);
             l0 *= a0, l1 *= a1;
             m0 = mc0, m1 = mc1;
             const int src = qd * 8;  // lane of row 2 qd; O^T columns are rows 2 qd, 2 qd + 1 (+ 8)
@@ -304,14 +327,14 @@ __global__ void __launch_bounds__(kWarps * 32, tree_small_blocks(D, FMT != ATTN_
                 }
             }
         }
-        const float n0 = m0 == -INFINITY ? 0.0f : -m0 * sl2, n1 = m1 == -INFINITY ? 0.0f : -m1 * sl2;
+        const float n0 = m0 == -INFINITY ? 0.0f : -m0 * s0, n1 = m1 == -INFINITY ? 0.0f : -m1 * s1;
         float pr[2][4];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
-            pr[nt][0] = ex2_mufu(fmaf(sc[nt][0], sl2, n0));
-            pr[nt][1] = ex2_mufu(fmaf(sc[nt][1], sl2, n0));
-            pr[nt][2] = ex2_mufu(fmaf(sc[nt][2], sl2, n1));
-            pr[nt][3] = ex2_mufu(fmaf(sc[nt][3], sl2, n1));
+            pr[nt][0] = ex2_mufu(fmaf(sc[nt][0], s0, n0));
+            pr[nt][1] = ex2_mufu(fmaf(sc[nt][1], s0, n0));
+            pr[nt][2] = ex2_mufu(fmaf(sc[nt][2], s1, n1));
+            pr[nt][3] = ex2_mufu(fmaf(sc[nt][3], s1, n1));
         }
         l0 += (pr[0][0] + pr[0][1]) + (pr[1][0] + pr[1][1]);
         l1 += (pr[0][2] + pr[0][3]) + (pr[1][2] + pr[1][3]);
@@ -365,10 +388,10 @@ __global__ void __launch_bounds__(kWarps * 32, tree_small_blocks(D, FMT != ATTN_
     float* sm_m = sm_o + kWarps * GN * L::kRowO;
     float* sm_l = sm_m + kWarps * GN;
     if (qd == 0) {
-        sm_m[warp * GN + g0] = m0;
+        sm_m[warp * GN + g0] = F8 ? m0 * s0 : m0;  // (8-bit caches: as an exponent of two, the row's factor included)
         sm_l[warp * GN + g0] = l0;
         if (GN == 16) {
-            sm_m[warp * GN + g0 + 8] = m1;
+            sm_m[warp * GN + g0 + 8] = F8 ? m1 * s1 : m1;
             sm_l[warp * GN + g0 + 8] = l1;
         }
     }
@@ -400,14 +423,14 @@ __global__ void __launch_bounds__(kWarps * 32, tree_small_blocks(D, FMT != ATTN_
         for (int w = 0; w < kWarps; ++w) {
             // a warp without a visible key has m = -inf and only zeros (or NaN, which has to stay)
             const float mw = sm_m[w * GN + r];
-            const float f = mw == -INFINITY ? 1.0f : ex2_mufu((mw - mm) * sl2);
+            const float f = mw == -INFINITY ? 1.0f : ex2_mufu(F8 ? mw - mm : (mw - mm) * p.scale_log2);
             ll += f * sm_l[w * GN + r];
             const float4 o = *reinterpret_cast<const float4*>(sm_o + (w * GN + r) * L::kRowO + d0);
             acc[0] += f * o.x, acc[1] += f * o.y, acc[2] += f * o.z, acc[3] += f * o.w;
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[e] = ll == 0.0f ? 0.0f : acc[e] / ll * p.v_descale;
-        const float lse = ll == 0.0f ? -INFINITY : mm * p.scale + logf(ll);
+        const float lse = ll == 0.0f ? -INFINITY : mm * (F8 ? 0.6931471805599453f : p.scale) + logf(ll);
         const long long orow = out_row(r);
         if (nsplit == 1) {
             *reinterpret_cast<uint2*>(p.o + orow * D + d0) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));

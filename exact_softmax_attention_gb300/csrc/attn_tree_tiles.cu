@@ -46,6 +46,8 @@
 #include "launch.cuh"
 #include "tree_device.cuh"
 
+#include <float.h>
+
 namespace attn {
 namespace {
 
@@ -639,8 +641,9 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[L::bQ]);
         }
-        // (a product that rounds to 0 would turn masked scores, -inf, into NaN)
-        const float scale = F8 ? p.scale * row_scale : p.scale, sl2 = F8 ? fmaxf(p.scale_log2 * row_scale, 0x1p-126f) : p.scale_log2;
+        // (a product that rounds to 0, or to infinity, would turn masked scores, -inf, or scores of 0 into NaN)
+        const float scale = F8 ? fminf(p.scale * row_scale, FLT_MAX) : p.scale;
+        const float sl2 = F8 ? fminf(fmaxf(p.scale_log2 * row_scale, 0x1p-126f), FLT_MAX) : p.scale_log2;
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int i = 0; i < tiles; ++i) {

@@ -362,10 +362,11 @@ attn_status_t attn_kv_read_paged(const void* k_cache, const void* v_cache, void*
  * recorded.
  * Arithmetic: products on the tensor cores with fp32 accumulation, fp32 softmax, probabilities
  * rounded to bf16 (8-bit caches: f16) for the second product. bf16 caches: bf16 products. 8-bit
- * caches, up to 16 rows (max_q * Hq / Hkv; d = 64 up to 32 where the table holds few tokens): codes widened
- * exactly to f16, q converted to f16 (see attn_decode_paged_fp8). More rows: keys multiplied as they are by q split into two e4m3 parts (after
- * scaling each row by a power of two), exact for elements down to 2^-9 of the row's largest and
- * within 2^-17 of that for smaller ones; values widened exactly to f16.
+ * caches take q of any bf16 range, each row scaled by a power of two first, which the scores' factor gives back:
+ * up to 16 rows (max_q * Hq / Hkv; d = 64 up to 32 where the table holds few tokens) codes widened exactly to f16
+ * and q as f16, exact for elements down to 2^-31 of the row's largest; more rows: keys multiplied as they are by q
+ * split into two e4m3 parts, exact for elements down to 2^-9 of the row's largest and within 2^-17 of that for
+ * smaller ones; values widened exactly to f16.
  * Up to eight splits per sequence, when all blocks fit on the GPU at once: one launch (the splits of a group are a
  * thread-block cluster, which joins them) and no workspace. Else workspace, launches and programmatic dependents as
  * for attn_decode_paged: partial outputs of the splits (T * Hq * splits * (d + 1) + 1 floats) from the library's

@@ -367,6 +367,36 @@ def test_queries_of_any_range(A, fmt, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("n,d,wide", [(1, 128, 1), (3, 128, 1), (3, 64, 1), (6, 64, 1), (6, 64, 4000), (2, 64, 1)])
+@pytest.mark.parametrize("power", [-100, -40, 20, 100])
+def test_queries_of_any_range_in_few_rows(A, fmt, n, d, wide, power):
+    """8-bit caches: what q may be does not depend on the number of rows or on the width of the table. Rows of 2^power,
+    one 2^8 above and one of zeros, elements spread over 2^20 within a row, and the scale that brings them back."""
+    c = widened(Case(fmt, 8, 2, d, 16, [n, n], [n + 250, n + 40], "tree", 21), wide)
+    rs = np.random.RandomState(4)
+    c.q.copy_((c.q.double() * torch.from_numpy(2.0 ** (power - rs.randint(0, 20, c.q.shape).astype(float))).to(DEV)).bfloat16())
+    c.q[0, 2] *= 2.0**8
+    c.q[0, 3] = 0
+    scale = 2.0 ** (-power - 2)
+    c.run(A, 0, scale)
+    assert A.attn_get_device_status() == 0
+    c.check(scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,n,d", [("e4m3", 3, 128), ("e5m2", 6, 64), ("e4m3", 30, 64), ("bf16", 3, 128), ("bf16", 30, 128)])
+def test_large_queries_on_zero_keys(A, fmt, n, d):
+    """Scores of 0 from factors whose product leaves fp32: a plain mean over what each row sees."""
+    c = Case(fmt, 4, 1, d, 16, [n], [n + 70], "any", 25)
+    c.q.fill_(2.0**125)
+    c.c[0].zero_()
+    c.run(A, 2, 2.0**120 if fmt == "bf16" else 2.0**125)
+    assert A.attn_get_device_status() == 0
+    c.check(1.0)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt,n", [("e4m3", 30), ("bf16", 30), ("bf16", 3)])
 def test_vanishing_queries_and_scales(A, fmt, n):
     """Scores far below the range of fp32: a plain mean over what each row sees."""
