@@ -183,6 +183,28 @@ __device__ __noinline__ bool widen_clean(uint32_t src, uint32_t dst, int t, int 
     return widen_tile<D, FMT, true>(src, dst, t, held);
 }
 
+// Non-finite values out of a 16-bit V tile of kBytes bytes at vt, by a warp; true when there were any in the first
+// `held` rows (the boxes also bring rows behind the last token).
+template <int kBytes>
+__device__ __noinline__ bool clean_tile(uint32_t vt, int held) {
+    bool odd = false;
+#pragma unroll 4
+    for (int x = threadIdx.x & 31; x < kBytes / 16; x += 32) {
+        uint32_t w[4];
+        lds128(vt + 16 * x, w);
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t keep = finite_halves(w[e], false);
+            bad |= keep != 0xFFFFFFFFu;
+            w[e] &= keep;
+        }
+        if (bad) sts128(vt + 16 * x, w[0], w[1], w[2], w[3]);
+        odd |= bad && ((x >> 3) & (kTileKeys - 1)) < held;
+    }
+    return odd;
+}
+
 // Tiles from this one on (six at most) hold drafted tokens or the end of the sequence.
 __device__ __forceinline__ int first_mixed_tile(int ctx, int t_begin) { return ctx <= t_begin ? 0 : (ctx - t_begin) / kTileKeys; }
 
@@ -508,23 +530,7 @@ __global__ void __launch_bounds__((TileLayout<D, FMT>::kThreads), 2)
                 const int st = i % NS;
                 if (!wait_all(&bars[L::bV + st], (uint32_t)((i / NS) & 1), abort_flag, wd)) break;
                 if (i >= first_mixed) {
-                    const int held = t_end - t_begin - i * kTileKeys;  // the boxes also bring rows behind the last token
-                    const uint32_t vt = ring + st * 2 * L::kLoad + L::kLoad;
-                    bool odd = false;
-#pragma unroll 4
-                    for (int x = lane; x < L::kTile16 / 16; x += 32) {
-                        uint32_t w[4];
-                        lds128(vt + 16 * x, w);
-                        bool bad = false;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t keep = finite_halves(w[e], false);
-                            bad |= keep != 0xFFFFFFFFu;
-                            w[e] &= keep;
-                        }
-                        if (bad) sts128(vt + 16 * x, w[0], w[1], w[2], w[3]);
-                        odd |= bad && ((x >> 3) & (kTileKeys - 1)) < held;
-                    }
+                    const bool odd = clean_tile<L::kTile16>(ring + st * 2 * L::kLoad + L::kLoad, t_end - t_begin - i * kTileKeys);
                     if (odd) atomicOr(odd_v, 1 << (i - first_mixed));
                     __threadfence_block();
                     fence_smem_to_async();

@@ -383,13 +383,16 @@ __device__ __noinline__ void add_nonfinite(const TreeParams& p, int b, int kvh, 
 #pragma unroll
     for (int e = 0; e < 2; ++e) row[e] = t0 + lane + 32 * e < t_end ? cache_row(p, pt, t0 + lane + 32 * e) : -1;
     unsigned long long pos[PER] = {}, neg[PER] = {}, nan[PER] = {};
-#pragma unroll 8
+#pragma unroll 4
     for (int t = 0; t < 64; ++t) {
         const int r = __shfl_sync(0xffffffffu, t < 32 ? row[0] : row[1], t & 31);
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             const float v = r >= 0 ? cached_value<FMT>(p.v_cache, ((long long)r * p.Hkv + kvh) * D + lane * PER + e) : 0.0f;
-            if (!isfinite(v)) (isnan(v) ? nan : v > 0 ? pos : neg)[e] |= 1ull << t;
+            const unsigned long long bit = 1ull << t;
+            pos[e] |= v == INFINITY ? bit : 0;
+            neg[e] |= v == -INFINITY ? bit : 0;
+            nan[e] |= isnan(v) ? bit : 0;
         }
     }
     for (int k = 0; first + k * step < rows; ++k) {
