@@ -507,7 +507,7 @@ cudaError_t launch_fmt(const TreeParams& p, int fmt, cudaStream_t stream) {
 void tree_plan(TreeParams& p, int d, bool f8, int num_splits) {
     const int B = p.B, Hkv = p.Hkv, rows = p.max_q * p.G, num_sms = p.num_sms;
     const long long lmax = (long long)p.max_pages * p.page_size;
-    const bool tiles = tree_takes_tiles(rows, d, f8, (long long)B * Hkv * lmax, num_sms);
+    const bool tiles = tree_takes_tiles(rows, d, f8, p.page_size, B, Hkv, lmax, num_sms);
     p.tiles = tiles;
     const long long groups = (long long)B * Hkv * (tiles ? (rows + 127) / 128 : (rows + 15) / 16);
     const long long slots = (long long)num_sms * (tiles ? kTreeTileBlocks : tree_small_blocks(d, f8, rows));

@@ -51,15 +51,27 @@ struct TreeTmaps {
 cudaError_t launch_attn_tree(const TreeParams& p, const TreeTmaps& tm, int d, int kv_format, cudaStream_t stream);
 cudaError_t launch_tree_tiles(const TreeParams& p, const TreeTmaps& tm, int d, int kv_format, cudaStream_t stream);
 
+// Sequences up to which the blocks choose the split size by the lengths (two per lane of a warp).
+constexpr int kTreeFitSeqs = 64;
+
 // 128-row tiles, or 16-row products? The latter up to 16 rows per kv head, where the cache is read once either way.
-// Up to 32 rows they read it twice (once through the L2), but start sooner and need no padding: with d = 64 and
-// little work (tokens: of all sequences and kv heads, by the capacity of the page table) they are faster. Measured,
-// 24 rows, 16-row products / tiles, us: 8-bit codes 48 sequences of up to 8000 tokens x 3 kv heads (7600 tokens
-// per SM) 34 / 39 to 41 / 42, 16 of 4096 x 8 (3400) 36.5 / 34.5, 64 of up to 1000 x 8 (3400) 26 / 28, 64 of up to
-// 8000 x 8 114 / 87; bf16 64 of up to 1000 x 3 (1300) 17 / 19, 16 of 4096 x 8 38.6 / 34.4. With d = 128: 8-bit codes 64 of
-// up to 1000 x 8 46 / 34, bf16 48 / 40.
-inline bool tree_takes_tiles(long long rows, int d, bool f8, long long tokens, int num_sms) {
-    return rows > 16 && (d != 64 || rows > 32 || tokens > (f8 ? 8192LL : 2048LL) * num_sms);
+// Up to 32 rows they read it twice (once through the L2), but start sooner and need no padding: with d = 64 they are
+// faster while an SM has few tokens, by the capacity of the page table (the lengths are not known here). The tiles
+// catch up later over codes (they widen V) and where no box divides the pages (one warp copies row by row). Measured,
+// 17 to 32 rows, 1 to 64 sequences x 1 to 8 kv heads, full and half-full tables, 16-row products / tiles: pages of 16, codes,
+// 850 tokens per SM 17.2 / 18.8 us, 1730 23.9 / 24.2, 3400 38.1 / 37.6, 6900 63.5 / 55.2; bf16 430 13.8 / 15.2, 860 17.0 / 17.3, 1730
+// 24.3 / 21.9; pages of 7, codes 3400 36.6 / 37.8, 6900 65.9 / 62.9, bf16 1730 24.0 / 24.3, 3450 40.5 / 39.1 (522 points: 0.3% behind the
+// faster one on average, 9% at most: full tables a little below a limit, half-full ones a little above). With more
+// sequences the split size does not follow the lengths, and the 16-row products keep their lead only while a sequence and
+// kv head have an SM for themselves: 100 sequences of U[100, 1000] x 1 kv head 13.4 / 17.8, 200 x 1 21.2 / 17.1, 200 x 8 102 / 85
+// (273 points: 3% behind the faster one on average; 100 sequences of U[20, 100] x 8 24 / 31). With d = 128: 8-bit codes 64 of up
+// to 1000 x 8 46 / 34, bf16 48 / 40.
+inline bool tree_takes_tiles(long long rows, int d, bool f8, int page_size, int B, int Hkv, long long max_len, int num_sms) {
+    if (rows <= 16) return false;
+    if (d != 64 || rows > 32) return true;
+    const bool boxes = page_size % 16 == 0;
+    const long long limit = f8 ? (boxes ? 3400 : 8000) : (boxes ? 1500 : 3400);  // tokens per SM
+    return (long long)B * Hkv * max_len > limit * num_sms || (B > kTreeFitSeqs && (long long)B * Hkv > num_sms);
 }
 
 // Grid of a split kernel; sets the work order. The last splits are shorter in general: started after all
@@ -89,9 +101,6 @@ inline dim3 tree_grid(TreeParams& p) {
     p.ranked = 0;
     return dim3((unsigned)(p.max_splits * HG), (unsigned)p.B);
 }
-
-// Sequences up to which the blocks choose the split size by the lengths (two per lane of a warp).
-constexpr int kTreeFitSeqs = 64;
 
 // Blocks of the split kernels that share an SM. (64 8-bit codes, up to 8 rows, five, not four: 64 sequences of U[100, 1000]
 // 17.0 us, not 20.1, of U[1K, 32K] 197, not 206; with up to 16 rows the registers do not suffice: 242, not 218.)

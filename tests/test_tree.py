@@ -665,6 +665,20 @@ def test_tiles_of_odd_pages_split_by_the_lengths(A, fmt, n, d, page, batch):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt,page", [("bf16", 16), ("bf16", 5), ("e4m3", 64), ("e5m2", 7)])
+@pytest.mark.parametrize("B,Hkv,times", [(4, 2, 1), (4, 2, 9000), (80, 1, 1), (80, 2, 1)])
+def test_narrow_heads_whatever_the_table_holds(A, fmt, page, B, Hkv, times):
+    """17 to 32 rows of 64 elements where 16-row products and where tiles are taken: small and very wide tables, more
+    sequences than the lengths are looked at for."""
+    rs = np.random.RandomState(5)
+    lens = [int(x) for x in rs.randint(6, 200, B)]
+    c = widened(Case(fmt, 4 * Hkv, Hkv, 64, page, [6] * B, lens, "any", 29), times)
+    c.run(A)
+    assert A.attn_get_device_status() == 0
+    c.check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3", "e5m2"])
 @pytest.mark.parametrize("n,page,num_splits", [(5, 16, 0), (8, 7, 1), (7, 1, 3), (6, 64, 12), (8, 16, 8)])
 def test_two_row_groups_of_narrow_heads(A, fmt, n, page, num_splits):
