@@ -605,6 +605,63 @@ def test_streams_at_once_with_few_and_many_splits(A, num_splits):
     assert A.attn_get_device_status() == 0
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,Hq", [("bf16", 1), ("e4m3", 17)])
+def test_more_sequences_than_grid_rows_for_two_orders(A, fmt, Hq):
+    """With two splits and more than half of 65535 sequences the splits of a sequence share a grid row; the second kernel
+    joins them."""
+    rs = np.random.RandomState(30)
+    B = 33000
+    lens = [int(x) for x in rs.randint(0, 20, B)]
+    for b, l in ((0, 150), (1, 64), (2, 129), (B - 1, 150)):
+        lens[b] = l
+    c = Case(fmt, Hq, 1, 64, 16, [1] * B, lens, "chain", 31, dense=True)
+    c.run(A, 2)
+    assert A.attn_get_device_status() == 0
+    if Hq > 1:  # every row and head of some of them
+        some = [*range(4), *range(4, B - 4, 400), *range(B - 4, B)]
+        c.q, c.o, c.lse, c.pt = c.q[some], c.o[some], c.lse[some], c.pt[some]
+        c.n, c.lens, c.seen, c.T, c.cu = [1] * len(some), [c.lens[b] for b in some], [c.seen[b] for b in some], len(some), np.arange(len(some) + 1)
+    c.check()
+
+
+@pytest.mark.gpu
+def test_calls_from_several_host_threads(A):
+    """Threads with a stream and buffers each, through clusters, workspaces and both kernels, give the bytes of calls one
+    after the other."""
+    import threading
+    cases = [(Case("bf16", 8, 2, 128, 16, [24, 24], [900, 2000], "tree", 13), 0), (Case("e4m3", 8, 2, 128, 16, [2, 2], [3000, 2000], "tree", 14), 20),
+             (Case("e5m2", 8, 8, 64, 7, [24], [2500], "chain", 15), 8), (Case("bf16", 16, 8, 64, 16, [3] * 12, [40 * i + 3 for i in range(12)], "any", 16), 0)]
+    want = []
+    for c, splits in cases:
+        c.run(A, splits)
+        want.append((c.o.clone(), c.lse.clone()))
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(c, splits, o, lse):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(30):
+                with torch.cuda.stream(s):
+                    c.o.fill_(7)
+                c.run(A, splits, stream=s)
+            s.synchronize()
+            if not (torch.equal(c.o, o) and torch.equal(c.lse, lse)):
+                failed.append("other bytes")
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(*c, *w)) for c, w in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed and A.attn_get_device_status() == 0
+    for c, _ in cases:
+        c.check()
+
+
 BATCHES = {  # cached tokens of each sequence, and how many times wider than needed the page table is
     "equal": ([512] * 20, 1),
     "ragged": ([(i * 97) % 500 + 20 for i in range(18)] + [0, 22], 1),
