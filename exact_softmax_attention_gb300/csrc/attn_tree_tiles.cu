@@ -34,9 +34,12 @@
 // (S 8 x 48, bound by the 6 KB of shared memory that each reads, P V 4 x 64). With up to 128 rows the bf16
 // form is bounded by the memory: 16 drafted tokens x 4 query heads over 64 sequences of U[1K, 32K] tokens
 // take 640 us, 6770 GB/s, 1.00 of the measured copy rate (8 tokens with page size 64: 618 us; page size 1:
-// 770 us). 8-bit caches have half the bytes for the same products: 439 us, 4950 GB/s (0.73), bounded by the
-// tensor pipe, the shared memory and the chain S -> softmax -> P V of two buffers. More than 128 rows:
-// every further tile reads the cache again through the L2 (64 drafted tokens: 918 us, 0.71 of the floor).
+// 770 us). 8-bit caches have half the bytes for the same products: 424 us in short bursts, 447 us under steady
+// load, where the power limit lowers the clock (0.76, 0.72). No unit is full (tensor pipe 48 % active, memory 52 %, issue
+// slots 39 %): a block follows the chain S -> softmax -> P V over two score buffers, and its cost does not fall
+// with the rows. More than 128 rows: every further tile reads the cache again through the L2 (64 drafted tokens:
+// bf16 904 us, 0.72 of the floor; e4m3 887 us, 0.64). d = 64: half the bytes per key and nearly the same chain
+// (64 rows: bf16 343 us, 0.93; e4m3 338 us, 0.47).
 // Tried and slower (same case, bf16 / 8-bit, before the work order; this form then took 698 / 584, with S and
 // P V in a thread each and raw K 685 / 511): Q in tensor memory with one S buffer 713 / 753, or with S in
 // steps of 32 keys 813 / 844 (a product takes 32 clocks at least); one S buffer with two separate P

@@ -300,7 +300,8 @@ attn_status_t attn_rope_freqs(double* inv_freq, double* amplitude, int rot_dim, 
  * A sequence whose length is below its rows or above its page table, a page outside
  * [0, num_pages), and offsets that decrease or pass T are recorded as ATTN_ERR_DEVICE_BAD_INDEX;
  * their rows are not written. Rows that name the same cache slot (pages shared between sequences)
- * leave it to one of them, in pieces of 8 elements.
+ * leave it to one of them in pieces of 8 elements, or element by element when rot_begin or rot_dim is no
+ * multiple of 16: what the slot then holds may be mixed of their rows.
  * Alignment: k, v, k_cache, v_cache 16 bytes; integers 4; inv_freq 8.
  */
 attn_status_t attn_kv_write_paged(const void* k, const void* v, long long k_stride, long long v_stride, void* k_cache,
@@ -354,8 +355,10 @@ attn_status_t attn_kv_read_paged(const void* k_cache, const void* v_cache, void*
  *            most 64 * mask_words with a mask); max_q * Hq / Hkv at most 65535, T * Hq below 2^31
  * mask_words words per row of tree_mask, 1 .. 4 (ignored without a mask)
  * Hq, Hkv, d as for attn_decode_paged (d = 64 or 128); scale finite
- * num_splits 0: choose the number of key splits from the SM count, the sizes and the lengths (in a captured
- *            graph those of the replay); n > 0: at most n
+ * num_splits 0: choose the number of key splits from the SM count and the sizes, by the capacity of the page
+ *            table; and for at most 64 sequences, whose (sequence, kv head, row group) groups fit on the GPU at
+ *            once but not with all their splits, from the lengths (in a captured graph those of the replay);
+ *            n > 0: at most n
  * k_descale, v_descale  finite; ignored for ATTN_KV_BF16 (pass 1)
  * What a masked or unused cache slot holds does not matter, NaN and infinities included. A page
  * outside [0, num_pages) is not read: its rows count as zeros and ATTN_ERR_DEVICE_BAD_INDEX is
