@@ -662,6 +662,43 @@ def test_calls_from_several_host_threads(A):
         c.check()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("num_splits", [8, 20])
+def test_two_graphs_replayed_at_once(A, num_splits):
+    """Each captured call has a workspace of its own: replays on two streams give the bytes of calls one after the other."""
+    cases = [Case("bf16", 8, 2, 128, 16, [24, 24], [900, 2000], "tree", 13), Case("bf16", 8, 2, 128, 16, [24, 24], [1900, 1000], "tree", 17),
+             Case("e4m3", 8, 2, 64, 16, [3, 2], [3000, 2000], "tree", 14)]
+    want, graphs, streams = [], [], []
+    for c in cases:
+        c.run(A, num_splits)
+        want.append((c.o.clone(), c.lse.clone()))
+        g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(3):
+                c.run(A, num_splits)
+        graphs.append(g)
+        streams.append(s)
+        c.o.fill_(7)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for c, (o, lse) in zip(cases, want):
+        assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
+    assert A.attn_get_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,Hq,Hkv,n,d", [("bf16", 600, 1, 2, 64), ("e4m3", 700, 1, 1, 128), ("e5m2", 900, 900, 1, 64), ("bf16", 1000, 500, 9, 64)])
+def test_many_heads(A, fmt, Hq, Hkv, n, d):
+    c = Case(fmt, Hq, Hkv, d, 16, [n, n], [n + 30, n + 200], "tree", 18)
+    c.run(A)
+    assert A.attn_get_device_status() == 0
+    c.check()
+
+
 BATCHES = {  # cached tokens of each sequence, and how many times wider than needed the page table is
     "equal": ([512] * 20, 1),
     "ragged": ([(i * 97) % 500 + 20 for i in range(18)] + [0, 22], 1),
