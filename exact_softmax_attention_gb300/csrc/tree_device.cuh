@@ -52,7 +52,7 @@ __device__ __forceinline__ bool tree_seq(const TreeParams& p, int b, TreeSeq& s)
 // the least size. Measured, batches of 1 to 32 sequences of up to 32768 tokens, equal and ragged: 4% behind the
 // best of ten fixed sizes per batch on average, 6% when the page table is four times wider than the lengths need
 // (sizes from the capacity alone: 7% and 34%). 40 and 64 sequences (128 cases): 10% behind on average with tight tables,
-// 4% ahead with ones four times wider; at worst 61%, 40 equal ones of 1000 tokens x 4 kv heads in tiles, where 320 blocks
+// 4% ahead with ones four times wider; at worst 61% and 68%, 40 equal ones of 1000 tokens x 4 kv heads in tiles, where 320 blocks
 // follow each other in 304 places, which the time above does not count as a second round. It takes 1.3 us, 2.6 us for 64 sequences, the load
 // of the lengths included. out: tokens per split, sequence (-1: no work), split (-1: the last one), head group.
 __device__ __noinline__ void tree_fit(const int* seqlens, int* chunk_out, int B, int max_len, int HG, int slots, int least,
