@@ -143,7 +143,7 @@ def work(case):
     table = 4 * int(pages.sum()) + 4 * len(lens)
     if case["op"] == "score":
         seen = int((n * lens - n * (n - 1) // 2).sum())  # query i of n does not see the n - 1 - i tokens after its own
-        sums = 4 * int(lens.sum()) * hkv * (2 if case["decay"] else 1)
+        sums = 4 * hkv * int((2 * lens - n if case["decay"] else lens).sum())
         return {"bytes": int(lens.sum()) * hkv * d * e + sums + int(n.sum()) * case["hq"] * (2 * d + 4) + table,
                 "flops": 2 * seen * case["hq"] * d}
     # sequences above the budget are looked through; the last tokens move, and of those chosen between them and the first
@@ -319,8 +319,9 @@ def _scored(s):
     at = torch.nonzero(torch.arange(total.shape[2], device=DEV) < s["seqlens"].long()[:, None])
     page, slot = s["page_table"][at[:, 0], at[:, 1] // c["page"]].long(), at[:, 1] % c["page"]
     new = total[at[:, 0], :, at[:, 1]]
-    if c["decay"]:
-        new = new + c["decay"] * s["score"][page, :, slot]
+    if c["decay"]:  # the queries' own tokens are new: what their slots hold is of no token
+        old = at[:, 1] < (s["seqlens"] - (s["cu"][1:] - s["cu"][:-1]))[at[:, 0]]
+        new = new + torch.where(old[:, None], c["decay"] * s["score"][page, :, slot], 0.0)
     s["score"][page, :, slot] = new
     return {"score": s["score"]}
 
@@ -458,7 +459,8 @@ def exact(case, seed):
                 for r in range(h * G, (h + 1) * G):
                     e = s["q"][at:at + m, r].double() @ K.T / math.sqrt(d) - s["lse"][at:at + m, r].double()[:, None]
                     new += e.exp().masked_fill(hidden, 0.0).sum(0)
-                sums[where[0], h, where[1]] = sums[where[0], h, where[1]] * case["decay"] + new
+                new[:l - m] += sums[where[0], h, where[1]][:l - m] * case["decay"]
+                sums[where[0], h, where[1]] = new
             at += m
         return {"score": sums}
     score, kc, vc = s["score"].cpu().numpy(), s["kc"].clone(), s["vc"].clone()
