@@ -47,7 +47,8 @@ ROPE_SCALINGS = {"plain": ATTN_ROPE_PLAIN, "linear": ATTN_ROPE_LINEAR, "ntk": AT
 
 #: every symbol the header declares
 EXPORTS = ("attn_fwd", "attn_fwd_hd", "attn_fwd_fp8", "attn_decode_paged", "attn_decode_paged_fp8", "attn_decode_paged_noalloc",
-           "attn_rope", "attn_rope_freqs", "attn_kv_write_paged", "attn_kv_read_paged", "attn_decode_paged_tree", "attn_decode_plan",
+           "attn_rope", "attn_rope_freqs", "attn_kv_write_paged", "attn_kv_read_paged", "attn_decode_paged_tree", "attn_qk_norm_rope",
+           "attn_qk_norm_rope_bwd", "attn_kv_score_paged", "attn_kv_select_paged", "attn_kv_compact_paged", "attn_decode_plan",
            "attn_decode_workspace_bytes", "attn_status_string", "attn_get_device_status",
            "attn_set_option", "attn_get_option", "attn_read_counters", "attn_debug_exp2", "attn_debug_watchdog",
            "attn_version")
@@ -89,6 +90,16 @@ lib.attn_kv_read_paged.argtypes = [_vp] * 4 + [_ll, _ll] + [_vp] * 3 + [_i] * 8 
 lib.attn_kv_read_paged.restype = _i
 lib.attn_decode_paged_tree.argtypes = [_vp] * 7 + [_i, _i] + [_vp] * 3 + [_i] * 8 + [_f, _i, _i, _f, _f]
 lib.attn_decode_paged_tree.restype = _i
+lib.attn_qk_norm_rope.argtypes = [_vp] * 6 + [_f] + [_vp] * 2 + [_i] * 6 + [_ll] * 4 + [_i] * 2 + [_f, _vp]
+lib.attn_qk_norm_rope.restype = _i
+lib.attn_qk_norm_rope_bwd.argtypes = [_vp] * 6 + [_f] + [_vp] * 6 + [_i] * 6 + [_ll] * 6 + [_i] * 2 + [_f, _vp]
+lib.attn_qk_norm_rope_bwd.restype = _i
+lib.attn_kv_score_paged.argtypes = [_vp] * 7 + [_i] * 9 + [_f, _f, _i, _f, _vp]
+lib.attn_kv_score_paged.restype = _i
+lib.attn_kv_select_paged.argtypes = [_vp] * 5 + [_i] * 8 + [_vp]
+lib.attn_kv_select_paged.restype = _i
+lib.attn_kv_compact_paged.argtypes = [_vp] * 6 + [_i] * 8 + [_vp]
+lib.attn_kv_compact_paged.restype = _i
 lib.attn_decode_plan.argtypes = [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_i), ctypes.POINTER(_i)]
 lib.attn_decode_plan.restype = _i
 lib.attn_decode_workspace_bytes.argtypes = [_i, _i, _i, _i]
@@ -262,6 +273,58 @@ def attn_decode_paged_tree(q, k_cache, v_cache, page_table, seqlens, cu_seqlens,
                                     int(num_pages), float(scale), int(num_splits), _code(KV_FORMATS, kv_format),
                                     float(k_descale), float(v_descale))
     return _check(rc, "attn_decode_paged_tree", raise_on_error)
+
+
+def attn_qk_norm_rope(q, k, q_out, k_out, q_weight, k_weight, eps, positions, inv_freq, T, Hq, Hk, d, rot_begin, rot_dim, q_stride,
+                      k_stride, q_out_stride, k_out_stride, elem_type="bf16", interleaved=0, amplitude=1.0, stream=None,
+                      raise_on_error=True):
+    """Norms of the heads of q and k and their rotary positions in one pass; see ``attn_qk_norm_rope`` in
+    include/attn.h. ``elem_type`` is "bf16" or "f32" (or the ATTN_TYPE_* code)."""
+    rc = lib.attn_qk_norm_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(q_weight), _ptr(k_weight), float(eps),
+                               _ptr(positions), _ptr(inv_freq), int(T), int(Hq), int(Hk), int(d), int(rot_begin), int(rot_dim),
+                               int(q_stride), int(k_stride), int(q_out_stride), int(k_out_stride), _code(ELEM_TYPES, elem_type),
+                               int(interleaved), float(amplitude), _stream(stream))
+    return _check(rc, "attn_qk_norm_rope", raise_on_error)
+
+
+def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, eps, positions, inv_freq, dq, dk, dq_weight, dk_weight, T, Hq, Hk, d,
+                          rot_begin, rot_dim, q_stride, k_stride, dq_out_stride, dk_out_stride, dq_stride, dk_stride, elem_type="bf16",
+                          interleaved=0, amplitude=1.0, stream=None, raise_on_error=True):
+    """Gradient of ``attn_qk_norm_rope``; see ``attn_qk_norm_rope_bwd`` in include/attn.h."""
+    rc = lib.attn_qk_norm_rope_bwd(_ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(q_weight), _ptr(k_weight), float(eps),
+                                   _ptr(positions), _ptr(inv_freq), _ptr(dq), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), int(T),
+                                   int(Hq), int(Hk), int(d), int(rot_begin), int(rot_dim), int(q_stride), int(k_stride),
+                                   int(dq_out_stride), int(dk_out_stride), int(dq_stride), int(dk_stride),
+                                   _code(ELEM_TYPES, elem_type), int(interleaved), float(amplitude), _stream(stream))
+    return _check(rc, "attn_qk_norm_rope_bwd", raise_on_error)
+
+
+def attn_kv_score_paged(q, lse, k_cache, score, page_table, seqlens, cu_seqlens, page_size, T, B, max_q, Hq, Hkv, d, max_pages_per_seq,
+                        num_pages, scale, decay=1.0, kv_format="bf16", k_descale=1.0, stream=None, raise_on_error=True):
+    """Attention weight per cached token, added to its sums; see ``attn_kv_score_paged`` in include/attn.h."""
+    rc = lib.attn_kv_score_paged(_ptr(q), _ptr(lse), _ptr(k_cache), _ptr(score), _ptr(page_table), _ptr(seqlens), _ptr(cu_seqlens),
+                                 int(page_size), int(T), int(B), int(max_q), int(Hq), int(Hkv), int(d), int(max_pages_per_seq),
+                                 int(num_pages), float(scale), float(decay), _code(KV_FORMATS, kv_format), float(k_descale),
+                                 _stream(stream))
+    return _check(rc, "attn_kv_score_paged", raise_on_error)
+
+
+def attn_kv_select_paged(score, page_table, seqlens, kept, new_seqlens, page_size, B, Hkv, max_pages_per_seq, num_pages, budget,
+                         sinks=0, recent=0, stream=None, raise_on_error=True):
+    """The cached tokens that stay within ``budget``; see ``attn_kv_select_paged`` in include/attn.h."""
+    rc = lib.attn_kv_select_paged(_ptr(score), _ptr(page_table), _ptr(seqlens), _ptr(kept), _ptr(new_seqlens), int(page_size), int(B),
+                                  int(Hkv), int(max_pages_per_seq), int(num_pages), int(budget), int(sinks), int(recent),
+                                  _stream(stream))
+    return _check(rc, "attn_kv_select_paged", raise_on_error)
+
+
+def attn_kv_compact_paged(k_cache, v_cache, score, kept, new_seqlens, page_table, page_size, B, Hkv, d, max_pages_per_seq, num_pages,
+                          budget, kv_format="bf16", stream=None, raise_on_error=True):
+    """The kept tokens to their slots, in place; see ``attn_kv_compact_paged`` in include/attn.h."""
+    rc = lib.attn_kv_compact_paged(_ptr(k_cache), _ptr(v_cache), _ptr(score), _ptr(kept), _ptr(new_seqlens), _ptr(page_table),
+                                   int(page_size), int(B), int(Hkv), int(d), int(max_pages_per_seq), int(num_pages), int(budget),
+                                   _code(KV_FORMATS, kv_format), _stream(stream))
+    return _check(rc, "attn_kv_compact_paged", raise_on_error)
 
 
 def attn_decode_plan(B, Hq, Hkv, max_pages_per_seq, page_size, num_splits=0, num_sms=0):

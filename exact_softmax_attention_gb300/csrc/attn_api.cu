@@ -712,4 +712,12 @@ int current_device_info(int** status, int* num_sms) {
     *num_sms = ds->num_sms;
     return ATTN_OK;
 }
+
+int current_device_pool(cudaMemPool_t* pool) {
+    DeviceState* ds = nullptr;
+    const attn_status_t st = device_state(&ds);
+    return st != ATTN_OK ? st : device_pool(ds, pool);
+}
+
+unsigned long long watchdog_ns() { return (unsigned long long)(options().watchdog_ms * 1e6); }
 }  // namespace attn

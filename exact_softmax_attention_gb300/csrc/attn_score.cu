@@ -1,0 +1,285 @@
+// Attention weight per cached token, accumulated: score[t, h] = decay score[t, h] + sum over the rows that see
+// token t and the query heads of kv head h of exp(scale q.k - lse); the rows' own tokens have no old sum. This file: argument checks, and the kernel for up to
+// 16 rows per kv head (a decode step: one row times the query heads of a kv head).
+//
+// With few rows the keys are read once and little is computed with them: the kernel is bounded by the memory. So a
+// warp reads K from the cache straight into the operand registers of mma.sync m16n8k16: 16 tokens are the rows of
+// A, the queries the columns of B. The order of the columns of K inside the sum is free, as long as q has the same: a
+// lane takes the 16 bytes that it loads of a token as its elements of two (8-bit codes: four) products. The next 16
+// tokens are loaded while these are multiplied, and the page table is read one group ahead of them. A block's warps take the
+// kv heads of the same tokens, so a cache row is read as a whole. Sums over the rows are two shuffles.
+#include "score.cuh"
+
+#include <float.h>
+#include <string.h>
+
+namespace attn {
+namespace {
+
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two 8-bit codes in the low (or high) half of w as an f16 pair; e5m2 is the upper byte of an f16.
+template <int FMT>
+__device__ __forceinline__ uint32_t widen(uint32_t w, int high) {
+    if constexpr (FMT == ATTN_FP8_E5M2) {
+        return __byte_perm(w, 0, high ? 0x3424 : 0x1404);
+    } else {
+        const uint16_t v = (uint16_t)(high ? w >> 16 : w);
+        uint32_t d;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(v));
+        return d;
+    }
+}
+
+__device__ __forceinline__ uint32_t half_pair(uint32_t bf16_pair, float factor) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(bf16_pair & 0xFFFF0000u) * factor), "f"(__uint_as_float(bf16_pair << 16) * factor));
+    return r;
+}
+
+constexpr int kRowWarps = 8;  // warps per block, at most
+
+// NT: groups of 8 rows.
+template <int D, int FMT, int NT>
+__global__ void __launch_bounds__(kRowWarps * 32, 2) score_rows_kernel(const __grid_constant__ ScoreParams p) {
+    constexpr bool F8 = FMT != ATTN_KV_BF16;
+    constexpr int kLoads = F8 ? D / 64 : D / 32;  // 16-byte loads of a lane per token
+    constexpr int kSteps = D / 16;                // products
+    constexpr int kPer = kSteps / kLoads;         // of each load
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int heads = min(p.Hkv, kRowWarps), parts = (blockDim.x >> 5) / heads;
+    const int h = blockIdx.y * heads + warp % heads, part = warp / heads;
+    const int b = (int)(blockIdx.x / (unsigned)p.chunks), t_begin = (int)(blockIdx.x % (unsigned)p.chunks) * p.chunk;
+    ScoreSeq s;
+    if (h >= p.Hkv || !score_seq(p, b, s) || t_begin >= s.len) return;
+    const int t_end = min(s.len, t_begin + p.chunk), R = s.n * p.G;
+    const int* pt = p.page_table + (long long)b * p.max_pages;
+
+    // rows g and g + 8: their operands, then for the columns 2 t, 2 t + 1 that this lane gets: factor of the scores, LSE,
+    // last token seen
+    uint32_t qb[NT][kSteps][2];
+    float factor[NT][2], lse2[NT][2];
+    int last[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int r = g + 8 * n, i = r / p.G;
+        const bool valid = r < R;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + ((long long)(s.q0 + i) * p.Hq + h * p.G + (r - i * p.G)) * D);
+        uint4 w[D / 32];  // bf16: the lane's 8 elements of 32; 8-bit caches: 16 elements of 64
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x)
+            w[x] = valid ? __ldg(src + (F8 ? (x >> 1) * 8 + 2 * t + (x & 1) : 4 * x + t)) : make_uint4(0, 0, 0, 0);
+        float up = 1.0f;
+        if constexpr (F8) {
+            // a power of two brings the row's largest magnitude into [2^14, 2^15)
+            uint32_t top = 0;
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) {
+                const uint32_t e[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) top = max(top, max(e[y] & 0x7FFFu, (e[y] >> 16) & 0x7FFFu));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int exponent = (int)(top >> 7);  // biased; 0: zero or subnormal, 255: not finite
+            // (the factor 2^(127 + 14 - exponent) and its inverse as floats; exponents whose factor would leave the range stay)
+            if (exponent > 14 && exponent < 255) up = __uint_as_float((unsigned)(127 + 127 + 14 - exponent) << 23);
+            if (exponent <= 14 && top != 0) up = __uint_as_float(254u << 23);
+        }
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+            const uint32_t e[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int step = 2 * x + y;
+                qb[n][step][0] = F8 ? half_pair(e[2 * y], up) : e[2 * y];
+                qb[n][step][1] = F8 ? half_pair(e[2 * y + 1], up) : e[2 * y + 1];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int rc = 2 * t + e + 8 * n, ic = rc / p.G;
+            const float l = rc < R ? __ldg(p.lse + (long long)(s.q0 + ic) * p.Hq + h * p.G + (rc - ic * p.G)) : -INFINITY;
+            last[n][e] = l == -INFINITY ? -1 : s.ctx + ic;  // (such rows saw nothing)
+            lse2[n][e] = l == -INFINITY ? 0.0f : l * 1.4426950408889634f;
+            const float of_row = __shfl_sync(0xffffffffu, up, (2 * t + e) * 4);
+            factor[n][e] = F8 ? p.scale_log2 / of_row : p.scale_log2;
+        }
+    }
+
+    // tokens g and g + 8 of a group of 16; lanes 0 and 1 of four keep their sums
+    struct Group {
+        int page[2], slot[2];
+    };
+    const int step = 16 * parts;
+    auto look_up = [&](int t0, Group& at) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) at.page[e] = t0 + g + 8 * e < t_end ? score_place(p, pt, t0 + g + 8 * e, at.slot[e]) : -1;
+    };
+    uint4 kv[2][kLoads];
+    float old = 0.0f;
+    auto load = [&](const Group& at, int from) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const long long row = at.page[e] >= 0 ? (long long)at.page[e] * p.page_size + at.slot[e] : 0;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_cache) + (row * p.Hkv + h) * (F8 ? D : 2 * D));
+#pragma unroll
+            for (int x = 0; x < kLoads; ++x) kv[e][x] = at.page[e] >= 0 ? __ldg(src + 4 * x + t) : make_uint4(0, 0, 0, 0);
+        }
+        if (p.decay != 0.0f && t < 2) {
+            const int page = t ? at.page[1] : at.page[0], slot = t ? at.slot[1] : at.slot[0];
+            old = page >= 0 && from + g + 8 * t < s.ctx ? p.decay * *score_slot(p, page, slot, h) : 0.0f;
+        }
+    };
+    Group now, next;
+    int t0 = t_begin + 16 * part;
+    look_up(t0, now);
+    look_up(t0 + step, next);
+    load(now, t0);
+    for (; t0 < t_end; t0 += step) {
+        float acc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+            const uint32_t lo[4] = {kv[0][x].x, kv[0][x].y, kv[0][x].z, kv[0][x].w};
+            const uint32_t hi[4] = {kv[1][x].x, kv[1][x].y, kv[1][x].z, kv[1][x].w};
+#pragma unroll
+            for (int y = 0; y < kPer; ++y) {
+                uint32_t a[4];
+                if constexpr (F8) {
+                    a[0] = widen<FMT>(lo[y], 0), a[1] = widen<FMT>(hi[y], 0);
+                    a[2] = widen<FMT>(lo[y], 1), a[3] = widen<FMT>(hi[y], 1);
+                } else {
+                    a[0] = lo[2 * y], a[1] = hi[2 * y], a[2] = lo[2 * y + 1], a[3] = hi[2 * y + 1];
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if constexpr (F8)
+                        mma_f16_16816(acc[n], a, qb[n][x * kPer + y][0], qb[n][x * kPer + y][1]);
+                    else
+                        mma_bf16_16816(acc[n], a, qb[n][x * kPer + y][0], qb[n][x * kPer + y][1]);
+                }
+            }
+        }
+        const float before = old;
+        const Group mine = now;
+        now = next;
+        look_up(t0 + 2 * step, next);
+        load(now, t0 + step);
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float x0 = ex2_mufu(fmaf(acc[n][e], factor[n][e], -lse2[n][e]));
+                const float x1 = ex2_mufu(fmaf(acc[n][2 + e], factor[n][e], -lse2[n][e]));
+                sum[0] += t0 + g <= last[n][e] ? x0 : 0.0f;
+                sum[1] += t0 + g + 8 <= last[n][e] ? x1 : 0.0f;
+            }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
+            sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
+        }
+        if (t < 2) {
+            const int page = t ? mine.page[1] : mine.page[0], slot = t ? mine.slot[1] : mine.slot[0];
+            const float total = t ? sum[1] : sum[0];
+            if (page >= 0) *score_slot(p, page, slot, h) = before + total;
+        }
+    }
+}
+
+template <int D, int FMT>
+cudaError_t launch_rows(ScoreParams p, cudaStream_t stream) {
+    const int heads = p.Hkv < kRowWarps ? p.Hkv : kRowWarps, parts = kRowWarps / heads;
+    const int groups = (p.Hkv + heads - 1) / heads;
+    // tokens per block: about 16 blocks per SM when every table is full, 1024 at most
+    const long long capacity = (long long)p.max_pages * p.page_size;
+    const int least = 16 * parts;
+    long long c = ((long long)p.B * capacity * groups + 16LL * p.num_sms - 1) / (16LL * p.num_sms);
+    c = c > 1024 ? 1024 : c;
+    c = (c + least - 1) / least * least;
+    while ((capacity + c - 1) / c * p.B > INT32_MAX) c *= 2;
+    p.chunk = (int)c;
+    p.chunks = (int)((capacity + c - 1) / c);
+    const dim3 grid((unsigned)((long long)p.B * p.chunks), (unsigned)groups);
+    const unsigned threads = (unsigned)(heads * parts * 32);
+    return (long long)p.max_q * p.G <= 8 ? launch_kernel(score_rows_kernel<D, FMT, 1>, grid, threads, 0, stream, {}, p)
+                                         : launch_kernel(score_rows_kernel<D, FMT, 2>, grid, threads, 0, stream, {}, p);
+}
+
+template <int D>
+cudaError_t launch_fmt(const ScoreParams& p, int fmt, cudaStream_t stream) {
+    return fmt == ATTN_FP8_E4M3   ? launch_rows<D, ATTN_FP8_E4M3>(p, stream)
+           : fmt == ATTN_FP8_E5M2 ? launch_rows<D, ATTN_FP8_E5M2>(p, stream)
+                                  : launch_rows<D, ATTN_KV_BF16>(p, stream);
+}
+
+bool multiple(const void* p, long long bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+}  // namespace
+
+cudaError_t launch_score_rows(const ScoreParams& p, int d, int kv_format, cudaStream_t stream) {
+    return d == 128 ? launch_fmt<128>(p, kv_format, stream) : launch_fmt<64>(p, kv_format, stream);
+}
+
+}  // namespace attn
+
+extern "C" attn_status_t attn_kv_score_paged(const void* q, const float* lse, const void* k_cache, float* score, const int* page_table,
+                                             const int* seqlens, const int* cu_seqlens, int page_size, int T, int B, int max_q, int Hq,
+                                             int Hkv, int d, int max_pages_per_seq, int num_pages, float scale, float decay,
+                                             int kv_format, float k_descale, void* stream) {
+    using namespace attn;
+    if (!q || !lse || !k_cache || !score || !page_table || !seqlens) return ATTN_ERR_NULL_PTR;
+    if (kv_format != ATTN_FP8_E4M3 && kv_format != ATTN_FP8_E5M2 && kv_format != ATTN_KV_BF16) return ATTN_ERR_BAD_ARG;
+    if (!isfinite(k_descale) || !isfinite(decay)) return ATTN_ERR_BAD_ARG;
+    if (T < 0 || B < 0 || B > 65535 || max_q < 1 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hkv > 65535 || (d != 64 && d != 128) ||
+        page_size <= 0 || max_pages_per_seq <= 0 || num_pages <= 0)
+        return ATTN_ERR_BAD_SHAPE;
+    if ((long long)num_pages * page_size > INT32_MAX) return ATTN_ERR_BAD_SHAPE;  // cache rows are 32-bit indices
+    if ((long long)max_pages_per_seq * page_size > INT32_MAX / 2 || (long long)T * Hq > INT32_MAX) return ATTN_ERR_BAD_SHAPE;
+    if (!cu_seqlens && T > 0 && (B == 0 || T % B != 0 || T / B > max_q)) return ATTN_ERR_BAD_SHAPE;
+    if (!isfinite(scale)) return ATTN_ERR_BAD_SHAPE;
+    if (!multiple(q, 16) || !multiple(k_cache, 16) || !multiple(lse, 4) || !multiple(score, 4) || !multiple(page_table, 4) ||
+        !multiple(seqlens, 4) || (cu_seqlens && !multiple(cu_seqlens, 4)))
+        return ATTN_ERR_ALIGN;
+    const double factor = (double)scale * (kv_format == ATTN_KV_BF16 ? 1.0 : (double)k_descale) * 1.4426950408889634;
+    if (!(fabs(factor) <= (double)FLT_MAX)) return ATTN_ERR_BAD_ARG;  // a float in the kernels
+    if (B == 0 || T == 0) return ATTN_OK;
+    ScoreParams p;
+    memset(&p, 0, sizeof p);
+    const attn_status_t st = current_device_info(&p.status, &p.num_sms);
+    if (st != ATTN_OK) return st;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.lse = lse;
+    p.k_cache = k_cache;
+    p.score = score;
+    p.page_table = page_table;
+    p.seqlens = seqlens;
+    p.cu_seqlens = cu_seqlens;
+    p.B = B, p.T = T;
+    p.max_q = cu_seqlens ? (max_q < T ? max_q : T) : T / B;
+    p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv;
+    p.page_size = page_size, p.max_pages = max_pages_per_seq, p.num_pages = num_pages;
+    p.scale_log2 = (float)factor;
+    p.decay = decay;
+    p.watchdog_ns = watchdog_ns();
+    if (page_size > 1) {  // tok / page_size for tok < 2^31: multiplier ceil(2^(31+k) / page_size), k = ceil(log2 page_size)
+        int k = 0;
+        while ((1LL << k) < page_size) ++k;
+        p.ps_magic = (unsigned)(((1ULL << (31 + k)) + (unsigned long long)page_size - 1) / (unsigned long long)page_size);
+        p.ps_shift = k - 1;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = (long long)p.max_q * p.G <= kScoreFewRows ? launch_score_rows(p, d, kv_format, s) : launch_score_tiles(p, d, kv_format, s);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}

@@ -128,6 +128,10 @@ cudaError_t launch_attn_decode_fp8(const DecodeParams& p, int d, int fmt, cudaSt
 // Status word and SM count of the current device (checks that it is an sm_103 GPU);
 // returns an attn_status_t code.
 int current_device_info(int** status, int* num_sms);
+// The library's stream-ordered memory pool on the current device; returns an attn_status_t code.
+int current_device_pool(cudaMemPool_t* pool);
+// Device waits give up after this time (option "watchdog_ms").
+unsigned long long watchdog_ns();
 
 // Diagnostics
 cudaError_t launch_exp2_probe(const float* x, float* y, long long n, int mode, cudaStream_t stream);

@@ -1,0 +1,90 @@
+// Shared by the two kernels that accumulate attention weight per cached token: parameters, the sequences'
+// rows and lengths, places in the paged cache.
+#pragma once
+
+#include "attn.h"
+#include "kernels.cuh"
+#include "launch.cuh"
+#include "ptx.cuh"
+
+#include <math.h>
+
+namespace attn {
+
+struct ScoreParams {
+    const __nv_bfloat16* q;  // [T, Hq, d]
+    const float* lse;        // [T, Hq]
+    const void* k_cache;     // [num_pages, page_size, Hkv, d], bf16 or 8-bit codes
+    float* score;            // [num_pages, Hkv, page_size]
+    const int* page_table;   // [B, max_pages]
+    const int* seqlens;      // [B], the rows' tokens included
+    const int* cu_seqlens;   // [B + 1] or nullptr: T / B rows each
+    int B, T, max_q, Hq, Hkv, G, page_size, max_pages, num_pages, num_sms;
+    float scale_log2, decay;  // scale (key descale included) times log2(e)
+    unsigned int ps_magic;   // tok / page_size by multiplication, as in DecodeParams
+    int ps_shift;
+    int chunk, chunks;       // few rows: tokens per block, blocks of the longest sequence
+    float* partial;          // tiles: [blocks, 2, 256] sums of units that lie in several blocks
+    int* status;
+    unsigned long long watchdog_ns;
+};
+
+cudaError_t launch_score_rows(const ScoreParams& p, int d, int kv_format, cudaStream_t stream);
+cudaError_t launch_score_tiles(const ScoreParams& p, int d, int kv_format, cudaStream_t stream);
+
+// Rows per kv head (queries x query heads) up to which a warp's 16-row products take them; more go to the tiles.
+constexpr int kScoreFewRows = 16;
+
+#ifdef __CUDACC__
+namespace {
+
+// Rows and cached tokens of sequence b. False: none of its slots are touched (no rows; or a length or offsets out
+// of range, which is recorded).
+struct ScoreSeq {
+    int q0, n;     // first row of q, rows
+    int len, ctx;  // cached tokens, those before the rows' own
+};
+__device__ __forceinline__ bool score_seq(const ScoreParams& p, int b, ScoreSeq& s) {
+    long long c0, c1;
+    const int len = __ldg(p.seqlens + b);
+    if (p.cu_seqlens) {
+        c0 = __ldg(p.cu_seqlens + b), c1 = __ldg(p.cu_seqlens + b + 1);
+    } else {
+        const int n = p.T / p.B;
+        c0 = (long long)b * n, c1 = c0 + n;
+    }
+    const long long n = c1 - c0;
+    if (n == 0) return false;
+    if (c0 < 0 || n < 0 || c1 > p.T || n > p.max_q || len < n || len > (long long)p.max_pages * p.page_size) {
+        atomicCAS(p.status, 0, kDevBadIndex);
+        return false;
+    }
+    s.q0 = (int)c0, s.n = (int)n;
+    s.len = len;
+    s.ctx = len - s.n;
+    return true;
+}
+
+// Page-table index and slot of token tok (0 <= tok < 2^31).
+__device__ __forceinline__ int score_page(const ScoreParams& p, int tok, int& slot) {
+    const int q = p.ps_magic ? (int)(__umulhi((unsigned)tok, p.ps_magic) >> p.ps_shift) : tok;
+    slot = tok - q * p.page_size;
+    return q;
+}
+
+// Physical page of a token, or -1 (recorded) for one out of range; pt: the sequence's row of the page table.
+__device__ __forceinline__ int score_place(const ScoreParams& p, const int* pt, int tok, int& slot) {
+    const int page = __ldg(pt + score_page(p, tok, slot));
+    if (page >= 0 && page < p.num_pages) return page;
+    atomicCAS(p.status, 0, kDevBadIndex);
+    return -1;
+}
+
+__device__ __forceinline__ float* score_slot(const ScoreParams& p, int page, int slot, int h) {
+    return p.score + ((long long)page * p.Hkv + h) * p.page_size + slot;
+}
+
+}  // namespace
+#endif
+
+}  // namespace attn

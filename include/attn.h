@@ -53,7 +53,7 @@ typedef int attn_status_t;
 #define ATTN_FP8_E5M2 1 /* 5 exponent bits (bias 15), 2 mantissa bits, largest 57344 */
 #define ATTN_KV_BF16 2  /* a paged cache in bf16, where a call takes the format of its cache */
 
-/* element types of attn_rope */
+/* element types of attn_rope and attn_qk_norm_rope */
 #define ATTN_TYPE_BF16 0
 #define ATTN_TYPE_F32 1
 
@@ -381,6 +381,119 @@ attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const v
                                      int mask_words, int page_size, void* o, float* lse, void* stream, int T, int B,
                                      int max_q, int Hq, int Hkv, int d, int max_pages_per_seq, int num_pages,
                                      float scale, int num_splits, int kv_format, float k_descale, float v_descale);
+
+/*
+ * Norms of the heads of q and k with their rotary positions in the same pass: every head x of a row becomes
+ *   y = amplitude R(position) (weight * x / sqrt(mean(x^2) + eps)),
+ * the rotation (and the amplitude) on the columns [rot_begin, rot_begin + rot_dim) only, as in attn_rope.
+ *
+ * q, k, q_out, k_out, positions, inv_freq, T, Hq, Hk, d, rot_begin, strides, elem_type, interleaved, amplitude
+ *            as for attn_rope (q_out may be q, k_out k, with the same stride); rot_dim = 0: norms only (positions and
+ *            inv_freq may be NULL)
+ * q_weight, k_weight  device, fp32 [d] each, one weight per column shared by the heads, or NULL: ones
+ * eps        finite, >= 0
+ * All arithmetic is fp32, rounded once to elem_type; the sum of squares of a head has to stay in the range of fp32.
+ * Alignment: as for attn_rope (wide accesses need d, rot_begin and rot_dim multiples of 32 bytes); weights 4 bytes.
+ */
+attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const float* q_weight,
+                                const float* k_weight, float eps, const int* positions, const double* inv_freq, int T,
+                                int Hq, int Hk, int d, int rot_begin, int rot_dim, long long q_stride,
+                                long long k_stride, long long q_out_stride, long long k_out_stride, int elem_type,
+                                int interleaved, float amplitude, void* stream);
+
+/*
+ * Gradient of attn_qk_norm_rope. With n = x / sqrt(mean(x^2) + eps) of a head and g = amplitude R(position)^T dy:
+ *   dweight = sum over rows and heads of n g,   dx = (weight g - n mean(n weight g)) / sqrt(mean(x^2) + eps).
+ *
+ * q, k            the inputs of the forward call
+ * dq_out, dk_out  gradients of its outputs, [T, Hq, d] and [T, Hk, d] in elem_type, rows dq_out_stride
+ *                 (dk_out_stride) elements apart (>= 0)
+ * dq, dk          gradients of its inputs (written), strides >= Hq * d (Hk * d). dq may be dq_out or q with the same stride,
+ *                 dk likewise; other overlaps are not allowed.
+ * dq_weight, dk_weight  device, fp32 [d] (written), or NULL where not wanted (dk_weight has to be NULL when Hk = 0). The sums
+ *                 are added in a fixed order, so equal calls give equal bytes; their parts take memory from the library's
+ *                 stream-ordered pool on `stream` and a second kernel, launched as a programmatic dependent.
+ * Everything else is as for attn_qk_norm_rope.
+ */
+attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                                    const float* q_weight, const float* k_weight, float eps, const int* positions,
+                                    const double* inv_freq, void* dq, void* dk, float* dq_weight, float* dk_weight, int T,
+                                    int Hq, int Hk, int d, int rot_begin, int rot_dim, long long q_stride,
+                                    long long k_stride, long long dq_out_stride, long long dk_out_stride,
+                                    long long dq_stride, long long dk_stride, int elem_type, int interleaved,
+                                    float amplitude, void* stream);
+
+/*
+ * Attention weight per cached token, accumulated: for every token t of every sequence with rows in the call, and every kv head h,
+ *   score[t, h] = decay score[t, h] + sum exp(scale q_i,g . k_t,h - lse_i,g)
+ * over the sequence's rows i that see the token and the query heads g of h. It measures how much a cached token is looked at,
+ * which attn_kv_select_paged chooses by. The tokens of the rows themselves are new: they have no old sum, whatever their slots
+ * hold, so slots need not be cleared before they are used (again).
+ *
+ * q          device, bf16 [T, Hq, d], packed by sequence: the queries of the last n cached tokens of sequence b, in order (all tokens
+ *            of a prompt, its last few, or the one of a decode step). Row i sees the cached tokens up to its own.
+ * lse        device, fp32 [T, Hq], what the attention call of these rows returned (attn_fwd, attn_decode_paged and its forms);
+ *            heads of a row with lse = -inf (that saw nothing) add nothing
+ * k_cache, page_table, page_size, max_pages_per_seq, num_pages, kv_format, k_descale  as for attn_decode_paged_tree
+ * score      device, fp32 [num_pages, Hkv, page_size], the sums of the cache's slots (read and written; with decay = 0 not
+ *            read). Only the slots of tokens below seqlens[b] of sequences with rows are touched. A slot that several of these
+ *            sequences share is left to one of them.
+ * seqlens    device, int32 [B], cached tokens of each sequence, those of the rows included
+ * cu_seqlens device, int32 [B+1], prefix offsets of the sequences' rows in q and lse (non-decreasing, empty sequences allowed), or
+ *            NULL: T / B rows each
+ * max_q      largest number of rows of a sequence (>= 1; at least T / B without cu_seqlens)
+ * Hq, Hkv, d as for attn_decode_paged (d = 64 or 128); T * Hq below 2^31; scale finite
+ * decay      finite; 1 adds to the old sums, 0 overwrites them
+ * A sequence whose length is below its rows or above its page table, or whose offsets decrease, pass T or hold more than max_q rows, is
+ * recorded as ATTN_ERR_DEVICE_BAD_INDEX and its slots are left as they were; so are those of a page outside [0, num_pages).
+ * Arithmetic: products on the tensor cores with fp32 accumulation (bf16, or for 8-bit caches f16: codes widened exactly, q scaled per row
+ * by a power of two that is given back, exact for elements down to 2^-29 of the row's largest), fp32 exponentials and sums, which are
+ * added in a fixed order. Many rows of few tokens are split between the SMs: their parts then take memory from the library's
+ * stream-ordered pool on `stream` and a second kernel, launched as a programmatic dependent.
+ * Alignment: q, k_cache 16 bytes; the others 4.
+ */
+attn_status_t attn_kv_score_paged(const void* q, const float* lse, const void* k_cache, float* score, const int* page_table,
+                                  const int* seqlens, const int* cu_seqlens, int page_size, int T, int B, int max_q, int Hq,
+                                  int Hkv, int d, int max_pages_per_seq, int num_pages, float scale, float decay, int kv_format,
+                                  float k_descale, void* stream);
+
+/*
+ * Which cached tokens stay, for every sequence and kv head on its own. A sequence of more than `budget` tokens keeps its first `sinks`,
+ * its last `recent`, and of those between them the budget - sinks - recent with the largest scores (ties: the earlier token; -0 equals 0,
+ * NaN is above everything). Shorter sequences keep all they have.
+ *
+ * kept       device, int32 [B, Hkv, budget] (written): the token that goes to each slot, -1 behind the last one. A kept token whose index is
+ *            below budget - recent stays in its slot; the slots of the others there are filled in ascending order by the kept tokens
+ *            behind them; the last `recent` tokens follow in order. So kept[j] >= j, few rows have to move, and the next call finds
+ *            the most recent tokens at the end again. (Attention over a cache does not depend on the order of its tokens.)
+ * new_seqlens  device, int32 [B] (written): min(seqlens[b], budget). Not seqlens itself.
+ * score, page_table, page_size, max_pages_per_seq, num_pages  as for attn_kv_score_paged; seqlens device, int32 [B]
+ * budget     >= 1;  sinks, recent >= 0, sinks + recent <= budget
+ * A sequence whose length is negative or above its page table is recorded as ATTN_ERR_DEVICE_BAD_INDEX: its entries of kept are -1, its
+ * new length is the old one. A token on a page outside [0, num_pages) is recorded too and counts as less than every score.
+ * Alignment: 4 bytes.
+ */
+attn_status_t attn_kv_select_paged(const float* score, const int* page_table, const int* seqlens, int* kept, int* new_seqlens,
+                                   int page_size, int B, int Hkv, int max_pages_per_seq, int num_pages, int budget, int sinks,
+                                   int recent, void* stream);
+
+/*
+ * Moves the kept tokens to their slots, in place: row kept[b, h, j] of kv head h of sequence b becomes its row j, for j below
+ * new_seqlens[b], in both caches and in the scores. The slots behind stay as they are (their pages can be given back once no
+ * head needs them, that is behind new_seqlens[b]).
+ *
+ * k_cache, v_cache  device, [num_pages, page_size, Hkv, d] in kv_format (read and written)
+ * score      device, fp32 [num_pages, Hkv, page_size] (read and written), or NULL
+ * kept, new_seqlens  as attn_kv_select_paged gives them. kept[j] >= j has to hold for every j (nothing else: other choices may be
+ *            passed too); entries below j, or of a token beyond the page table, are recorded as ATTN_ERR_DEVICE_BAD_INDEX (-1 is not)
+ *            and their slot stays as it is, and so with pages outside [0, num_pages). The pages of a sequence must not repeat or be shared
+ *            with another one of the call.
+ * d          a multiple of 16, at most 256;  kv_format ATTN_KV_BF16, ATTN_FP8_E4M3 or ATTN_FP8_E5M2 (rows are copied bit for bit)
+ * Alignment: k_cache, v_cache 16 bytes; the others 4.
+ */
+attn_status_t attn_kv_compact_paged(void* k_cache, void* v_cache, float* score, const int* kept, const int* new_seqlens,
+                                    const int* page_table, int page_size, int B, int Hkv, int d, int max_pages_per_seq,
+                                    int num_pages, int budget, int kv_format, void* stream);
 
 /*
  * Host-side split choice of attn_decode_paged (the num_splits = 0 heuristic of "Faster,
