@@ -719,5 +719,19 @@ int current_device_pool(cudaMemPool_t* pool) {
     return st != ATTN_OK ? st : device_pool(ds, pool);
 }
 
+int encode_tiled_map(CUtensorMap* map, const void* base, int elem, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box) {
+    const attn_status_t st = encode_fn();
+    if (st != ATTN_OK) return st;
+    cuuint64_t d[5], s[5];
+    cuuint32_t b[5], one[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) d[i] = dims[i], b[i] = box[i], s[i] = i + 1 < rank ? strides[i] : 0;
+    const CUresult r = g_encode(map, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), d, s,
+                                b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                box[0] * elem == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 unsigned long long watchdog_ns() { return (unsigned long long)(options().watchdog_ms * 1e6); }
 }  // namespace attn

@@ -4,8 +4,8 @@
 // The transposed scores S^T = K Q^T have the tokens as rows of the accumulator, so that a thread owns a token: it
 // reads its row of S^T from tensor memory, adds exp2(scale s - lse) over the columns, and needs no sum across threads. A unit of
 // work is 256 tokens of a (sequence, kv head), two accumulator tiles that share the operand Q; a task is a unit times a
-// block of 128 rows (queries x query heads, in the order of q) that see any of it. The tasks of the whole call, in the order
-// sequence, kv head, tokens, rows, are dealt out in equal runs to one persistent block per SM. A unit that lies in more than
+// block of up to 128 rows (as many whole queries times their query heads as fit) that see any of it. The tasks of the whole call, in the
+// order sequence, kv head, tokens, rows, are dealt out in equal runs to one persistent block per SM. A unit that lies in more than
 // one run leaves partial sums, which a second kernel adds in order.
 //
 // What bounds it. With d = 128 a task is 2 x 8 products of 128 x 128 x 16, 1024 clocks of the tensor pipe, and 32768
@@ -13,11 +13,12 @@
 // keys for that, more than the memory delivers in the time.
 //
 // Roles of the warps: 0-3 and 4-7 exponentials and sums, a group per accumulator tile (two buffers each, so that the
-// products of a task run during the exponentials of the one before); 8-11 loads (16-byte asynchronous copies of rows that the page
-// table gives, so any page size); 12 the products, issued by one thread.
+// products of a task run during the exponentials of the one before); 8 and 9 the keys of a tile each, through tensor copies of 64 or
+// 16 rows where the page size is a multiple of that, else by 16-byte copies of rows that the page table gives; 10 the blocks of q
+// through tensor copies (one box is the heads of as many queries as fit) and their LSE; 12 the products, issued by one thread.
 //
-// 8-bit caches: K is multiplied as it is (kind::f8f6f4), each row of Q scaled by a power of two and split into two e4m3
-// parts: exact unless an element is more than 2^9 below the row's largest (then off by at most 2^-17 of that).
+// 8-bit caches: K is multiplied as it is (kind::f8f6f4). A kernel before this one scales each row of q by a power of two and splits
+// it into two e4m3 parts: exact unless an element is more than 2^9 below the row's largest (then off by at most 2^-17 of that).
 #include "score.cuh"
 
 namespace attn {
@@ -32,25 +33,34 @@ template <int D, int FMT>
 struct ScoreLayout {
     static constexpr bool kF8 = FMT != ATTN_KV_BF16;
     static constexpr int kRow = kF8 ? D : 2 * D;             // bytes of a key
-    static constexpr int kChunk = 128 * (kRow < 128 ? kRow : 128);  // [128 rows x 128 (64) bytes]
-    static constexpr int kChunks = kRow > 128 ? 2 : 1;       // of a tile of keys or a 16-bit block of q
+    static constexpr int kBox = kRow < 128 ? kRow : 128;     // bytes of a row in a copy
+    static constexpr int kChunk = 128 * kBox;                // [128 rows x 128 (64) bytes]
+    static constexpr int kChunks = kRow / kBox;              // of a tile of keys
     static constexpr int kTile = kChunk * kChunks;
-    static constexpr int kQ = kF8 ? 2 * kTile : kTile;       // the block of q, in two parts when 8-bit
+    static constexpr int kQChunks = kF8 ? 2 : kChunks;       // of a block of q: its columns, or its two 8-bit parts
+    static constexpr int kQ = kQChunks * kChunk;
     static constexpr int kK = 2 * kTile;                     // keys of a unit
-    static constexpr int kKOff = 0;                          // two stages
-    static constexpr int kQOff = 2 * kK;                     // two stages
-    // per row of a block of q: LSE (times log2 e), factor of the scores, last token seen
+    static constexpr int kKStages = kK > 32768 ? 2 : 4;
+    static constexpr int kKOff = 0, kQOff = kKStages * kK;   // (q: two stages)
+    // per row of a block of q: minus the LSE (times log2 e), factor of the scores, last token seen
     static constexpr int kLseOff = kQOff + 2 * kQ, kLseStage = 3 * kBlockRows * 4;
     static constexpr int kBarOff = kLseOff + kLseStages * kLseStage;
-    static constexpr int bK = 0, bKFree = 2, bQ = 4, bQFree = 6, bLFree = 8, bS = bLFree + kLseStages, bSFree = bS + 4;
-    static constexpr int bL = bSFree + 4, bDrain = bL + kLseStages, kBars = bDrain + 1;
-    // tensor-memory base, abort flag; rows that need their own limits, per lse stage and loading warp; the plan
-    static constexpr int kMiscOff = kBarOff + kBars * 8, kOddOff = kMiscOff + 8, kPlanOff = kOddOff + kLseStages * 16;
-    static constexpr int kBytes = kPlanOff + 64;
-    static_assert(kBarOff % 8 == 0 && kOddOff % 16 == 0 && kBytes <= 232448, "shared memory of an SM");
+    static constexpr int bK = 0, bKFree = bK + kKStages, bQ = bKFree + kKStages, bQFree = bQ + 2, bL = bQFree + 2, bLFree = bL + kLseStages;
+    static constexpr int bS = bLFree + kLseStages, bSFree = bS + 4, bDrain = bSFree + 4, kBars = bDrain + 1;
+    // tensor-memory base, abort flag; per lse stage: do rows need their own limits; the plan
+    static constexpr int kMiscOff = kBarOff + kBars * 8, kOddOff = kMiscOff + 8, kPlanOff = kOddOff + kLseStages * 4;
+    static constexpr int kBytes = kPlanOff + 16;
+    static_assert(kBarOff % 8 == 0 && kPlanOff % 8 == 0 && kBytes <= 232448, "shared memory of an SM");
 };
 
 __device__ __forceinline__ void fence_smem_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c, int r) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(r)
+        : "memory");
+}
 
 __device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -98,28 +108,70 @@ __device__ __forceinline__ void e4m3x4_values(uint32_t w, float (&f)[4]) {
     }
 }
 
+// Rows of q for an 8-bit cache: parts [T Hq, 2, D] of e4m3 and the factor of each row's scores. D / 8 threads per row.
+template <int D>
+__global__ void __launch_bounds__(256) split_q_kernel(const __nv_bfloat16* q, uint8_t* parts, float* factor, long long rows, float scale_log2) {
+    grid_dependents_launch();
+    constexpr int kUnits = D / 8;
+    const long long r = ((long long)blockIdx.x * 256 + threadIdx.x) / kUnits;
+    const int u = threadIdx.x % kUnits;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (r < rows) w = __ldg(reinterpret_cast<const uint4*>(q + r * D) + u);
+    const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) top = max(top, max(e[y] & 0x7FFFu, (e[y] >> 16) & 0x7FFFu));
+#pragma unroll
+    for (int o = 1; o < kUnits; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (r >= rows) return;
+    // 2^up brings the largest magnitude into [128, 256) (biased exponent 127 + 7 + 127 - exponent; the tiniest rows as far as a
+    // float reaches)
+    const int exponent = (int)(top >> 7);
+    float up = 1.0f;
+    if (exponent < 255 && top != 0) up = __uint_as_float((unsigned)min(254, 261 - exponent) << 23);
+    uint32_t part[2][2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        float f[4], v[4];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            f[2 * z] = __uint_as_float(e[2 * y + z] << 16) * up;
+            f[2 * z + 1] = __uint_as_float(e[2 * y + z] & 0xFFFF0000u) * up;
+        }
+        part[0][y] = e4m3x4(f[0], f[1], f[2], f[3]);
+        e4m3x4_values(part[0][y], v);
+        part[1][y] = e4m3x4(f[0] - v[0], f[1] - v[1], f[2] - v[2], f[3] - v[3]);
+    }
+    uint2* to = reinterpret_cast<uint2*>(parts + r * 2 * D);
+    to[u] = make_uint2(part[0][0], part[0][1]);
+    to[kUnits + u] = make_uint2(part[1][0], part[1][1]);
+    // a row with a non-finite element gives NaN
+    if (u == 0) factor[r] = exponent == 255 ? __int_as_float(0x7fffffff) : scale_log2 / up;
+}
+
 // ---- the tasks of a call
 
-// Tasks of one kv head of a sequence. Unit u (tokens from 256 u on) is seen by the blocks of rows from first(u) on.
+// Tasks of one kv head of a sequence. Unit u (tokens from 256 u on) is taken with the blocks of rows from first(u) on; blocks that
+// do not see it may be among them (when the queries of a block do not divide 256).
 struct SeqTasks {
     int units, blocks;
-    long long skip;  // first(u) = max(0, 2 G u - skip)
-    int G2;
-    __device__ __forceinline__ SeqTasks(const ScoreSeq& s, int G) {
+    long long skip;  // first(u) = max(0, each u - skip)
+    int each;        // blocks of 256 tokens, rounded down
+    __device__ __forceinline__ SeqTasks(const ScoreSeq& s, int block_tok, int head_blocks) {
         units = (s.len + kUnitTok - 1) / kUnitTok;
-        blocks = (int)(((long long)s.n * G + kBlockRows - 1) / kBlockRows);
-        // row i G of token 256 u is in block floor((256 u - ctx) G / 128) = 2 G u - ceil(ctx G / 128)
-        skip = ((long long)s.ctx * G + kBlockRows - 1) / kBlockRows;
-        G2 = 2 * G;
+        blocks = (s.n + block_tok - 1) / block_tok * head_blocks;
+        // token 256 u is query 256 u - ctx, in block floor((256 u - ctx) / block_tok) >= floor(256 / block_tok) u - ceil(ctx / block_tok)
+        each = kUnitTok / block_tok * head_blocks;
+        skip = (long long)((s.ctx + block_tok - 1) / block_tok) * head_blocks;
     }
     __device__ __forceinline__ int first(int u) const {
-        const long long f = (long long)G2 * u - skip;
+        const long long f = (long long)each * u - skip;
         return f > 0 ? (int)f : 0;
     }
     // tasks of the units before u
     __device__ __forceinline__ long long before(int u) const {
-        const long long from = skip / G2 + 1;  // the first unit that not all blocks see
-        const long long cut = u > from ? (long long)G2 * ((from + u - 1) * (u - from) / 2) - skip * (u - from) : 0;
+        const long long from = skip / each + 1;  // the first unit that not all blocks see
+        const long long cut = u > from ? (long long)each * ((from + u - 1) * (u - from) / 2) - skip * (u - from) : 0;
         return (long long)blocks * u - cut;
     }
 };
@@ -129,9 +181,9 @@ struct TaskWalk {
     int b, h, u, r;
     ScoreSeq s;
     SeqTasks seq;
-    __device__ __forceinline__ TaskWalk(const ScoreParams& p, int b_, long long rest) : b(b_), s(), seq(s, 1) {
+    __device__ __forceinline__ TaskWalk(const ScoreParams& p, int b_, long long rest) : b(b_), s(), seq(s, 1, 1) {
         score_seq(p, b, s);
-        seq = SeqTasks(s, p.G);
+        seq = SeqTasks(s, p.block_tok, p.head_blocks);
         const long long each = seq.before(seq.units);
         h = (int)(rest / each);
         rest -= each * h;
@@ -147,6 +199,12 @@ struct TaskWalk {
         r = seq.first(u) + (int)(rest - seq.before(u));
     }
     __device__ __forceinline__ bool last_block() const { return r + 1 == seq.blocks; }
+    // first query of the block, its rows that there are
+    __device__ __forceinline__ int query(const ScoreParams& p) const { return p.head_blocks > 1 ? r / p.head_blocks : r * p.block_tok; }
+    __device__ __forceinline__ int rows(const ScoreParams& p) const {
+        if (p.head_blocks > 1) return min(kBlockRows, p.G - r % p.head_blocks * kBlockRows);
+        return min(p.block_tok, s.n - r * p.block_tok) * p.G;
+    }
     // The next task (there is one). Returns whether the unit changes; q_changes: whether the block of q does.
     __device__ __forceinline__ bool next(const ScoreParams& p, bool& q_changes) {
         const int r0 = r;
@@ -162,7 +220,7 @@ struct TaskWalk {
         h = 0;
         do ++b;
         while (!score_seq(p, b, s));
-        seq = SeqTasks(s, p.G);
+        seq = SeqTasks(s, p.block_tok, p.head_blocks);
         return true;
     }
 };
@@ -171,15 +229,15 @@ struct TaskWalk {
 __device__ __forceinline__ long long tasks_of(const ScoreParams& p, int b) {
     ScoreSeq s;
     if (!score_seq(p, b, s)) return 0;
-    const SeqTasks t(s, p.G);
+    const SeqTasks t(s, p.block_tok, p.head_blocks);
     return t.before(t.units) * p.Hkv;
 }
 
 // The run of tasks [from, from + count) of block `block`: its first sequence and the task within that. Every thread of the
-// block calls it; scratch: 8-byte words for the threads' sums (kWarps) and four results.
+// block calls it; sums: a word per warp, out: two.
 struct TaskRun {
-    long long each, from, total;  // tasks per block; of this one: its first, and the call's number
-    long long rest;               // tasks of sequence b before it
+    long long each, from;  // tasks per block; the first one of this
+    long long rest;        // tasks of sequence b before it
     int b, count;
 };
 template <int kThreads>
@@ -203,7 +261,6 @@ __device__ __forceinline__ TaskRun task_run(const ScoreParams& p, int block, int
         total += sums[w];
     }
     TaskRun run;
-    run.total = total;
     run.each = (total + blocks - 1) / blocks;
     run.from = run.each * block;
     const long long left = total - run.from;
@@ -223,31 +280,35 @@ __device__ __forceinline__ TaskRun task_run(const ScoreParams& p, int block, int
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kTileThreads, 1) score_tiles_kernel(const __grid_constant__ ScoreParams p) {
+__global__ void __launch_bounds__(kTileThreads, 1)
+    score_tiles_kernel(const __grid_constant__ ScoreParams p, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK) {
     grid_dependents_launch();
     using L = ScoreLayout<D, FMT>;
     constexpr bool F8 = L::kF8;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
     const TaskRun run = task_run<kTileThreads>(p, blockIdx.x, gridDim.x, reinterpret_cast<long long*>(smem), reinterpret_cast<long long*>(smem + L::kPlanOff));
-    if (run.count == 0) return;
-    if (smem_u32(smem) & 1023u) {  // the swizzles count from such boundaries
-        if (threadIdx.x == 0) atomicCAS(p.status, 0, kDevTimeout);
+    if (run.count == 0 || smem_u32(smem) & 1023u) {  // (the swizzles count from such boundaries)
+        if (run.count > 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kDevTimeout);
+        if (F8) grid_dependency_wait();
         return;
     }
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+    int* odd_rows = reinterpret_cast<int*>(smem + L::kOddOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t wd = p.watchdog_ns;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars[L::bK + i], 4);
+        for (int i = 0; i < L::kKStages; ++i) {
+            mbar_init(&bars[L::bK + i], 2);
             mbar_init(&bars[L::bKFree + i], 1);
-            mbar_init(&bars[L::bQ + i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[L::bQ + i], 1);
             mbar_init(&bars[L::bQFree + i], 1);
         }
         for (int i = 0; i < kLseStages; ++i) {
-            mbar_init(&bars[L::bL + i], 4);
+            mbar_init(&bars[L::bL + i], 1);
             mbar_init(&bars[L::bLFree + i], 8);
         }
         for (int i = 0; i < 4; ++i) {
@@ -257,7 +318,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) score_tiles_kernel(const __gr
         mbar_init(&bars[L::bDrain], 1);
         *abort_flag = 0;
         fence_mbar_init();
+        tma_prefetch_desc(&tmQ);
+        if (p.box_rows > 1) tma_prefetch_desc(&tmK);
     }
+    // rows that no copy of q writes are zeros
+    for (int i = threadIdx.x; i < 2 * L::kQ / 16; i += kTileThreads) reinterpret_cast<uint4*>(smem + L::kQOff)[i] = make_uint4(0, 0, 0, 0);
+    fence_smem_to_async();
     if (warp == 12) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
@@ -268,147 +334,177 @@ __global__ void __launch_bounds__(kTileThreads, 1) score_tiles_kernel(const __gr
     const uint32_t tmem = *tmem_slot;
     const uint32_t base = smem_u32(smem);
     TaskWalk at(p, run.b, run.rest);
-    // stages of units and blocks of q are counted from the first of the run
-    unsigned unit = 0, qn = 0;
 
-    if (warp >= 8 && warp < 12) {
-        // ---------------------------------------------------------------- loads
-        const int tid = threadIdx.x - 256;
-        uint64_t *pending = nullptr, *pending_lse = nullptr;  // of the load whose copies may still be on their way
-        bool ok = true;
-        auto hand_over = [&](auto left) {
+    if (warp == 8 || warp == 9) {
+        // ---------------------------------------------------------------- keys of tile warp - 8
+        const int tile = warp - 8;
+        bool ok = true, ignored;
+        int unit = 0;
+        const CUtensorMap* map = &tmK;
+        const int none = p.num_pages * p.page_size;  // the first row past the cache: zeros
+        uint64_t* pending = nullptr;                  // the stage whose 16-byte copies may still be on their way
+        auto hand_over = [&]() {
             if (!pending) return;
-            cp_async_wait<decltype(left)::value>();
             fence_smem_to_async();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(pending);
-                if (pending_lse) mbar_arrive(pending_lse);
-            }
-            pending = pending_lse = nullptr;
+            if (lane == 0) mbar_arrive(pending);
+            pending = nullptr;
         };
-        // a stage that is not free yet may wait for what this warp has not handed over
-        auto wait_free = [&](uint64_t* bar, uint32_t parity) {
-            if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
-            hand_over(std::integral_constant<int, 0>{});
-            return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, wd));
-        };
-        bool new_unit = true, new_q = true;
-        for (int i = 0; ok; ++i) {
-            if (new_unit) {
-                const int st = unit & 1;
-                if (!(ok = wait_free(&bars[L::bKFree + st], (unit >> 1 & 1u) ^ 1u))) break;
-                // a thread copies unit tid % kUnits of rows tid / kUnits, + kStep, ...
-                constexpr int kUnits = L::kRow / 16, kStep = 128 / kUnits;
-                const int* pt = p.page_table + (long long)at.b * p.max_pages;
-                const int t0 = at.u * kUnitTok, u = tid % kUnits;
+        for (int i = 0;;) {
+            const int st = unit % L::kKStages;
+            const uint32_t parity = (uint32_t)(unit / L::kKStages & 1) ^ 1u;
+            const int t0 = at.u * kUnitTok + tile * kTileTok;
+            const int* pt = p.page_table + (long long)at.b * p.max_pages;
+            const uint32_t to = base + L::kKOff + st * L::kK + tile * L::kTile;
+            uint64_t* full = &bars[L::bK + st];
+            if (p.box_rows > 1) {
+                // lane -> rows of one page, and which columns of them
+                const int boxes = kTileTok / p.box_rows;
+                const int part = lane / boxes, first = (lane - part * boxes) * p.box_rows;
+                const bool active = lane < L::kChunks * boxes;
+                int row = none, slot;
+                if (active && t0 + first < at.s.len) {
+                    const int page = score_place(p, pt, t0 + first, slot);
+                    if (page >= 0) row = page * p.page_size + slot;
+                }
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::bKFree + st], parity, abort_flag, wd)))) break;
+                if (lane == 0) mbar_arrive_expect_tx(full, L::kTile);
+                __syncwarp();
+                if (active) copy_box(to + part * L::kChunk + first * L::kBox, map, full, at.h * D + part * (L::kBox / (F8 ? 1 : 2)), row);
+                __syncwarp();
+            } else {
+                // rows of tokens lane, lane + 32, ...; 16-byte pieces of all of them
+                constexpr int kUnits = L::kRow / 16, kStep = 32 / kUnits;
+                int row[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    int slot;
+                    const int page = t0 + lane + 32 * e < at.s.len ? score_place(p, pt, t0 + lane + 32 * e, slot) : -1;
+                    row[e] = page >= 0 ? page * p.page_size + slot : -1;
+                }
+                // (a stage that is not free yet may wait for what this warp has not handed over)
+                if (!__all_sync(0xffffffffu, mbar_test_wait(&bars[L::bKFree + st], parity))) {
+                    cp_async_wait<0>();
+                    hand_over();
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::bKFree + st], parity, abort_flag, wd)))) break;
+                }
+                const int u = lane % kUnits;
                 const uint8_t* keys = static_cast<const uint8_t*>(p.k_cache) + (long long)at.h * L::kRow + 16 * u;
-                const uint32_t to = base + L::kKOff + st * L::kK;
+                const long long row_bytes = (long long)p.Hkv * L::kRow;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
 #pragma unroll 8
-                for (int r = tid / kUnits; r < kUnitTok; r += kStep) {
-                    int slot = 0;
-                    const int page = t0 + r < at.s.len ? score_place(p, pt, t0 + r, slot) : -1;
-                    const long long row = page >= 0 ? (long long)page * p.page_size + slot : 0;
-                    cp_async16(to + (r / kTileTok) * L::kTile + unit_at<L::kRow>(r % kTileTok, u), keys + row * p.Hkv * L::kRow, page >= 0 ? 16 : 0);
-                }
-                cp_async_commit();
-                hand_over(std::integral_constant<int, 1>{});
-                pending = &bars[L::bK + st];
-                ++unit;
-            }
-            if (new_q) {
-                const int st = qn & 1, ls = qn % kLseStages;
-                if (!(ok = wait_free(&bars[L::bQFree + st], (qn >> 1 & 1u) ^ 1u))) break;
-                if (!(ok = wait_free(&bars[L::bLFree + ls], (qn / kLseStages & 1u) ^ 1u))) break;
-                const int rows = (int)min((long long)kBlockRows, (long long)at.s.n * p.G - (long long)at.r * kBlockRows);
-                const int r0 = at.r * kBlockRows;  // (below n G < 2^31)
-                auto row_of = [&](int r) {
-                    const int i = (r0 + r) / p.G;
-                    return (long long)(at.s.q0 + i) * p.Hq + at.h * p.G + (r0 + r - i * p.G);
-                };
-                float* lse2 = reinterpret_cast<float*>(smem + L::kLseOff + ls * L::kLseStage);
-                const uint32_t to = base + L::kQOff + st * L::kQ;
-                constexpr int kUnits = D / 8, kStep = 128 / kUnits;
-                const int u = tid % kUnits;
-                if constexpr (!F8) {
-#pragma unroll 4
-                    for (int r = tid / kUnits; r < kBlockRows; r += kStep)
-                        cp_async16(to + unit_at<L::kRow>(r, u), p.q + row_of(r < rows ? r : 0) * D + 8 * u, r < rows ? 16 : 0);
-                } else {
-                    // 2^up brings the largest magnitude of the row into [128, 256)
-#pragma unroll 4
-                    for (int r = tid / kUnits; r < kBlockRows; r += kStep) {
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        if (r < rows) w = __ldg(reinterpret_cast<const uint4*>(p.q + row_of(r) * D) + u);
-                        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
-                        uint32_t top = 0;
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) top = max(top, max(e[y] & 0x7FFFu, (e[y] >> 16) & 0x7FFFu));
-#pragma unroll
-                        for (int o = 1; o < kUnits; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const int exponent = (int)(top >> 7);
-                        // (biased exponent 127 + 7 + 127 - exponent; the tiniest rows as far as a float reaches)
-                        float up = 1.0f;
-                        if (exponent < 255 && top != 0) up = __uint_as_float((unsigned)min(254, 261 - exponent) << 23);
-                        uint32_t part[2][2];
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            float f[4], v[4];
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                f[2 * z] = __uint_as_float(e[2 * y + z] << 16) * up;
-                                f[2 * z + 1] = __uint_as_float(e[2 * y + z] & 0xFFFF0000u) * up;
-                            }
-                            part[0][y] = e4m3x4(f[0], f[1], f[2], f[3]);
-                            e4m3x4_values(part[0][y], v);
-                            part[1][y] = e4m3x4(f[0] - v[0], f[1] - v[1], f[2] - v[2], f[3] - v[3]);
-                        }
-                        const uint32_t dst = to + unit_at<L::kRow>(r, u >> 1) + 8 * (u & 1);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst + x * L::kTile), "r"(part[x][0]), "r"(part[x][1]) : "memory");
-                        // a row with a non-finite element gives NaN
-                        if (u == 0) lse2[kBlockRows + r] = exponent == 255 ? __int_as_float(0x7fffffff) : p.scale_log2 / up;
+                    for (int r = lane / kUnits; r < 32; r += kStep) {
+                        const int from = __shfl_sync(0xffffffffu, row[e], r);
+                        cp_async16(to + unit_at<L::kRow>(32 * e + r, u), keys + (from >= 0 ? from : 0) * row_bytes, from >= 0 ? 16 : 0);
                     }
-                }
-                // LSE and last token of row tid; does any row need its own limit besides the causal one?
-                const float l = tid < rows ? __ldg(p.lse + row_of(tid)) : -INFINITY;
-                lse2[tid] = l == -INFINITY ? 0.0f : l * 1.4426950408889634f;
-                reinterpret_cast<int*>(lse2)[2 * kBlockRows + tid] = l == -INFINITY ? -1 : at.s.ctx + (r0 + tid) / p.G;
-                const bool odd = __any_sync(0xffffffffu, l == -INFINITY);
-                if (lane == 0) reinterpret_cast<int*>(smem + L::kOddOff)[ls * 4 + (tid >> 5)] = odd;
                 cp_async_commit();
-                hand_over(std::integral_constant<int, 1>{});
-                pending = &bars[L::bQ + st];
-                pending_lse = &bars[L::bL + ls];
-                ++qn;
+                if (pending) cp_async_wait<1>();
+                hand_over();
+                pending = full;
             }
-            if (i + 1 == run.count) break;
-            new_unit = at.next(p, new_q);
+            ++unit;
+            // on to the next unit
+            bool more = false;
+            while (++i < run.count && !(more = at.next(p, ignored))) {
+            }
+            if (!more) break;
         }
-        hand_over(std::integral_constant<int, 0>{});
         cp_async_wait<0>();
+        hand_over();
+        if (!ok && p.box_rows > 1) {
+            // let the copies in flight land before the block can end
+            int dummy = 0;
+            for (int x = unit > L::kKStages ? unit - L::kKStages : 0; x < unit; ++x)
+                mbar_wait(&bars[L::bK + x % L::kKStages], (uint32_t)(x / L::kKStages & 1), &dummy, 20000000ull);
+        }
+    } else if (warp == 10) {
+        // ---------------------------------------------------------------- blocks of q and their LSE
+        if (F8) grid_dependency_wait();  // the parts of q
+        const bool by_head = p.head_blocks > 1;
+        const int box_heads = by_head ? kBlockRows : p.G;
+        const uint32_t bytes = (uint32_t)(box_heads * p.block_tok * L::kBox * L::kQChunks);
+        int query[4], head[4];  // of rows lane, lane + 32, ... of a block
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = lane + 32 * e;
+            query[e] = by_head ? 0 : r / p.G;
+            head[e] = by_head ? r : r - query[e] * p.G;
+        }
+        bool ok = true, new_q = true;
+        int qn = 0;
+        for (int i = 0;;) {
+            const int st = qn & 1, ls = qn % kLseStages;
+            const int i0 = at.query(p), h0 = by_head ? at.r % p.head_blocks * kBlockRows : 0;  // first query, first of the kv head's heads
+            float l[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool there = query[e] < p.block_tok && i0 + query[e] < at.s.n && h0 + head[e] < p.G;
+                const long long row = (long long)(at.s.q0 + i0 + query[e]) * p.Hq + at.h * p.G + h0 + head[e];
+                l[e] = there ? __ldg(p.lse + row) : -INFINITY;
+            }
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::bQFree + st], (uint32_t)(qn >> 1 & 1) ^ 1u, abort_flag, wd)))) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars[L::bQ + st], bytes);
+#pragma unroll
+                for (int c = 0; c < L::kQChunks; ++c)
+                    tma_load_3d(smem + L::kQOff + st * L::kQ + c * L::kChunk, &tmQ, &bars[L::bQ + st], c * (L::kBox / (F8 ? 1 : 2)), at.h * p.G + h0,
+                                at.s.q0 + i0);
+            }
+            __syncwarp();
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::bLFree + ls], (uint32_t)(qn / kLseStages & 1) ^ 1u, abort_flag, wd)))) {
+                ++qn;
+                break;
+            }
+            float* lse2 = reinterpret_cast<float*>(smem + L::kLseOff + ls * L::kLseStage);
+            bool odd = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = lane + 32 * e;
+                // rows behind the box are zeros and get weight 0; others that are not there, or saw nothing, are masked
+                const bool none = l[e] == -INFINITY, behind = query[e] >= p.block_tok;
+                odd = odd || (none && !behind);
+                lse2[r] = none ? (behind ? -INFINITY : 0.0f) : l[e] * -1.4426950408889634f;
+                reinterpret_cast<int*>(lse2)[2 * kBlockRows + r] = none ? (behind ? INT32_MAX : -1) : at.s.ctx + i0 + query[e];
+                if (F8)
+                    lse2[kBlockRows + r] = none ? 0.0f
+                                                : __ldg(p.factor + (long long)(at.s.q0 + i0 + query[e]) * p.Hq + at.h * p.G + h0 + head[e]);
+            }
+            odd = __any_sync(0xffffffffu, odd);
+            if (lane == 0) odd_rows[ls] = odd;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[L::bL + ls]);
+            ++qn;
+            new_q = false;
+            while (++i < run.count) {
+                at.next(p, new_q);
+                if (new_q) break;
+            }
+            if (i >= run.count) break;
+        }
+        if (!ok) {
+            int dummy = 0;
+            for (int x = qn > 2 ? qn - 2 : 0; x < qn; ++x) mbar_wait(&bars[L::bQ + (x & 1)], (uint32_t)(x >> 1 & 1), &dummy, 20000000ull);
+        }
     } else if (warp == 12) {
         // ---------------------------------------------------------------- products
         if (lane == 0) {
-            constexpr bool kNarrow = L::kRow == 64;
-            auto desc = [&](int off) { return kNarrow ? smem_desc_sw64(base + off) : smem_desc_sw128(base + off, L::kChunk, 1024); };
+            auto desc = [&](int off) { return L::kBox == 64 ? smem_desc_sw64(base + off) : smem_desc_sw128(base + off, L::kChunk, 1024); };
             const uint64_t dk = desc(L::kKOff), dq = desc(L::kQOff);
             auto wait = [&](int bar, uint32_t parity) { return mbar_wait(&bars[bar], parity, abort_flag, wd); };
             bool any = false, new_unit = true, new_q = true;
-            unsigned units = 0, qs = 0;  // stages waited for
+            int units = 0, qs = 0;  // stages waited for
             for (int i = 0;; ++i) {
                 if (new_unit) {
-                    if (!wait(L::bK + (units & 1), units >> 1 & 1u)) break;
+                    if (!wait(L::bK + units % L::kKStages, units / L::kKStages & 1)) break;
                     ++units;
                 }
                 if (new_q) {
-                    if (!wait(L::bQ + (qs & 1), qs >> 1 & 1u)) break;
+                    if (!wait(L::bQ + (qs & 1), qs >> 1 & 1)) break;
                     ++qs;
                 }
-                const int ks = (units - 1) & 1, st = (qs - 1) & 1, buf = i & 1;
-                const int rows = (int)min((long long)kBlockRows, (long long)at.s.n * p.G - (long long)at.r * kBlockRows);
-                const uint32_t idesc = score_idesc<FMT>((rows + 31) & ~31);
+                const int ks = (units - 1) % L::kKStages, st = (qs - 1) & 1, buf = i & 1;
+                const uint32_t idesc = score_idesc<FMT>((at.rows(p) + 31) & ~31);
                 bool go = true;
 #pragma unroll 1
                 for (int t = 0; t < 2 && (go = wait(L::bSFree + 2 * t + buf, (unsigned)(i >> 1 & 1) ^ 1u)); ++t) {
@@ -418,9 +514,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) score_tiles_kernel(const __gr
                     const uint64_t kd = dk + (uint64_t)((ks * L::kK + t * L::kTile) >> 4), qd = dq + (uint64_t)((st * L::kQ) >> 4);
                     if constexpr (F8) {
 #pragma unroll
-                        for (int x = 0; x < 2 * (D / 32); ++x) {  // both parts of Q
+                        for (int x = 0; x < 2 * (D / 32); ++x) {  // both parts of q
                             const int part = x / (D / 32), k = x % (D / 32);
-                            mma8_ss(d, kd + (uint64_t)((k * 32) >> 4), qd + (uint64_t)((part * L::kTile + k * 32) >> 4), idesc, x > 0);
+                            mma8_ss(d, kd + (uint64_t)((k * 32) >> 4), qd + (uint64_t)((part * L::kChunk + k * 32) >> 4), idesc, x > 0);
                         }
                     } else {
 #pragma unroll
@@ -444,61 +540,76 @@ __global__ void __launch_bounds__(kTileThreads, 1) score_tiles_kernel(const __gr
             }
         }
         __syncwarp();
-    } else {
+    } else if (warp < 8) {
         // ---------------------------------------------------------------- exponentials and sums
         const int tile = warp >> 2, quarter = warp & 3, mine = tile * kTileTok + quarter * 32 + lane;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         bool new_unit = true, new_q = true, whole = at.r == at.seq.first(at.u);
         int piece = whole ? 1 : 0;  // place of a partial sum: 0 for the unit that an earlier run began, 1 for the last one
-        unsigned qs = 0;
+        int qs = 0;
         float total = 0.0f;
         for (int i = 0;; ++i) {
             if (new_unit) total = 0.0f;
             if (new_q) ++qs;
             const int ls = (qs - 1) % kLseStages, buf = i & 1;
-            const int rows = (int)min((long long)kBlockRows, (long long)at.s.n * p.G - (long long)at.r * kBlockRows);
+            const int rows = at.rows(p), i0 = at.query(p);
             const int tok = at.u * kUnitTok + mine, first = at.u * kUnitTok + tile * kTileTok;
             // (not the barrier of q: its stage may have been filled twice since)
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars[L::bL + ls], (qs - 1) / kLseStages & 1u, abort_flag, wd))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars[L::bL + ls], (uint32_t)((qs - 1) / kLseStages & 1), abort_flag, wd))) break;
             const float* lse2 = reinterpret_cast<const float*>(smem + L::kLseOff + ls * L::kLseStage);
             const float* factor = lse2 + kBlockRows;
             const int* last = reinterpret_cast<const int*>(lse2 + 2 * kBlockRows);
-            const int4 odd = *reinterpret_cast<const int4*>(smem + L::kOddOff + ls * 16);
             // the first row sees the fewest tokens, the last one the most
-            const int top = at.s.ctx + (at.r * kBlockRows + rows - 1) / p.G;
-            const bool mixed = (odd.x | odd.y | odd.z | odd.w) != 0 || at.s.ctx + at.r * kBlockRows / p.G < first + kTileTok - 1;
+            const int top = at.s.ctx + min(i0 + p.block_tok, at.s.n) - 1;
+            const bool mixed = odd_rows[ls] != 0 || at.s.ctx + i0 < first + kTileTok - 1;
             if (!__all_sync(0xffffffffu, mbar_wait(&bars[L::bS + 2 * tile + buf], (unsigned)(i >> 1 & 1), abort_flag, wd))) break;
             tc_fence_after();
             const uint32_t from = tmem + lane_off + (uint32_t)(2 * tile + buf) * 128;
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (first <= top && first < at.s.len) {
-#pragma unroll 1
-                for (int c = 0; c < rows; c += 32) {
-                    uint32_t x[32];
-                    tmem_ld32(from + c, x);
-                    tc_wait_ld();
-                    reg_fence(x);
+            auto add = [&](const uint32_t (&x)[32], int c, auto masked) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 l = *reinterpret_cast<const float4*>(lse2 + c + e);
-                        float4 f = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
-                        if constexpr (F8) f = *reinterpret_cast<const float4*>(factor + c + e);
-                        float y[4];
-                        ffma2(y[0], y[1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]), f.x, f.y, -l.x, -l.y);
-                        ffma2(y[2], y[3], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]), f.z, f.w, -l.z, -l.w);
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 l = *reinterpret_cast<const float4*>(lse2 + c + e);
+                    float4 f = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+                    if constexpr (F8) f = *reinterpret_cast<const float4*>(factor + c + e);
+                    float y[4];
+                    ffma2(y[0], y[1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]), f.x, f.y, l.x, l.y);
+                    ffma2(y[2], y[3], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]), f.z, f.w, l.z, l.w);
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) y[z] = ex2_mufu(y[z]);
-                        if (mixed) {
-                            const int4 m = *reinterpret_cast<const int4*>(last + c + e);
-                            y[0] = tok <= m.x ? y[0] : 0.0f;
-                            y[1] = tok <= m.y ? y[1] : 0.0f;
-                            y[2] = tok <= m.z ? y[2] : 0.0f;
-                            y[3] = tok <= m.w ? y[3] : 0.0f;
-                        }
-                        fadd2(sum[0], sum[1], sum[0], sum[1], y[0], y[1]);
-                        fadd2(sum[2], sum[3], sum[2], sum[3], y[2], y[3]);
+                    for (int z = 0; z < 4; ++z) y[z] = ex2_mufu(y[z]);
+                    if constexpr (decltype(masked)::value) {
+                        const int4 m = *reinterpret_cast<const int4*>(last + c + e);
+                        y[0] = tok <= m.x ? y[0] : 0.0f;
+                        y[1] = tok <= m.y ? y[1] : 0.0f;
+                        y[2] = tok <= m.z ? y[2] : 0.0f;
+                        y[3] = tok <= m.w ? y[3] : 0.0f;
                     }
+                    fadd2(sum[0], sum[1], sum[0], sum[1], y[0], y[1]);
+                    fadd2(sum[2], sum[3], sum[2], sum[3], y[2], y[3]);
                 }
+            };
+            if (first <= top && first < at.s.len) {
+                // the next columns are on their way while these are added
+                uint32_t x0[32], x1[32];
+                auto all = [&](auto masked) {
+                    tmem_ld32(from, x0);
+#pragma unroll 1
+                    for (int c = 0; c < rows; c += 64) {
+                        tc_wait_ld();
+                        reg_fence(x0);
+                        if (c + 32 < rows) tmem_ld32(from + c + 32, x1);
+                        add(x0, c, masked);
+                        if (c + 32 >= rows) break;
+                        tc_wait_ld();
+                        reg_fence(x1);
+                        if (c + 64 < rows) tmem_ld32(from + c + 64, x0);
+                        add(x1, c + 32, masked);
+                    }
+                };
+                if (mixed)
+                    all(std::true_type{});
+                else
+                    all(std::false_type{});
             }
             tc_fence_before();
             __syncwarp();
@@ -543,6 +654,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) score_tiles_kernel(const __gr
 __global__ void __launch_bounds__(kUnitTok) score_join_kernel(const __grid_constant__ ScoreParams p) {
     __shared__ long long sums[kUnitTok / 32], out[2];
     const TaskRun run = task_run<kUnitTok>(p, blockIdx.x, gridDim.x, sums, out);
+    grid_dependency_wait();
     if (run.count == 0) return;
     // the unit of the run's last task
     long long rest = run.rest + run.count - 1;
@@ -551,7 +663,6 @@ __global__ void __launch_bounds__(kUnitTok) score_join_kernel(const __grid_const
     const TaskWalk at(p, b, rest);
     const long long begin = run.from + run.count - 1 - (at.r - at.seq.first(at.u)), end = begin + at.seq.blocks - at.seq.first(at.u);
     if (begin < run.from || end <= run.from + run.count) return;
-    grid_dependency_wait();
     float total = p.partial[((long long)blockIdx.x * 2 + 1) * kUnitTok + threadIdx.x];
     for (long long c = blockIdx.x + 1; c * run.each < end; ++c) total += p.partial[c * 2 * kUnitTok + threadIdx.x];
     const int tok = at.u * kUnitTok + threadIdx.x;
@@ -565,30 +676,57 @@ __global__ void __launch_bounds__(kUnitTok) score_join_kernel(const __grid_const
 
 template <int D, int FMT>
 cudaError_t launch_tiles(ScoreParams p, cudaStream_t stream) {
-    constexpr int bytes = ScoreLayout<D, FMT>::kBytes;
+    using L = ScoreLayout<D, FMT>;
+    constexpr int bytes = L::kBytes, elem = L::kF8 ? 1 : 2;
     static std::atomic<bool> attr_set[kMaxAttrDevices];
     cudaError_t e = ensure_smem_attr(score_tiles_kernel<D, FMT>, bytes, attr_set);
     if (e != cudaSuccess) return e;
+    // a block of rows: the heads of as many queries as fit, or 128 heads of one
+    p.block_tok = p.G <= kBlockRows ? kBlockRows / p.G : 1;
+    p.head_blocks = (p.G + kBlockRows - 1) / kBlockRows;
+    p.box_rows = p.page_size % 64 == 0 ? 64 : (p.page_size % 16 == 0 ? 16 : 1);
     // no more blocks than there can be tasks
-    const long long blocks = ((long long)p.max_q * p.G + kBlockRows - 1) / kBlockRows;
-    const long long most = (long long)p.B * p.Hkv * (((long long)p.max_pages * p.page_size + kUnitTok - 1) / kUnitTok) * blocks;
-    const unsigned grid = (unsigned)(most < p.num_sms ? most : p.num_sms);
+    const long long blocks = ((long long)p.max_q + p.block_tok - 1) / p.block_tok * p.head_blocks;
+    const long long most = (long long)p.B * p.Hkv * (((long long)p.max_pages * p.page_size + kUnitTok - 1) / kUnitTok);
+    const unsigned grid = (unsigned)(most >= p.num_sms || most * blocks >= p.num_sms ? p.num_sms : most * blocks);
+    // memory of the call: partial sums (unless a unit is one task), factors and parts of q
+    const size_t rows = (size_t)p.T * p.Hq;
+    const size_t n_partial = blocks > 1 ? (size_t)grid * 2 * kUnitTok : 0, n_factor = L::kF8 ? (rows + 3) / 4 * 4 : 0;
+    const size_t ws_bytes = (n_partial + n_factor) * sizeof(float) + (L::kF8 ? rows * 2 * D : 0);
     void* ws = nullptr;
-    if (blocks > 1) {  // else a unit is one task
+    uint8_t* parts = nullptr;
+    if (ws_bytes > 0) {
         cudaMemPool_t pool = nullptr;
         if (current_device_pool(&pool) != ATTN_OK) return cudaErrorUnknown;
-        if ((e = cudaMallocFromPoolAsync(&ws, (size_t)grid * 2 * kUnitTok * sizeof(float), pool, stream)) != cudaSuccess) {
+        if ((e = cudaMallocFromPoolAsync(&ws, ws_bytes, pool, stream)) != cudaSuccess) {
             cudaGetLastError();  // (out of memory is no error of the next call)
             return e;
         }
         p.partial = static_cast<float*>(ws);
+        p.factor = p.partial + n_partial;
+        parts = reinterpret_cast<uint8_t*>(p.factor + n_factor);
     }
-    e = launch_kernel(score_tiles_kernel<D, FMT>, dim3(grid), kTileThreads, bytes, stream, {}, p);
-    if (e == cudaSuccess && blocks > 1) {
-        LaunchMode mode;
-        mode.dependent = true;
-        e = launch_kernel(score_join_kernel, dim3(grid), kUnitTok, 0, stream, mode, p);
+    CUtensorMap tmQ, tmK;
+    const uint64_t q_row = (uint64_t)D * 2;  // bytes of a row of q, in bf16 or in its two parts
+    const uint64_t q_dims[3] = {q_row / elem, (uint64_t)p.Hq, (uint64_t)p.T}, q_strides[2] = {q_row, q_row * p.Hq};
+    const uint32_t q_box[3] = {(uint32_t)(L::kBox / elem), (uint32_t)(p.G < kBlockRows ? p.G : kBlockRows), (uint32_t)p.block_tok};
+    int st = encode_tiled_map(&tmQ, L::kF8 ? (const void*)parts : (const void*)p.q, elem, 3, q_dims, q_strides, q_box);
+    if (p.box_rows > 1) {
+        const uint64_t k_dims[2] = {(uint64_t)p.Hkv * D, (uint64_t)p.num_pages * p.page_size}, k_strides[1] = {(uint64_t)p.Hkv * D * elem};
+        const uint32_t k_box[2] = {(uint32_t)(L::kBox / elem), (uint32_t)p.box_rows};
+        if (st == ATTN_OK) st = encode_tiled_map(&tmK, p.k_cache, elem, 2, k_dims, k_strides, k_box);
+    } else {
+        tmK = tmQ;
     }
+    e = st == ATTN_OK ? cudaSuccess : cudaErrorInvalidValue;
+    LaunchMode dependent;
+    dependent.dependent = true;
+    if (L::kF8 && e == cudaSuccess)
+        e = launch_kernel(split_q_kernel<D>, dim3((unsigned)((rows * (D / 8) + 255) / 256)), 256, 0, stream, {}, p.q, parts, p.factor, (long long)rows,
+                          p.scale_log2);
+    if (e == cudaSuccess)
+        e = launch_kernel(score_tiles_kernel<D, FMT>, dim3(grid), kTileThreads, bytes, stream, L::kF8 ? dependent : LaunchMode{}, p, tmQ, tmK);
+    if (e == cudaSuccess && n_partial > 0) e = launch_kernel(score_join_kernel, dim3(grid), kUnitTok, 0, stream, dependent, p);
     if (ws) cudaFreeAsync(ws, stream);
     return e;
 }

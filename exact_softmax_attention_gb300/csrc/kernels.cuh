@@ -130,6 +130,10 @@ cudaError_t launch_attn_decode_fp8(const DecodeParams& p, int d, int fmt, cudaSt
 int current_device_info(int** status, int* num_sms);
 // The library's stream-ordered memory pool on the current device; returns an attn_status_t code.
 int current_device_pool(cudaMemPool_t* pool);
+// Tiled map of a tensor of bf16 (elem 2) or bytes (elem 1): dims, innermost first; strides in bytes of the dims after the first;
+// box of the copies, its first side 128 or 64 bytes with the swizzle of that width; zeros outside. Returns an attn_status_t code.
+int encode_tiled_map(CUtensorMap* map, const void* base, int elem, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box);
 // Device waits give up after this time (option "watchdog_ms").
 unsigned long long watchdog_ns();
 

@@ -173,6 +173,10 @@ MANY = [
     ([700, 40], [700, 1000], 8, 1, 64, 16, False),        # units split between the blocks
     ([1500], [1800], 8, 1, 128, 5, True),
     ([1000], [1000], 1, 1, 128, 256, True),
+    ([40, 300], [300, 300], 200, 1, 64, 16, False),       # more heads of a kv head than a block of rows
+    ([9, 50], [300, 260], 100, 1, 128, 16, False),        # one query per block
+    ([400, 7], [600, 90], 10, 2, 64, 32, False),          # 25 queries per block
+    ([600], [1100], 21, 3, 128, 128, True),
     ([20] * 500, [20 + i % 7 for i in range(500)], 1, 1, 64, 16, True),  # more sequences than a block's threads
 ]
 
