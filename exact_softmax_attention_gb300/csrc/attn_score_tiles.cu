@@ -12,10 +12,11 @@
 // exponentials, 1024 clocks of the MUFU; rows that stay the same (up to 128) against new tokens every task are 64 KB of bf16
 // keys for that, more than the memory delivers in the time.
 //
-// Roles of the warps: 0-3 and 4-7 exponentials and sums, a group per accumulator tile (two buffers each, so that the
-// products of a task run during the exponentials of the one before); 8 and 9 the keys of a tile each, through tensor copies of 64 or
-// 16 rows where the page size is a multiple of that, else by 16-byte copies of rows that the page table gives; 10 the blocks of q
-// through tensor copies (one box is the heads of as many queries as fit) and their LSE; 12 the products, issued by one thread.
+// Roles of the warps: 0-15 exponentials and sums, for each accumulator tile two groups of four warps that take half of the columns
+// each (two buffers per tile, so that the products of a task run during the exponentials of the one before); 16 and 17 the keys of a tile
+// each, through tensor copies of 64 or 16 rows where the page size is a multiple of that, else by 16-byte copies of rows that the page
+// table gives; 18 the blocks of q through tensor copies (one box is the heads of as many queries as fit) and their LSE; 19 and 20 the
+// products of a tile each, issued by one thread: while one waits for its buffer, the other one's products run.
 //
 // 8-bit caches: K is multiplied as it is (kind::f8f6f4). A kernel before this one scales each row of q by a power of two and splits
 // it into two e4m3 parts: exact unless an element is more than 2^9 below the row's largest (then off by at most 2^-17 of that).
@@ -26,10 +27,11 @@ namespace {
 
 constexpr int kTileTok = 128, kUnitTok = 2 * kTileTok;  // tokens of an accumulator tile, of a unit
 constexpr int kBlockRows = 128;                         // rows of a task
-constexpr int kLseStages = 4;
-constexpr int kTileThreads = 13 * 32;
+constexpr int kTileThreads = 21 * 32;
+constexpr int kSumWarps = 16, kKeyWarp = 16, kQueryWarp = 18, kProductWarp = 19;
 
-template <int D, int FMT>
+// LONG: many blocks of rows against the same keys; else many keys against the same rows.
+template <int D, int FMT, bool LONG>
 struct ScoreLayout {
     static constexpr bool kF8 = FMT != ATTN_KV_BF16;
     static constexpr int kRow = kF8 ? D : 2 * D;             // bytes of a key
@@ -40,17 +42,21 @@ struct ScoreLayout {
     static constexpr int kQChunks = kF8 ? 2 : kChunks;       // of a block of q: its columns, or its two 8-bit parts
     static constexpr int kQ = kQChunks * kChunk;
     static constexpr int kK = 2 * kTile;                     // keys of a unit
-    static constexpr int kKStages = kK > 32768 ? 2 : 4;
-    static constexpr int kKOff = 0, kQOff = kKStages * kK;   // (q: two stages)
+    // What streams has the stages: 128 KB (64 KB with narrow 8-bit heads) on their way per SM.
+    static constexpr int kKStages = LONG ? (kK > 32768 ? 1 : 2) : (kK > 32768 ? 2 : 4);
+    static constexpr int kQStages = LONG ? 4 : 2, kLseStages = kQStages + 2;
+    static constexpr int kKOff = 0, kQOff = kKStages * kK;
     // per row of a block of q: minus the LSE (times log2 e), factor of the scores, last token seen
-    static constexpr int kLseOff = kQOff + 2 * kQ, kLseStage = 3 * kBlockRows * 4;
+    static constexpr int kLseOff = kQOff + kQStages * kQ, kLseStage = 3 * kBlockRows * 4;
     static constexpr int kBarOff = kLseOff + kLseStages * kLseStage;
-    static constexpr int bK = 0, bKFree = bK + kKStages, bQ = bKFree + kKStages, bQFree = bQ + 2, bL = bQFree + 2, bLFree = bL + kLseStages;
-    static constexpr int bS = bLFree + kLseStages, bSFree = bS + 4, bDrain = bSFree + 4, kBars = bDrain + 1;
+    static constexpr int bK = 0, bKFree = bK + kKStages, bQ = bKFree + kKStages, bQFree = bQ + kQStages, bL = bQFree + kQStages, bLFree = bL + kLseStages;
+    static constexpr int bS = bLFree + kLseStages, bSFree = bS + 4, bHalf = bSFree + 4, bHalfFree = bHalf + 4;
+    static constexpr int bDrain = bHalfFree + 4, kBars = bDrain + 2;
     // tensor-memory base, abort flag; per lse stage: do rows need their own limits; the plan
     static constexpr int kMiscOff = kBarOff + kBars * 8, kOddOff = kMiscOff + 8, kPlanOff = kOddOff + kLseStages * 4;
-    static constexpr int kBytes = kPlanOff + 16;
-    static_assert(kBarOff % 8 == 0 && kPlanOff % 8 == 0 && kBytes <= 232448, "shared memory of an SM");
+    static constexpr int kHalfOff = kPlanOff + 16;  // sums over the upper columns, of two units in turn
+    static constexpr int kBytes = kHalfOff + 2 * kUnitTok * 4;
+    static_assert(kBarOff % 8 == 0 && kPlanOff % 8 == 0 && kLseStages % 2 == 0 && kBytes <= 232448, "shared memory of an SM");
 };
 
 __device__ __forceinline__ void fence_smem_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -176,12 +182,15 @@ struct SeqTasks {
     }
 };
 
-// Where a task lies: sequence, kv head, unit, block of rows.
-struct TaskWalk {
-    int b, h, u, r;
+// The units of a run in turn, each with the blocks [r, end) of its rows that the run holds.
+struct UnitWalk {
+    int b, h, u, r, end;
+    int left;        // tasks of the run behind this unit
+    long long from;  // each u - skip
+    bool whole;      // the run holds the first of the unit's tasks
     ScoreSeq s;
     SeqTasks seq;
-    __device__ __forceinline__ TaskWalk(const ScoreParams& p, int b_, long long rest) : b(b_), s(), seq(s, 1, 1) {
+    __device__ __forceinline__ UnitWalk(const ScoreParams& p, int b_, long long rest, int count) : b(b_), s(), seq(s, 1, 1) {
         score_seq(p, b, s);
         seq = SeqTasks(s, p.block_tok, p.head_blocks);
         const long long each = seq.before(seq.units);
@@ -196,32 +205,47 @@ struct TaskWalk {
                 hi = mid - 1;
         }
         u = lo;
-        r = seq.first(u) + (int)(rest - seq.before(u));
+        const int behind = (int)(rest - seq.before(u));
+        r = seq.first(u) + behind;
+        whole = behind == 0;
+        from = (long long)seq.each * u - seq.skip;
+        left = count;
+        cut();
     }
-    __device__ __forceinline__ bool last_block() const { return r + 1 == seq.blocks; }
-    // first query of the block, its rows that there are
-    __device__ __forceinline__ int query(const ScoreParams& p) const { return p.head_blocks > 1 ? r / p.head_blocks : r * p.block_tok; }
-    __device__ __forceinline__ int rows(const ScoreParams& p) const {
-        if (p.head_blocks > 1) return min(kBlockRows, p.G - r % p.head_blocks * kBlockRows);
-        return min(p.block_tok, s.n - r * p.block_tok) * p.G;
+    __device__ __forceinline__ void cut() {
+        end = min(seq.blocks, r + left);
+        left -= end - r;
     }
-    // The next task (there is one). Returns whether the unit changes; q_changes: whether the block of q does.
-    __device__ __forceinline__ bool next(const ScoreParams& p, bool& q_changes) {
-        const int r0 = r;
-        q_changes = true;
-        if (++r < seq.blocks) return false;
+    __device__ __forceinline__ bool complete() const { return end == seq.blocks; }
+    // On to the next unit (left > 0). Returns whether its first block of q is another one than the last one of this.
+    __device__ __forceinline__ bool next(const ScoreParams& p) {
+        const int last = end - 1;
+        whole = true;
         if (++u < seq.units) {
-            r = seq.first(u);
-            q_changes = r != r0;
-            return true;
+            from += seq.each;
+            r = from > 0 ? (int)from : 0;
+            cut();
+            return r != last;
         }
         u = r = 0;
-        if (++h < p.Hkv) return true;
-        h = 0;
-        do ++b;
-        while (!score_seq(p, b, s));
-        seq = SeqTasks(s, p.block_tok, p.head_blocks);
+        if (++h >= p.Hkv) {
+            h = 0;
+            do ++b;
+            while (!score_seq(p, b, s));
+            seq = SeqTasks(s, p.block_tok, p.head_blocks);
+        }
+        from = -seq.skip;
+        cut();
         return true;
+    }
+    // first query of a block, its first head, its rows
+    __device__ __forceinline__ int query(const ScoreParams& p, int block) const {
+        return p.head_blocks > 1 ? block / p.head_blocks : block * p.block_tok;
+    }
+    __device__ __forceinline__ int head(const ScoreParams& p, int block) const { return p.head_blocks > 1 ? block % p.head_blocks * kBlockRows : 0; }
+    __device__ __forceinline__ int rows(const ScoreParams& p, int block) const {
+        if (p.head_blocks > 1) return min(kBlockRows, p.G - head(p, block));
+        return min(p.block_tok, s.n - block * p.block_tok) * p.G;
     }
 };
 
@@ -279,11 +303,11 @@ __device__ __forceinline__ TaskRun task_run(const ScoreParams& p, int block, int
     return run;
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool LONG>
 __global__ void __launch_bounds__(kTileThreads, 1)
     score_tiles_kernel(const __grid_constant__ ScoreParams p, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK) {
     grid_dependents_launch();
-    using L = ScoreLayout<D, FMT>;
+    using L = ScoreLayout<D, FMT, LONG>;
     constexpr bool F8 = L::kF8;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -301,30 +325,33 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::kKStages; ++i) {
             mbar_init(&bars[L::bK + i], 2);
-            mbar_init(&bars[L::bKFree + i], 1);
+            mbar_init(&bars[L::bKFree + i], 2);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < L::kQStages; ++i) {
             mbar_init(&bars[L::bQ + i], 1);
-            mbar_init(&bars[L::bQFree + i], 1);
+            mbar_init(&bars[L::bQFree + i], 2);
         }
-        for (int i = 0; i < kLseStages; ++i) {
+        for (int i = 0; i < L::kLseStages; ++i) {
             mbar_init(&bars[L::bL + i], 1);
-            mbar_init(&bars[L::bLFree + i], 8);
+            mbar_init(&bars[L::bLFree + i], kSumWarps);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bars[L::bS + i], 1);
-            mbar_init(&bars[L::bSFree + i], 4);
+            mbar_init(&bars[L::bHalf + i], 4);
+            mbar_init(&bars[L::bHalfFree + i], 4);
+            mbar_init(&bars[L::bSFree + i], kSumWarps / 2);
         }
         mbar_init(&bars[L::bDrain], 1);
+        mbar_init(&bars[L::bDrain + 1], 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmQ);
         if (p.box_rows > 1) tma_prefetch_desc(&tmK);
     }
     // rows that no copy of q writes are zeros
-    for (int i = threadIdx.x; i < 2 * L::kQ / 16; i += kTileThreads) reinterpret_cast<uint4*>(smem + L::kQOff)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < L::kQStages * L::kQ / 16; i += kTileThreads) reinterpret_cast<uint4*>(smem + L::kQOff)[i] = make_uint4(0, 0, 0, 0);
     fence_smem_to_async();
-    if (warp == 12) {
+    if (warp == kProductWarp) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -333,12 +360,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t base = smem_u32(smem);
-    TaskWalk at(p, run.b, run.rest);
+    UnitWalk at(p, run.b, run.rest, run.count);
 
-    if (warp == 8 || warp == 9) {
-        // ---------------------------------------------------------------- keys of tile warp - 8
-        const int tile = warp - 8;
-        bool ok = true, ignored;
+    if (warp == kKeyWarp || warp == kKeyWarp + 1) {
+        // ---------------------------------------------------------------- keys of a tile
+        const int tile = warp - kKeyWarp;
+        bool ok = true;
         int unit = 0;
         const CUtensorMap* map = &tmK;
         const int none = p.num_pages * p.page_size;  // the first row past the cache: zeros
@@ -350,7 +377,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (lane == 0) mbar_arrive(pending);
             pending = nullptr;
         };
-        for (int i = 0;;) {
+        for (;;) {
             const int st = unit % L::kKStages;
             const uint32_t parity = (uint32_t)(unit / L::kKStages & 1) ^ 1u;
             const int t0 = at.u * kUnitTok + tile * kTileTok;
@@ -404,11 +431,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 pending = full;
             }
             ++unit;
-            // on to the next unit
-            bool more = false;
-            while (++i < run.count && !(more = at.next(p, ignored))) {
-            }
-            if (!more) break;
+            if (at.left == 0) break;
+            at.next(p);
         }
         cp_async_wait<0>();
         hand_over();
@@ -418,12 +442,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int x = unit > L::kKStages ? unit - L::kKStages : 0; x < unit; ++x)
                 mbar_wait(&bars[L::bK + x % L::kKStages], (uint32_t)(x / L::kKStages & 1), &dummy, 20000000ull);
         }
-    } else if (warp == 10) {
+    } else if (warp == kQueryWarp) {
         // ---------------------------------------------------------------- blocks of q and their LSE
         if (F8) grid_dependency_wait();  // the parts of q
         const bool by_head = p.head_blocks > 1;
-        const int box_heads = by_head ? kBlockRows : p.G;
-        const uint32_t bytes = (uint32_t)(box_heads * p.block_tok * L::kBox * L::kQChunks);
+        const uint32_t bytes = (uint32_t)((by_head ? kBlockRows : p.G) * p.block_tok * L::kBox * L::kQChunks);
         int query[4], head[4];  // of rows lane, lane + 32, ... of a block
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -431,87 +454,80 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             query[e] = by_head ? 0 : r / p.G;
             head[e] = by_head ? r : r - query[e] * p.G;
         }
-        bool ok = true, new_q = true;
+        bool ok = true, fresh = true;
         int qn = 0;
-        for (int i = 0;;) {
-            const int st = qn & 1, ls = qn % kLseStages;
-            const int i0 = at.query(p), h0 = by_head ? at.r % p.head_blocks * kBlockRows : 0;  // first query, first of the kv head's heads
-            float l[4];
+        while (ok) {
+            for (int r = fresh ? at.r : at.r + 1; r < at.end; ++r) {
+                const int st = qn % L::kQStages, ls = qn % L::kLseStages;
+                const int i0 = at.query(p, r), h0 = at.head(p, r);
+                float l[4], f[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool there = query[e] < p.block_tok && i0 + query[e] < at.s.n && h0 + head[e] < p.G;
-                const long long row = (long long)(at.s.q0 + i0 + query[e]) * p.Hq + at.h * p.G + h0 + head[e];
-                l[e] = there ? __ldg(p.lse + row) : -INFINITY;
-            }
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::bQFree + st], (uint32_t)(qn >> 1 & 1) ^ 1u, abort_flag, wd)))) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bars[L::bQ + st], bytes);
+                for (int e = 0; e < 4; ++e) {
+                    const bool there = query[e] < p.block_tok && i0 + query[e] < at.s.n && h0 + head[e] < p.G;
+                    const long long row = (long long)(at.s.q0 + i0 + query[e]) * p.Hq + at.h * p.G + h0 + head[e];
+                    l[e] = there ? __ldg(p.lse + row) : -INFINITY;
+                    f[e] = F8 && there ? __ldg(p.factor + row) : 0.0f;
+                }
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::bQFree + st], (uint32_t)(qn / L::kQStages & 1) ^ 1u, abort_flag, wd)))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars[L::bQ + st], bytes);
 #pragma unroll
-                for (int c = 0; c < L::kQChunks; ++c)
-                    tma_load_3d(smem + L::kQOff + st * L::kQ + c * L::kChunk, &tmQ, &bars[L::bQ + st], c * (L::kBox / (F8 ? 1 : 2)), at.h * p.G + h0,
-                                at.s.q0 + i0);
-            }
-            __syncwarp();
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::bLFree + ls], (uint32_t)(qn / kLseStages & 1) ^ 1u, abort_flag, wd)))) {
+                    for (int c = 0; c < L::kQChunks; ++c)
+                        tma_load_3d(smem + L::kQOff + st * L::kQ + c * L::kChunk, &tmQ, &bars[L::bQ + st], c * (L::kBox / (F8 ? 1 : 2)),
+                                    at.h * p.G + h0, at.s.q0 + i0);
+                }
+                __syncwarp();
                 ++qn;
-                break;
-            }
-            float* lse2 = reinterpret_cast<float*>(smem + L::kLseOff + ls * L::kLseStage);
-            bool odd = false;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::bLFree + ls], (uint32_t)((qn - 1) / L::kLseStages & 1) ^ 1u, abort_flag, wd)))) break;
+                float* lse2 = reinterpret_cast<float*>(smem + L::kLseOff + ls * L::kLseStage);
+                bool odd = false;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = lane + 32 * e;
-                // rows behind the box are zeros and get weight 0; others that are not there, or saw nothing, are masked
-                const bool none = l[e] == -INFINITY, behind = query[e] >= p.block_tok;
-                odd = odd || (none && !behind);
-                lse2[r] = none ? (behind ? -INFINITY : 0.0f) : l[e] * -1.4426950408889634f;
-                reinterpret_cast<int*>(lse2)[2 * kBlockRows + r] = none ? (behind ? INT32_MAX : -1) : at.s.ctx + i0 + query[e];
-                if (F8)
-                    lse2[kBlockRows + r] = none ? 0.0f
-                                                : __ldg(p.factor + (long long)(at.s.q0 + i0 + query[e]) * p.Hq + at.h * p.G + h0 + head[e]);
+                for (int e = 0; e < 4; ++e) {
+                    const int x = lane + 32 * e;
+                    // rows behind the box are zeros and get weight 0; others that are not there, or saw nothing, are masked
+                    const bool none = l[e] == -INFINITY, behind = query[e] >= p.block_tok;
+                    odd = odd || (none && !behind);
+                    lse2[x] = none ? (behind ? -INFINITY : 0.0f) : l[e] * -1.4426950408889634f;
+                    if (F8) lse2[kBlockRows + x] = none ? 0.0f : f[e];
+                    reinterpret_cast<int*>(lse2)[2 * kBlockRows + x] = none ? (behind ? INT32_MAX : -1) : at.s.ctx + i0 + query[e];
+                }
+                odd = __any_sync(0xffffffffu, odd);
+                if (lane == 0) odd_rows[ls] = odd;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[L::bL + ls]);
             }
-            odd = __any_sync(0xffffffffu, odd);
-            if (lane == 0) odd_rows[ls] = odd;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[L::bL + ls]);
-            ++qn;
-            new_q = false;
-            while (++i < run.count) {
-                at.next(p, new_q);
-                if (new_q) break;
-            }
-            if (i >= run.count) break;
+            if (at.left == 0) break;
+            fresh = at.next(p);
         }
         if (!ok) {
             int dummy = 0;
-            for (int x = qn > 2 ? qn - 2 : 0; x < qn; ++x) mbar_wait(&bars[L::bQ + (x & 1)], (uint32_t)(x >> 1 & 1), &dummy, 20000000ull);
+            for (int x = qn > L::kQStages ? qn - L::kQStages : 0; x < qn; ++x)
+                mbar_wait(&bars[L::bQ + x % L::kQStages], (uint32_t)(x / L::kQStages & 1), &dummy, 20000000ull);
         }
-    } else if (warp == 12) {
-        // ---------------------------------------------------------------- products
+    } else if (warp >= kProductWarp) {
+        // ---------------------------------------------------------------- products of tile t
         if (lane == 0) {
+            const int t = warp - kProductWarp;
             auto desc = [&](int off) { return L::kBox == 64 ? smem_desc_sw64(base + off) : smem_desc_sw128(base + off, L::kChunk, 1024); };
             const uint64_t dk = desc(L::kKOff), dq = desc(L::kQOff);
             auto wait = [&](int bar, uint32_t parity) { return mbar_wait(&bars[bar], parity, abort_flag, wd); };
-            bool any = false, new_unit = true, new_q = true;
-            int units = 0, qs = 0;  // stages waited for
-            for (int i = 0;; ++i) {
-                if (new_unit) {
-                    if (!wait(L::bK + units % L::kKStages, units / L::kKStages & 1)) break;
-                    ++units;
-                }
-                if (new_q) {
-                    if (!wait(L::bQ + (qs & 1), qs >> 1 & 1)) break;
-                    ++qs;
-                }
-                const int ks = (units - 1) % L::kKStages, st = (qs - 1) & 1, buf = i & 1;
-                const uint32_t idesc = score_idesc<FMT>((at.rows(p) + 31) & ~31);
-                bool go = true;
-#pragma unroll 1
-                for (int t = 0; t < 2 && (go = wait(L::bSFree + 2 * t + buf, (unsigned)(i >> 1 & 1) ^ 1u)); ++t) {
+            bool any = false, go = true, fresh = true;
+            int units = 0, qs = 0, i = 0;  // stages waited for, tasks
+            while (go && (go = wait(L::bK + units % L::kKStages, units / L::kKStages & 1))) {
+                const int ks = units++ % L::kKStages;
+                for (int r = at.r; r < at.end; ++r, ++i) {
+                    if (fresh) {
+                        if (!(go = wait(L::bQ + qs % L::kQStages, qs / L::kQStages & 1))) break;
+                        ++qs;
+                    }
+                    const int st = (qs - 1) % L::kQStages, buf = i & 1;
+                    const uint64_t qd = dq + (uint64_t)((st * L::kQ) >> 4);
+                    const uint32_t idesc = score_idesc<FMT>((at.rows(p, r) + 31) & ~31);
+                    if (!(go = wait(L::bSFree + 2 * t + buf, (unsigned)(i >> 1 & 1) ^ 1u))) break;
                     tc_fence_after();
                     any = true;
                     const uint32_t d = tmem + (uint32_t)(2 * t + buf) * 128;
-                    const uint64_t kd = dk + (uint64_t)((ks * L::kK + t * L::kTile) >> 4), qd = dq + (uint64_t)((st * L::kQ) >> 4);
+                    const uint64_t kd = dk + (uint64_t)((ks * L::kK + t * L::kTile) >> 4);
                     if constexpr (F8) {
 #pragma unroll
                         for (int x = 0; x < 2 * (D / 32); ++x) {  // both parts of q
@@ -525,99 +541,120 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                       qd + (uint64_t)(((k >> 2) * L::kChunk + (k & 3) * 32) >> 4), idesc, k > 0);
                     }
                     tc_commit(&bars[L::bS + 2 * t + buf]);
+                    fresh = true;
+                    if (r + 1 < at.end) tc_commit(&bars[L::bQFree + st]);
                 }
-                if (!go) break;
-                if (i + 1 == run.count) break;
-                new_unit = at.next(p, new_q);
-                if (new_q) tc_commit(&bars[L::bQFree + st]);
-                if (new_unit) tc_commit(&bars[L::bKFree + ks]);
+                if (!go || at.left == 0) break;
+                fresh = at.next(p);
+                if (fresh) tc_commit(&bars[L::bQFree + (qs - 1) % L::kQStages]);
+                tc_commit(&bars[L::bKFree + ks]);
             }
             if (any) {
                 // every product has completed before the tensor memory is released
-                tc_commit(&bars[L::bDrain]);
+                tc_commit(&bars[L::bDrain + t]);
                 int dummy = 0;
-                mbar_wait(&bars[L::bDrain], 0, &dummy, 50000000ull);
+                mbar_wait(&bars[L::bDrain + t], 0, &dummy, 50000000ull);
             }
         }
         __syncwarp();
-    } else if (warp < 8) {
+    } else if (warp < kSumWarps) {
         // ---------------------------------------------------------------- exponentials and sums
-        const int tile = warp >> 2, quarter = warp & 3, mine = tile * kTileTok + quarter * 32 + lane;
-        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        bool new_unit = true, new_q = true, whole = at.r == at.seq.first(at.u);
-        int piece = whole ? 1 : 0;  // place of a partial sum: 0 for the unit that an earlier run began, 1 for the last one
-        int qs = 0;
-        float total = 0.0f;
-        for (int i = 0;; ++i) {
-            if (new_unit) total = 0.0f;
-            if (new_q) ++qs;
-            const int ls = (qs - 1) % kLseStages, buf = i & 1;
-            const int rows = at.rows(p), i0 = at.query(p);
-            const int tok = at.u * kUnitTok + mine, first = at.u * kUnitTok + tile * kTileTok;
-            // (not the barrier of q: its stage may have been filled twice since)
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars[L::bL + ls], (uint32_t)((qs - 1) / kLseStages & 1), abort_flag, wd))) break;
-            const float* lse2 = reinterpret_cast<const float*>(smem + L::kLseOff + ls * L::kLseStage);
-            const float* factor = lse2 + kBlockRows;
-            const int* last = reinterpret_cast<const int*>(lse2 + 2 * kBlockRows);
-            // the first row sees the fewest tokens, the last one the most
-            const int top = at.s.ctx + min(i0 + p.block_tok, at.s.n) - 1;
-            const bool mixed = odd_rows[ls] != 0 || at.s.ctx + i0 < first + kTileTok - 1;
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars[L::bS + 2 * tile + buf], (unsigned)(i >> 1 & 1), abort_flag, wd))) break;
-            tc_fence_after();
-            const uint32_t from = tmem + lane_off + (uint32_t)(2 * tile + buf) * 128;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            auto add = [&](const uint32_t (&x)[32], int c, auto masked) {
+        const int tile = warp >> 3, half = warp >> 2 & 1, quarter = warp & 3, mine = tile * kTileTok + quarter * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(256 * tile + 64 * half);
+        float* halves = reinterpret_cast<float*>(smem + L::kHalfOff);
+        bool go = true, fresh = true;
+        int qs = 0, i = 0, units = 0;
+        int piece = at.whole ? 1 : 0;  // place of a partial sum: 0 for the unit that an earlier run began, 1 for the last one
+        while (go) {
+            const int first = at.u * kUnitTok + tile * kTileTok, tok = at.u * kUnitTok + mine;
+            float total = 0.0f;
+            for (int r = at.r; r < at.end; ++r, ++i) {
+                if (fresh) ++qs;
+                const int ls = (qs - 1) % L::kLseStages, buf = i & 1;
+                const int i0 = at.query(p, r), columns = at.rows(p, r) - 64 * half;
+                // (not the barrier of q: its stage may have been filled twice since)
+                if (!(go = __all_sync(0xffffffffu, mbar_wait(&bars[L::bL + ls], (uint32_t)((qs - 1) / L::kLseStages & 1), abort_flag, wd)))) break;
+                const float* lse2 = reinterpret_cast<const float*>(smem + L::kLseOff + ls * L::kLseStage) + 64 * half;
+                const float* factor = lse2 + kBlockRows;
+                const int* last = reinterpret_cast<const int*>(lse2 + 2 * kBlockRows);
+                // the first row sees the fewest tokens, the last one the most
+                const int top = at.s.ctx + min(i0 + p.block_tok, at.s.n) - 1;
+                const bool mixed = odd_rows[ls] != 0 || at.s.ctx + i0 < first + kTileTok - 1;
+                if (!(go = __all_sync(0xffffffffu, mbar_wait(&bars[L::bS + 2 * tile + buf], (unsigned)(i >> 1 & 1), abort_flag, wd)))) break;
+                tc_fence_after();
+                const uint32_t from = lanes + (uint32_t)buf * 128;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                auto add = [&](const uint32_t (&x)[32], int c, auto masked) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 l = *reinterpret_cast<const float4*>(lse2 + c + e);
-                    float4 f = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
-                    if constexpr (F8) f = *reinterpret_cast<const float4*>(factor + c + e);
-                    float y[4];
-                    ffma2(y[0], y[1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]), f.x, f.y, l.x, l.y);
-                    ffma2(y[2], y[3], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]), f.z, f.w, l.z, l.w);
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 l = *reinterpret_cast<const float4*>(lse2 + c + e);
+                        float4 f = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+                        if constexpr (F8) f = *reinterpret_cast<const float4*>(factor + c + e);
+                        float y[4];
+                        ffma2(y[0], y[1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]), f.x, f.y, l.x, l.y);
+                        ffma2(y[2], y[3], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]), f.z, f.w, l.z, l.w);
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) y[z] = ex2_mufu(y[z]);
-                    if constexpr (decltype(masked)::value) {
-                        const int4 m = *reinterpret_cast<const int4*>(last + c + e);
-                        y[0] = tok <= m.x ? y[0] : 0.0f;
-                        y[1] = tok <= m.y ? y[1] : 0.0f;
-                        y[2] = tok <= m.z ? y[2] : 0.0f;
-                        y[3] = tok <= m.w ? y[3] : 0.0f;
-                    }
-                    fadd2(sum[0], sum[1], sum[0], sum[1], y[0], y[1]);
-                    fadd2(sum[2], sum[3], sum[2], sum[3], y[2], y[3]);
-                }
-            };
-            if (first <= top && first < at.s.len) {
-                // the next columns are on their way while these are added
-                uint32_t x0[32], x1[32];
-                auto all = [&](auto masked) {
-                    tmem_ld32(from, x0);
-#pragma unroll 1
-                    for (int c = 0; c < rows; c += 64) {
-                        tc_wait_ld();
-                        reg_fence(x0);
-                        if (c + 32 < rows) tmem_ld32(from + c + 32, x1);
-                        add(x0, c, masked);
-                        if (c + 32 >= rows) break;
-                        tc_wait_ld();
-                        reg_fence(x1);
-                        if (c + 64 < rows) tmem_ld32(from + c + 64, x0);
-                        add(x1, c + 32, masked);
+                        for (int z = 0; z < 4; ++z) y[z] = ex2_mufu(y[z]);
+                        if constexpr (decltype(masked)::value) {
+                            const int4 m = *reinterpret_cast<const int4*>(last + c + e);
+                            y[0] = tok <= m.x ? y[0] : 0.0f;
+                            y[1] = tok <= m.y ? y[1] : 0.0f;
+                            y[2] = tok <= m.z ? y[2] : 0.0f;
+                            y[3] = tok <= m.w ? y[3] : 0.0f;
+                        }
+                        fadd2(sum[0], sum[1], sum[0], sum[1], y[0], y[1]);
+                        fadd2(sum[2], sum[3], sum[2], sum[3], y[2], y[3]);
                     }
                 };
-                if (mixed)
-                    all(std::true_type{});
-                else
-                    all(std::false_type{});
+                auto columns_of = [&](auto masked) {
+                    uint32_t x[32];
+                    tmem_ld32(from, x);
+                    tc_wait_ld();
+                    reg_fence(x);
+                    if (columns > 32) {
+                        add(x, 0, masked);
+                        tmem_ld32(from + 32, x);
+                        tc_wait_ld();
+                        reg_fence(x);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[L::bSFree + 2 * tile + buf]);  // (the next products need not wait for the last exponentials)
+                    add(x, columns > 32 ? 32 : 0, masked);
+                };
+                if (first <= top && first < at.s.len && columns > 0) {
+                    if (mixed)
+                        columns_of(std::true_type{});
+                    else
+                        columns_of(std::false_type{});
+                } else {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[L::bSFree + 2 * tile + buf]);
+                }
+                total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                fresh = true;
+                if (r + 1 < at.end) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[L::bLFree + ls]);
+                }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[L::bSFree + 2 * tile + buf]);
-            total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            const bool end = i + 1 == run.count, complete = at.last_block();
-            if (complete || end) {
-                if (complete && whole) {
+            if (!go) break;
+            // the sums over the upper columns to the warps of the lower ones, in two places in turn
+            float* other = halves + (units & 1) * kUnitTok + mine;
+            const int pair = 2 * tile + (units & 1);
+            const uint32_t turn = (uint32_t)(units >> 1 & 1);
+            if (half) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars[L::bHalfFree + pair], turn ^ 1u, abort_flag, wd))) break;
+                *other = total;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[L::bHalf + pair]);
+            } else {
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars[L::bHalf + pair], turn, abort_flag, wd))) break;
+                total += *other;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[L::bHalfFree + pair]);
+                if (at.complete() && at.whole) {
                     int slot;
                     if (tok < at.s.len) {
                         const int page = score_place(p, p.page_table + (long long)at.b * p.max_pages, tok, slot);
@@ -629,14 +666,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 } else {
                     p.partial[((long long)blockIdx.x * 2 + piece) * kUnitTok + mine] = total;
                 }
-                whole = true;
-                piece = 1;
             }
-            if (end) break;
-            new_unit = at.next(p, new_q);
-            if (new_q) {
+            piece = 1;
+            ++units;
+            if (at.left == 0) break;
+            fresh = at.next(p);
+            if (fresh) {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[L::bLFree + ls]);
+                if (lane == 0) mbar_arrive(&bars[L::bLFree + (qs - 1) % L::kLseStages]);
             }
         }
     }
@@ -646,7 +683,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc_fence_before();
     named_bar_sync(1, kTileThreads);
     tc_fence_after();
-    if (warp == 12) tmem_dealloc(tmem, 512);
+    if (warp == kProductWarp) tmem_dealloc(tmem, 512);
     if (threadIdx.x == 0 && *abort_flag) atomicCAS(p.status, 0, kDevTimeout);
 }
 
@@ -660,7 +697,7 @@ __global__ void __launch_bounds__(kUnitTok) score_join_kernel(const __grid_const
     long long rest = run.rest + run.count - 1;
     int b = run.b;
     for (long long n; rest >= (n = tasks_of(p, b)); ++b) rest -= n;
-    const TaskWalk at(p, b, rest);
+    const UnitWalk at(p, b, rest, 1);
     const long long begin = run.from + run.count - 1 - (at.r - at.seq.first(at.u)), end = begin + at.seq.blocks - at.seq.first(at.u);
     if (begin < run.from || end <= run.from + run.count) return;
     float total = p.partial[((long long)blockIdx.x * 2 + 1) * kUnitTok + threadIdx.x];
@@ -674,16 +711,13 @@ __global__ void __launch_bounds__(kUnitTok) score_join_kernel(const __grid_const
     *to = p.decay != 0.0f && tok < at.s.ctx ? fmaf(p.decay, *to, total) : total;
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool LONG>
 cudaError_t launch_tiles(ScoreParams p, cudaStream_t stream) {
-    using L = ScoreLayout<D, FMT>;
+    using L = ScoreLayout<D, FMT, LONG>;
     constexpr int bytes = L::kBytes, elem = L::kF8 ? 1 : 2;
     static std::atomic<bool> attr_set[kMaxAttrDevices];
-    cudaError_t e = ensure_smem_attr(score_tiles_kernel<D, FMT>, bytes, attr_set);
+    cudaError_t e = ensure_smem_attr(score_tiles_kernel<D, FMT, LONG>, bytes, attr_set);
     if (e != cudaSuccess) return e;
-    // a block of rows: the heads of as many queries as fit, or 128 heads of one
-    p.block_tok = p.G <= kBlockRows ? kBlockRows / p.G : 1;
-    p.head_blocks = (p.G + kBlockRows - 1) / kBlockRows;
     p.box_rows = p.page_size % 64 == 0 ? 64 : (p.page_size % 16 == 0 ? 16 : 1);
     // no more blocks than there can be tasks
     const long long blocks = ((long long)p.max_q + p.block_tok - 1) / p.block_tok * p.head_blocks;
@@ -725,22 +759,31 @@ cudaError_t launch_tiles(ScoreParams p, cudaStream_t stream) {
         e = launch_kernel(split_q_kernel<D>, dim3((unsigned)((rows * (D / 8) + 255) / 256)), 256, 0, stream, {}, p.q, parts, p.factor, (long long)rows,
                           p.scale_log2);
     if (e == cudaSuccess)
-        e = launch_kernel(score_tiles_kernel<D, FMT>, dim3(grid), kTileThreads, bytes, stream, L::kF8 ? dependent : LaunchMode{}, p, tmQ, tmK);
+        e = launch_kernel(score_tiles_kernel<D, FMT, LONG>, dim3(grid), kTileThreads, bytes, stream, L::kF8 ? dependent : LaunchMode{}, p, tmQ, tmK);
     if (e == cudaSuccess && n_partial > 0) e = launch_kernel(score_join_kernel, dim3(grid), kUnitTok, 0, stream, dependent, p);
     if (ws) cudaFreeAsync(ws, stream);
     return e;
 }
 
+template <int D, int FMT>
+cudaError_t launch_rows(const ScoreParams& p, cudaStream_t stream) {
+    return p.max_q > p.block_tok || p.head_blocks > 1 ? launch_tiles<D, FMT, true>(p, stream) : launch_tiles<D, FMT, false>(p, stream);
+}
+
 template <int D>
 cudaError_t launch_fmt(const ScoreParams& p, int fmt, cudaStream_t stream) {
-    return fmt == ATTN_FP8_E4M3   ? launch_tiles<D, ATTN_FP8_E4M3>(p, stream)
-           : fmt == ATTN_FP8_E5M2 ? launch_tiles<D, ATTN_FP8_E5M2>(p, stream)
-                                  : launch_tiles<D, ATTN_KV_BF16>(p, stream);
+    return fmt == ATTN_FP8_E4M3   ? launch_rows<D, ATTN_FP8_E4M3>(p, stream)
+           : fmt == ATTN_FP8_E5M2 ? launch_rows<D, ATTN_FP8_E5M2>(p, stream)
+                                  : launch_rows<D, ATTN_KV_BF16>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_score_tiles(const ScoreParams& p, int d, int kv_format, cudaStream_t stream) {
+cudaError_t launch_score_tiles(const ScoreParams& p_in, int d, int kv_format, cudaStream_t stream) {
+    ScoreParams p = p_in;
+    // a block of rows: the heads of as many queries as fit, or 128 heads of one
+    p.block_tok = p.G <= kBlockRows ? kBlockRows / p.G : 1;
+    p.head_blocks = (p.G + kBlockRows - 1) / kBlockRows;
     return d == 128 ? launch_fmt<128>(p, kv_format, stream) : launch_fmt<64>(p, kv_format, stream);
 }
 
