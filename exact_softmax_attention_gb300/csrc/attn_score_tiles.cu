@@ -3,20 +3,20 @@
 //
 // The transposed scores S^T = K Q^T have the tokens as rows of the accumulator, so that a thread owns a token: it
 // reads its row of S^T from tensor memory, adds exp2(scale s - lse) over the columns, and needs no sum across threads. A unit of
-// work is 256 tokens of a (sequence, kv head), two accumulator tiles that share the operand Q; a task is a unit times a
-// block of up to 128 rows (as many whole queries times their query heads as fit) that see any of it. The tasks of the whole call, in the
-// order sequence, kv head, tokens, rows, are dealt out in equal runs to one persistent block per SM. A unit that lies in more than
-// one run leaves partial sums, which a second kernel adds in order.
+// work is 512 tokens of a (sequence, kv head) (fewer where there would be fewer units than SMs), four accumulator tiles of 128 that share the
+// operand Q; a task is a unit times a block of up to 128 rows (as many whole queries times their query heads as fit) that see any of it. The
+// tasks of the whole call, in the order sequence, kv head, tokens, rows, are dealt out in equal runs to one persistent block per SM. A unit
+// that lies in more than one run leaves partial sums, which a second kernel adds in order.
 //
-// What bounds it. With d = 128 a task is 2 x 8 products of 128 x 128 x 16, 1024 clocks of the tensor pipe, and 32768
-// exponentials, 1024 clocks of the MUFU; rows that stay the same (up to 128) against new tokens every task are 64 KB of bf16
-// keys for that, more than the memory delivers in the time.
+// What bounds it. With d = 128 a task is 4 x 8 products of 128 x 128 x 16, 2048 clocks of the tensor pipe, and 65536
+// exponentials, 2048 clocks of the MUFU, for 32 KB of q from the L2 (with units of 256 tokens the L2 was the bound: 153 us for the whole prompts
+// below); rows that stay the same (up to 128) against new tokens every task are 128 KB of bf16 keys for that, more than the memory delivers
+// in the time.
 //
-// Roles of the warps: 0-15 exponentials and sums, for each accumulator tile two groups of four warps that take half of the columns
-// each (two buffers per tile, so that the products of a task run during the exponentials of the one before); 16 and 17 the keys of a tile
-// each, through tensor copies of 64 or 16 rows where the page size is a multiple of that, else by 16-byte copies of rows that the page
-// table gives; 18 the blocks of q through tensor copies (one box is the heads of as many queries as fit) and their LSE; 19 and 20 the
-// products of a tile each, issued by one thread: while one waits for its buffer, the other one's products run.
+// Roles of the warps: 0-15 exponentials and sums, four warps per accumulator tile; 16 and 17 the keys of two tiles each, through tensor
+// copies of 64 or 16 rows where the page size is a multiple of that, else by 16-byte copies of rows that the page table gives; 18 the blocks
+// of q through tensor copies (one box is the heads of as many queries as fit) and their LSE; 19 and 20 the products of two tiles each,
+// issued by one thread: while one waits for its buffer, the other one's products run.
 //
 // 8-bit caches: K is multiplied as it is (kind::f8f6f4). A kernel before this one scales each row of q by a power of two and splits
 // it into two e4m3 parts: exact unless an element is more than 2^9 below the row's largest (then off by at most 2^-17 of that).
@@ -25,13 +25,13 @@
 namespace attn {
 namespace {
 
-constexpr int kTileTok = 128, kUnitTok = 2 * kTileTok;  // tokens of an accumulator tile, of a unit
-constexpr int kBlockRows = 128;                         // rows of a task
+constexpr int kTileTok = 128, kTiles = 4;   // tokens of an accumulator tile, tiles of a unit at most
+constexpr int kUnitTok = kTiles * kTileTok;
+constexpr int kBlockRows = 128;             // rows of a task
 constexpr int kTileThreads = 21 * 32;
 constexpr int kSumWarps = 16, kKeyWarp = 16, kQueryWarp = 18, kProductWarp = 19;
 
-// LONG: many blocks of rows against the same keys; else many keys against the same rows.
-template <int D, int FMT, bool LONG>
+template <int D, int FMT>
 struct ScoreLayout {
     static constexpr bool kF8 = FMT != ATTN_KV_BF16;
     static constexpr int kRow = kF8 ? D : 2 * D;             // bytes of a key
@@ -41,21 +41,17 @@ struct ScoreLayout {
     static constexpr int kTile = kChunk * kChunks;
     static constexpr int kQChunks = kF8 ? 2 : kChunks;       // of a block of q: its columns, or its two 8-bit parts
     static constexpr int kQ = kQChunks * kChunk;
-    static constexpr int kK = 2 * kTile;                     // keys of a unit
-    // What streams has the stages: 128 KB (64 KB with narrow 8-bit heads) on their way per SM.
-    static constexpr int kKStages = LONG ? (kK > 32768 ? 1 : 2) : (kK > 32768 ? 2 : 4);
-    static constexpr int kQStages = LONG ? 4 : 2, kLseStages = kQStages + 2;
-    static constexpr int kKOff = 0, kQOff = kKStages * kK;
+    static constexpr int kKStages = kTile > 16384 ? 4 : 8;   // tiles of keys
+    static constexpr int kQStages = kQ > 16384 ? 2 : 4, kLseStages = kQStages + 2;
+    static constexpr int kKOff = 0, kQOff = kKStages * kTile;
     // per row of a block of q: minus the LSE (times log2 e), factor of the scores, last token seen
     static constexpr int kLseOff = kQOff + kQStages * kQ, kLseStage = 3 * kBlockRows * 4;
     static constexpr int kBarOff = kLseOff + kLseStages * kLseStage;
     static constexpr int bK = 0, bKFree = bK + kKStages, bQ = bKFree + kKStages, bQFree = bQ + kQStages, bL = bQFree + kQStages, bLFree = bL + kLseStages;
-    static constexpr int bS = bLFree + kLseStages, bSFree = bS + 4, bHalf = bSFree + 4, bHalfFree = bHalf + 4;
-    static constexpr int bDrain = bHalfFree + 4, kBars = bDrain + 2;
+    static constexpr int bS = bLFree + kLseStages, bSFree = bS + kTiles, bDrain = bSFree + kTiles, kBars = bDrain + 2;
     // tensor-memory base, abort flag; per lse stage: do rows need their own limits; the plan
     static constexpr int kMiscOff = kBarOff + kBars * 8, kOddOff = kMiscOff + 8, kPlanOff = kOddOff + kLseStages * 4;
-    static constexpr int kHalfOff = kPlanOff + 16;  // sums over the upper columns, of two units in turn
-    static constexpr int kBytes = kHalfOff + 2 * kUnitTok * 4;
+    static constexpr int kBytes = kPlanOff + 16;
     static_assert(kBarOff % 8 == 0 && kPlanOff % 8 == 0 && kLseStages % 2 == 0 && kBytes <= 232448, "shared memory of an SM");
 };
 
@@ -157,17 +153,17 @@ __global__ void __launch_bounds__(256) split_q_kernel(const __nv_bfloat16* q, ui
 
 // ---- the tasks of a call
 
-// Tasks of one kv head of a sequence. Unit u (tokens from 256 u on) is taken with the blocks of rows from first(u) on; blocks that
-// do not see it may be among them (when the queries of a block do not divide 256).
+// Tasks of one kv head of a sequence. Unit u (tokens from unit_tok u on) is taken with the blocks of rows from first(u) on; blocks that
+// do not see it may be among them (when the queries of a block do not divide a unit).
 struct SeqTasks {
     int units, blocks;
     long long skip;  // first(u) = max(0, each u - skip)
-    int each;        // blocks of 256 tokens, rounded down
-    __device__ __forceinline__ SeqTasks(const ScoreSeq& s, int block_tok, int head_blocks) {
-        units = (s.len + kUnitTok - 1) / kUnitTok;
+    int each;        // blocks of a unit's tokens, rounded down
+    __device__ __forceinline__ SeqTasks(const ScoreSeq& s, int unit_tok, int block_tok, int head_blocks) {
+        units = (s.len + unit_tok - 1) / unit_tok;
         blocks = (s.n + block_tok - 1) / block_tok * head_blocks;
-        // token 256 u is query 256 u - ctx, in block floor((256 u - ctx) / block_tok) >= floor(256 / block_tok) u - ceil(ctx / block_tok)
-        each = kUnitTok / block_tok * head_blocks;
+        // token U u is query U u - ctx, in block floor((U u - ctx) / block_tok) >= floor(U / block_tok) u - ceil(ctx / block_tok)
+        each = unit_tok / block_tok * head_blocks;
         skip = (long long)((s.ctx + block_tok - 1) / block_tok) * head_blocks;
     }
     __device__ __forceinline__ int first(int u) const {
@@ -190,9 +186,9 @@ struct UnitWalk {
     bool whole;      // the run holds the first of the unit's tasks
     ScoreSeq s;
     SeqTasks seq;
-    __device__ __forceinline__ UnitWalk(const ScoreParams& p, int b_, long long rest, int count) : b(b_), s(), seq(s, 1, 1) {
+    __device__ __forceinline__ UnitWalk(const ScoreParams& p, int b_, long long rest, int count) : b(b_), s(), seq(s, 1, 1, 1) {
         score_seq(p, b, s);
-        seq = SeqTasks(s, p.block_tok, p.head_blocks);
+        seq = SeqTasks(s, p.unit_tok, p.block_tok, p.head_blocks);
         const long long each = seq.before(seq.units);
         h = (int)(rest / each);
         rest -= each * h;
@@ -232,12 +228,16 @@ struct UnitWalk {
             h = 0;
             do ++b;
             while (!score_seq(p, b, s));
-            seq = SeqTasks(s, p.block_tok, p.head_blocks);
+            seq = SeqTasks(s, p.unit_tok, p.block_tok, p.head_blocks);
         }
         from = -seq.skip;
         cut();
         return true;
     }
+    // tiles of the unit that there are
+    __device__ __forceinline__ int tiles(const ScoreParams& p) const { return min(p.unit_tok, s.len - u * p.unit_tok + kTileTok - 1) / kTileTok; }
+    // last token that a block of rows sees
+    __device__ __forceinline__ int top(const ScoreParams& p, int i0) const { return s.ctx + min(i0 + p.block_tok, s.n) - 1; }
     // first query of a block, its first head, its rows
     __device__ __forceinline__ int query(const ScoreParams& p, int block) const {
         return p.head_blocks > 1 ? block / p.head_blocks : block * p.block_tok;
@@ -253,7 +253,7 @@ struct UnitWalk {
 __device__ __forceinline__ long long tasks_of(const ScoreParams& p, int b) {
     ScoreSeq s;
     if (!score_seq(p, b, s)) return 0;
-    const SeqTasks t(s, p.block_tok, p.head_blocks);
+    const SeqTasks t(s, p.unit_tok, p.block_tok, p.head_blocks);
     return t.before(t.units) * p.Hkv;
 }
 
@@ -303,11 +303,11 @@ __device__ __forceinline__ TaskRun task_run(const ScoreParams& p, int block, int
     return run;
 }
 
-template <int D, int FMT, bool LONG>
+template <int D, int FMT>
 __global__ void __launch_bounds__(kTileThreads, 1)
     score_tiles_kernel(const __grid_constant__ ScoreParams p, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK) {
     grid_dependents_launch();
-    using L = ScoreLayout<D, FMT, LONG>;
+    using L = ScoreLayout<D, FMT>;
     constexpr bool F8 = L::kF8;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -324,8 +324,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint64_t wd = p.watchdog_ns;
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::kKStages; ++i) {
-            mbar_init(&bars[L::bK + i], 2);
-            mbar_init(&bars[L::bKFree + i], 2);
+            mbar_init(&bars[L::bK + i], 1);
+            mbar_init(&bars[L::bKFree + i], 1);
         }
         for (int i = 0; i < L::kQStages; ++i) {
             mbar_init(&bars[L::bQ + i], 1);
@@ -335,11 +335,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_init(&bars[L::bL + i], 1);
             mbar_init(&bars[L::bLFree + i], kSumWarps);
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kTiles; ++i) {
             mbar_init(&bars[L::bS + i], 1);
-            mbar_init(&bars[L::bHalf + i], 4);
-            mbar_init(&bars[L::bHalfFree + i], 4);
-            mbar_init(&bars[L::bSFree + i], kSumWarps / 2);
+            mbar_init(&bars[L::bSFree + i], 4);
         }
         mbar_init(&bars[L::bDrain], 1);
         mbar_init(&bars[L::bDrain + 1], 1);
@@ -362,11 +360,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t base = smem_u32(smem);
     UnitWalk at(p, run.b, run.rest, run.count);
 
+    // The stages of the keys belong to the tiles of a unit, the same number to each, so that one warp fills a stage and one thread
+    // multiplies what it holds; its n-th use:
+    const int per_tile = L::kKStages * kTileTok / p.unit_tok;
+    auto key_stage = [&](int t, int n) { return t * per_tile + (n & (per_tile - 1)); };  // (powers of two)
+    auto key_turn = [&](int n) { return (uint32_t)(n / per_tile & 1); };
+
     if (warp == kKeyWarp || warp == kKeyWarp + 1) {
-        // ---------------------------------------------------------------- keys of a tile
-        const int tile = warp - kKeyWarp;
+        // ---------------------------------------------------------------- keys, every other tile
         bool ok = true;
-        int unit = 0;
+        int uses[2] = {0, 0};  // of the stages of this warp's two tiles
         const CUtensorMap* map = &tmK;
         const int none = p.num_pages * p.page_size;  // the first row past the cache: zeros
         uint64_t* pending = nullptr;                  // the stage whose 16-byte copies may still be on their way
@@ -377,70 +380,76 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (lane == 0) mbar_arrive(pending);
             pending = nullptr;
         };
-        for (;;) {
-            const int st = unit % L::kKStages;
-            const uint32_t parity = (uint32_t)(unit / L::kKStages & 1) ^ 1u;
-            const int t0 = at.u * kUnitTok + tile * kTileTok;
+        while (ok) {
+            const int tiles = at.tiles(p);
             const int* pt = p.page_table + (long long)at.b * p.max_pages;
-            const uint32_t to = base + L::kKOff + st * L::kK + tile * L::kTile;
-            uint64_t* full = &bars[L::bK + st];
-            if (p.box_rows > 1) {
-                // lane -> rows of one page, and which columns of them
-                const int boxes = kTileTok / p.box_rows;
-                const int part = lane / boxes, first = (lane - part * boxes) * p.box_rows;
-                const bool active = lane < L::kChunks * boxes;
-                int row = none, slot;
-                if (active && t0 + first < at.s.len) {
-                    const int page = score_place(p, pt, t0 + first, slot);
-                    if (page >= 0) row = page * p.page_size + slot;
-                }
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::bKFree + st], parity, abort_flag, wd)))) break;
-                if (lane == 0) mbar_arrive_expect_tx(full, L::kTile);
-                __syncwarp();
-                if (active) copy_box(to + part * L::kChunk + first * L::kBox, map, full, at.h * D + part * (L::kBox / (F8 ? 1 : 2)), row);
-                __syncwarp();
-            } else {
-                // rows of tokens lane, lane + 32, ...; 16-byte pieces of all of them
-                constexpr int kUnits = L::kRow / 16, kStep = 32 / kUnits;
-                int row[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    int slot;
-                    const int page = t0 + lane + 32 * e < at.s.len ? score_place(p, pt, t0 + lane + 32 * e, slot) : -1;
-                    row[e] = page >= 0 ? page * p.page_size + slot : -1;
-                }
-                // (a stage that is not free yet may wait for what this warp has not handed over)
-                if (!__all_sync(0xffffffffu, mbar_test_wait(&bars[L::bKFree + st], parity))) {
-                    cp_async_wait<0>();
-                    hand_over();
-                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::bKFree + st], parity, abort_flag, wd)))) break;
-                }
-                const int u = lane % kUnits;
-                const uint8_t* keys = static_cast<const uint8_t*>(p.k_cache) + (long long)at.h * L::kRow + 16 * u;
-                const long long row_bytes = (long long)p.Hkv * L::kRow;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll 8
-                    for (int r = lane / kUnits; r < 32; r += kStep) {
-                        const int from = __shfl_sync(0xffffffffu, row[e], r);
-                        cp_async16(to + unit_at<L::kRow>(32 * e + r, u), keys + (from >= 0 ? from : 0) * row_bytes, from >= 0 ? 16 : 0);
+            for (int x = 0; x < kTiles / 2; ++x) {
+                const int t = warp - kKeyWarp + 2 * x, st = key_stage(t, uses[x]);
+                if (!ok || t >= tiles) continue;
+                const uint32_t parity = key_turn(uses[x]) ^ 1u;
+                const int t0 = at.u * p.unit_tok + t * kTileTok;
+                const uint32_t to = base + L::kKOff + st * L::kTile;
+                uint64_t* full = &bars[L::bK + st];
+                if (p.box_rows > 1) {
+                    // lane -> rows of one page, and which columns of them
+                    const int boxes = kTileTok / p.box_rows;
+                    const int part = lane / boxes, first = (lane - part * boxes) * p.box_rows;
+                    const bool active = lane < L::kChunks * boxes;
+                    int row = none, slot;
+                    if (active && t0 + first < at.s.len) {
+                        const int page = score_place(p, pt, t0 + first, slot);
+                        if (page >= 0) row = page * p.page_size + slot;
                     }
-                cp_async_commit();
-                if (pending) cp_async_wait<1>();
-                hand_over();
-                pending = full;
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::bKFree + st], parity, abort_flag, wd)))) continue;
+                    if (lane == 0) mbar_arrive_expect_tx(full, L::kTile);
+                    __syncwarp();
+                    if (active) copy_box(to + part * L::kChunk + first * L::kBox, map, full, at.h * D + part * (L::kBox / (F8 ? 1 : 2)), row);
+                    __syncwarp();
+                } else {
+                    // rows of tokens lane, lane + 32, ...; 16-byte pieces of all of them
+                    constexpr int kUnits = L::kRow / 16, kStep = 32 / kUnits;
+                    int row[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        int slot;
+                        const int page = t0 + lane + 32 * e < at.s.len ? score_place(p, pt, t0 + lane + 32 * e, slot) : -1;
+                        row[e] = page >= 0 ? page * p.page_size + slot : -1;
+                    }
+                    // (a stage that is not free yet may wait for what this warp has not handed over)
+                    if (!__all_sync(0xffffffffu, mbar_test_wait(&bars[L::bKFree + st], parity))) {
+                        cp_async_wait<0>();
+                        hand_over();
+                        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::bKFree + st], parity, abort_flag, wd)))) continue;
+                    }
+                    const int u = lane % kUnits;
+                    const uint8_t* keys = static_cast<const uint8_t*>(p.k_cache) + (long long)at.h * L::kRow + 16 * u;
+                    const long long row_bytes = (long long)p.Hkv * L::kRow;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll 8
+                        for (int r = lane / kUnits; r < 32; r += kStep) {
+                            const int from = __shfl_sync(0xffffffffu, row[e], r);
+                            cp_async16(to + unit_at<L::kRow>(32 * e + r, u), keys + (from >= 0 ? from : 0) * row_bytes, from >= 0 ? 16 : 0);
+                        }
+                    cp_async_commit();
+                    if (pending) cp_async_wait<1>();
+                    hand_over();
+                    pending = full;
+                }
+                ++uses[x];
             }
-            ++unit;
-            if (at.left == 0) break;
+            if (!ok || at.left == 0) break;
             at.next(p);
         }
         cp_async_wait<0>();
         hand_over();
-        if (!ok && p.box_rows > 1) {
+        if (!ok) {
             // let the copies in flight land before the block can end
             int dummy = 0;
-            for (int x = unit > L::kKStages ? unit - L::kKStages : 0; x < unit; ++x)
-                mbar_wait(&bars[L::bK + x % L::kKStages], (uint32_t)(x / L::kKStages & 1), &dummy, 20000000ull);
+            for (int x = 0; x < kTiles / 2; ++x)
+                for (int n = max(0, uses[x] - per_tile); n < uses[x]; ++n)
+                    mbar_wait(&bars[L::bK + key_stage(warp - kKeyWarp + 2 * x, n)], key_turn(n), &dummy, 20000000ull);
         }
     } else if (warp == kQueryWarp) {
         // ---------------------------------------------------------------- blocks of q and their LSE
@@ -505,134 +514,136 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 mbar_wait(&bars[L::bQ + x % L::kQStages], (uint32_t)(x / L::kQStages & 1), &dummy, 20000000ull);
         }
     } else if (warp >= kProductWarp) {
-        // ---------------------------------------------------------------- products of tile t
+        // ---------------------------------------------------------------- products of every other tile
         if (lane == 0) {
-            const int t = warp - kProductWarp;
+            const int mine = warp - kProductWarp;
             auto desc = [&](int off) { return L::kBox == 64 ? smem_desc_sw64(base + off) : smem_desc_sw128(base + off, L::kChunk, 1024); };
             const uint64_t dk = desc(L::kKOff), dq = desc(L::kQOff);
             auto wait = [&](int bar, uint32_t parity) { return mbar_wait(&bars[bar], parity, abort_flag, wd); };
             bool any = false, go = true, fresh = true;
-            int units = 0, qs = 0, i = 0;  // stages waited for, tasks
-            while (go && (go = wait(L::bK + units % L::kKStages, units / L::kKStages & 1))) {
-                const int ks = units++ % L::kKStages;
-                for (int r = at.r; r < at.end; ++r, ++i) {
+            int qs = 0;                          // stages of q waited for
+            int keys[kTiles / 2] = {0, 0};       // uses of the stages of the two tiles' keys
+            uint32_t uses[kTiles / 2] = {0, 0};  // of the two tiles' buffers
+            while (go) {
+                const int tiles = at.tiles(p);
+                for (int r = at.r; r < at.end; ++r) {
                     if (fresh) {
                         if (!(go = wait(L::bQ + qs % L::kQStages, qs / L::kQStages & 1))) break;
                         ++qs;
                     }
-                    const int st = (qs - 1) % L::kQStages, buf = i & 1;
+                    const int st = (qs - 1) % L::kQStages, top = at.top(p, at.query(p, r));
                     const uint64_t qd = dq + (uint64_t)((st * L::kQ) >> 4);
                     const uint32_t idesc = score_idesc<FMT>((at.rows(p, r) + 31) & ~31);
-                    if (!(go = wait(L::bSFree + 2 * t + buf, (unsigned)(i >> 1 & 1) ^ 1u))) break;
-                    tc_fence_after();
-                    any = true;
-                    const uint32_t d = tmem + (uint32_t)(2 * t + buf) * 128;
-                    const uint64_t kd = dk + (uint64_t)((ks * L::kK + t * L::kTile) >> 4);
-                    if constexpr (F8) {
 #pragma unroll
-                        for (int x = 0; x < 2 * (D / 32); ++x) {  // both parts of q
-                            const int part = x / (D / 32), k = x % (D / 32);
-                            mma8_ss(d, kd + (uint64_t)((k * 32) >> 4), qd + (uint64_t)((part * L::kChunk + k * 32) >> 4), idesc, x > 0);
+                    for (int x = 0; x < kTiles / 2; ++x) {
+                        const int t = mine + 2 * x, ks = key_stage(t, keys[x]);
+                        if (!go || t >= tiles) continue;
+                        if (r == at.r && !(go = wait(L::bK + ks, key_turn(keys[x])))) continue;
+                        if (at.u * p.unit_tok + t * kTileTok > top) continue;  // these rows see nothing of it
+                        if (!(go = wait(L::bSFree + t, (uses[x]++ & 1) ^ 1u))) continue;
+                        tc_fence_after();
+                        any = true;
+                        const uint32_t d = tmem + (uint32_t)t * 128;
+                        const uint64_t kd = dk + (uint64_t)((ks * L::kTile) >> 4);
+                        if constexpr (F8) {
+#pragma unroll
+                            for (int y = 0; y < 2 * (D / 32); ++y) {  // both parts of q
+                                const int part = y / (D / 32), k = y % (D / 32);
+                                mma8_ss(d, kd + (uint64_t)((k * 32) >> 4), qd + (uint64_t)((part * L::kChunk + k * 32) >> 4), idesc, y > 0);
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k)
+                                tc_mma_ss(d, kd + (uint64_t)(((k >> 2) * L::kChunk + (k & 3) * 32) >> 4),
+                                          qd + (uint64_t)(((k >> 2) * L::kChunk + (k & 3) * 32) >> 4), idesc, k > 0);
                         }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            tc_mma_ss(d, kd + (uint64_t)(((k >> 2) * L::kChunk + (k & 3) * 32) >> 4),
-                                      qd + (uint64_t)(((k >> 2) * L::kChunk + (k & 3) * 32) >> 4), idesc, k > 0);
+                        tc_commit(&bars[L::bS + t]);
                     }
-                    tc_commit(&bars[L::bS + 2 * t + buf]);
+                    if (!go) break;
                     fresh = true;
                     if (r + 1 < at.end) tc_commit(&bars[L::bQFree + st]);
                 }
                 if (!go || at.left == 0) break;
+#pragma unroll
+                for (int x = 0; x < kTiles / 2; ++x)
+                    if (mine + 2 * x < tiles) tc_commit(&bars[L::bKFree + key_stage(mine + 2 * x, keys[x]++)]);
                 fresh = at.next(p);
                 if (fresh) tc_commit(&bars[L::bQFree + (qs - 1) % L::kQStages]);
-                tc_commit(&bars[L::bKFree + ks]);
             }
             if (any) {
                 // every product has completed before the tensor memory is released
-                tc_commit(&bars[L::bDrain + t]);
+                tc_commit(&bars[L::bDrain + mine]);
                 int dummy = 0;
-                mbar_wait(&bars[L::bDrain + t], 0, &dummy, 50000000ull);
+                mbar_wait(&bars[L::bDrain + mine], 0, &dummy, 50000000ull);
             }
         }
         __syncwarp();
     } else if (warp < kSumWarps) {
         // ---------------------------------------------------------------- exponentials and sums
-        const int tile = warp >> 3, half = warp >> 2 & 1, quarter = warp & 3, mine = tile * kTileTok + quarter * 32 + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(256 * tile + 64 * half);
-        float* halves = reinterpret_cast<float*>(smem + L::kHalfOff);
+        const int tile = warp >> 2, quarter = warp & 3, mine = tile * kTileTok + quarter * 32 + lane;
+        const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)tile * 128;
         bool go = true, fresh = true;
-        int qs = 0, i = 0, units = 0;
+        int qs = 0;
+        uint32_t uses = 0;                // of the tile's buffer
         int piece = at.whole ? 1 : 0;  // place of a partial sum: 0 for the unit that an earlier run began, 1 for the last one
         while (go) {
-            const int first = at.u * kUnitTok + tile * kTileTok, tok = at.u * kUnitTok + mine;
+            const int first = at.u * p.unit_tok + tile * kTileTok, tok = at.u * p.unit_tok + mine;
+            const bool there = tile < at.tiles(p);
             float total = 0.0f;
-            for (int r = at.r; r < at.end; ++r, ++i) {
+            for (int r = at.r; r < at.end; ++r) {
                 if (fresh) ++qs;
-                const int ls = (qs - 1) % L::kLseStages, buf = i & 1;
-                const int i0 = at.query(p, r), columns = at.rows(p, r) - 64 * half;
+                const int ls = (qs - 1) % L::kLseStages, i0 = at.query(p, r), rows = at.rows(p, r);
                 // (not the barrier of q: its stage may have been filled twice since)
                 if (!(go = __all_sync(0xffffffffu, mbar_wait(&bars[L::bL + ls], (uint32_t)((qs - 1) / L::kLseStages & 1), abort_flag, wd)))) break;
-                const float* lse2 = reinterpret_cast<const float*>(smem + L::kLseOff + ls * L::kLseStage) + 64 * half;
+                const float* lse2 = reinterpret_cast<const float*>(smem + L::kLseOff + ls * L::kLseStage);
                 const float* factor = lse2 + kBlockRows;
                 const int* last = reinterpret_cast<const int*>(lse2 + 2 * kBlockRows);
-                // the first row sees the fewest tokens, the last one the most
-                const int top = at.s.ctx + min(i0 + p.block_tok, at.s.n) - 1;
-                const bool mixed = odd_rows[ls] != 0 || at.s.ctx + i0 < first + kTileTok - 1;
-                if (!(go = __all_sync(0xffffffffu, mbar_wait(&bars[L::bS + 2 * tile + buf], (unsigned)(i >> 1 & 1), abort_flag, wd)))) break;
-                tc_fence_after();
-                const uint32_t from = lanes + (uint32_t)buf * 128;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                auto add = [&](const uint32_t (&x)[32], int c, auto masked) {
+                if (there && first <= at.top(p, i0)) {
+                    // the first row sees the fewest tokens
+                    const bool mixed = odd_rows[ls] != 0 || at.s.ctx + i0 < first + kTileTok - 1;
+                    if (!(go = __all_sync(0xffffffffu, mbar_wait(&bars[L::bS + tile], uses++ & 1, abort_flag, wd)))) break;
+                    tc_fence_after();
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    auto add = [&](auto masked) {
+#pragma unroll 1
+                        for (int c = 0; c < rows; c += 32) {
+                            uint32_t x[32];
+                            tmem_ld32(from + c, x);
+                            tc_wait_ld();
+                            reg_fence(x);
+                            if (c + 32 >= rows) {  // (the next products need not wait for the last exponentials)
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&bars[L::bSFree + tile]);
+                            }
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 l = *reinterpret_cast<const float4*>(lse2 + c + e);
-                        float4 f = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
-                        if constexpr (F8) f = *reinterpret_cast<const float4*>(factor + c + e);
-                        float y[4];
-                        ffma2(y[0], y[1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]), f.x, f.y, l.x, l.y);
-                        ffma2(y[2], y[3], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]), f.z, f.w, l.z, l.w);
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 l = *reinterpret_cast<const float4*>(lse2 + c + e);
+                                float4 f = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+                                if constexpr (F8) f = *reinterpret_cast<const float4*>(factor + c + e);
+                                float y[4];
+                                ffma2(y[0], y[1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]), f.x, f.y, l.x, l.y);
+                                ffma2(y[2], y[3], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]), f.z, f.w, l.z, l.w);
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) y[z] = ex2_mufu(y[z]);
-                        if constexpr (decltype(masked)::value) {
-                            const int4 m = *reinterpret_cast<const int4*>(last + c + e);
-                            y[0] = tok <= m.x ? y[0] : 0.0f;
-                            y[1] = tok <= m.y ? y[1] : 0.0f;
-                            y[2] = tok <= m.z ? y[2] : 0.0f;
-                            y[3] = tok <= m.w ? y[3] : 0.0f;
+                                for (int z = 0; z < 4; ++z) y[z] = ex2_mufu(y[z]);
+                                if constexpr (decltype(masked)::value) {
+                                    const int4 m = *reinterpret_cast<const int4*>(last + c + e);
+                                    y[0] = tok <= m.x ? y[0] : 0.0f;
+                                    y[1] = tok <= m.y ? y[1] : 0.0f;
+                                    y[2] = tok <= m.z ? y[2] : 0.0f;
+                                    y[3] = tok <= m.w ? y[3] : 0.0f;
+                                }
+                                fadd2(sum[0], sum[1], sum[0], sum[1], y[0], y[1]);
+                                fadd2(sum[2], sum[3], sum[2], sum[3], y[2], y[3]);
+                            }
                         }
-                        fadd2(sum[0], sum[1], sum[0], sum[1], y[0], y[1]);
-                        fadd2(sum[2], sum[3], sum[2], sum[3], y[2], y[3]);
-                    }
-                };
-                auto columns_of = [&](auto masked) {
-                    uint32_t x[32];
-                    tmem_ld32(from, x);
-                    tc_wait_ld();
-                    reg_fence(x);
-                    if (columns > 32) {
-                        add(x, 0, masked);
-                        tmem_ld32(from + 32, x);
-                        tc_wait_ld();
-                        reg_fence(x);
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars[L::bSFree + 2 * tile + buf]);  // (the next products need not wait for the last exponentials)
-                    add(x, columns > 32 ? 32 : 0, masked);
-                };
-                if (first <= top && first < at.s.len && columns > 0) {
+                    };
                     if (mixed)
-                        columns_of(std::true_type{});
+                        add(std::true_type{});
                     else
-                        columns_of(std::false_type{});
-                } else {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars[L::bSFree + 2 * tile + buf]);
+                        add(std::false_type{});
+                    total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 }
-                total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 fresh = true;
                 if (r + 1 < at.end) {
                     __syncwarp();
@@ -640,35 +651,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
             }
             if (!go) break;
-            // the sums over the upper columns to the warps of the lower ones, in two places in turn
-            float* other = halves + (units & 1) * kUnitTok + mine;
-            const int pair = 2 * tile + (units & 1);
-            const uint32_t turn = (uint32_t)(units >> 1 & 1);
-            if (half) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars[L::bHalfFree + pair], turn ^ 1u, abort_flag, wd))) break;
-                *other = total;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[L::bHalf + pair]);
-            } else {
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars[L::bHalf + pair], turn, abort_flag, wd))) break;
-                total += *other;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[L::bHalfFree + pair]);
-                if (at.complete() && at.whole) {
-                    int slot;
-                    if (tok < at.s.len) {
-                        const int page = score_place(p, p.page_table + (long long)at.b * p.max_pages, tok, slot);
-                        if (page >= 0) {
-                            float* to = score_slot(p, page, slot, at.h);
-                            *to = p.decay != 0.0f && tok < at.s.ctx ? fmaf(p.decay, *to, total) : total;
-                        }
+            if (at.complete() && at.whole) {
+                int slot;
+                if (tok < at.s.len && mine < p.unit_tok) {
+                    const int page = score_place(p, p.page_table + (long long)at.b * p.max_pages, tok, slot);
+                    if (page >= 0) {
+                        float* to = score_slot(p, page, slot, at.h);
+                        *to = p.decay != 0.0f && tok < at.s.ctx ? fmaf(p.decay, *to, total) : total;
                     }
-                } else {
-                    p.partial[((long long)blockIdx.x * 2 + piece) * kUnitTok + mine] = total;
                 }
+            } else {
+                p.partial[((long long)blockIdx.x * 2 + piece) * kUnitTok + mine] = total;
             }
             piece = 1;
-            ++units;
             if (at.left == 0) break;
             fresh = at.next(p);
             if (fresh) {
@@ -702,8 +697,8 @@ __global__ void __launch_bounds__(kUnitTok) score_join_kernel(const __grid_const
     if (begin < run.from || end <= run.from + run.count) return;
     float total = p.partial[((long long)blockIdx.x * 2 + 1) * kUnitTok + threadIdx.x];
     for (long long c = blockIdx.x + 1; c * run.each < end; ++c) total += p.partial[c * 2 * kUnitTok + threadIdx.x];
-    const int tok = at.u * kUnitTok + threadIdx.x;
-    if (tok >= at.s.len) return;
+    const int tok = at.u * p.unit_tok + threadIdx.x;
+    if (tok >= at.s.len || (int)threadIdx.x >= p.unit_tok) return;
     int slot;
     const int page = score_place(p, p.page_table + (long long)at.b * p.max_pages, tok, slot);
     if (page < 0) return;
@@ -711,18 +706,21 @@ __global__ void __launch_bounds__(kUnitTok) score_join_kernel(const __grid_const
     *to = p.decay != 0.0f && tok < at.s.ctx ? fmaf(p.decay, *to, total) : total;
 }
 
-template <int D, int FMT, bool LONG>
+template <int D, int FMT>
 cudaError_t launch_tiles(ScoreParams p, cudaStream_t stream) {
-    using L = ScoreLayout<D, FMT, LONG>;
+    using L = ScoreLayout<D, FMT>;
     constexpr int bytes = L::kBytes, elem = L::kF8 ? 1 : 2;
     static std::atomic<bool> attr_set[kMaxAttrDevices];
-    cudaError_t e = ensure_smem_attr(score_tiles_kernel<D, FMT, LONG>, bytes, attr_set);
+    cudaError_t e = ensure_smem_attr(score_tiles_kernel<D, FMT>, bytes, attr_set);
     if (e != cudaSuccess) return e;
     p.box_rows = p.page_size % 64 == 0 ? 64 : (p.page_size % 16 == 0 ? 16 : 1);
-    // no more blocks than there can be tasks
+    // Units of 512 tokens read q half as often as units of 256, but there have to be units (of full tables, or tasks of them) for all SMs.
     const long long blocks = ((long long)p.max_q + p.block_tok - 1) / p.block_tok * p.head_blocks;
-    const long long most = (long long)p.B * p.Hkv * (((long long)p.max_pages * p.page_size + kUnitTok - 1) / kUnitTok);
-    const unsigned grid = (unsigned)(most >= p.num_sms || most * blocks >= p.num_sms ? p.num_sms : most * blocks);
+    const long long capacity = (long long)p.max_pages * p.page_size, heads = (long long)p.B * p.Hkv;
+    p.unit_tok = kUnitTok;
+    auto tasks = [&]() { return heads * ((capacity + p.unit_tok - 1) / p.unit_tok) * (blocks < p.num_sms ? blocks : p.num_sms); };
+    while (p.unit_tok > kTileTok && tasks() < p.num_sms) p.unit_tok /= 2;
+    const unsigned grid = (unsigned)(tasks() < p.num_sms ? tasks() : p.num_sms);  // no more blocks than tasks
     // memory of the call: partial sums (unless a unit is one task), factors and parts of q
     const size_t rows = (size_t)p.T * p.Hq;
     const size_t n_partial = blocks > 1 ? (size_t)grid * 2 * kUnitTok : 0, n_factor = L::kF8 ? (rows + 3) / 4 * 4 : 0;
@@ -759,22 +757,17 @@ cudaError_t launch_tiles(ScoreParams p, cudaStream_t stream) {
         e = launch_kernel(split_q_kernel<D>, dim3((unsigned)((rows * (D / 8) + 255) / 256)), 256, 0, stream, {}, p.q, parts, p.factor, (long long)rows,
                           p.scale_log2);
     if (e == cudaSuccess)
-        e = launch_kernel(score_tiles_kernel<D, FMT, LONG>, dim3(grid), kTileThreads, bytes, stream, L::kF8 ? dependent : LaunchMode{}, p, tmQ, tmK);
+        e = launch_kernel(score_tiles_kernel<D, FMT>, dim3(grid), kTileThreads, bytes, stream, L::kF8 ? dependent : LaunchMode{}, p, tmQ, tmK);
     if (e == cudaSuccess && n_partial > 0) e = launch_kernel(score_join_kernel, dim3(grid), kUnitTok, 0, stream, dependent, p);
     if (ws) cudaFreeAsync(ws, stream);
     return e;
 }
 
-template <int D, int FMT>
-cudaError_t launch_rows(const ScoreParams& p, cudaStream_t stream) {
-    return p.max_q > p.block_tok || p.head_blocks > 1 ? launch_tiles<D, FMT, true>(p, stream) : launch_tiles<D, FMT, false>(p, stream);
-}
-
 template <int D>
 cudaError_t launch_fmt(const ScoreParams& p, int fmt, cudaStream_t stream) {
-    return fmt == ATTN_FP8_E4M3   ? launch_rows<D, ATTN_FP8_E4M3>(p, stream)
-           : fmt == ATTN_FP8_E5M2 ? launch_rows<D, ATTN_FP8_E5M2>(p, stream)
-                                  : launch_rows<D, ATTN_KV_BF16>(p, stream);
+    return fmt == ATTN_FP8_E4M3   ? launch_tiles<D, ATTN_FP8_E4M3>(p, stream)
+           : fmt == ATTN_FP8_E5M2 ? launch_tiles<D, ATTN_FP8_E5M2>(p, stream)
+                                  : launch_tiles<D, ATTN_KV_BF16>(p, stream);
 }
 
 }  // namespace

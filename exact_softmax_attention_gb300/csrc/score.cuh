@@ -24,8 +24,9 @@ struct ScoreParams {
     unsigned int ps_magic;   // tok / page_size by multiplication, as in DecodeParams
     int ps_shift;
     int chunk, chunks;       // few rows: tokens per block, blocks of the longest sequence
-    // tiles: [blocks, 2, 256] sums of units that lie in several blocks; 8-bit caches: factor of the scores of each row of q
+    // tiles: [blocks, 2, unit_tok] sums of units that lie in several blocks; 8-bit caches: factor of the scores of each row of q
     float *partial, *factor;
+    int unit_tok;                // tokens of a unit: 128, 256 or 512
     int block_tok, head_blocks;  // tokens of a block of rows; blocks of rows of a token (one of the two is 1)
     int box_rows;                // rows of a copy of keys through the map (64 or 16, dividing the page size), 1: no map
     int* status;

@@ -177,6 +177,8 @@ MANY = [
     ([9, 50], [300, 260], 100, 1, 128, 16, False),        # one query per block
     ([400, 7], [600, 90], 10, 2, 64, 32, False),          # 25 queries per block
     ([600], [1100], 21, 3, 128, 128, True),
+    ([32] * 12, [600 + 400 * i for i in range(12)], 16, 8, 128, 16, True),  # many units of 512 tokens and less for each block
+    ([32] * 12, [600 + 400 * i for i in range(12)], 16, 8, 64, 7, True),
     ([20] * 500, [20 + i % 7 for i in range(500)], 1, 1, 64, 16, True),  # more sequences than a block's threads
 ]
 
