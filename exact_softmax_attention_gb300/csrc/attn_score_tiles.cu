@@ -539,7 +539,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         const int t = mine + 2 * x, ks = key_stage(t, keys[x]);
                         if (!go || t >= tiles) continue;
                         if (r == at.r && !(go = wait(L::bK + ks, key_turn(keys[x])))) continue;
-                        if (at.u * p.unit_tok + t * kTileTok > top) continue;  // these rows see nothing of it
+                        if (at.u * p.unit_tok + t * kTileTok > top) {  // these rows see nothing of it
+                            if (r + 1 == at.end) tc_commit(&bars[L::bKFree + ks]), ++keys[x];
+                            continue;
+                        }
                         if (!(go = wait(L::bSFree + t, (uses[x]++ & 1) ^ 1u))) continue;
                         tc_fence_after();
                         any = true;
@@ -558,15 +561,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                           qd + (uint64_t)(((k >> 2) * L::kChunk + (k & 3) * 32) >> 4), idesc, k > 0);
                         }
                         tc_commit(&bars[L::bS + t]);
+                        if (r + 1 == at.end) tc_commit(&bars[L::bKFree + ks]), ++keys[x];
                     }
                     if (!go) break;
                     fresh = true;
                     if (r + 1 < at.end) tc_commit(&bars[L::bQFree + st]);
                 }
                 if (!go || at.left == 0) break;
-#pragma unroll
-                for (int x = 0; x < kTiles / 2; ++x)
-                    if (mine + 2 * x < tiles) tc_commit(&bars[L::bKFree + key_stage(mine + 2 * x, keys[x]++)]);
                 fresh = at.next(p);
                 if (fresh) tc_commit(&bars[L::bQFree + (qs - 1) % L::kQStages]);
             }
