@@ -2,20 +2,23 @@
 // slots that remain (attn_kv_compact_paged).
 //
 // Selection, one block per (sequence, kv head). Of the tokens between the first `sinks` and the last `recent` the m with the
-// largest scores stay, ties to the earlier token. Scores become unsigned keys of the same order; the m-th largest key is found by
-// digits of 8 bits from the top: a histogram of the keys that share the digits found so far, the digit in which the count from
-// above passes m. Then every thread knows of its tokens whether they stay, but for those equal to that key, which
-// are numbered in token order. A kept token below end = budget - recent stays in its slot; the holes there, numbered in
-// order, take the kept tokens behind end, numbered in order. The keys are read from memory once and held in registers
-// when a block's threads have room for them, else read again in every pass. Bounded by latency: a dozen block-wide steps.
+// largest scores stay, ties to the earlier token. Scores become unsigned keys of the same order, held in shared memory; the m-th largest
+// is found by digits of 11, 11 and 10 bits from the top: a histogram of the keys that share the digits found so far, the digit in
+// which the count from above passes m. After the first digit few keys are left in general, which go to a list, so that only the
+// first histogram is of all keys. Then a thread takes neighbouring tokens, so that one scan over the block each numbers the equals of
+// the m-th key, and the holes and tails: a kept token below end = budget - recent stays in its slot, the holes there take in order
+// the kept tokens behind it. Bounded by latency: the loads and a dozen block-wide steps. (With keys in registers, four digits of 8
+// bits, and a numbering per 1024 tokens: 64 x 8 rows of 4100-4352 tokens ~100 us.)
 //
-// Compaction: row kept[j] -> j with kept[j] >= j. A block walks the slots in ascending order: it loads a run of rows,
-// then stores them. Every row that it reads later lies at or behind the end of the run, so nothing is overwritten that is still needed,
-// and only the loads and the stores of one run need a barrier between them. Blocks share nothing: one has a (sequence, kv head) and
-// some 16-byte columns of its rows, fewer columns where there are few sequences. Bounded by the memory.
+// Compaction: row kept[j] -> j with kept[j] >= j. A block lists the slots that get another row, in ascending order, with the
+// cache rows of both, and moves them in runs: it loads the rows of a run, then stores them. Every row that it reads later belongs to a slot
+// behind the run, and so lies there too: nothing is overwritten that is still needed, and only the loads and the stores of one run
+// need a barrier between them. Blocks share nothing: one has a (sequence, kv head) and some 16-byte columns of its rows, fewer columns
+// where there are few sequences. Bounded by the memory. (Walking all slots instead of a list took 150 us more in that case.)
 #include "attn.h"
 #include "kernels.cuh"
 #include "launch.cuh"
+#include "ptx.cuh"
 
 #include <math.h>
 #include <string.h>
@@ -23,9 +26,10 @@
 namespace attn {
 namespace {
 
-constexpr int kSelectThreads = 1024;
-constexpr int kHeld = 16;  // keys per thread in registers
-constexpr int kPairs = 4096;  // holes paired with tokens at a time
+constexpr int kLongThreads = 1024;   // selection from more tokens than the shared memory holds
+constexpr int kPairs = 4096;         // there: holes paired with tokens at a time
+constexpr int kSelectKeys = 50176;   // tokens of a row whose keys the shared memory holds: 196 KB, and 17 KB besides
+constexpr int kList = 2048;          // keys with the same first digit
 
 struct EvictParams {
     float* score;           // [num_pages, Hkv, page_size]
@@ -53,7 +57,7 @@ __device__ __forceinline__ int warps_before(int mine, int* sums, int& total) {
     __syncthreads();
     if (lane == 0) sums[warp] = mine;
     __syncthreads();
-    const int x = sums[lane];  // 32 warps
+    const int x = lane < (int)(blockDim.x >> 5) ? sums[lane] : 0;
     int upto = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -71,194 +75,332 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ int hist[256], sums[32], digit_at[2], place[kPairs];
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int b = (int)(blockIdx.x / (unsigned)p.Hkv), h = (int)(blockIdx.x % (unsigned)p.Hkv);
-    const int len = __ldg(p.seqlens + b), K = p.budget;
-    int* kept = p.kept + (long long)blockIdx.x * K;
-    if (len < 0 || len > (long long)p.max_pages * p.page_size) {
-        for (int j = tid; j < K; j += kSelectThreads) kept[j] = -1;
-        if (tid == 0) {
-            atomicCAS(p.status, 0, kDevBadIndex);
-            if (h == 0) p.new_seqlens[b] = len;
-        }
-        return;
+// What every selection does for a row: lengths, and the tokens that always stay. False: nothing is left to choose.
+struct SelectRow {
+    int h, len, end, stop, m, n;  // m of n tokens from `sinks` on stay, m < n
+    int* kept;
+    const int* pt;
+};
+__device__ __forceinline__ bool select_row(const EvictParams& p, SelectRow& s) {
+    const int b = (int)(blockIdx.x / (unsigned)p.Hkv), K = p.budget, tid = threadIdx.x, nt = blockDim.x;
+    s.h = (int)(blockIdx.x % (unsigned)p.Hkv);
+    s.len = __ldg(p.seqlens + b);
+    s.kept = p.kept + (long long)blockIdx.x * K;
+    s.pt = p.page_table + (long long)b * p.max_pages;
+    const bool bad = s.len < 0 || s.len > (long long)p.max_pages * p.page_size;
+    if (tid == 0) {
+        if (bad) atomicCAS(p.status, 0, kDevBadIndex);
+        if (s.h == 0) p.new_seqlens[b] = bad ? s.len : min(s.len, K);
     }
-    if (h == 0 && tid == 0) p.new_seqlens[b] = min(len, K);
-    if (len <= K) {
-        for (int j = tid; j < K; j += kSelectThreads) kept[j] = j < len ? j : -1;
-        return;
+    if (bad || s.len <= K) {
+        for (int j = tid; j < K; j += nt) s.kept[j] = !bad && j < s.len ? j : -1;
+        return false;
     }
-    const int end = K - p.recent, stop = len - p.recent;
-    for (int j = tid; j < p.sinks; j += kSelectThreads) kept[j] = j;
-    for (int j = tid; j < p.recent; j += kSelectThreads) kept[end + j] = stop + j;
-    const int m = end - p.sinks, n = stop - p.sinks;  // m of n tokens stay, m < n
-    if (m == 0) return;
-    const int* pt = p.page_table + (long long)b * p.max_pages;
-    auto key_of = [&](int i) -> uint32_t {  // of token sinks + i
-        if (i >= n) return 0;
-        int slot;
-        const int page = __ldg(pt + evict_page(p, p.sinks + i, slot));
-        if (page < 0 || page >= p.num_pages) {
-            atomicCAS(p.status, 0, kDevBadIndex);
-            return 0;
-        }
-        return score_key(__ldg(p.score + ((long long)page * p.Hkv + h) * p.page_size + slot));
-    };
-    uint32_t held[kHeld];
-    const bool fits = n <= kHeld * kSelectThreads;
-    if (fits) {
-#pragma unroll
-        for (int x = 0; x < kHeld; ++x) held[x] = key_of(x * kSelectThreads + tid);
-    }
-    const int rounds = (n + kSelectThreads - 1) / kSelectThreads;
-    // f(key, i) for all tokens in rounds of one per thread; every thread takes part in every round
-    auto each = [&](auto f) {
-        if (fits) {
-#pragma unroll
-            for (int x = 0; x < kHeld; ++x)
-                if (x < rounds) f(held[x], x * kSelectThreads + tid);
-        } else {
-            for (int x = 0; x < rounds; ++x) f(key_of(x * kSelectThreads + tid), x * kSelectThreads + tid);
-        }
-    };
+    s.end = K - p.recent, s.stop = s.len - p.recent;
+    for (int j = tid; j < p.sinks; j += nt) s.kept[j] = j;
+    for (int j = tid; j < p.recent; j += nt) s.kept[s.end + j] = s.stop + j;
+    s.m = s.end - p.sinks, s.n = s.stop - p.sinks;
+    return s.m > 0;
+}
 
-    // the m-th largest key, and how many of its equals stay
-    uint32_t found = 0;
-    int left = m;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        each([&](uint32_t key, int i) {
-            if (i < n && (shift == 24 || (key ^ found) >> (shift + 8) == 0)) atomicAdd(&hist[(key >> shift) & 255], 1);
-        });
-        __syncthreads();
-        if (tid < 32) {  // counts from the top: lane l has digits 255 - 8 l ... 248 - 8 l
-            int c[8], sum = 0;
+// Key of token sinks + i.
+__device__ __forceinline__ uint32_t key_of(const EvictParams& p, const SelectRow& s, int i) {
+    int slot;
+    const int page = __ldg(s.pt + evict_page(p, p.sinks + i, slot));
+    if (page < 0 || page >= p.num_pages) {
+        atomicCAS(p.status, 0, kDevBadIndex);
+        return 0;
+    }
+    return score_key(__ldg(p.score + ((long long)page * p.Hkv + s.h) * p.page_size + slot));
+}
+
+// The digit in which the count of the histogram from the top passes `left`, and how many of that digit are then left. Every
+// thread calls it; scratch: 34 words.
+template <int kBins>
+__device__ __forceinline__ void find_digit(const int* hist, int* scratch, int& digit, int& left) {
+    constexpr int kGroup = kBins / 32, kPer = kGroup / 32;  // bins of a group, of its lanes
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    for (int g = warp; g < 32; g += warps) {  // group g from the top
+        int c = 0;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) sum += c[x] = hist[255 - 8 * lane - x];
-            int upto = sum;
+        for (int x = 0; x < kPer; ++x) c += hist[kBins - (g + 1) * kGroup + 32 * x + lane];
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (lane == 0) scratch[g] = c;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        auto scan = [&](int x) {  // inclusive
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += y;
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
             }
-            int above = upto - sum;
+            return x;
+        };
+        const int c = scratch[lane], upto = scan(c);
+        const int g = __ffs(__ballot_sync(0xffffffffu, upto >= left)) - 1;
+        int above = __shfl_sync(0xffffffffu, upto - c, g);
+        const int top = kBins - g * kGroup - 1;  // lane l has its bins top - l kPer, ...
+        int mine[kPer], sum = 0;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                if (above < left && above + c[x] >= left) digit_at[0] = 255 - 8 * lane - x, digit_at[1] = left - above;
-                above += c[x];
-            }
+        for (int x = 0; x < kPer; ++x) sum += mine[x] = hist[top - lane * kPer - x];
+        above += scan(sum) - sum;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+            if (above < left && above + mine[x] >= left) scratch[32] = top - lane * kPer - x, scratch[33] = left - above;
+            above += mine[x];
+        }
+    }
+    __syncthreads();
+    digit = scratch[32];
+    left = scratch[33];
+}
+
+// Exclusive sum over the block's threads; every thread calls it.
+template <typename Sum>
+__device__ __forceinline__ Sum block_before(Sum mine, Sum* sums) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    Sum upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sum y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    Sum x = lane < warp && lane < warps ? sums[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return upto - mine + x;
+}
+
+__global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ EvictParams p) {
+    grid_dependents_launch();
+    extern __shared__ __align__(16) uint32_t keys[];
+    __shared__ int hist[2048], scratch[34], listed;
+    __shared__ uint32_t list[kList];
+    __shared__ unsigned long long sums[32];
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
+    SelectRow s;
+    if (!select_row(p, s)) return;
+    const int m = s.m, n = s.n;
+    auto clear = [&]() {
+        for (int i = tid; i < 2048; i += nt) hist[i] = 0;
+    };
+    clear();
+    if (tid == 0) listed = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = tid; i < n; i += nt) {
+        const uint32_t k = key_of(p, s, i);
+        keys[i] = k;
+        atomicAdd(&hist[k >> 21], 1);
+    }
+    __syncthreads();
+    // the m-th largest key, and how many of its equals stay
+    int digit, left = m;
+    find_digit<2048>(hist, scratch, digit, left);
+    uint32_t found = (uint32_t)digit << 21;
+    clear();
+    for (int i = tid; i - lane < n; i += nt) {
+        const bool in = i < n && (keys[i] ^ found) >> 21 == 0;
+        const uint32_t which = __ballot_sync(0xffffffffu, in);
+        if (which == 0) continue;
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&listed, __popc(which));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(which & ((1u << lane) - 1));
+        if (in && at < kList) list[at] = keys[i];
+    }
+    __syncthreads();
+    const bool all = listed > kList;  // (more than the list holds: through all keys again)
+    const uint32_t* from = all ? keys : list;
+    const int count = all ? n : listed;
+    for (int i = tid; i < count; i += nt)
+        if ((from[i] ^ found) >> 21 == 0) atomicAdd(&hist[from[i] >> 10 & 2047], 1);
+    __syncthreads();
+    find_digit<2048>(hist, scratch, digit, left);
+    found |= (uint32_t)digit << 10;
+    clear();
+    __syncthreads();
+    for (int i = tid; i < count; i += nt)
+        if ((from[i] ^ found) >> 10 == 0) atomicAdd(&hist[from[i] & 1023], 1);
+    __syncthreads();
+    find_digit<1024>(hist, scratch, digit, left);
+    found |= (uint32_t)digit;
+
+    // neighbouring tokens of this thread; an odd number of them, so that the threads of a warp read different banks
+    const int each = (n + nt - 1) / nt | 1, first = min(n, tid * each), behind = min(n, first + each);
+    int equals = 0;
+    for (int i = first; i < behind; ++i) equals += keys[i] == found;
+    int before = (int)block_before<unsigned long long>(equals, sums);
+    static_assert(((kSelectKeys + 1023) / 1024 | 1) <= 64, "a bit for each token of a thread");
+    unsigned long long stays = 0;
+    int holes = 0, tails = 0;
+    for (int i = first; i < behind; ++i) {
+        const uint32_t k = keys[i];
+        const bool stay = k > found || (k == found && before++ < left);
+        stays |= (unsigned long long)stay << (i - first);
+        holes += i < m && !stay;
+        tails += i >= m && stay;
+    }
+    const unsigned long long ahead = block_before(((unsigned long long)tails << 32) + holes, sums);
+    // (all keys have been read) word i < m: i, or the number of the hole; the tails behind them, as many as there are holes
+    int hole = (int)(uint32_t)ahead, tail = (int)(ahead >> 32);
+    for (int i = first; i < behind; ++i) {
+        const bool stay = stays >> (i - first) & 1;
+        if (i < m)
+            keys[i] = stay ? (uint32_t)i : 0x80000000u | (uint32_t)hole++;
+        else if (stay)
+            keys[m + tail++] = (uint32_t)i;
+    }
+    __syncthreads();
+    for (int i = tid; i < m; i += nt) {
+        const uint32_t x = keys[i];
+        s.kept[p.sinks + i] = p.sinks + (int)(x & 0x80000000u ? keys[m + (x & 0x7FFFFFFFu)] : x);
+    }
+}
+
+// The same from more tokens: the keys are read again for every step, and the tokens numbered in rounds of one per thread.
+__global__ void __launch_bounds__(kLongThreads, 1) select_long_kernel(const __grid_constant__ EvictParams p) {
+    grid_dependents_launch();
+    __shared__ int hist[2048], scratch[34], sums[32], place[kPairs];
+    const int tid = threadIdx.x, lane = tid & 31;
+    SelectRow s;
+    if (!select_row(p, s)) return;
+    const int m = s.m, n = s.n;
+    uint32_t found = 0;
+    int left = m;
+    for (int shift = 21;; shift = shift == 21 ? 10 : 0) {  // digits of 11, 11 and 10 bits
+        for (int i = tid; i < 2048; i += kLongThreads) hist[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kLongThreads) {
+            const uint32_t k = key_of(p, s, i);
+            if (shift == 21 || (k ^ found) >> (shift == 10 ? 21 : 10) == 0) atomicAdd(&hist[shift > 0 ? k >> shift & 2047 : k & 1023], 1);
         }
         __syncthreads();
-        found |= (uint32_t)digit_at[0] << shift;
-        left = digit_at[1];
+        int digit;
+        if (shift > 0)
+            find_digit<2048>(hist, scratch, digit, left);
+        else
+            find_digit<1024>(hist, scratch, digit, left);
+        found |= (uint32_t)digit << shift;
+        if (shift == 0) break;
+        __syncthreads();
     }
-
-    // In token order: equals of that key stay while their number is below `left`; then the holes and the kept tokens behind
-    // `end` are numbered. All of a round's warps are numbered at once.
-    uint32_t stays = 0;  // bit x: token x of this thread (when held); else worked out again below
-    int equals = 0;      // before this round
-    int holes = 0, tails = 0;
-    const uint32_t below = (1u << lane) - 1;
-    // numbers of a round: equals of this key before this thread
-    auto stay = [&](uint32_t key, int i) {
-        const bool equal = i < n && key == found;
-        const uint32_t ballot = __ballot_sync(0xffffffffu, equal);
-        int total;
-        const int before = equals + warps_before(__popc(ballot), sums, total) + __popc(ballot & below);
-        equals += total;
-        return i < n && (key > found || (equal && before < left));
-    };
     // holes in turn, kPairs at a time
-    for (int first = 0;; first += kPairs) {
-        equals = holes = tails = 0;
-        int x = 0;
-        each([&](uint32_t key, int i) {
-            bool s;
-            if (first == 0 || !fits) {
-                s = stay(key, i);
-                if (fits) stays |= (uint32_t)s << x;
-            } else {
-                s = stays >> x & 1;
-            }
-            ++x;
-            const int tok = p.sinks + i;
-            const bool hole = i < n && tok < end && !s, tail = i < n && tok >= end && s;
-            if (i < n && tok < end && s && first == 0) kept[tok] = tok;
+    const uint32_t below = (1u << lane) - 1;
+    for (int first = 0, holes;; first += kPairs) {
+        int equals = 0, tails = 0;
+        holes = 0;
+        for (int base = 0; base < n; base += kLongThreads) {
+            const int i = base + tid;
+            const uint32_t key = i < n ? key_of(p, s, i) : 0;
+            const bool equal = i < n && key == found;
             int total;
+            const uint32_t be = __ballot_sync(0xffffffffu, equal);
+            const int number = equals + warps_before(__popc(be), sums, total) + __popc(be & below);
+            equals += total;
+            const bool stay = i < n && (key > found || (equal && number < left));
+            const bool hole = i < m && !stay, tail = i >= m && stay;
+            if (i < m && stay && first == 0) s.kept[p.sinks + i] = p.sinks + i;
             const uint32_t bh = __ballot_sync(0xffffffffu, hole), bt = __ballot_sync(0xffffffffu, tail);
             const int before = warps_before(__popc(bh) | __popc(bt) << 16, sums, total);
             const int nh = holes + (before & 0xFFFF) + __popc(bh & below) - first, ntl = tails + (before >> 16) + __popc(bt & below) - first;
             holes += total & 0xFFFF;
             tails += total >> 16;
-            // (all holes come before the first token behind `end`, but for those of the same round)
-            if (hole && nh >= 0 && nh < kPairs) place[nh] = tok;
+            // (all holes come before the first token behind them, but for those of the same round)
+            if (hole && nh >= 0 && nh < kPairs) place[nh] = p.sinks + i;
             __syncthreads();
-            if (tail && ntl >= 0 && ntl < kPairs) kept[place[ntl]] = tok;
-        });
+            if (tail && ntl >= 0 && ntl < kPairs) s.kept[place[ntl]] = p.sinks + i;
+        }
         if (holes <= first + kPairs) break;
         __syncthreads();
     }
 }
 
-// One 16-byte column of K and V rows per lane; kRun rows per thread and run.
-constexpr int kCompactThreads = 512, kRun = 8;
+// 16-byte columns of K and V rows, one per lane; kRun rows per thread and run.
+constexpr int kCompactThreads = 512, kRun = 8, kMoves = 2048;
 
-__global__ void __launch_bounds__(kCompactThreads) compact_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const __grid_constant__ EvictParams p) {
+    __shared__ int src[kMoves], dst[kMoves], sums[32];  // cache rows of the moves listed
+    grid_dependency_wait();                             // (launched as a programmatic dependent of what is before it)
     const int b = (int)(blockIdx.x / (unsigned)p.Hkv), h = (int)(blockIdx.x % (unsigned)p.Hkv);
     const int n = min(__ldg(p.seqlens + b), p.budget), limit = p.max_pages * p.page_size;
     const int* kept = p.kept + (long long)blockIdx.x * p.budget;
     const int* pt = p.page_table + (long long)b * p.max_pages;
-    const int each = p.row_bytes / 16;                        // columns of K, and of V
-    const int lanes = p.columns, col = blockIdx.y * lanes + threadIdx.x % lanes;  // 2 each: the score
-    const int rows = kCompactThreads / lanes, row0 = threadIdx.x / lanes;
-    const bool active = row0 < rows && col < 2 * each + (p.score ? 1 : 0);
-    uint8_t* cache = p.cache[col >= each && col < 2 * each];
-    const int offset = 16 * (col >= each ? col - each : col);
-    // address of token tok's 16 bytes (the score: 4), nullptr for a bad page
-    auto at = [&](int tok) -> uint8_t* {
+    const int each = p.row_bytes / 16, tid = threadIdx.x, lane = tid & 31;  // columns of K, and of V
+    const int lanes = p.columns, col = blockIdx.y * lanes + tid % lanes;
+    const int rows = kCompactThreads / lanes, row0 = tid / lanes;
+    const bool active = row0 < rows && col < 2 * each;
+    uint8_t* cache = p.cache[col >= each] + (long long)h * p.row_bytes + 16 * (col >= each ? col - each : col);
+    const long long row_bytes = (long long)p.Hkv * p.row_bytes;
+    auto row_of = [&](int tok) {  // -1: a page out of range
         int slot;
         const int page = __ldg(pt + evict_page(p, tok, slot));
-        if (page < 0 || page >= p.num_pages) {
-            atomicCAS(p.status, 0, kDevBadIndex);
-            return nullptr;
-        }
-        if (col == 2 * each) return reinterpret_cast<uint8_t*>(p.score + ((long long)page * p.Hkv + h) * p.page_size + slot);
-        return cache + (((long long)page * p.page_size + slot) * p.Hkv + h) * p.row_bytes + offset;
+        if (page >= 0 && page < p.num_pages) return page * p.page_size + slot;
+        atomicCAS(p.status, 0, kDevBadIndex);
+        return -1;
     };
-    for (int j0 = 0; j0 < n; j0 += rows * kRun) {
-        uint4 v[kRun];
-        uint8_t* to[kRun];
+    auto sum_of = [&](int row) {  // the score of a cache row
+        const int page = row / p.page_size;
+        return p.score + ((long long)page * p.Hkv + h) * p.page_size + (row - page * p.page_size);
+    };
+    for (int j0 = 0; j0 < n; j0 += kMoves) {
+        // the slots from j0 on that get another row
+        int from[kMoves / kCompactThreads], to[kMoves / kCompactThreads];
+        int listed = 0;
 #pragma unroll
-        for (int x = 0; x < kRun; ++x) {
-            const int j = j0 + x * rows + row0;
-            to[x] = nullptr;
-            if (!active || j >= n) continue;
-            const int src = __ldg(kept + j);
-            if (src == j || src == -1) continue;
-            if (src < j || src >= limit) {
+        for (int x = 0; x < kMoves / kCompactThreads; ++x) {
+            const int j = j0 + x * kCompactThreads + tid, tok = j < n ? __ldg(kept + j) : -1;
+            from[x] = to[x] = -1;
+            if (tok == -1 || tok == j) continue;
+            if (tok < j || tok >= limit) {
                 atomicCAS(p.status, 0, kDevBadIndex);
                 continue;
             }
-            const uint8_t* from = at(src);
-            if (!from) continue;
-            to[x] = at(j);
-            if (col == 2 * each)
-                v[x].x = *reinterpret_cast<const uint32_t*>(from);
-            else
-                v[x] = *reinterpret_cast<const uint4*>(from);
+            from[x] = row_of(tok);
+            to[x] = row_of(j);
         }
-        __syncthreads();  // the run is read before any of its slots is written
 #pragma unroll
-        for (int x = 0; x < kRun; ++x) {
-            if (!to[x]) continue;
-            if (col == 2 * each)
-                *reinterpret_cast<uint32_t*>(to[x]) = v[x].x;
-            else
-                *reinterpret_cast<uint4*>(to[x]) = v[x];
+        for (int x = 0; x < kMoves / kCompactThreads; ++x) {
+            const bool move = from[x] >= 0 && to[x] >= 0;
+            const uint32_t which = __ballot_sync(0xffffffffu, move);
+            int total;
+            const int at = listed + warps_before(__popc(which), sums, total) + __popc(which & ((1u << lane) - 1));
+            if (move) src[at] = from[x], dst[at] = to[x];
+            listed += total;
         }
+        __syncthreads();
+        for (int i0 = 0; i0 < listed; i0 += rows * kRun) {
+            uint4 v[kRun];
+#pragma unroll
+            for (int x = 0; x < kRun; ++x) {
+                const int i = i0 + x * rows + row0;
+                if (active && i < listed) v[x] = *reinterpret_cast<const uint4*>(cache + src[i] * row_bytes);
+            }
+            // (the scores with the first columns, a thread per row)
+            const int run = min(rows * kRun, listed - i0);
+            constexpr int kSums = kRun / 2;  // (two columns at least: no more rows than that for a thread)
+            float sum[kSums];
+            if (p.score && blockIdx.y == 0) {
+#pragma unroll
+                for (int x = 0; x < kSums; ++x)
+                    if (x * kCompactThreads + tid < run) sum[x] = *sum_of(src[i0 + x * kCompactThreads + tid]);
+            }
+            __syncthreads();  // the run is read before any of its slots is written
+#pragma unroll
+            for (int x = 0; x < kRun; ++x) {
+                const int i = i0 + x * rows + row0;
+                if (active && i < listed) *reinterpret_cast<uint4*>(cache + dst[i] * row_bytes) = v[x];
+            }
+            if (p.score && blockIdx.y == 0) {
+#pragma unroll
+                for (int x = 0; x < kSums; ++x)
+                    if (x * kCompactThreads + tid < run) *sum_of(dst[i0 + x * kCompactThreads + tid]) = sum[x];
+            }
+        }
+        __syncthreads();  // the list is done with
     }
 }
 
@@ -304,7 +446,21 @@ extern "C" attn_status_t attn_kv_select_paged(const float* score, const int* pag
     p.kept = kept;
     p.new_seqlens = new_seqlens;
     p.sinks = sinks, p.recent = recent;
-    const cudaError_t e = launch_kernel(select_kernel, dim3((unsigned)(B * Hkv)), kSelectThreads, 0, static_cast<cudaStream_t>(stream), {}, p);
+    // tokens to choose from at most
+    const long long most = (long long)max_pages_per_seq * page_size - sinks - recent;
+    const dim3 grid((unsigned)(B * Hkv));
+    cudaError_t e;
+    if (most > kSelectKeys) {
+        e = launch_kernel(select_long_kernel, grid, kLongThreads, 0, static_cast<cudaStream_t>(stream), {}, p);
+    } else {
+        // a thread for 16 tokens: the blocks of many short rows share the SMs, long rows have all threads of one
+        unsigned threads = 128;
+        while (threads < 1024 && threads * 16 < most) threads *= 2;
+        static std::atomic<bool> attr_set[kMaxAttrDevices];
+        e = ensure_smem_attr(select_kernel, kSelectKeys * 4, attr_set);
+        if (e == cudaSuccess)
+            e = launch_kernel(select_kernel, grid, threads, (size_t)(most > 0 ? most : 0) * 4, static_cast<cudaStream_t>(stream), {}, p);
+    }
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -331,11 +487,13 @@ extern "C" attn_status_t attn_kv_compact_paged(void* k_cache, void* v_cache, flo
     p.seqlens = new_seqlens;
     p.page_table = page_table;
     p.row_bytes = kv_format == ATTN_KV_BF16 ? 2 * d : d;
-    // all columns of a row in one block, fewer (but whole 32-byte sectors) while there are SMs left
-    const int all = p.row_bytes / 8 + (score ? 1 : 0);
+    // All columns of a row in one block; fewer, but whole 32-byte sectors, until there are three blocks for every SM.
+    const int all = p.row_bytes / 8;
     p.columns = all;
-    while (p.columns > 2 && (long long)B * Hkv * ((all + p.columns - 1) / p.columns) * 2 <= num_sms) p.columns = (p.columns + 3) / 4 * 2;
+    while (p.columns > 2 && (long long)B * Hkv * ((all + p.columns - 1) / p.columns) * 2 <= 3LL * num_sms) p.columns = (p.columns + 3) / 4 * 2;
     const unsigned parts = (unsigned)((all + p.columns - 1) / p.columns);
-    const cudaError_t e = launch_kernel(compact_kernel, dim3((unsigned)(B * Hkv), parts), kCompactThreads, 0, static_cast<cudaStream_t>(stream), {}, p);
+    LaunchMode mode;
+    mode.dependent = true;
+    const cudaError_t e = launch_kernel(compact_kernel, dim3((unsigned)(B * Hkv), parts), kCompactThreads, 0, static_cast<cudaStream_t>(stream), mode, p);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
