@@ -4,11 +4,11 @@
 // Selection, one block per (sequence, kv head). Of the tokens between the first `sinks` and the last `recent` the m with the
 // largest scores stay, ties to the earlier token. Scores become unsigned keys of the same order, held in shared memory; the m-th largest
 // is found by digits of 11, 11 and 10 bits from the top: a histogram of the keys that share the digits found so far, the digit in
-// which the count from above passes m. After the first digit few keys are left in general, which go to a list, so that only the
-// first histogram is of all keys. Then a thread takes neighbouring tokens, so that one scan over the block each numbers the equals of
-// the m-th key, and the holes and tails: a kept token below end = budget - recent stays in its slot, the holes there take in order
-// the kept tokens behind it. Bounded by latency: the loads and a dozen block-wide steps. (With keys in registers, four digits of 8
-// bits, and a numbering per 1024 tokens: 64 x 8 rows of 4100-4352 tokens ~100 us.)
+// which the count from above passes m. Then a warp's vote per 32 tokens says which stay, in one word. Of the words' counts one
+// scan over the block numbers the holes and the tails: a kept token below end = budget - recent stays in its slot, the holes there take in
+// order the kept tokens behind it. Bounded by latency and instructions: the loads, a dozen block-wide steps, and per 32 tokens about as many
+// instructions. (With neighbouring tokens numbered by one thread each: 64 x 8 rows of 4100-4352 tokens 23 us, 16 x 8 of up to
+// 32768 29 us; with keys in registers, four digits of 8 bits, and a numbering per 1024 tokens about 100 us.)
 //
 // Compaction: row kept[j] -> j with kept[j] >= j. A block lists the slots that get another row, in ascending order, with the
 // cache rows of both, and moves them in runs: it loads the rows of a run, then stores them. Every row that it reads later belongs to a slot
@@ -28,8 +28,7 @@ namespace {
 
 constexpr int kLongThreads = 1024;   // selection from more tokens than the shared memory holds
 constexpr int kPairs = 4096;         // there: holes paired with tokens at a time
-constexpr int kSelectKeys = 50176;   // tokens of a row whose keys the shared memory holds: 196 KB, and 17 KB besides
-constexpr int kList = 2048;          // keys with the same first digit
+constexpr int kSelectKeys = 49152;   // tokens of a row whose keys the shared memory holds: 210 KB with 12 bytes per 32, and 9 KB besides
 
 struct EvictParams {
     float* score;           // [num_pages, Hkv, page_size]
@@ -39,6 +38,7 @@ struct EvictParams {
     int* kept;              // [B, Hkv, budget]
     int* new_seqlens;       // [B]
     int B, Hkv, page_size, max_pages, num_pages, budget, sinks, recent;
+    int most;                // selection: tokens to choose from at most, rounded up to a multiple of 32
     int row_bytes, columns;  // of one kv head; 16-byte columns of K and V that a block moves
     unsigned int ps_magic;  // tok / page_size by multiplication, as in DecodeParams
     int ps_shift;
@@ -114,10 +114,10 @@ __device__ __forceinline__ uint32_t key_of(const EvictParams& p, const SelectRow
     return score_key(__ldg(p.score + ((long long)page * p.Hkv + s.h) * p.page_size + slot));
 }
 
-// The digit in which the count of the histogram from the top passes `left`, and how many of that digit are then left. Every
-// thread calls it; scratch: 34 words.
+// The digit in which the count of the histogram from the top passes `left`, how many of that digit are then left, and of how many. Every
+// thread calls it; scratch: 35 words.
 template <int kBins>
-__device__ __forceinline__ void find_digit(const int* hist, int* scratch, int& digit, int& left) {
+__device__ __forceinline__ void find_digit(const int* hist, int* scratch, int& digit, int& left, int& of) {
     constexpr int kGroup = kBins / 32, kPer = kGroup / 32;  // bins of a group, of its lanes
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     for (int g = warp; g < 32; g += warps) {  // group g from the top
@@ -147,13 +147,14 @@ __device__ __forceinline__ void find_digit(const int* hist, int* scratch, int& d
         above += scan(sum) - sum;
 #pragma unroll
         for (int x = 0; x < kPer; ++x) {
-            if (above < left && above + mine[x] >= left) scratch[32] = top - lane * kPer - x, scratch[33] = left - above;
+            if (above < left && above + mine[x] >= left) scratch[32] = top - lane * kPer - x, scratch[33] = left - above, scratch[34] = mine[x];
             above += mine[x];
         }
     }
     __syncthreads();
     digit = scratch[32];
     left = scratch[33];
+    of = scratch[34];
 }
 
 // Exclusive sum over the block's threads; every thread calls it.
@@ -175,96 +176,146 @@ __device__ __forceinline__ Sum block_before(Sum mine, Sum* sums) {
     return upto - mine + x;
 }
 
+// QUADS: page_size is a multiple of 4 and score 16-byte aligned.
+template <bool QUADS>
 __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ EvictParams p) {
     grid_dependents_launch();
     extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ int hist[2048], scratch[34], listed;
-    __shared__ uint32_t list[kList];
+    __shared__ int hist[2048], scratch[35];
     __shared__ unsigned long long sums[32];
-    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
-    SelectRow s;
-    if (!select_row(p, s)) return;
-    const int m = s.m, n = s.n;
+    // behind the keys, per 32 tokens: holes and tails before them, which of them stay
+    uint2* ahead = reinterpret_cast<uint2*>(keys + p.most);
+    uint32_t* bits = reinterpret_cast<uint32_t*>(ahead + p.most / 32);
+    static_assert(2048 >= kSelectKeys / 32, "the histogram also takes the equals among 32 tokens each");
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
     auto clear = [&]() {
         for (int i = tid; i < 2048; i += nt) hist[i] = 0;
     };
     clear();
-    if (tid == 0) listed = 0;
+    SelectRow s;
+    if (!select_row(p, s)) return;
+    const int m = s.m, n = s.n;
     __syncthreads();
+    if constexpr (QUADS) {
+        // tokens 4 q .. 4 q + 3, on one page
+#pragma unroll 8
+        for (int q = (p.sinks >> 2) + tid; 4 * q < s.stop; q += nt) {
+            int slot;
+            const int page = __ldg(s.pt + evict_page(p, 4 * q, slot));
+            const bool bad = page < 0 || page >= p.num_pages;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (!bad) x = __ldg(reinterpret_cast<const float4*>(p.score + ((long long)page * p.Hkv + s.h) * p.page_size + slot));
+            const float f[4] = {x.x, x.y, x.z, x.w};
+            if (bad) atomicCAS(p.status, 0, kDevBadIndex);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 4 * q + e - p.sinks;
+                if (i < 0 || i >= n) continue;
+                const uint32_t k = bad ? 0 : score_key(f[e]);
+                keys[i] = k;
+                atomicAdd(&hist[k >> 21], 1);
+            }
+        }
+    } else {
 #pragma unroll 4
-    for (int i = tid; i < n; i += nt) {
-        const uint32_t k = key_of(p, s, i);
-        keys[i] = k;
-        atomicAdd(&hist[k >> 21], 1);
+        for (int i = tid; i < n; i += nt) {
+            const uint32_t k = key_of(p, s, i);
+            keys[i] = k;
+            atomicAdd(&hist[k >> 21], 1);
+        }
     }
     __syncthreads();
     // the m-th largest key, and how many of its equals stay
-    int digit, left = m;
-    find_digit<2048>(hist, scratch, digit, left);
+    int digit, left = m, of;
+    find_digit<2048>(hist, scratch, digit, left, of);
     uint32_t found = (uint32_t)digit << 21;
     clear();
-    for (int i = tid; i - lane < n; i += nt) {
-        const bool in = i < n && (keys[i] ^ found) >> 21 == 0;
-        const uint32_t which = __ballot_sync(0xffffffffu, in);
-        if (which == 0) continue;
-        int at = 0;
-        if (lane == 0) at = atomicAdd(&listed, __popc(which));
-        at = __shfl_sync(0xffffffffu, at, 0) + __popc(which & ((1u << lane) - 1));
-        if (in && at < kList) list[at] = keys[i];
-    }
     __syncthreads();
-    const bool all = listed > kList;  // (more than the list holds: through all keys again)
-    const uint32_t* from = all ? keys : list;
-    const int count = all ? n : listed;
-    for (int i = tid; i < count; i += nt)
-        if ((from[i] ^ found) >> 21 == 0) atomicAdd(&hist[from[i] >> 10 & 2047], 1);
+    // f(word, its lane's key, is there one) for 32 tokens each, loaded ahead of it
+    const int words = (n + 31) >> 5;
+    auto each_word = [&](int first, auto f) {
+        constexpr int kAhead = 8;
+        for (int w = first + warp; w < words; w += kAhead * warps) {
+            uint32_t k[kAhead];
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+                const int i = 32 * (w + x * warps) + lane;
+                k[x] = i < n ? keys[i] : 0;
+            }
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x)
+                if (w + x * warps < words) f(w + x * warps, k[x], 32 * (w + x * warps) + lane < n);
+        }
+    };
+    each_word(0, [&](int, uint32_t key, bool in) {
+        if (in && (key ^ found) >> 21 == 0) atomicAdd(&hist[key >> 10 & 2047], 1);
+    });
     __syncthreads();
-    find_digit<2048>(hist, scratch, digit, left);
+    find_digit<2048>(hist, scratch, digit, left, of);
     found |= (uint32_t)digit << 10;
     clear();
     __syncthreads();
-    for (int i = tid; i < count; i += nt)
-        if ((from[i] ^ found) >> 10 == 0) atomicAdd(&hist[from[i] & 1023], 1);
+    each_word(0, [&](int, uint32_t key, bool in) {
+        if (in && (key ^ found) >> 10 == 0) atomicAdd(&hist[key & 1023], 1);
+    });
     __syncthreads();
-    find_digit<1024>(hist, scratch, digit, left);
+    find_digit<1024>(hist, scratch, digit, left, of);
     found |= (uint32_t)digit;
 
-    // neighbouring tokens of this thread; an odd number of them, so that the threads of a warp read different banks
-    const int each = (n + nt - 1) / nt | 1, first = min(n, tid * each), behind = min(n, first + each);
-    int equals = 0;
-    for (int i = first; i < behind; ++i) equals += keys[i] == found;
-    int before = (int)block_before<unsigned long long>(equals, sums);
-    static_assert(((kSelectKeys + 1023) / 1024 | 1) <= 64, "a bit for each token of a thread");
-    unsigned long long stays = 0;
-    int holes = 0, tails = 0;
-    for (int i = first; i < behind; ++i) {
-        const uint32_t k = keys[i];
-        const bool stay = k > found || (k == found && before++ < left);
-        stays |= (unsigned long long)stay << (i - first);
-        holes += i < m && !stay;
-        tails += i >= m && stay;
+    // which of 32 tokens stay; when not all equals do, those apart
+    const bool ties = left < of;
+    each_word(0, [&](int w, uint32_t key, bool in) {
+        const uint32_t stay = __ballot_sync(0xffffffffu, in && (ties ? key > found : key >= found));
+        if (lane == 0) bits[w] = stay;
+        if (ties) {
+            const uint32_t equal = __ballot_sync(0xffffffffu, in && key == found);
+            if (lane == 0) hist[w] = (int)equal;
+        }
+    });
+    __syncthreads();
+    // neighbouring words of this thread
+    const int each = (words + nt - 1) / nt, w0 = min(words, tid * each), w1 = min(words, w0 + each);
+    if (ties) {
+        int equals = 0;
+        for (int w = w0; w < w1; ++w) equals += __popc(hist[w]);
+        int room = left - (int)block_before<unsigned long long>(equals, sums);  // equals that may stay from here on
+        for (int w = w0; w < w1 && room > 0; ++w) {
+            uint32_t equal = (uint32_t)hist[w];
+            for (; equal && room > 0; equal &= equal - 1, --room) bits[w] |= equal & -equal;
+        }
+        __syncthreads();
     }
-    const unsigned long long ahead = block_before(((unsigned long long)tails << 32) + holes, sums);
-    // (all keys have been read) word i < m: i, or the number of the hole; the tails behind them, as many as there are holes
-    int hole = (int)(uint32_t)ahead, tail = (int)(ahead >> 32);
-    for (int i = first; i < behind; ++i) {
-        const bool stay = stays >> (i - first) & 1;
-        if (i < m)
-            keys[i] = stay ? (uint32_t)i : 0x80000000u | (uint32_t)hole++;
-        else if (stay)
-            keys[m + tail++] = (uint32_t)i;
+    // bits of word w that are tokens below m; behind them
+    auto below_m = [&](int w) { return 32 * w + 32 <= m ? ~0u : 32 * w >= m ? 0u : (1u << (m - 32 * w)) - 1; };
+    unsigned holes = 0, tails = 0;
+    for (int w = w0; w < w1; ++w) holes += __popc(~bits[w] & below_m(w)), tails += __popc(bits[w] & ~below_m(w));
+    const unsigned long long before = block_before(((unsigned long long)tails << 32) + holes, sums);
+    uint2 upto = make_uint2((unsigned)before, (unsigned)(before >> 32));
+    for (int w = w0; w < w1; ++w) {
+        ahead[w] = upto;
+        upto.x += __popc(~bits[w] & below_m(w)), upto.y += __popc(bits[w] & ~below_m(w));
     }
     __syncthreads();
-    for (int i = tid; i < m; i += nt) {
-        const uint32_t x = keys[i];
-        s.kept[p.sinks + i] = p.sinks + (int)(x & 0x80000000u ? keys[m + (x & 0x7FFFFFFFu)] : x);
+    // (the keys are done with) the tails in their order, then every slot
+    const uint32_t lower = (1u << lane) - 1;
+#pragma unroll 4
+    for (int w = (m >> 5) + warp; w < words; w += warps) {
+        const uint32_t tail = bits[w] & ~below_m(w);
+        if (tail >> lane & 1) keys[ahead[w].y + __popc(tail & lower)] = (uint32_t)(32 * w + lane);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int w = warp; 32 * w < m; w += warps) {
+        const uint32_t hole = ~bits[w] & below_m(w);
+        const int i = 32 * w + lane;
+        if (i < m) s.kept[p.sinks + i] = p.sinks + (hole >> lane & 1 ? (int)keys[ahead[w].x + __popc(hole & lower)] : i);
     }
 }
 
 // The same from more tokens: the keys are read again for every step, and the tokens numbered in rounds of one per thread.
 __global__ void __launch_bounds__(kLongThreads, 1) select_long_kernel(const __grid_constant__ EvictParams p) {
     grid_dependents_launch();
-    __shared__ int hist[2048], scratch[34], sums[32], place[kPairs];
+    __shared__ int hist[2048], scratch[35], sums[32], place[kPairs];
     const int tid = threadIdx.x, lane = tid & 31;
     SelectRow s;
     if (!select_row(p, s)) return;
@@ -279,11 +330,11 @@ __global__ void __launch_bounds__(kLongThreads, 1) select_long_kernel(const __gr
             if (shift == 21 || (k ^ found) >> (shift == 10 ? 21 : 10) == 0) atomicAdd(&hist[shift > 0 ? k >> shift & 2047 : k & 1023], 1);
         }
         __syncthreads();
-        int digit;
+        int digit, of;
         if (shift > 0)
-            find_digit<2048>(hist, scratch, digit, left);
+            find_digit<2048>(hist, scratch, digit, left, of);
         else
-            find_digit<1024>(hist, scratch, digit, left);
+            find_digit<1024>(hist, scratch, digit, left, of);
         found |= (uint32_t)digit << shift;
         if (shift == 0) break;
         __syncthreads();
@@ -320,16 +371,18 @@ __global__ void __launch_bounds__(kLongThreads, 1) select_long_kernel(const __gr
 }
 
 // 16-byte columns of K and V rows, one per lane; kRun rows per thread and run.
-constexpr int kCompactThreads = 512, kRun = 8, kMoves = 2048;
+constexpr int kCompactThreads = 512, kRun = 8, kMoves = 4096, kLook = kMoves / kCompactThreads;
 
 __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ int src[kMoves], dst[kMoves], sums[32];  // cache rows of the moves listed
+    __shared__ int src[kMoves], dst[kMoves];  // cache rows of the moves listed
+    __shared__ unsigned sums[32];
+    __shared__ int total;
     grid_dependency_wait();                             // (launched as a programmatic dependent of what is before it)
     const int b = (int)(blockIdx.x / (unsigned)p.Hkv), h = (int)(blockIdx.x % (unsigned)p.Hkv);
     const int n = min(__ldg(p.seqlens + b), p.budget), limit = p.max_pages * p.page_size;
     const int* kept = p.kept + (long long)blockIdx.x * p.budget;
     const int* pt = p.page_table + (long long)b * p.max_pages;
-    const int each = p.row_bytes / 16, tid = threadIdx.x, lane = tid & 31;  // columns of K, and of V
+    const int each = p.row_bytes / 16, tid = threadIdx.x;  // columns of K, and of V
     const int lanes = p.columns, col = blockIdx.y * lanes + tid % lanes;
     const int rows = kCompactThreads / lanes, row0 = tid / lanes;
     const bool active = row0 < rows && col < 2 * each;
@@ -347,29 +400,30 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const __gri
         return p.score + ((long long)page * p.Hkv + h) * p.page_size + (row - page * p.page_size);
     };
     for (int j0 = 0; j0 < n; j0 += kMoves) {
-        // the slots from j0 on that get another row
-        int from[kMoves / kCompactThreads], to[kMoves / kCompactThreads];
-        int listed = 0;
+        // the slots from j0 on that get another row; neighbouring ones of this thread
+        const int first = j0 + tid * kLook;
+        int tok[kLook];
+        unsigned moves = 0;
 #pragma unroll
-        for (int x = 0; x < kMoves / kCompactThreads; ++x) {
-            const int j = j0 + x * kCompactThreads + tid, tok = j < n ? __ldg(kept + j) : -1;
-            from[x] = to[x] = -1;
-            if (tok == -1 || tok == j) continue;
-            if (tok < j || tok >= limit) {
+        for (int x = 0; x < kLook; ++x) tok[x] = first + x < n ? __ldg(kept + first + x) : -1;
+#pragma unroll
+        for (int x = 0; x < kLook; ++x) {
+            if (tok[x] != -1 && (tok[x] < first + x || tok[x] >= limit)) {
                 atomicCAS(p.status, 0, kDevBadIndex);
-                continue;
+                tok[x] = -1;
             }
-            from[x] = row_of(tok);
-            to[x] = row_of(j);
+            moves += tok[x] > first + x;
         }
+        unsigned at = block_before(moves, sums);
+        if (tid == kCompactThreads - 1) total = (int)(at + moves);
 #pragma unroll
-        for (int x = 0; x < kMoves / kCompactThreads; ++x) {
-            const bool move = from[x] >= 0 && to[x] >= 0;
-            const uint32_t which = __ballot_sync(0xffffffffu, move);
-            int total;
-            const int at = listed + warps_before(__popc(which), sums, total) + __popc(which & ((1u << lane) - 1));
-            if (move) src[at] = from[x], dst[at] = to[x];
-            listed += total;
+        for (int x = 0; x < kLook; ++x)
+            if (tok[x] > first + x) src[at] = tok[x], dst[at++] = first + x;
+        __syncthreads();
+        const int listed = total;
+        for (int i = tid; i < listed; i += kCompactThreads) {
+            const int from = row_of(src[i]), to = row_of(dst[i]);
+            src[i] = to < 0 ? -1 : from, dst[i] = to;
         }
         __syncthreads();
         for (int i0 = 0; i0 < listed; i0 += rows * kRun) {
@@ -377,28 +431,28 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const __gri
 #pragma unroll
             for (int x = 0; x < kRun; ++x) {
                 const int i = i0 + x * rows + row0;
-                if (active && i < listed) v[x] = *reinterpret_cast<const uint4*>(cache + src[i] * row_bytes);
+                if (active && i < listed && src[i] >= 0) v[x] = *reinterpret_cast<const uint4*>(cache + src[i] * row_bytes);
             }
             // (the scores with the first columns, a thread per row)
             const int run = min(rows * kRun, listed - i0);
             constexpr int kSums = kRun / 2;  // (two columns at least: no more rows than that for a thread)
             float sum[kSums];
-            if (p.score && blockIdx.y == 0) {
+            auto scores = [&](auto f) {
+                if (!p.score || blockIdx.y != 0) return;
 #pragma unroll
-                for (int x = 0; x < kSums; ++x)
-                    if (x * kCompactThreads + tid < run) sum[x] = *sum_of(src[i0 + x * kCompactThreads + tid]);
-            }
+                for (int x = 0; x < kSums; ++x) {
+                    const int i = i0 + x * kCompactThreads + tid;
+                    if (x * kCompactThreads + tid < run && src[i] >= 0) f(sum[x], i);
+                }
+            };
+            scores([&](float& f, int i) { f = *sum_of(src[i]); });
             __syncthreads();  // the run is read before any of its slots is written
 #pragma unroll
             for (int x = 0; x < kRun; ++x) {
                 const int i = i0 + x * rows + row0;
-                if (active && i < listed) *reinterpret_cast<uint4*>(cache + dst[i] * row_bytes) = v[x];
+                if (active && i < listed && src[i] >= 0) *reinterpret_cast<uint4*>(cache + dst[i] * row_bytes) = v[x];
             }
-            if (p.score && blockIdx.y == 0) {
-#pragma unroll
-                for (int x = 0; x < kSums; ++x)
-                    if (x * kCompactThreads + tid < run) *sum_of(dst[i0 + x * kCompactThreads + tid]) = sum[x];
-            }
+            scores([&](float& f, int i) { *sum_of(dst[i]) = f; });
         }
         __syncthreads();  // the list is done with
     }
@@ -453,13 +507,15 @@ extern "C" attn_status_t attn_kv_select_paged(const float* score, const int* pag
     if (most > kSelectKeys) {
         e = launch_kernel(select_long_kernel, grid, kLongThreads, 0, static_cast<cudaStream_t>(stream), {}, p);
     } else {
-        // a thread for 16 tokens: the blocks of many short rows share the SMs, long rows have all threads of one
+        // a thread for 8 tokens: the blocks of many short rows share the SMs, long rows have all threads of one
         unsigned threads = 128;
-        while (threads < 1024 && threads * 16 < most) threads *= 2;
-        static std::atomic<bool> attr_set[kMaxAttrDevices];
-        e = ensure_smem_attr(select_kernel, kSelectKeys * 4, attr_set);
-        if (e == cudaSuccess)
-            e = launch_kernel(select_kernel, grid, threads, (size_t)(most > 0 ? most : 0) * 4, static_cast<cudaStream_t>(stream), {}, p);
+        while (threads < 1024 && threads * 8 < most) threads *= 2;
+        static std::atomic<bool> attr_set[2][kMaxAttrDevices];
+        const bool quads = page_size % 4 == 0 && multiple(score, 16);
+        const auto kernel = quads ? select_kernel<true> : select_kernel<false>;
+        p.most = most > 0 ? (int)((most + 31) / 32 * 32) : 0;
+        e = ensure_smem_attr(kernel, kSelectKeys / 32 * 140, attr_set[quads]);
+        if (e == cudaSuccess) e = launch_kernel(kernel, grid, threads, (size_t)p.most / 32 * 140, static_cast<cudaStream_t>(stream), {}, p);
     }
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
