@@ -1,14 +1,15 @@
 // Eviction from a paged cache by accumulated attention weight: which tokens stay (attn_kv_select_paged), and their move to the
 // slots that remain (attn_kv_compact_paged).
 //
-// Selection, one block per (sequence, kv head). Of the tokens between the first `sinks` and the last `recent` the m with the
-// largest scores stay, ties to the earlier token. Scores become unsigned keys of the same order, held in shared memory; the m-th largest
-// is found by digits of 11, 11 and 10 bits from the top: a histogram of the keys that share the digits found so far, the digit in
-// which the count from above passes m. Then a warp's vote per 32 tokens says which stay, in one word. Of the words' counts one
-// scan over the block numbers the holes and the tails: a kept token below end = budget - recent stays in its slot, the holes there take in
-// order the kept tokens behind it. Bounded by latency and instructions: the loads, a dozen block-wide steps, and per 32 tokens about as many
-// instructions. (With neighbouring tokens numbered by one thread each: 64 x 8 rows of 4100-4352 tokens 23 us, 16 x 8 of up to
-// 32768 29 us; with keys in registers, four digits of 8 bits, and a numbering per 1024 tokens about 100 us.)
+// Selection, one block or cluster of blocks per (sequence, kv head). Of the tokens between the first `sinks` and the last `recent` the m
+// with the largest scores stay, ties to the earlier token. Scores become unsigned keys of the same order, held in shared memory; the m-th
+// largest is found by digits of 11, 11 and 10 bits from the top: a histogram of the keys that share the digits found so far, the digit
+// in which the count from above passes m. Then a lane looks at four neighbouring tokens, a warp at 128, and four votes mark the holes (tokens below
+// m that go) and the tails (later ones that stay). One scan over the counts of 128 tokens each numbers the marks in token order, first the holes,
+// then the tails, as many of either: hole k takes tail k. Bounded by latency and instructions: the loads, a dozen steps of the whole block,
+// and about ten instructions per pass and 32 tokens. Several blocks share a row where rows are long and few: a block counts and marks its part,
+// and the others read the counts in its shared memory. (One block for each row, votes on 32 tokens: 16 x 8 rows of up to 32768 tokens 25 us,
+// 64 x 8 rows of 4100-4352 tokens 21 us; with keys in registers, four digits of 8 bits, and a numbering per 1024 tokens about 100 us.)
 //
 // Compaction: row kept[j] -> j with kept[j] >= j. A block lists the slots that get another row, in ascending order, with the
 // cache rows of both, and moves them in runs: it loads the rows of a run, then stores them. Every row that it reads later belongs to a slot
@@ -26,9 +27,12 @@
 namespace attn {
 namespace {
 
-constexpr int kLongThreads = 1024;   // selection from more tokens than the shared memory holds
-constexpr int kPairs = 4096;         // there: holes paired with tokens at a time
-constexpr int kSelectKeys = 49152;   // tokens of a row whose keys the shared memory holds: 210 KB with 12 bytes per 32, and 9 KB besides
+constexpr int kLongThreads = 1024;  // selection from more tokens than the shared memories of a cluster hold
+constexpr int kPairs = 4096;        // there: holes paired with tokens at a time
+constexpr int kGroup = 128;         // tokens that a warp looks at
+// Groups of a block's part: 512 bytes of keys and 20 of marks and counts each, 41 KB besides.
+constexpr int kPartGroups = 352, kGroupBytes = kGroup * 4 + 20;
+constexpr int kMaxParts = 8;
 
 struct EvictParams {
     float* score;           // [num_pages, Hkv, page_size]
@@ -38,7 +42,7 @@ struct EvictParams {
     int* kept;              // [B, Hkv, budget]
     int* new_seqlens;       // [B]
     int B, Hkv, page_size, max_pages, num_pages, budget, sinks, recent;
-    int most;                // selection: tokens to choose from at most, rounded up to a multiple of 32
+    int groups;              // selection: groups of a block's part
     int row_bytes, columns;  // of one kv head; 16-byte columns of K and V that a block moves
     unsigned int ps_magic;  // tok / page_size by multiplication, as in DecodeParams
     int ps_shift;
@@ -81,11 +85,12 @@ struct SelectRow {
     int* kept;
     const int* pt;
 };
-__device__ __forceinline__ bool select_row(const EvictParams& p, SelectRow& s) {
-    const int b = (int)(blockIdx.x / (unsigned)p.Hkv), K = p.budget, tid = threadIdx.x, nt = blockDim.x;
-    s.h = (int)(blockIdx.x % (unsigned)p.Hkv);
+__device__ __forceinline__ bool select_row(const EvictParams& p, SelectRow& s, int parts = 1, int part = 0) {
+    const unsigned row = blockIdx.x / (unsigned)parts;
+    const int b = (int)(row / (unsigned)p.Hkv), K = p.budget, tid = part * blockDim.x + threadIdx.x, nt = parts * blockDim.x;
+    s.h = (int)(row % (unsigned)p.Hkv);
     s.len = __ldg(p.seqlens + b);
-    s.kept = p.kept + (long long)blockIdx.x * K;
+    s.kept = p.kept + (long long)row * K;
     s.pt = p.page_table + (long long)b * p.max_pages;
     const bool bad = s.len < 0 || s.len > (long long)p.max_pages * p.page_size;
     if (tid == 0) {
@@ -176,140 +181,247 @@ __device__ __forceinline__ Sum block_before(Sum mine, Sum* sums) {
     return upto - mine + x;
 }
 
-// QUADS: page_size is a multiple of 4 and score 16-byte aligned.
-template <bool QUADS>
+// The same place of the shared memory of another block of the cluster.
+template <typename T>
+__device__ __forceinline__ const T* of_part(const T* p, int rank) {
+    const T* r;
+    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
+    return r;
+}
+
+// QUADS: page_size is a multiple of 4 and score 16-byte aligned. PARTS: blocks of the cluster that share a row.
+template <bool QUADS, int PARTS>
 __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ EvictParams p) {
     grid_dependents_launch();
     extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ int hist[2048], scratch[35];
-    __shared__ unsigned long long sums[32];
-    // behind the keys, per 32 tokens: holes and tails before them, which of them stay
-    uint2* ahead = reinterpret_cast<uint2*>(keys + p.most);
-    uint32_t* bits = reinterpret_cast<uint32_t*>(ahead + p.most / 32);
-    static_assert(2048 >= kSelectKeys / 32, "the histogram also takes the equals among 32 tokens each");
+    __shared__ int counts[3][2048], merged[PARTS > 1 ? 2048 : 1], scratch[35], totals[2];  // totals of this part: equals, marks
+    __shared__ unsigned sums[32];
+    // behind the keys, per group: four votes (of the lanes' first, second, ... tokens), marks before it
+    uint4* votes = reinterpret_cast<uint4*>(keys + p.groups * kGroup);
+    unsigned* ahead = reinterpret_cast<unsigned*>(votes + p.groups);
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
-    auto clear = [&]() {
-        for (int i = tid; i < 2048; i += nt) hist[i] = 0;
+    const int part = PARTS > 1 ? (int)(blockIdx.x % PARTS) : 0;
+    auto all_sync = [&]() {
+        if constexpr (PARTS > 1)
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        else
+            __syncthreads();
     };
-    clear();
+    for (int i = tid; i < 3 * 2048; i += nt) (&counts[0][0])[i] = 0;
     SelectRow s;
-    if (!select_row(p, s)) return;
-    const int m = s.m, n = s.n;
+    if (!select_row(p, s, PARTS, part)) return;  // (the whole cluster)
+    // places count from a multiple of four tokens on: tokens [off, off + n) of these, the first m of them below the row's end
+    const int base = p.sinks & ~3, off = p.sinks - base, n = off + s.n, m = off + s.m;
+    const int at0 = part * p.groups * kGroup, here = min(p.groups * kGroup, n - at0);  // this part's tokens (maybe none)
+    const int groups = here > 0 ? (here + kGroup - 1) / kGroup : 0;
     __syncthreads();
     if constexpr (QUADS) {
-        // tokens 4 q .. 4 q + 3, on one page
-#pragma unroll 8
-        for (int q = (p.sinks >> 2) + tid; 4 * q < s.stop; q += nt) {
-            int slot;
-            const int page = __ldg(s.pt + evict_page(p, 4 * q, slot));
-            const bool bad = page < 0 || page >= p.num_pages;
-            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (!bad) x = __ldg(reinterpret_cast<const float4*>(p.score + ((long long)page * p.Hkv + s.h) * p.page_size + slot));
-            const float f[4] = {x.x, x.y, x.z, x.w};
-            if (bad) atomicCAS(p.status, 0, kDevBadIndex);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 4 * q + e - p.sinks;
-                if (i < 0 || i >= n) continue;
-                const uint32_t k = bad ? 0 : score_key(f[e]);
-                keys[i] = k;
-                atomicAdd(&hist[k >> 21], 1);
+#pragma unroll 4
+        for (int q = tid; q < groups * (kGroup / 4); q += nt) {
+            const int i = at0 + 4 * q;
+            uint4 k = make_uint4(0, 0, 0, 0);
+            if (i < n) {
+                int slot;
+                const int page = __ldg(s.pt + evict_page(p, base + i, slot));
+                if (page >= 0 && page < p.num_pages) {
+                    const float4 x = __ldg(reinterpret_cast<const float4*>(p.score + ((long long)page * p.Hkv + s.h) * p.page_size + slot));
+                    k = make_uint4(score_key(x.x), score_key(x.y), score_key(x.z), score_key(x.w));
+                } else {
+                    atomicCAS(p.status, 0, kDevBadIndex);
+                }
             }
+            reinterpret_cast<uint4*>(keys)[q] = k;
         }
     } else {
 #pragma unroll 4
-        for (int i = tid; i < n; i += nt) {
-            const uint32_t k = key_of(p, s, i);
-            keys[i] = k;
-            atomicAdd(&hist[k >> 21], 1);
+        for (int x = tid; x < groups * kGroup; x += nt) {
+            keys[x] = at0 + x >= off && at0 + x < n ? key_of(p, s, at0 + x - off) : 0;
         }
     }
     __syncthreads();
-    // the m-th largest key, and how many of its equals stay
-    int digit, left = m, of;
-    find_digit<2048>(hist, scratch, digit, left, of);
-    uint32_t found = (uint32_t)digit << 21;
-    clear();
-    __syncthreads();
-    // f(word, its lane's key, is there one) for 32 tokens each, loaded ahead of it
-    const int words = (n + 31) >> 5;
-    auto each_word = [&](int first, auto f) {
-        constexpr int kAhead = 8;
-        for (int w = first + warp; w < words; w += kAhead * warps) {
-            uint32_t k[kAhead];
-#pragma unroll
-            for (int x = 0; x < kAhead; ++x) {
-                const int i = 32 * (w + x * warps) + lane;
-                k[x] = i < n ? keys[i] : 0;
-            }
-#pragma unroll
-            for (int x = 0; x < kAhead; ++x)
-                if (w + x * warps < words) f(w + x * warps, k[x], 32 * (w + x * warps) + lane < n);
+    // f(group, the lane's first place, its four keys, which of them are there), the keys loaded one group ahead of it. (Few groups
+    // come to a warp: instructions are fetched for nearly every one, so nothing is unrolled that need not be.)
+    auto each_group = [&](auto f) {
+        uint4 next = make_uint4(0, 0, 0, 0);
+        if (warp < groups) next = reinterpret_cast<const uint4*>(keys)[warp * 32 + lane];
+#pragma unroll 1
+        for (int g = warp; g < groups; g += warps) {
+            const uint32_t key[4] = {next.x, next.y, next.z, next.w};
+            if (g + warps < groups) next = reinterpret_cast<const uint4*>(keys)[(g + warps) * 32 + lane];
+            const int i = at0 + g * kGroup + 4 * lane;
+            // bits i .. i + 3 of [off, n)
+            const uint32_t there = 15u << min(4, max(0, off - i)) & 15u >> min(4, max(0, i + 4 - n));
+            f(g, i, key, there);
         }
     };
-    each_word(0, [&](int, uint32_t key, bool in) {
-        if (in && (key ^ found) >> 21 == 0) atomicAdd(&hist[key >> 10 & 2047], 1);
+    // histogram d of all parts
+    auto histogram = [&](int d) -> const int* {
+        all_sync();
+        if constexpr (PARTS > 1) {
+            const int* from[PARTS];
+#pragma unroll
+            for (int x = 0; x < PARTS; ++x) from[x] = of_part(counts[d], x);
+#pragma unroll 2
+            for (int i = tid; i < (d == 2 ? 1024 : 2048); i += nt) {
+                int c = 0;
+#pragma unroll
+                for (int x = 0; x < PARTS; ++x) c += from[x][i];
+                merged[i] = c;
+            }
+            __syncthreads();
+            return merged;
+        } else {
+            return counts[d];
+        }
+    };
+    // the m-th largest key, and how many of its equals stay
+    int digit, left = s.m, of;
+    each_group([&](int, int, const uint32_t(&key)[4], uint32_t there) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (there >> e & 1) atomicAdd(&counts[0][key[e] >> 21], 1);
     });
-    __syncthreads();
-    find_digit<2048>(hist, scratch, digit, left, of);
+    find_digit<2048>(histogram(0), scratch, digit, left, of);
+    uint32_t found = (uint32_t)digit << 21;
+    each_group([&](int, int, const uint32_t(&key)[4], uint32_t there) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if ((key[e] ^ found) >> 21 == 0 && (there >> e & 1)) atomicAdd(&counts[1][key[e] >> 10 & 2047], 1);
+    });
+    find_digit<2048>(histogram(1), scratch, digit, left, of);
     found |= (uint32_t)digit << 10;
-    clear();
-    __syncthreads();
-    each_word(0, [&](int, uint32_t key, bool in) {
-        if (in && (key ^ found) >> 10 == 0) atomicAdd(&hist[key & 1023], 1);
+    each_group([&](int, int, const uint32_t(&key)[4], uint32_t there) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if ((key[e] ^ found) >> 10 == 0 && (there >> e & 1)) atomicAdd(&counts[2][key[e] & 1023], 1);
     });
-    __syncthreads();
-    find_digit<1024>(hist, scratch, digit, left, of);
+    find_digit<1024>(histogram(2), scratch, digit, left, of);
     found |= (uint32_t)digit;
 
-    // which of 32 tokens stay; when not all equals do, those apart
-    const bool ties = left < of;
-    each_word(0, [&](int w, uint32_t key, bool in) {
-        const uint32_t stay = __ballot_sync(0xffffffffu, in && (ties ? key > found : key >= found));
-        if (lane == 0) bits[w] = stay;
-        if (ties) {
-            const uint32_t equal = __ballot_sync(0xffffffffu, in && key == found);
-            if (lane == 0) hist[w] = (int)equal;
+    // counts of the groups (in ahead) to the counts before them; total[which] is the part's. Returns those of the parts before.
+    auto number = [&](int which) {
+        __syncthreads();
+        const int each = (groups + nt - 1) / nt, g0 = min(groups, tid * each), g1 = min(groups, g0 + each);
+        unsigned c = 0;
+        for (int g = g0; g < g1; ++g) c += ahead[g];
+        unsigned upto = block_before(c, sums);
+        if (tid == nt - 1) totals[which] = (int)(upto + c);
+        for (int g = g0; g < g1; ++g) {
+            const unsigned x = ahead[g];
+            ahead[g] = upto;
+            upto += x;
+        }
+        all_sync();
+        unsigned before = 0;
+        if constexpr (PARTS > 1)
+#pragma unroll
+            for (int x = 0; x < PARTS - 1; ++x)
+                if (x < part) before += (unsigned)of_part(totals, x)[which];
+        return before;
+    };
+    const uint32_t lower = (1u << lane) - 1;
+    auto before_lane = [&](const uint4& v) { return __popc(v.x & lower) + __popc(v.y & lower) + __popc(v.z & lower) + __popc(v.w & lower); };
+    auto vote4 = [&](uint32_t flags) {
+        return make_uint4(__ballot_sync(0xffffffffu, flags & 1), __ballot_sync(0xffffffffu, flags & 2), __ballot_sync(0xffffffffu, flags & 4),
+                          __ballot_sync(0xffffffffu, flags & 8));
+    };
+    const bool ties = left < of;  // not all equals stay
+    auto equals = [&](const uint32_t(&key)[4], uint32_t there) {
+        uint32_t f = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f |= (uint32_t)(key[e] == found) << e;
+        return f & there;
+    };
+    unsigned first_equal = 0;
+    if (ties) {
+        each_group([&](int g, int, const uint32_t(&key)[4], uint32_t there) {
+            const uint4 v = vote4(equals(key, there));
+            if (lane == 0) ahead[g] = __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
+        });
+        first_equal = number(0);
+    }
+    // the marks: tokens below m that go, later ones that stay
+    each_group([&](int g, int i, const uint32_t(&key)[4], uint32_t there) {
+        uint32_t stay = 0;
+        if (!ties) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) stay |= (uint32_t)(key[e] >= found) << e;
+        } else {
+            const uint32_t equal = equals(key, there);
+            int rank = (int)(first_equal + ahead[g]) + before_lane(vote4(equal));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                stay |= (uint32_t)(key[e] > found || ((equal >> e & 1) && rank < left)) << e;
+                rank += equal >> e & 1;
+            }
+        }
+        uint32_t below = i + 3 < m ? 15u : i >= m ? 0u : (1u << (m - i)) - 1;
+        const uint4 v = vote4((stay ^ below) & there);
+        __syncwarp();
+        if (lane == 0) {
+            votes[g] = v;
+            ahead[g] = __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
         }
     });
-    __syncthreads();
-    // neighbouring words of this thread
-    const int each = (words + nt - 1) / nt, w0 = min(words, tid * each), w1 = min(words, w0 + each);
-    if (ties) {
-        int equals = 0;
-        for (int w = w0; w < w1; ++w) equals += __popc(hist[w]);
-        int room = left - (int)block_before<unsigned long long>(equals, sums);  // equals that may stay from here on
-        for (int w = w0; w < w1 && room > 0; ++w) {
-            uint32_t equal = (uint32_t)hist[w];
-            for (; equal && room > 0; equal &= equal - 1, --room) bits[w] |= equal & -equal;
+    const unsigned first_mark = number(1);
+    // holes in all; the first tail of each part
+    unsigned marks = 0, holes;
+    if constexpr (PARTS > 1) {
+#pragma unroll
+        for (int x = 0; x < PARTS; ++x) marks += (unsigned)of_part(totals, x)[1];
+    } else {
+        marks = (unsigned)totals[1];
+    }
+    holes = marks / 2;  // (as many as tails)
+    // (the keys are done with) this part's tails in their order, from its first one on
+    const unsigned first_tail = first_mark > holes ? first_mark : holes;
+    auto marked = [&](int g, auto f) {  // f(place, number of the mark before it, is it one)
+        const uint4 v = votes[g];
+        unsigned rank = first_mark + ahead[g] + before_lane(v);
+        const uint32_t bit[4] = {v.x >> lane & 1, v.y >> lane & 1, v.z >> lane & 1, v.w >> lane & 1};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            f(at0 + g * kGroup + 4 * lane + e, rank, bit[e] != 0);
+            rank += bit[e];
         }
-        __syncthreads();
+    };
+#pragma unroll 1
+    for (int g = max(0, m - at0) / kGroup + warp; g < groups; g += warps)
+        marked(g, [&](int i, unsigned rank, bool is) {
+            if (is && i >= m) keys[rank - first_tail] = (uint32_t)i;
+        });
+    all_sync();
+    // every slot from `sinks` to the end
+    unsigned tail_of[PARTS];  // number of the first tail of each part
+    if constexpr (PARTS > 1) {
+        unsigned c = 0;
+#pragma unroll
+        for (int x = 0; x < PARTS; ++x) {
+            tail_of[x] = c > holes ? c : holes;
+            c += (unsigned)of_part(totals, x)[1];
+        }
     }
-    // bits of word w that are tokens below m; behind them
-    auto below_m = [&](int w) { return 32 * w + 32 <= m ? ~0u : 32 * w >= m ? 0u : (1u << (m - 32 * w)) - 1; };
-    unsigned holes = 0, tails = 0;
-    for (int w = w0; w < w1; ++w) holes += __popc(~bits[w] & below_m(w)), tails += __popc(bits[w] & ~below_m(w));
-    const unsigned long long before = block_before(((unsigned long long)tails << 32) + holes, sums);
-    uint2 upto = make_uint2((unsigned)before, (unsigned)(before >> 32));
-    for (int w = w0; w < w1; ++w) {
-        ahead[w] = upto;
-        upto.x += __popc(~bits[w] & below_m(w)), upto.y += __popc(bits[w] & ~below_m(w));
-    }
-    __syncthreads();
-    // (the keys are done with) the tails in their order, then every slot
-    const uint32_t lower = (1u << lane) - 1;
-#pragma unroll 4
-    for (int w = (m >> 5) + warp; w < words; w += warps) {
-        const uint32_t tail = bits[w] & ~below_m(w);
-        if (tail >> lane & 1) keys[ahead[w].y + __popc(tail & lower)] = (uint32_t)(32 * w + lane);
-    }
-    __syncthreads();
-#pragma unroll 4
-    for (int w = warp; 32 * w < m; w += warps) {
-        const uint32_t hole = ~bits[w] & below_m(w);
-        const int i = 32 * w + lane;
-        if (i < m) s.kept[p.sinks + i] = p.sinks + (hole >> lane & 1 ? (int)keys[ahead[w].x + __popc(hole & lower)] : i);
-    }
+#pragma unroll 1
+    for (int g = warp; g < groups && at0 + g * kGroup < m; g += warps)
+        marked(g, [&](int i, unsigned rank, bool is) {
+            if (i < off || i >= m) return;
+            int from = i;
+            if (is) {
+                if constexpr (PARTS > 1) {
+                    const unsigned want = holes + rank;  // the last part whose tails begin at or before it has it
+                    int x = 0;
+                    unsigned first = tail_of[0];
+#pragma unroll
+                    for (int y = 1; y < PARTS; ++y)
+                        if (want >= tail_of[y]) x = y, first = tail_of[y];
+                    from = (int)of_part(keys, x)[want - first];
+                } else {
+                    from = (int)keys[rank];
+                }
+            }
+            s.kept[base + i] = base + from;
+        });
+    if constexpr (PARTS > 1) all_sync();  // a block stays until the others have read its tails
 }
 
 // The same from more tokens: the keys are read again for every step, and the tokens numbered in rounds of one per thread.
@@ -458,6 +570,20 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const __gri
     }
 }
 
+template <int PARTS>
+cudaError_t launch_select(EvictParams p, bool quads, long long groups, long long rows, int num_sms, cudaStream_t stream) {
+    static std::atomic<bool> attr_set[2][kMaxAttrDevices];
+    p.groups = (int)((groups + PARTS - 1) / PARTS);
+    // A thread for 8 tokens, but no more than run at once (1024 on an SM, by their registers): 64 x 8 rows of 4100-4352 tokens with 512
+    // threads each, two waves of blocks, 22 us.
+    unsigned threads = 128;
+    while (threads < 1024 && threads * 8 < (unsigned)p.groups * kGroup && rows * PARTS * threads * 2 <= 1024LL * num_sms) threads *= 2;
+    const auto kernel = quads ? select_kernel<true, PARTS> : select_kernel<false, PARTS>;
+    const cudaError_t e = ensure_smem_attr(kernel, kPartGroups * kGroupBytes, attr_set[quads]);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kernel, dim3((unsigned)(rows * PARTS)), threads, (size_t)p.groups * kGroupBytes, stream, {false, PARTS > 1 ? PARTS : 0}, p);
+}
+
 bool multiple(const void* p, long long bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 attn_status_t check_sizes(EvictParams& p, int page_size, int B, int Hkv, int max_pages, int num_pages, int budget) {
@@ -500,23 +626,23 @@ extern "C" attn_status_t attn_kv_select_paged(const float* score, const int* pag
     p.kept = kept;
     p.new_seqlens = new_seqlens;
     p.sinks = sinks, p.recent = recent;
-    // tokens to choose from at most
+    // Places to choose from at most, in groups. A row has the blocks that its keys need room in, and further ones while each still has
+    // 2048 places and an SM for itself (its 1024 threads fill the registers: 16 x 8 rows of up to 32768 tokens 25 us, in four parts each 66).
     const long long most = (long long)max_pages_per_seq * page_size - sinks - recent;
-    const dim3 grid((unsigned)(B * Hkv));
+    const long long groups = most > 0 ? (most + 3 + kGroup - 1) / kGroup : 1, rows = (long long)B * Hkv;
+    int parts = 1;
+    while (parts < kMaxParts && groups > (long long)kPartGroups * parts) parts *= 2;
+    while (parts < kMaxParts && groups >= 32LL * parts && rows * parts * 2 <= num_sms) parts *= 2;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const bool quads = page_size % 4 == 0 && multiple(score, 16);
     cudaError_t e;
-    if (most > kSelectKeys) {
-        e = launch_kernel(select_long_kernel, grid, kLongThreads, 0, static_cast<cudaStream_t>(stream), {}, p);
-    } else {
-        // a thread for 8 tokens: the blocks of many short rows share the SMs, long rows have all threads of one
-        unsigned threads = 128;
-        while (threads < 1024 && threads * 8 < most) threads *= 2;
-        static std::atomic<bool> attr_set[2][kMaxAttrDevices];
-        const bool quads = page_size % 4 == 0 && multiple(score, 16);
-        const auto kernel = quads ? select_kernel<true> : select_kernel<false>;
-        p.most = most > 0 ? (int)((most + 31) / 32 * 32) : 0;
-        e = ensure_smem_attr(kernel, kSelectKeys / 32 * 140, attr_set[quads]);
-        if (e == cudaSuccess) e = launch_kernel(kernel, grid, threads, (size_t)p.most / 32 * 140, static_cast<cudaStream_t>(stream), {}, p);
-    }
+    if (groups > (long long)kPartGroups * parts || rows * parts > INT32_MAX)
+        e = launch_kernel(select_long_kernel, dim3((unsigned)rows), kLongThreads, 0, cs, {}, p);
+    else
+        e = parts == 1   ? launch_select<1>(p, quads, groups, rows, num_sms, cs)
+            : parts == 2 ? launch_select<2>(p, quads, groups, rows, num_sms, cs)
+            : parts == 4 ? launch_select<4>(p, quads, groups, rows, num_sms, cs)
+                         : launch_select<8>(p, quads, groups, rows, num_sms, cs);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

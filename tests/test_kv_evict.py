@@ -166,6 +166,10 @@ CASES = [  # lengths, Hkv, page, budget, sinks, recent
     ([30000], 1, 1, 14000, 1, 0),
     ([14000], 1, 16, 12000, 0, 0),             # held, holes in one turn
     ([16000], 2, 16, 8000, 0, 0),
+    ([33000, 20000, 900], 1, 16, 15000, 6, 5000),  # several blocks for each row, the slots' end within one of them
+    ([70000], 3, 12, 512, 2, 64),
+    ([400000, 5], 1, 64, 3000, 4, 10),             # more than their shared memories hold
+    ([390000], 1, 16, 380000, 0, 7),
 ]
 
 
