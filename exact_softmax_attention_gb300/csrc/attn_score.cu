@@ -1,13 +1,17 @@
 // Attention weight per cached token, accumulated: score[t, h] = decay score[t, h] + sum over the rows that see
 // token t and the query heads of kv head h of exp(scale q.k - lse); the rows' own tokens have no old sum. This file: argument checks, and the kernel for up to
-// 16 rows per kv head (a decode step: one row times the query heads of a kv head).
+// 32 rows per kv head (a decode step: one row times the query heads of a kv head).
 //
 // With few rows the keys are read once and little is computed with them: the kernel is bounded by the memory. So a
 // warp reads K from the cache straight into the operand registers of mma.sync m16n8k16: 16 tokens are the rows of
 // A, the queries the columns of B. The order of the columns of K inside the sum is free, as long as q has the same: a
 // lane takes the 16 bytes that it loads of a token as its elements of two (8-bit codes: four) products. The next 16
-// tokens are loaded while these are multiplied, and the page table is read one group ahead of them. A block's warps take the
-// kv heads of the same tokens, so a cache row is read as a whole. Sums over the rows are two shuffles.
+// tokens (8-bit codes: 32) are loaded while these are multiplied, and the page table is read one group ahead of them. A block's warps take
+// the kv heads of the same tokens, so a cache row is read as a whole.
+//
+// Work order. When the blocks of all sequences' full tables run at once, a block has a piece of a sequence. Else the tokens that there are,
+// of all sequences one after the other, are dealt out in equal runs to as many blocks as the SMs hold: every SM is busy to the end, however
+// ragged the lengths (pieces of 1024 tokens: 64 sequences of U[1K, 32K] x 8 heads of 128 361 us, with e4m3 282 us).
 #include "score.cuh"
 
 #include <float.h>
@@ -45,183 +49,253 @@ __device__ __forceinline__ uint32_t half_pair(uint32_t bf16_pair, float factor) 
 
 constexpr int kRowWarps = 8;  // warps per block, at most
 
+// Tokens of a warp's step in 16s; blocks on an SM.
+template <bool F8>
+constexpr int kRowGroups = F8 ? 2 : 1;
+constexpr int row_blocks(int d, bool f8, int nt) { return d == 64 ? (nt <= 2 ? 3 : 2) : (nt == 1 ? 3 : 2); }
+
+// Tokens of a sequence in steps of a block.
+__device__ __forceinline__ int steps_of(const ScoreParams& p, int b, int step) {
+    ScoreSeq s;
+    return score_seq(p, b, s) ? (s.len + step - 1) / step : 0;
+}
+
 // NT: groups of 8 rows.
 template <int D, int FMT, int NT>
-__global__ void __launch_bounds__(kRowWarps * 32, 2) score_rows_kernel(const __grid_constant__ ScoreParams p) {
+__global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_BF16, NT)) score_rows_kernel(const __grid_constant__ ScoreParams p) {
     constexpr bool F8 = FMT != ATTN_KV_BF16;
-    constexpr int kLoads = F8 ? D / 64 : D / 32;  // 16-byte loads of a lane per token
-    constexpr int kSteps = D / 16;                // products
-    constexpr int kPer = kSteps / kLoads;         // of each load
+    constexpr int TG = kRowGroups<F8>, TE = 2 * TG;  // groups of 16 tokens, of 8
+    constexpr int kLoads = F8 ? D / 64 : D / 32;     // 16-byte loads of a lane per token
+    constexpr int kSteps = D / 16;                   // products
+    constexpr int kPer = kSteps / kLoads;            // of each load
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int heads = min(p.Hkv, kRowWarps), parts = (blockDim.x >> 5) / heads;
+    const int heads = min(p.Hkv, kRowWarps), warps = blockDim.x >> 5, parts = warps / heads;
     const int h = blockIdx.y * heads + warp % heads, part = warp / heads;
-    const int b = (int)(blockIdx.x / (unsigned)p.chunks), t_begin = (int)(blockIdx.x % (unsigned)p.chunks) * p.chunk;
-    ScoreSeq s;
-    if (h >= p.Hkv || !score_seq(p, b, s) || t_begin >= s.len) return;
-    const int t_end = min(s.len, t_begin + p.chunk), R = s.n * p.G;
-    const int* pt = p.page_table + (long long)b * p.max_pages;
+    const int step = 16 * TG * parts;  // tokens of a block's step
 
-    // rows g and g + 8: their operands, then for the columns 2 t, 2 t + 1 that this lane gets: factor of the scores, LSE,
-    // last token seen
-    uint32_t qb[NT][kSteps][2];
-    float factor[NT][2], lse2[NT][2];
-    int last[NT][2];
+    // the block's tokens: [begin, begin + left) steps from sequence b on
+    int b, begin, left;
+    if (p.chunks > 0) {
+        b = (int)(blockIdx.x / (unsigned)p.chunks);
+        begin = (int)(blockIdx.x % (unsigned)p.chunks) * (p.chunk / step);
+        left = min(p.chunk / step, steps_of(p, b, step) - begin);
+    } else {
+        __shared__ long long sums[kRowWarps], first[2];
+        const int per = (p.B + (int)blockDim.x - 1) / (int)blockDim.x, b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+        long long mine = 0;
+        for (int x = b0; x < b1; ++x) mine += steps_of(p, x, step);
+        long long upto = mine, total = 0;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int r = g + 8 * n, i = r / p.G;
-        const bool valid = r < R;
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + ((long long)(s.q0 + i) * p.Hq + h * p.G + (r - i * p.G)) * D);
-        uint4 w[D / 32];  // bf16: the lane's 8 elements of 32; 8-bit caches: 16 elements of 64
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        if (lane == 31) sums[warp] = upto;
+        __syncthreads();
+        for (int w = 0; w < warps; ++w) {
+            if (w == warp) upto += total;
+            total += sums[w];
+        }
+        const long long each = (total + gridDim.x - 1) / gridDim.x, from = each * blockIdx.x;
+        if (from >= total) return;
+        if (from >= upto - mine && from < upto) {
+            long long rest = from - (upto - mine);
+            int x = b0;
+            for (int n; rest >= (n = steps_of(p, x, step)); ++x) rest -= n;
+            first[0] = x, first[1] = rest;
+        }
+        __syncthreads();
+        b = (int)first[0];
+        begin = (int)first[1];
+        left = (int)min(each, total - from);
+    }
+    if (h >= p.Hkv) return;
+
+    for (; left > 0; ++b, begin = 0) {
+        ScoreSeq s;
+        if (!score_seq(p, b, s)) continue;
+        const int take = min(left, (s.len + step - 1) / step - begin);
+        const int t_begin = begin * step, t_end = min(s.len, (begin + take) * step), R = s.n * p.G;
+        left -= take;
+        const int* pt = p.page_table + (long long)b * p.max_pages;
+
+        // rows g, g + 8, ...: their operands, then for the columns 2 t, 2 t + 1 that this lane gets: factor of the scores, LSE,
+        // last token seen
+        uint32_t qb[NT][kSteps][2];
+        float factor[NT][2], lse2[NT][2];
+        int last[NT][2];
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x)
-            w[x] = valid ? __ldg(src + (F8 ? (x >> 1) * 8 + 2 * t + (x & 1) : 4 * x + t)) : make_uint4(0, 0, 0, 0);
-        float up = 1.0f;
-        if constexpr (F8) {
-            // a power of two brings the row's largest magnitude into [2^14, 2^15)
-            uint32_t top = 0;
+        for (int n = 0; n < NT; ++n) {
+            const int r = g + 8 * n, i = r / p.G;
+            const bool valid = r < R;
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + ((long long)(s.q0 + i) * p.Hq + h * p.G + (r - i * p.G)) * D);
+            uint4 w[D / 32];  // bf16: the lane's 8 elements of 32; 8-bit caches: 16 elements of 64
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x)
+                w[x] = valid ? __ldg(src + (F8 ? (x >> 1) * 8 + 2 * t + (x & 1) : 4 * x + t)) : make_uint4(0, 0, 0, 0);
+            float up = 1.0f;
+            if constexpr (F8) {
+                // a power of two brings the row's largest magnitude into [2^14, 2^15)
+                uint32_t top = 0;
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    const uint32_t e[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) top = max(top, max(e[y] & 0x7FFFu, (e[y] >> 16) & 0x7FFFu));
+                }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // (biased exponent 127 + 14 + 127 - exponent; the tiniest rows as far as a float reaches; 255: not finite)
+                const int exponent = (int)(top >> 7);
+                if (exponent < 255 && top != 0) up = __uint_as_float((unsigned)min(254, 268 - exponent) << 23);
+            }
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) {
                 const uint32_t e[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
 #pragma unroll
-                for (int y = 0; y < 4; ++y) top = max(top, max(e[y] & 0x7FFFu, (e[y] >> 16) & 0x7FFFu));
-            }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int exponent = (int)(top >> 7);  // biased; 0: zero or subnormal, 255: not finite
-            // (the factor 2^(127 + 14 - exponent) and its inverse as floats; exponents whose factor would leave the range stay)
-            if (exponent > 14 && exponent < 255) up = __uint_as_float((unsigned)(127 + 127 + 14 - exponent) << 23);
-            if (exponent <= 14 && top != 0) up = __uint_as_float(254u << 23);
-        }
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-            const uint32_t e[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int step = 2 * x + y;
-                qb[n][step][0] = F8 ? half_pair(e[2 * y], up) : e[2 * y];
-                qb[n][step][1] = F8 ? half_pair(e[2 * y + 1], up) : e[2 * y + 1];
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int rc = 2 * t + e + 8 * n, ic = rc / p.G;
-            const float l = rc < R ? __ldg(p.lse + (long long)(s.q0 + ic) * p.Hq + h * p.G + (rc - ic * p.G)) : -INFINITY;
-            last[n][e] = l == -INFINITY ? -1 : s.ctx + ic;  // (such rows saw nothing)
-            lse2[n][e] = l == -INFINITY ? 0.0f : l * 1.4426950408889634f;
-            const float of_row = __shfl_sync(0xffffffffu, up, (2 * t + e) * 4);
-            factor[n][e] = F8 ? p.scale_log2 / of_row : p.scale_log2;
-        }
-    }
-
-    // tokens g and g + 8 of a group of 16; lanes 0 and 1 of four keep their sums
-    struct Group {
-        int page[2], slot[2];
-    };
-    const int step = 16 * parts;
-    auto look_up = [&](int t0, Group& at) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) at.page[e] = t0 + g + 8 * e < t_end ? score_place(p, pt, t0 + g + 8 * e, at.slot[e]) : -1;
-    };
-    uint4 kv[2][kLoads];
-    float old = 0.0f;
-    auto load = [&](const Group& at, int from) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const long long row = at.page[e] >= 0 ? (long long)at.page[e] * p.page_size + at.slot[e] : 0;
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_cache) + (row * p.Hkv + h) * (F8 ? D : 2 * D));
-#pragma unroll
-            for (int x = 0; x < kLoads; ++x) kv[e][x] = at.page[e] >= 0 ? __ldg(src + 4 * x + t) : make_uint4(0, 0, 0, 0);
-        }
-        if (p.decay != 0.0f && t < 2) {
-            const int page = t ? at.page[1] : at.page[0], slot = t ? at.slot[1] : at.slot[0];
-            old = page >= 0 && from + g + 8 * t < s.ctx ? p.decay * *score_slot(p, page, slot, h) : 0.0f;
-        }
-    };
-    Group now, next;
-    int t0 = t_begin + 16 * part;
-    look_up(t0, now);
-    look_up(t0 + step, next);
-    load(now, t0);
-    for (; t0 < t_end; t0 += step) {
-        float acc[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
-#pragma unroll
-        for (int x = 0; x < kLoads; ++x) {
-            const uint32_t lo[4] = {kv[0][x].x, kv[0][x].y, kv[0][x].z, kv[0][x].w};
-            const uint32_t hi[4] = {kv[1][x].x, kv[1][x].y, kv[1][x].z, kv[1][x].w};
-#pragma unroll
-            for (int y = 0; y < kPer; ++y) {
-                uint32_t a[4];
-                if constexpr (F8) {
-                    a[0] = widen<FMT>(lo[y], 0), a[1] = widen<FMT>(hi[y], 0);
-                    a[2] = widen<FMT>(lo[y], 1), a[3] = widen<FMT>(hi[y], 1);
-                } else {
-                    a[0] = lo[2 * y], a[1] = hi[2 * y], a[2] = lo[2 * y + 1], a[3] = hi[2 * y + 1];
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if constexpr (F8)
-                        mma_f16_16816(acc[n], a, qb[n][x * kPer + y][0], qb[n][x * kPer + y][1]);
-                    else
-                        mma_bf16_16816(acc[n], a, qb[n][x * kPer + y][0], qb[n][x * kPer + y][1]);
+                for (int y = 0; y < 2; ++y) {
+                    qb[n][2 * x + y][0] = F8 ? half_pair(e[2 * y], up) : e[2 * y];
+                    qb[n][2 * x + y][1] = F8 ? half_pair(e[2 * y + 1], up) : e[2 * y + 1];
                 }
             }
-        }
-        const float before = old;
-        const Group mine = now;
-        now = next;
-        look_up(t0 + 2 * step, next);
-        load(now, t0 + step);
-        float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float x0 = ex2_mufu(fmaf(acc[n][e], factor[n][e], -lse2[n][e]));
-                const float x1 = ex2_mufu(fmaf(acc[n][2 + e], factor[n][e], -lse2[n][e]));
-                sum[0] += t0 + g <= last[n][e] ? x0 : 0.0f;
-                sum[1] += t0 + g + 8 <= last[n][e] ? x1 : 0.0f;
+                const int rc = 2 * t + e + 8 * n, ic = rc / p.G;
+                const float l = rc < R ? __ldg(p.lse + (long long)(s.q0 + ic) * p.Hq + h * p.G + (rc - ic * p.G)) : -INFINITY;
+                last[n][e] = l == -INFINITY ? -1 : s.ctx + ic;  // (such rows saw nothing)
+                lse2[n][e] = l == -INFINITY ? 0.0f : l * 1.4426950408889634f;
+                const float of_row = __shfl_sync(0xffffffffu, up, (2 * t + e) * 4);
+                factor[n][e] = F8 ? p.scale_log2 / of_row : p.scale_log2;
             }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
-            sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
         }
-        if (t < 2) {
-            const int page = t ? mine.page[1] : mine.page[0], slot = t ? mine.slot[1] : mine.slot[0];
-            const float total = t ? sum[1] : sum[0];
-            if (page >= 0) *score_slot(p, page, slot, h) = before + total;
+
+        // Of the step's tokens this lane looks up, and keeps the sum of, token g + 8 t.
+        struct Place {
+            int page, slot;
+        };
+        auto look_up = [&](int t0, Place& at) { at.page = t < TE && t0 + g + 8 * t < t_end ? score_place(p, pt, t0 + g + 8 * t, at.slot) : -1; };
+        uint4 kv[TE][kLoads];
+        float old = 0.0f;
+        auto load = [&](const Place& at, int from) {
+            const int row = at.page >= 0 ? at.page * p.page_size + at.slot : -1;
+#pragma unroll
+            for (int e = 0; e < TE; ++e) {
+                const int x = __shfl_sync(0xffffffffu, row, (lane & 28) + e);
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_cache) + ((long long)x * p.Hkv + h) * (F8 ? D : 2 * D));
+#pragma unroll
+                for (int y = 0; y < kLoads; ++y) kv[e][y] = x >= 0 ? __ldg(src + 4 * y + t) : make_uint4(0, 0, 0, 0);
+            }
+            if (p.decay != 0.0f) old = row >= 0 && from + g + 8 * t < s.ctx ? p.decay * *score_slot(p, at.page, at.slot, h) : 0.0f;
+        };
+        Place now, next;
+        int t0 = t_begin + 16 * TG * part;
+        look_up(t0, now);
+        look_up(t0 + step, next);
+        load(now, t0);
+        for (; t0 < t_end; t0 += step) {
+            float acc[TG][NT][4];
+#pragma unroll
+            for (int c = 0; c < TG; ++c)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[c][n][e] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < TG; ++c)
+#pragma unroll
+                for (int x = 0; x < kLoads; ++x) {
+                    const uint4 l4 = kv[2 * c][x], h4 = kv[2 * c + 1][x];
+                    const uint32_t lo[4] = {l4.x, l4.y, l4.z, l4.w}, hi[4] = {h4.x, h4.y, h4.z, h4.w};
+#pragma unroll
+                    for (int y = 0; y < kPer; ++y) {
+                        uint32_t a[4];
+                        if constexpr (F8) {
+                            a[0] = widen<FMT>(lo[y], 0), a[1] = widen<FMT>(hi[y], 0);
+                            a[2] = widen<FMT>(lo[y], 1), a[3] = widen<FMT>(hi[y], 1);
+                        } else {
+                            a[0] = lo[2 * y], a[1] = hi[2 * y], a[2] = lo[2 * y + 1], a[3] = hi[2 * y + 1];
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            if constexpr (F8)
+                                mma_f16_16816(acc[c][n], a, qb[n][x * kPer + y][0], qb[n][x * kPer + y][1]);
+                            else
+                                mma_bf16_16816(acc[c][n], a, qb[n][x * kPer + y][0], qb[n][x * kPer + y][1]);
+                        }
+                    }
+                }
+            const float before = old;
+            const Place mine = now;
+            now = next;
+            look_up(t0 + 2 * step, next);
+            load(now, t0 + step);
+            float sum[TE];
+#pragma unroll
+            for (int e = 0; e < TE; ++e) sum[e] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < TG; ++c)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float x0 = ex2_mufu(fmaf(acc[c][n][e], factor[n][e], -lse2[n][e]));
+                        const float x1 = ex2_mufu(fmaf(acc[c][n][2 + e], factor[n][e], -lse2[n][e]));
+                        sum[2 * c] += t0 + 16 * c + g <= last[n][e] ? x0 : 0.0f;
+                        sum[2 * c + 1] += t0 + 16 * c + g + 8 <= last[n][e] ? x1 : 0.0f;
+                    }
+            // over the columns of the four lanes; lane t keeps tokens g + 8 t
+            float total;
+            const bool odd = t & 1;
+            total = (odd ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, odd ? sum[0] : sum[1], 1);
+            if constexpr (TG == 1) {
+                total += __shfl_xor_sync(0xffffffffu, total, 2);
+            } else {
+                const float upper = (odd ? sum[3] : sum[2]) + __shfl_xor_sync(0xffffffffu, odd ? sum[2] : sum[3], 1);
+                total = (t & 2 ? upper : total) + __shfl_xor_sync(0xffffffffu, t & 2 ? total : upper, 2);
+            }
+            if (mine.page >= 0) *score_slot(p, mine.page, mine.slot, h) = before + total;
         }
     }
 }
 
-template <int D, int FMT>
+template <int D, int FMT, int NT>
 cudaError_t launch_rows(ScoreParams p, cudaStream_t stream) {
+    constexpr int kBlocks = row_blocks(D, FMT != ATTN_KV_BF16, NT);
     const int heads = p.Hkv < kRowWarps ? p.Hkv : kRowWarps, parts = kRowWarps / heads;
-    const int groups = (p.Hkv + heads - 1) / heads;
-    // tokens per block: about 16 blocks per SM when every table is full, 1024 at most
-    const long long capacity = (long long)p.max_pages * p.page_size;
-    const int least = 16 * parts;
-    long long c = ((long long)p.B * capacity * groups + 16LL * p.num_sms - 1) / (16LL * p.num_sms);
-    c = c > 1024 ? 1024 : c;
-    c = (c + least - 1) / least * least;
-    while ((capacity + c - 1) / c * p.B > INT32_MAX) c *= 2;
-    p.chunk = (int)c;
-    p.chunks = (int)((capacity + c - 1) / c);
-    const dim3 grid((unsigned)((long long)p.B * p.chunks), (unsigned)groups);
-    const unsigned threads = (unsigned)(heads * parts * 32);
-    return (long long)p.max_q * p.G <= 8 ? launch_kernel(score_rows_kernel<D, FMT, 1>, grid, threads, 0, stream, {}, p)
-                                         : launch_kernel(score_rows_kernel<D, FMT, 2>, grid, threads, 0, stream, {}, p);
+    const long long groups = (p.Hkv + heads - 1) / heads, capacity = (long long)p.max_pages * p.page_size;
+    const int step = 16 * kRowGroups<FMT != ATTN_KV_BF16> * parts;
+    const long long slots = (long long)p.num_sms * kBlocks * kRowWarps / (heads * parts);
+    // pieces of every sequence's table for as many blocks as run at once, a few steps each at least; if that is too many blocks, runs
+    long long c = ((long long)p.B * capacity * groups + slots - 1) / slots;
+    c = (c + step - 1) / step * step;
+    if (c < 2 * step) c = 2 * step;
+    const long long pieces = (capacity + c - 1) / c;
+    dim3 grid;
+    if (pieces * p.B * groups <= slots) {
+        p.chunk = (int)c, p.chunks = (int)pieces;
+        grid = dim3((unsigned)(pieces * p.B), (unsigned)groups);
+    } else {
+        p.chunk = p.chunks = 0;
+        const long long x = slots / groups;
+        grid = dim3((unsigned)(x > 0 ? x : 1), (unsigned)groups);
+    }
+    return launch_kernel(score_rows_kernel<D, FMT, NT>, grid, (unsigned)(heads * parts * 32), 0, stream, {}, p);
+}
+
+template <int D, int FMT>
+cudaError_t launch_nt(const ScoreParams& p, cudaStream_t stream) {
+    const long long rows = (long long)p.max_q * p.G;
+    return rows <= 8    ? launch_rows<D, FMT, 1>(p, stream)
+           : rows <= 16 ? launch_rows<D, FMT, 2>(p, stream)
+           : rows <= 24 ? launch_rows<D, FMT, 3>(p, stream)
+                        : launch_rows<D, FMT, 4>(p, stream);
 }
 
 template <int D>
 cudaError_t launch_fmt(const ScoreParams& p, int fmt, cudaStream_t stream) {
-    return fmt == ATTN_FP8_E4M3   ? launch_rows<D, ATTN_FP8_E4M3>(p, stream)
-           : fmt == ATTN_FP8_E5M2 ? launch_rows<D, ATTN_FP8_E5M2>(p, stream)
-                                  : launch_rows<D, ATTN_KV_BF16>(p, stream);
+    return fmt == ATTN_FP8_E4M3   ? launch_nt<D, ATTN_FP8_E4M3>(p, stream)
+           : fmt == ATTN_FP8_E5M2 ? launch_nt<D, ATTN_FP8_E5M2>(p, stream)
+                                  : launch_nt<D, ATTN_KV_BF16>(p, stream);
 }
 
 bool multiple(const void* p, long long bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }

@@ -23,7 +23,7 @@ struct ScoreParams {
     float scale_log2, decay;  // scale (key descale included) times log2(e)
     unsigned int ps_magic;   // tok / page_size by multiplication, as in DecodeParams
     int ps_shift;
-    int chunk, chunks;       // few rows: tokens per block, blocks of the longest sequence
+    int chunk, chunks;       // few rows: tokens per block, blocks of the longest sequence; 0: runs of all tokens there are
     // tiles: [blocks, 2, unit_tok] sums of units that lie in several blocks; 8-bit caches: factor of the scores of each row of q
     float *partial, *factor;
     int unit_tok;                // tokens of a unit: 128, 256 or 512
@@ -36,8 +36,8 @@ struct ScoreParams {
 cudaError_t launch_score_rows(const ScoreParams& p, int d, int kv_format, cudaStream_t stream);
 cudaError_t launch_score_tiles(const ScoreParams& p, int d, int kv_format, cudaStream_t stream);
 
-// Rows per kv head (queries x query heads) up to which a warp's 16-row products take them; more go to the tiles.
-constexpr int kScoreFewRows = 16;
+// Rows per kv head (queries x query heads) up to which a warp's products take them; more go to the tiles.
+constexpr int kScoreFewRows = 32;
 
 #ifdef __CUDACC__
 namespace {

@@ -163,9 +163,14 @@ FEW = [  # rows, lengths, Hq, Hkv, d, page, dense
     ([1], [130], 20, 20, 64, 100, True),
     ([16, 5], [16, 70], 5, 5, 128, 3, False),
     ([1], [20000], 3, 1, 128, 16, True),
+    ([5, 3, 0, 4], [700, 30, 9, 1100], 8, 2, 128, 16, False),  # 20 and
+    ([8, 1], [600, 3000], 8, 2, 64, 7, False),                 # 32 rows
+    ([1] * 40, [3000 - 70 * i for i in range(40)], 16, 8, 128, 16, True),  # equal runs over ragged lengths
+    ([1] * 300, [100 + 7 * i for i in range(300)], 12, 12, 64, 16, True),  # more sequences than threads, two groups of heads
 ]
 MANY = [
-    ([17], [17], 1, 1, 64, 1, True),
+    ([33], [33], 1, 1, 64, 1, True),
+    ([17], [17], 2, 1, 64, 1, True),
     ([32, 0, 5, 31], [400, 9, 700, 31], 8, 2, 128, 16, False),
     ([33] * 3, [33, 256, 1025], 3, 1, 64, 7, True),       # a group that does not divide 128
     ([32] * 4, [3000, 100, 257, 513], 16, 4, 128, 64, True),  # 128 rows
