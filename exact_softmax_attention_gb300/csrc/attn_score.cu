@@ -49,10 +49,12 @@ __device__ __forceinline__ uint32_t half_pair(uint32_t bf16_pair, float factor) 
 
 constexpr int kRowWarps = 8;  // warps per block, at most
 
-// Tokens of a warp's step in 16s; blocks on an SM.
+// Tokens of a warp's step in 16s, steps that are loaded ahead, blocks on an SM.
 template <bool F8>
 constexpr int kRowGroups = F8 ? 2 : 1;
-constexpr int row_blocks(int d, bool f8, int nt) { return d == 64 ? (nt <= 2 ? 3 : 2) : (nt == 1 ? 3 : 2); }
+template <bool F8>
+constexpr int kRowAhead = F8 ? 2 : 1;
+constexpr int row_blocks(int d, bool f8, int nt) { return d == 64 ? (nt <= 2 ? 3 : 2) : (nt == 1 && !f8 ? 3 : 2); }
 
 // Tokens of a sequence in steps of a block.
 __device__ __forceinline__ int steps_of(const ScoreParams& p, int b, int step) {
@@ -64,7 +66,7 @@ __device__ __forceinline__ int steps_of(const ScoreParams& p, int b, int step) {
 template <int D, int FMT, int NT>
 __global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_BF16, NT)) score_rows_kernel(const __grid_constant__ ScoreParams p) {
     constexpr bool F8 = FMT != ATTN_KV_BF16;
-    constexpr int TG = kRowGroups<F8>, TE = 2 * TG;  // groups of 16 tokens, of 8
+    constexpr int TG = kRowGroups<F8>, TE = 2 * TG, S = kRowAhead<F8>;  // groups of 16 tokens, of 8; steps loaded ahead
     constexpr int kLoads = F8 ? D / 64 : D / 32;     // 16-byte loads of a lane per token
     constexpr int kSteps = D / 16;                   // products
     constexpr int kPer = kSteps / kLoads;            // of each load
@@ -174,25 +176,28 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_B
             int page, slot;
         };
         auto look_up = [&](int t0, Place& at) { at.page = t < TE && t0 + g + 8 * t < t_end ? score_place(p, pt, t0 + g + 8 * t, at.slot) : -1; };
-        uint4 kv[TE][kLoads];
-        float old = 0.0f;
-        auto load = [&](const Place& at, int from) {
-            const int row = at.page >= 0 ? at.page * p.page_size + at.slot : -1;
+        uint4 kv[S][TE][kLoads];
+        float old[S];
+        Place at[S], next;
+        auto load = [&](int j, int from) {  // into place j of the steps ahead
+            const int row = at[j].page >= 0 ? at[j].page * p.page_size + at[j].slot : -1;
 #pragma unroll
             for (int e = 0; e < TE; ++e) {
                 const int x = __shfl_sync(0xffffffffu, row, (lane & 28) + e);
                 const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_cache) + ((long long)x * p.Hkv + h) * (F8 ? D : 2 * D));
 #pragma unroll
-                for (int y = 0; y < kLoads; ++y) kv[e][y] = x >= 0 ? __ldg(src + 4 * y + t) : make_uint4(0, 0, 0, 0);
+                for (int y = 0; y < kLoads; ++y) kv[j][e][y] = x >= 0 ? __ldg(src + 4 * y + t) : make_uint4(0, 0, 0, 0);
             }
-            if (p.decay != 0.0f) old = row >= 0 && from + g + 8 * t < s.ctx ? p.decay * *score_slot(p, at.page, at.slot, h) : 0.0f;
+            old[j] = 0.0f;
+            if (p.decay != 0.0f && row >= 0 && from + g + 8 * t < s.ctx) old[j] = p.decay * *score_slot(p, at[j].page, at[j].slot, h);
         };
-        Place now, next;
-        int t0 = t_begin + 16 * TG * part;
-        look_up(t0, now);
-        look_up(t0 + step, next);
-        load(now, t0);
-        for (; t0 < t_end; t0 += step) {
+        const int from = t_begin + 16 * TG * part;
+#pragma unroll
+        for (int j = 0; j < S; ++j) look_up(from + j * step, at[j]);
+        look_up(from + S * step, next);
+#pragma unroll
+        for (int j = 0; j < S; ++j) load(j, from + j * step);
+        auto step_of = [&](int j, int t0) {
             float acc[TG][NT][4];
 #pragma unroll
             for (int c = 0; c < TG; ++c)
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_B
             for (int c = 0; c < TG; ++c)
 #pragma unroll
                 for (int x = 0; x < kLoads; ++x) {
-                    const uint4 l4 = kv[2 * c][x], h4 = kv[2 * c + 1][x];
+                    const uint4 l4 = kv[j][2 * c][x], h4 = kv[j][2 * c + 1][x];
                     const uint32_t lo[4] = {l4.x, l4.y, l4.z, l4.w}, hi[4] = {h4.x, h4.y, h4.z, h4.w};
 #pragma unroll
                     for (int y = 0; y < kPer; ++y) {
@@ -224,11 +229,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_B
                         }
                     }
                 }
-            const float before = old;
-            const Place mine = now;
-            now = next;
-            look_up(t0 + 2 * step, next);
-            load(now, t0 + step);
+            const float before = old[j];
+            const Place mine = at[j];
+            at[j] = next;
+            look_up(t0 + (S + 1) * step, next);
+            load(j, t0 + S * step);
             float sum[TE];
 #pragma unroll
             for (int e = 0; e < TE; ++e) sum[e] = 0.0f;
@@ -254,17 +259,33 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_B
                 total = (t & 2 ? upper : total) + __shfl_xor_sync(0xffffffffu, t & 2 ? total : upper, 2);
             }
             if (mine.page >= 0) *score_slot(p, mine.page, mine.slot, h) = before + total;
+        };
+        for (int t0 = from; t0 < t_end; t0 += S * step) {
+#pragma unroll
+            for (int j = 0; j < S; ++j)
+                if (t0 + j * step < t_end) step_of(j, t0 + j * step);
         }
     }
 }
 
+// Blocks of so many threads of a kernel that an SM holds.
+template <typename Kernel>
+int resident_blocks(Kernel kernel, int threads, std::atomic<int> (&known)[kRowWarps + 1]) {
+    int n = known[threads / 32].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) n = 1;
+        known[threads / 32].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 template <int D, int FMT, int NT>
 cudaError_t launch_rows(ScoreParams p, cudaStream_t stream) {
-    constexpr int kBlocks = row_blocks(D, FMT != ATTN_KV_BF16, NT);
+    static std::atomic<int> known[kRowWarps + 1];
     const int heads = p.Hkv < kRowWarps ? p.Hkv : kRowWarps, parts = kRowWarps / heads;
     const long long groups = (p.Hkv + heads - 1) / heads, capacity = (long long)p.max_pages * p.page_size;
     const int step = 16 * kRowGroups<FMT != ATTN_KV_BF16> * parts;
-    const long long slots = (long long)p.num_sms * kBlocks * kRowWarps / (heads * parts);
+    const long long slots = (long long)p.num_sms * resident_blocks(score_rows_kernel<D, FMT, NT>, heads * parts * 32, known);
     // pieces of every sequence's table for as many blocks as run at once, a few steps each at least; if that is too many blocks, runs
     long long c = ((long long)p.B * capacity * groups + slots - 1) / slots;
     c = (c + step - 1) / step * step;
