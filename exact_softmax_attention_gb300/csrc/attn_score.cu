@@ -49,12 +49,12 @@ __device__ __forceinline__ uint32_t half_pair(uint32_t bf16_pair, float factor) 
 
 constexpr int kRowWarps = 8;  // warps per block, at most
 
-// Tokens of a warp's step in 16s, steps that are loaded ahead, blocks on an SM.
+// Tokens of a warp's step in 16s: 8-bit keys, half the bytes, take two. (64 sequences of U[1K, 32K] x 8 heads of 128, e4m3: one 236 us, two 194.)
 template <bool F8>
 constexpr int kRowGroups = F8 ? 2 : 1;
-template <bool F8>
-constexpr int kRowAhead = F8 ? 2 : 1;
-constexpr int row_blocks(int d, bool f8, int nt) { return d == 64 ? (nt <= 2 ? 3 : 2) : (nt == 1 && !f8 ? 3 : 2); }
+// Blocks on an SM that the registers are limited to. Spilled registers cost more than the warps give: the same case with three blocks of
+// 80 registers 212 us, two of 128 194; and two steps loaded ahead instead of one, two blocks, 208.
+constexpr int row_blocks(int d, bool f8, int nt) { return (d == 64 && nt == 1) || (nt == 1 && !f8) ? 3 : 2; }
 
 // Tokens of a sequence in steps of a block.
 __device__ __forceinline__ int steps_of(const ScoreParams& p, int b, int step) {
@@ -66,7 +66,7 @@ __device__ __forceinline__ int steps_of(const ScoreParams& p, int b, int step) {
 template <int D, int FMT, int NT>
 __global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_BF16, NT)) score_rows_kernel(const __grid_constant__ ScoreParams p) {
     constexpr bool F8 = FMT != ATTN_KV_BF16;
-    constexpr int TG = kRowGroups<F8>, TE = 2 * TG, S = kRowAhead<F8>;  // groups of 16 tokens, of 8; steps loaded ahead
+    constexpr int TG = kRowGroups<F8>, TE = 2 * TG;  // groups of 16 tokens, of 8
     constexpr int kLoads = F8 ? D / 64 : D / 32;     // 16-byte loads of a lane per token
     constexpr int kSteps = D / 16;                   // products
     constexpr int kPer = kSteps / kLoads;            // of each load
@@ -176,28 +176,25 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_B
             int page, slot;
         };
         auto look_up = [&](int t0, Place& at) { at.page = t < TE && t0 + g + 8 * t < t_end ? score_place(p, pt, t0 + g + 8 * t, at.slot) : -1; };
-        uint4 kv[S][TE][kLoads];
-        float old[S];
-        Place at[S], next;
-        auto load = [&](int j, int from) {  // into place j of the steps ahead
-            const int row = at[j].page >= 0 ? at[j].page * p.page_size + at[j].slot : -1;
+        uint4 kv[TE][kLoads];
+        float old = 0.0f;
+        auto load = [&](const Place& at, int from) {
+            const int row = at.page >= 0 ? at.page * p.page_size + at.slot : -1;
 #pragma unroll
             for (int e = 0; e < TE; ++e) {
                 const int x = __shfl_sync(0xffffffffu, row, (lane & 28) + e);
                 const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_cache) + ((long long)x * p.Hkv + h) * (F8 ? D : 2 * D));
 #pragma unroll
-                for (int y = 0; y < kLoads; ++y) kv[j][e][y] = x >= 0 ? __ldg(src + 4 * y + t) : make_uint4(0, 0, 0, 0);
+                for (int y = 0; y < kLoads; ++y) kv[e][y] = x >= 0 ? __ldg(src + 4 * y + t) : make_uint4(0, 0, 0, 0);
             }
-            old[j] = 0.0f;
-            if (p.decay != 0.0f && row >= 0 && from + g + 8 * t < s.ctx) old[j] = p.decay * *score_slot(p, at[j].page, at[j].slot, h);
+            if (p.decay != 0.0f) old = row >= 0 && from + g + 8 * t < s.ctx ? p.decay * *score_slot(p, at.page, at.slot, h) : 0.0f;
         };
-        const int from = t_begin + 16 * TG * part;
-#pragma unroll
-        for (int j = 0; j < S; ++j) look_up(from + j * step, at[j]);
-        look_up(from + S * step, next);
-#pragma unroll
-        for (int j = 0; j < S; ++j) load(j, from + j * step);
-        auto step_of = [&](int j, int t0) {
+        Place now, next;
+        int t0 = t_begin + 16 * TG * part;
+        look_up(t0, now);
+        look_up(t0 + step, next);
+        load(now, t0);
+        for (; t0 < t_end; t0 += step) {
             float acc[TG][NT][4];
 #pragma unroll
             for (int c = 0; c < TG; ++c)
@@ -209,7 +206,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_B
             for (int c = 0; c < TG; ++c)
 #pragma unroll
                 for (int x = 0; x < kLoads; ++x) {
-                    const uint4 l4 = kv[j][2 * c][x], h4 = kv[j][2 * c + 1][x];
+                    const uint4 l4 = kv[2 * c][x], h4 = kv[2 * c + 1][x];
                     const uint32_t lo[4] = {l4.x, l4.y, l4.z, l4.w}, hi[4] = {h4.x, h4.y, h4.z, h4.w};
 #pragma unroll
                     for (int y = 0; y < kPer; ++y) {
@@ -229,11 +226,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_B
                         }
                     }
                 }
-            const float before = old[j];
-            const Place mine = at[j];
-            at[j] = next;
-            look_up(t0 + (S + 1) * step, next);
-            load(j, t0 + S * step);
+            const float before = old;
+            const Place mine = now;
+            now = next;
+            look_up(t0 + 2 * step, next);
+            load(now, t0 + step);
             float sum[TE];
 #pragma unroll
             for (int e = 0; e < TE; ++e) sum[e] = 0.0f;
@@ -259,11 +256,6 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_B
                 total = (t & 2 ? upper : total) + __shfl_xor_sync(0xffffffffu, t & 2 ? total : upper, 2);
             }
             if (mine.page >= 0) *score_slot(p, mine.page, mine.slot, h) = before + total;
-        };
-        for (int t0 = from; t0 < t_end; t0 += S * step) {
-#pragma unroll
-            for (int j = 0; j < S; ++j)
-                if (t0 + j * step < t_end) step_of(j, t0 + j * step);
         }
     }
 }
