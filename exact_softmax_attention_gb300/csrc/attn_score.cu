@@ -6,7 +6,7 @@
 // warp reads K from the cache straight into the operand registers of mma.sync m16n8k16: 16 tokens are the rows of
 // A, the queries the columns of B. The order of the columns of K inside the sum is free, as long as q has the same: a
 // lane takes the 16 bytes that it loads of a token as its elements of two (8-bit codes: four) products. The next 16
-// tokens (8-bit codes: 32) are loaded while these are multiplied, and the page table is read one group ahead of them. A block's warps take
+// tokens (narrower rows: 32) are loaded while these are multiplied, and the page table is read one group ahead of them. A block's warps take
 // the kv heads of the same tokens, so a cache row is read as a whole.
 //
 // Work order. When the blocks of all sequences' full tables run at once, a block has a piece of a sequence. Else the tokens that there are,
@@ -49,9 +49,10 @@ __device__ __forceinline__ uint32_t half_pair(uint32_t bf16_pair, float factor) 
 
 constexpr int kRowWarps = 8;  // warps per block, at most
 
-// Tokens of a warp's step in 16s: 8-bit keys, half the bytes, take two. (64 sequences of U[1K, 32K] x 8 heads of 128, e4m3: one 236 us, two 194.)
-template <bool F8>
-constexpr int kRowGroups = F8 ? 2 : 1;
+// Tokens of a warp's step in 16s: 2 KB of keys at least. (64 sequences of U[1K, 32K] x 8 heads of 128, e4m3: one 236 us, two 194; 48 of
+// U[5333, 16000] x 8 heads of 64, bf16: one 129 us, two 92; e4m3: two 77, four 74, but with 24 rows their registers spill: 29 us, not 26.)
+template <int D, bool F8>
+constexpr int kRowGroups = D == 128 && !F8 ? 1 : 2;
 // Blocks on an SM that the registers are limited to. Spilled registers cost more than the warps give: the same case with three blocks of
 // 80 registers 212 us, two of 128 194; and two steps loaded ahead instead of one, two blocks, 208.
 constexpr int row_blocks(int d, bool f8, int nt) { return (d == 64 && nt == 1) || (nt == 1 && !f8) ? 3 : 2; }
@@ -66,7 +67,7 @@ __device__ __forceinline__ int steps_of(const ScoreParams& p, int b, int step) {
 template <int D, int FMT, int NT>
 __global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_BF16, NT)) score_rows_kernel(const __grid_constant__ ScoreParams p) {
     constexpr bool F8 = FMT != ATTN_KV_BF16;
-    constexpr int TG = kRowGroups<F8>, TE = 2 * TG;  // groups of 16 tokens, of 8
+    constexpr int TG = kRowGroups<D, F8>, TE = 2 * TG;  // groups of 16 tokens, of 8
     constexpr int kLoads = F8 ? D / 64 : D / 32;     // 16-byte loads of a lane per token
     constexpr int kSteps = D / 16;                   // products
     constexpr int kPer = kSteps / kLoads;            // of each load
@@ -276,7 +277,7 @@ cudaError_t launch_rows(ScoreParams p, cudaStream_t stream) {
     static std::atomic<int> known[kRowWarps + 1];
     const int heads = p.Hkv < kRowWarps ? p.Hkv : kRowWarps, parts = kRowWarps / heads;
     const long long groups = (p.Hkv + heads - 1) / heads, capacity = (long long)p.max_pages * p.page_size;
-    const int step = 16 * kRowGroups<FMT != ATTN_KV_BF16> * parts;
+    const int step = 16 * kRowGroups<D, FMT != ATTN_KV_BF16> * parts;
     const long long slots = (long long)p.num_sms * resident_blocks(score_rows_kernel<D, FMT, NT>, heads * parts * 32, known);
     // pieces of every sequence's table for as many blocks as run at once, a few steps each at least; if that is too many blocks, runs
     long long c = ((long long)p.B * capacity * groups + slots - 1) / slots;
@@ -301,7 +302,7 @@ cudaError_t launch_nt(const ScoreParams& p, cudaStream_t stream) {
     return rows <= 8    ? launch_rows<D, FMT, 1>(p, stream)
            : rows <= 16 ? launch_rows<D, FMT, 2>(p, stream)
            : rows <= 24 ? launch_rows<D, FMT, 3>(p, stream)
-                        : launch_rows<D, FMT, 4>(p, stream);
+                        : launch_rows<D, FMT, D == 64 ? 4 : 3>(p, stream);  // (128: no more rows come here)
 }
 
 template <int D>
@@ -367,6 +368,6 @@ extern "C" attn_status_t attn_kv_score_paged(const void* q, const float* lse, co
         p.ps_shift = k - 1;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = (long long)p.max_q * p.G <= kScoreFewRows ? launch_score_rows(p, d, kv_format, s) : launch_score_tiles(p, d, kv_format, s);
+    const cudaError_t e = (long long)p.max_q * p.G <= score_few_rows(d) ? launch_score_rows(p, d, kv_format, s) : launch_score_tiles(p, d, kv_format, s);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

@@ -36,8 +36,10 @@ struct ScoreParams {
 cudaError_t launch_score_rows(const ScoreParams& p, int d, int kv_format, cudaStream_t stream);
 cudaError_t launch_score_tiles(const ScoreParams& p, int d, int kv_format, cudaStream_t stream);
 
-// Rows per kv head (queries x query heads) up to which a warp's products take them; more go to the tiles.
-constexpr int kScoreFewRows = 32;
+// Rows per kv head (queries x query heads) up to which a warp's products take them; more go to the tiles. Measured, us, products / tiles, 32 x
+// U[1333, 4000] tokens: 8 heads of 64, 32 rows, bf16 28.8 / 32.7, e4m3 28.8 / 34.7; 2 heads of 128, 20 rows, 15.0 / 18.5, e4m3 16.6 / 19.2;
+// one of 128, 24 rows, 12.3 / 15.5 (48 x U[5333, 16000] 30.7 / 31.3); 8 heads of 128, 32 rows, 63 / 39.
+constexpr int score_few_rows(int d) { return d == 64 ? 32 : 24; }
 
 #ifdef __CUDACC__
 namespace {

@@ -132,7 +132,7 @@ class Problem:
             # the product: d fp32 additions of |q k| (2^-23 each, for units that truncate), factor and difference in fp32, ex2 within
             # 2^-21; two 8-bit parts of q leave 2^-17 of the row's largest element times |k|
             e = size * self.d * 2.0**-23 + (s.abs().nan_to_num(posinf=0.0) + torch.where(seen, lse.abs(), 0.0)[..., None]) * 4 * 2.0**-24 + 2.0**-21
-            if self.fmt != "bf16" and self.max_q * self.G > 16:
+            if self.fmt != "bf16" and self.max_q * self.G > 24:
                 top = self.q[at - n:at].double().abs().amax(-1).view(n, self.Hkv, self.G, 1)
                 e = e + (top * self.keys(b).abs().sum(-1).T[None, :, None]).reshape(n, self.Hq, L) * abs(self.scale) * 2.0**-17
             group = lambda x: x.view(n, self.Hkv, self.G, L).sum((0, 2)).T
