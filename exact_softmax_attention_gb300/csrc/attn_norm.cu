@@ -65,12 +65,74 @@ __device__ __forceinline__ float group_sum(float x, int lanes) {
     return x;
 }
 
-// Weights of both tensors into shared memory, ones where there are none.
+// Place of element i of a row of n in shared memory: lane j reads elements 8 j .. 8 j + 7 of bf16 rows by two 16-byte loads, which lie in two
+// halves of the row, so that neighbouring lanes read neighbouring 16 bytes. (Side by side they conflict in every other bank: forward
+// 72 us, the gradient 107 us.) V = 4 and 1 read in order.
+template <int V>
+__device__ __forceinline__ int spread(int i, int n) {
+    return V == 8 ? (i & 4 ? n / 2 : 0) + (i >> 3) * 4 + (i & 3) : i;
+}
+// Elements V j .. V j + V - 1 of such a row.
+template <int V>
+__device__ __forceinline__ void load_spread(const float* row, int j, int n, float (&x)[V]) {
+    if constexpr (V == 8) {
+        float lo[4], hi[4];
+        load_angles<4>(row + 4 * j, lo);
+        load_angles<4>(row + n / 2 + 4 * j, hi);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = lo[e], x[4 + e] = hi[e];
+    } else {
+        load_angles<V>(row + V * j, x);
+    }
+}
+
+// Weights of both tensors into shared memory, ones where there are none: in the order of the columns, rows of d spread.
+template <int V>
 __device__ __forceinline__ void stage_weights(const NormParams& p, float* w) {
     for (int i = threadIdx.x; i < 2 * p.cols.d; i += blockDim.x) {
-        const bool k = i >= p.cols.d;
+        const int k = i >= p.cols.d, c = i - k * p.cols.d;
         const float* from = p.weight[k];
-        w[i] = from ? from[i - (k ? p.cols.d : 0)] : 1.0f;
+        w[k * p.cols.d + spread<V>(c, p.cols.d)] = from ? from[c] : 1.0f;
+    }
+}
+
+// cos and sin (times the amplitude) of the block's tokens into cs[token][rot / 2] and sn[token][rot / 2], the rows spread unless the pairs
+// are interleaved (whose lanes read four neighbouring ones at a time). Every thread of the block calls it.
+template <int V>
+__device__ __forceinline__ void stage_angles(const NormParams& p, long long t0, int tokens, bool transpose, float* cs, float* sn) {
+    const int half = p.cols.rot / 2;
+    if (half == 0) return;
+    const int nt = blockDim.x, groups = max(1, nt / half), grp = threadIdx.x / half;
+    if (grp >= groups) return;
+    for (int i = groups > 1 ? (int)threadIdx.x % half : (int)threadIdx.x; i < half; i += groups > 1 ? half : nt) {
+        const double f = p.inv_freq[i];
+        const unsigned long long frac = turn_fraction(f);
+        const float amp = isfinite(f) ? p.amplitude : __int_as_float(0x7fffffff);  // no angle: NaN
+        const int at = p.cols.interleaved ? i : spread<V>(i, half);
+        for (int t = groups > 1 ? grp : 0; t < tokens; t += groups) {
+            float c, s;
+            position_angle(frac, p.positions[t0 + t], c, s);
+            cs[t * half + at] = c * amp;
+            sn[t * half + at] = (transpose ? -s : s) * amp;
+        }
+    }
+}
+
+// Rotate the pairs of item j.
+template <int V>
+__device__ __forceinline__ void turn_item(float (&xa)[V], float (&xb)[V], const RopeCols& cols, int j, const float* cs, const float* sn) {
+    if (V == 8 && !cols.interleaved) {
+        float c[V], s[V];
+        load_spread<V>(cs, j, cols.rot / 2, c);
+        load_spread<V>(sn, j, cols.rot / 2, s);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float u = xa[e], w = xb[e];
+            xa[e] = u * c[e] - w * s[e];
+            xb[e] = u * s[e] + w * c[e];
+        }
+    } else {
+        rotate_item<V>(xa, xb, cols, j, cs, sn);
     }
 }
 
@@ -111,8 +173,8 @@ __global__ void __launch_bounds__(256, norm_blocks(R)) norm_rope_kernel(const __
             if (some[r]) ra[r] = load_raw<E, V>(src + a[r]), rb[r] = load_raw<E, V>(src + b[r]);
     };
     if (at.t < tokens) load();
-    if (half > 0) block_angles(p.inv_freq, p.positions + t0, tokens, half, p.amplitude, false, cs, sn);
-    stage_weights(p, w);
+    stage_angles<V>(p, t0, tokens, false, cs, sn);
+    stage_weights<V>(p, w);
     __syncthreads();
     // (a warp goes on while its first group has a head: the groups of a warp take part in its shuffles)
     const int all = tokens * H;
@@ -140,11 +202,11 @@ __global__ void __launch_bounds__(256, norm_blocks(R)) norm_rope_kernel(const __
         for (int r = 0; r < R; ++r) {
             if (!some[r]) continue;
             float wa[V], wb[V];
-            load_angles<V>(wh + a[r], wa);
-            load_angles<V>(wh + b[r], wb);
+            load_spread<V>(wh, a[r] / V, d, wa);
+            load_spread<V>(wh, b[r] / V, d, wb);
             times<V>(xa[r], wa, scale);
             times<V>(xb[r], wb, scale);
-            if (turned[r]) rotate_item<V>(xa[r], xb[r], p.cols, lane + r * p.lanes, cs + t * half, sn + t * half);
+            if (turned[r]) turn_item<V>(xa[r], xb[r], p.cols, lane + r * p.lanes, cs + t * half, sn + t * half);
             store_row<V>(dst + a[r], xa[r]);
             store_row<V>(dst + b[r], xb[r]);
         }
@@ -162,8 +224,8 @@ __global__ void __launch_bounds__(256) norm_rope_any_kernel(const __grid_constan
     float* sn = cs + p.tokens * half;
     const long long t0 = (long long)blockIdx.x * p.tokens;
     const int tokens = (int)min((long long)p.tokens, p.T - t0), lane = threadIdx.x & 31;
-    if (half > 0) block_angles(p.inv_freq, p.positions + t0, tokens, half, p.amplitude, false, cs, sn);
-    stage_weights(p, w);
+    stage_angles<1>(p, t0, tokens, false, cs, sn);
+    stage_weights<1>(p, w);
     __syncthreads();
     for (HeadWalk at(threadIdx.x >> 5, blockDim.x >> 5, H); at.t < tokens; at.next()) {
         const int k = at.h >= p.heads[0];
@@ -219,8 +281,8 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
         some[r] = lane + r * p.lanes < p.items;
         turned[r] = item_cols<V>(p.cols, some[r] ? lane + r * p.lanes : 0, a[r], b[r]);
     }
-    if (half > 0) block_angles(p.inv_freq, p.positions + t0, tokens, half, p.amplitude, true, cs, sn);
-    stage_weights(p, w);
+    stage_angles<V>(p, t0, tokens, true, cs, sn);
+    stage_weights<V>(p, w);
     __syncthreads();
     for (int k = 0; k < 2; ++k) {  // the heads of q, then of k
         if (p.heads[k] == 0) continue;
@@ -256,10 +318,10 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 if (!some[r] || !mine) continue;
-                if (turned[r]) rotate_item<V>(ya[r], yb[r], p.cols, lane + r * p.lanes, cs + t * half, sn + t * half);
+                if (turned[r]) turn_item<V>(ya[r], yb[r], p.cols, lane + r * p.lanes, cs + t * half, sn + t * half);
                 float wa[V], wb[V];
-                load_angles<V>(w + k * d + a[r], wa);
-                load_angles<V>(w + k * d + b[r], wb);
+                load_spread<V>(w + k * d, a[r] / V, d, wa);
+                load_spread<V>(w + k * d, b[r] / V, d, wb);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     ss = fmaf(xa[r][e], xa[r][e], fmaf(xb[r][e], xb[r][e], ss));
@@ -274,8 +336,8 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
             for (int r = 0; r < R; ++r) {
                 if (!some[r]) continue;
                 float wa[V], wb[V];
-                load_angles<V>(w + k * d + a[r], wa);
-                load_angles<V>(w + k * d + b[r], wb);
+                load_spread<V>(w + k * d, a[r] / V, d, wa);
+                load_spread<V>(w + k * d, b[r] / V, d, wb);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     wa_sum[r][e] = fmaf(xa[r][e] * scale, ya[r][e], wa_sum[r][e]);
@@ -321,8 +383,8 @@ __global__ void __launch_bounds__(256) norm_rope_bwd_any_kernel(const __grid_con
     const long long t0 = (long long)blockIdx.x * p.tokens;
     const int tokens = (int)min((long long)p.tokens, p.T - t0);
     float* row = rows + (threadIdx.x >> 5) * d;
-    if (half > 0) block_angles(p.inv_freq, p.positions + t0, tokens, half, p.amplitude, true, cs, sn);
-    stage_weights(p, w);
+    stage_angles<1>(p, t0, tokens, true, cs, sn);
+    stage_weights<1>(p, w);
     __syncthreads();
     for (int k = 0; k < 2; ++k) {
         if (p.heads[k] == 0) continue;
