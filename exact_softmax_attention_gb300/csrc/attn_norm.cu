@@ -60,9 +60,25 @@ struct HeadWalk {
     }
 };
 
+// Sum over a group of W lanes (0: `lanes`).
+template <int W>
 __device__ __forceinline__ float group_sum(float x, int lanes) {
-    for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if constexpr (W > 0) {
+#pragma unroll
+        for (int o = W / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    } else {
+        for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    }
     return x;
+}
+
+// Two products, one instruction.
+__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
 // Place of element i of a row of n in shared memory: lane j reads elements 8 j .. 8 j + 7 of bf16 rows by two 16-byte loads, which lie in two
@@ -118,6 +134,36 @@ __device__ __forceinline__ void stage_angles(const NormParams& p, long long t0, 
     }
 }
 
+template <int V>
+__device__ __forceinline__ void times(float (&x)[V], const float (&w)[V], float r) {
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+        float a, b;
+        fmul2(a, b, w[e], w[e + 1], r, r);
+        fmul2(x[e], x[e + 1], x[e], x[e + 1], a, b);
+    }
+}
+
+// Pairs (u, w) turned: u c - w s, u s + w c.
+template <int V>
+__device__ __forceinline__ void turn(float (&u)[V], float (&w)[V], const float (&c)[V], const float (&s)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+        float a0, a1, b0, b1;
+        fmul2(a0, a1, u[e], u[e + 1], c[e], c[e + 1]);
+        fmul2(b0, b1, u[e], u[e + 1], s[e], s[e + 1]);
+        ffma2(u[e], u[e + 1], w[e], w[e + 1], -s[e], -s[e + 1], a0, a1);
+        ffma2(w[e], w[e + 1], w[e], w[e + 1], c[e], c[e + 1], b0, b1);
+    }
+}
+
+// Sum of the products over both runs of an item, added to that of two interleaved halves.
+template <int V>
+__device__ __forceinline__ void add_products(float (&sum)[2], const float (&x)[V], const float (&y)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; e += 2) ffma2(sum[0], sum[1], x[e], x[e + 1], y[e], y[e + 1], sum[0], sum[1]);
+}
+
 // Rotate the pairs of item j.
 template <int V>
 __device__ __forceinline__ void turn_item(float (&xa)[V], float (&xb)[V], const RopeCols& cols, int j, const float* cs, const float* sn) {
@@ -125,25 +171,15 @@ __device__ __forceinline__ void turn_item(float (&xa)[V], float (&xb)[V], const 
         float c[V], s[V];
         load_spread<V>(cs, j, cols.rot / 2, c);
         load_spread<V>(sn, j, cols.rot / 2, s);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float u = xa[e], w = xb[e];
-            xa[e] = u * c[e] - w * s[e];
-            xb[e] = u * s[e] + w * c[e];
-        }
+        turn<V>(xa, xb, c, s);
     } else {
         rotate_item<V>(xa, xb, cols, j, cs, sn);
     }
 }
 
-template <int V>
-__device__ __forceinline__ void times(float (&x)[V], const float (&w)[V], float r) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) x[e] *= r * w[e];
-}
-
 // Forward for heads that fit into the registers of a group of lanes.
-template <typename E, int V, int R>
+// W > 0: a head is exactly W lanes of R items; 0: p.lanes, the last ones may be idle.
+template <typename E, int V, int R, int W>
 __global__ void __launch_bounds__(256, norm_blocks(R)) norm_rope_kernel(const __grid_constant__ NormParams p) {
     extern __shared__ __align__(16) float shared[];
     typedef typename RawOf<E, V>::type Raw;
@@ -153,15 +189,15 @@ __global__ void __launch_bounds__(256, norm_blocks(R)) norm_rope_kernel(const __
     float* sn = cs + p.tokens * half;
     const long long t0 = (long long)blockIdx.x * p.tokens;
     const int tokens = (int)min((long long)p.tokens, p.T - t0);
-    const int lane = threadIdx.x & (p.lanes - 1), shift = 31 - __clz(p.lanes);
+    const int lanes = W > 0 ? W : p.lanes, lane = threadIdx.x & (lanes - 1), shift = 31 - __clz(lanes);
     const int groups = blockDim.x >> shift;
     HeadWalk at(threadIdx.x >> shift, groups, H);
     int a[R], b[R];
     bool turned[R], some[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        some[r] = lane + r * p.lanes < p.items;
-        turned[r] = item_cols<V>(p.cols, some[r] ? lane + r * p.lanes : 0, a[r], b[r]);
+        some[r] = W > 0 || lane + r * lanes < p.items;
+        turned[r] = item_cols<V>(p.cols, some[r] ? lane + r * lanes : 0, a[r], b[r]);
     }
     Raw ra[R], rb[R];
     auto load = [&]() {
@@ -182,18 +218,17 @@ __global__ void __launch_bounds__(256, norm_blocks(R)) norm_rope_kernel(const __
         const bool mine = at.t < tokens;
         const int t = at.t, h = at.h;
         const bool k = h >= p.heads[0];
-        float xa[R][V], xb[R][V], ss = 0.0f;
+        float xa[R][V], xb[R][V], ss[2] = {0.0f, 0.0f};  // (a group without a head sums what it finds, for itself)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) xa[r][e] = xb[r][e] = 0.0f;
-            if (some[r] && mine) unpack<E, V>(ra[r], xa[r]), unpack<E, V>(rb[r], xb[r]);
-#pragma unroll
-            for (int e = 0; e < V; ++e) ss = fmaf(xa[r][e], xa[r][e], fmaf(xb[r][e], xb[r][e], ss));
+            if (!some[r]) continue;
+            unpack<E, V>(ra[r], xa[r]), unpack<E, V>(rb[r], xb[r]);
+            add_products<V>(ss, xa[r], xa[r]);
+            add_products<V>(ss, xb[r], xb[r]);
         }
         at.next();
         if (at.t < tokens) load();
-        const float scale = rsqrtf(fmaf(group_sum(ss, p.lanes), p.inv_d, p.eps));
+        const float scale = rsqrtf(fmaf(group_sum<W>(ss[0] + ss[1], lanes), p.inv_d, p.eps));
         if (!mine) continue;
         E* dst = static_cast<E*>(k ? p.out[1] : p.out[0]) + (t0 + t) * (k ? p.out_stride[1] : p.out_stride[0]) +
                  (long long)(k ? h - p.heads[0] : h) * d;
@@ -206,7 +241,7 @@ __global__ void __launch_bounds__(256, norm_blocks(R)) norm_rope_kernel(const __
             load_spread<V>(wh, b[r] / V, d, wb);
             times<V>(xa[r], wa, scale);
             times<V>(xb[r], wb, scale);
-            if (turned[r]) turn_item<V>(xa[r], xb[r], p.cols, lane + r * p.lanes, cs + t * half, sn + t * half);
+            if (turned[r]) turn_item<V>(xa[r], xb[r], p.cols, lane + r * lanes, cs + t * half, sn + t * half);
             store_row<V>(dst + a[r], xa[r]);
             store_row<V>(dst + b[r], xb[r]);
         }
@@ -234,7 +269,7 @@ __global__ void __launch_bounds__(256) norm_rope_any_kernel(const __grid_constan
         E* dst = static_cast<E*>(p.out[k]) + (t0 + at.t) * p.out_stride[k] + (long long)h * d;
         float ss = 0.0f;
         for (int i = lane; i < d; i += 32) ss = fmaf((float)src[i], (float)src[i], ss);
-        const float scale = rsqrtf(fmaf(group_sum(ss, 32), p.inv_d, p.eps));
+        const float scale = rsqrtf(fmaf(group_sum<32>(ss, 32), p.inv_d, p.eps));
         __syncwarp();
         for (int j = lane; j < p.items; j += 32) {
             int a, b;
@@ -260,7 +295,7 @@ __device__ __forceinline__ void block_sums(const NormParams& p, const float* row
     __syncthreads();
 }
 
-template <typename E, int V, int R>
+template <typename E, int V, int R, int W>
 __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(const __grid_constant__ NormParams p) {
     grid_dependents_launch();
     extern __shared__ __align__(16) float shared[];
@@ -272,14 +307,14 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
     float* sn = cs + p.tokens * half;
     const long long t0 = (long long)blockIdx.x * p.tokens;
     const int tokens = (int)min((long long)p.tokens, p.T - t0);
-    const int lane = threadIdx.x & (p.lanes - 1), shift = 31 - __clz(p.lanes);
+    const int lanes = W > 0 ? W : p.lanes, lane = threadIdx.x & (lanes - 1), shift = 31 - __clz(lanes);
     const int groups = blockDim.x >> shift;
     int a[R], b[R];
     bool turned[R], some[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        some[r] = lane + r * p.lanes < p.items;
-        turned[r] = item_cols<V>(p.cols, some[r] ? lane + r * p.lanes : 0, a[r], b[r]);
+        some[r] = W > 0 || lane + r * lanes < p.items;
+        turned[r] = item_cols<V>(p.cols, some[r] ? lane + r * lanes : 0, a[r], b[r]);
     }
     stage_angles<V>(p, t0, tokens, true, cs, sn);
     stage_weights<V>(p, w);
@@ -304,12 +339,10 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
         for (int i = (threadIdx.x & ~31) >> shift; i < all; i += groups) {
             const bool mine = at.t < tokens;
             const int t = at.t, h = at.h;
-            float xa[R][V], xb[R][V], ya[R][V], yb[R][V], ss = 0.0f, dot = 0.0f;
+            float xa[R][V], xb[R][V], ya[R][V], yb[R][V], ss[2] = {0.0f, 0.0f}, dot[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) xa[r][e] = xb[r][e] = ya[r][e] = yb[r][e] = 0.0f;
-                if (!some[r] || !mine) continue;
+                if (!some[r]) continue;
                 unpack<E, V>(ra[r], xa[r]), unpack<E, V>(rb[r], xb[r]);
                 unpack<E, V>(ga[r], ya[r]), unpack<E, V>(gb[r], yb[r]);
             }
@@ -317,19 +350,23 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
             if (at.t < tokens) load();
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                if (!some[r] || !mine) continue;
-                if (turned[r]) turn_item<V>(ya[r], yb[r], p.cols, lane + r * p.lanes, cs + t * half, sn + t * half);
+                if (!some[r]) continue;
+                if (turned[r] && mine) turn_item<V>(ya[r], yb[r], p.cols, lane + r * lanes, cs + t * half, sn + t * half);
                 float wa[V], wb[V];
                 load_spread<V>(w + k * d, a[r] / V, d, wa);
                 load_spread<V>(w + k * d, b[r] / V, d, wb);
+                add_products<V>(ss, xa[r], xa[r]);
+                add_products<V>(ss, xb[r], xb[r]);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    ss = fmaf(xa[r][e], xa[r][e], fmaf(xb[r][e], xb[r][e], ss));
-                    dot = fmaf(xa[r][e], wa[e] * ya[r][e], fmaf(xb[r][e], wb[e] * yb[r][e], dot));
+                for (int e = 0; e < V; e += 2) {
+                    fmul2(wa[e], wa[e + 1], wa[e], wa[e + 1], ya[r][e], ya[r][e + 1]);
+                    fmul2(wb[e], wb[e + 1], wb[e], wb[e + 1], yb[r][e], yb[r][e + 1]);
                 }
+                add_products<V>(dot, xa[r], wa);
+                add_products<V>(dot, xb[r], wb);
             }
-            const float scale = rsqrtf(fmaf(group_sum(ss, p.lanes), p.inv_d, p.eps));
-            const float along = group_sum(dot, p.lanes) * p.inv_d * scale * scale;  // mean(n w g) r: times x, that is n mean(n w g)
+            const float scale = rsqrtf(fmaf(group_sum<W>(ss[0] + ss[1], lanes), p.inv_d, p.eps));
+            const float along = group_sum<W>(dot[0] + dot[1], lanes) * p.inv_d * scale * scale;  // mean(n w g) r: times x, that is n mean(n w g)
             if (!mine) continue;
             E* dst = static_cast<E*>(p.out[k]) + (t0 + t) * p.out_stride[k] + (long long)h * d;
 #pragma unroll
@@ -338,13 +375,21 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
                 float wa[V], wb[V];
                 load_spread<V>(w + k * d, a[r] / V, d, wa);
                 load_spread<V>(w + k * d, b[r] / V, d, wb);
+                // dx = r (w g) - x (r along); dw += (r x) g
+                const float back = -scale * along;
+                auto finish = [&](float(&x)[V], const float(&y)[V], const float(&wt)[V], float(&w_sum)[V]) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    wa_sum[r][e] = fmaf(xa[r][e] * scale, ya[r][e], wa_sum[r][e]);
-                    wb_sum[r][e] = fmaf(xb[r][e] * scale, yb[r][e], wb_sum[r][e]);
-                    xa[r][e] = scale * (wa[e] * ya[r][e] - xa[r][e] * along);
-                    xb[r][e] = scale * (wb[e] * yb[r][e] - xb[r][e] * along);
-                }
+                    for (int e = 0; e < V; e += 2) {
+                        float n0, n1, g0, g1, q0, q1;
+                        fmul2(n0, n1, x[e], x[e + 1], scale, scale);
+                        ffma2(w_sum[e], w_sum[e + 1], n0, n1, y[e], y[e + 1], w_sum[e], w_sum[e + 1]);
+                        fmul2(g0, g1, y[e], y[e + 1], wt[e], wt[e + 1]);
+                        fmul2(q0, q1, x[e], x[e + 1], back, back);
+                        ffma2(x[e], x[e + 1], g0, g1, scale, scale, q0, q1);
+                    }
+                };
+                finish(xa[r], ya[r], wa, wa_sum[r]);
+                finish(xb[r], yb[r], wb, wb_sum[r]);
                 store_row<V>(dst + a[r], xa[r]);
                 store_row<V>(dst + b[r], xb[r]);
             }
@@ -354,12 +399,12 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                for (int o = p.lanes; o < 32; o <<= 1) {
+                for (int o = lanes; o < 32; o <<= 1) {
                     wa_sum[r][e] += __shfl_xor_sync(0xffffffffu, wa_sum[r][e], o);
                     wb_sum[r][e] += __shfl_xor_sync(0xffffffffu, wb_sum[r][e], o);
                 }
         float* row = rows + (threadIdx.x >> 5) * d;
-        if ((threadIdx.x & 31) < p.lanes) {
+        if ((threadIdx.x & 31) < lanes) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 if (some[r])
@@ -408,8 +453,8 @@ __global__ void __launch_bounds__(256) norm_rope_bwd_any_kernel(const __grid_con
                 ss = fmaf(xa[0], xa[0], fmaf(xb[0], xb[0], ss));
                 dot = fmaf(xa[0], w[k * d + a] * ya[0], fmaf(xb[0], w[k * d + b] * yb[0], dot));
             }
-            const float scale = rsqrtf(fmaf(group_sum(ss, 32), p.inv_d, p.eps));
-            const float along = group_sum(dot, 32) * p.inv_d * scale * scale;
+            const float scale = rsqrtf(fmaf(group_sum<32>(ss, 32), p.inv_d, p.eps));
+            const float along = group_sum<32>(dot, 32) * p.inv_d * scale * scale;
             for (int j = lane; j < p.items; j += 32) {
                 item(j, a, b, xa, xb, ya, yb);
                 row[a] = fmaf(xa[0] * scale, ya[0], row[a]);
@@ -453,10 +498,24 @@ void head_shape(int items, int& lanes, int& each) {
     }
 }
 
-template <typename E, int V, int R>
+template <typename E, int V, int R, int W>
 cudaError_t launch_wide(const NormParams& p, bool back, unsigned blocks, unsigned threads, size_t smem, cudaStream_t s) {
-    return back ? launch_kernel(norm_rope_bwd_kernel<E, V, R>, dim3(blocks), threads, smem, s, {}, p)
-                : launch_kernel(norm_rope_kernel<E, V, R>, dim3(blocks), threads, smem, s, {}, p);
+    return back ? launch_kernel(norm_rope_bwd_kernel<E, V, R, W>, dim3(blocks), threads, smem, s, {}, p)
+                : launch_kernel(norm_rope_kernel<E, V, R, W>, dim3(blocks), threads, smem, s, {}, p);
+}
+
+// The common widths have kernels of their own (64, 128 and 256, and with V = 8 items of bf16 192: three items on 4 lanes).
+template <typename E, int V>
+cudaError_t launch_shape(const NormParams& p, int each, bool back, unsigned blocks, unsigned threads, size_t smem, cudaStream_t s) {
+    const bool full = p.items == p.lanes * each;
+    if (each == 1 && full && p.lanes == 4) return launch_wide<E, V, 1, 4>(p, back, blocks, threads, smem, s);
+    if (each == 1 && full && p.lanes == 8) return launch_wide<E, V, 1, 8>(p, back, blocks, threads, smem, s);
+    if (each == 1 && full && p.lanes == 16) return launch_wide<E, V, 1, 16>(p, back, blocks, threads, smem, s);
+    if (each == 1) return launch_wide<E, V, 1, 0>(p, back, blocks, threads, smem, s);
+    if (each == 2) return launch_wide<E, V, 2, 0>(p, back, blocks, threads, smem, s);
+    if (each == 3 && full && p.lanes == (V == 8 ? 4 : 8)) return launch_wide<E, V, 3, V == 8 ? 4 : 8>(p, back, blocks, threads, smem, s);
+    if (each == 3) return launch_wide<E, V, 3, 0>(p, back, blocks, threads, smem, s);
+    return launch_wide<E, V, 4, 0>(p, back, blocks, threads, smem, s);
 }
 
 template <typename E>
@@ -493,14 +552,8 @@ cudaError_t launch_norm(NormParams p, bool wide, bool back, int num_sms, float* 
         if (!wide)
             e = back ? launch_kernel(norm_rope_bwd_any_kernel<E>, dim3((unsigned)blocks), threads, smem, s, {}, p)
                      : launch_kernel(norm_rope_any_kernel<E>, dim3((unsigned)blocks), threads, smem, s, {}, p);
-        else if (each == 1)
-            e = launch_wide<E, V, 1>(p, back, (unsigned)blocks, threads, smem, s);
-        else if (each == 2)
-            e = launch_wide<E, V, 2>(p, back, (unsigned)blocks, threads, smem, s);
-        else if (each == 3)
-            e = launch_wide<E, V, 3>(p, back, (unsigned)blocks, threads, smem, s);
         else
-            e = launch_wide<E, V, 4>(p, back, (unsigned)blocks, threads, smem, s);
+            e = launch_shape<E, V>(p, each, back, (unsigned)blocks, threads, smem, s);
     }
     if (e == cudaSuccess && sums) {
         LaunchMode mode;
