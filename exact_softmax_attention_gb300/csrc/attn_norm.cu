@@ -22,11 +22,11 @@ namespace attn {
 namespace {
 
 constexpr int kNormMaxDim = 1024;
-// Blocks of 256 threads that an SM holds, by the items per lane: their registers (64 to 255 per thread).
-constexpr int norm_blocks(int items) { return items == 1 ? 4 : 2; }
+// Blocks of 256 threads that an SM holds, by the items per lane: their registers (48 to 255 per thread).
+constexpr int norm_blocks(int items) { return items == 1 ? 5 : 2; }
 constexpr int norm_bwd_blocks(int items) { return items == 1 ? 2 : 1; }
-constexpr int kNormItems = 4;      // heads per group of lanes, at least
-constexpr int kNormAngles = 4096;  // floats for the angles of a block's tokens
+constexpr int kNormItems = 8;      // heads per group of lanes, at least
+constexpr int kNormAngles = 8192;  // floats for the angles of a block's tokens
 
 struct NormParams {
     const void* in[2];     // q, k
