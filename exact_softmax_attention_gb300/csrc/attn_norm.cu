@@ -72,15 +72,6 @@ __device__ __forceinline__ float group_sum(float x, int lanes) {
     return x;
 }
 
-// Two products, one instruction.
-__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
-    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d0), "=f"(d1)
-        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-
 // Place of element i of a row of n in shared memory: lane j reads elements 8 j .. 8 j + 7 of bf16 rows by two 16-byte loads, which lie in two
 // halves of the row, so that neighbouring lanes read neighbouring 16 bytes. (Side by side they conflict in every other bank: forward
 // 72 us, the gradient 107 us.) V = 4 and 1 read in order.

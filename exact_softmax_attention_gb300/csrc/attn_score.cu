@@ -361,12 +361,7 @@ extern "C" attn_status_t attn_kv_score_paged(const void* q, const float* lse, co
     p.scale_log2 = (float)factor;
     p.decay = decay;
     p.watchdog_ns = watchdog_ns();
-    if (page_size > 1) {  // tok / page_size for tok < 2^31: multiplier ceil(2^(31+k) / page_size), k = ceil(log2 page_size)
-        int k = 0;
-        while ((1LL << k) < page_size) ++k;
-        p.ps_magic = (unsigned)(((1ULL << (31 + k)) + (unsigned long long)page_size - 1) / (unsigned long long)page_size);
-        p.ps_shift = k - 1;
-    }
+    p.by_page = Divisor(page_size);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = (long long)p.max_q * p.G <= score_few_rows(d) ? launch_score_rows(p, d, kv_format, s) : launch_score_tiles(p, d, kv_format, s);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

@@ -29,9 +29,10 @@ constexpr int kTileTok = 128, kTiles = 4;   // tokens of an accumulator tile, ti
 constexpr int kUnitTok = kTiles * kTileTok;
 constexpr int kBlockRows = 128;             // rows of a task
 constexpr int kTileThreads = 21 * 32;
+constexpr float kBf16Max = 0x1.FEp127f;
 constexpr int kSumWarps = 16, kKeyWarp = 16, kQueryWarp = 18, kProductWarp = 19;
 
-template <int D, int FMT>
+template <int D, int FMT, bool FOLD>
 struct ScoreLayout {
     static constexpr bool kF8 = FMT != ATTN_KV_BF16;
     static constexpr int kRow = kF8 ? D : 2 * D;             // bytes of a key
@@ -46,7 +47,9 @@ struct ScoreLayout {
     static constexpr int kKOff = 0, kQOff = kKStages * kTile;
     // per row of a block of q: minus the LSE (times log2 e), factor of the scores, last token seen
     static constexpr int kLseOff = kQOff + kQStages * kQ, kLseStage = 3 * kBlockRows * 4;
-    static constexpr int kBarOff = kLseOff + kLseStages * kLseStage;
+    // further columns of the operands that give minus the LSE: 16 ones and zeros per token, the three bf16 parts per row of a stage of q
+    static constexpr int kFoldK = (kLseOff + kLseStages * kLseStage + 255) / 256 * 256, kFold = FOLD ? 128 * 32 : 0, kFoldQ = kFoldK + kFold;
+    static constexpr int kBarOff = kFoldQ + kQStages * kFold;
     static constexpr int bK = 0, bKFree = bK + kKStages, bQ = bKFree + kKStages, bQFree = bQ + kQStages, bL = bQFree + kQStages, bLFree = bL + kLseStages;
     static constexpr int bS = bLFree + kLseStages, bSFree = bS + kTiles, bDrain = bSFree + kTiles, kBars = bDrain + 2;
     // tensor-memory base, abort flag; per lse stage: do rows need their own limits; the plan
@@ -77,6 +80,14 @@ __device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a_desc, uint64_t b_
 __device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(512 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)4 << 61;
 }
+
+// The same for rows of 32 bytes with the 32-byte swizzle.
+__device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(256 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)6 << 61;
+}
+
+// 16-byte unit u of row r of such rows.
+__device__ __forceinline__ uint4* unit32(uint8_t* tile, int r, int u) { return reinterpret_cast<uint4*>(tile + r * 32 + ((u ^ ((r >> 2) & 1)) << 4)); }
 
 // Instruction descriptor, fp32 accumulation, M = 128: bf16 operands, or A in the cache's 8-bit format and B e4m3.
 template <int FMT>
@@ -159,12 +170,15 @@ struct SeqTasks {
     int units, blocks;
     long long skip;  // first(u) = max(0, each u - skip)
     int each;        // blocks of a unit's tokens, rounded down
-    __device__ __forceinline__ SeqTasks(const ScoreSeq& s, int unit_tok, int block_tok, int head_blocks) {
-        units = (s.len + unit_tok - 1) / unit_tok;
-        blocks = (s.n + block_tok - 1) / block_tok * head_blocks;
+    int cut;         // the first unit that not all blocks see
+    __device__ __forceinline__ SeqTasks(const ScoreParams& p, const ScoreSeq& s) {
+        units = (s.len + p.unit_tok - 1) >> p.unit_shift;
+        blocks = p.by_block_tok(s.n + p.block_tok - 1) * p.head_blocks;
         // token U u is query U u - ctx, in block floor((U u - ctx) / block_tok) >= floor(U / block_tok) u - ceil(ctx / block_tok)
-        each = unit_tok / block_tok * head_blocks;
-        skip = (long long)((s.ctx + block_tok - 1) / block_tok) * head_blocks;
+        each = p.unit_blocks.d * p.head_blocks;
+        const int before = p.by_block_tok(s.ctx + p.block_tok - 1);
+        skip = (long long)before * p.head_blocks;
+        cut = p.unit_blocks(before) + 1;
     }
     __device__ __forceinline__ int first(int u) const {
         const long long f = (long long)each * u - skip;
@@ -172,9 +186,8 @@ struct SeqTasks {
     }
     // tasks of the units before u
     __device__ __forceinline__ long long before(int u) const {
-        const long long from = skip / each + 1;  // the first unit that not all blocks see
-        const long long cut = u > from ? (long long)each * ((from + u - 1) * (u - from) / 2) - skip * (u - from) : 0;
-        return (long long)blocks * u - cut;
+        const long long n = u - cut;  // units of which some blocks are left out
+        return (long long)blocks * u - (n > 0 ? each * ((cut + u - 1) * n / 2) - skip * n : 0);
     }
 };
 
@@ -186,9 +199,9 @@ struct UnitWalk {
     bool whole;      // the run holds the first of the unit's tasks
     ScoreSeq s;
     SeqTasks seq;
-    __device__ __forceinline__ UnitWalk(const ScoreParams& p, int b_, long long rest, int count) : b(b_), s(), seq(s, 1, 1, 1) {
+    __device__ __forceinline__ UnitWalk(const ScoreParams& p, int b_, long long rest, int count) : b(b_), s(), seq(p, s) {
         score_seq(p, b, s);
-        seq = SeqTasks(s, p.unit_tok, p.block_tok, p.head_blocks);
+        seq = SeqTasks(p, s);
         const long long each = seq.before(seq.units);
         h = (int)(rest / each);
         rest -= each * h;
@@ -228,7 +241,7 @@ struct UnitWalk {
             h = 0;
             do ++b;
             while (!score_seq(p, b, s));
-            seq = SeqTasks(s, p.unit_tok, p.block_tok, p.head_blocks);
+            seq = SeqTasks(p, s);
         }
         from = -seq.skip;
         cut();
@@ -253,7 +266,7 @@ struct UnitWalk {
 __device__ __forceinline__ long long tasks_of(const ScoreParams& p, int b) {
     ScoreSeq s;
     if (!score_seq(p, b, s)) return 0;
-    const SeqTasks t(s, p.unit_tok, p.block_tok, p.head_blocks);
+    const SeqTasks t(p, s);
     return t.before(t.units) * p.Hkv;
 }
 
@@ -303,32 +316,30 @@ __device__ __forceinline__ TaskRun task_run(const ScoreParams& p, int block, int
     return run;
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool FOLD>
 __global__ void __launch_bounds__(kTileThreads, 1)
     score_tiles_kernel(const __grid_constant__ ScoreParams p, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK) {
-    grid_dependents_launch();
-    using L = ScoreLayout<D, FMT>;
+    using L = ScoreLayout<D, FMT, FOLD>;
     constexpr bool F8 = L::kF8;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
-    const TaskRun run = task_run<kTileThreads>(p, blockIdx.x, gridDim.x, reinterpret_cast<long long*>(smem), reinterpret_cast<long long*>(smem + L::kPlanOff));
-    if (run.count == 0 || smem_u32(smem) & 1023u) {  // (the swizzles count from such boundaries)
-        if (run.count > 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kDevTimeout);
-        if (F8) grid_dependency_wait();
-        return;
-    }
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
     int* odd_rows = reinterpret_cast<int*>(smem + L::kOddOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t wd = p.watchdog_ns;
+    if (smem_u32(smem) & 1023u) {  // (the swizzles count from such boundaries)
+        if (threadIdx.x == 0) atomicCAS(p.status, 0, kDevTimeout);
+        grid_dependency_wait();
+        return;
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::kKStages; ++i) {
             mbar_init(&bars[L::bK + i], 1);
             mbar_init(&bars[L::bKFree + i], 1);
         }
         for (int i = 0; i < L::kQStages; ++i) {
-            mbar_init(&bars[L::bQ + i], 1);
+            mbar_init(&bars[L::bQ + i], FOLD ? 2 : 1);
             mbar_init(&bars[L::bQFree + i], 2);
         }
         for (int i = 0; i < L::kLseStages; ++i) {
@@ -347,16 +358,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (p.box_rows > 1) tma_prefetch_desc(&tmK);
     }
     // rows that no copy of q writes are zeros
-    for (int i = threadIdx.x; i < L::kQStages * L::kQ / 16; i += kTileThreads) reinterpret_cast<uint4*>(smem + L::kQOff)[i] = make_uint4(0, 0, 0, 0);
+    if (p.block_tok * p.G < kBlockRows)
+        for (int i = threadIdx.x; i < L::kQStages * L::kQ / 16; i += kTileThreads) reinterpret_cast<uint4*>(smem + L::kQOff)[i] = make_uint4(0, 0, 0, 0);
+    if (FOLD && threadIdx.x < 256)
+        *unit32(smem + L::kFoldK, threadIdx.x >> 1, threadIdx.x & 1) = threadIdx.x & 1 ? make_uint4(0, 0, 0, 0) : make_uint4(0x3F803F80u, 0x3F80u, 0, 0);
     fence_smem_to_async();
+    // Nothing that an earlier kernel writes is read before this, and no tensor memory is held that one may still ask for. (8-bit caches: only
+    // the kernel that makes the parts of q is still running, which the warp that copies them waits for.)
+    if (!F8) grid_dependency_wait();
+    grid_dependents_launch();
     if (warp == kProductWarp) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
     tc_fence_before();
-    __syncthreads();
+    const TaskRun run = task_run<kTileThreads>(p, blockIdx.x, gridDim.x, reinterpret_cast<long long*>(smem + L::kLseOff), reinterpret_cast<long long*>(smem + L::kPlanOff));
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (run.count == 0) {
+        if (F8) grid_dependency_wait();
+        if (warp == kProductWarp) tmem_dealloc(tmem, 512);
+        return;
+    }
     const uint32_t base = smem_u32(smem);
     UnitWalk at(p, run.b, run.rest, run.count);
 
@@ -486,6 +509,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                     at.h * p.G + h0, at.s.q0 + i0);
                 }
                 __syncwarp();
+                if constexpr (FOLD) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        // minus the LSE in units of the products; rows behind the box get weight 0
+                        float v = l[e] * p.unit;
+                        if (l[e] == -INFINITY) v = query[e] >= p.block_tok ? copysignf(kBf16Max, p.unit) : 0.0f;
+                        v = v > kBf16Max ? kBf16Max : v < -kBf16Max ? -kBf16Max : v;
+                        const float hi = __bfloat162float(__float2bfloat16_rn(v)), rest = v - hi, mid = __bfloat162float(__float2bfloat16_rn(rest));
+                        uint8_t* to = smem + L::kFoldQ + st * L::kFold;
+                        *unit32(to, lane + 32 * e, 0) = make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(rest - mid, 0.0f), 0, 0);
+                        *unit32(to, lane + 32 * e, 1) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_smem_to_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[L::bQ + st]);
+                }
                 ++qn;
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::bLFree + ls], (uint32_t)((qn - 1) / L::kLseStages & 1) ^ 1u, abort_flag, wd)))) break;
                 float* lse2 = reinterpret_cast<float*>(smem + L::kLseOff + ls * L::kLseStage);
@@ -518,7 +557,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (lane == 0) {
             const int mine = warp - kProductWarp;
             auto desc = [&](int off) { return L::kBox == 64 ? smem_desc_sw64(base + off) : smem_desc_sw128(base + off, L::kChunk, 1024); };
-            const uint64_t dk = desc(L::kKOff), dq = desc(L::kQOff);
+            const uint64_t dk = desc(L::kKOff), dq = desc(L::kQOff), fold_k = smem_desc_sw32(base + L::kFoldK), fold_q = smem_desc_sw32(base + L::kFoldQ);
             auto wait = [&](int bar, uint32_t parity) { return mbar_wait(&bars[bar], parity, abort_flag, wd); };
             bool any = false, go = true, fresh = true;
             int qs = 0;                          // stages of q waited for
@@ -559,6 +598,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             for (int k = 0; k < D / 16; ++k)
                                 tc_mma_ss(d, kd + (uint64_t)(((k >> 2) * L::kChunk + (k & 3) * 32) >> 4),
                                           qd + (uint64_t)(((k >> 2) * L::kChunk + (k & 3) * 32) >> 4), idesc, k > 0);
+                            if constexpr (FOLD) tc_mma_ss(d, fold_k, fold_q + (uint64_t)((st * L::kFold) >> 4), idesc, 1);
                         }
                         tc_commit(&bars[L::bS + t]);
                         if (r + 1 == at.end) tc_commit(&bars[L::bKFree + ks]), ++keys[x];
@@ -619,12 +659,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             }
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
-                                const float4 l = *reinterpret_cast<const float4*>(lse2 + c + e);
-                                float4 f = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
-                                if constexpr (F8) f = *reinterpret_cast<const float4*>(factor + c + e);
                                 float y[4];
-                                ffma2(y[0], y[1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]), f.x, f.y, l.x, l.y);
-                                ffma2(y[2], y[3], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]), f.z, f.w, l.z, l.w);
+                                if constexpr (FOLD) {
+                                    fmul2(y[0], y[1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]), p.scale_log2, p.scale_log2);
+                                    fmul2(y[2], y[3], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]), p.scale_log2, p.scale_log2);
+                                } else {
+                                    const float4 l = *reinterpret_cast<const float4*>(lse2 + c + e);
+                                    float4 f = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+                                    if constexpr (F8) f = *reinterpret_cast<const float4*>(factor + c + e);
+                                    ffma2(y[0], y[1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]), f.x, f.y, l.x, l.y);
+                                    ffma2(y[2], y[3], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]), f.z, f.w, l.z, l.w);
+                                }
 #pragma unroll
                                 for (int z = 0; z < 4; ++z) y[z] = ex2_mufu(y[z]);
                                 if constexpr (decltype(masked)::value) {
@@ -687,32 +732,40 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 __global__ void __launch_bounds__(kUnitTok) score_join_kernel(const __grid_constant__ ScoreParams p) {
     __shared__ long long sums[kUnitTok / 32], out[2];
     const TaskRun run = task_run<kUnitTok>(p, blockIdx.x, gridDim.x, sums, out);
-    grid_dependency_wait();
-    if (run.count == 0) return;
     // the unit of the run's last task
-    long long rest = run.rest + run.count - 1;
-    int b = run.b;
-    for (long long n; rest >= (n = tasks_of(p, b)); ++b) rest -= n;
-    const UnitWalk at(p, b, rest, 1);
-    const long long begin = run.from + run.count - 1 - (at.r - at.seq.first(at.u)), end = begin + at.seq.blocks - at.seq.first(at.u);
-    if (begin < run.from || end <= run.from + run.count) return;
+    bool there = run.count > 0;
+    long long begin = 0, end = 0;
+    float* to = nullptr;
+    float old = 0.0f;
+    if (there) {
+        long long rest = run.rest + run.count - 1;
+        int b = run.b;
+        for (long long n; rest >= (n = tasks_of(p, b)); ++b) rest -= n;
+        const UnitWalk at(p, b, rest, 1);
+        begin = run.from + run.count - 1 - (at.r - at.seq.first(at.u)), end = begin + at.seq.blocks - at.seq.first(at.u);
+        const int tok = at.u * p.unit_tok + threadIdx.x;
+        there = begin >= run.from && end > run.from + run.count && tok < at.s.len && (int)threadIdx.x < p.unit_tok;
+        if (there) {
+            int slot;
+            const int page = score_place(p, p.page_table + (long long)at.b * p.max_pages, tok, slot);
+            there = page >= 0;
+            if (there) to = score_slot(p, page, slot, at.h);
+            if (there && p.decay != 0.0f && tok < at.s.ctx) old = p.decay * *to;  // (no other block writes it)
+        }
+    }
+    grid_dependency_wait();
+    if (!there) return;
     float total = p.partial[((long long)blockIdx.x * 2 + 1) * kUnitTok + threadIdx.x];
     for (long long c = blockIdx.x + 1; c * run.each < end; ++c) total += p.partial[c * 2 * kUnitTok + threadIdx.x];
-    const int tok = at.u * p.unit_tok + threadIdx.x;
-    if (tok >= at.s.len || (int)threadIdx.x >= p.unit_tok) return;
-    int slot;
-    const int page = score_place(p, p.page_table + (long long)at.b * p.max_pages, tok, slot);
-    if (page < 0) return;
-    float* to = score_slot(p, page, slot, at.h);
-    *to = p.decay != 0.0f && tok < at.s.ctx ? fmaf(p.decay, *to, total) : total;
+    *to = old + total;
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool FOLD>
 cudaError_t launch_tiles(ScoreParams p, cudaStream_t stream) {
-    using L = ScoreLayout<D, FMT>;
+    using L = ScoreLayout<D, FMT, FOLD>;
     constexpr int bytes = L::kBytes, elem = L::kF8 ? 1 : 2;
     static std::atomic<bool> attr_set[kMaxAttrDevices];
-    cudaError_t e = ensure_smem_attr(score_tiles_kernel<D, FMT>, bytes, attr_set);
+    cudaError_t e = ensure_smem_attr(score_tiles_kernel<D, FMT, FOLD>, bytes, attr_set);
     if (e != cudaSuccess) return e;
     p.box_rows = p.page_size % 64 == 0 ? 64 : (p.page_size % 16 == 0 ? 16 : 1);
     // Units of 512 tokens read q half as often as units of 256, but there have to be units (of full tables, or tasks of them) for all SMs.
@@ -721,6 +774,8 @@ cudaError_t launch_tiles(ScoreParams p, cudaStream_t stream) {
     p.unit_tok = kUnitTok;
     auto tasks = [&]() { return heads * ((capacity + p.unit_tok - 1) / p.unit_tok) * (blocks < p.num_sms ? blocks : p.num_sms); };
     while (p.unit_tok > kTileTok && tasks() < p.num_sms) p.unit_tok /= 2;
+    p.unit_shift = p.unit_tok == 512 ? 9 : p.unit_tok == 256 ? 8 : 7;
+    p.unit_blocks = Divisor(p.unit_tok / p.block_tok);
     const unsigned grid = (unsigned)(tasks() < p.num_sms ? tasks() : p.num_sms);  // no more blocks than tasks
     // memory of the call: partial sums (unless a unit is one task), factors and parts of q
     const size_t rows = (size_t)p.T * p.Hq;
@@ -758,7 +813,7 @@ cudaError_t launch_tiles(ScoreParams p, cudaStream_t stream) {
         e = launch_kernel(split_q_kernel<D>, dim3((unsigned)((rows * (D / 8) + 255) / 256)), 256, 0, stream, {}, p.q, parts, p.factor, (long long)rows,
                           p.scale_log2);
     if (e == cudaSuccess)
-        e = launch_kernel(score_tiles_kernel<D, FMT>, dim3(grid), kTileThreads, bytes, stream, L::kF8 ? dependent : LaunchMode{}, p, tmQ, tmK);
+        e = launch_kernel(score_tiles_kernel<D, FMT, FOLD>, dim3(grid), kTileThreads, bytes, stream, dependent, p, tmQ, tmK);
     if (e == cudaSuccess && n_partial > 0) e = launch_kernel(score_join_kernel, dim3(grid), kUnitTok, 0, stream, dependent, p);
     if (ws) cudaFreeAsync(ws, stream);
     return e;
@@ -766,9 +821,12 @@ cudaError_t launch_tiles(ScoreParams p, cudaStream_t stream) {
 
 template <int D>
 cudaError_t launch_fmt(const ScoreParams& p, int fmt, cudaStream_t stream) {
-    return fmt == ATTN_FP8_E4M3   ? launch_tiles<D, ATTN_FP8_E4M3>(p, stream)
-           : fmt == ATTN_FP8_E5M2 ? launch_tiles<D, ATTN_FP8_E5M2>(p, stream)
-                                  : launch_tiles<D, ATTN_KV_BF16>(p, stream);
+    // Minus the LSE comes with the products where the scale lets it keep its 24 bits in three bf16 parts.
+    const bool fold = fabsf(p.scale_log2) > 0x1p-60f && fabsf(p.scale_log2) < 0x1p60f;
+    return fmt == ATTN_FP8_E4M3   ? launch_tiles<D, ATTN_FP8_E4M3, false>(p, stream)
+           : fmt == ATTN_FP8_E5M2 ? launch_tiles<D, ATTN_FP8_E5M2, false>(p, stream)
+           : fold                 ? launch_tiles<D, ATTN_KV_BF16, true>(p, stream)
+                                  : launch_tiles<D, ATTN_KV_BF16, false>(p, stream);
 }
 
 }  // namespace
@@ -777,7 +835,9 @@ cudaError_t launch_score_tiles(const ScoreParams& p_in, int d, int kv_format, cu
     ScoreParams p = p_in;
     // a block of rows: the heads of as many queries as fit, or 128 heads of one
     p.block_tok = p.G <= kBlockRows ? kBlockRows / p.G : 1;
+    p.by_block_tok = Divisor(p.block_tok);
     p.head_blocks = (p.G + kBlockRows - 1) / kBlockRows;
+    p.unit = (float)(-1.4426950408889634 / (double)p.scale_log2);
     return d == 128 ? launch_fmt<128>(p, kv_format, stream) : launch_fmt<64>(p, kv_format, stream);
 }
 

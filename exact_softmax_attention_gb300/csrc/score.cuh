@@ -11,6 +11,24 @@
 
 namespace attn {
 
+// x / d for 0 <= x < 2^31: multiplier ceil(2^(31+k) / d), k = ceil(log2 d).
+struct Divisor {
+    int d;
+    unsigned magic;
+    int shift;
+    Divisor() = default;
+    explicit Divisor(int divisor) : d(divisor), magic(0), shift(0) {
+        if (d == 1) return;
+        int k = 0;
+        while ((1LL << k) < d) ++k;
+        magic = (unsigned)(((1ULL << (31 + k)) + (unsigned long long)d - 1) / (unsigned long long)d);
+        shift = k - 1;
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int operator()(int x) const { return magic ? (int)(__umulhi((unsigned)x, magic) >> shift) : x; }
+#endif
+};
+
 struct ScoreParams {
     const __nv_bfloat16* q;  // [T, Hq, d]
     const float* lse;        // [T, Hq]
@@ -21,13 +39,15 @@ struct ScoreParams {
     const int* cu_seqlens;   // [B + 1] or nullptr: T / B rows each
     int B, T, max_q, Hq, Hkv, G, page_size, max_pages, num_pages, num_sms;
     float scale_log2, decay;  // scale (key descale included) times log2(e)
-    unsigned int ps_magic;   // tok / page_size by multiplication, as in DecodeParams
-    int ps_shift;
+    float unit;              // tiles: -log2(e) / scale_log2
+    Divisor by_page;
     int chunk, chunks;       // few rows: tokens per block, blocks of the longest sequence; 0: runs of all tokens there are
     // tiles: [blocks, 2, unit_tok] sums of units that lie in several blocks; 8-bit caches: factor of the scores of each row of q
     float *partial, *factor;
-    int unit_tok;                // tokens of a unit: 128, 256 or 512
+    int unit_tok, unit_shift;    // tokens of a unit: 128, 256 or 512; their logarithm
     int block_tok, head_blocks;  // tokens of a block of rows; blocks of rows of a token (one of the two is 1)
+    Divisor by_block_tok;
+    Divisor unit_blocks;         // blocks of rows for the tokens of a unit, rounded down, and the division by that
     int box_rows;                // rows of a copy of keys through the map (64 or 16, dividing the page size), 1: no map
     int* status;
     unsigned long long watchdog_ns;
@@ -73,7 +93,7 @@ __device__ __forceinline__ bool score_seq(const ScoreParams& p, int b, ScoreSeq&
 
 // Page-table index and slot of token tok (0 <= tok < 2^31).
 __device__ __forceinline__ int score_page(const ScoreParams& p, int tok, int& slot) {
-    const int q = p.ps_magic ? (int)(__umulhi((unsigned)tok, p.ps_magic) >> p.ps_shift) : tok;
+    const int q = p.by_page(tok);
     slot = tok - q * p.page_size;
     return q;
 }
