@@ -278,12 +278,12 @@ struct TaskRun {
     int b, count;
 };
 template <int kThreads>
-__device__ __forceinline__ TaskRun task_run(const ScoreParams& p, int block, int blocks, long long* sums, long long* out) {
-    constexpr int kWarps = kThreads / 32;
+__device__ __forceinline__ TaskRun task_run(const ScoreParams& p, int block, long long* sums, long long* out) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += tasks_of(p, b);
+    const int per = p.B <= kThreads ? 1 : (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    const long long first = b0 < b1 ? tasks_of(p, b0) : 0;
+    long long mine = first;
+    for (int b = b0 + 1; b < b1; ++b) mine += tasks_of(p, b);
     long long upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -293,20 +293,20 @@ __device__ __forceinline__ TaskRun task_run(const ScoreParams& p, int block, int
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
     long long total = 0;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w * 32 * per < p.B; ++w) {  // (warps that have sequences)
         if (w == warp) upto += total;
         total += sums[w];
     }
     TaskRun run;
-    run.each = (total + blocks - 1) / blocks;
+    run.each = total < INT32_MAX - p.grid.d ? p.grid((int)total + p.grid.d - 1) : (total + p.grid.d - 1) / p.grid.d;
     run.from = run.each * block;
     const long long left = total - run.from;
     run.count = (int)(left < run.each ? (left > 0 ? left : 0) : run.each);
     const long long ahead = upto - mine;
-    if (run.count > 0 && run.from >= ahead && run.from < upto) {
+    if (run.count > 0 && b0 < b1 && run.from >= ahead && run.from < upto) {
         long long rest = run.from - ahead;
         int b = b0;
-        for (long long n; rest >= (n = tasks_of(p, b)); ++b) rest -= n;
+        for (long long n = first; rest >= n; n = tasks_of(p, ++b)) rest -= n;
         out[0] = b;
         out[1] = rest;
     }
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tmem_relinquish();
     }
     tc_fence_before();
-    const TaskRun run = task_run<kTileThreads>(p, blockIdx.x, gridDim.x, reinterpret_cast<long long*>(smem + L::kLseOff), reinterpret_cast<long long*>(smem + L::kPlanOff));
+    const TaskRun run = task_run<kTileThreads>(p, blockIdx.x, reinterpret_cast<long long*>(smem + L::kLseOff), reinterpret_cast<long long*>(smem + L::kPlanOff));
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     if (run.count == 0) {
@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // Units that lie in more than one run: the block whose run begins one adds the parts up in order.
 __global__ void __launch_bounds__(kUnitTok) score_join_kernel(const __grid_constant__ ScoreParams p) {
     __shared__ long long sums[kUnitTok / 32], out[2];
-    const TaskRun run = task_run<kUnitTok>(p, blockIdx.x, gridDim.x, sums, out);
+    const TaskRun run = task_run<kUnitTok>(p, blockIdx.x, sums, out);
     // the unit of the run's last task
     bool there = run.count > 0;
     long long begin = 0, end = 0;
@@ -777,6 +777,7 @@ cudaError_t launch_tiles(ScoreParams p, cudaStream_t stream) {
     p.unit_shift = p.unit_tok == 512 ? 9 : p.unit_tok == 256 ? 8 : 7;
     p.unit_blocks = Divisor(p.unit_tok / p.block_tok);
     const unsigned grid = (unsigned)(tasks() < p.num_sms ? tasks() : p.num_sms);  // no more blocks than tasks
+    p.grid = Divisor((int)grid);
     // memory of the call: partial sums (unless a unit is one task), factors and parts of q
     const size_t rows = (size_t)p.T * p.Hq;
     const size_t n_partial = blocks > 1 ? (size_t)grid * 2 * kUnitTok : 0, n_factor = L::kF8 ? (rows + 3) / 4 * 4 : 0;

@@ -48,6 +48,7 @@ struct ScoreParams {
     int block_tok, head_blocks;  // tokens of a block of rows; blocks of rows of a token (one of the two is 1)
     Divisor by_block_tok;
     Divisor unit_blocks;         // blocks of rows for the tokens of a unit, rounded down, and the division by that
+    Divisor grid;                // blocks
     int box_rows;                // rows of a copy of keys through the map (64 or 16, dividing the page size), 1: no map
     int* status;
     unsigned long long watchdog_ns;
