@@ -193,6 +193,7 @@ __device__ __forceinline__ const T* of_part(const T* p, int rank) {
 template <bool QUADS, int PARTS>
 __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ EvictParams p) {
     grid_dependents_launch();
+    grid_dependency_wait();
     extern __shared__ __align__(16) uint32_t keys[];
     __shared__ int counts[3][2048], merged[PARTS > 1 ? 2048 : 1], scratch[35], totals[2];  // totals of this part: equals, marks
     __shared__ unsigned sums[32];
@@ -427,6 +428,7 @@ __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ Ev
 // The same from more tokens: the keys are read again for every step, and the tokens numbered in rounds of one per thread.
 __global__ void __launch_bounds__(kLongThreads, 1) select_long_kernel(const __grid_constant__ EvictParams p) {
     grid_dependents_launch();
+    grid_dependency_wait();
     __shared__ int hist[2048], scratch[35], sums[32], place[kPairs];
     const int tid = threadIdx.x, lane = tid & 31;
     SelectRow s;
@@ -489,7 +491,8 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const __gri
     __shared__ int src[kMoves], dst[kMoves];  // cache rows of the moves listed
     __shared__ unsigned sums[32];
     __shared__ int total;
-    grid_dependency_wait();                             // (launched as a programmatic dependent of what is before it)
+    grid_dependents_launch();
+    grid_dependency_wait();
     const int b = (int)(blockIdx.x / (unsigned)p.Hkv), h = (int)(blockIdx.x % (unsigned)p.Hkv);
     const int n = min(__ldg(p.seqlens + b), p.budget), limit = p.max_pages * p.page_size;
     const int* kept = p.kept + (long long)blockIdx.x * p.budget;
@@ -581,7 +584,7 @@ cudaError_t launch_select(EvictParams p, bool quads, long long groups, long long
     const auto kernel = quads ? select_kernel<true, PARTS> : select_kernel<false, PARTS>;
     const cudaError_t e = ensure_smem_attr(kernel, kPartGroups * kGroupBytes, attr_set[quads]);
     if (e != cudaSuccess) return e;
-    return launch_kernel(kernel, dim3((unsigned)(rows * PARTS)), threads, (size_t)p.groups * kGroupBytes, stream, {false, PARTS > 1 ? PARTS : 0}, p);
+    return launch_kernel(kernel, dim3((unsigned)(rows * PARTS)), threads, (size_t)p.groups * kGroupBytes, stream, {true, PARTS > 1 ? PARTS : 0}, p);
 }
 
 bool multiple(const void* p, long long bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
@@ -637,7 +640,7 @@ extern "C" attn_status_t attn_kv_select_paged(const float* score, const int* pag
     const bool quads = page_size % 4 == 0 && multiple(score, 16);
     cudaError_t e;
     if (groups > (long long)kPartGroups * parts || rows * parts > INT32_MAX)
-        e = launch_kernel(select_long_kernel, dim3((unsigned)rows), kLongThreads, 0, cs, {}, p);
+        e = launch_kernel(select_long_kernel, dim3((unsigned)rows), kLongThreads, 0, cs, {true}, p);
     else
         e = parts == 1   ? launch_select<1>(p, quads, groups, rows, num_sms, cs)
             : parts == 2 ? launch_select<2>(p, quads, groups, rows, num_sms, cs)

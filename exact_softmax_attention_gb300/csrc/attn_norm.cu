@@ -172,6 +172,8 @@ __device__ __forceinline__ void turn_item(float (&xa)[V], float (&xb)[V], const 
 // W > 0: a head is exactly W lanes of R items; 0: p.lanes, the last ones may be idle.
 template <typename E, int V, int R, int W>
 __global__ void __launch_bounds__(256, norm_blocks(R)) norm_rope_kernel(const __grid_constant__ NormParams p) {
+    grid_dependents_launch();
+    grid_dependency_wait();
     extern __shared__ __align__(16) float shared[];
     typedef typename RawOf<E, V>::type Raw;
     const int half = p.cols.rot / 2, d = p.cols.d, H = p.heads[0] + p.heads[1];
@@ -243,6 +245,8 @@ __global__ void __launch_bounds__(256, norm_blocks(R)) norm_rope_kernel(const __
 // from the L1).
 template <typename E>
 __global__ void __launch_bounds__(256) norm_rope_any_kernel(const __grid_constant__ NormParams p) {
+    grid_dependents_launch();
+    grid_dependency_wait();
     extern __shared__ __align__(16) float shared[];
     const int half = p.cols.rot / 2, d = p.cols.d, H = p.heads[0] + p.heads[1];
     float* w = shared;
@@ -289,6 +293,7 @@ __device__ __forceinline__ void block_sums(const NormParams& p, const float* row
 template <typename E, int V, int R, int W>
 __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(const __grid_constant__ NormParams p) {
     grid_dependents_launch();
+    grid_dependency_wait();
     extern __shared__ __align__(16) float shared[];
     typedef typename RawOf<E, V>::type Raw;
     const int half = p.cols.rot / 2, d = p.cols.d;
@@ -410,6 +415,7 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
 template <typename E>
 __global__ void __launch_bounds__(256) norm_rope_bwd_any_kernel(const __grid_constant__ NormParams p) {
     grid_dependents_launch();
+    grid_dependency_wait();
     extern __shared__ __align__(16) float shared[];
     const int half = p.cols.rot / 2, d = p.cols.d, lane = threadIdx.x & 31;
     float* w = shared;
@@ -491,8 +497,8 @@ void head_shape(int items, int& lanes, int& each) {
 
 template <typename E, int V, int R, int W>
 cudaError_t launch_wide(const NormParams& p, bool back, unsigned blocks, unsigned threads, size_t smem, cudaStream_t s) {
-    return back ? launch_kernel(norm_rope_bwd_kernel<E, V, R, W>, dim3(blocks), threads, smem, s, {}, p)
-                : launch_kernel(norm_rope_kernel<E, V, R, W>, dim3(blocks), threads, smem, s, {}, p);
+    return back ? launch_kernel(norm_rope_bwd_kernel<E, V, R, W>, dim3(blocks), threads, smem, s, {true}, p)
+                : launch_kernel(norm_rope_kernel<E, V, R, W>, dim3(blocks), threads, smem, s, {true}, p);
 }
 
 // The common widths have kernels of their own (64, 128 and 256, and with V = 8 items of bf16 192: three items on 4 lanes).
@@ -541,8 +547,8 @@ cudaError_t launch_norm(NormParams p, bool wide, bool back, int num_sms, float* 
     }
     if (blocks > 0) {
         if (!wide)
-            e = back ? launch_kernel(norm_rope_bwd_any_kernel<E>, dim3((unsigned)blocks), threads, smem, s, {}, p)
-                     : launch_kernel(norm_rope_any_kernel<E>, dim3((unsigned)blocks), threads, smem, s, {}, p);
+            e = back ? launch_kernel(norm_rope_bwd_any_kernel<E>, dim3((unsigned)blocks), threads, smem, s, {true}, p)
+                     : launch_kernel(norm_rope_any_kernel<E>, dim3((unsigned)blocks), threads, smem, s, {true}, p);
         else
             e = launch_shape<E, V>(p, each, back, (unsigned)blocks, threads, smem, s);
     }

@@ -66,6 +66,8 @@ __device__ __forceinline__ int steps_of(const ScoreParams& p, int b, int step) {
 // NT: groups of 8 rows.
 template <int D, int FMT, int NT>
 __global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_BF16, NT)) score_rows_kernel(const __grid_constant__ ScoreParams p) {
+    grid_dependents_launch();
+    grid_dependency_wait();
     constexpr bool F8 = FMT != ATTN_KV_BF16;
     constexpr int TG = kRowGroups<D, F8>, TE = 2 * TG;  // groups of 16 tokens, of 8
     constexpr int kLoads = F8 ? D / 64 : D / 32;     // 16-byte loads of a lane per token
@@ -293,7 +295,7 @@ cudaError_t launch_rows(ScoreParams p, cudaStream_t stream) {
         const long long x = slots / groups;
         grid = dim3((unsigned)(x > 0 ? x : 1), (unsigned)groups);
     }
-    return launch_kernel(score_rows_kernel<D, FMT, NT>, grid, (unsigned)(heads * parts * 32), 0, stream, {}, p);
+    return launch_kernel(score_rows_kernel<D, FMT, NT>, grid, (unsigned)(heads * parts * 32), 0, stream, {true}, p);
 }
 
 template <int D, int FMT>
