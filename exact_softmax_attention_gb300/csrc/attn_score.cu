@@ -277,10 +277,15 @@ int resident_blocks(Kernel kernel, int threads, std::atomic<int> (&known)[kRowWa
 template <int D, int FMT, int NT>
 cudaError_t launch_rows(ScoreParams p, cudaStream_t stream) {
     static std::atomic<int> known[kRowWarps + 1];
-    const int heads = p.Hkv < kRowWarps ? p.Hkv : kRowWarps, parts = kRowWarps / heads;
+    const int heads = p.Hkv < kRowWarps ? p.Hkv : kRowWarps;
+    // As many warps as an SM holds, in the largest blocks that give so many: with 3 heads blocks of 3 warps (15) instead of 6 (12).
+    auto blocks_of = [&](int parts) { return resident_blocks(score_rows_kernel<D, FMT, NT>, heads * parts * 32, known); };
+    int parts = kRowWarps / heads;
+    for (int x = parts - 1; x > 0; --x)
+        if (blocks_of(x) * x > blocks_of(parts) * parts) parts = x;
     const long long groups = (p.Hkv + heads - 1) / heads, capacity = (long long)p.max_pages * p.page_size;
     const int step = 16 * kRowGroups<D, FMT != ATTN_KV_BF16> * parts;
-    const long long slots = (long long)p.num_sms * resident_blocks(score_rows_kernel<D, FMT, NT>, heads * parts * 32, known);
+    const long long slots = (long long)p.num_sms * blocks_of(parts);
     // pieces of every sequence's table for as many blocks as run at once, a few steps each at least; if that is too many blocks, runs
     long long c = ((long long)p.B * capacity * groups + slots - 1) / slots;
     c = (c + step - 1) / step * step;
