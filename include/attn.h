@@ -437,7 +437,7 @@ attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq
  * k_cache, page_table, page_size, max_pages_per_seq, num_pages, kv_format, k_descale  as for attn_decode_paged_tree
  * score      device, fp32 [num_pages, Hkv, page_size], the sums of the cache's slots (read and written; with decay = 0 not
  *            read). Only the slots of tokens below seqlens[b] of sequences with rows are touched. A slot that several of these
- *            sequences share is left to one of them.
+ *            sequences share gets the sum of one of them or of several, which is not defined.
  * seqlens    device, int32 [B], cached tokens of each sequence, those of the rows included
  * cu_seqlens device, int32 [B+1], prefix offsets of the sequences' rows in q and lse (non-decreasing, empty sequences allowed), or
  *            NULL: T / B rows each
@@ -446,10 +446,13 @@ attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq
  * decay      finite; 1 adds to the old sums, 0 overwrites them
  * A sequence whose length is below its rows or above its page table, or whose offsets decrease, pass T or hold more than max_q rows, is
  * recorded as ATTN_ERR_DEVICE_BAD_INDEX and its slots are left as they were; so are those of a page outside [0, num_pages).
- * Arithmetic: products on the tensor cores with fp32 accumulation (bf16, or for 8-bit caches f16: codes widened exactly, q scaled per row
- * by a power of two that is given back, exact for elements down to 2^-29 of the row's largest), fp32 exponentials and sums, which are
- * added in a fixed order. Many rows of few tokens are split between the SMs: their parts then take memory from the library's
- * stream-ordered pool on `stream` and a second kernel, launched as a programmatic dependent.
+ * A key with an element that is not finite leaves the sum of its token and kv head undefined, and no other.
+ * Arithmetic: products on the tensor cores with fp32 accumulation, fp32 exponentials and sums, which are added in a fixed order. bf16 keys
+ * are multiplied as they are. With few rows per kv head (max_q * Hq / Hkv up to 32 for d = 64, 24 for d = 128) 8-bit codes are widened exactly
+ * to f16 and q is scaled per row by a power of two that is given back, exact for elements down to 2^-29 of the row's largest. With more rows
+ * 8-bit codes are multiplied as they are by q in two e4m3 parts, exact for elements down to 2^-9 of the row's largest, others are off by at
+ * most 2^-17 of that. There a call takes memory from the library's stream-ordered pool on `stream`: T * Hq * (2 d + 4) bytes for the parts of q
+ * (8-bit caches), 4 KB an SM for sums of tokens whose rows are split between SMs, which a second kernel joins.
  * Alignment: q, k_cache 16 bytes; the others 4.
  */
 attn_status_t attn_kv_score_paged(const void* q, const float* lse, const void* k_cache, float* score, const int* page_table,

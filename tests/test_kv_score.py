@@ -244,6 +244,36 @@ def test_rows_that_saw_nothing_and_nan(A, n, lens):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n,lens", [([1, 1], [50, 300]), ([40, 33], [300, 200])])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("scale", [0.1, -0.1, 1e-15, 1e15, 1e-25, 1e25])
+def test_lse_far_out(A, n, lens, fmt, scale):
+    """An LSE far above every score gives weight 0, one far below weight infinity, NaN gives NaN to the tokens that its row sees."""
+    p = Problem(n, lens, 8, 2, 128, 16, fmt, seed=6, q_size=2.0 / max(1.0, abs(scale)), scale=scale)
+    first = lens[1] - n[1]  # the last token that the first row of sequence 1 sees
+    kept = p.lse.clone()
+    before, results = p.score.clone(), []
+    for value in (-math.inf, math.inf, 3e38, 1e9):
+        p.lse.copy_(kept)
+        p.lse[:, 0::4] = value  # a query head of each kv head
+        p.score.copy_(before)
+        p.run(A)
+        results.append(p.score.clone())
+    assert all(torch.equal(results[0], x) for x in results[1:])  # as heads that saw nothing
+    for value, wrong in ((-3e38, torch.isposinf), (-1e9, torch.isposinf), (math.nan, torch.isnan)):
+        p.lse.copy_(kept)
+        p.lse[n[0], 3] = value  # kv head 0
+        p.score.zero_()
+        p.run(A)
+        pg, sl = p.places(1)
+        got = p.score[pg, :, sl]
+        assert wrong(got[:first + 1, 0]).all() and torch.isfinite(got[first + 1:, 0]).all() and torch.isfinite(got[:, 1]).all()
+        pg, sl = p.places(0)
+        assert torch.isfinite(p.score[pg, :, sl]).all()
+    assert A.attn_get_device_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n,lens", [([1, 1, 1], [50, 300, 20]), ([40, 33, 5], [300, 200, 20]), ([500, 33, 5], [600, 200, 20])])
 def test_bad_lengths_pages_and_offsets(A, n, lens):
     bad = A.ATTN_ERR_DEVICE_BAD_INDEX
