@@ -26,7 +26,8 @@ constexpr int kNormMaxDim = 1024;
 constexpr int norm_blocks(int items) { return items == 1 ? 5 : 2; }
 constexpr int norm_bwd_blocks(int items) { return items == 1 ? 2 : 1; }
 constexpr int kNormItems = 8;      // heads per group of lanes, at least
-constexpr int kNormAngles = 8192;  // floats for the angles of a block's tokens
+constexpr int kNormAngles = 8192;  // floats for the angles of a block's tokens, at most
+constexpr int kNormShared = 12288; // for them, the weights and the warps' sums (48 KB)
 
 struct NormParams {
     const void* in[2];     // q, k
@@ -529,10 +530,12 @@ cudaError_t launch_norm(NormParams p, bool wide, bool back, int num_sms, float* 
     // tokens per block: some heads for every group of lanes, no more than the angles have room for
     const int H = p.heads[0] + p.heads[1], groups = threads / p.lanes;
     long long n = back ? kNormAngles : ((long long)kNormItems * groups + H - 1) / H;
-    if (p.cols.rot > 0 && n > kNormAngles / p.cols.rot) n = kNormAngles / p.cols.rot;
+    const int rows = 2 + (back ? (int)threads / 32 : 0);  // of shared memory, besides the angles
+    const int angles = kNormShared - rows * p.cols.d < kNormAngles ? kNormShared - rows * p.cols.d : kNormAngles;
+    if (p.cols.rot > 0 && n > angles / p.cols.rot) n = angles / p.cols.rot;
     p.tokens = p.T > 0 ? whole_waves(p.T, n, (long long)num_sms * (back ? norm_bwd_blocks(each) : norm_blocks(each))) : 1;
     const long long blocks = ((long long)p.T + p.tokens - 1) / p.tokens;
-    const size_t smem = ((size_t)p.tokens * p.cols.rot + (2 + (back ? threads / 32 : 0)) * (size_t)p.cols.d) * sizeof(float);
+    const size_t smem = ((size_t)p.tokens * p.cols.rot + (size_t)rows * p.cols.d) * sizeof(float);
     const bool sums = back && (dq_weight || dk_weight);
     cudaError_t e = cudaSuccess;
     void* ws = nullptr;

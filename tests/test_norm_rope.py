@@ -208,6 +208,13 @@ def test_gradient(A, T, Hq, Hk, d, begin, rot, inter, et, weights):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,d,et", [(1216, 1024, "f32"), (4864, 512, "bf16"), (1300, 1022, "f32")])
+def test_gradient_of_wide_heads_with_many_angles(A, T, d, et):
+    """Rows of wide heads for the weights' sums next to the angles of as many tokens as a block takes."""
+    test_gradient(A, T, 1, 0, d, 0, d, 0, et, True)
+
+
+@pytest.mark.gpu
 def test_gradient_by_differences(A):
     """<dL/dx, v> and <dL/dw, u> against central differences of the forward call."""
     T, Hq, Hk, d, h = 6, 2, 1, 64, 2.0**-5
