@@ -12,6 +12,11 @@
 // weights lie in shared memory. A lane keeps its columns over all heads, so the weights' gradient is a sum in its
 // registers, joined over the block at the end; a second kernel adds the blocks' sums in a fixed order. No atomics: the
 // same call gives the same bytes.
+//
+// Measured, bf16, 40 heads of 128, 18432 rows: 62.3 us, 6060 GB/s, 0.89 of a copy's rate (instructions issue in 69 % of the cycles); the gradient
+// of 16384 rows 90.6 us, 5560 GB/s, 0.82 (16 warps of 118 registers on an SM, waiting for loads). fp32, 32 heads
+// of 192, 64 interleaved columns rotated, 8192 rows, gradient: 98.6 us, 6120 GB/s. Not kept: heads loaded two or three ahead (forward 75-85 us), four or eight heads of a
+// token for each group of lanes with angles and weights in registers (86-93).
 #include "attn.h"
 #include "launch.cuh"
 #include "rows.cuh"

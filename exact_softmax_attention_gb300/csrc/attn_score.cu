@@ -9,6 +9,11 @@
 // tokens (narrower rows: 32) are loaded while these are multiplied, and the page table is read one group ahead of them. A block's warps take
 // the kv heads of the same tokens, so a cache row is read as a whole.
 //
+// Measured, 64 sequences of U[1K, 32K] tokens, 32/8 heads of 128: bf16 327 us, 6790 GB/s (the rate of a copy); e4m3 198 us, 5800 GB/s (loads that
+// the warps wait for, two blocks of 8 warps on an SM). 48 x U[1, 8000], 1-6 rows of 4 heads x 3 heads of 64, e5m2, pages of 7: 21 us for 41 MB, a
+// chain of dependent loads in one wave of blocks (without the exponentials of rows that a sequence has not, or with the keys loaded before the rows:
+// no change).
+//
 // Work order. When the blocks of all sequences' full tables run at once, a block has a piece of a sequence. Else the tokens that there are,
 // of all sequences one after the other, are dealt out in equal runs to as many blocks as the SMs hold: every SM is busy to the end, however
 // ragged the lengths (pieces of 1024 tokens: 64 sequences of U[1K, 32K] x 8 heads of 128 361 us, with e4m3 282 us).

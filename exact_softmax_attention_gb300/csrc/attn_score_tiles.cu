@@ -8,15 +8,31 @@
 // tasks of the whole call, in the order sequence, kv head, tokens, rows, are dealt out in equal runs to one persistent block per SM. A unit
 // that lies in more than one run leaves partial sums, which a second kernel adds in order.
 //
-// What bounds it. With d = 128 a task is 4 x 8 products of 128 x 128 x 16, 2048 clocks of the tensor pipe, and 65536
-// exponentials, 2048 clocks of the MUFU, for 32 KB of q from the L2 (with units of 256 tokens the L2 was the bound: 153 us for the whole prompts
-// below); rows that stay the same (up to 128) against new tokens every task are 128 KB of bf16 keys for that, more than the memory delivers
-// in the time.
+// What bounds it. With d = 128 a task is 4 x 8 products of 128 x 128 x 16 and 65536 exponentials, 2048 clocks of the tensor pipe and of the MUFU,
+// for 32 KB of q from the L2 (with units of 256 tokens the L2 was the bound: 153 us for the whole prompts below). Measured: 3300 clocks, the
+// tensor pipe 57 % busy, the MUFU 51 %. The products take 92 clocks each, not 64, because both operands come out of shared memory, and a tile's
+// only buffer is held through the products and three quarters of the exponentials. Rows that stay the same (up to 128) against new tokens every
+// task are 128 KB of bf16 keys for that, more than the memory delivers in the time.
+// Whole prompts, 8 x U[512, 4096] tokens, 32/8 heads of 128, bf16: 130 us, 1020 TFLOP/s (without exponentials 107 us, with an eighth of the
+// products 132, with neither 69). The last 32 queries of 16 x U[2K, 16K] cached
+// tokens: 52 us, 5.4 TB/s.
+// Other arrangements, whole prompts, at 138 us then: 32 columns of all tiles to four warps each 179 us; 64 columns of all tiles to four of eight
+// warps with their LSE in registers 258; eight warps for every other tile 160; the two product threads in turns 143; later, at 130: keys in
+// tensor memory as operand A, products with 64 rows at a time, 161; parts of 32 columns left out in tiles on the diagonal 159; shares of the work
+// by the tiles that a task's rows see, instead of by tasks, 133.
+//
+// The LSE. exp2(c s - l) is exp2(c (s - l / c)): for bf16 keys -l / c comes with the products, as three more columns of q (its bf16 parts) against
+// ones, which spares a load from shared memory per column (128 us -> 126). Where the scale does not leave it 24 bits (2^-60 < |c| < 2^60 does), and for
+// 8-bit keys, whose rows have factors of their own, it is read per column.
 //
 // Roles of the warps: 0-15 exponentials and sums, four warps per accumulator tile; 16 and 17 the keys of two tiles each, through tensor
 // copies of 64 or 16 rows where the page size is a multiple of that, else by 16-byte copies of rows that the page table gives; 18 the blocks
 // of q through tensor copies (one box is the heads of as many queries as fit) and their LSE; 19 and 20 the products of two tiles each,
 // issued by one thread: while one waits for its buffer, the other one's products run.
+//
+// Start. 14500 clocks passed before the first product, 5300 in the shares of the work and 2900 in the search of its first task, mostly divisions;
+// with multipliers for them, as a programmatic dependent, and with the joining kernel's own search done before it waits: 138 -> 130 us,
+// the queries against cached tokens 55.7 -> 52.4.
 //
 // 8-bit caches: K is multiplied as it is (kind::f8f6f4). A kernel before this one scales each row of q by a power of two and splits
 // it into two e4m3 parts: exact unless an element is more than 2^9 below the row's largest (then off by at most 2^-17 of that).

@@ -58,8 +58,9 @@ cudaError_t launch_score_rows(const ScoreParams& p, int d, int kv_format, cudaSt
 cudaError_t launch_score_tiles(const ScoreParams& p, int d, int kv_format, cudaStream_t stream);
 
 // Rows per kv head (queries x query heads) up to which a warp's products take them; more go to the tiles. Measured, us, products / tiles, 32 x
-// U[1333, 4000] tokens: 8 heads of 64, 32 rows, bf16 28.8 / 32.7, e4m3 28.8 / 34.7; 2 heads of 128, 20 rows, 15.0 / 18.5, e4m3 16.6 / 19.2;
-// one of 128, 24 rows, 12.3 / 15.5 (48 x U[5333, 16000] 30.7 / 31.3); 8 heads of 128, 32 rows, 63 / 39.
+// U[1333, 4000] tokens: 8 heads of 64, 24 rows, bf16 26.2 / 29.0, e4m3 22.7 / 32.1; 32 rows 30.9 / 29.0, 27.8 / 31.7; one head, 32 rows, 8.4 / 11.3,
+// 9.6 / 14.4. 8 heads of 128, 16 rows, 36.4 / 35.6, e4m3 26.6 / 34.2; 24 rows 38.6 / 35.5, 40.2 / 34.4; one head, 24 rows, 10.0 / 12.2, 11.0 / 14.7;
+// 8 heads, 32 rows, 63 / 36.
 constexpr int score_few_rows(int d) { return d == 64 ? 32 : 24; }
 
 #ifdef __CUDACC__
