@@ -9,13 +9,16 @@
 // then the tails, as many of either: hole k takes tail k. Bounded by latency and instructions: the loads, a dozen steps of the whole block,
 // and about ten instructions per pass and 32 tokens. Several blocks share a row where rows are long and few: a block counts and marks its part,
 // and the others read the counts in its shared memory. (One block for each row, votes on 32 tokens: 16 x 8 rows of up to 32768 tokens 25 us,
-// 64 x 8 rows of 4100-4352 tokens 21 us; with keys in registers, four digits of 8 bits, and a numbering per 1024 tokens about 100 us.)
+// 64 x 8 rows of 4100-4352 tokens 21 us; with keys in registers, four digits of 8 bits, and a numbering per 1024 tokens about 100 us.) Now, on new
+// scores in a graph: 8 rows of 1000 tokens 7.2 us, 16 x 8 of U[2048, 32768] 20, 64 x 8 of U[4100, 4352] 18.5.
 //
 // Compaction: row kept[j] -> j with kept[j] >= j. A block lists the slots that get another row, in ascending order, with the
 // cache rows of both, and moves them in runs: it loads the rows of a run, then stores them. Every row that it reads later belongs to a slot
 // behind the run, and so lies there too: nothing is overwritten that is still needed, and only the loads and the stores of one run
 // need a barrier between them. Blocks share nothing: one has a (sequence, kv head) and some 16-byte columns of its rows, fewer columns
-// where there are few sequences. Bounded by the memory. (Walking all slots instead of a list took 150 us more in that case.)
+// where there are few sequences. Measured on new scores: 16 x 8 x U[2048, 32768] tokens to 2048, bf16 heads of 128, 198011 rows of K and of V
+// in and out, 43 us, 4.7 TB/s; 64 x 8 x U[4100, 4352] to 4096, e4m3, 196210 rows, 26.6 us, 3.8 TB/s: the memory, behind the chain list, pages, rows of each
+// block. (Walking all slots instead of a list took 150 us more in the first case; blocks of 256 threads, three or four on an SM, 47-55 and 29-31 us.)
 #include "attn.h"
 #include "kernels.cuh"
 #include "launch.cuh"
