@@ -14,8 +14,8 @@
 // same call gives the same bytes.
 //
 // Measured, bf16, 40 heads of 128, 18432 rows: 62.3 us, 6060 GB/s, 0.89 of a copy's rate (instructions issue in 69 % of the cycles); the gradient
-// of 16384 rows 90.6 us, 5560 GB/s, 0.82 (16 warps of 118 registers on an SM, waiting for loads). fp32, 32 heads
-// of 192, 64 interleaved columns rotated, 8192 rows, gradient: 98.6 us, 6120 GB/s. Not kept: heads loaded two or three ahead (forward 75-85 us), four or eight heads of a
+// of 16384 rows 84.3 us, 5970 GB/s, 0.88. fp32, 32 heads
+// of 192, 64 interleaved columns rotated, 8192 rows, gradient: 98 us, 6170 GB/s. Not kept: heads loaded two or three ahead (forward 75-85 us), four or eight heads of a
 // token for each group of lanes with angles and weights in registers (86-93).
 #include "attn.h"
 #include "launch.cuh"
@@ -30,6 +30,10 @@ constexpr int kNormMaxDim = 1024;
 // Blocks of 256 threads that an SM holds, by the items per lane: their registers (48 to 255 per thread).
 constexpr int norm_blocks(int items) { return items == 1 ? 5 : 2; }
 constexpr int norm_bwd_blocks(int items) { return items == 1 ? 2 : 1; }
+// Heads that a group of lanes of the gradient has in shared memory or on their way there, 64 bytes of a lane for each of its items: with one
+// item per lane two are on their way while one is computed (16384 rows of 40 heads of 128: 84.3 us; one, in registers, 90.6; three 89; four 87).
+template <int R>
+constexpr int kNormStages = R == 1 ? 3 : 2;
 constexpr int kNormItems = 8;      // heads per group of lanes, at least
 constexpr int kNormAngles = 8192;  // floats for the angles of a block's tokens, at most
 constexpr int kNormShared = 12288; // for them, the weights and the warps' sums (48 KB)
@@ -301,9 +305,11 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
     grid_dependents_launch();
     grid_dependency_wait();
     extern __shared__ __align__(16) float shared[];
-    typedef typename RawOf<E, V>::type Raw;
+    constexpr int kStages = kNormStages<R>;
     const int half = p.cols.rot / 2, d = p.cols.d;
-    float* w = shared;
+    uint4* ring = reinterpret_cast<uint4*>(shared) + threadIdx.x;  // [stage][item][x a, x b, dy a, dy b][thread]
+    auto piece = [&](int stage, int r, int x) { return ring + ((stage * R + r) * 4 + x) * (int)blockDim.x; };
+    float* w = shared + kStages * R * 16 * (int)blockDim.x;
     float* rows = w + 2 * d;  // [warps][d]
     float* cs = rows + (blockDim.x >> 5) * d;
     float* sn = cs + p.tokens * half;
@@ -323,33 +329,40 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
     __syncthreads();
     for (int k = 0; k < 2; ++k) {  // the heads of q, then of k
         if (p.heads[k] == 0) continue;
-        HeadWalk at(threadIdx.x >> shift, groups, p.heads[k]);
-        Raw ra[R], rb[R], ga[R], gb[R];
-        auto load = [&]() {
-            const E* src = static_cast<const E*>(p.in[k]) + (t0 + at.t) * p.in_stride[k] + (long long)at.h * d;
-            const E* grad = static_cast<const E*>(p.grad[k]) + (t0 + at.t) * p.grad_stride[k] + (long long)at.h * d;
+        HeadWalk at(threadIdx.x >> shift, groups, p.heads[k]), ahead = at;
+        auto load = [&](int stage) {
+            if (ahead.t < tokens) {
+                const E* src = static_cast<const E*>(p.in[k]) + (t0 + ahead.t) * p.in_stride[k] + (long long)ahead.h * d;
+                const E* grad = static_cast<const E*>(p.grad[k]) + (t0 + ahead.t) * p.grad_stride[k] + (long long)ahead.h * d;
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (some[r]) {
-                    ra[r] = load_raw<E, V>(src + a[r]), rb[r] = load_raw<E, V>(src + b[r]);
-                    ga[r] = load_raw<E, V>(grad + a[r]), gb[r] = load_raw<E, V>(grad + b[r]);
-                }
+                for (int r = 0; r < R; ++r)
+                    if (some[r]) {
+                        cp_async16(smem_u32(piece(stage, r, 0)), src + a[r], 16), cp_async16(smem_u32(piece(stage, r, 1)), src + b[r], 16);
+                        cp_async16(smem_u32(piece(stage, r, 2)), grad + a[r], 16), cp_async16(smem_u32(piece(stage, r, 3)), grad + b[r], 16);
+                    }
+            }
+            cp_async_commit();
+            ahead.next();
         };
-        if (at.t < tokens) load();
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) load(s);
         float wa_sum[R][V] = {}, wb_sum[R][V] = {};
         const int all = tokens * p.heads[k];
+        int stage = 0;
         for (int i = (threadIdx.x & ~31) >> shift; i < all; i += groups) {
             const bool mine = at.t < tokens;
             const int t = at.t, h = at.h;
+            cp_async_wait<kStages - 2>();
             float xa[R][V], xb[R][V], ya[R][V], yb[R][V], ss[2] = {0.0f, 0.0f}, dot[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 if (!some[r]) continue;
-                unpack<E, V>(ra[r], xa[r]), unpack<E, V>(rb[r], xb[r]);
-                unpack<E, V>(ga[r], ya[r]), unpack<E, V>(gb[r], yb[r]);
+                unpack<E, V>(*piece(stage, r, 0), xa[r]), unpack<E, V>(*piece(stage, r, 1), xb[r]);
+                unpack<E, V>(*piece(stage, r, 2), ya[r]), unpack<E, V>(*piece(stage, r, 3), yb[r]);
             }
             at.next();
-            if (at.t < tokens) load();
+            load(stage == 0 ? kStages - 1 : stage - 1);  // (where the head before this one was)
+            stage = stage + 1 == kStages ? 0 : stage + 1;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 if (!some[r]) continue;
@@ -396,6 +409,7 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
                 store_row<V>(dst + b[r], xb[r]);
             }
         }
+        cp_async_wait<0>();
         if (!p.partial) continue;
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -503,8 +517,14 @@ void head_shape(int items, int& lanes, int& each) {
 
 template <typename E, int V, int R, int W>
 cudaError_t launch_wide(const NormParams& p, bool back, unsigned blocks, unsigned threads, size_t smem, cudaStream_t s) {
-    return back ? launch_kernel(norm_rope_bwd_kernel<E, V, R, W>, dim3(blocks), threads, smem, s, {true}, p)
-                : launch_kernel(norm_rope_kernel<E, V, R, W>, dim3(blocks), threads, smem, s, {true}, p);
+    if (back) {
+        static std::atomic<bool> attr_set[kMaxAttrDevices];
+        const size_t ring = (size_t)kNormStages<R> * R * 64 * threads;
+        const cudaError_t e = ensure_smem_attr(norm_rope_bwd_kernel<E, V, R, W>, (int)(kNormStages<R> * R * 64 * 256 + kNormShared * 4), attr_set);
+        if (e != cudaSuccess) return e;
+        return launch_kernel(norm_rope_bwd_kernel<E, V, R, W>, dim3(blocks), threads, ring + smem, s, {true}, p);
+    }
+    return launch_kernel(norm_rope_kernel<E, V, R, W>, dim3(blocks), threads, smem, s, {true}, p);
 }
 
 // The common widths have kernels of their own (64, 128 and 256, and with V = 8 items of bf16 192: three items on 4 lanes).
