@@ -8,14 +8,14 @@
 //
 // A group of W lanes, W a power of two, holds a whole head in registers: R items per lane, each two runs of V
 // columns that the rotation pairs (item_cols). So the sums over a head are a few shuffles, the head is read once,
-// and the next head is loaded while this one is computed. Angles (one set per token, shared by all heads) and
+// and the next ones are copied to shared memory, every lane's pieces to its own places, while this one is computed. Angles (one set per token, shared by all heads) and
 // weights lie in shared memory. A lane keeps its columns over all heads, so the weights' gradient is a sum in its
 // registers, joined over the block at the end; a second kernel adds the blocks' sums in a fixed order. No atomics: the
 // same call gives the same bytes.
 //
-// Measured, bf16, 40 heads of 128, 18432 rows: 62.3 us, 6060 GB/s, 0.89 of a copy's rate (instructions issue in 69 % of the cycles); the gradient
+// Measured, bf16, 40 heads of 128, 18432 rows: 59.1 us, 6390 GB/s, 0.94 of a copy's rate; the gradient
 // of 16384 rows 84.3 us, 5970 GB/s, 0.88. fp32, 32 heads
-// of 192, 64 interleaved columns rotated, 8192 rows, gradient: 98 us, 6170 GB/s. Not kept: heads loaded two or three ahead (forward 75-85 us), four or eight heads of a
+// of 192, 64 interleaved columns rotated, 8192 rows, gradient: 98 us, 6170 GB/s. Not kept: heads loaded two or three ahead into registers (forward 75-85 us), four or eight heads of a
 // token for each group of lanes with angles and weights in registers (86-93).
 #include "attn.h"
 #include "launch.cuh"
@@ -27,9 +27,13 @@ namespace attn {
 namespace {
 
 constexpr int kNormMaxDim = 1024;
-// Blocks of 256 threads that an SM holds, by the items per lane: their registers (48 to 255 per thread).
-constexpr int norm_blocks(int items) { return items == 1 ? 5 : 2; }
+// Blocks of 256 threads that an SM holds, by the items per lane: their registers (64 to 255 per thread).
+constexpr int norm_blocks(int items) { return items == 1 ? 4 : 2; }
 constexpr int norm_bwd_blocks(int items) { return items == 1 ? 2 : 1; }
+// Heads that a group of lanes has in shared memory or on their way there, 32 bytes of a lane for each of its items: two are on their way while one
+// is computed. (18432 rows of 40 heads of 128, blocks on an SM x heads: 4 x 3 59.1 us, 4 x 4 59.4, 3 x 4 59.8, 5 x 3 61.4, 5 x 2 63.9, 6 x 3 67.2; one
+// head ahead in registers, 5 blocks, 62.6.)
+constexpr int kNormFwdStages = 3;
 // Heads that a group of lanes of the gradient has in shared memory or on their way there, 64 bytes of a lane for each of its items: with one
 // item per lane two are on their way while one is computed (16384 rows of 40 heads of 128: 84.3 us; one, in registers, 90.6; three 89; four 87).
 template <int R>
@@ -185,16 +189,18 @@ __global__ void __launch_bounds__(256, norm_blocks(R)) norm_rope_kernel(const __
     grid_dependents_launch();
     grid_dependency_wait();
     extern __shared__ __align__(16) float shared[];
-    typedef typename RawOf<E, V>::type Raw;
+    constexpr int kStages = kNormFwdStages;
     const int half = p.cols.rot / 2, d = p.cols.d, H = p.heads[0] + p.heads[1];
-    float* w = shared;
-    float* cs = shared + 2 * d;
+    uint4* ring = reinterpret_cast<uint4*>(shared) + threadIdx.x;  // [stage][item][a, b][thread]
+    auto piece = [&](int stage, int r, int x) { return ring + ((stage * R + r) * 2 + x) * (int)blockDim.x; };
+    float* w = shared + kStages * R * 8 * (int)blockDim.x;
+    float* cs = w + 2 * d;
     float* sn = cs + p.tokens * half;
     const long long t0 = (long long)blockIdx.x * p.tokens;
     const int tokens = (int)min((long long)p.tokens, p.T - t0);
     const int lanes = W > 0 ? W : p.lanes, lane = threadIdx.x & (lanes - 1), shift = 31 - __clz(lanes);
     const int groups = blockDim.x >> shift;
-    HeadWalk at(threadIdx.x >> shift, groups, H);
+    HeadWalk at(threadIdx.x >> shift, groups, H), ahead = at;
     int a[R], b[R];
     bool turned[R], some[R];
 #pragma unroll
@@ -202,35 +208,42 @@ __global__ void __launch_bounds__(256, norm_blocks(R)) norm_rope_kernel(const __
         some[r] = W > 0 || lane + r * lanes < p.items;
         turned[r] = item_cols<V>(p.cols, some[r] ? lane + r * lanes : 0, a[r], b[r]);
     }
-    Raw ra[R], rb[R];
-    auto load = [&]() {
-        const bool k = at.h >= p.heads[0];
-        const E* src = static_cast<const E*>(k ? p.in[1] : p.in[0]) + (t0 + at.t) * (k ? p.in_stride[1] : p.in_stride[0]) +
-                       (long long)(k ? at.h - p.heads[0] : at.h) * d;
+    auto load = [&](int stage) {
+        if (ahead.t < tokens) {
+            const bool k = ahead.h >= p.heads[0];
+            const E* src = static_cast<const E*>(k ? p.in[1] : p.in[0]) + (t0 + ahead.t) * (k ? p.in_stride[1] : p.in_stride[0]) +
+                           (long long)(k ? ahead.h - p.heads[0] : ahead.h) * d;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (some[r]) ra[r] = load_raw<E, V>(src + a[r]), rb[r] = load_raw<E, V>(src + b[r]);
+            for (int r = 0; r < R; ++r)
+                if (some[r]) cp_async16(smem_u32(piece(stage, r, 0)), src + a[r], 16), cp_async16(smem_u32(piece(stage, r, 1)), src + b[r], 16);
+        }
+        cp_async_commit();
+        ahead.next();
     };
-    if (at.t < tokens) load();
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) load(s);
     stage_angles<V>(p, t0, tokens, false, cs, sn);
     stage_weights<V>(p, w);
     __syncthreads();
     // (a warp goes on while its first group has a head: the groups of a warp take part in its shuffles)
     const int all = tokens * H;
+    int stage = 0;
     for (int i = (threadIdx.x & ~31) >> shift; i < all; i += groups) {
         const bool mine = at.t < tokens;
         const int t = at.t, h = at.h;
         const bool k = h >= p.heads[0];
+        cp_async_wait<kStages - 2>();
         float xa[R][V], xb[R][V], ss[2] = {0.0f, 0.0f};  // (a group without a head sums what it finds, for itself)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (!some[r]) continue;
-            unpack<E, V>(ra[r], xa[r]), unpack<E, V>(rb[r], xb[r]);
+            unpack<E, V>(*piece(stage, r, 0), xa[r]), unpack<E, V>(*piece(stage, r, 1), xb[r]);
             add_products<V>(ss, xa[r], xa[r]);
             add_products<V>(ss, xb[r], xb[r]);
         }
         at.next();
-        if (at.t < tokens) load();
+        load(stage == 0 ? kStages - 1 : stage - 1);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
         const float scale = rsqrtf(fmaf(group_sum<W>(ss[0] + ss[1], lanes), p.inv_d, p.eps));
         if (!mine) continue;
         E* dst = static_cast<E*>(k ? p.out[1] : p.out[0]) + (t0 + t) * (k ? p.out_stride[1] : p.out_stride[0]) +
@@ -524,7 +537,11 @@ cudaError_t launch_wide(const NormParams& p, bool back, unsigned blocks, unsigne
         if (e != cudaSuccess) return e;
         return launch_kernel(norm_rope_bwd_kernel<E, V, R, W>, dim3(blocks), threads, ring + smem, s, {true}, p);
     }
-    return launch_kernel(norm_rope_kernel<E, V, R, W>, dim3(blocks), threads, smem, s, {true}, p);
+    static std::atomic<bool> attr_set[kMaxAttrDevices];
+    const size_t ring = (size_t)kNormFwdStages * R * 32 * threads;
+    const cudaError_t e = ensure_smem_attr(norm_rope_kernel<E, V, R, W>, (int)(kNormFwdStages * R * 32 * 256 + kNormShared * 4), attr_set);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(norm_rope_kernel<E, V, R, W>, dim3(blocks), threads, ring + smem, s, {true}, p);
 }
 
 // The common widths have kernels of their own (64, 128 and 256, and with V = 8 items of bf16 192: three items on 4 lanes).
