@@ -413,3 +413,51 @@ def test_decode_with_eviction(A, fmt, captured):
                     sums[b][h] = sums[b][h][row]
             assert lens.tolist() == [min(n, budget) for n in ns]
     assert A.attn_get_device_status() == 0 and max(ns) >= budget
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [2, 300])
+def test_calls_behind_one_another(A, fmt, n):
+    """Each call reads what the one before it writes, and may start before that has ended: the same bytes with the device idle in between."""
+    B, Hq, Hkv, d, page, budget, length = 24, 8, 2, 128, 16, 160, 600
+    W, T, width = (Hq + 2 * Hkv) * d, B * n, -(-length // page)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    x = torch.randn((T, W), generator=g, device=DEV).bfloat16()
+    pt = torch.randperm(B * width, generator=g, device=DEV).int().view(B, width)
+    shape = (B * width, page, Hkv, d)
+    cache = [torch.randn(shape, generator=g, device=DEV).bfloat16() if fmt == "bf16" else
+             torch.randn(shape, generator=g, device=DEV).to(torch.float8_e4m3fn).view(torch.uint8) for _ in range(2)]
+    sums = torch.rand((B * width, Hkv, page), generator=g, device=DEV)
+    lens = torch.full((B,), length, dtype=torch.int32, device=DEV)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    inv = torch.tensor(A.attn_rope_freqs(d)[0], dtype=torch.float64, device=DEV)
+    w = torch.rand(d, generator=g, device=DEV) + 0.5
+    lse = torch.rand((T, Hq), generator=g, device=DEV) + 5
+    dy = torch.randn((T, Hq * d), generator=g, device=DEV).bfloat16()
+
+    def run(between):
+        kc, vc, score = cache[0].clone(), cache[1].clone(), sums.clone()
+        q, dq = torch.zeros((2, T, Hq, d), dtype=torch.bfloat16, device=DEV)
+        k, dw = torch.zeros((T, Hkv, d), dtype=torch.bfloat16, device=DEV), torch.zeros(d, device=DEV)
+        kept, new = torch.zeros((B, Hkv, budget), dtype=torch.int32, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+        for call in (
+                lambda: A.attn_qk_norm_rope(x, x[:, Hq * d:], q, k, w, w, 1e-6, pos, inv, T, Hq, Hkv, d, 0, d, W, W, Hq * d, Hkv * d),
+                lambda: A.attn_qk_norm_rope_bwd(q, None, dy, None, w, None, 1e-6, pos, inv, dq, None, dw, None, T, Hq, 0, d, 0, d, Hq * d, 0,
+                                                Hq * d, 0, Hq * d, 0),
+                lambda: A.attn_kv_write_paged(k, x[:, (Hq + Hkv) * d:], Hkv * d, W, kc, vc, pt, lens, None, page, T, B, Hkv, d, width, B * width, fmt),
+                lambda: A.attn_kv_score_paged(q, lse, kc, score, pt, lens, None, page, T, B, n, Hq, Hkv, d, width, B * width, 0.1, 0.5, fmt),
+                lambda: A.attn_kv_score_paged(dq, lse, kc, score, pt, lens, None, page, T, B, n, Hq, Hkv, d, width, B * width, 0.1, 0.5, fmt),
+                lambda: A.attn_kv_select_paged(score, pt, lens, kept, new, page, B, Hkv, width, B * width, budget, 4, 16),
+                lambda: A.attn_kv_compact_paged(kc, vc, score, kept, new, pt, page, B, Hkv, d, width, B * width, budget, fmt),
+                lambda: A.attn_kv_score_paged(q[:B], lse[:B], kc, score, pt, new, None, page, B, B, 1, Hq, Hkv, d, width, B * width, 0.1, 1.0, fmt)):
+            call()
+            between()
+        return q, k, dq, dw, kc, vc, score, kept, new
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(5):
+        for a, b in zip(run(lambda: None), want):
+            assert torch.equal(a, b)
+    assert A.attn_get_device_status() == 0

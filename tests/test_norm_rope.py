@@ -308,6 +308,27 @@ def test_streams_graph_and_repeated_rows(A):
 
 
 @pytest.mark.gpu
+def test_two_captured_gradients_at_once(A):
+    """Graphs with their own parts of the weights' sums, replayed together on two streams."""
+    ps = [Problem(A, T, 4, 2, 128, 0, 128, 0, "bf16", True, seed=8) for T in (900, 1700)]
+    want = [p.backward(A) for p in ps]
+    graphs, got, streams = [], [], [torch.cuda.Stream() for _ in ps]
+    for p in ps:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(p.backward(A))
+        graphs.append(g)
+    for _ in range(5):
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (dq, dk, dw), (rq, rk, rw) in zip(got, want):
+            assert torch.equal(dq, rq) and torch.equal(dk[:, :256], rk[:, :256]) and torch.equal(dw[0], rw[0]) and torch.equal(dw[1], rw[1])
+
+
+@pytest.mark.gpu
 def test_offsets_beyond_32_bits(A):
     """Rows further apart than 2^31 elements in all, in and out, both ways."""
     T, H, d, stride = 17, 2, 64, 2**27 + 8
