@@ -10,7 +10,7 @@
 // and about ten instructions per pass and 32 tokens. Several blocks share a row where rows are long and few: a block counts and marks its part,
 // and the others read the counts in its shared memory. (One block for each row, votes on 32 tokens: 16 x 8 rows of up to 32768 tokens 25 us,
 // 64 x 8 rows of 4100-4352 tokens 21 us; with keys in registers, four digits of 8 bits, and a numbering per 1024 tokens about 100 us.) Now, on new
-// scores in a graph: 8 rows of 1000 tokens 7.2 us, 16 x 8 of U[2048, 32768] 20, 64 x 8 of U[4100, 4352] 18.5.
+// scores in a graph: 8 rows of 1000 tokens 6.7 us (a piece of code per digit instead of a loop: 7.2), 16 x 8 of U[2048, 32768] 20, 64 x 8 of U[4100, 4352] 18.3.
 //
 // Compaction: row kept[j] -> j with kept[j] >= j. A block lists the slots that get another row, in ascending order, with the
 // cache rows of both, and moves them in runs: it loads the rows of a run, then stores them. Every row that it reads later belongs to a slot
@@ -195,10 +195,9 @@ __device__ __forceinline__ const T* of_part(const T* p, int rank) {
 // QUADS: page_size is a multiple of 4 and score 16-byte aligned. PARTS: blocks of the cluster that share a row.
 template <bool QUADS, int PARTS>
 __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ EvictParams p) {
-    grid_dependents_launch();
-    grid_dependency_wait();
     extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ int counts[3][2048], merged[PARTS > 1 ? 2048 : 1], scratch[35], totals[2];  // totals of this part: equals, marks
+    __shared__ __align__(16) int counts[3][2048];
+    __shared__ int merged[PARTS > 1 ? 2048 : 1], scratch[35], totals[2];  // totals of this part: equals, marks
     __shared__ unsigned sums[32];
     // behind the keys, per group: four votes (of the lanes' first, second, ... tokens), marks before it
     uint4* votes = reinterpret_cast<uint4*>(keys + p.groups * kGroup);
@@ -211,7 +210,9 @@ __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ Ev
         else
             __syncthreads();
     };
-    for (int i = tid; i < 3 * 2048; i += nt) (&counts[0][0])[i] = 0;
+    for (int i = tid; i < 3 * 2048 / 4; i += nt) reinterpret_cast<uint4*>(counts)[i] = make_uint4(0, 0, 0, 0);
+    grid_dependents_launch();
+    grid_dependency_wait();
     SelectRow s;
     if (!select_row(p, s, PARTS, part)) return;  // (the whole cluster)
     // places count from a multiple of four tokens on: tokens [off, off + n) of these, the first m of them below the row's end
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ Ev
 #pragma unroll
             for (int x = 0; x < PARTS; ++x) from[x] = of_part(counts[d], x);
 #pragma unroll 2
-            for (int i = tid; i < (d == 2 ? 1024 : 2048); i += nt) {
+            for (int i = tid; i < 2048; i += nt) {
                 int c = 0;
 #pragma unroll
                 for (int x = 0; x < PARTS; ++x) c += from[x][i];
@@ -279,28 +280,22 @@ __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ Ev
         }
     };
     // the m-th largest key, and how many of its equals stay
-    int digit, left = s.m, of;
-    each_group([&](int, int, const uint32_t(&key)[4], uint32_t there) {
+    int left = s.m, of;
+    uint32_t found = 0, above = 0;  // the digits found, and their bits
+#pragma unroll 1
+    for (int d = 0; d < 3; ++d) {  // (a loop: the instructions are fetched once)
+        const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+        const uint32_t mask = d < 2 ? 2047 : 1023;
+        each_group([&](int, int, const uint32_t(&key)[4], uint32_t there) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (there >> e & 1) atomicAdd(&counts[0][key[e] >> 21], 1);
-    });
-    find_digit<2048>(histogram(0), scratch, digit, left, of);
-    uint32_t found = (uint32_t)digit << 21;
-    each_group([&](int, int, const uint32_t(&key)[4], uint32_t there) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if ((key[e] ^ found) >> 21 == 0 && (there >> e & 1)) atomicAdd(&counts[1][key[e] >> 10 & 2047], 1);
-    });
-    find_digit<2048>(histogram(1), scratch, digit, left, of);
-    found |= (uint32_t)digit << 10;
-    each_group([&](int, int, const uint32_t(&key)[4], uint32_t there) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if ((key[e] ^ found) >> 10 == 0 && (there >> e & 1)) atomicAdd(&counts[2][key[e] & 1023], 1);
-    });
-    find_digit<1024>(histogram(2), scratch, digit, left, of);
-    found |= (uint32_t)digit;
+            for (int e = 0; e < 4; ++e)
+                if (((key[e] ^ found) & above) == 0 && (there >> e & 1)) atomicAdd(&counts[d][key[e] >> shift & mask], 1);
+        });
+        int digit;
+        find_digit<2048>(histogram(d), scratch, digit, left, of);
+        found |= (uint32_t)digit << shift;
+        above |= mask << shift;
+    }
 
     // counts of the groups (in ahead) to the counts before them; total[which] is the part's. Returns those of the parts before.
     auto number = [&](int which) {
