@@ -337,28 +337,29 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
         some[r] = W > 0 || lane + r * lanes < p.items;
         turned[r] = item_cols<V>(p.cols, some[r] ? lane + r * lanes : 0, a[r], b[r]);
     }
+    HeadWalk ahead(threadIdx.x >> shift, groups, p.heads[0]);
+    auto load = [&](int k, int stage) {
+        if (ahead.t < tokens) {
+            const E* src = static_cast<const E*>(p.in[k]) + (t0 + ahead.t) * p.in_stride[k] + (long long)ahead.h * d;
+            const E* grad = static_cast<const E*>(p.grad[k]) + (t0 + ahead.t) * p.grad_stride[k] + (long long)ahead.h * d;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (some[r]) {
+                    cp_async16(smem_u32(piece(stage, r, 0)), src + a[r], 16), cp_async16(smem_u32(piece(stage, r, 1)), src + b[r], 16);
+                    cp_async16(smem_u32(piece(stage, r, 2)), grad + a[r], 16), cp_async16(smem_u32(piece(stage, r, 3)), grad + b[r], 16);
+                }
+        }
+        cp_async_commit();
+        ahead.next();
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) load(0, s);
     stage_angles<V>(p, t0, tokens, true, cs, sn);
     stage_weights<V>(p, w);
     __syncthreads();
     for (int k = 0; k < 2; ++k) {  // the heads of q, then of k
         if (p.heads[k] == 0) continue;
-        HeadWalk at(threadIdx.x >> shift, groups, p.heads[k]), ahead = at;
-        auto load = [&](int stage) {
-            if (ahead.t < tokens) {
-                const E* src = static_cast<const E*>(p.in[k]) + (t0 + ahead.t) * p.in_stride[k] + (long long)ahead.h * d;
-                const E* grad = static_cast<const E*>(p.grad[k]) + (t0 + ahead.t) * p.grad_stride[k] + (long long)ahead.h * d;
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (some[r]) {
-                        cp_async16(smem_u32(piece(stage, r, 0)), src + a[r], 16), cp_async16(smem_u32(piece(stage, r, 1)), src + b[r], 16);
-                        cp_async16(smem_u32(piece(stage, r, 2)), grad + a[r], 16), cp_async16(smem_u32(piece(stage, r, 3)), grad + b[r], 16);
-                    }
-            }
-            cp_async_commit();
-            ahead.next();
-        };
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) load(s);
+        HeadWalk at(threadIdx.x >> shift, groups, p.heads[k]);
         float wa_sum[R][V] = {}, wb_sum[R][V] = {};
         const int all = tokens * p.heads[k];
         int stage = 0;
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
                 unpack<E, V>(*piece(stage, r, 2), ya[r]), unpack<E, V>(*piece(stage, r, 3), yb[r]);
             }
             at.next();
-            load(stage == 0 ? kStages - 1 : stage - 1);  // (where the head before this one was)
+            load(k, stage == 0 ? kStages - 1 : stage - 1);  // (where the head before this one was)
             stage = stage + 1 == kStages ? 0 : stage + 1;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -423,6 +424,11 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
             }
         }
         cp_async_wait<0>();
+        if (k == 0 && p.heads[1] > 0) {
+            ahead = HeadWalk(threadIdx.x >> shift, groups, p.heads[1]);
+#pragma unroll
+            for (int s = 0; s < kStages - 1; ++s) load(1, s);
+        }
         if (!p.partial) continue;
 #pragma unroll
         for (int r = 0; r < R; ++r)
