@@ -58,9 +58,11 @@ constexpr int kRowWarps = 8;  // warps per block, at most
 // U[5333, 16000] x 8 heads of 64, bf16: one 129 us, two 92; e4m3: two 77, four 74, but with 24 rows their registers spill: 29 us, not 26.)
 template <int D, bool F8>
 constexpr int kRowGroups = D == 128 && !F8 ? 1 : 2;
-// Blocks on an SM that the registers are limited to. Spilled registers cost more than the warps give: the same case with three blocks of
-// 80 registers 212 us, two of 128 194; and two steps loaded ahead instead of one, two blocks, 208.
-constexpr int row_blocks(int d, bool f8, int nt) { return (d == 64 && nt == 1) || (nt == 1 && !f8) ? 3 : 2; }
+// Registers of a thread: 80 (24 warps on an SM), 96 (20) or 128 (16), as many warps as do without spilled registers. (64 sequences of U[1K, 32K] x 8
+// heads of 128, e4m3, one row of 4 heads: 80 212 us, 96 186, 128 198, and with two steps loaded ahead instead of one 208. 48 of U[5333, 16000] x 8
+// heads of 64, 16 rows: 96 88 us, e4m3 67, 128 96 and 75; 24 rows 132 and 81, 128 102 and 81.)
+template <int D, bool F8, int NT>
+constexpr int kRowRegs = NT == 1 ? (D == 64 || !F8 ? 80 : 96) : D == 64 && NT == 2 ? 96 : 128;
 
 // Tokens of a sequence in steps of a block.
 __device__ __forceinline__ int steps_of(const ScoreParams& p, int b, int step) {
@@ -70,7 +72,7 @@ __device__ __forceinline__ int steps_of(const ScoreParams& p, int b, int step) {
 
 // NT: groups of 8 rows.
 template <int D, int FMT, int NT>
-__global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_BF16, NT)) score_rows_kernel(const __grid_constant__ ScoreParams p) {
+__global__ void __maxnreg__((kRowRegs<D, FMT != ATTN_KV_BF16, NT>)) score_rows_kernel(const __grid_constant__ ScoreParams p) {
     grid_dependents_launch();
     grid_dependency_wait();
     constexpr bool F8 = FMT != ATTN_KV_BF16;
@@ -79,7 +81,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_blocks(D, FMT != ATTN_KV_B
     constexpr int kSteps = D / 16;                   // products
     constexpr int kPer = kSteps / kLoads;            // of each load
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int heads = min(p.Hkv, kRowWarps), warps = blockDim.x >> 5, parts = warps / heads;
+    const int heads = p.row_heads, warps = blockDim.x >> 5, parts = warps / heads;
     const int h = blockIdx.y * heads + warp % heads, part = warp / heads;
     const int step = 16 * TG * parts;  // tokens of a block's step
 
@@ -282,15 +284,20 @@ int resident_blocks(Kernel kernel, int threads, std::atomic<int> (&known)[kRowWa
 template <int D, int FMT, int NT>
 cudaError_t launch_rows(ScoreParams p, cudaStream_t stream) {
     static std::atomic<int> known[kRowWarps + 1];
-    const int heads = p.Hkv < kRowWarps ? p.Hkv : kRowWarps;
-    // As many warps as an SM holds, in the largest blocks that give so many: with 3 heads blocks of 3 warps (15) instead of 6 (12).
-    auto blocks_of = [&](int parts) { return resident_blocks(score_rows_kernel<D, FMT, NT>, heads * parts * 32, known); };
-    int parts = kRowWarps / heads;
-    for (int x = parts - 1; x > 0; --x)
-        if (blocks_of(x) * x > blocks_of(parts) * parts) parts = x;
+    // Blocks of all heads (8 at most), with as many parts of a step's tokens as fit into 8 warps; smaller ones, of fewer parts or heads, where an SM then
+    // holds a quarter more warps. (3 heads of 64, 24 rows, e5m2: blocks of 3 warps, 15 on an SM, 21.2 us, of 6 warps, 12, 24.4. 8 heads of 128, one
+    // row of 4 heads, e4m3: blocks of 4 warps, 20, 186 us, of 8, 16, 198; 3 heads of those, 3 warps, 21, 44.8 us, 6 warps, 18, 40.4.)
+    auto warps_of = [&](int warps) { return resident_blocks(score_rows_kernel<D, FMT, NT>, warps * 32, known) * warps; };
+    int heads = p.Hkv < kRowWarps ? p.Hkv : kRowWarps, parts = kRowWarps / heads;
+    auto consider = [&](int h, int n) {
+        if (warps_of(h * n) * 4 >= warps_of(heads * parts) * 5) heads = h, parts = n;
+    };
+    for (int n = parts - 1; n > 0; --n) consider(heads, n);
+    for (int h = heads / 2; parts == 1 && h > 0 && p.Hkv % h == 0; h /= 2) consider(h, 1);
+    p.row_heads = heads;
     const long long groups = (p.Hkv + heads - 1) / heads, capacity = (long long)p.max_pages * p.page_size;
     const int step = 16 * kRowGroups<D, FMT != ATTN_KV_BF16> * parts;
-    const long long slots = (long long)p.num_sms * blocks_of(parts);
+    const long long slots = (long long)p.num_sms * (warps_of(heads * parts) / (heads * parts));
     // pieces of every sequence's table for as many blocks as run at once, a few steps each at least; if that is too many blocks, runs
     long long c = ((long long)p.B * capacity * groups + slots - 1) / slots;
     c = (c + step - 1) / step * step;

@@ -41,6 +41,7 @@ struct ScoreParams {
     float scale_log2, decay;  // scale (key descale included) times log2(e)
     float unit;              // tiles: -log2(e) / scale_log2
     Divisor by_page;
+    int row_heads;           // few rows: kv heads of a block
     int chunk, chunks;       // few rows: tokens per block, blocks of the longest sequence; 0: runs of all tokens there are
     // tiles: [blocks, 2, unit_tok] sums of units that lie in several blocks; 8-bit caches: factor of the scores of each row of q
     float *partial, *factor;
