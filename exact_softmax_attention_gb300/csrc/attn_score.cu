@@ -9,8 +9,8 @@
 // tokens (narrower rows: 32) are loaded while these are multiplied, and the page table is read one group ahead of them. A block's warps take
 // the kv heads of the same tokens, so a cache row is read as a whole.
 //
-// Measured, 64 sequences of U[1K, 32K] tokens, 32/8 heads of 128: bf16 327 us, 6790 GB/s (the rate of a copy); e4m3 198 us, 5800 GB/s (loads that
-// the warps wait for, two blocks of 8 warps on an SM). 48 x U[1, 8000], 1-6 rows of 4 heads x 3 heads of 64, e5m2, pages of 7: 21 us for 41 MB, a
+// Measured, 64 sequences of U[1K, 32K] tokens, 32/8 heads of 128: bf16 327 us, 6790 GB/s (the rate of a copy); e4m3 186 us, 6160 GB/s (loads that
+// the warps wait for, 20 on an SM). 48 x U[1, 8000], 1-6 rows of 4 heads x 3 heads of 64, e5m2, pages of 7: 21 us for 41 MB, a
 // chain of dependent loads in one wave of blocks (without the exponentials of rows that a sequence has not, or with the keys loaded before the rows:
 // no change).
 //
@@ -58,11 +58,12 @@ constexpr int kRowWarps = 8;  // warps per block, at most
 // U[5333, 16000] x 8 heads of 64, bf16: one 129 us, two 92; e4m3: two 77, four 74, but with 24 rows their registers spill: 29 us, not 26.)
 template <int D, bool F8>
 constexpr int kRowGroups = D == 128 && !F8 ? 1 : 2;
-// Registers of a thread: 80 (24 warps on an SM), 96 (20) or 128 (16), as many warps as do without spilled registers. (64 sequences of U[1K, 32K] x 8
+// Registers of a thread: 80 (24 warps on an SM), 96 (20), 128 (16) or 160 (12), as many warps as do without many spilled registers. (64 sequences of U[1K, 32K] x 8
 // heads of 128, e4m3, one row of 4 heads: 80 212 us, 96 186, 128 198, and with two steps loaded ahead instead of one 208. 48 of U[5333, 16000] x 8
-// heads of 64, 16 rows: 96 88 us, e4m3 67, 128 96 and 75; 24 rows 132 and 81, 128 102 and 81.)
+// heads of 64, 16 rows: 96 88 us, e4m3 67, 128 96 and 75; 24 rows 132 and 81, 128 102 and 81. Of 128,
+// 24 rows, e4m3: 128 142, 160 117; bf16 128 171, 160 191.)
 template <int D, bool F8, int NT>
-constexpr int kRowRegs = NT == 1 ? (D == 64 || !F8 ? 80 : 96) : D == 64 && NT == 2 ? 96 : 128;
+constexpr int kRowRegs = NT == 1 ? (D == 64 || !F8 ? 80 : 96) : D == 64 && NT == 2 ? 96 : D == 128 && F8 && NT == 3 ? 160 : 128;
 
 // Tokens of a sequence in steps of a block.
 __device__ __forceinline__ int steps_of(const ScoreParams& p, int b, int step) {
