@@ -208,6 +208,20 @@ def test_against_64_bits(A, n, lens, Hq, Hkv, d, page, dense, fmt, decay):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hkv", [2, 4, 6, 8, 12, 24])
+@pytest.mark.parametrize("d,fmt", [(64, "bf16"), (64, "e4m3"), (128, "bf16"), (128, "e5m2")])
+def test_heads_of_a_block(A, Hkv, d, fmt):
+    """One to 24 rows per kv head over numbers of heads that blocks take whole, in parts or a few at a time; short batches and many sequences."""
+    for G, n in ((1, 1), (4, 1), (2, 8), (3, 8)):
+        for B, length in ((1, 100), (50, 900)):
+            p = Problem([n] * B, [n + (length * (i + 1)) // B for i in range(B)], G * Hkv, Hkv, d, 16, fmt, seed=9, dense=True)
+            before = p.score.clone()
+            p.run(A, 0.5)
+            p.check(before, 0.5)
+    assert A.attn_get_device_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n,lens,Hq,Hkv", [([1] * 3, [5, 40, 700], 8, 2), ([40, 20], [300, 200], 8, 2)])
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3", "e5m2"])
 def test_magnitudes_and_scales(A, n, lens, Hq, Hkv, fmt):
