@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
                 add_products<V>(dot, xb[r], wb);
             }
             const float scale = rsqrtf(fmaf(group_sum<W>(ss[0] + ss[1], lanes), p.inv_d, p.eps));
-            const float along = group_sum<W>(dot[0] + dot[1], lanes) * p.inv_d * scale * scale;  // mean(n w g) r: times x, that is n mean(n w g)
+            const float along = group_sum<W>(dot[0] + dot[1], lanes) * p.inv_d * scale;  // mean(n w g)
             if (!mine) continue;
             E* dst = static_cast<E*>(p.out[k]) + (t0 + t) * p.out_stride[k] + (long long)h * d;
 #pragma unroll
@@ -405,17 +405,16 @@ __global__ void __launch_bounds__(256, norm_bwd_blocks(R)) norm_rope_bwd_kernel(
                 float wa[V], wb[V];
                 load_spread<V>(w + k * d, a[r] / V, d, wa);
                 load_spread<V>(w + k * d, b[r] / V, d, wb);
-                // dx = r (w g) - x (r along); dw += (r x) g
-                const float back = -scale * along;
+                // dx = r (w g - n along); dw += n g. (In this order: r^2 along, and r^2 alone for heads below 10^-19, leave fp32 before dx does.)
                 auto finish = [&](float(&x)[V], const float(&y)[V], const float(&wt)[V], float(&w_sum)[V]) {
 #pragma unroll
                     for (int e = 0; e < V; e += 2) {
-                        float n0, n1, g0, g1, q0, q1;
+                        float n0, n1, g0, g1;
                         fmul2(n0, n1, x[e], x[e + 1], scale, scale);
                         ffma2(w_sum[e], w_sum[e + 1], n0, n1, y[e], y[e + 1], w_sum[e], w_sum[e + 1]);
                         fmul2(g0, g1, y[e], y[e + 1], wt[e], wt[e + 1]);
-                        fmul2(q0, q1, x[e], x[e + 1], back, back);
-                        ffma2(x[e], x[e + 1], g0, g1, scale, scale, q0, q1);
+                        ffma2(g0, g1, n0, n1, -along, -along, g0, g1);
+                        fmul2(x[e], x[e + 1], g0, g1, scale, scale);
                     }
                 };
                 finish(xa[r], ya[r], wa, wa_sum[r]);
@@ -491,11 +490,12 @@ __global__ void __launch_bounds__(256) norm_rope_bwd_any_kernel(const __grid_con
                 dot = fmaf(xa[0], w[k * d + a] * ya[0], fmaf(xb[0], w[k * d + b] * yb[0], dot));
             }
             const float scale = rsqrtf(fmaf(group_sum<32>(ss, 32), p.inv_d, p.eps));
-            const float along = group_sum<32>(dot, 32) * p.inv_d * scale * scale;
+            const float along = group_sum<32>(dot, 32) * p.inv_d * scale;
             for (int j = lane; j < p.items; j += 32) {
                 item(j, a, b, xa, xb, ya, yb);
-                row[a] = fmaf(xa[0] * scale, ya[0], row[a]);
-                row[b] = fmaf(xb[0] * scale, yb[0], row[b]);
+                xa[0] *= scale, xb[0] *= scale;
+                row[a] = fmaf(xa[0], ya[0], row[a]);
+                row[b] = fmaf(xb[0], yb[0], row[b]);
                 xa[0] = scale * (w[k * d + a] * ya[0] - xa[0] * along);
                 xb[0] = scale * (w[k * d + b] * yb[0] - xb[0] * along);
                 store_row<1>(dst + a, xa);

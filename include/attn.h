@@ -413,7 +413,8 @@ attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q_out, void*
  * dq_weight, dk_weight  device, fp32 [d] (written), or NULL where not wanted (dk_weight has to be NULL when Hk = 0). The sums
  *                 are added in a fixed order, so equal calls give equal bytes; their parts take memory from the library's
  *                 stream-ordered pool on `stream` and a second kernel, launched as a programmatic dependent.
- * Everything else is as for attn_qk_norm_rope.
+ * The products weight g of a head and their sum with x have to stay in the range of fp32, like its sum of squares; everything else is as
+ * for attn_qk_norm_rope.
  */
 attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
                                     const float* q_weight, const float* k_weight, float eps, const int* positions,

@@ -345,3 +345,41 @@ def test_offsets_beyond_32_bits(A):
             else:
                 A.attn_qk_norm_rope(src, None, dst, None, w, None, 1e-6, pos, inv, T, H, 0, d, 0, d, a, 0, b, 0)
         assert torch.equal(y, near)
+
+
+RANGE = [  # d, begin, rot, interleaved, type: two or one items per lane, idle places, element by element
+    (128, 0, 128, 0, "bf16"),
+    (128, 0, 0, 0, "f32"),
+    (192, 128, 64, 1, "f32"),
+    (160, 0, 32, 0, "f32"),
+    (80, 3, 10, 0, "bf16"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,begin,rot,inter,et", RANGE)
+@pytest.mark.parametrize("size,grad", [(1e-18, 1e4), (1e-18, 1e-4), (1e17, 1e4), (1e17, 1e-4), (1e-10, 1e19)])
+def test_gradient_over_the_range(A, d, begin, rot, inter, et, size, grad):
+    """Without eps, heads whose squares, and products with the gradient, fit into fp32 as documented: so does every intermediate value. The
+    bound is that of test_gradient, relative to the operands throughout (sums of 10^-36 to 10^34 lose nothing)."""
+    T, Hq, Hk = 37, 3, 2
+    p = Problem(A, T, Hq, Hk, d, begin, rot, inter, et, True, seed=11, scale=size)
+    p.eps = 0.0
+    p.gq, p.gk = ((x.double() * grad).to(p.t) for x in (p.gq, p.gk))
+    dq, dk, dw = p.backward(A)
+    for i, (H, dx) in enumerate(((Hq, dq), (Hk, dk))):
+        x, w, dy, r = p.heads(i)
+        g, off = p.turn(dy, 1)
+        n = x * r
+        along = (n * w * g).mean(-1, keepdims=True)
+        ref = r * (w * g - n * along)
+        e = norm_error(d)
+        dot = (np.abs(n * w * g) * (2 * e + (d + 4) * 2.0**-24) + np.abs(n * w) * off).mean(-1, keepdims=True)
+        bound = r * (np.abs(w) * off + np.abs(w * g) * 2 * e + np.abs(n) * (dot + np.abs(along) * 4 * e))
+        got = dx[:, :H * d].double().cpu().numpy().reshape(ref.shape)
+        tol = bound + STEP[et] * (np.abs(ref) + bound) + 1e-38
+        assert np.isfinite(got).all() and (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
+        ref = (n * g).sum((0, 1))
+        tol = (np.abs(n * g) * (e + (T * H + 2) * 2.0**-24) + np.abs(n) * off).sum((0, 1))
+        got = dw[i].double().cpu().numpy()
+        assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
