@@ -140,13 +140,13 @@ __device__ __forceinline__ void stage_angles(const NormParams& p, long long t0, 
     }
 }
 
+// w (r x): r x is at most sqrt(d), where w r may leave fp32 though the result does not.
 template <int V>
 __device__ __forceinline__ void times(float (&x)[V], const float (&w)[V], float r) {
 #pragma unroll
     for (int e = 0; e < V; e += 2) {
-        float a, b;
-        fmul2(a, b, w[e], w[e + 1], r, r);
-        fmul2(x[e], x[e + 1], x[e], x[e + 1], a, b);
+        fmul2(x[e], x[e + 1], x[e], x[e + 1], r, r);
+        fmul2(x[e], x[e + 1], x[e], x[e + 1], w[e], w[e + 1]);
     }
 }
 
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(256) norm_rope_any_kernel(const __grid_constan
         for (int j = lane; j < p.items; j += 32) {
             int a, b;
             const bool turned = item_cols<1>(p.cols, j, a, b);
-            float xa[1] = {(float)src[a] * (scale * w[k * d + a])}, xb[1] = {(float)src[b] * (scale * w[k * d + b])};
+            float xa[1] = {(float)src[a] * scale * w[k * d + a]}, xb[1] = {(float)src[b] * scale * w[k * d + b]};
             if (turned) rotate_item<1>(xa, xb, p.cols, j, cs + at.t * half, sn + at.t * half);
             store_row<1>(dst + a, xa);
             store_row<1>(dst + b, xb);

@@ -383,3 +383,23 @@ def test_gradient_over_the_range(A, d, begin, rot, inter, et, size, grad):
         tol = (np.abs(n * g) * (e + (T * H + 2) * 2.0**-24) + np.abs(n) * off).sum((0, 1))
         got = dw[i].double().cpu().numpy()
         assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,begin,rot,inter,et", RANGE)
+@pytest.mark.parametrize("size,weight", [(1e-18, 1e25), (1e-18, 1e-25), (1e17, 1e30), (1e17, 1e-18)])
+def test_forward_over_the_range(A, d, begin, rot, inter, et, size, weight):
+    """Weights far from one on small and large heads, without eps; the bound is that of test_forward."""
+    T, Hq, Hk = 37, 3, 2
+    p = Problem(A, T, Hq, Hk, d, begin, rot, inter, et, True, seed=12, scale=size)
+    p.eps = 0.0
+    p.wq, p.wk = p.wq * weight, p.wk * weight
+    out = p.forward(A)
+    for i, H in ((0, Hq), (1, Hk)):
+        x, w, _, r = p.heads(i)
+        ref, bound = p.turn(x * r * w, 0)
+        size_ = np.abs(p.turn(np.abs(x * r * w), 0)[1]) / (np.pi * 2.0**-25) + np.abs(ref)
+        got = out[i][:, :H * d].double().cpu().numpy().reshape(ref.shape)
+        bound = bound + size_ * norm_error(d)
+        tol = bound + STEP[et] * (np.abs(ref) + bound) + 1e-38
+        assert np.isfinite(got).all() and (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
