@@ -92,7 +92,7 @@ __device__ __forceinline__ bool select_row(const EvictParams& p, SelectRow& s, i
     const unsigned row = blockIdx.x / (unsigned)parts;
     const int b = (int)(row / (unsigned)p.Hkv), K = p.budget, tid = part * blockDim.x + threadIdx.x, nt = parts * blockDim.x;
     s.h = (int)(row % (unsigned)p.Hkv);
-    s.len = __ldg(p.seqlens + b);
+    s.len = p.seqlens[b];
     s.kept = p.kept + (long long)row * K;
     s.pt = p.page_table + (long long)b * p.max_pages;
     const bool bad = s.len < 0 || s.len > (long long)p.max_pages * p.page_size;
@@ -114,12 +114,12 @@ __device__ __forceinline__ bool select_row(const EvictParams& p, SelectRow& s, i
 // Key of token sinks + i.
 __device__ __forceinline__ uint32_t key_of(const EvictParams& p, const SelectRow& s, int i) {
     int slot;
-    const int page = __ldg(s.pt + evict_page(p, p.sinks + i, slot));
+    const int page = s.pt[evict_page(p, p.sinks + i, slot)];
     if (page < 0 || page >= p.num_pages) {
         atomicCAS(p.status, 0, kDevBadIndex);
         return 0;
     }
-    return score_key(__ldg(p.score + ((long long)page * p.Hkv + s.h) * p.page_size + slot));
+    return score_key(p.score[((long long)page * p.Hkv + s.h) * p.page_size + slot]);
 }
 
 // The digit in which the count of the histogram from the top passes `left`, how many of that digit are then left, and of how many. Every
@@ -227,9 +227,9 @@ __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ Ev
             uint4 k = make_uint4(0, 0, 0, 0);
             if (i < n) {
                 int slot;
-                const int page = __ldg(s.pt + evict_page(p, base + i, slot));
+                const int page = s.pt[evict_page(p, base + i, slot)];
                 if (page >= 0 && page < p.num_pages) {
-                    const float4 x = __ldg(reinterpret_cast<const float4*>(p.score + ((long long)page * p.Hkv + s.h) * p.page_size + slot));
+                    const float4 x = *reinterpret_cast<const float4*>(p.score + ((long long)page * p.Hkv + s.h) * p.page_size + slot);
                     k = make_uint4(score_key(x.x), score_key(x.y), score_key(x.z), score_key(x.w));
                 } else {
                     atomicCAS(p.status, 0, kDevBadIndex);
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const __gri
     grid_dependents_launch();
     grid_dependency_wait();
     const int b = (int)(blockIdx.x / (unsigned)p.Hkv), h = (int)(blockIdx.x % (unsigned)p.Hkv);
-    const int n = min(__ldg(p.seqlens + b), p.budget), limit = p.max_pages * p.page_size;
+    const int n = min(p.seqlens[b], p.budget), limit = p.max_pages * p.page_size;
     const int* kept = p.kept + (long long)blockIdx.x * p.budget;
     const int* pt = p.page_table + (long long)b * p.max_pages;
     const int each = p.row_bytes / 16, tid = threadIdx.x;  // columns of K, and of V
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const __gri
     const long long row_bytes = (long long)p.Hkv * p.row_bytes;
     auto row_of = [&](int tok) {  // -1: a page out of range
         int slot;
-        const int page = __ldg(pt + evict_page(p, tok, slot));
+        const int page = pt[evict_page(p, tok, slot)];
         if (page >= 0 && page < p.num_pages) return page * p.page_size + slot;
         atomicCAS(p.status, 0, kDevBadIndex);
         return -1;
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const __gri
         int tok[kLook];
         unsigned moves = 0;
 #pragma unroll
-        for (int x = 0; x < kLook; ++x) tok[x] = first + x < n ? __ldg(kept + first + x) : -1;
+        for (int x = 0; x < kLook; ++x) tok[x] = first + x < n ? kept[first + x] : -1;
 #pragma unroll
         for (int x = 0; x < kLook; ++x) {
             if (tok[x] != -1 && (tok[x] < first + x || tok[x] >= limit)) {

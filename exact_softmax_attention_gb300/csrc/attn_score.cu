@@ -145,7 +145,7 @@ __global__ void __maxnreg__((kRowRegs<D, FMT != ATTN_KV_BF16, NT>)) score_rows_k
             uint4 w[D / 32];  // bf16: the lane's 8 elements of 32; 8-bit caches: 16 elements of 64
 #pragma unroll
             for (int x = 0; x < D / 32; ++x)
-                w[x] = valid ? __ldg(src + (F8 ? (x >> 1) * 8 + 2 * t + (x & 1) : 4 * x + t)) : make_uint4(0, 0, 0, 0);
+                w[x] = valid ? src[F8 ? (x >> 1) * 8 + 2 * t + (x & 1) : 4 * x + t] : make_uint4(0, 0, 0, 0);
             float up = 1.0f;
             if constexpr (F8) {
                 // a power of two brings the row's largest magnitude into [2^14, 2^15)
@@ -174,7 +174,7 @@ __global__ void __maxnreg__((kRowRegs<D, FMT != ATTN_KV_BF16, NT>)) score_rows_k
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int rc = 2 * t + e + 8 * n, ic = rc / p.G;
-                const float l = rc < R ? __ldg(p.lse + (long long)(s.q0 + ic) * p.Hq + h * p.G + (rc - ic * p.G)) : -INFINITY;
+                const float l = rc < R ? p.lse[(long long)(s.q0 + ic) * p.Hq + h * p.G + (rc - ic * p.G)] : -INFINITY;
                 last[n][e] = l == -INFINITY ? -1 : s.ctx + ic;  // (such rows saw nothing)
                 lse2[n][e] = l == -INFINITY ? 0.0f : l * 1.4426950408889634f;
                 const float of_row = __shfl_sync(0xffffffffu, up, (2 * t + e) * 4);
@@ -196,7 +196,7 @@ __global__ void __maxnreg__((kRowRegs<D, FMT != ATTN_KV_BF16, NT>)) score_rows_k
                 const int x = __shfl_sync(0xffffffffu, row, (lane & 28) + e);
                 const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_cache) + ((long long)x * p.Hkv + h) * (F8 ? D : 2 * D));
 #pragma unroll
-                for (int y = 0; y < kLoads; ++y) kv[e][y] = x >= 0 ? __ldg(src + 4 * y + t) : make_uint4(0, 0, 0, 0);
+                for (int y = 0; y < kLoads; ++y) kv[e][y] = x >= 0 ? src[4 * y + t] : make_uint4(0, 0, 0, 0);
             }
             if (p.decay != 0.0f) old = row >= 0 && from + g + 8 * t < s.ctx ? p.decay * *score_slot(p, at.page, at.slot, h) : 0.0f;
         };

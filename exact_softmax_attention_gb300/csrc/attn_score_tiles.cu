@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(256) split_q_kernel(const __nv_bfloat16* q, ui
     const long long r = ((long long)blockIdx.x * 256 + threadIdx.x) / kUnits;
     const int u = threadIdx.x % kUnits;
     uint4 w = make_uint4(0, 0, 0, 0);
-    if (r < rows) w = __ldg(reinterpret_cast<const uint4*>(q + r * D) + u);
+    if (r < rows) w = reinterpret_cast<const uint4*>(q + r * D)[u];
     const uint32_t e[4] = {w.x, w.y, w.z, w.w};
     uint32_t top = 0;
 #pragma unroll
@@ -513,8 +513,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int e = 0; e < 4; ++e) {
                     const bool there = query[e] < p.block_tok && i0 + query[e] < at.s.n && h0 + head[e] < p.G;
                     const long long row = (long long)(at.s.q0 + i0 + query[e]) * p.Hq + at.h * p.G + h0 + head[e];
-                    l[e] = there ? __ldg(p.lse + row) : -INFINITY;
-                    f[e] = F8 && there ? __ldg(p.factor + row) : 0.0f;
+                    l[e] = there ? p.lse[row] : -INFINITY;
+                    f[e] = F8 && there ? p.factor[row] : 0.0f;
                 }
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::bQFree + st], (uint32_t)(qn / L::kQStages & 1) ^ 1u, abort_flag, wd)))) break;
                 if (lane == 0) {

@@ -64,7 +64,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 // start before the grid ahead of it on the stream ends. The earlier grid lets it start by
 // executing grid_dependents_launch in each of its CTAs (or by ending); the later one waits in
 // grid_dependency_wait until the earlier grid has completed and its memory writes are visible.
-// Without a programmatic launch both are no-ops.
+// Without a programmatic launch both are no-ops. What the earlier kernel may write is read by plain loads behind the wait, not by
+// __ldg: the data is not constant for the lifetime of the later kernel, and the compiler may move such loads over the wait.
 __device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

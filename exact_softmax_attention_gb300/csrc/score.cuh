@@ -75,9 +75,9 @@ struct ScoreSeq {
 };
 __device__ __forceinline__ bool score_seq(const ScoreParams& p, int b, ScoreSeq& s) {
     long long c0, c1;
-    const int len = __ldg(p.seqlens + b);
+    const int len = p.seqlens[b];
     if (p.cu_seqlens) {
-        c0 = __ldg(p.cu_seqlens + b), c1 = __ldg(p.cu_seqlens + b + 1);
+        c0 = p.cu_seqlens[b], c1 = p.cu_seqlens[b + 1];
     } else {
         const int n = p.T / p.B;
         c0 = (long long)b * n, c1 = c0 + n;
@@ -103,7 +103,7 @@ __device__ __forceinline__ int score_page(const ScoreParams& p, int tok, int& sl
 
 // Physical page of a token, or -1 (recorded) for one out of range; pt: the sequence's row of the page table.
 __device__ __forceinline__ int score_place(const ScoreParams& p, const int* pt, int tok, int& slot) {
-    const int page = __ldg(pt + score_page(p, tok, slot));
+    const int page = pt[score_page(p, tok, slot)];
     if (page >= 0 && page < p.num_pages) return page;
     atomicCAS(p.status, 0, kDevBadIndex);
     return -1;
