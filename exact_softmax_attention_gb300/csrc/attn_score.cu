@@ -271,24 +271,31 @@ __global__ void __maxnreg__((kRowRegs<D, FMT != ATTN_KV_BF16, NT>)) score_rows_k
     }
 }
 
-// Blocks of so many threads of a kernel that an SM holds.
+// Blocks of so many threads of a kernel that an SM of the current device holds; known by device and warps per block. An answer that could not be had
+// is not kept: this call goes on with one block, which is slower but right.
 template <typename Kernel>
-int resident_blocks(Kernel kernel, int threads, std::atomic<int> (&known)[kRowWarps + 1]) {
-    int n = known[threads / 32].load(std::memory_order_relaxed);
-    if (n == 0) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) n = 1;
-        known[threads / 32].store(n, std::memory_order_relaxed);
+int resident_blocks(Kernel kernel, int device, int threads, std::atomic<int> (&known)[kMaxAttrDevices][kRowWarps + 1]) {
+    std::atomic<int>* entry = device >= 0 && device < kMaxAttrDevices ? &known[device][threads / 32] : nullptr;
+    int n = entry ? entry->load(std::memory_order_relaxed) : 0;
+    if (n > 0) return n;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) {
+        cudaGetLastError();  // (no error of the next call)
+        return 1;
     }
+    if (entry) entry->store(n, std::memory_order_relaxed);
     return n;
 }
 
 template <int D, int FMT, int NT>
 cudaError_t launch_rows(ScoreParams p, cudaStream_t stream) {
-    static std::atomic<int> known[kRowWarps + 1];
+    static std::atomic<int> known[kMaxAttrDevices][kRowWarps + 1];
+    int device = 0;
+    const cudaError_t found = cudaGetDevice(&device);
+    if (found != cudaSuccess) return found;
     // Blocks of all heads (8 at most), with as many parts of a step's tokens as fit into 8 warps; smaller ones, of fewer parts or heads, where an SM then
     // holds a quarter more warps. (3 heads of 64, 24 rows, e5m2: blocks of 3 warps, 15 on an SM, 21.2 us, of 6 warps, 12, 24.4. 8 heads of 128, one
     // row of 4 heads, e4m3: blocks of 4 warps, 20, 186 us, of 8, 16, 198; 3 heads of those, 3 warps, 21, 44.8 us, 6 warps, 18, 40.4.)
-    auto warps_of = [&](int warps) { return resident_blocks(score_rows_kernel<D, FMT, NT>, warps * 32, known) * warps; };
+    auto warps_of = [&](int warps) { return resident_blocks(score_rows_kernel<D, FMT, NT>, device, warps * 32, known) * warps; };
     int heads = p.Hkv < kRowWarps ? p.Hkv : kRowWarps, parts = kRowWarps / heads;
     auto consider = [&](int h, int n) {
         if (warps_of(h * n) * 4 >= warps_of(heads * parts) * 5) heads = h, parts = n;

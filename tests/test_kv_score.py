@@ -409,3 +409,42 @@ def test_weights_of_a_decode_and_a_prefill_add_up(A, fmt):
         total = score.permute(0, 2, 1).reshape(-1, Hkv)[:n].double().sum(0)
         assert (total / (n * Hq // Hkv) - 1).abs().max() <= 2.1e-3
     assert A.attn_get_device_status() == 0
+
+
+# ------------------------------------------------------------------------------------- CPU: the host's cache of answers
+
+def test_resident_blocks_by_device(tmp_path):
+    """How many blocks an SM holds is known per device, and an answer that could not be had is asked for again: the function itself, from the
+    source, with the CUDA calls replaced."""
+    import ctypes
+    import os
+    import re
+    import subprocess
+
+    from helpers import ROOT
+    with open(os.path.join(ROOT, "exact_softmax_attention_gb300", "csrc", "attn_score.cu")) as f:
+        function = re.search(r"template <typename Kernel>\nint resident_blocks\(.*?\n}\n", f.read(), flags=re.S).group(0)
+    src = tmp_path / "resident.cpp"
+    src.write_text("""#include <atomic>
+typedef int cudaError_t;
+constexpr int cudaSuccess = 0, kMaxAttrDevices = 64, kRowWarps = 8;
+static int answer, pending;
+static int cudaOccupancyMaxActiveBlocksPerMultiprocessor(int* n, int, int, int) {
+    if (answer < 0) return pending = 1;
+    *n = answer;
+    return 0;
+}
+static int cudaGetLastError() { const int e = pending; pending = 0; return e; }
+""" + function + """
+static std::atomic<int> known[kMaxAttrDevices][kRowWarps + 1];
+extern "C" int ask(int device, int threads, int a) { answer = a; return resident_blocks(0, device, threads, known); }
+extern "C" int left() { return pending; }
+""")
+    lib = tmp_path / "resident.so"
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", str(src), "-o", str(lib)], check=True)
+    c = ctypes.CDLL(str(lib))
+    assert c.ask(0, 64, 5) == 5 and c.ask(0, 64, 9) == 5  # kept
+    assert c.ask(0, 96, 4) == 4 and c.ask(1, 64, 7) == 7  # of other blocks, on another device
+    assert c.ask(2, 64, -1) == 1 and c.left() == 0        # no answer: one block for this call, and no error left behind
+    assert c.ask(2, 64, 6) == 6
+    assert c.ask(64, 64, 3) == 3 and c.ask(64, 64, 2) == 2 and c.ask(-1, 64, 8) == 8
