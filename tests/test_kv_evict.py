@@ -461,3 +461,25 @@ def test_calls_behind_one_another(A, fmt, n):
         for a, b in zip(run(lambda: None), want):
             assert torch.equal(a, b)
     assert A.attn_get_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,Hkv,budget,sinks,recent", [([1000], 2, 256, 4, 32), ([10, 0, 3000, 64, 65], 3, 64, 4, 8), ([9000, 40], 1, 8000, 0, 100)])
+@pytest.mark.parametrize("page,tokens", [(16, 131072), (7, 131068), (16, 2**20)])
+@pytest.mark.parametrize("values", ["sums", "few", "all"])
+def test_short_sequences_in_a_wide_table(A, lens, Hkv, budget, sinks, recent, page, tokens, values):
+    """A page table for far longer contexts (several blocks share a row, or the keys are read again for every step), most parts of it empty."""
+    c = Cache(lens, Hkv, 16, page, values=values)
+    c.ptd = torch.nn.functional.pad(c.ptd, (0, tokens // page - c.width), value=-1).contiguous()
+    c.width = tokens // page
+    c.select(A, budget, sinks, recent)
+    assert A.attn_get_device_status() == 0
+    score = c.score.cpu().numpy()
+    want = np.stack([[wanted(score[c.place(b, np.arange(n))[0], h, c.place(b, np.arange(n))[1]], int(n), budget, sinks, recent)
+                      for h in range(Hkv)] for b, n in enumerate(c.lens)])
+    assert np.array_equal(c.kept.cpu().numpy(), want)
+    expect = c.expect(want)
+    c.compact(A)
+    assert A.attn_get_device_status() == 0
+    for got, ref in zip((c.kc, c.vc, c.score), expect):
+        assert np.array_equal(got.cpu().numpy(), ref, equal_nan=got.dtype == torch.float32)

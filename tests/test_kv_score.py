@@ -448,3 +448,135 @@ extern "C" int left() { return pending; }
     assert c.ask(2, 64, -1) == 1 and c.left() == 0        # no answer: one block for this call, and no error left behind
     assert c.ask(2, 64, 6) == 6
     assert c.ask(64, 64, 3) == 3 and c.ask(64, 64, 2) == 2 and c.ask(-1, 64, 8) == 8
+
+
+# ------------------------------------------------------------------------------------- GPU: precision, refusals and strays, closer
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,G,n", [(64, 4, 8), (64, 4, 7), (64, 2, 13), (64, 1, 25), (64, 3, 8), (64, 4, 1), (128, 4, 6), (128, 2, 9), (128, 8, 1)])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("B,length", [(3, 200), (40, 1500)])
+def test_8_bit_keys_with_few_rows_are_exact(A, d, G, n, fmt, B, length):
+    """Up to 32 rows per kv head of 64, 24 of 128, codes are widened exactly and q keeps elements down to 2^-29 of the row's largest. One element
+    of each row is 2^11 to 2^14, the others are a few, and it meets keys of zero, so what a coarser q loses is far outside the bound."""
+    Hkv = 2
+    p = Problem([n] * B, [n + (length * (i + 1)) // B for i in range(B)], G * Hkv, Hkv, d, 16, fmt, seed=12, dense=True)
+    big = 2.0 ** torch.randint(11, 15, (p.T, G * Hkv), device=DEV)
+    p.q[..., 5] = big.bfloat16()
+    zeroed = p.kc[..., 5]
+    zeroed[p.held] = 0
+    at = 0
+    for b in range(B):
+        p.lse[at:at + n] = p.logits(b).logsumexp(-1).float()
+        at += n
+    before = p.score.clone()
+    p.run(A, 0.5)
+    assert A.attn_get_device_status() == 0
+    p.max_q = 0  # (the check's allowance for q in two parts is for more rows)
+    p.check(before, 0.5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,lens", [([1, 1, 1], [50, 300, 20]), ([40, 33, 5], [300, 200, 90]), ([500, 33, 5], [600, 200, 90]), ([3, 2, 1], [30, 50, 9])])
+@pytest.mark.parametrize("at,value", [(3, "far"), (3, "past"), (1, "both"), (2, "back"), (1, "negative"), (0, "skip"), (0, "negative")])
+def test_bad_offsets_touch_nothing_else(A, n, lens, at, value):
+    """Sequences whose offsets are out of range keep their slots bit for bit; those whose offsets stay valid get the sums of the rows that
+    they then own."""
+    import copy
+    p = Problem(n, lens, 8, 2, 64, 16, "bf16", seed=5)
+    before = p.score.clone()
+    p.cu[at] = {"far": 2**30, "past": p.T + 1, "both": n[0] + n[1] + 1, "back": n[0] - 1, "negative": -2, "skip": 1}[value]
+    cu = p.cu.tolist()
+    p.run(A, 0.5)
+    refused = 0
+    expected = before.clone()
+    for b in range(3):
+        c0, c1 = cu[b:b + 2]
+        rows = c1 - c0
+        if rows == 0:
+            continue
+        if c0 < 0 or rows < 0 or c1 > p.T or rows > p.max_q or lens[b] < rows:
+            refused += 1
+            continue
+        one = copy.copy(p)
+        one.n, one.lens, one.B, one.pt = np.array([rows]), np.array(lens[b:b + 1]), 1, p.pt[b:b + 1]
+        one.q, one.lse = p.q[c0:c1], p.lse[c0:c1]
+        pg, sl = p.places(b)
+        one.score = before.clone()
+        one.score[pg, :, sl] = expected[pg, :, sl] = p.score[pg, :, sl]
+        one.check(before, 0.5)
+    assert torch.equal(p.score, expected)
+    assert A.attn_get_device_status() == (A.ATTN_ERR_DEVICE_BAD_INDEX if refused else 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,lens", [([1, 1], [50, 300]), ([6, 2], [50, 300]), ([40, 33], [300, 200]), ([300, 200], [300, 900])])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "e5m2"])
+def test_nan_reaches_what_sees_it_and_nothing_else(A, n, lens, fmt):
+    """A NaN in a row of q makes the sums of exactly those tokens NaN that the row sees, of its kv head; all others are the same bytes as without
+    it. So are all but one for a NaN in a key."""
+    p = Problem(n, lens, 8, 2, 64, 16, fmt, seed=14)
+    start = p.score.clone()
+    p.run(A)
+    clean = p.score.clone()
+    row, head, i = n[0] + n[1] // 2, 6, n[1] // 2  # a query head of kv head 1, in the middle of sequence 1
+    q = p.q.clone()
+    p.q[row, head, 9] = math.nan
+    p.score.copy_(start)
+    p.run(A)
+    pg, sl = p.places(1)
+    seen = lens[1] - n[1] + i + 1
+    wrong = torch.zeros_like(clean, dtype=torch.bool)
+    wrong[pg[:seen], 1, sl[:seen]] = True
+    assert torch.isnan(p.score[wrong]).all() and torch.equal(p.score[~wrong], clean[~wrong])
+    p.q.copy_(q)
+    token = min(37, lens[1] - 1)
+    p.kc[pg[token], sl[token], 0, 3] = math.nan if fmt == "bf16" else 0x7F
+    p.score.copy_(start)
+    p.run(A)
+    wrong.zero_()
+    wrong[pg[token], 0, sl[token]] = True
+    assert torch.equal(p.score[~wrong], clean[~wrong])
+    assert A.attn_get_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,lens", [([1], [2000]), ([1] * 9, [5, 40, 700, 1, 300, 20, 90, 1100, 64]), ([40, 20], [300, 200]), ([700], [700])])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("tokens", [131072, 2**20])
+def test_short_sequences_in_a_wide_table(A, n, lens, fmt, tokens):
+    """A page table for the longest context that a server allows, and sequences far below it."""
+    p = Problem(n, lens, 8, 2, 128, 16, fmt, seed=15)
+    p.ptd = torch.nn.functional.pad(p.ptd, (0, tokens // 16 - p.width), value=-1).contiguous()
+    p.width = tokens // 16
+    before = p.score.clone()
+    p.run(A, 0.5)
+    assert A.attn_get_device_status() == 0
+    p.check(before, 0.5)
+
+
+@pytest.mark.gpu
+def test_calls_from_several_host_threads(A):
+    """Calls of different sizes at once, each thread on a stream of its own: the same bytes as one after the other."""
+    from concurrent.futures import ThreadPoolExecutor
+    ps = [Problem(n, lens, 8, 2, d, page, fmt, seed=16) for d, page, fmt in ((64, 16, "bf16"), (128, 7, "e4m3"), (128, 16, "bf16"))
+          for n, lens in (([1] * 5, [40, 900, 333, 1, 2000]), ([40, 20], [300, 200]), ([300], [800]))]
+    start = [p.score.clone() for p in ps]
+    for p in ps:
+        p.run(A)
+    want = [p.score.clone() for p in ps]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                ps[i].score.copy_(start[i])
+                ps[i].run(A)
+        s.synchronize()
+
+    torch.cuda.synchronize()
+    with ThreadPoolExecutor(len(ps)) as pool:
+        list(pool.map(work, range(len(ps))))
+    for p, w in zip(ps, want):
+        assert torch.equal(p.score, w)
+    assert A.attn_get_device_status() == 0
