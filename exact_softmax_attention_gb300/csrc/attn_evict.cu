@@ -101,7 +101,7 @@ __device__ __forceinline__ bool select_row(const EvictParams& p, SelectRow& s, i
         if (s.h == 0) p.new_seqlens[b] = bad ? s.len : min(s.len, K);
     }
     if (bad || s.len <= K) {
-        for (int j = tid; j < K; j += nt) s.kept[j] = !bad && j < s.len ? j : -1;
+        for (unsigned j = tid; j < (unsigned)K; j += nt) s.kept[j] = !bad && j < (unsigned)s.len ? (int)j : -1;  // (j + nt may pass 2^31)
         return false;
     }
     s.end = K - p.recent, s.stop = s.len - p.recent;
@@ -512,9 +512,9 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const __gri
         const int page = row / p.page_size;
         return p.score + ((long long)page * p.Hkv + h) * p.page_size + (row - page * p.page_size);
     };
-    for (int j0 = 0; j0 < n; j0 += kMoves) {
+    for (unsigned j0 = 0; j0 < (unsigned)max(n, 0); j0 += kMoves) {  // (unsigned: behind the last slots of a bad length j0 is 2^31)
         // the slots from j0 on that get another row; neighbouring ones of this thread
-        const int first = j0 + tid * kLook;
+        const int first = (int)j0 + tid * kLook;
         int tok[kLook];
         unsigned moves = 0;
 #pragma unroll

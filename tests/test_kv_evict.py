@@ -483,3 +483,26 @@ def test_short_sequences_in_a_wide_table(A, lens, Hkv, budget, sinks, recent, pa
     assert A.attn_get_device_status() == 0
     for got, ref in zip((c.kc, c.vc, c.score), expect):
         assert np.array_equal(got.cpu().numpy(), ref, equal_nan=got.dtype == torch.float32)
+
+
+@pytest.mark.gpu
+def test_the_largest_budget(A):
+    """A budget of 2^31 - 1: one short row and all entries behind it; then a length out of range, whose slots up to 2^31 - 1 are all looked at
+    and left alone."""
+    budget = 2**31 - 1
+    c = Cache([50, 20], 1, 16, 8, seed=17)
+    c.B, c.lend = 1, c.lend[:1].clone()
+    c.select(A, budget, 3, 2**31 - 100)
+    assert A.attn_get_device_status() == 0 and c.new[0] == 50
+    assert torch.equal(c.kept[0, 0, :50], torch.arange(50, dtype=torch.int32, device=DEV))
+    assert all((c.kept[0, 0, i:min(i + 2**28, budget)] == -1).all() for i in [50] + list(range(2**28, budget, 2**28)))
+    before = c.kc.clone()
+    c.compact(A)
+    assert torch.equal(c.kc, before) and A.attn_get_device_status() == 0
+    c.lend[0] = budget
+    c.kept.fill_(-9)
+    A.attn_kv_select_paged(c.score, c.ptd, c.lend, c.kept, c.new, c.page, 1, 1, c.width, c.num, budget, 3, 4)
+    assert A.attn_get_device_status() == A.ATTN_ERR_DEVICE_BAD_INDEX and c.new[0] == budget
+    assert all((c.kept[0, 0, i:min(i + 2**28, budget)] == -1).all() for i in range(0, budget, 2**28))
+    c.compact(A)
+    assert torch.equal(c.kc, before) and A.attn_get_device_status() == 0
