@@ -32,3 +32,13 @@ def test_every_dependent_kernel_waits(name):
     for p in parts:
         kernel = re.search(r"(\w+_kernel)\s*\(", p).group(1)
         assert "grid_dependency_wait()" in p or kernel == "split_q_kernel", kernel
+
+
+def test_the_parts_of_q_come_from_an_ordinary_launch():
+    """score_tiles_kernel over 8-bit caches and score_join_kernel read lengths, pages, keys and old sums before they wait: whatever wrote those
+    has ended by then, because split_q_kernel does not start before it has (and for bf16 the tile kernel waits before it lets dependents start)."""
+    text = code("attn_score_tiles.cu")
+    assert re.search(r"launch_kernel\(split_q_kernel<D>, [^;]*?, stream, \{\}, ", text)
+    tiles = text.split("score_tiles_kernel(", 1)[1]
+    wait, start = tiles.index("if (!F8) grid_dependency_wait();"), tiles.index("grid_dependents_launch();")
+    assert wait < start

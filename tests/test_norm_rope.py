@@ -403,3 +403,15 @@ def test_forward_over_the_range(A, d, begin, rot, inter, et, size, weight):
         bound = bound + size_ * norm_error(d)
         tol = bound + STEP[et] * (np.abs(ref) + bound) + 1e-38
         assert np.isfinite(got).all() and (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,begin,rot,inter,et", RANGE)
+@pytest.mark.parametrize("T", [5, 900])
+def test_gradient_in_the_place_of_the_input(A, d, begin, rot, inter, et, T):
+    """dq and dk written over q and k: the same bytes as beside them."""
+    p = Problem(A, T, 5, 2, d, begin, rot, inter, et, True, seed=13)
+    dq, dk, dw = p.backward(A)
+    _, _, again = p.backward(A, dq=p.q, dk=p.k)
+    assert torch.equal(p.q, dq) and torch.equal(p.k, dk[:, :2 * d])
+    assert all(torch.equal(a, b) for a, b in zip(again, dw))
