@@ -67,6 +67,14 @@ constexpr int score_few_rows(int d) { return d == 64 ? 32 : 24; }
 #ifdef __CUDACC__
 namespace {
 
+// A load that stays in its place, behind the wait for the kernel before. (Plain loads do as well, but with them the compiler arranged the tile
+// kernel so that whole prompts took 129 us, not 126.)
+__device__ __forceinline__ int load_in_place(const int* p) {
+    int x;
+    asm volatile("ld.global.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+    return x;
+}
+
 // Rows and cached tokens of sequence b. False: none of its slots are touched (no rows; or a length or offsets out
 // of range, which is recorded).
 struct ScoreSeq {
@@ -75,9 +83,9 @@ struct ScoreSeq {
 };
 __device__ __forceinline__ bool score_seq(const ScoreParams& p, int b, ScoreSeq& s) {
     long long c0, c1;
-    const int len = p.seqlens[b];
+    const int len = load_in_place(p.seqlens + b);
     if (p.cu_seqlens) {
-        c0 = p.cu_seqlens[b], c1 = p.cu_seqlens[b + 1];
+        c0 = load_in_place(p.cu_seqlens + b), c1 = load_in_place(p.cu_seqlens + b + 1);
     } else {
         const int n = p.T / p.B;
         c0 = (long long)b * n, c1 = c0 + n;
