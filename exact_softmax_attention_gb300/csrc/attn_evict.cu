@@ -10,7 +10,12 @@
 // and about ten instructions per pass and 32 tokens. Several blocks share a row where rows are long and few: a block counts and marks its part,
 // and the others read the counts in its shared memory. (One block for each row, votes on 32 tokens: 16 x 8 rows of up to 32768 tokens 25 us,
 // 64 x 8 rows of 4100-4352 tokens 21 us; with keys in registers, four digits of 8 bits, and a numbering per 1024 tokens about 100 us.) Now, on new
-// scores in a graph: 8 rows of 1000 tokens 6.7 us (a piece of code per digit instead of a loop: 7.2), 16 x 8 of U[2048, 32768] 20, 64 x 8 of U[4100, 4352] 18.3.
+// scores in a graph: 8 rows of 1000 tokens 6.6 us (a piece of code per digit instead of a loop: 7.2), 16 x 8 of U[2048, 32768] 20.5, 64 x 8 of
+// U[4100, 4352] 18.2.
+// Parts and their shared memory go by the page table's capacity, which the host knows, not by the lengths. What that costs in tables much wider than
+// the sequences: 64 x 8 rows of 600-1000 tokens 8 us in a tight table, 10 in one of 8192 tokens, 19 in one of 32768, 206 in one of 131072 (four blocks
+// a row, one on an SM), 21 in one of 524288, which select_long_kernel takes; 16 x 8 of 1100-4000 tokens 8.4, 7.1, 7.1, 50 and 13; 8 rows of 1000
+// tokens 6.5, 11, 16, 15 and 6.
 //
 // Compaction: row kept[j] -> j with kept[j] >= j. A block lists the slots that get another row, in ascending order, with the
 // cache rows of both, and moves them in runs: it loads the rows of a run, then stores them. Every row that it reads later belongs to a slot
@@ -18,7 +23,8 @@
 // need a barrier between them. Blocks share nothing: one has a (sequence, kv head) and some 16-byte columns of its rows, fewer columns
 // where there are few sequences. Measured on new scores: 16 x 8 x U[2048, 32768] tokens to 2048, bf16 heads of 128, 198011 rows of K and of V
 // in and out, 43 us, 4.7 TB/s; 64 x 8 x U[4100, 4352] to 4096, e4m3, 196210 rows, 26.6 us, 3.8 TB/s: the memory, behind the chain list, pages, rows of each
-// block. (Walking all slots instead of a list took 150 us more in the first case; blocks of 256 threads, three or four on an SM, 47-55 and 29-31 us.)
+// block, and nothing is loaded while a run is stored. (Walking all slots instead of a list took 150 us more in the first case; blocks of 256 threads,
+// three or four on an SM, 47-55 and 29-31 us.)
 #include "attn.h"
 #include "kernels.cuh"
 #include "launch.cuh"
@@ -33,7 +39,7 @@ namespace {
 constexpr int kLongThreads = 1024;  // selection from more tokens than the shared memories of a cluster hold
 constexpr int kPairs = 4096;        // there: holes paired with tokens at a time
 constexpr int kGroup = 128;         // tokens that a warp looks at
-// Groups of a block's part: 512 bytes of keys and 20 of marks and counts each, 41 KB besides.
+// Groups of a block's part: 512 bytes of keys and 20 of marks and counts each, 33 KB besides (25 KB for one part).
 constexpr int kPartGroups = 352, kGroupBytes = kGroup * 4 + 20;
 constexpr int kMaxParts = 8;
 

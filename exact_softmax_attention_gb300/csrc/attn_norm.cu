@@ -14,8 +14,9 @@
 // same call gives the same bytes.
 //
 // Measured, bf16, 40 heads of 128, 18432 rows: 59.1 us, 6390 GB/s, 0.94 of a copy's rate; the gradient
-// of 16384 rows 82.7 us, 6080 GB/s, 0.90. fp32, 32 heads
-// of 192, 64 interleaved columns rotated, 8192 rows, gradient: 97.2 us, 6210 GB/s. Not kept: heads loaded two or three ahead into registers (forward 75-85 us), four or eight heads of a
+// of 16384 rows 83-85 us, 6000 GB/s, 0.89. fp32, 32 heads
+// of 192, 64 interleaved columns rotated, 8192 rows: 63.3 us, 6360 GB/s, the gradient 97.2 us, 6210 GB/s; 40 heads of 128, 9216 rows: 58.7 us, 6430 GB/s, the
+// gradient of 8192 rows 82-84 us. Not kept: heads loaded two or three ahead into registers (forward 75-85 us), four or eight heads of a
 // token for each group of lanes with angles and weights in registers (86-93).
 #include "attn.h"
 #include "launch.cuh"
@@ -35,7 +36,7 @@ constexpr int norm_bwd_blocks(int items) { return items == 1 ? 2 : 1; }
 // head ahead in registers, 5 blocks, 62.6.)
 constexpr int kNormFwdStages = 3;
 // Heads that a group of lanes of the gradient has in shared memory or on their way there, 64 bytes of a lane for each of its items: with one
-// item per lane two are on their way while one is computed (16384 rows of 40 heads of 128: 82.7 us; one 91, three 90, four 94. fp32 heads
+// item per lane two are on their way while one is computed (16384 rows of 40 heads of 128: 83 us; one 91, three 90, four 94. fp32 heads
 // of 192, three items per lane: one on its way 97.2, two 100; with two blocks on an SM 107).
 template <int R>
 constexpr int kNormStages = R == 1 ? 3 : 2;

@@ -1,6 +1,6 @@
 // Attention weight per cached token, accumulated: score[t, h] = decay score[t, h] + sum over the rows that see
 // token t and the query heads of kv head h of exp(scale q.k - lse); the rows' own tokens have no old sum. This file: argument checks, and the kernel for up to
-// 32 rows per kv head (a decode step: one row times the query heads of a kv head).
+// score_few_rows rows per kv head (32 of 64 elements, 24 of 128; a decode step has one row times the query heads of a kv head).
 //
 // With few rows the keys are read once and little is computed with them: the kernel is bounded by the memory. So a
 // warp reads K from the cache straight into the operand registers of mma.sync m16n8k16: 16 tokens are the rows of
@@ -9,14 +9,17 @@
 // tokens (narrower rows: 32) are loaded while these are multiplied, and the page table is read one group ahead of them. A block's warps take
 // the kv heads of the same tokens, so a cache row is read as a whole.
 //
-// Measured, 64 sequences of U[1K, 32K] tokens, 32/8 heads of 128: bf16 327 us, 6790 GB/s (the rate of a copy); e4m3 186 us, 6160 GB/s (loads that
+// Measured, 64 sequences of U[1K, 32K] tokens, 32/8 heads of 128: bf16 324-328 us, 6800 GB/s (the rate of a copy); e4m3 182-186 us, 6200 GB/s (loads that
 // the warps wait for, 20 on an SM). 48 x U[1, 8000], 1-6 rows of 4 heads x 3 heads of 64, e5m2, pages of 7: 21 us for 41 MB, a
 // chain of dependent loads in one wave of blocks (without the exponentials of rows that a sequence has not, or with the keys loaded before the rows:
-// no change).
+// no change). 48 x U[5333, 16000] tokens, 8 heads: 16 rows of 64 bf16 88 us, e4m3 67 us (floors 75 and 40); 24 rows of 64 102 and 82 (75, 40); 16 of 128
+// 165 and 100 (146, 75); 24 of 128 171 and 117 (146, 75): q's operands in registers leave 12 to 20 warps on an SM, which wait for keys.
 //
 // Work order. When the blocks of all sequences' full tables run at once, a block has a piece of a sequence. Else the tokens that there are,
 // of all sequences one after the other, are dealt out in equal runs to as many blocks as the SMs hold: every SM is busy to the end, however
-// ragged the lengths (pieces of 1024 tokens: 64 sequences of U[1K, 32K] x 8 heads of 128 361 us, with e4m3 282 us).
+// ragged the lengths (pieces of 1024 tokens: 64 sequences of U[1K, 32K] x 8 heads of 128 361 us, with e4m3 282 us). What pieces cost where tables are
+// much wider than the sequences, which leaves most blocks without tokens: one of 2000 tokens, 8 heads of 128, 4.4 us in a tight table, 7.5 in one of
+// 32768, 15.4 in one of 131072; sixteen of U[500, 2000] 9.8 and 10.3.
 #include "score.cuh"
 
 #include <float.h>

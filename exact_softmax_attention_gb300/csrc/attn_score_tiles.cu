@@ -1,4 +1,4 @@
-// Attention weight per cached token for more than 16 rows per kv head (the last queries of a prompt, or all of them):
+// Attention weight per cached token for more rows per kv head than score_few_rows (the last queries of a prompt, or all of them):
 // 128-row tiles on the tcgen05 tensor cores.
 //
 // The transposed scores S^T = K Q^T have the tokens as rows of the accumulator, so that a thread owns a token: it
@@ -9,13 +9,17 @@
 // that lies in more than one run leaves partial sums, which a second kernel adds in order.
 //
 // What bounds it. With d = 128 a task is 4 x 8 products of 128 x 128 x 16 and 65536 exponentials, 2048 clocks of the tensor pipe and of the MUFU,
-// for 32 KB of q from the L2 (with units of 256 tokens the L2 was the bound: 153 us for the whole prompts below). Measured: 3300 clocks, the
-// tensor pipe 57 % busy, the MUFU 51 %. The products take 92 clocks each, not 64, because both operands come out of shared memory, and a tile's
-// only buffer is held through the products and three quarters of the exponentials. Rows that stay the same (up to 128) against new tokens every
-// task are 128 KB of bf16 keys for that, more than the memory delivers in the time.
-// Whole prompts, 8 x U[512, 4096] tokens, 32/8 heads of 128, bf16: 130 us, 1020 TFLOP/s (without exponentials 107 us, with an eighth of the
-// products 132, with neither 69). The last 32 queries of 16 x U[2K, 16K] cached
-// tokens: 52 us, 5.4 TB/s.
+// for 32 KB of q from the L2 (with units of 256 tokens the L2 was the bound: 153 us for the whole prompts below). Measured: 3300 clocks. The
+// products take 92 clocks each, not 64, because both operands come out of shared memory, and a tile's only buffer is held through the products and
+// three quarters of the exponentials. Rows that stay the same (up to 128) against new tokens every task are 128 KB of bf16 keys for that, more than
+// the memory delivers in the time.
+// Whole prompts, 8 x U[512, 4096] tokens, 32/8 heads of 128, bf16: 130 us, 1020 TFLOP/s. Parts left out one by one, three calls in turn (127 us
+// then): no exponentials 126, neither them nor the loads of the accumulators 127, an eighth of the products 120, that without exponentials 84. So
+// the products take all of the time, the exponentials and loads nearly all, side by side: only less of both would be faster.
+// The same over e4m3: 187 us, about 37 of them for the parts of q (151 MB in, as much out). Without exponentials 173, with an eighth of the products 179,
+// without loads of the accumulators 174, without reading LSE and factors per column 159: these reads from shared memory cost most.
+// The last 32 queries of 16 x U[2K, 16K] cached tokens: bf16 52 us, 5.4 TB/s; e4m3 51 us, heads of 64 44 and 49 us. With any of these parts left out, bf16
+// and e4m3 take at most 3 us less: the keys' way into shared memory, and the start.
 // Other arrangements, whole prompts, at 138 us then: 32 columns of all tiles to four warps each 179 us; 64 columns of all tiles to four of eight
 // warps with their LSE in registers 258; eight warps for every other tile 160; the two product threads in turns 143; later, at 130: keys in
 // tensor memory as operand A, products with 64 rows at a time, 161; parts of 32 columns left out in tiles on the diagonal 159; shares of the work
@@ -29,6 +33,10 @@
 // copies of 64 or 16 rows where the page size is a multiple of that, else by 16-byte copies of rows that the page table gives; 18 the blocks
 // of q through tensor copies (one box is the heads of as many queries as fit) and their LSE; 19 and 20 the products of two tiles each,
 // issued by one thread: while one waits for its buffer, the other one's products run.
+//
+// Work split: the tasks are those of the lengths, but the size of a unit and the number of blocks go by the page table's capacity. It makes little
+// difference: 32 queries of 4 x U[500, 2000] tokens 9.8 us in a tight table, 9.0 in one of 131072 tokens; of 2000 tokens 7.6 and 8.1; one prompt of
+// 1500 tokens 21.6 in both.
 //
 // Start. 14500 clocks passed before the first product, 5300 in the shares of the work and 2900 in the search of its first task, mostly divisions;
 // with multipliers for them, as a programmatic dependent, and with the joining kernel's own search done before it waits: 138 -> 130 us,
@@ -380,7 +388,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         *unit32(smem + L::kFoldK, threadIdx.x >> 1, threadIdx.x & 1) = threadIdx.x & 1 ? make_uint4(0, 0, 0, 0) : make_uint4(0x3F803F80u, 0x3F80u, 0, 0);
     fence_smem_to_async();
     // Nothing that an earlier kernel writes is read before this, and no tensor memory is held that one may still ask for. (8-bit caches: only
-    // the kernel that makes the parts of q is still running, which the warp that copies them waits for.)
+    // split_q_kernel can still be running, since that is an ordinary launch. So lengths, pages, keys and old sums are read, and tensor memory is asked
+    // for, without a wait; the parts of q and their factors behind one, in the warp that copies them.)
     if (!F8) grid_dependency_wait();
     grid_dependents_launch();
     if (warp == kProductWarp) {
@@ -744,7 +753,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (threadIdx.x == 0 && *abort_flag) atomicCAS(p.status, 0, kDevTimeout);
 }
 
-// Units that lie in more than one run: the block whose run begins one adds the parts up in order.
+// Units that lie in more than one run: the block whose run begins one adds the parts up in order. Before its wait it reads only what
+// kernels before score_tiles_kernel wrote, which have ended: every block of that one knows it before it lets this one start.
 __global__ void __launch_bounds__(kUnitTok) score_join_kernel(const __grid_constant__ ScoreParams p) {
     __shared__ long long sums[kUnitTok / 32], out[2];
     const TaskRun run = task_run<kUnitTok>(p, blockIdx.x, sums, out);
@@ -826,6 +836,7 @@ cudaError_t launch_tiles(ScoreParams p, cudaStream_t stream) {
     e = st == ATTN_OK ? cudaSuccess : cudaErrorInvalidValue;
     LaunchMode dependent;
     dependent.dependent = true;
+    // (split_q_kernel has to be an ordinary launch, not a dependent: the two kernels behind it rely on all earlier work having ended)
     if (L::kF8 && e == cudaSuccess)
         e = launch_kernel(split_q_kernel<D>, dim3((unsigned)((rows * (D / 8) + 255) / 256)), 256, 0, stream, {}, p.q, parts, p.factor, (long long)rows,
                           p.scale_log2);

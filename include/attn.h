@@ -475,6 +475,8 @@ attn_status_t attn_kv_score_paged(const void* q, const float* lse, const void* k
  * budget     >= 1;  sinks, recent >= 0, sinks + recent <= budget
  * A sequence whose length is negative or above its page table is recorded as ATTN_ERR_DEVICE_BAD_INDEX: its entries of kept are -1, its
  * new length is the old one. A token on a page outside [0, num_pages) is recorded too and counts as less than every score.
+ * Blocks and their shared memory go by the tokens of the page table, max_pages_per_seq * page_size: with many sequences and a table many times
+ * wider than the longest of them a call takes several times longer than with one of its width.
  * Alignment: 4 bytes.
  */
 attn_status_t attn_kv_select_paged(const float* score, const int* page_table, const int* seqlens, int* kept, int* new_seqlens,
